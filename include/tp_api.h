@@ -530,6 +530,105 @@ int tp_q4_sharded_to_all_noalloc(int N, const void *const *x, int64_t T, int64_t
                                  tp_stream_t stream);
 
 /*
+ * The operators between the sharded linears.  No arithmetic of theirs crosses
+ * ranks: a rank owns Hq query heads and Hk key-value heads of the layer, and
+ * query head h reads key-value head h / (Hq / Hk).
+ *
+ * The paged cache.  k_cache[r] and v_cache[r] hold `pages` pages, dt TP_BF16
+ * or TP_F16, element (page p, head h, row j, value d) at
+ * p * ld_page + (h * page + j) * D + d; ld_page >= Hk * page * D, a multiple of
+ * D.  Bases 16-byte aligned; D is 64 or 128; `page` (rows of a page) a power
+ * of two in 16..256.  Position i of sequence b lies in row i % page of page
+ * block_table[b * ld_table + i / page]; entries behind a sequence's last page
+ * are not read, and rows that hold no position of a sequence may hold anything
+ * (NaN too).
+ * Page numbers, slots, positions and lengths are device data: one that is out
+ * of range records TP_ERR_INVALID_ARG in the device status word
+ * (tp_query_status); nothing outside the arrays is then read or written, and
+ * the results of that token or sequence are unspecified.
+ *
+ * tp_qkv_append: per-head norms, rotation, and the write into the cache, for T
+ *   tokens of the fused projection's output.
+ *     qkv[r]  (T, (Hq + 2 Hk) * D) in_dt (any tp_dtype), row stride ld: the
+ *             query heads, then the key heads, then the value heads;
+ *     q_norm, k_norm  NULL or float32 (D): x * rsqrt(mean(x^2) + eps) * gain
+ *             for each query / key head;
+ *     rope    NULL (no rotation) or float32 (rope_rows, rope_dim): row p holds
+ *             the rope_dim / 2 cosines of position p, then its sines.
+ *             rope_dim is a multiple of 16 up to D; values behind it are not
+ *             turned.  The pair (a, b) of factor i becomes
+ *             (a cos - b sin, b cos + a sin): values i and i + rope_dim / 2,
+ *             or with interleaved != 0 values 2i and 2i + 1;
+ *     positions  int32 (T), read where rope is given;
+ *     slots   int64 (T): token t goes to row slots[t] % page of page
+ *             slots[t] / page; a negative slot writes no key and value
+ *             (padding).  No two tokens may share a slot;
+ *     q[r]    (T, Hq * D) dt, row stride ldq: the queries.
+ *   Computed in float32 and rounded once to dt.  T = 0 launches nothing.
+ *
+ * tp_paged_decode: attention of one token per sequence, the last of its
+ *   seq_lens[b] cached positions:
+ *     s_j = f(scale * q . k_j),  f(x) = softcap * tanh(x / softcap), or x for 0;
+ *     o   = sum_j softmax_j(s) v_j  over j < seq_lens[b], and where window > 0
+ *           only j >= seq_lens[b] - window.
+ *   q[r], o[r]  (B, Hq * D) dt, row strides ldq, ldo; block_table int32
+ *   (B, width); seq_lens int32 (B).  A sequence of length 0 gives zeros.
+ *   The scores, the softmax and the sums are float32; the softmax's terms are
+ *   rounded to dt before they meet the values.  The sequences' work is split
+ *   evenly over the GPU and the parts joined in a fixed order: the same call
+ *   gives the same bytes.  Uses the per-(device, stream) workspace.
+ *
+ * tp_paged_prefill: the same attention for ragged chunks of several tokens.
+ *   Rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 of q and o are the last cached
+ *   positions of sequence b (whose keys and values are in the cache already).
+ *   The token at position p sees position j < seq_lens[b] where
+ *     j <= p and (window = 0 or j > p - window), or j < prefix_lens[b].
+ *   cu_seqlens int32 (B + 1), ascending; prefix_lens NULL or int32 (B).  A row
+ *   that sees nothing is zero, and so is a row of no sequence.
+ *
+ * tp_sample: one token per row of logits (B, V) in_dt (any tp_dtype), row
+ *   stride ld, V <= 2^22.  The parameters are device arrays of B; all but u may
+ *   be NULL (temperature 1, no filter).  With x the row (NaN counts as -inf,
+ *   +inf as the largest float), M its largest and T the temperature:
+ *     e_i = exp((x_i - M) * (1 / T)),  w_i = floor(e_i * 2^40).
+ *   Sort by x, largest first, the lower index first among equals.  top_k keeps
+ *   the first top_k (<= 0: all); top_p keeps of those the ones whose weight
+ *   before them is below part(their total, top_p), the first always (>= 1:
+ *   all); min_p drops those with e_i < min(min_p, 1).  The token is the lowest
+ *   index at which the running weight of the kept, in index order, is above
+ *   part(their total, u).  part(W, f) = floor(W * floor(f * 2^24) / 2^24), u
+ *   taken into [0, 1).  Temperatures below 2^-20 take the largest logit.
+ *   tokens int64 (B); logprobs NULL or float32 (B): the token's log-probability
+ *   under the row's own softmax (temperature 1, unfiltered).  A row without a
+ *   logit above -inf gives token -1 and -inf.
+ * Errors: TP_ERR_NOT_DIVISIBLE if Hq % Hk != 0; TP_ERR_UNSUPPORTED for a D,
+ * page, rope_dim or V this build does not take; TP_ERR_ALIGNMENT for a pointer
+ * not aligned to its element size (caches: 16 bytes); TP_ERR_INVALID_ARG for
+ * null pointers, a row stride below the row, N outside 1..64, scale <= 0,
+ * softcap < 0, window < 0.  T = 0 or B = 0 launches nothing.
+ */
+int tp_qkv_append(int N, const void *const *qkv, int64_t T, int64_t ld, tp_dtype in_dt, int Hq,
+                  int Hk, int D, const float *q_norm, const float *k_norm, float eps,
+                  const float *rope, int64_t rope_rows, int rope_dim, int interleaved,
+                  const int32_t *positions, const int64_t *slots, void *const *q, int64_t ldq,
+                  void *const *k_cache, void *const *v_cache, int64_t pages, int page,
+                  int64_t ld_page, tp_dtype dt, tp_stream_t stream);
+int tp_paged_decode(int N, const void *const *q, int64_t B, int64_t ldq, int Hq, int Hk, int D,
+                    void *const *k_cache, void *const *v_cache, int64_t pages, int page,
+                    int64_t ld_page, const int32_t *block_table, int64_t width, int64_t ld_table,
+                    const int32_t *seq_lens, float scale, float softcap, int window, tp_dtype dt,
+                    void *const *o, int64_t ldo, tp_stream_t stream);
+int tp_paged_prefill(int N, const void *const *q, int64_t T, int64_t ldq, int Hq, int Hk, int D,
+                     void *const *k_cache, void *const *v_cache, int64_t pages, int page,
+                     int64_t ld_page, const int32_t *block_table, int64_t B, int64_t width,
+                     int64_t ld_table, const int32_t *cu_seqlens, const int32_t *seq_lens,
+                     const int32_t *prefix_lens, float scale, float softcap, int window,
+                     tp_dtype dt, void *const *o, int64_t ldo, tp_stream_t stream);
+int tp_sample(const void *logits, int64_t B, int64_t V, int64_t ld, tp_dtype in_dt, const float *u,
+              const float *temperature, const int32_t *top_k, const float *top_p,
+              const float *min_p, int64_t *tokens, float *logprobs, tp_stream_t stream);
+
+/*
  * Fault check of the bounded waits (no counterpart on the pages): launches a
  * one-block kernel that waits on a shared-memory barrier nothing ever
  * arrives at, with the given limit (1e6 .. 6e10 ns).  The wait runs out,

@@ -75,6 +75,7 @@ def _load() -> ctypes.CDLL:
                                % LIB_PATH)
         L = ctypes.CDLL(LIB_PATH)
         i32, i64, vp = ctypes.c_int, ctypes.c_int64, ctypes.c_void_p
+        f32 = ctypes.c_float
         vpp = ctypes.POINTER(ctypes.c_void_p)
         sig = {
             "tp_version": ([], i32),
@@ -105,6 +106,13 @@ def _load() -> ctypes.CDLL:
             "tp_q4_quantize": ([vp, i64, i64, i32, vp, vp, vp, vp], i32),
             "tp_q4_all_to_sharded": ([i32, vp, i64, i64, vpp, vpp, vpp, i32, i64, vpp, vpp, i64, i32, vp], i32),
             "tp_q4_sharded_to_all": ([i32, vpp, i64, i64, vpp, vpp, vpp, i32, i64, vp, vp, i64, i32, vp], i32),
+            "tp_qkv_append": ([i32, vpp, i64, i64, i32, i32, i32, i32, vp, vp, f32, vp, i64, i32, i32, vp, vp, vpp,
+                               i64, vpp, vpp, i64, i32, i64, i32, vp], i32),
+            "tp_paged_decode": ([i32, vpp, i64, i64, i32, i32, i32, vpp, vpp, i64, i32, i64, vp, i64, i64, vp, f32,
+                                 f32, i32, i32, vpp, i64, vp], i32),
+            "tp_paged_prefill": ([i32, vpp, i64, i64, i32, i32, i32, vpp, vpp, i64, i32, i64, vp, i64, i64, i64, vp,
+                                  vp, vp, f32, f32, i32, i32, vpp, i64, vp], i32),
+            "tp_sample": ([vp, i64, i64, i64, i32, vp, vp, vp, vp, vp, vp, vp, vp], i32),
             "tp_debug_wait_timeout": ([i64, vp], i32),
             "tp_debug_prep_alone": ([i32], i32),
             "tp_set_trace": ([vp, i64], i32),
@@ -762,3 +770,188 @@ def tp_mx_sharded_to_all(x, codes, scales, bias=None, out=None, out_dtype=None, 
     _check(lib().tp_mx_sharded_to_all(N, xp, T, Kn * N, cp, sp, O, None if bias is None else bias.data_ptr(),
                                       out.data_ptr(), out.stride(0) if T > 1 else O, _dt(out), _stream(stream)))
     return out
+
+
+# ------------------------------------------------------------------ attention side
+# A per-rank argument is a list of N tensors, or one tensor whose first
+# dimension is the ranks (rank r is its slice [r]).
+def _ranks(x, name, dim):
+    """(pointer array, what keeps it alive, N, rank 0's shape and strides, dtype, device) of a per-rank argument."""
+    if isinstance(x, (list, tuple)):
+        t0 = x[0]
+        shape, stride, dtype, device = t0.shape, t0.stride(), t0.dtype, t0.device
+        for t in x[1:]:
+            if t.shape != shape or t.stride() != stride or t.dtype != dtype or t.device != device:
+                raise ValueError("%s: all ranks need one shape, stride, dtype and device" % name)
+        ptrs = [t.data_ptr() for t in x]
+    else:
+        shape, stride, dtype, device = x.shape[1:], x.stride(), x.dtype, x.device
+        base, step = x.data_ptr(), stride[0] * x.element_size()
+        stride = stride[1:]
+        ptrs = [base + i * step for i in range(x.shape[0])]
+    if device.type != "cuda":
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if len(shape) != dim:
+        raise ValueError("%s: each rank's tensor must be %d-D" % (name, dim))
+    n = len(ptrs)
+    arr = (ctypes.c_void_p * n)(*ptrs)
+    return ctypes.cast(arr, ctypes.POINTER(ctypes.c_void_p)), n, shape, stride, dtype, device
+
+
+def _rows_ld(shape, stride, name):
+    if shape[1] > 1 and stride[1] != 1:
+        raise ValueError("%s must have unit column stride" % name)
+    return stride[0] if shape[0] > 1 else max(shape[1], 1)
+
+
+def _param(t, name, dtype, n, device):
+    """Device pointer of a contiguous 1-D parameter array (None stays None)."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s" % (name, dtype))
+    if t.device != device:
+        raise ValueError("%s must be on %s" % (name, device))
+    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise ValueError("%s must be contiguous with %d elements" % (name, n))
+    return t.data_ptr()
+
+
+def _paged_cache(k_cache, v_cache):
+    """(k pointers, v pointers, N, (pages, Hk, page, D), page stride, dtype code, device)."""
+    kp, n, shape, stride, dtype, device = _ranks(k_cache, "k_cache", 4)
+    vp, nv, vshape, vstride, vdtype, vdevice = _ranks(v_cache, "v_cache", 4)
+    if (n, shape, stride, dtype, device) != (nv, vshape, vstride, vdtype, vdevice):
+        raise ValueError("k_cache and v_cache need the same ranks, shape, strides, dtype and device")
+    P, Hk, page, D = shape
+    if stride[3] != 1 or stride[2] != D or (Hk > 1 and stride[1] != page * D):
+        raise ValueError("the heads, rows and values of a cache page must be contiguous")
+    return kp, vp, n, shape, (stride[0] if P > 1 else Hk * page * D), _dtype_code(dtype), device
+
+
+def _dtype_code(dtype):
+    torch = _torch()
+    if dtype == torch.bfloat16:
+        return TP_BF16
+    if dtype == torch.float16:
+        return TP_F16
+    if dtype == torch.float32:
+        return TP_F32
+    raise TypeError("unsupported dtype %s" % dtype)
+
+
+def _heads(cols, D, name):
+    if cols % D:
+        raise ValueError("%s: %d columns are not whole heads of %d" % (name, cols, D))
+    return cols // D
+
+
+def tp_qkv_append(qkv, k_cache, v_cache, slots, positions=None, rope=None, q_norm=None, k_norm=None, eps: float = 1e-6,
+                  interleaved: bool = False, out=None, stream=None):
+    """Norms and rotation of the query and key heads of the fused projection
+    ``qkv`` (per rank (T, (Hq + 2 Hk) D)), keys and values written to the paged
+    caches (per rank (pages, Hk, page, D)) at ``slots``; returns the queries,
+    per rank (T, Hq D) in the cache's dtype (one (N, T, Hq D) tensor unless
+    ``out`` is given)."""
+    torch = _torch()
+    kp, vp, N, (P, Hk, page, D), ldp, dt, device = _paged_cache(k_cache, v_cache)
+    xp, n, shape, stride, dtype, xdev = _ranks(qkv, "qkv", 2)
+    if n != N or xdev != device:
+        raise ValueError("qkv and the caches need the same ranks on one device")
+    T = shape[0]
+    Hq = _heads(shape[1], D, "qkv") - 2 * Hk
+    if out is None:
+        out = torch.empty((N, T, max(Hq, 0) * D), dtype=torch.bfloat16 if dt == TP_BF16 else torch.float16,
+                          device=device)
+    op, no, oshape, ostride, odtype, odev = _ranks(out, "out", 2)
+    if no != N or tuple(oshape) != (T, Hq * D) or _dtype_code(odtype) != dt or odev != device:
+        raise ValueError("out must be (T, Hq * D) per rank in the cache's dtype")
+    rp, rows, rot = None, 0, 0
+    if rope is not None:
+        if rope.dtype != torch.float32 or rope.dim() != 2 or not rope.is_contiguous() or rope.device != device:
+            raise ValueError("rope must be a contiguous float32 (positions, rope_dim) tensor on the caches' device")
+        rp, (rows, rot) = rope.data_ptr(), rope.shape
+        if positions is None:
+            raise ValueError("rope needs positions")
+    _check(lib().tp_qkv_append(
+        N, xp, T, _rows_ld(shape, stride, "qkv"), _dtype_code(dtype), Hq, Hk, D,
+        _param(q_norm, "q_norm", torch.float32, D, device), _param(k_norm, "k_norm", torch.float32, D, device), eps,
+        rp, rows, rot, 1 if interleaved else 0, _param(positions, "positions", torch.int32, T, device),
+        _param(slots, "slots", torch.int64, T, device), op, _rows_ld(oshape, ostride, "out"), kp, vp, P, page, ldp, dt,
+        _stream(stream)))
+    return out
+
+
+def _attention(q, k_cache, v_cache, block_table, out):
+    torch = _torch()
+    kp, vp, N, (P, Hk, page, D), ldp, dt, device = _paged_cache(k_cache, v_cache)
+    qp, n, shape, stride, dtype, qdev = _ranks(q, "q", 2)
+    if n != N or qdev != device:
+        raise ValueError("q and the caches need the same ranks on one device")
+    if _dtype_code(dtype) != dt:
+        raise TypeError("q must have the caches' dtype")
+    if out is None:
+        out = torch.empty((N,) + tuple(shape), dtype=dtype, device=device)
+    op, no, oshape, ostride, odtype, odev = _ranks(out, "out", 2)
+    if no != N or oshape != shape or odtype != dtype or odev != device:
+        raise ValueError("out must have q's shape per rank and its dtype")
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.device != device or (
+            block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError("block_table must be a 2-D int32 tensor with unit column stride on the caches' device")
+    width = block_table.shape[1]
+    ldt = block_table.stride(0) if block_table.shape[0] > 1 else width
+    return (out, device, shape[0],
+            (N, qp, shape[0], _rows_ld(shape, stride, "q"), _heads(shape[1], D, "q"), Hk, D, kp, vp, P, page, ldp,
+             block_table.data_ptr()), (width, ldt), (dt, op, _rows_ld(oshape, ostride, "out")))
+
+
+def tp_paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale=None, softcap: float = 0.0, window: int = 0,
+                    out=None, stream=None):
+    """Attention of one new token per sequence over the paged caches: q per rank
+    (B, Hq D), seq_lens (B) counts the new token.  Returns o, per rank
+    (B, Hq D) (one (N, B, Hq D) tensor unless ``out`` is given)."""
+    out, device, B, head, table, tail = _attention(q, k_cache, v_cache, block_table, out)
+    if block_table.shape[0] != B:
+        raise ValueError("block_table needs one row per sequence")
+    if scale is None:
+        scale = head[6] ** -0.5
+    _check(lib().tp_paged_decode(*head, *table, _param(seq_lens, "seq_lens", _torch().int32, B, device), scale, softcap,
+                                 window, *tail, _stream(stream)))
+    return out
+
+
+def tp_paged_prefill(q, k_cache, v_cache, block_table, cu_seqlens, seq_lens, prefix_lens=None, scale=None,
+                     softcap: float = 0.0, window: int = 0, out=None, stream=None):
+    """Causal attention of ragged chunks over the paged caches: rows
+    cu_seqlens[b] .. cu_seqlens[b + 1] - 1 of q are the last positions of
+    sequence b.  Returns o as tp_paged_decode."""
+    i32 = _torch().int32
+    out, device, T, head, table, tail = _attention(q, k_cache, v_cache, block_table, out)
+    B = block_table.shape[0]
+    if scale is None:
+        scale = head[6] ** -0.5
+    _check(lib().tp_paged_prefill(*head, B, *table, _param(cu_seqlens, "cu_seqlens", i32, B + 1, device),
+                                  _param(seq_lens, "seq_lens", i32, B, device),
+                                  _param(prefix_lens, "prefix_lens", i32, B, device), scale, softcap, window, *tail,
+                                  _stream(stream)))
+    return out
+
+
+def tp_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, tokens=None, logprobs=None,
+              stream=None):
+    """Draws one token per row of ``logits`` (B, V) with the given uniform
+    numbers ``u`` (B); returns (tokens int64 (B), logprobs float32 (B))."""
+    torch = _torch()
+    _rowmajor(logits, "logits")
+    B, V = logits.shape
+    device, f32 = logits.device, torch.float32
+    if tokens is None:
+        tokens = torch.empty((B,), dtype=torch.int64, device=device)
+    if logprobs is None:
+        logprobs = torch.empty((B,), dtype=f32, device=device)
+    _check(lib().tp_sample(logits.data_ptr(), B, V, logits.stride(0) if B > 1 else V, _dtype_code(logits.dtype),
+                           _param(u, "u", f32, B, device), _param(temperature, "temperature", f32, B, device),
+                           _param(top_k, "top_k", torch.int32, B, device), _param(top_p, "top_p", f32, B, device),
+                           _param(min_p, "min_p", f32, B, device), _param(tokens, "tokens", torch.int64, B, device),
+                           _param(logprobs, "logprobs", f32, B, device), _stream(stream)))
+    return tokens, logprobs

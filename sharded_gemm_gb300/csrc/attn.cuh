@@ -1,0 +1,91 @@
+// attn.cuh -- what the attention-side kernels share: the arguments of the
+// append, the two paged attentions and the token draw, and small device helpers.
+//
+// The paged cache of one rank is (pages, Hk, page, D): a page holds `page`
+// consecutive positions of one sequence, and within a page each key-value
+// head's positions lie side by side, so 16 positions of a head are one
+// contiguous block.  `ld_page` is the distance in elements between pages
+// (Hk * page * D, or more when keys and values share an allocation).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "tp_internal.h"
+
+namespace tp {
+
+struct AppendArgs {
+  const void *qkv[kMaxShards];
+  void *q[kMaxShards], *k_cache[kMaxShards], *v_cache[kMaxShards];
+  const float *q_norm, *k_norm;  // nullable, (D)
+  const float *rope;             // nullable, (rope_rows, rot): cosines, then sines
+  const int32_t *positions;      // (T), read where rope is given
+  const int64_t *slots;          // (T)
+  int64_t T, ld, ldq, pages, ld_page, rope_rows;
+  int N, Hq, Hk, D, page, rot, interleaved;
+  int in_dt, dt;
+  float eps;
+  int *status;
+};
+
+struct AttnArgs {
+  const void *q[kMaxShards], *k_cache[kMaxShards], *v_cache[kMaxShards];
+  void *o[kMaxShards];
+  const int32_t *block_table;  // (B, width), row stride ld_table
+  const int32_t *seq_lens;     // (B)
+  const int32_t *cu_seqlens;   // (B + 1), or null: one query token per sequence
+  const int32_t *prefix_lens;  // nullable, (B)
+  int64_t T, B, ldq, ldo, pages, ld_page, ld_table, width;
+  int N, Hq, Hk, D, page, page_log2;
+  int dt, window;              // window 0: none
+  float scale, softcap;        // softcap 0: none
+  int *status;
+};
+
+struct SampleArgs {
+  const void *logits;
+  const float *u, *temperature, *top_p, *min_p;  // all but u nullable
+  const int32_t *top_k;                          // nullable
+  int64_t *tokens;
+  float *logprobs;  // nullable
+  int64_t B, V, ld;
+  int in_dt;
+};
+
+int launch_append(const AppendArgs &a, cudaStream_t s);
+int launch_attn_simt(const AttnArgs &a, cudaStream_t s);
+int launch_sample(const SampleArgs &a, cudaStream_t s);
+
+#ifdef __CUDACC__
+
+template <typename T>
+struct Half2;  // packed pairs of the 16-bit types
+template <>
+struct Half2<__nv_bfloat16> {
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<uint32_t *>(&v);
+  }
+  static __device__ __forceinline__ float2 unpack(uint32_t u) {
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+  }
+};
+template <>
+struct Half2<__half> {
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<uint32_t *>(&v);
+  }
+  static __device__ __forceinline__ float2 unpack(uint32_t u) {
+    return __half22float2(*reinterpret_cast<__half2 *>(&u));
+  }
+};
+
+// Records a bad value found in device memory (a page, slot or position out of
+// range); the first error wins and tp_query_status() reports it.
+__device__ __forceinline__ void record_bad_value(int *status) { atomicCAS(status, 0, TP_ERR_INVALID_ARG); }
+
+#endif  // __CUDACC__
+
+}  // namespace tp

@@ -1,0 +1,573 @@
+"""GPU parity of the attention-side operators against plain float64 forms.
+
+Tolerances.  With u the unit roundoff of the 16-bit type (2^-8 for bfloat16,
+2^-11 for float16), an attention output is rounded once (u |o|) and each
+softmax term is rounded once before it meets its value (u sum_j p_j |v_j|);
+float32 scores and exponentials add less than 2^-13 of that sum.  A float16
+term below 2^-14 of the largest has an absolute error of 2^-25 instead.
+An appended value is rounded once, after at most 2^-20 of relative error of its
+norm and rotation.
+"""
+import numpy as np
+import pytest
+import torch
+
+import sharded_gemm_gb300 as tp
+from sharded_gemm_gb300 import build as tpbuild
+
+pytestmark = pytest.mark.gpu
+
+U = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}
+NAN = float("nan")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    tpbuild.build()
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    yield
+    tp.tp_set_policy(tp.TP_POLICY_AUTO)
+
+
+@pytest.fixture(params=[tp.TP_POLICY_AUTO, tp.TP_POLICY_SIMT], ids=["auto", "simt"])
+def policy(request):
+    tp.tp_set_policy(request.param)
+    yield request.param
+    tp.tp_set_policy(tp.TP_POLICY_AUTO)
+
+
+def status_ok():
+    torch.cuda.synchronize()
+    assert tp.tp_query_status() == 0
+
+
+# ------------------------------------------------------------------ append
+def append_ref(x, Hq, Hk, D, qn, kn, eps, rope, pos, interleaved):
+    """(q, k, v) of x (T, (Hq + 2 Hk) D) in float64."""
+    x = x.double().cpu().reshape(len(x), Hq + 2 * Hk, D)
+    y = x[:, :Hq + Hk].clone()
+    for lo, hi, g in ((0, Hq, qn), (Hq, Hq + Hk, kn)):
+        if g is not None:
+            z = y[:, lo:hi]
+            y[:, lo:hi] = z / torch.sqrt(z.pow(2).mean(-1, keepdim=True) + eps) * g.double().cpu()
+    if rope is not None:
+        rot = rope.shape[1]
+        row = rope.double().cpu()[pos.long().cpu()]
+        c, s = row[:, None, :rot // 2], row[:, None, rot // 2:]
+        ia = torch.arange(rot // 2) * 2 if interleaved else torch.arange(rot // 2)
+        ib = ia + 1 if interleaved else ia + rot // 2
+        a, b = y[..., ia].clone(), y[..., ib].clone()
+        y[..., ia], y[..., ib] = a * c - b * s, b * c + a * s
+    return y[:, :Hq], y[:, Hq:], x[:, Hq + Hk:]
+
+
+def rope_table(rows, rot):
+    ang = np.arange(rows)[:, None] * 10000.0 ** (-np.arange(rot // 2) * 2.0 / rot)
+    return torch.from_numpy(np.concatenate([np.cos(ang), np.sin(ang)], 1).astype(np.float32)).cuda()
+
+
+@pytest.mark.parametrize("T,N,Hq,Hk,D,page,rot,inter,norm,in_dt,dt", [
+    (1, 1, 1, 1, 64, 16, 64, False, True, torch.bfloat16, torch.bfloat16),
+    (1, 2, 32, 8, 128, 16, 128, False, True, torch.bfloat16, torch.bfloat16),
+    (37, 3, 6, 2, 64, 32, 32, True, False, torch.float32, torch.float16),
+    (37, 1, 5, 5, 128, 64, 16, False, True, torch.float16, torch.float16),
+    (333, 2, 7, 1, 128, 256, 48, True, True, torch.float32, torch.bfloat16),
+    (1025, 4, 12, 3, 64, 16, 0, False, True, torch.bfloat16, torch.bfloat16),
+    (700, 1, 4, 4, 128, 128, 128, False, False, torch.float16, torch.bfloat16)])
+def test_append(T, N, Hq, Hk, D, page, rot, inter, norm, in_dt, dt):
+    g = torch.Generator(device="cuda").manual_seed(T + N)
+    rng = np.random.default_rng(T * N)
+    pages = -(-T // page) + 3
+    wide = (Hq + 2 * Hk) * D
+    qkv = [torch.randn((T, wide), generator=g, device="cuda").to(in_dt) for _ in range(N)]
+    kc = torch.randn((N, pages, Hk, page, D), generator=g, device="cuda").to(dt)
+    vc = torch.randn((N, pages, Hk, page, D), generator=g, device="cuda").to(dt)
+    slots = torch.from_numpy(rng.permutation(pages * page)[:T].astype(np.int64)).cuda()
+    if T > 4:
+        slots[3] = -1  # padding
+    pos = torch.from_numpy(rng.integers(0, 500, T).astype(np.int32)).cuda()
+    rope = rope_table(500, rot) if rot else None
+    qn = torch.rand(D, generator=g, device="cuda") + 0.5 if norm else None
+    kn = torch.rand(D, generator=g, device="cuda") + 0.5 if norm else None
+    k0, v0 = kc.clone(), vc.clone()
+    q = tp.tp_qkv_append(qkv, kc, vc, slots, positions=pos, rope=rope, q_norm=qn, k_norm=kn, eps=1e-5, interleaved=inter)
+    status_ok()
+    live = slots >= 0
+    at, off = slots[live] // page, slots[live] % page
+    for r in range(N):
+        rq, rk, rv = append_ref(qkv[r], Hq, Hk, D, qn, kn, 1e-5, rope, pos, inter)
+        tol = U[dt] + 2.0 ** -20
+        got = q[r].double().cpu().reshape(T, Hq, D)
+        # the rotated value's own size bounds the float32 error, its pair's size that of the sum
+        big = rq.abs().amax(-1, keepdim=True)
+        assert ((got - rq).abs() <= U[dt] * rq.abs() + 2.0 ** -20 * big + 2.0 ** -24).all()
+        gk = kc[r][at, :, off].double().cpu()
+        rk, rv = rk[live.cpu()], rv[live.cpu()]
+        assert ((gk - rk).abs() <= U[dt] * rk.abs() + 2.0 ** -20 * rk.abs().amax(-1, keepdim=True) + 2.0 ** -24).all()
+        assert torch.equal(vc[r][at, :, off].cpu(), rv.to(dt)), tol
+        k0[r][at, :, off], v0[r][at, :, off] = kc[r][at, :, off], vc[r][at, :, off]
+    assert torch.equal(kc, k0) and torch.equal(vc, v0)  # nothing else was written
+
+
+def test_append_strides_and_unaligned_rows():
+    T, Hq, Hk, D, page = 19, 3, 1, 64, 16
+    g = torch.Generator(device="cuda").manual_seed(5)
+    wide = (Hq + 2 * Hk) * D
+    buf = torch.randn((T, wide + 3), generator=g, device="cuda").to(torch.bfloat16)
+    qkv = buf[:, 1:wide + 1]  # odd row stride, base not 16-byte aligned
+    kv = torch.zeros((4, 2, Hk, page, D), dtype=torch.bfloat16, device="cuda")  # keys and values of a page together
+    obuf = torch.zeros((T, Hq * D + 5), dtype=torch.bfloat16, device="cuda")
+    slots = torch.arange(T, device="cuda") + 20
+    got = tp.tp_qkv_append([qkv], [kv[:, 0]], [kv[:, 1]], slots, out=[obuf[:, 3:3 + Hq * D]])[0]
+    status_ok()
+    assert torch.equal(got, qkv[:, :Hq * D])
+    assert torch.equal(kv[slots // page, 0, 0, slots % page], qkv[:, Hq * D:(Hq + 1) * D])
+    assert torch.equal(kv[slots // page, 1, 0, slots % page], qkv[:, (Hq + 1) * D:])
+    assert (obuf[:, :3] == 0).all() and (obuf[:, 3 + Hq * D:] == 0).all()
+
+
+def test_append_bad_slot_and_position_are_recorded():
+    qkv = torch.ones((2, 3 * 64), dtype=torch.bfloat16, device="cuda")
+    kc = torch.zeros((2, 1, 16, 64), dtype=torch.bfloat16, device="cuda")
+    vc = torch.zeros_like(kc)
+    pos = torch.zeros(2, dtype=torch.int32, device="cuda")
+    tp.tp_qkv_append([qkv], [kc], [vc], torch.tensor([0, 32], device="cuda"), positions=pos)
+    assert tp.tp_query_status() == tp.TP_ERR_INVALID_ARG
+    assert (vc[1] == 0).all() and (vc[0, :, 1:] == 0).all() and (vc[0, :, 0] == 1).all()
+    tp.tp_qkv_append([qkv], [kc], [vc], torch.tensor([0, 1], device="cuda"), positions=pos + 9, rope=rope_table(9, 64))
+    assert tp.tp_query_status() == tp.TP_ERR_INVALID_ARG
+    assert tp.tp_query_status() == 0
+
+
+# ------------------------------------------------------------------ attention
+def paged(lens, N, Hk, D, page, dt, seed, fill=NAN, spare=2, std=1.0):
+    """Caches whose rows outside every sequence hold `fill`, the block table (unused entries -1) and each
+    sequence's keys and values (N, Hk, len, D)."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    rng = np.random.default_rng(seed)
+    need = [-(-n // page) for n in lens]
+    pages = sum(need) + spare
+    ids = rng.permutation(pages)[:sum(need)]
+    width = max(need + [0]) + 1
+    table = np.full((len(lens), width), -1, np.int32)
+    kc = torch.full((N, pages, Hk, page, D), fill, device="cuda").to(dt)
+    vc = torch.full((N, pages, Hk, page, D), fill, device="cuda").to(dt)
+    kv, at = [], 0
+    for b, n in enumerate(lens):
+        mine = ids[at:at + need[b]]
+        at += need[b]
+        table[b, :need[b]] = mine
+        k = (torch.randn((N, Hk, n, D), generator=g, device="cuda") * std).to(dt)
+        v = torch.randn((N, Hk, n, D), generator=g, device="cuda").to(dt)
+        for i, p in enumerate(mine):
+            m = min(page, n - i * page)
+            kc[:, p, :, :m], vc[:, p, :, :m] = k[:, :, i * page:i * page + m], v[:, :, i * page:i * page + m]
+        kv.append((k, v))
+    return kc, vc, torch.from_numpy(table).cuda(), kv
+
+
+def attn_ref(q, k, v, seen, scale, cap):
+    """q (R, G, D), k / v (n, D), seen (R, n): (o, sum_j p_j |v_j|) in float64, zero where a row sees nothing."""
+    s = torch.einsum("rgd,nd->rgn", q.double(), k.double()) * scale
+    if cap:
+        s = cap * torch.tanh(s / cap)
+    s = s.masked_fill(~seen[:, None], -float("inf"))
+    p = torch.nan_to_num(torch.softmax(s, -1), nan=0.0) if s.shape[-1] else s
+    return torch.einsum("rgn,nd->rgd", p, v.double()), torch.einsum("rgn,nd->rgd", p, v.double().abs())
+
+
+def check_attention(got, q, kv, rows, lens, Hq, Hk, D, dt, scale, cap, window, prefix=None):
+    """got, q (N, T, Hq D); rows[b] = (first row, rows)."""
+    N, G = q.shape[0], Hq // Hk
+    assert torch.isfinite(got.float()).all()
+    for b, n in enumerate(lens):
+        t0, m = rows[b]
+        pos = n - m + torch.arange(m, device="cuda")[:, None]
+        j = torch.arange(n, device="cuda")[None]
+        seen = j <= pos
+        if window:
+            seen = seen & (j > pos - window)
+        if prefix is not None:
+            seen = seen | (j < prefix[b])
+        for r in range(N):
+            for h in range(Hk):
+                qq = q[r, t0:t0 + m].reshape(m, Hq, D)[:, h * G:(h + 1) * G]
+                ref, mass = attn_ref(qq, kv[b][0][r, h], kv[b][1][r, h], seen, scale, cap)
+                o = got[r, t0:t0 + m].reshape(m, Hq, D)[:, h * G:(h + 1) * G].double()
+                tol = U[dt] * ref.abs() + (U[dt] + 2.0 ** -13) * mass + 2.0 ** -24
+                if dt == torch.float16:
+                    tol = tol + n * 2.0 ** -25 * 6
+                bad = (o - ref).abs() > tol
+                assert not bad.any(), (b, r, h, float(((o - ref).abs() / tol).max()))
+                assert (o[~seen.any(1)] == 0).all()
+
+
+def run_decode(lens, N, Hq, Hk, D, page, dt, cap=0.0, window=0, seed=0, std=1.0):
+    kc, vc, table, kv = paged(lens, N, Hk, D, page, dt, seed, std=std)
+    B = len(lens)
+    q = torch.randn((N, B, Hq * D), device="cuda", generator=torch.Generator(device="cuda").manual_seed(seed + 1)).to(dt)
+    seq = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    o = tp.tp_paged_decode(q, kc, vc, table, seq, softcap=cap, window=window)
+    status_ok()
+    check_attention(o, q, kv, [(b, 1) for b in range(B)], lens, Hq, Hk, D, dt, D ** -0.5, cap, window)
+    return o, (q, kc, vc, table, seq)
+
+
+BF, F16 = torch.bfloat16, torch.float16
+
+
+@pytest.mark.parametrize("lens,N,Hq,Hk,D,page,dt,cap,window", [
+    ([1], 1, 1, 1, 128, 16, BF, 0.0, 0),
+    ([0], 1, 4, 2, 64, 16, BF, 0.0, 0),
+    ([0, 0, 17, 0], 2, 4, 2, 128, 16, F16, 0.0, 0),
+    ([1, 15, 16, 17, 31, 127, 128, 129, 255, 257], 1, 8, 2, 128, 16, BF, 0.0, 0),
+    ([1, 2, 63, 64, 65, 300], 3, 6, 2, 64, 32, F16, 0.0, 0),
+    ([517], 1, 32, 8, 128, 16, BF, 0.0, 0),
+    ([1000, 3, 0, 777], 2, 16, 1, 128, 256, BF, 0.0, 0),
+    ([1000, 3, 0, 777], 2, 9, 1, 64, 64, BF, 0.0, 0),
+    ([400, 90], 1, 40, 2, 128, 128, F16, 0.0, 0),
+    ([300, 41], 1, 71, 1, 64, 16, BF, 0.0, 0),
+    ([2000, 1999, 100, 5], 2, 5, 5, 128, 64, F16, 20.0, 0),
+    ([2000, 1999, 100, 5, 0], 1, 14, 2, 64, 16, BF, 0.0, 100),
+    ([513, 1, 16, 17], 1, 8, 8, 128, 32, BF, 5.0, 1),
+    ([513, 129, 16, 17], 4, 3, 3, 64, 128, F16, 50.0, 16),
+    ([9001], 1, 2, 1, 128, 64, BF, 0.0, 0),
+    ([20000, 1], 1, 8, 1, 64, 16, F16, 0.0, 0)])
+def test_decode(policy, lens, N, Hq, Hk, D, page, dt, cap, window):
+    run_decode(lens, N, Hq, Hk, D, page, dt, cap, window)
+
+
+def test_decode_many_sequences(policy):
+    rng = np.random.default_rng(3)
+    run_decode([int(n) for n in rng.integers(0, 90, 700)], 1, 4, 2, 64, 16, BF)
+
+
+def test_decode_large_scores(policy):
+    run_decode([300, 33, 700], 1, 8, 2, 128, 16, BF, std=30.0)
+
+
+def test_decode_peak_at_the_end_and_the_front(policy):
+    """The running maximum rises late, and falls: the sums have to be rescaled, and not by a stale maximum."""
+    D, n = 64, 640
+    for peak in (0, 5, 127, 128, 639):
+        kc, vc, table, kv = paged([n], 1, 1, D, 16, F16, seed=peak)
+        k = kv[0][0]
+        k.mul_(0.01)
+        k[0, 0, peak] = 4.0
+        for i in range(n // 16):
+            kc[0, table[0, i], 0] = k[0, 0, 16 * i:16 * i + 16]
+        q = torch.full((1, 1, D), 2.0, dtype=F16, device="cuda")
+        o = tp.tp_paged_decode(q, kc, vc, table, torch.tensor([n], dtype=torch.int32, device="cuda"))
+        status_ok()
+        check_attention(o, q, kv, [(0, 1)], [n], 1, 1, D, F16, D ** -0.5, 0.0, 0)
+
+
+def test_decode_repeats_bit_for_bit():
+    o, args = run_decode([3000, 1, 700, 0, 64], 2, 8, 2, 128, 64, BF)
+    for _ in range(4):
+        assert torch.equal(tp.tp_paged_decode(*args), o)
+
+
+def test_decode_lists_strides_other_stream_and_prepare():
+    lens, N, Hq, Hk, D, page = [77, 300, 16], 2, 8, 2, 64, 16
+    o, (q, kc, vc, table, seq) = run_decode(lens, N, Hq, Hk, D, page, BF)
+    B, P = len(lens), kc.shape[1]
+    kv = [torch.zeros((P, 2, Hk, page, D), dtype=BF, device="cuda") for _ in range(N)]
+    qw = [torch.zeros((B, Hq * D + 7), dtype=BF, device="cuda") for _ in range(N)]
+    ow = [torch.zeros((B, Hq * D + 9), dtype=BF, device="cuda") for _ in range(N)]
+    wide = torch.full((B, table.shape[1] + 3), -1, dtype=torch.int32, device="cuda")
+    wide[:, :table.shape[1]] = table
+    for r in range(N):
+        kv[r][:, 0], kv[r][:, 1], qw[r][:, 5:5 + Hq * D] = kc[r], vc[r], q[r]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    args = ([x[:, 5:5 + Hq * D] for x in qw], [x[:, 0] for x in kv], [x[:, 1] for x in kv], wide[:, :table.shape[1]], seq)
+    out = [x[:, 1:1 + Hq * D] for x in ow]
+    call = tp.prepare(tp.tp_paged_decode, *args, out=out)
+    call(s)
+    s.synchronize()
+    for r in range(N):
+        assert torch.equal(out[r], o[r])
+        assert (ow[r][:, 0] == 0).all() and (ow[r][:, 1 + Hq * D:] == 0).all()
+
+
+def test_decode_in_a_graph():
+    o, args = run_decode([3000, 1, 700, 0, 64], 2, 8, 2, 128, 64, BF)
+    out = torch.zeros_like(o)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    tp.tp_paged_decode(*args, out=out, stream=s)  # the stream's workspace
+    s.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        tp.tp_paged_decode(*args, out=out, stream=s)
+    out.zero_()
+    for _ in range(2):
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, o)
+
+
+def test_decode_bad_page_and_length_are_recorded(policy):
+    _, (q, kc, vc, table, seq) = run_decode([40, 20], 1, 2, 1, 64, 16, BF)
+    for bad in (-1, kc.shape[1], 1 << 30):
+        t2 = table.clone()
+        t2[0, 1] = bad
+        tp.tp_paged_decode(q, kc, vc, t2, seq)
+        assert tp.tp_query_status() == tp.TP_ERR_INVALID_ARG
+    tp.tp_paged_decode(q, kc, vc, table, seq + 100000)
+    assert tp.tp_query_status() == tp.TP_ERR_INVALID_ARG
+    tp.tp_paged_decode(q, kc, vc, table, seq - 100000)  # a negative length is an empty sequence
+    torch.cuda.synchronize()
+    assert tp.tp_query_status() in (0, tp.TP_ERR_INVALID_ARG)
+    tp.tp_paged_decode(q, kc, vc, table, seq)
+    assert tp.tp_query_status() == 0
+
+
+def test_a_cache_beyond_32_bit_offsets():
+    """Pages whose byte and element offsets pass 2^32 (a 17 GB key cache)."""
+    Hk, page, D = 8, 256, 128
+    pages = (1 << 33) // (Hk * page * D) + 2
+    kc = torch.zeros((pages, Hk, page, D), dtype=BF, device="cuda")
+    vc = torch.zeros_like(kc)
+    q = torch.randn((1, 1, Hk * D), device="cuda").to(BF)
+    x = torch.randn((1, 300, 3 * Hk * D), device="cuda").to(BF)
+    slots = torch.cat([torch.arange(256, device="cuda") + (pages - 1) * page, torch.arange(44, device="cuda") + page])
+    tp.tp_qkv_append(x, [kc], [vc], slots)
+    status_ok()
+    k, v = (x[0, :, i * Hk * D:(i + 1) * Hk * D].view(300, Hk, D).transpose(0, 1) for i in (1, 2))
+    assert torch.equal(kc[pages - 1], k[:, :256]) and torch.equal(vc[pages - 1], v[:, :256])
+    assert torch.equal(kc[1, :, :44], k[:, 256:]) and (kc[1, :, 44:] == 0).all()
+    table = torch.tensor([[pages - 1, 1]], dtype=torch.int32, device="cuda")
+    for chunk in (False, True):
+        n = torch.tensor([300], dtype=torch.int32, device="cuda")
+        if chunk:
+            o = tp.tp_paged_prefill(q, [kc], [vc], table, torch.tensor([0, 1], dtype=torch.int32, device="cuda"), n)
+        else:
+            o = tp.tp_paged_decode(q, [kc], [vc], table, n)
+        status_ok()
+        check_attention(o, q, [(k[None], v[None])], [(0, 1)], [300], Hk, Hk, D, BF, D ** -0.5, 0.0, 0)
+
+
+def run_prefill(chunks, N, Hq, Hk, D, page, dt, cap=0.0, window=0, prefix=None, seed=0, std=1.0):
+    """chunks: (new tokens, cached before them) of each sequence."""
+    lens = [m + c for m, c in chunks]
+    kc, vc, table, kv = paged(lens, N, Hk, D, page, dt, seed, std=std)
+    cu = np.concatenate([[0], np.cumsum([m for m, _ in chunks])]).astype(np.int32)
+    T = int(cu[-1])
+    q = torch.randn((N, T, Hq * D), device="cuda", generator=torch.Generator(device="cuda").manual_seed(seed + 1)).to(dt)
+    seq = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    pre = torch.tensor(prefix, dtype=torch.int32, device="cuda") if prefix is not None else None
+    args = (q, kc, vc, table, torch.from_numpy(cu).cuda(), seq, pre)
+    o = tp.tp_paged_prefill(*args, softcap=cap, window=window)
+    status_ok()
+    check_attention(o, q, kv, [(int(cu[b]), chunks[b][0]) for b in range(len(chunks))], lens, Hq, Hk, D, dt, D ** -0.5,
+                    cap, window, prefix)
+    return o, args
+
+
+@pytest.mark.parametrize("chunks,N,Hq,Hk,D,page,dt,cap,window,prefix", [
+    ([(1, 0)], 1, 1, 1, 128, 16, BF, 0.0, 0, None),
+    ([(1, 40)], 1, 8, 2, 64, 16, F16, 0.0, 0, None),
+    ([(0, 5), (3, 0), (0, 0), (20, 0)], 2, 4, 2, 128, 16, BF, 0.0, 0, None),
+    ([(127, 0), (128, 0), (129, 0)], 1, 2, 2, 128, 64, BF, 0.0, 0, None),
+    ([(150, 60), (7, 90), (33, 1), (64, 64)], 2, 8, 2, 64, 16, F16, 20.0, 0, None),
+    ([(300, 0)], 1, 7, 1, 128, 128, BF, 0.0, 0, None),
+    ([(300, 200)], 1, 5, 1, 64, 256, BF, 0.0, 0, None),
+    ([(77, 300)], 2, 48, 3, 128, 32, F16, 0.0, 0, None),
+    ([(40, 3)], 1, 130, 1, 64, 16, BF, 0.0, 0, None),
+    ([(600, 100), (1, 500)], 1, 8, 2, 128, 16, BF, 0.0, 100, None),
+    ([(600, 0)], 1, 4, 4, 64, 64, F16, 30.0, 1, None),
+    ([(300, 100), (90, 0), (5, 200)], 1, 8, 2, 128, 16, BF, 0.0, 0, [350, 0, 1]),
+    ([(700, 100), (90, 0)], 1, 4, 1, 64, 32, BF, 0.0, 33, [90, 90]),
+    ([(1030, 2000)], 1, 4, 1, 128, 64, BF, 0.0, 0, None)])
+def test_prefill(policy, chunks, N, Hq, Hk, D, page, dt, cap, window, prefix):
+    run_prefill(chunks, N, Hq, Hk, D, page, dt, cap, window, prefix)
+
+
+def test_prefill_large_scores(policy):
+    run_prefill([(260, 100), (33, 0)], 1, 8, 2, 128, 16, BF, std=30.0)
+
+
+def test_prefill_many_sequences(policy):
+    rng = np.random.default_rng(4)
+    run_prefill([(int(a), int(b)) for a, b in zip(rng.integers(0, 9, 300), rng.integers(0, 60, 300))], 1, 4, 2, 64, 16, BF)
+
+
+def test_prefill_rows_before_the_first_position_and_of_no_sequence(policy):
+    """More new tokens than positions: the first rows see nothing.  Rows outside cu_seqlens are zero."""
+    kc, vc, table, kv = paged([10, 30], 1, 1, 64, 16, BF, seed=8)
+    q = torch.randn((1, 60, 128), device="cuda").to(BF)
+    cu = torch.tensor([3, 20, 50], dtype=torch.int32, device="cuda")
+    seq = torch.tensor([10, 30], dtype=torch.int32, device="cuda")
+    o = tp.tp_paged_prefill(q, kc, vc, table, cu, seq, out=torch.full_like(q, NAN))
+    status_ok()
+    assert (o[0, :3] == 0).all() and (o[0, 50:] == 0).all()
+    check_attention(o, q, kv, [(3, 17), (20, 30)], [10, 30], 2, 1, 64, BF, 0.125, 0.0, 0)
+
+
+def test_prefill_of_one_token_is_decode():
+    lens = [77, 300, 16]
+    o, (q, kc, vc, table, seq) = run_decode(lens, 2, 8, 2, 64, 16, BF)
+    cu = torch.arange(4, dtype=torch.int32, device="cuda")
+    o2 = tp.tp_paged_prefill(q, kc, vc, table, cu, seq)
+    status_ok()
+    assert ((o - o2).float().abs() <= 2 * U[BF] * (o.float().abs() + 1)).all()
+
+
+def test_prefill_strides_other_stream():
+    o, (q, kc, vc, table, cu, seq, _) = run_prefill([(50, 20), (200, 0)], 2, 4, 2, 128, 16, F16)
+    N, T, C = q.shape
+    qw = torch.zeros((N, T, C + 8), dtype=F16, device="cuda")
+    qw[:, :, :C] = q
+    qo = torch.zeros((N, T, C + 1), dtype=F16, device="cuda")
+    qo[:, :, 1:] = q
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for view in (qw[:, :, :C], qo[:, :, 1:]):
+        ow = torch.zeros((N, T, C + 3), dtype=F16, device="cuda")
+        torch.cuda.synchronize()
+        tp.tp_paged_prefill(view, kc, vc, table, cu, seq, out=ow[:, :, 2:2 + C], stream=s)
+        s.synchronize()
+        assert torch.equal(ow[:, :, 2:2 + C], o)
+        assert (ow[:, :, :2] == 0).all() and (ow[:, :, 2 + C:] == 0).all()
+
+
+def test_prefill_bad_page_and_length_are_recorded(policy):
+    _, (q, kc, vc, table, cu, seq, _) = run_prefill([(40, 0), (20, 4)], 1, 2, 1, 64, 16, BF)
+    t2 = table.clone()
+    t2[0, 1] = kc.shape[1]
+    tp.tp_paged_prefill(q, kc, vc, t2, cu, seq)
+    assert tp.tp_query_status() == tp.TP_ERR_INVALID_ARG
+    tp.tp_paged_prefill(q, kc, vc, table, cu, seq + 100000)
+    assert tp.tp_query_status() == tp.TP_ERR_INVALID_ARG
+    tp.tp_paged_prefill(q, kc, vc, table, cu, seq)
+    assert tp.tp_query_status() == 0
+
+
+# ------------------------------------------------------------------ sampling
+def kept_set(x, t, k, p, m, slack):
+    """Indices that may be kept and those that must be, in float64, `slack` the allowed relative error of a share."""
+    order = np.argsort(-x, kind="stable")
+    e = np.exp((x[order] - x[order[0]]) / t)
+    n = len(x) if k <= 0 else min(k, len(x))
+    before = np.cumsum(e[:n]) - e[:n]
+    total = e[:n].sum()
+
+    def cut(sign):
+        keep = np.ones(n, bool) if p >= 1 else before < (p + sign * slack) * total
+        keep[0] = True
+        keep &= e[:n] >= min(m, 1.0) * (1 - sign * slack)
+        return set(order[:n][keep].tolist())
+    return cut(+1), cut(-1)
+
+
+def check_draw(x, token, t, k, p, m, u, slack=2e-5):
+    x = np.where(np.isnan(x), -np.inf, np.minimum(x, np.finfo(np.float32).max)).astype(np.float64)
+    if t < 2.0 ** -20:
+        t, k = 1.0, 1
+    may, must = kept_set(x, t, k, p, m, slack)
+    assert token in may
+    w = np.exp((x - x.max()) / t)
+    hi = sum(w[i] for i in may if i <= token) / sum(w[i] for i in must)
+    lo = sum(w[i] for i in must if i < token) / sum(w[i] for i in may)
+    assert lo - slack <= u <= hi + slack, (lo, u, hi)
+
+
+@pytest.mark.parametrize("B,V,dt", [(1, 1, torch.float32), (3, 2, torch.float16), (5, 31, torch.bfloat16),
+                                    (64, 1000, torch.float32), (40, 5001, torch.bfloat16), (9, 50272, torch.float32),
+                                    (7, 50272, torch.float16), (3, 200003, torch.float32), (2, 1 << 20, torch.bfloat16)])
+def test_sample(B, V, dt):
+    rng = np.random.default_rng(B + V)
+    x = torch.from_numpy(rng.standard_normal((B, V + 3)).astype(np.float32) * 2.5).cuda().to(dt)[:, 1:V + 1]
+    u = rng.random(B, dtype=np.float32)
+    t = rng.choice(np.float32([0, 0.3, 0.7, 1, 1.5, 5]), B).astype(np.float32)
+    k = rng.choice([0, -1, 1, 2, 50, 1000, 1 << 30], B).astype(np.int32)
+    p = rng.choice(np.float32([1, 0, 1e-4, 0.3, 0.9, 0.999, 2]), B).astype(np.float32)
+    m = rng.choice(np.float32([0, 0, 0.01, 0.3, 1, 7]), B).astype(np.float32)
+    dev = [torch.from_numpy(a).cuda() for a in (u, t, k, p, m)]
+    tok, lp = tp.tp_sample(x, *dev)
+    status_ok()
+    xh = x.double().cpu().numpy()
+    tok, lp = tok.cpu().numpy(), lp.cpu().numpy()
+    for b in range(B):
+        check_draw(xh[b], int(tok[b]), float(t[b]), int(k[b]), float(p[b]), float(m[b]), float(u[b]))
+        z = xh[b] - xh[b].max()
+        ref = z[tok[b]] - np.log(np.exp(z).sum())
+        assert abs(lp[b] - ref) <= 1e-5 * (1 + abs(ref))
+
+
+def test_sample_defaults_and_repeat():
+    x = torch.randn((33, 777), device="cuda")
+    u = torch.rand(33, device="cuda")
+    tok, lp = tp.tp_sample(x, u)
+    for b in range(33):
+        check_draw(x[b].double().cpu().numpy(), int(tok[b]), 1.0, 0, 1.0, 0.0, float(u[b]))
+    again, lp2 = tp.tp_sample(x, u)
+    assert torch.equal(tok, again) and torch.equal(lp, lp2)
+
+
+@pytest.mark.parametrize("V", [4, 1000, 50000, 200000])
+def test_sample_ties_go_to_the_lowest_index(V):
+    """All logits equal: every weight is 2^40, so every filter and draw has one exact answer."""
+    B = 6
+    x = torch.full((B, V), -3.25, device="cuda")
+    x[1] = 0.0
+    x[1, ::2] = -0.0  # one zero
+    n = V // 2
+    k = torch.tensor([1, n, n, 0, 0, n], dtype=torch.int32, device="cuda")
+    p = torch.tensor([1, 1, 0.5, 0.25, 1, 0.5], dtype=torch.float32, device="cuda")
+    u = torch.tensor([0.9, 0.5, 0.999999, 0.999999, 0.5, 0.0], dtype=torch.float32, device="cuda")
+    tok, lp = tp.tp_sample(x, u, top_k=k, top_p=p)
+    part = lambda w, f: int(w) * int(np.float32(f) * np.float32(1 << 24)) >> 24  # noqa: E731
+    want = []
+    for b in range(B):
+        kept = int(k[b]) or V
+        if float(p[b]) < 1:
+            kept = max(1, -(-part(kept << 40, float(p[b])) // (1 << 40)))
+        want.append(part(kept << 40, float(u[b])) >> 40)
+    assert tok.tolist() == want
+    assert np.allclose(lp.cpu().numpy(), -np.log(V), atol=1e-5)
+
+
+def test_sample_masked_and_special_logits():
+    V, inf = 5000, float("inf")
+    x = torch.randn((7, V), device="cuda")
+    x[0] = -inf                      # nothing to draw
+    x[1] = -inf
+    x[1, 4321] = -50.0               # one token left
+    x[2, 100] = inf                  # the largest float: the only one with weight
+    x[3, :] = NAN
+    x[3, 17] = 1.0                   # NaN is never drawn
+    x[4, :] = -inf
+    x[4, [5, 10]] = 0.0
+    x[5] = torch.finfo(torch.float32).min
+    x[5, 4000:] = 0.0
+    x[6, :] = NAN
+    u = torch.tensor([0.5, 0.9, 0.99, 0.3, 0.75, 0.0, 0.1], device="cuda")
+    k = torch.tensor([0, 10, 0, 3, 2, 0, 1], dtype=torch.int32, device="cuda")
+    p = torch.tensor([1, 0.9, 1, 0.5, 0.99, 1, 1], device="cuda")
+    tok, lp = tp.tp_sample(x, u, top_k=k, top_p=p)
+    assert tok.tolist() == [-1, 4321, 100, 17, 10, 4000, -1]
+    lp = lp.tolist()
+    assert lp[0] == -inf and lp[6] == -inf and lp[1] == 0.0 and lp[2] == 0.0 and lp[3] == 0.0
+    assert abs(lp[4] + np.log(2)) < 1e-6
+    # odd parameters: outside [0, 1], NaN
+    x = torch.randn((4, V), device="cuda")
+    u = torch.tensor([-1.0, 1.0, 2.0, NAN], device="cuda")
+    tok, _ = tp.tp_sample(x, u, temperature=torch.tensor([1, 1, 1, NAN], device="cuda"),
+                          top_p=torch.tensor([NAN, 1, 1, 1], device="cuda"),
+                          min_p=torch.tensor([NAN, 0, 0, 0], device="cuda"))
+    assert tok[0] == 0 and tok[3] == int(x[3].argmax())
+    assert tok[1] == tok[2] == V - 1 or tok[1] > V - 50
+
+
+def test_sample_distribution():
+    """20000 draws of one row: each share within five standard deviations of its probability."""
+    V, n = 12, 20000
+    row = torch.linspace(-2, 2, V, device="cuda")
+    u = torch.from_numpy(np.random.default_rng(1).random(n, dtype=np.float32)).cuda()
+    tok, _ = tp.tp_sample(row.expand(n, V).contiguous(), u)
+    prob = torch.softmax(row.double(), 0).cpu().numpy()
+    share = np.bincount(tok.cpu().numpy(), minlength=V) / n
+    assert (np.abs(share - prob) <= 5 * np.sqrt(prob * (1 - prob) / n)).all()
