@@ -54,6 +54,7 @@ struct SampleArgs {
 };
 
 int launch_append(const AppendArgs &a, cudaStream_t s);
+int launch_decode(const AttnArgs &a, cudaStream_t s);
 int launch_attn_simt(const AttnArgs &a, cudaStream_t s);
 int launch_sample(const SampleArgs &a, cudaStream_t s);
 

@@ -129,7 +129,7 @@ int tp_paged_decode(int N, const void *const *q, int64_t B, int64_t ldq, int Hq,
     return rc;
   if (B == 0) return TP_OK;
   if (int rc = need_status(&a.status)) return rc;
-  return launch_attn_simt(a, (cudaStream_t)stream);
+  return simt_policy() ? launch_attn_simt(a, (cudaStream_t)stream) : launch_decode(a, (cudaStream_t)stream);
 }
 
 int tp_paged_prefill(int N, const void *const *q, int64_t T, int64_t ldq, int Hq, int Hk, int D, void *const *k_cache,
