@@ -55,6 +55,7 @@ struct SampleArgs {
 
 int launch_append(const AppendArgs &a, cudaStream_t s);
 int launch_decode(const AttnArgs &a, cudaStream_t s);
+int launch_prefill(const AttnArgs &a, cudaStream_t s);
 int launch_attn_simt(const AttnArgs &a, cudaStream_t s);
 int launch_sample(const SampleArgs &a, cudaStream_t s);
 
@@ -64,6 +65,7 @@ template <typename T>
 struct Half2;  // packed pairs of the 16-bit types
 template <>
 struct Half2<__nv_bfloat16> {
+  static constexpr bool kBf16 = true;
   static __device__ __forceinline__ uint32_t pack(float a, float b) {
     __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<uint32_t *>(&v);
@@ -74,6 +76,7 @@ struct Half2<__nv_bfloat16> {
 };
 template <>
 struct Half2<__half> {
+  static constexpr bool kBf16 = false;
   static __device__ __forceinline__ uint32_t pack(float a, float b) {
     __half2 v = __floats2half2_rn(a, b);
     return *reinterpret_cast<uint32_t *>(&v);

@@ -1,0 +1,697 @@
+// k_pprefill.cu -- tp_paged_prefill on the tensor cores: attention of ragged
+// chunks of tokens over the paged cache.
+//
+// A unit is one sequence, rank, key-value head, group of its query heads and
+// block of tokens: two query tiles of 128 rows, a row being one (token, head),
+// so all query heads of a key-value head share its key and value tiles.  Per
+// key tile of 128 positions and query tile,
+//   S = Q K^T          128 x 128, float32 in tensor memory
+//   P = 2^(S' - m)     S' the scaled (and capped) scores in log2, m the row's
+//                      running maximum; rounded to the 16-bit type, over S
+//   O += P V           128 x D, float32 in tensor memory, P read from there
+// One thread owns one row, so maxima and sums need no exchange.  O is rescaled
+// only where a row's maximum grows by more than 2^8 (the 16-bit terms and the
+// float32 sums have room for that), which after the first tiles is rare.
+//
+// Persistent, one CTA per SM, twelve warps:
+//   warp 0       units (dealt out at run time: their lengths differ) and the
+//                tensor copies of the key and value pages, 128-byte swizzled,
+//                into a ring of tiles;
+//   warp 1       one thread issues every tcgen05.mma: P0 V, Q0 K', P1 V, Q1 K',
+//                so one query tile's softmax runs under the other's products;
+//   warps 2, 3   the next unit's queries into shared memory;
+//   warps 4..11  softmax, rescale and output, one warpgroup per query tile.
+// Rows of a value tile behind the sequence's end (or in pages that are not
+// read) are written as zeros: stale rows never meet a product.
+//
+// Tensor rate bounds long chunks: 4 D flop per visible pair.
+#include "attn.cuh"
+#include "mma16.cuh"
+#include "ptx.cuh"
+
+namespace tp {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kTile = 128;  // rows of a query tile, positions of a key tile
+constexpr float kSlack = 8.0f;
+// Registers a thread: 384 * 168 at launch = 128 * 72 + 256 * 216.
+constexpr int kRegsFew = 72, kRegsMany = 216;
+
+template <int D>
+struct Sh {
+  static constexpr int kTileBytes = kTile * D * 2;
+  static constexpr int kHalf = kTile * 128;  // bytes of a tile's 64-value column block
+  static constexpr int kQBytes = 2 * kTileBytes;
+  static constexpr int kSlots = D == 128 ? 5 : 10;
+  static constexpr int kSmem = kQBytes + kSlots * kTileBytes + 1024;
+};
+
+template <int MAXN>
+struct PrefillArgs {
+  CUtensorMap k[MAXN], v[MAXN];
+  AttnArgs a;
+  int groups, gsize, tpt;  // head groups of a key-value head, heads of a group, tokens of a query tile
+  int box;                 // rows of a page copy
+  int vec_q, vec_o;
+  int *counters;
+  uint64_t wait_ns;
+};
+
+struct Unit {
+  int valid, b, r, h, grp;
+  int tok0, ntok;  // first token (row of q), tokens
+  int pos0;        // its position
+  int to, prefix;  // positions of the sequence; bidirectional ones
+  int seen0;       // no row of the unit sees a position below this
+  int j0;          // first key tile's position
+  int n[2];        // key tiles of the query tiles
+};
+
+struct Control {
+  uint64_t unit_full[2], unit_free[2], q_full[2], q_free[2], s_full[2], p_full[2], o_done[2], drain;
+  uint64_t kv_full[10], kv_free[10];
+  Unit unit[2];
+  uint32_t tmem;
+  int abort;
+};
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// mbar_wait without its out-of-line slow path: a call would spill the scores
+// that the softmax warps hold in registers.
+__device__ __forceinline__ bool wait_inline(uint32_t bar, uint32_t parity, uint64_t limit_ns, int *status,
+                                            volatile int *abort) {
+  bool done = mbar_try_wait(bar, parity);
+  if (!__all_sync(0xffffffffu, done)) {
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t i = 1; !done; ++i) {
+      done = mbar_try_wait(bar, parity);
+      if (done || (i & 31)) continue;
+      if (*abort) break;
+      if (globaltimer_ns() - t0 > limit_ns) {
+        atomicCAS(status, 0, TP_ERR_TIMEOUT);
+        *abort = 1;
+      }
+    }
+    done = __all_sync(0xffffffffu, done);
+  }
+  return done;
+}
+
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// The tokens of sequence b, kept inside q whatever cu_seqlens holds.
+__device__ __forceinline__ void token_range(const AttnArgs &a, int64_t b, int64_t &t0, int64_t &t1) {
+  const int64_t c0 = a.cu_seqlens[b], c1 = a.cu_seqlens[b + 1];
+  t0 = c0 < 0 ? 0 : c0 > a.T ? a.T : c0;
+  t1 = c1 < t0 ? t0 : c1 > a.T ? a.T : c1;
+  if (c0 != t0 || c1 != t1) record_bad_value(a.status);
+}
+
+template <typename T, int D, int MAXN>
+__global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_constant__ PrefillArgs<MAXN> pa) {
+  using S = Sh<D>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Control ctl;
+  const AttnArgs &a = pa.a;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t smem = (smem_u32(smem_raw) + 1023) & ~1023u;
+  uint8_t *smem_gen = smem_raw + (smem - smem_u32(smem_raw));
+  const uint32_t q_smem = smem, kv_smem = smem + S::kQBytes;
+  volatile int *abort = &ctl.abort;
+  const uint64_t limit = pa.wait_ns;
+  // the same answer in every lane of the warp
+  auto wait = [&](uint64_t &bar, uint32_t parity) {
+    return (bool)__all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), parity, limit, a.status, abort));
+  };
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&ctl.unit_full[i]), 1);
+      mbar_init(smem_u32(&ctl.unit_free[i]), 11);  // warps 1..11
+      mbar_init(smem_u32(&ctl.q_full[i]), 64);
+      mbar_init(smem_u32(&ctl.q_free[i]), 1);
+      mbar_init(smem_u32(&ctl.s_full[i]), 1);
+      mbar_init(smem_u32(&ctl.p_full[i]), 4);
+      mbar_init(smem_u32(&ctl.o_done[i]), 1);
+    }
+    mbar_init(smem_u32(&ctl.drain), 1);
+    for (int i = 0; i < S::kSlots; ++i) {
+      mbar_init(smem_u32(&ctl.kv_full[i]), 1);
+      mbar_init(smem_u32(&ctl.kv_free[i]), 1);
+    }
+    ctl.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&ctl.tmem), 512);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl.tmem;
+  griddep_launch_dependents();
+  griddep_wait();
+
+  const int block = 2 * pa.tpt;  // tokens of a unit
+  const int heads_units = a.N * a.Hk * pa.groups;
+
+  if (warp < 4) {
+    regs_down<kRegsFew>();
+    if (warp == 0) {
+      // ---------------------------------------------------------------- units, keys and values
+      int64_t cur_b = 0;
+      long long cur_base = 0;  // units of the sequences before cur_b
+      long long u = blockIdx.x;
+      int slot = 0, seq = 0;
+      unsigned fills = 0;  // ring slots filled so far
+      uint32_t kv_phase = 0;
+      bool ok = true;
+      for (;; ++seq) {
+        // the next unit is asked for before this one's copies
+        long long next = 0;
+        if (lane == 0) next = (long long)gridDim.x + atomicAdd(pa.counters, 1);
+        // find unit u: 32 sequences at a time from the cursor
+        int64_t b = -1;
+        long long base = 0;
+        int64_t t0 = 0, t1 = 0;
+        while (cur_b < a.B) {
+          int64_t x0 = 0, x1 = 0;
+          if (cur_b + lane < a.B) token_range(a, cur_b + lane, x0, x1);
+          long long mine = (x1 - x0 + block - 1) / block * heads_units, run = mine;
+#pragma unroll
+          for (int m = 1; m < 32; m *= 2) {
+            const long long o = __shfl_up_sync(0xffffffffu, run, m);
+            if (lane >= m) run += o;
+          }
+          const uint32_t hit = __ballot_sync(0xffffffffu, cur_base + run > u);
+          if (hit) {
+            const int l = __ffs(hit) - 1;
+            b = cur_b + l;
+            base = cur_base + __shfl_sync(0xffffffffu, run - mine, l);
+            t0 = __shfl_sync(0xffffffffu, x0, l);
+            t1 = __shfl_sync(0xffffffffu, x1, l);
+            break;
+          }
+          cur_base += __shfl_sync(0xffffffffu, run, 31);
+          cur_b += 32;
+        }
+        Unit w;
+        w.valid = b >= 0;
+        if (w.valid) {
+          const long long local = u - base;
+          const int blocks = (int)((t1 - t0 + block - 1) / block);
+          const int hu = (int)(local / blocks);
+          const int qb = blocks - 1 - (int)(local % blocks);  // longest first
+          w.b = (int)b;
+          w.grp = hu % pa.groups;
+          w.h = hu / pa.groups % a.Hk;
+          w.r = hu / pa.groups / a.Hk;
+          w.tok0 = (int)t0 + qb * block;
+          w.ntok = (int)(t1 - w.tok0 < block ? t1 - w.tok0 : block);
+          const int64_t cap = a.width << a.page_log2;
+          int64_t n = a.seq_lens[b];
+          if (n > cap) {
+            n = cap;
+            if (lane == 0) record_bad_value(a.status);
+          }
+          if (n < 0) n = 0;
+          w.to = (int)n;
+          int pre = a.prefix_lens ? a.prefix_lens[b] : 0;
+          w.prefix = pre < 0 ? 0 : pre > w.to ? w.to : pre;
+          w.pos0 = w.to - (int)(t1 - t0) + qb * block;
+          int lo = a.window && w.prefix == 0 ? w.pos0 - a.window + 1 : 0;
+          w.seen0 = lo < 0 ? 0 : lo;
+          w.j0 = w.seen0 & ~(kTile - 1);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int rows = w.ntok - i * pa.tpt < pa.tpt ? w.ntok - i * pa.tpt : pa.tpt;
+            int hi = w.pos0 + i * pa.tpt + rows;  // behind the last row's position
+            if (hi < w.prefix) hi = w.prefix;
+            if (hi > w.to) hi = w.to;
+            w.n[i] = rows > 0 && hi > w.j0 ? (hi - w.j0 + kTile - 1) / kTile : 0;
+          }
+        }
+        const int us = seq & 1;
+        if (seq >= 2) ok = wait(ctl.unit_free[us], ((seq >> 1) - 1) & 1);
+        if (!ok) break;
+        if (lane == 0) {
+          ctl.unit[us] = w;
+          mbar_arrive(smem_u32(&ctl.unit_full[us]));
+        }
+        if (!w.valid) {
+          if (lane == 0) {
+            // out of units: the last CTA to see that clears the counters for the next call
+            // (every CTA's additions to the first are done before its one to the second)
+            __threadfence();
+            if (atomicAdd(pa.counters + 1, 1) == (int)gridDim.x - 1) {
+              __threadfence();
+              atomicExch(pa.counters, 0);
+              atomicExch(pa.counters + 1, 0);
+            }
+          }
+          break;
+        }
+        const int nmax = w.n[0] > w.n[1] ? w.n[0] : w.n[1];
+        const int *table = a.block_table + w.b * a.ld_table;
+        const int pieces = kTile / pa.box;  // page copies of a tile
+        for (int j = 0; j < nmax && ok; ++j) {
+          const int jt = w.j0 + j * kTile;
+          // lane i < pieces: piece i's page, its row in the map, whether it is read, whether all of it is
+          int row = -1;
+          bool part = false;
+          if (lane < pieces) {
+            const int pj = jt + lane * pa.box;
+            if (pj < w.to && pj + pa.box > w.seen0) {
+              const int pg = table[pj >> a.page_log2];
+              if (pg < 0 || pg >= a.pages) {
+                record_bad_value(a.status);
+              } else {
+                row = (int)(pg * (a.ld_page / D) + (int64_t)w.h * a.page + (pj & (a.page - 1)));
+                part = pj + pa.box > w.to;
+              }
+            }
+          }
+          const uint32_t read = __ballot_sync(0xffffffffu, row >= 0);
+          const uint32_t whole = __ballot_sync(0xffffffffu, row >= 0 && !part);
+          for (int kv = 0; kv < 2 && ok; ++kv) {
+            ok = wait(ctl.kv_free[slot], kv_phase ^ 1);
+            if (!ok) break;
+            const uint32_t dst = kv_smem + slot * S::kTileBytes;
+            const uint32_t bar = smem_u32(&ctl.kv_full[slot]);
+            const uint32_t copied = kv ? whole : read;  // hidden keys may hold anything, values not
+            if (kv && whole != (pieces == 32 ? 0xffffffffu : (1u << pieces) - 1)) {
+              // rows of the pieces that are not copied whole: the sequence's own, and zeros
+              uint8_t *gen = smem_gen + S::kQBytes + slot * S::kTileBytes;
+              for (int p = 0; p < pieces; ++p) {
+                if (whole >> p & 1) continue;
+                const int prow = __shfl_sync(0xffffffffu, row, p), pj = jt + p * pa.box;
+                const T *src = static_cast<const T *>(a.v_cache[w.r]) + (int64_t)prow * D;
+                for (int e = lane; e < pa.box * (D / 8); e += 32) {
+                  const int i = e / (D / 8), c = e % (D / 8), tr = p * pa.box + i;
+                  uint4 x = make_uint4(0, 0, 0, 0);
+                  if (prow >= 0 && pj + i < w.to) x = *reinterpret_cast<const uint4 *>(src + (int64_t)i * D + c * 8);
+                  *reinterpret_cast<uint4 *>(gen + (c >> 3) * S::kHalf + tr * 128 + (((c & 7) ^ (tr & 7)) << 4)) = x;
+                }
+              }
+              fence_proxy_async_smem();
+              __syncwarp();
+            }
+            if (lane == 0) mbar_arrive_expect_tx(bar, __popc(copied) * pa.box * D * 2);
+            __syncwarp();
+            if (copied >> lane & 1) {
+#pragma unroll
+              for (int c = 0; c < D / 64; ++c)
+                tma_load_2d(dst + c * S::kHalf + lane * pa.box * 128, kv ? &pa.v[w.r] : &pa.k[w.r], bar, c * 64, row);
+            }
+            if (++slot == S::kSlots) slot = 0, kv_phase ^= 1;
+            ++fills;
+          }
+        }
+        if (!ok) break;
+        u = __shfl_sync(0xffffffffu, next, 0);
+      }
+      if (!ok) {
+        // gave up: the copies in flight still land in this CTA's shared memory
+        for (unsigned i = 0; i < S::kSlots && i < fills; ++i) {
+          const unsigned f = fills - 1 - i;
+          mbar_wait(smem_u32(&ctl.kv_full[f % S::kSlots]), (f / S::kSlots) & 1, limit, a.status, nullptr);
+        }
+        __syncwarp();
+      }
+    } else if (warp == 1) {
+      // ---------------------------------------------------------------- products
+      constexpr uint32_t fmt = sizeof(T) == 2 && Half2<T>::kBf16 ? 1 : 0;
+      constexpr uint32_t id_qk = umma_idesc_f16(fmt, 0, kTile, kTile), id_pv = umma_idesc_f16(fmt, 1, kTile, D);
+      int slot = 0;
+      uint32_t kv_phase = 0, p_phase[2] = {0, 0}, q_phase[2] = {0, 0};
+      bool ok = true;
+      for (int seq = 0; ok; ++seq) {
+        const int us = seq & 1;
+        ok = wait(ctl.unit_full[us], (seq >> 1) & 1);
+        if (!ok) break;
+        const int valid = ctl.unit[us].valid, n0 = ctl.unit[us].n[0], n1 = ctl.unit[us].n[1];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctl.unit_free[us]));
+        if (!valid) break;
+        const int n[2] = {n0, n1};
+        const int nmax = n0 > n1 ? n0 : n1;
+        auto qk = [&](int i, int ks) {  // S_i = Q_i K^T, K in ring slot ks
+          if (lane == 0) {
+            tc_fence_after();
+            const uint32_t qa = q_smem + i * S::kTileBytes, kb = kv_smem + ks * S::kTileBytes;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = (kk / 4) * S::kHalf + (kk % 4) * 32;
+              umma_f16(tmem + i * kTile, umma_desc_sw128(qa + off, 16, 1024), umma_desc_sw128(kb + off, 16, 1024), id_qk,
+                       kk > 0);
+            }
+            umma_commit(smem_u32(&ctl.s_full[i]));
+          }
+          __syncwarp();
+        };
+        auto pv = [&](int i, int vs, bool add) {  // O_i (+)= P_i V, V in ring slot vs
+          if (lane == 0) {
+            tc_fence_after();
+            const uint32_t vb = kv_smem + vs * S::kTileBytes;
+#pragma unroll
+            for (int kk = 0; kk < kTile / 16; ++kk)
+              umma_f16_ts(tmem + 256 + i * D, tmem + i * kTile + kk * 8, umma_desc_sw128(vb + kk * 2048, S::kHalf, 1024),
+                          id_pv, add || kk > 0);
+            umma_commit(smem_u32(&ctl.o_done[i]));
+          }
+          __syncwarp();
+        };
+        auto next_slot = [&]() {
+          if (++slot == S::kSlots) slot = 0, kv_phase ^= 1;
+        };
+        auto release = [&](uint64_t &bar) {
+          if (lane == 0) umma_commit(smem_u32(&bar));
+          __syncwarp();
+        };
+        // first scores
+        int ks = slot;
+        if (nmax > 0) {
+          ok = wait(ctl.kv_full[slot], kv_phase);
+          next_slot();
+        }
+        for (int i = 0; i < 2 && ok; ++i) {
+          ok = wait(ctl.q_full[i], q_phase[i]);  // loaded for every unit, used or not
+          q_phase[i] ^= 1;
+          if (!ok) break;
+          if (n[i] > 0) qk(i, ks);
+          if (n[i] <= 1) release(ctl.q_free[i]);
+        }
+        if (nmax > 0 && ok) release(ctl.kv_free[ks]);
+        for (int j = 0; j < nmax && ok; ++j) {
+          const int vs = slot;
+          ok = wait(ctl.kv_full[vs], kv_phase);
+          if (!ok) break;
+          next_slot();
+          ks = slot;
+          if (j + 1 < nmax) {
+            ok = wait(ctl.kv_full[ks], kv_phase);
+            if (!ok) break;
+            next_slot();
+          }
+          for (int i = 0; i < 2 && ok; ++i) {
+            if (j >= n[i]) continue;
+            ok = wait(ctl.p_full[i], p_phase[i]);
+            p_phase[i] ^= 1;
+            if (!ok) break;
+            pv(i, vs, j > 0);
+            if (j + 1 < n[i]) qk(i, ks);
+            if (j + 2 == n[i]) release(ctl.q_free[i]);
+          }
+          if (!ok) break;
+          release(ctl.kv_free[vs]);
+          if (j + 1 < nmax) release(ctl.kv_free[ks]);
+        }
+      }
+      // every product issued has ended before the tensor memory goes back
+      if (lane == 0) {
+        umma_commit(smem_u32(&ctl.drain));
+        mbar_wait(smem_u32(&ctl.drain), 0, limit, a.status, nullptr);
+      }
+      __syncwarp();
+    } else {
+      // ---------------------------------------------------------------- queries
+      const int th = threadIdx.x - 64, G = a.Hq / a.Hk;
+      for (int seq = 0;; ++seq) {
+        const int us = seq & 1;
+        if (!wait(ctl.unit_full[us], (seq >> 1) & 1)) break;
+        const Unit w = ctl.unit[us];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctl.unit_free[us]));
+        if (!w.valid) {
+          // rows of no sequence are zero
+          int64_t c0 = a.cu_seqlens[0], c1 = a.cu_seqlens[a.B];
+          c0 = c0 < 0 ? 0 : c0 > a.T ? a.T : c0;
+          c1 = c1 < c0 ? c0 : c1 > a.T ? a.T : c1;
+          const int64_t outside = c0 + a.T - c1, row = (int64_t)a.Hq * D;
+          for (int64_t i = blockIdx.x * 64 + th; i < outside * a.N * row; i += (int64_t)gridDim.x * 64) {
+            const int64_t t = i / row % outside;
+            const int r = (int)(i / row / outside);
+            static_cast<T *>(a.o[r])[(t < c0 ? t : c1 + t - c0) * a.ldo + i % row] = static_cast<T>(0.0f);
+          }
+          break;
+        }
+        const int heads = G - w.grp * pa.gsize < pa.gsize ? G - w.grp * pa.gsize : pa.gsize;
+        const T *q = static_cast<const T *>(a.q[w.r]) + (int64_t)w.tok0 * a.ldq +
+                     ((int64_t)w.h * G + w.grp * pa.gsize) * D;
+        bool ok = true;
+        for (int i = 0; i < 2; ++i) {
+          if (seq > 0) ok = wait(ctl.q_free[i], (seq - 1) & 1);
+          if (!ok) break;
+          const uint32_t base = i * S::kTileBytes;
+          for (int e = th; e < kTile * (D / 8); e += 64) {
+            const int row = e / (D / 8), c = e % (D / 8), tk = row / pa.gsize, hd = row - tk * pa.gsize;
+            const bool live = tk < pa.tpt && i * pa.tpt + tk < w.ntok && hd < heads;
+            const T *src = q + (live ? (int64_t)(i * pa.tpt + tk) * a.ldq + (int64_t)hd * D + c * 8 : 0);
+            const uint32_t off = base + (c >> 3) * S::kHalf + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+            if (pa.vec_q) {
+              cp_async16(q_smem + off, src, live);
+            } else {
+              uint16_t x[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) x[k] = live ? reinterpret_cast<const uint16_t *>(src)[k] : 0;
+              *reinterpret_cast<uint4 *>(smem_gen + off) =
+                  make_uint4(x[0] | x[1] << 16, x[2] | x[3] << 16, x[4] | x[5] << 16, x[6] | x[7] << 16);
+            }
+          }
+          cp_async_commit();
+          cp_async_wait<0>();
+          fence_proxy_async_smem();
+          mbar_arrive(smem_u32(&ctl.q_full[i]));
+        }
+        if (!ok) break;
+      }
+    }
+  } else {
+    // ------------------------------------------------------------------ softmax and output
+    regs_up<kRegsMany>();
+    const int i = (warp - 4) / 4, row = (warp % 4) * 32 + lane, G = a.Hq / a.Hk;
+    const uint32_t lanes = (uint32_t)(warp % 4) << 21;  // lane 32 * (warp % 4) of tensor memory
+    const uint32_t s_tmem = tmem + i * kTile + lanes, o_tmem = tmem + 256 + i * D + lanes;
+    const int tk = row / pa.gsize, hd = row - tk * pa.gsize;
+    const bool cap = a.softcap > 0.0f;
+    const float log2e = 1.4426950408889634f;
+    // log2 scores: s * scale * log2e, or with a cap c: c * log2e * tanh(s * scale / c),
+    // tanh y = 1 - 2 / (1 + 2^(2 y log2e)), whose error is absolute and so is the score's
+    const float scale = cap ? 2.0f * log2e * a.scale / a.softcap : a.scale * log2e;
+    const float cap2 = a.softcap * log2e;
+    uint32_t s_phase = 0, o_count = 0;
+    bool ok = true;
+    for (int seq = 0;; ++seq) {
+      const int us = seq & 1;
+      if (!wait_inline(smem_u32(&ctl.unit_full[us]), (seq >> 1) & 1, limit, a.status, abort)) break;
+      const Unit w = ctl.unit[us];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ctl.unit_free[us]));
+      if (!w.valid) break;
+      const int heads = G - w.grp * pa.gsize < pa.gsize ? G - w.grp * pa.gsize : pa.gsize;
+      const bool live = tk < pa.tpt && i * pa.tpt + tk < w.ntok && hd < heads;
+      // this row sees [lo, hi) and [0, prefix)
+      const int pos = w.pos0 + i * pa.tpt + tk;
+      const int hi = pos + 1 < w.to ? pos + 1 : w.to;
+      const int lo = a.window && pos - a.window + 1 > 0 ? pos - a.window + 1 : 0;
+      // what every row of the tile sees
+      const int t_last = (w.ntok - i * pa.tpt < pa.tpt ? w.ntok - i * pa.tpt : pa.tpt) - 1;
+      const int all_hi = w.pos0 + i * pa.tpt + 1 < w.to ? w.pos0 + i * pa.tpt + 1 : w.to;
+      const int pos_last = w.pos0 + i * pa.tpt + t_last;
+      const int all_lo = a.window && pos_last - a.window + 1 > 0 ? pos_last - a.window + 1 : 0;
+      float m = -INFINITY, l = 0.0f;
+      for (int j = 0; j < w.n[i]; ++j) {
+        ok = wait_inline(smem_u32(&ctl.s_full[i]), s_phase, limit, a.status, abort);
+        s_phase ^= 1;
+        if (!ok) break;
+        tc_fence_after();
+        float s[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(s_tmem + c * 32, s[c]);
+        tmem_wait_ld();
+        const int jt = w.j0 + j * kTile;
+        if (cap) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int x = 0; x < 32; ++x)
+              s[c][x] = fmaf(-2.0f * cap2, rcp_approx(1.0f + exp2_approx(s[c][x] * scale)), cap2);
+        }
+        if (!(jt + kTile <= w.prefix || (jt >= all_lo && jt + kTile <= all_hi))) {
+          const int from = lo - jt, to = hi - jt, pre = w.prefix - jt;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int x = 0; x < 32; ++x)
+              if ((c * 32 + x < from || c * 32 + x >= to) && c * 32 + x >= pre) s[c][x] = -INFINITY;
+        }
+        float top[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          top[c] = s[c][0];
+#pragma unroll
+          for (int x = 1; x < 32; ++x) top[c] = fmaxf(top[c], s[c][x]);
+        }
+        const float f = cap ? 1.0f : scale;
+        const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * f;
+        const bool rise = mx > m + kSlack;
+        if (j == 0) {
+          m = mx;
+        } else if (__any_sync(0xffffffffu, rise)) {
+          // the products up to the previous tile have to be in O
+          ok = wait_inline(smem_u32(&ctl.o_done[i]), (o_count - 1) & 1, limit, a.status, abort);
+          if (!ok) break;
+          tc_fence_after();
+          const float keep = rise ? exp2_approx(m - mx) : 1.0f;
+          if (rise) m = mx;
+          l *= keep;
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            float o[16];
+            uint32_t r[16];
+            tmem_ld16(o_tmem + c * 16, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int x = 0; x < 16; ++x) r[x] = __float_as_uint(o[x] * keep);
+            tmem_st16(o_tmem + c * 16, r);
+          }
+        }
+        const float neg = m == -INFINITY ? 0.0f : -m;
+        float sum[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t pk[16];
+          sum[c] = 0.0f;
+#pragma unroll
+          for (int x = 0; x < 16; ++x) {
+            const float e0 = exp2_approx(fmaf(s[c][2 * x], f, neg)), e1 = exp2_approx(fmaf(s[c][2 * x + 1], f, neg));
+            sum[c] += e0;
+            sum[c] += e1;
+            pk[x] = Half2<T>::pack(e0, e1);
+          }
+          tmem_st16(s_tmem + c * 16, pk);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctl.p_full[i]));
+        ++o_count;
+      }
+      if (!ok) break;
+      if (w.n[i] > 0) {
+        ok = wait_inline(smem_u32(&ctl.o_done[i]), (o_count - 1) & 1, limit, a.status, abort);
+        if (!ok) break;
+        tc_fence_after();
+      }
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      T *out = static_cast<T *>(a.o[w.r]) + (int64_t)(w.tok0 + i * pa.tpt + tk) * a.ldo +
+               ((int64_t)w.h * G + w.grp * pa.gsize + hd) * D;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        float o[32];
+        if (w.n[i] > 0) {
+          tmem_ld32(o_tmem + c * 32, o);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int x = 0; x < 32; ++x) o[x] = 0.0f;
+        }
+        if (live) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int x = 0; x < 16; ++x) pk[x] = Half2<T>::pack(o[2 * x] * inv, o[2 * x + 1] * inv);
+          if (pa.vec_o) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              *reinterpret_cast<uint4 *>(out + c * 32 + x * 8) =
+                  make_uint4(pk[4 * x], pk[4 * x + 1], pk[4 * x + 2], pk[4 * x + 3]);
+          } else {
+            uint16_t *p = reinterpret_cast<uint16_t *>(out + c * 32);
+#pragma unroll
+            for (int x = 0; x < 16; ++x) p[2 * x] = (uint16_t)pk[x], p[2 * x + 1] = (uint16_t)(pk[x] >> 16);
+          }
+        }
+        __syncwarp();
+      }
+      tc_fence_before();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <typename T, int D, int MAXN>
+int launch(const AttnArgs &a, cudaStream_t s) {
+  PrefillArgs<MAXN> p;
+  memset(&p, 0, sizeof(p));
+  p.a = a;
+  const int G = a.Hq / a.Hk;
+  p.groups = (G + kTile - 1) / kTile;
+  p.gsize = (G + p.groups - 1) / p.groups;
+  p.tpt = kTile / p.gsize;
+  p.box = a.page < kTile ? a.page : kTile;
+  p.wait_ns = wait_limit_ns();
+  p.vec_q = (a.ldq * 2) % 16 == 0;
+  p.vec_o = (a.ldo * 2) % 16 == 0;
+  const CUtensorMapDataType mt = Half2<T>::kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  for (int r = 0; r < a.N; ++r) {
+    p.vec_q = p.vec_q && (uintptr_t)a.q[r] % 16 == 0;
+    p.vec_o = p.vec_o && (uintptr_t)a.o[r] % 16 == 0;
+    const uint64_t rows = (uint64_t)a.pages * (uint64_t)(a.ld_page / D);
+    if (rows > 0x7fffffff) return set_error(TP_ERR_UNSUPPORTED, "a cache of more than 2^31 - 1 rows of D");
+    // without pages nothing is read, but a map needs an address
+    const void *kc = a.pages ? a.k_cache[r] : a.q[r], *vc = a.pages ? a.v_cache[r] : a.q[r];
+    if (a.pages == 0) continue;
+    if (int rc = make_tmap_2d(&p.k[r], kc, mt, 2, D, rows, D, 64, p.box, CU_TENSOR_MAP_SWIZZLE_128B)) return rc;
+    if (int rc = make_tmap_2d(&p.v[r], vc, mt, 2, D, rows, D, 64, p.box, CU_TENSOR_MAP_SWIZZLE_128B)) return rc;
+  }
+  float *ws;
+  if (int rc = split_workspace(s, 0, 2, &ws, &p.counters)) return rc;
+  const int64_t most = (a.T / (2 * p.tpt) + a.B) * a.N * a.Hk * p.groups;
+  const int grid = most < sm_count() ? (int)most : sm_count();
+  auto kern = prefill_kernel<T, D, MAXN>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh<D>::kSmem);
+  if (e == cudaSuccess) e = launch_pdl(kern, dim3(grid), dim3(kThreads), Sh<D>::kSmem, s, p);
+  if (e != cudaSuccess) return cuda_error(e, "prefill launch");
+  note_launch();
+  return TP_OK;
+}
+
+template <typename T, int D>
+int launch_n(const AttnArgs &a, cudaStream_t s) {
+  return a.N <= 8 ? launch<T, D, 8>(a, s) : launch<T, D, kMaxShards>(a, s);
+}
+
+}  // namespace
+
+int launch_prefill(const AttnArgs &a, cudaStream_t s) {
+  if (a.dt == TP_BF16) return a.D == 64 ? launch_n<__nv_bfloat16, 64>(a, s) : launch_n<__nv_bfloat16, 128>(a, s);
+  return a.D == 64 ? launch_n<__half, 64>(a, s) : launch_n<__half, 128>(a, s);
+}
+
+}  // namespace tp

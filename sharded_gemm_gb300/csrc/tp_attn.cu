@@ -147,7 +147,7 @@ int tp_paged_prefill(int N, const void *const *q, int64_t T, int64_t ldq, int Hq
     return set_error(TP_ERR_ALIGNMENT, "cu_seqlens or prefix_lens not aligned to its element size");
   a.cu_seqlens = cu_seqlens, a.prefix_lens = prefix_lens;
   if (int rc = need_status(&a.status)) return rc;
-  return launch_attn_simt(a, (cudaStream_t)stream);
+  return simt_policy() ? launch_attn_simt(a, (cudaStream_t)stream) : launch_prefill(a, (cudaStream_t)stream);
 }
 
 int tp_sample(const void *logits, int64_t B, int64_t V, int64_t ld, tp_dtype in_dt, const float *u,
