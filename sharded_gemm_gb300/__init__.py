@@ -774,74 +774,98 @@ def tp_mx_sharded_to_all(x, codes, scales, bias=None, out=None, out_dtype=None, 
 
 # ------------------------------------------------------------------ attention side
 # A per-rank argument is a list of N tensors, or one tensor whose first
-# dimension is the ranks (rank r is its slice [r]).
+# dimension is the ranks (rank r is its slice [r]).  A decode step calls these
+# once a layer on kernels of a few microseconds, so the marshalling reads each
+# tensor attribute once and builds no intermediate objects.
+_array_types = {}
+_dtypes = {}
+
+
+def _pointer_array(n):
+    t = _array_types.get(n)
+    if t is None:
+        t = _array_types[n] = ctypes.c_void_p * n
+    return t
+
+
+def _dtype_code(dtype):
+    if not _dtypes:
+        torch = _torch()
+        _dtypes.update({torch.float32: TP_F32, torch.bfloat16: TP_BF16, torch.float16: TP_F16})
+    code = _dtypes.get(dtype)
+    if code is None:
+        raise TypeError("unsupported dtype %s" % dtype)
+    return code
+
+
+def _current_stream(stream, dev):
+    """_stream, with the current stream of device `dev` looked up without building a Stream object."""
+    if stream is None:
+        return _torch()._C._cuda_getCurrentRawStream(dev)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
 def _ranks(x, name, dim):
-    """(pointer array, what keeps it alive, N, rank 0's shape and strides, dtype, device) of a per-rank argument."""
+    """(pointer array, N, shape, strides, index of the rank's first dimension in them, dtype, device index)."""
     if isinstance(x, (list, tuple)):
-        t0 = x[0]
-        shape, stride, dtype, device = t0.shape, t0.stride(), t0.dtype, t0.device
-        for t in x[1:]:
-            if t.shape != shape or t.stride() != stride or t.dtype != dtype or t.device != device:
+        t = x[0]
+        shape, stride, dtype, dev, first, n = t.shape, t.stride(), t.dtype, t.get_device(), 0, len(x)
+        for o in x:
+            if o.shape != shape or o.stride() != stride or o.dtype != dtype or o.get_device() != dev:
                 raise ValueError("%s: all ranks need one shape, stride, dtype and device" % name)
-        ptrs = [t.data_ptr() for t in x]
+        arr = _pointer_array(n)(*[o.data_ptr() for o in x])
     else:
-        shape, stride, dtype, device = x.shape[1:], x.stride(), x.dtype, x.device
-        base, step = x.data_ptr(), stride[0] * x.element_size()
-        stride = stride[1:]
-        ptrs = [base + i * step for i in range(x.shape[0])]
-    if device.type != "cuda":
+        shape, stride, dtype, dev, first = x.shape, x.stride(), x.dtype, x.get_device(), 1
+        n = shape[0] if shape else 0
+        base = x.data_ptr()
+        if n == 1:
+            arr = _pointer_array(1)(base)
+        else:
+            step = stride[0] * x.element_size() if shape else 0
+            arr = _pointer_array(n)(*[base + i * step for i in range(n)])
+    if dev < 0:
         raise ValueError("%s must be a CUDA tensor" % name)
-    if len(shape) != dim:
+    if len(shape) != dim + first:
         raise ValueError("%s: each rank's tensor must be %d-D" % (name, dim))
-    n = len(ptrs)
-    arr = (ctypes.c_void_p * n)(*ptrs)
-    return ctypes.cast(arr, ctypes.POINTER(ctypes.c_void_p)), n, shape, stride, dtype, device
+    return arr, n, shape, stride, first, dtype, dev
 
 
-def _rows_ld(shape, stride, name):
-    if shape[1] > 1 and stride[1] != 1:
+def _ld(shape, stride, first, name):
+    """Row stride of a per-rank matrix."""
+    if stride[first + 1] != 1 and shape[first + 1] > 1:
         raise ValueError("%s must have unit column stride" % name)
-    return stride[0] if shape[0] > 1 else max(shape[1], 1)
+    return stride[first] if shape[first] > 1 else shape[first + 1]
 
 
-def _param(t, name, dtype, n, device):
+def _param(t, name, dtype, n, dev):
     """Device pointer of a contiguous 1-D parameter array (None stays None)."""
     if t is None:
         return None
     if t.dtype != dtype:
         raise TypeError("%s must be %s" % (name, dtype))
-    if t.device != device:
-        raise ValueError("%s must be on %s" % (name, device))
-    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+    if t.get_device() != dev:
+        raise ValueError("%s must be on device %d" % (name, dev))
+    if t.shape != (n,) or not t.is_contiguous():
         raise ValueError("%s must be contiguous with %d elements" % (name, n))
     return t.data_ptr()
 
 
 def _paged_cache(k_cache, v_cache):
-    """(k pointers, v pointers, N, (pages, Hk, page, D), page stride, dtype code, device)."""
-    kp, n, shape, stride, dtype, device = _ranks(k_cache, "k_cache", 4)
-    vp, nv, vshape, vstride, vdtype, vdevice = _ranks(v_cache, "v_cache", 4)
-    if (n, shape, stride, dtype, device) != (nv, vshape, vstride, vdtype, vdevice):
+    """(k pointers, v pointers, N, pages, Hk, page, D, page stride, dtype, device index)."""
+    kp, n, shape, stride, first, dtype, dev = _ranks(k_cache, "k_cache", 4)
+    vp, nv, vshape, vstride, vfirst, vdtype, vdev = _ranks(v_cache, "v_cache", 4)
+    if n != nv or shape[first:] != vshape[vfirst:] or stride[first:] != vstride[vfirst:] or dtype != vdtype \
+            or dev != vdev:
         raise ValueError("k_cache and v_cache need the same ranks, shape, strides, dtype and device")
-    P, Hk, page, D = shape
-    if stride[3] != 1 or stride[2] != D or (Hk > 1 and stride[1] != page * D):
+    P, Hk, page, D = shape[first:]
+    ld, ld_head, ld_row, unit = stride[first:]
+    if unit != 1 or ld_row != D or (ld_head != page * D and Hk > 1):
         raise ValueError("the heads, rows and values of a cache page must be contiguous")
-    return kp, vp, n, shape, (stride[0] if P > 1 else Hk * page * D), _dtype_code(dtype), device
-
-
-def _dtype_code(dtype):
-    torch = _torch()
-    if dtype == torch.bfloat16:
-        return TP_BF16
-    if dtype == torch.float16:
-        return TP_F16
-    if dtype == torch.float32:
-        return TP_F32
-    raise TypeError("unsupported dtype %s" % dtype)
+    return kp, vp, n, P, Hk, page, D, (ld if P > 1 else Hk * page * D), dtype, dev
 
 
 def _heads(cols, D, name):
-    if cols % D:
+    if D < 1 or cols % D:
         raise ValueError("%s: %d columns are not whole heads of %d" % (name, cols, D))
     return cols // D
 
@@ -854,55 +878,60 @@ def tp_qkv_append(qkv, k_cache, v_cache, slots, positions=None, rope=None, q_nor
     per rank (T, Hq D) in the cache's dtype (one (N, T, Hq D) tensor unless
     ``out`` is given)."""
     torch = _torch()
-    kp, vp, N, (P, Hk, page, D), ldp, dt, device = _paged_cache(k_cache, v_cache)
-    xp, n, shape, stride, dtype, xdev = _ranks(qkv, "qkv", 2)
-    if n != N or xdev != device:
+    kp, vp, N, P, Hk, page, D, ldp, cdtype, dev = _paged_cache(k_cache, v_cache)
+    xp, n, shape, stride, first, dtype, xdev = _ranks(qkv, "qkv", 2)
+    if n != N or xdev != dev:
         raise ValueError("qkv and the caches need the same ranks on one device")
-    T = shape[0]
-    Hq = _heads(shape[1], D, "qkv") - 2 * Hk
+    T = shape[first]
+    Hq = _heads(shape[first + 1], D, "qkv") - 2 * Hk
     if out is None:
-        out = torch.empty((N, T, max(Hq, 0) * D), dtype=torch.bfloat16 if dt == TP_BF16 else torch.float16,
-                          device=device)
-    op, no, oshape, ostride, odtype, odev = _ranks(out, "out", 2)
-    if no != N or tuple(oshape) != (T, Hq * D) or _dtype_code(odtype) != dt or odev != device:
+        if Hq < 1:
+            raise ValueError("qkv holds no query heads besides 2 * %d key and value heads" % Hk)
+        out = torch.empty((N, T, Hq * D), dtype=cdtype, device=k_cache[0].device)
+    op, no, oshape, ostride, ofirst, odtype, odev = _ranks(out, "out", 2)
+    if no != N or oshape[ofirst] != T or oshape[ofirst + 1] != Hq * D or odtype != cdtype or odev != dev:
         raise ValueError("out must be (T, Hq * D) per rank in the cache's dtype")
     rp, rows, rot = None, 0, 0
     if rope is not None:
-        if rope.dtype != torch.float32 or rope.dim() != 2 or not rope.is_contiguous() or rope.device != device:
+        if rope.dtype != torch.float32 or rope.dim() != 2 or not rope.is_contiguous() or rope.get_device() != dev:
             raise ValueError("rope must be a contiguous float32 (positions, rope_dim) tensor on the caches' device")
         rp, (rows, rot) = rope.data_ptr(), rope.shape
         if positions is None:
             raise ValueError("rope needs positions")
     _check(lib().tp_qkv_append(
-        N, xp, T, _rows_ld(shape, stride, "qkv"), _dtype_code(dtype), Hq, Hk, D,
-        _param(q_norm, "q_norm", torch.float32, D, device), _param(k_norm, "k_norm", torch.float32, D, device), eps,
-        rp, rows, rot, 1 if interleaved else 0, _param(positions, "positions", torch.int32, T, device),
-        _param(slots, "slots", torch.int64, T, device), op, _rows_ld(oshape, ostride, "out"), kp, vp, P, page, ldp, dt,
-        _stream(stream)))
+        N, xp, T, _ld(shape, stride, first, "qkv"), _dtype_code(dtype), Hq, Hk, D,
+        _param(q_norm, "q_norm", torch.float32, D, dev), _param(k_norm, "k_norm", torch.float32, D, dev), eps,
+        rp, rows, rot, 1 if interleaved else 0, _param(positions, "positions", torch.int32, T, dev),
+        _param(slots, "slots", torch.int64, T, dev), op, _ld(oshape, ostride, ofirst, "out"), kp, vp, P, page, ldp,
+        _dtype_code(cdtype), _current_stream(stream, dev)))
     return out
 
 
 def _attention(q, k_cache, v_cache, block_table, out):
+    """(out, device index, T, D, the arguments up to block_table, (width, ld_table), (dtype, o, ldo))."""
     torch = _torch()
-    kp, vp, N, (P, Hk, page, D), ldp, dt, device = _paged_cache(k_cache, v_cache)
-    qp, n, shape, stride, dtype, qdev = _ranks(q, "q", 2)
-    if n != N or qdev != device:
+    kp, vp, N, P, Hk, page, D, ldp, cdtype, dev = _paged_cache(k_cache, v_cache)
+    qp, n, shape, stride, first, dtype, qdev = _ranks(q, "q", 2)
+    if n != N or qdev != dev:
         raise ValueError("q and the caches need the same ranks on one device")
-    if _dtype_code(dtype) != dt:
+    if dtype != cdtype:
         raise TypeError("q must have the caches' dtype")
+    T, cols = shape[first], shape[first + 1]
     if out is None:
-        out = torch.empty((N,) + tuple(shape), dtype=dtype, device=device)
-    op, no, oshape, ostride, odtype, odev = _ranks(out, "out", 2)
-    if no != N or oshape != shape or odtype != dtype or odev != device:
+        out = torch.empty((N, T, cols), dtype=dtype, device=block_table.device)
+    op, no, oshape, ostride, ofirst, odtype, odev = _ranks(out, "out", 2)
+    if no != N or oshape[ofirst] != T or oshape[ofirst + 1] != cols or odtype != dtype or odev != dev:
         raise ValueError("out must have q's shape per rank and its dtype")
-    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.device != device or (
-            block_table.shape[1] > 1 and block_table.stride(1) != 1):
-        raise ValueError("block_table must be a 2-D int32 tensor with unit column stride on the caches' device")
-    width = block_table.shape[1]
-    ldt = block_table.stride(0) if block_table.shape[0] > 1 else width
-    return (out, device, shape[0],
-            (N, qp, shape[0], _rows_ld(shape, stride, "q"), _heads(shape[1], D, "q"), Hk, D, kp, vp, P, page, ldp,
-             block_table.data_ptr()), (width, ldt), (dt, op, _rows_ld(oshape, ostride, "out")))
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.get_device() != dev:
+        raise ValueError("block_table must be a 2-D int32 tensor on the caches' device")
+    rows, width = block_table.shape
+    ldt, unit = block_table.stride()
+    if unit != 1 and width > 1:
+        raise ValueError("block_table must have unit column stride")
+    return (out, dev, T, D,
+            (N, qp, T, _ld(shape, stride, first, "q"), _heads(cols, D, "q"), Hk, D, kp, vp, P, page, ldp,
+             block_table.data_ptr()), (width, ldt if rows > 1 else width),
+            (_dtype_code(dtype), op, _ld(oshape, ostride, ofirst, "out")))
 
 
 def tp_paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale=None, softcap: float = 0.0, window: int = 0,
@@ -910,13 +939,13 @@ def tp_paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale=None, soft
     """Attention of one new token per sequence over the paged caches: q per rank
     (B, Hq D), seq_lens (B) counts the new token.  Returns o, per rank
     (B, Hq D) (one (N, B, Hq D) tensor unless ``out`` is given)."""
-    out, device, B, head, table, tail = _attention(q, k_cache, v_cache, block_table, out)
+    out, dev, B, D, head, table, tail = _attention(q, k_cache, v_cache, block_table, out)
     if block_table.shape[0] != B:
         raise ValueError("block_table needs one row per sequence")
     if scale is None:
-        scale = head[6] ** -0.5
-    _check(lib().tp_paged_decode(*head, *table, _param(seq_lens, "seq_lens", _torch().int32, B, device), scale, softcap,
-                                 window, *tail, _stream(stream)))
+        scale = D ** -0.5
+    _check(lib().tp_paged_decode(*head, *table, _param(seq_lens, "seq_lens", _torch().int32, B, dev), scale, softcap,
+                                 window, *tail, _current_stream(stream, dev)))
     return out
 
 
@@ -926,14 +955,14 @@ def tp_paged_prefill(q, k_cache, v_cache, block_table, cu_seqlens, seq_lens, pre
     cu_seqlens[b] .. cu_seqlens[b + 1] - 1 of q are the last positions of
     sequence b.  Returns o as tp_paged_decode."""
     i32 = _torch().int32
-    out, device, T, head, table, tail = _attention(q, k_cache, v_cache, block_table, out)
+    out, dev, T, D, head, table, tail = _attention(q, k_cache, v_cache, block_table, out)
     B = block_table.shape[0]
     if scale is None:
-        scale = head[6] ** -0.5
-    _check(lib().tp_paged_prefill(*head, B, *table, _param(cu_seqlens, "cu_seqlens", i32, B + 1, device),
-                                  _param(seq_lens, "seq_lens", i32, B, device),
-                                  _param(prefix_lens, "prefix_lens", i32, B, device), scale, softcap, window, *tail,
-                                  _stream(stream)))
+        scale = D ** -0.5
+    _check(lib().tp_paged_prefill(*head, B, *table, _param(cu_seqlens, "cu_seqlens", i32, B + 1, dev),
+                                  _param(seq_lens, "seq_lens", i32, B, dev),
+                                  _param(prefix_lens, "prefix_lens", i32, B, dev), scale, softcap, window, *tail,
+                                  _current_stream(stream, dev)))
     return out
 
 
@@ -943,15 +972,14 @@ def tp_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, t
     numbers ``u`` (B); returns (tokens int64 (B), logprobs float32 (B))."""
     torch = _torch()
     _rowmajor(logits, "logits")
-    B, V = logits.shape
-    device, f32 = logits.device, torch.float32
+    (B, V), dev, f32 = logits.shape, logits.get_device(), torch.float32
     if tokens is None:
-        tokens = torch.empty((B,), dtype=torch.int64, device=device)
+        tokens = torch.empty((B,), dtype=torch.int64, device=logits.device)
     if logprobs is None:
-        logprobs = torch.empty((B,), dtype=f32, device=device)
+        logprobs = torch.empty((B,), dtype=f32, device=logits.device)
     _check(lib().tp_sample(logits.data_ptr(), B, V, logits.stride(0) if B > 1 else V, _dtype_code(logits.dtype),
-                           _param(u, "u", f32, B, device), _param(temperature, "temperature", f32, B, device),
-                           _param(top_k, "top_k", torch.int32, B, device), _param(top_p, "top_p", f32, B, device),
-                           _param(min_p, "min_p", f32, B, device), _param(tokens, "tokens", torch.int64, B, device),
-                           _param(logprobs, "logprobs", f32, B, device), _stream(stream)))
+                           _param(u, "u", f32, B, dev), _param(temperature, "temperature", f32, B, dev),
+                           _param(top_k, "top_k", torch.int32, B, dev), _param(top_p, "top_p", f32, B, dev),
+                           _param(min_p, "min_p", f32, B, dev), _param(tokens, "tokens", torch.int64, B, dev),
+                           _param(logprobs, "logprobs", f32, B, dev), _current_stream(stream, dev)))
     return tokens, logprobs

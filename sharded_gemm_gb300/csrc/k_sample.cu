@@ -60,8 +60,601 @@ __device__ unsigned long long block_sum(unsigned long long v, unsigned long long
   return v;
 }
 
+// ---------------------------------------------------------------- rows held on chip
+// A row is held as float32 in the shared memory of a cluster of 1, 2, 4 or 8
+// CTAs, so the logits are read once.  Thread i of CTA c owns the run of
+// elements (c * 1024 + i) * R .. + R - 1, R odd (runs of neighbouring threads
+// then start in different banks), and sums over runs in order are sums over the
+// row in order.  The end of the last run is padded with -inf.
+//
+// The end of a kept prefix is found with 2048 bins over x: elements are counted
+// (or their weights added up) per bin, the bin that holds the end is picked, and
+// its elements, a few hundred, are sorted on one CTA.
+//
+// What bounds it is arithmetic: about 20 instructions an element for each pass
+// that needs exact weights, two to four passes.
+
+constexpr int kBins = 2048, kList = 2048;
+constexpr float kBinScale = 64.0f;  // 1/64 of a logit wide, from the largest down
+
+typedef unsigned long long u64;
+
+struct RowShared {
+  union {
+    uint32_t hist[kBins];
+    u64 hist64[kBins];
+    u64 list[kList];  // filled when the bins have been read
+  };
+  u64 warp_a[2][32], warp_b[2][32];
+  u64 xa[2], xb[2];  // this CTA's sums, exchanged over the cluster
+  uint32_t warp_m[2][32], xm[2];
+  u64 answer;
+  uint32_t list_n;
+  int bin0, bin1;
+};
+
+__device__ __forceinline__ u64 ld_cluster_u64(uint32_t addr) {
+  u64 v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_cluster_u64(uint32_t addr, u64 v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
+}
+__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t atom_cluster_add(uint32_t addr, uint32_t v) {
+  uint32_t o;
+  asm volatile("atom.relaxed.cluster.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(o) : "r"(addr), "r"(v) : "memory");
+  return o;
+}
+
+// floor(e * 2^40), e in [0, 1], summed: the upper and lower 20 bits come out of
+// two fused multiply-adds that round toward zero at 2^23, where a float's last
+// bit is 1.  The raw bit patterns are added; each carries the pattern of 2^23.
+struct WeightSum {
+  uint32_t hi = 0, lo = 0;
+  int n = 0;
+  __device__ __forceinline__ void add(float e) {
+    const float t1 = __fmaf_rz(e, 1048576.0f, 8388608.0f);
+    const float rest = __fmaf_rn(e, 1048576.0f, -__fsub_rn(t1, 8388608.0f));  // exact
+    hi += __float_as_uint(t1);
+    lo += __float_as_uint(__fmaf_rz(rest, 1048576.0f, 8388608.0f));
+    ++n;
+  }
+  __device__ __forceinline__ u64 total() const {
+    return ((u64)(hi - (uint32_t)n * 0x4B000000u) << 20) + (lo - (uint32_t)n * 0x4B000000u);
+  }
+};
+
+__device__ __forceinline__ float x_of_key(uint32_t key) {
+  return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
+}
+// Orders the row by (x descending, index ascending), without ties.
+__device__ __forceinline__ u64 q_of(float x, uint32_t index) { return (u64)order_key(x) << 32 | (uint32_t)~index; }
+__device__ __forceinline__ int bin_of(float x, float top) {
+  const int b = __float2int_rz((top - x) * kBinScale);
+  return b < kBins - 1 ? b : kBins - 1;
+}
+
+// A kept prefix: what is above x, and of x itself the indexes up to i.
+struct Cut {
+  float x;
+  uint32_t i;
+  __device__ __forceinline__ bool keeps(float v, uint32_t index) const { return v > x || (v == x && index <= i); }
+};
+
+struct Row {
+  RowShared &sh;
+  const float *run;  // this thread's elements
+  int R, C, rank;
+  uint32_t index0;   // of the run's first element
+  float top, inv_t, run_top;
+  int par, xpar;  // which of two buffers the next exchange in the block, and over the cluster, uses
+
+  __device__ __forceinline__ void sync() {
+    if (C > 1) cluster_sync_all(); else __syncthreads();
+  }
+  __device__ __forceinline__ uint32_t at0(const void *p) { return mapa_shared(smem_u32(p), 0); }
+  __device__ __forceinline__ float e_of(float x) { return ratio(x, top, inv_t); }
+
+  // Sums of a and b over the cluster; every thread gets them, and in before_a
+  // the sum of the CTAs of lower rank.
+  __device__ __forceinline__ void reduce(u64 &a, u64 &b, u64 *before_a = nullptr) {
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+#pragma unroll
+    for (int m = 16; m > 0; m /= 2) {
+      a += __shfl_xor_sync(0xffffffffu, a, m);
+      b += __shfl_xor_sync(0xffffffffu, b, m);
+    }
+    if (lane == 0) sh.warp_a[par][warp] = a, sh.warp_b[par][warp] = b;
+    __syncthreads();
+    a = sh.warp_a[par][lane], b = sh.warp_b[par][lane];
+#pragma unroll
+    for (int m = 16; m > 0; m /= 2) {
+      a += __shfl_xor_sync(0xffffffffu, a, m);
+      b += __shfl_xor_sync(0xffffffffu, b, m);
+    }
+    if (before_a) *before_a = 0;
+    if (C > 1) {
+      if (threadIdx.x == 0) sh.xa[xpar] = a, sh.xb[xpar] = b;
+      cluster_sync_all();
+      a = b = 0;
+      for (int c = 0; c < C; ++c) {
+        if (before_a && c == rank) *before_a = a;
+        a += ld_cluster_u64(mapa_shared(smem_u32(&sh.xa[xpar]), c));
+        b += ld_cluster_u64(mapa_shared(smem_u32(&sh.xb[xpar]), c));
+      }
+      xpar ^= 1;
+    }
+    par ^= 1;
+  }
+  __device__ __forceinline__ uint32_t reduce_max(uint32_t v) {
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    v = __reduce_max_sync(0xffffffffu, v);
+    if (lane == 0) sh.warp_m[par][warp] = v;
+    __syncthreads();
+    v = __reduce_max_sync(0xffffffffu, sh.warp_m[par][lane]);
+    if (C > 1) {
+      if (threadIdx.x == 0) sh.xm[xpar] = v;
+      cluster_sync_all();
+      v = 0;
+      for (int c = 0; c < C; ++c) {
+        const uint32_t o = ld_cluster_u32(mapa_shared(smem_u32(&sh.xm[xpar]), c));
+        v = o > v ? o : v;
+      }
+      xpar ^= 1;
+    }
+    par ^= 1;
+    return v;
+  }
+  // Sum over the block of the values of lower threads.
+  __device__ __forceinline__ u64 scan_before(u64 v, u64 &total) {
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    u64 run = v;
+#pragma unroll
+    for (int m = 1; m < 32; m *= 2) {
+      const u64 o = __shfl_up_sync(0xffffffffu, run, m);
+      if (lane >= m) run += o;
+    }
+    if (lane == 31) sh.warp_a[par][warp] = run;
+    __syncthreads();
+    const u64 w = sh.warp_a[par][lane];
+    u64 base = lane < warp ? w : 0;
+    total = w;
+#pragma unroll
+    for (int m = 16; m > 0; m /= 2) {
+      base += __shfl_xor_sync(0xffffffffu, base, m);
+      total += __shfl_xor_sync(0xffffffffu, total, m);
+    }
+    par ^= 1;
+    return base + run - v;
+  }
+
+  // Before bins are added to: the last readers of what they share memory with
+  // are a sync behind.
+  __device__ __forceinline__ void clear_bins() {
+    for (int i = threadIdx.x; i < kBins; i += kThreads) sh.hist64[i] = 0;
+    if (threadIdx.x == 0) sh.list_n = 0, sh.bin0 = sh.bin1 = kBins - 1;
+    __syncthreads();
+  }
+  // The bins over the cluster in which the running total reaches `target`,
+  // where the true totals are (bins << shift) plus less than slack << shift.
+  template <typename H>
+  __device__ __forceinline__ void pick_bins(const H *hist, u64 target, int shift, u64 slack, int &b0, int &b1) {
+    sync();  // every CTA's bins are complete
+    const int per = C == 1 ? 2 : 1, i = rank * (kBins / C) + (int)threadIdx.x * per;
+    u64 h0 = 0, h1 = 0;
+    if ((int)threadIdx.x * per < kBins / C) {
+      if (C == 1) {
+        h0 = hist[i], h1 = hist[i + 1];
+      } else {
+        for (int c = 0; c < C; ++c) {
+          const uint32_t at = mapa_shared(smem_u32(hist + i), c);
+          h0 += sizeof(H) == 4 ? ld_cluster_u32(at) : ld_cluster_u64(at);
+        }
+      }
+    }
+    u64 all, before = scan_before(h0 + h1, all), base = 0, unused = 0;
+    if (C > 1) {
+      u64 mine = threadIdx.x == 0 ? all : 0;
+      reduce(mine, unused, &base);
+    }
+    const u64 c0 = base + before, c1 = c0 + h0, c2 = c1 + h1;
+    auto over = [&](u64 cum, u64 more) { return ((cum + more) << shift) >= target; };
+    auto mark = [&](u64 from, u64 to, int at) {
+      if (from == to) return;
+      if (over(to, slack) && (from == 0 || !over(from, slack))) st_cluster_u32(at0(&sh.bin0), at);
+      if (over(to, 0) && !over(from, 0)) st_cluster_u32(at0(&sh.bin1), at);
+    };
+    mark(c0, c1, i);
+    mark(c1, c2, i + 1);
+    sync();
+    b0 = (int)ld_cluster_u32(at0(&sh.bin0)), b1 = (int)ld_cluster_u32(at0(&sh.bin1));
+  }
+
+  // Puts this thread's elements that `in` accepts (n of them) on rank 0's list.
+  template <typename In>
+  __device__ __forceinline__ void gather(int n, In in) {
+    if (n > 0) {
+      uint32_t at = atom_cluster_add(at0(&sh.list_n), n);
+      for (int j = 0; j < R; ++j)
+        if (in(run[j], index0 + j)) st_cluster_u64(at0(&sh.list[at++]), q_of(run[j], index0 + j));
+    }
+    sync();
+  }
+
+  // Rank 0's list: n elements, all of a stretch of the order behind which
+  // `place0` elements of weight `above` lie.  The cut that keeps the first k of
+  // the order and, with p_share < 2^24, of those the ones whose weight before
+  // them is under `want` (found here from p_share where the list starts the order).
+  __device__ __forceinline__ Cut resolve(int n, u64 place0, u64 above, u64 k, bool by_p, u64 want, u64 p_share) {
+    if (rank == 0) {
+      const int tid = threadIdx.x;
+      int size = 2;
+      while (size < n) size *= 2;
+      for (int i = n + tid; i < size; i += kThreads) sh.list[i] = 0;
+      __syncthreads();
+      for (int width = 2; width <= size; width *= 2)
+        for (int step = width / 2; step > 0; step /= 2) {
+          if (tid < size / 2) {
+            const int i = (tid & ~(step - 1)) << 1 | (tid & (step - 1));
+            const u64 x = sh.list[i], y = sh.list[i + step];
+            if ((x < y) == ((i & width) == 0)) sh.list[i] = y, sh.list[i + step] = x;
+          }
+          __syncthreads();
+        }
+      u64 w[2];
+      bool in[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int at = 2 * tid + i;
+        in[i] = at < n && place0 + at < k;
+        w[i] = in[i] ? weight(e_of(x_of_key((uint32_t)(sh.list[at] >> 32)))) : 0;
+      }
+      u64 total;
+      const u64 before = above + scan_before(w[0] + w[1], total);
+      par ^= 1;  // as on the other CTAs
+      if (by_p) {
+        if (place0 == 0 && above == 0 && p_share) want = part_of(total, p_share - 1);
+        in[0] = in[0] && (before < want || place0 + 2 * tid == 0);
+        in[1] = in[1] && before + w[0] < want;
+      }
+      const int kept = __syncthreads_count(in[0]) + __syncthreads_count(in[1]);
+      if (tid == 0) sh.answer = sh.list[kept - 1];
+    }
+    sync();
+    const u64 q = ld_cluster_u64(at0(&sh.answer));
+    return Cut{x_of_key((uint32_t)(q >> 32)), ~(uint32_t)q};
+  }
+
+  // The cut behind which the stretch [lo, hi] of the order ends the prefix:
+  // rounds of 2048 equal parts of the stretch.  For rows of many equal or
+  // near-equal values.
+  template <bool BY_WEIGHT>
+  __device__ __noinline__ Cut select_in(u64 lo, u64 hi, u64 above, u64 want) {
+    for (;;) {
+      const int bits = 64 - __clzll((hi - lo) | 1), shift = bits > 11 ? bits - 11 : 0;
+      clear_bins();
+      for (int j = 0; j < R; ++j) {
+        const u64 q = q_of(run[j], index0 + j);
+        if (q < lo || q > hi) continue;
+        const u64 add = BY_WEIGHT ? weight(e_of(run[j])) : 1;
+        if (add) atomicAdd(&sh.hist64[(hi - q) >> shift], add);
+      }
+      int b0, b1;
+      pick_bins(sh.hist64, want - above, 0, 0, b0, b1);
+      const u64 new_hi = hi - ((u64)b1 << shift), span = (1ull << shift) - 1;
+      const u64 new_lo = new_hi - lo > span ? new_hi - span : lo;
+      u64 over = 0, n = 0;
+      for (int j = 0; j < R; ++j) {
+        const u64 q = q_of(run[j], index0 + j);
+        if (q >= lo && q <= hi) {
+          if (q > new_hi) over += BY_WEIGHT ? weight(e_of(run[j])) : 1;
+          else if (q >= new_lo) ++n;
+        }
+      }
+      const int mine = (int)n;
+      reduce(over, n);
+      above += over;
+      lo = new_lo, hi = new_hi;
+      if (n <= kList) {
+        gather(mine, [&](float x, uint32_t i) { return q_of(x, i) >= lo && q_of(x, i) <= hi; });
+        return BY_WEIGHT ? resolve((int)n, 1, above, ~0ull, true, want, 0)
+                         : resolve((int)n, above, 0, want, false, 0, 0);
+      }
+    }
+  }
+
+  // The first k, and of those with by_p the ones under part_of(their weight, p_share).
+  __device__ __forceinline__ Cut select_count(u64 k, bool by_p, u64 p_share, bool &only_first) {
+    // k runs whose largest is in one of the first bins hold k elements in them
+    int limit = kBins - 1, unused;
+    if (k <= (u64)C * kThreads) {
+      clear_bins();
+      atomicAdd(&sh.hist[bin_of(run_top, top)], 1u);
+      pick_bins(sh.hist, k, 0, 0, unused, limit);
+    }
+    u64 n = 0, none = 0;
+    if (bin_of(run_top, top) <= limit)
+      for (int j = 0; j < R; ++j) n += bin_of(run[j], top) <= limit;
+    int mine = (int)n;
+    reduce(n, none);
+    u64 over = 0;
+    int first = 0;  // the list holds bins first..limit
+    if (n > kList) {
+      clear_bins();
+      if (mine)
+        for (int j = 0; j < R; ++j)
+          if (bin_of(run[j], top) <= limit) atomicAdd(&sh.hist[bin_of(run[j], top)], 1u);
+      pick_bins(sh.hist, k, 0, 0, unused, limit);
+      n = 0;
+      if (bin_of(run_top, top) <= limit)
+        for (int j = 0; j < R; ++j) {
+          const int b = bin_of(run[j], top);
+          n += b == limit;
+          over += b < limit;
+        }
+      mine = (int)n;
+      const int mine_over = (int)over;
+      reduce(n, over);
+      if (n + over <= kList) {
+        mine += mine_over;
+        n += over, over = 0;
+      } else {
+        first = limit;
+      }
+    }
+    Cut cut;
+    if (n <= kList) {
+      if (threadIdx.x == 0) sh.list_n = 0;
+      sync();
+      gather(mine, [&](float x, uint32_t) { return bin_of(x, top) >= first && bin_of(x, top) <= limit; });
+      const bool both = by_p && first == 0;
+      cut = resolve((int)n, over, 0, k, both, 0, p_share + 1);
+      if (both) return cut;
+    } else {
+      u64 lo, hi;
+      stretch(limit, limit, lo, hi);
+      cut = select_in<false>(lo, hi, over, k);
+    }
+    return by_p ? select_weight(0, p_share, cut, only_first) : cut;
+  }
+
+  // The stretch of the order that the elements of bins b0..b1 take.
+  __device__ __forceinline__ void stretch(int b0, int b1, u64 &lo, u64 &hi) {
+    uint32_t most = 0, not_least = 0;
+    for (int j = 0; j < R; ++j) {
+      const int b = bin_of(run[j], top);
+      const uint32_t key = order_key(run[j]);
+      if (b < b0 || b > b1) continue;
+      if (key > most) most = key;
+      if (~key > not_least) not_least = ~key;
+    }
+    hi = (u64)reduce_max(most) << 32 | 0xffffffffu;
+    lo = (u64)~reduce_max(not_least) << 32;
+  }
+
+  // Of what `from` keeps (weight `total`, 0: not known) the ones whose weight before
+  // them is under part_of(total, p_share).
+  __device__ __noinline__ Cut select_weight(u64 total, u64 p_share, Cut from, bool &only_first) {
+    u64 none = 0;
+    if (total == 0) {
+      WeightSum sum;
+      for (int j = 0; j < R; ++j) sum.add(from.keeps(run[j], index0 + j) ? e_of(run[j]) : 0.0f);
+      total = sum.total();
+      reduce(total, none);
+    }
+    const u64 want = part_of(total, p_share);
+    if (want == 0) {
+      only_first = true;
+      return from;
+    }
+    // Bins of 32 bits: what the dropped low bits may amount to is the slack.
+    const int bits = 64 - __clzll(total), shift = bits > 31 ? bits - 31 : 0;
+    const u64 slack = shift ? (u64)R * kThreads * C : 0;
+    clear_bins();
+#pragma unroll 4
+    for (int j = 0; j < R; ++j) {
+      const float x = run[j];
+      WeightSum w;
+      w.add(from.keeps(x, index0 + j) ? e_of(x) : 0.0f);
+      const uint32_t add = (uint32_t)(w.total() >> shift);
+      if (add) atomicAdd(&sh.hist[bin_of(x, top)], add);
+    }
+    int b0, b1;
+    pick_bins(sh.hist, want, shift, slack, b0, b1);
+    WeightSum sum;
+    u64 n = 0;
+#pragma unroll 4
+    for (int j = 0; j < R; ++j) {
+      const float x = run[j];
+      const int b = bin_of(x, top);
+      const bool kept = from.keeps(x, index0 + j);
+      sum.add(kept && b < b0 ? e_of(x) : 0.0f);
+      n += kept && b >= b0 && b <= b1;
+    }
+    const int mine = (int)n;
+    u64 above = sum.total();
+    reduce(above, n);
+    if (n <= kList) {
+      if (threadIdx.x == 0) sh.list_n = 0;
+      sync();
+      gather(mine, [&](float x, uint32_t i) {
+        return from.keeps(x, i) && bin_of(x, top) >= b0 && bin_of(x, top) <= b1;
+      });
+      return resolve((int)n, b0 > 0 || above ? 1 : 0, above, ~0ull, true, want, 0);
+    }
+    const u64 floor_q = q_of(from.x, from.i);
+    u64 lo, hi;
+    stretch(b0, b1, lo, hi);
+    return select_in<true>(lo > floor_q ? lo : floor_q, hi, above, want);
+  }
+};
+
 template <typename T>
-__global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant__ SampleArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) sample_row_kernel(const __grid_constant__ SampleArgs a, int C, int R) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  RowShared &sh = *reinterpret_cast<RowShared *>(smem);
+  float *xs = reinterpret_cast<float *>(smem + sizeof(RowShared));
+  griddep_launch_dependents();
+  griddep_wait();
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int64_t b = blockIdx.x / C;
+  const int rank = blockIdx.x % C, slice = R * kThreads;
+  const T *x = static_cast<const T *>(a.logits) + b * a.ld + (int64_t)rank * slice;
+  const int64_t left = a.V - (int64_t)rank * slice;
+  const int n = left < 0 ? 0 : left < slice ? (int)left : slice;
+
+  const float t = a.temperature ? a.temperature[b] : 1.0f, u = a.u[b];
+  const bool greedy = !(t >= 9.5367431640625e-7f);
+  long long k = greedy ? 1 : (a.top_k ? a.top_k[b] : 0);
+  if (k <= 0 || k > a.V) k = a.V;
+  const float p = a.top_p ? a.top_p[b] : 1.0f;
+  const bool by_p = p < 1.0f;
+  const u64 p_share = (u64)(fmaxf(p, 0.0f) * 16777216.0f);
+  float min_p = a.min_p ? a.min_p[b] : 0.0f;
+  min_p = min_p > 0.0f ? fminf(min_p, 1.0f) : 0.0f;
+
+  // ---- the slice into shared memory, and its largest
+  float top = -INFINITY;
+  auto clean = [](float v) { return isnan(v) ? -INFINITY : fminf(v, 3.402823466e38f) + 0.0f; };
+  constexpr int kVec = 16 / sizeof(T);
+  const int vecs = (uintptr_t)x % 16 == 0 ? n / kVec : 0;
+#pragma unroll 4
+  for (int i = tid; i < vecs; i += kThreads) {
+    const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(x) + i);
+    const uint32_t bits[4] = {v.x, v.y, v.z, v.w};
+    float f[kVec];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (sizeof(T) == 4) {
+        f[j] = clean(__uint_as_float(bits[j]));
+      } else {
+        const float2 pair = Half2<T>::unpack(bits[j]);
+        f[2 * j] = clean(pair.x), f[2 * j + 1] = clean(pair.y);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kVec; j += 4) {
+      *reinterpret_cast<float4 *>(xs + i * kVec + j) = make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]);
+      top = fmaxf(top, fmaxf(fmaxf(f[j], f[j + 1]), fmaxf(f[j + 2], f[j + 3])));
+    }
+  }
+  for (int i = vecs * kVec + tid; i < slice; i += kThreads) {
+    const float v = i < n ? clean(static_cast<float>(x[i])) : -INFINITY;
+    xs[i] = v;
+    top = fmaxf(top, v);
+  }
+  Row row{sh, xs + tid * R, R, C, rank, (uint32_t)(rank * slice + tid * R), 0.0f, greedy ? 1.0f : 1.0f / t, -INFINITY, 0, 0};
+  row.top = top = x_of_key(row.reduce_max(order_key(top)));  // also: the slice is in shared memory
+  if (top == -INFINITY) {  // nothing can be drawn
+    if (rank == 0 && tid == 0) {
+      a.tokens[b] = -1;
+      if (a.logprobs) a.logprobs[b] = -INFINITY;
+    }
+    if (C > 1) cluster_sync_all();
+    return;
+  }
+
+  // ---- the row's own softmax total, the first of the largest, and the weight of all where top-p asks for it
+  float z = 0.0f;
+  int first = -1;
+  WeightSum all;
+  if (by_p && k == a.V) {
+#pragma unroll 4
+    for (int j = R - 1; j >= 0; --j) all.add(row.e_of(row.run[j]));
+  }
+#pragma unroll 4
+  for (int j = R - 1; j >= 0; --j) {
+    const float v = row.run[j];
+    z += exp2f((v - top) * 1.4426950408889634f);
+    row.run_top = fmaxf(row.run_top, v);
+    if (v == top) first = j;
+  }
+  // the threads' sums are joined as whole numbers of 2^-40, which have no order
+  u64 zsum = (u64)(z * 1099511627776.0f), all_w = all.total();
+  row.reduce(zsum, all_w);
+  const float logz = logf((float)zsum * 9.094947017729282e-13f);
+
+  // ---- the kept prefix
+  Cut cut{-INFINITY, 0xffffffffu};
+  bool only_first = k == 1 || (by_p && p_share == 0);
+  if (!only_first) {
+    if (k < a.V) cut = row.select_count((u64)k, by_p, p_share, only_first);
+    else if (by_p) cut = row.select_weight(all_w, p_share, cut, only_first);
+  }
+  if (only_first) {
+    const uint32_t best = row.reduce_max(first >= 0 ? ~(row.index0 + first) : 0);
+    if (rank == 0 && tid == 0) {
+      a.tokens[b] = ~best;
+      if (a.logprobs) a.logprobs[b] = -logz;
+    }
+    if (C > 1) cluster_sync_all();
+    return;
+  }
+
+  // ---- the draw
+  auto kept_e = [&](int j) {
+    const float v = row.run[j], e = row.e_of(v);
+    return cut.keeps(v, row.index0 + j) && !(e < min_p) ? e : 0.0f;
+  };
+  WeightSum sum;
+  if (row.run_top >= cut.x) {
+#pragma unroll 4
+    for (int j = 0; j < R; ++j) sum.add(kept_e(j));
+  }
+  const u64 mine = sum.total();
+  u64 block, total, unused = 0, before = row.scan_before(mine, block), lower;
+  total = tid == 0 ? block : 0;
+  if (C > 1) {
+    row.reduce(total, unused, &lower);
+    before += lower;
+  } else {
+    total = block;
+  }
+  const u64 share = u > 0.0f ? (u64)(fminf(u, 1.0f) * 16777216.0f) : 0ull;
+  const u64 r = part_of(total, share < 16777216ull ? share : 16777215ull);
+  const uint32_t hit = __ballot_sync(0xffffffffu, r >= before && r < before + mine);
+  if (hit) {
+    // this warp holds the run: its elements 32 at a time
+    const int l = __ffs(hit) - 1;
+    row.run = xs + (warp * 32 + l) * R;
+    row.index0 = rank * slice + (warp * 32 + l) * R;
+    u64 at = __shfl_sync(0xffffffffu, before, l);
+    for (int j0 = 0; j0 < R; j0 += 32) {
+      const int j = j0 + lane;
+      u64 w = j < R ? weight(kept_e(j)) : 0;
+#pragma unroll
+      for (int m = 1; m < 32; m *= 2) {
+        const u64 o = __shfl_up_sync(0xffffffffu, w, m);
+        if (lane >= m) w += o;
+      }
+      const uint32_t found = __ballot_sync(0xffffffffu, at + w > r);
+      if (found) {
+        if (lane == __ffs(found) - 1) {
+          a.tokens[b] = row.index0 + j;
+          if (a.logprobs) a.logprobs[b] = row.run[j] - top - logz;
+        }
+        break;
+      }
+      at += __shfl_sync(0xffffffffu, w, 31);
+    }
+  }
+  if (C > 1) cluster_sync_all();  // no CTA leaves while another may still read its shared memory
+}
+
+constexpr int kMaxRun = 51;  // 51 * 1024 floats and RowShared fill a CTA's shared memory
+
+// ---------------------------------------------------------------- longer rows
+template <typename T>
+__global__ void __launch_bounds__(kThreads) sample_wide_kernel(const __grid_constant__ SampleArgs a) {
   __shared__ unsigned long long buf[32], hist[256];
   __shared__ float fbuf[32];
   __shared__ unsigned long long pick_before;
@@ -256,9 +849,41 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
   }
 }
 
+static_assert(sizeof(RowShared) + kMaxRun * kThreads * 4 <= 232448, "shared memory of a CTA");
+
 template <typename T>
 int launch(const SampleArgs &a, cudaStream_t s) {
-  const cudaError_t e = launch_pdl(sample_kernel<T>, dim3((unsigned)a.B), dim3(kThreads), 0, s, a);
+  cudaError_t e;
+  if (a.V > (int64_t)8 * kMaxRun * kThreads) {
+    // longer than a cluster holds: read again for every pass
+    e = launch_pdl(sample_wide_kernel<T>, dim3((unsigned)a.B), dim3(kThreads), 0, s, a);
+  } else {
+    // as many CTAs a row as it needs, and more while the batch leaves SMs idle
+    int C = 1;
+    while ((int64_t)C * kMaxRun * kThreads < a.V) C *= 2;
+    while (C < 8 && a.B * C * 2 <= sm_count() && a.V > (int64_t)C * kThreads) C *= 2;
+    const int R = (int)((a.V + (int64_t)C * kThreads - 1) / ((int64_t)C * kThreads)) | 1;
+    const size_t smem = sizeof(RowShared) + (size_t)R * kThreads * sizeof(float);
+    if (a.B * C > 0x7fffffff) return set_error(TP_ERR_UNSUPPORTED, "too many rows for one launch");
+    auto kern = sample_row_kernel<T>;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return cuda_error(e, "sample launch");
+    cudaLaunchConfig_t cfg;
+    memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = dim3((unsigned)(a.B * C));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = C;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    e = cudaLaunchKernelEx(&cfg, kern, a, C, R);
+  }
   if (e != cudaSuccess) return cuda_error(e, "sample launch");
   note_launch();
   return TP_OK;
