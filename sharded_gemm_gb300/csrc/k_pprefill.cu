@@ -187,9 +187,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       uint32_t kv_phase = 0;
       bool ok = true;
       for (;; ++seq) {
-        // the next unit is asked for before this one's copies
-        long long next = 0;
-        if (lane == 0) next = (long long)gridDim.x + atomicAdd(pa.counters, 1);
         // find unit u: 32 sequences at a time from the cursor
         int64_t b = -1;
         long long base = 0;
@@ -220,8 +217,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         if (w.valid) {
           const long long local = u - base;
           const int blocks = (int)((t1 - t0 + block - 1) / block);
-          const int hu = (int)(local / blocks);
-          const int qb = blocks - 1 - (int)(local % blocks);  // longest first
+          // longest first, a block's heads side by side: the CTAs then walk the
+          // same key tiles of a head at about the same time
+          const int hu = (int)(local % heads_units);
+          const int qb = blocks - 1 - (int)(local / heads_units);
           w.b = (int)b;
           w.grp = hu % pa.groups;
           w.h = hu / pa.groups % a.Hk;
@@ -328,7 +327,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           }
         }
         if (!ok) break;
-        u = __shfl_sync(0xffffffffu, next, 0);
+        // The next unit is asked for only now, a ring of tiles before this one's
+        // products end: asked for earlier, units went to CTAs that were still busy.
+        if (lane == 0) u = (long long)gridDim.x + atomicAdd(pa.counters, 1);
+        u = __shfl_sync(0xffffffffu, u, 0);
       }
       if (!ok) {
         // gave up: the copies in flight still land in this CTA's shared memory
