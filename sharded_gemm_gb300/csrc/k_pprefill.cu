@@ -69,7 +69,7 @@ struct Unit {
 };
 
 struct Control {
-  uint64_t unit_full[2], unit_free[2], q_full[2], q_free[2], s_full[2], p_full[2], o_done[2], drain;
+  uint64_t unit_full[2], unit_free[2], q_full[2], q_free[2], s_full[2], p_full[2][2], o_done[2], drain;
   uint64_t kv_full[10], kv_free[10];
   Unit unit[2];
   uint32_t tmem;
@@ -107,6 +107,31 @@ __device__ __forceinline__ bool wait_inline(uint32_t bar, uint32_t parity, uint6
     done = __all_sync(0xffffffffu, done);
   }
   return done;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+// Two float32 operations in one instruction.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t y;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(a), "f"(b));
+  return y;
+}
+__device__ __forceinline__ void unpack2(uint64_t x, float &a, float &b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t y;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(y) : "l"(a), "l"(b), "l"(c));
+  return y;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t y;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(a), "l"(b));
+  return y;
 }
 
 template <int N>
@@ -150,7 +175,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       mbar_init(smem_u32(&ctl.q_full[i]), 64);
       mbar_init(smem_u32(&ctl.q_free[i]), 1);
       mbar_init(smem_u32(&ctl.s_full[i]), 1);
-      mbar_init(smem_u32(&ctl.p_full[i]), 4);
+      mbar_init(smem_u32(&ctl.p_full[i][0]), 4);
+      mbar_init(smem_u32(&ctl.p_full[i][1]), 4);
       mbar_init(smem_u32(&ctl.o_done[i]), 1);
     }
     mbar_init(smem_u32(&ctl.drain), 1);
@@ -168,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   }
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = ctl.tmem;
+  constexpr uint32_t tmem = 0;  // all 512 columns are this CTA's, so they begin at the first
   griddep_launch_dependents();
   griddep_wait();
 
@@ -342,95 +368,99 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       }
     } else if (warp == 1) {
       // ---------------------------------------------------------------- products
-      constexpr uint32_t fmt = sizeof(T) == 2 && Half2<T>::kBf16 ? 1 : 0;
-      constexpr uint32_t id_qk = umma_idesc_f16(fmt, 0, kTile, kTile), id_pv = umma_idesc_f16(fmt, 1, kTile, D);
-      int slot = 0;
-      uint32_t kv_phase = 0, p_phase[2] = {0, 0}, q_phase[2] = {0, 0};
-      bool ok = true;
-      for (int seq = 0; ok; ++seq) {
-        const int us = seq & 1;
-        ok = wait(ctl.unit_full[us], (seq >> 1) & 1);
-        if (!ok) break;
-        const int valid = ctl.unit[us].valid, n0 = ctl.unit[us].n[0], n1 = ctl.unit[us].n[1];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&ctl.unit_free[us]));
-        if (!valid) break;
-        const int n[2] = {n0, n1};
-        const int nmax = n0 > n1 ? n0 : n1;
+      // elect_one in place of a branch on the lane: the compiler then keeps the
+      // descriptors in uniform registers (an MMA runs for 64 cycles; issued from
+      // a plain branch it took 95).
+      if (elect_one()) {
+        auto wait1 = [&](uint64_t &bar, uint32_t parity) {
+          return mbar_wait(smem_u32(&bar), parity, limit, a.status, abort);
+        };
+        constexpr uint32_t fmt = Half2<T>::kBf16 ? 1 : 0;
+        constexpr uint32_t id_qk = umma_idesc_f16(fmt, 0, kTile, kTile), id_pv = umma_idesc_f16(fmt, 1, kTile, D);
+        int slot = 0, n0 = 0, n1 = 0;
+        uint32_t kv_phase = 0, p_phase0 = 0, p_phase1 = 0, q_phase = 0;
+        bool ok = true;
         auto qk = [&](int i, int ks) {  // S_i = Q_i K^T, K in ring slot ks
-          if (lane == 0) {
-            tc_fence_after();
-            const uint32_t qa = q_smem + i * S::kTileBytes, kb = kv_smem + ks * S::kTileBytes;
+          tc_fence_after();
+          const uint32_t qa = q_smem + i * S::kTileBytes, kb = kv_smem + ks * S::kTileBytes;
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t off = (kk / 4) * S::kHalf + (kk % 4) * 32;
-              umma_f16(tmem + i * kTile, umma_desc_sw128(qa + off, 16, 1024), umma_desc_sw128(kb + off, 16, 1024), id_qk,
-                       kk > 0);
-            }
-            umma_commit(smem_u32(&ctl.s_full[i]));
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk / 4) * S::kHalf + (kk % 4) * 32;
+            umma_f16(tmem + i * kTile, umma_desc_sw128(qa + off, 16, 1024), umma_desc_sw128(kb + off, 16, 1024), id_qk,
+                     kk > 0);
           }
-          __syncwarp();
+          umma_commit(smem_u32(&ctl.s_full[i]));
         };
-        auto pv = [&](int i, int vs, bool add) {  // O_i (+)= P_i V, V in ring slot vs
-          if (lane == 0) {
-            tc_fence_after();
-            const uint32_t vb = kv_smem + vs * S::kTileBytes;
+        auto pv = [&](int i, int vs, bool add, int half) {  // O_i (+)= P_i V over half the positions, V in slot vs
+          tc_fence_after();
+          const uint32_t vb = kv_smem + vs * S::kTileBytes;
 #pragma unroll
-            for (int kk = 0; kk < kTile / 16; ++kk)
-              umma_f16_ts(tmem + 256 + i * D, tmem + i * kTile + kk * 8, umma_desc_sw128(vb + kk * 2048, S::kHalf, 1024),
-                          id_pv, add || kk > 0);
-            umma_commit(smem_u32(&ctl.o_done[i]));
+          for (int k = 0; k < kTile / 32; ++k) {
+            const int kk = half * (kTile / 32) + k;
+            umma_f16_ts(tmem + 256 + i * D, tmem + i * kTile + kk * 8, umma_desc_sw128(vb + kk * 2048, S::kHalf, 1024),
+                        id_pv, add || kk > 0);
           }
-          __syncwarp();
+          if (half) umma_commit(smem_u32(&ctl.o_done[i]));
         };
-        auto next_slot = [&]() {
+        auto take = [&](int &taken) {  // the next filled ring slot
+          taken = slot;
+          ok = wait1(ctl.kv_full[slot], kv_phase);
           if (++slot == S::kSlots) slot = 0, kv_phase ^= 1;
         };
-        auto release = [&](uint64_t &bar) {
-          if (lane == 0) umma_commit(smem_u32(&bar));
-          __syncwarp();
+        auto first = [&](int i, int n, int ks) {
+          if (ok) ok = wait1(ctl.q_full[i], q_phase);  // loaded for every unit, used or not
+          if (!ok) return;
+          if (n > 0) qk(i, ks);
+          if (n <= 1) umma_commit(smem_u32(&ctl.q_free[i]));
         };
-        // first scores
-        int ks = slot;
-        if (nmax > 0) {
-          ok = wait(ctl.kv_full[slot], kv_phase);
-          next_slot();
-        }
-        for (int i = 0; i < 2 && ok; ++i) {
-          ok = wait(ctl.q_full[i], q_phase[i]);  // loaded for every unit, used or not
-          q_phase[i] ^= 1;
+        auto values = [&](int i, int n, int j, int vs, uint32_t &p_phase) {
+          if (!ok || j >= n) return;
+          ok = wait1(ctl.p_full[i][0], p_phase);
+          if (!ok) return;
+          pv(i, vs, j > 0, 0);
+          ok = wait1(ctl.p_full[i][1], p_phase);
+          if (!ok) return;
+          p_phase ^= 1;
+          pv(i, vs, true, 1);
+        };
+        auto scores = [&](int i, int n, int j, int ks) {
+          if (!ok) return;
+          if (j + 1 < n) qk(i, ks);
+          if (j + 2 == n) umma_commit(smem_u32(&ctl.q_free[i]));
+        };
+        for (int seq = 0; ok; ++seq) {
+          const int us = seq & 1;
+          ok = wait1(ctl.unit_full[us], (seq >> 1) & 1);
           if (!ok) break;
-          if (n[i] > 0) qk(i, ks);
-          if (n[i] <= 1) release(ctl.q_free[i]);
-        }
-        if (nmax > 0 && ok) release(ctl.kv_free[ks]);
-        for (int j = 0; j < nmax && ok; ++j) {
-          const int vs = slot;
-          ok = wait(ctl.kv_full[vs], kv_phase);
-          if (!ok) break;
-          next_slot();
-          ks = slot;
-          if (j + 1 < nmax) {
-            ok = wait(ctl.kv_full[ks], kv_phase);
-            if (!ok) break;
-            next_slot();
+          const int valid = ctl.unit[us].valid;
+          n0 = ctl.unit[us].n[0], n1 = ctl.unit[us].n[1];
+          mbar_arrive(smem_u32(&ctl.unit_free[us]));
+          if (!valid) break;
+          const int nmax = n0 > n1 ? n0 : n1;
+          int ks = 0, vs = 0, next_vs = 0;
+          if (nmax > 0) take(ks);
+          first(0, n0, ks);
+          first(1, n1, ks);
+          q_phase ^= 1;
+          if (nmax > 0 && ok) {
+            umma_commit(smem_u32(&ctl.kv_free[ks]));
+            take(vs);
           }
-          for (int i = 0; i < 2 && ok; ++i) {
-            if (j >= n[i]) continue;
-            ok = wait(ctl.p_full[i], p_phase[i]);
-            p_phase[i] ^= 1;
+          // Waits stand where products just issued still run.
+          for (int j = 0; j < nmax && ok; ++j) {
+            values(0, n0, j, vs, p_phase0);
+            if (ok && j + 1 < nmax) take(ks);
+            scores(0, n0, j, ks);
+            if (ok && j + 1 < nmax) take(next_vs);
+            values(1, n1, j, vs, p_phase1);
+            scores(1, n1, j, ks);
             if (!ok) break;
-            pv(i, vs, j > 0);
-            if (j + 1 < n[i]) qk(i, ks);
-            if (j + 2 == n[i]) release(ctl.q_free[i]);
+            umma_commit(smem_u32(&ctl.kv_free[vs]));
+            if (j + 1 < nmax) umma_commit(smem_u32(&ctl.kv_free[ks]));
+            vs = next_vs;
           }
-          if (!ok) break;
-          release(ctl.kv_free[vs]);
-          if (j + 1 < nmax) release(ctl.kv_free[ks]);
         }
-      }
-      // every product issued has ended before the tensor memory goes back
-      if (lane == 0) {
+        // every product issued has ended before the tensor memory goes back
         umma_commit(smem_u32(&ctl.drain));
         mbar_wait(smem_u32(&ctl.drain), 0, limit, a.status, nullptr);
       }
@@ -547,57 +577,72 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             for (int x = 0; x < 32; ++x)
               if ((c * 32 + x < from || c * 32 + x >= to) && c * 32 + x >= pre) s[c][x] = -INFINITY;
         }
+        const float f = cap ? 1.0f : scale;
+        const uint64_t f2 = pack2(f, f);
+        // terms of half the positions into tensor memory, and their sum
+        auto half = [&](int h, float neg) {
+          const uint64_t neg2 = pack2(neg, neg);
+          uint64_t sum[2] = {0, 0};
+#pragma unroll
+          for (int c = 2 * h; c < 2 * h + 2; ++c) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+              float e0, e1;
+              unpack2(fma2(pack2(s[c][2 * x], s[c][2 * x + 1]), f2, neg2), e0, e1);
+              e0 = exp2_approx(e0), e1 = exp2_approx(e1);
+              sum[x & 1] = add2(sum[x & 1], pack2(e0, e1));
+              pk[x] = Half2<T>::pack(e0, e1);
+            }
+            tmem_st16(s_tmem + c * 16, pk);
+          }
+          float a0, a1;
+          unpack2(add2(sum[0], sum[1]), a0, a1);
+          return a0 + a1;
+        };
+        auto ready = [&](int h) {
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&ctl.p_full[i][h]));
+        };
+        // The first half goes by the maximum so far while the tile's own is
+        // found: most tiles do not raise it, and the two run side by side.
+        float sum0 = half(0, m == -INFINITY ? 0.0f : -m);
         float top[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          top[c] = s[c][0];
+          top[c] = fmaxf(s[c][0], s[c][1]);
 #pragma unroll
-          for (int x = 1; x < 32; ++x) top[c] = fmaxf(top[c], s[c][x]);
+          for (int x = 2; x < 32; x += 2) top[c] = max3(top[c], s[c][x], s[c][x + 1]);
         }
-        const float f = cap ? 1.0f : scale;
         const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * f;
         const bool rise = mx > m + kSlack;
-        if (j == 0) {
-          m = mx;
-        } else if (__any_sync(0xffffffffu, rise)) {
-          // the products up to the previous tile have to be in O
-          ok = wait_inline(smem_u32(&ctl.o_done[i]), (o_count - 1) & 1, limit, a.status, abort);
-          if (!ok) break;
-          tc_fence_after();
+        if (__any_sync(0xffffffffu, rise)) {
           const float keep = rise ? exp2_approx(m - mx) : 1.0f;
           if (rise) m = mx;
           l *= keep;
+          if (j > 0) {
+            // the products up to the previous tile have to be in O
+            ok = wait_inline(smem_u32(&ctl.o_done[i]), (o_count - 1) & 1, limit, a.status, abort);
+            if (!ok) break;
+            tc_fence_after();
 #pragma unroll
-          for (int c = 0; c < D / 16; ++c) {
-            float o[16];
-            uint32_t r[16];
-            tmem_ld16(o_tmem + c * 16, o);
-            tmem_wait_ld();
+            for (int c = 0; c < D / 16; ++c) {
+              float o[16];
+              uint32_t r[16];
+              tmem_ld16(o_tmem + c * 16, o);
+              tmem_wait_ld();
 #pragma unroll
-            for (int x = 0; x < 16; ++x) r[x] = __float_as_uint(o[x] * keep);
-            tmem_st16(o_tmem + c * 16, r);
+              for (int x = 0; x < 16; ++x) r[x] = __float_as_uint(o[x] * keep);
+              tmem_st16(o_tmem + c * 16, r);
+            }
           }
+          sum0 = half(0, m == -INFINITY ? 0.0f : -m);
         }
-        const float neg = m == -INFINITY ? 0.0f : -m;
-        float sum[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t pk[16];
-          sum[c] = 0.0f;
-#pragma unroll
-          for (int x = 0; x < 16; ++x) {
-            const float e0 = exp2_approx(fmaf(s[c][2 * x], f, neg)), e1 = exp2_approx(fmaf(s[c][2 * x + 1], f, neg));
-            sum[c] += e0;
-            sum[c] += e1;
-            pk[x] = Half2<T>::pack(e0, e1);
-          }
-          tmem_st16(s_tmem + c * 16, pk);
-        }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&ctl.p_full[i]));
+        ready(0);
+        l += sum0 + half(1, m == -INFINITY ? 0.0f : -m);
+        ready(1);
         ++o_count;
       }
       if (!ok) break;
@@ -643,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(ctl.tmem, 512);
   }
 }
 
