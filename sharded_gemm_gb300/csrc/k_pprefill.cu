@@ -35,8 +35,8 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kTile = 128;  // rows of a query tile, positions of a key tile
 constexpr float kSlack = 8.0f;
-// Registers a thread: 384 * 168 at launch = 128 * 72 + 256 * 216.
-constexpr int kRegsFew = 72, kRegsMany = 216;
+// Registers a thread: 384 * 168 at launch = 128 * 88 + 256 * 208.
+constexpr int kRegsFew = 88, kRegsMany = 208;
 
 template <int D>
 struct Sh {
@@ -113,6 +113,11 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float y;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
   return y;
+}
+// The n lowest bits, n clamped to 0..32.
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  n = n < 0 ? 0 : n > 32 ? 32 : n;
+  return (uint32_t)((1ull << n) - 1);
 }
 // Two float32 operations in one instruction.
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
@@ -299,25 +304,24 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         const int nmax = w.n[0] > w.n[1] ? w.n[0] : w.n[1];
         const int *table = a.block_table + w.b * a.ld_table;
         const int pieces = kTile / pa.box;  // page copies of a tile
-        for (int j = 0; j < nmax && ok; ++j) {
-          const int jt = w.j0 + j * kTile;
-          // lane i < pieces: piece i's page, its row in the map, whether it is read, whether all of it is
-          int row = -1;
-          bool part = false;
-          if (lane < pieces) {
-            const int pj = jt + lane * pa.box;
-            if (pj < w.to && pj + pa.box > w.seen0) {
-              const int pg = table[pj >> a.page_log2];
-              if (pg < 0 || pg >= a.pages) {
-                record_bad_value(a.status);
-              } else {
-                row = (int)(pg * (a.ld_page / D) + (int64_t)w.h * a.page + (pj & (a.page - 1)));
-                part = pj + pa.box > w.to;
-              }
-            }
+        // lane i < pieces: the row in the map of piece i of tile j, -1 where it is not read
+        auto lookup = [&](int j) {
+          const int pj = w.j0 + j * kTile + lane * pa.box;
+          if (lane >= pieces || pj >= w.to || pj + pa.box <= w.seen0) return -1;
+          const int pg = table[pj >> a.page_log2];
+          if (pg < 0 || pg >= a.pages) {
+            record_bad_value(a.status);
+            return -1;
           }
+          return (int)(pg * (a.ld_page / D) + (int64_t)w.h * a.page + (pj & (a.page - 1)));
+        };
+        int next_row = nmax > 0 ? lookup(0) : -1;
+        for (int j = 0; j < nmax && ok; ++j) {
+          const int jt = w.j0 + j * kTile, row = next_row;
+          const bool part = jt + (lane + 1) * pa.box > w.to;
           const uint32_t read = __ballot_sync(0xffffffffu, row >= 0);
           const uint32_t whole = __ballot_sync(0xffffffffu, row >= 0 && !part);
+          if (j + 1 < nmax) next_row = lookup(j + 1);  // a tile ahead: the table's latency stays off the copies
           for (int kv = 0; kv < 2 && ok; ++kv) {
             ok = wait(ctl.kv_free[slot], kv_phase ^ 1);
             if (!ok) break;
@@ -542,6 +546,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       if (!w.valid) break;
       const int heads = G - w.grp * pa.gsize < pa.gsize ? G - w.grp * pa.gsize : pa.gsize;
       const bool live = tk < pa.tpt && i * pa.tpt + tk < w.ntok && hd < heads;
+      T *out = live ? static_cast<T *>(a.o[w.r]) + (int64_t)(w.tok0 + i * pa.tpt + tk) * a.ldo +
+                          ((int64_t)w.h * G + w.grp * pa.gsize + hd) * D
+                    : nullptr;
+      const int tiles = w.n[i], prefix = w.prefix;
+      int jt = w.j0;
       // this row sees [lo, hi) and [0, prefix)
       const int pos = w.pos0 + i * pa.tpt + tk;
       const int hi = pos + 1 < w.to ? pos + 1 : w.to;
@@ -552,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       const int pos_last = w.pos0 + i * pa.tpt + t_last;
       const int all_lo = a.window && pos_last - a.window + 1 > 0 ? pos_last - a.window + 1 : 0;
       float m = -INFINITY, l = 0.0f;
-      for (int j = 0; j < w.n[i]; ++j) {
+      for (int j = 0; j < tiles; ++j, jt += kTile) {
         ok = wait_inline(smem_u32(&ctl.s_full[i]), s_phase, limit, a.status, abort);
         s_phase ^= 1;
         if (!ok) break;
@@ -561,7 +570,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(s_tmem + c * 32, s[c]);
         tmem_wait_ld();
-        const int jt = w.j0 + j * kTile;
         if (cap) {
 #pragma unroll
           for (int c = 0; c < 4; ++c)
@@ -569,13 +577,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             for (int x = 0; x < 32; ++x)
               s[c][x] = fmaf(-2.0f * cap2, rcp_approx(1.0f + exp2_approx(s[c][x] * scale)), cap2);
         }
-        if (!(jt + kTile <= w.prefix || (jt >= all_lo && jt + kTile <= all_hi))) {
-          const int from = lo - jt, to = hi - jt, pre = w.prefix - jt;
+        if (!(jt + kTile <= prefix || (jt >= all_lo && jt + kTile <= all_hi))) {
+          // one bit a position: compared one by one they cost the registers of the scores
+          const int from = lo - jt, to = hi - jt, pre = prefix - jt;
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t seen = (low_bits(to - c * 32) & ~low_bits(from - c * 32)) | low_bits(pre - c * 32);
 #pragma unroll
             for (int x = 0; x < 32; ++x)
-              if ((c * 32 + x < from || c * 32 + x >= to) && c * 32 + x >= pre) s[c][x] = -INFINITY;
+              if (!(seen >> x & 1)) s[c][x] = -INFINITY;
+          }
         }
         const float f = cap ? 1.0f : scale;
         const uint64_t f2 = pack2(f, f);
@@ -646,25 +657,23 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         ++o_count;
       }
       if (!ok) break;
-      if (w.n[i] > 0) {
+      if (tiles > 0) {
         ok = wait_inline(smem_u32(&ctl.o_done[i]), (o_count - 1) & 1, limit, a.status, abort);
         if (!ok) break;
         tc_fence_after();
       }
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-      T *out = static_cast<T *>(a.o[w.r]) + (int64_t)(w.tok0 + i * pa.tpt + tk) * a.ldo +
-               ((int64_t)w.h * G + w.grp * pa.gsize + hd) * D;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         float o[32];
-        if (w.n[i] > 0) {
+        if (tiles > 0) {
           tmem_ld32(o_tmem + c * 32, o);
           tmem_wait_ld();
         } else {
 #pragma unroll
           for (int x = 0; x < 32; ++x) o[x] = 0.0f;
         }
-        if (live) {
+        if (out) {
           uint32_t pk[16];
 #pragma unroll
           for (int x = 0; x < 16; ++x) pk[x] = Half2<T>::pack(o[2 * x] * inv, o[2 * x + 1] * inv);
