@@ -23,7 +23,7 @@ struct AppendArgs {
   const int32_t *positions;      // (T), read where rope is given
   const int64_t *slots;          // (T)
   int64_t T, ld, ldq, pages, ld_page, rope_rows;
-  int N, Hq, Hk, D, page, rot, interleaved;
+  int N, Hq, Hk, D, page, page_log2, rot, interleaved;
   int in_dt, dt;
   float eps;
   int *status;

@@ -70,78 +70,104 @@ __device__ __forceinline__ void store8(T *p, bool vec, const float (&x)[8]) {
   }
 }
 
+// 8 consecutive floats of a table, 16-byte aligned where vec.
+__device__ __forceinline__ void table8(const float *p, bool vec, float (&x)[8]) {
+  if (vec) {
+    const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = __ldg(p + i);
+  }
+}
+__device__ __forceinline__ void table4(const float *p, bool vec, float (&x)[4]) {
+  if (vec) {
+    const float4 a = __ldg(reinterpret_cast<const float4 *>(p));
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = __ldg(p + i);
+  }
+}
+
 constexpr int kThreads = 256;
 
+struct Aligned {
+  bool in, q, rope, gain;  // 16-byte accesses possible
+};
+
+// Block (x, y, z): x tokens, y a stretch of HPG heads, z a rank.
 template <typename TIn, typename T, int D, int HPG>
-__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendArgs a, int chunks,
-                                                          int64_t groups, int vec_in, int vec_q) {
+__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendArgs a, const Aligned vec) {
   constexpr int L = D / 8;  // lanes of a head
   griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x % L;
   // the lanes of this thread's group: groups of one warp may take different branches
   const uint32_t mask = ((1u << L) - 1) << (threadIdx.x % 32 - lane);
-  const int64_t g = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / L;
-  if (g >= groups) return;
-  const int chunk = (int)(g % chunks);
-  const int64_t unit = g / chunks;
-  const int64_t t = unit % a.T;
-  const int r = (int)(unit / a.T);
-  const int H = a.Hq + 2 * a.Hk, h0 = chunk * HPG;
-  const TIn *src = static_cast<const TIn *>(a.qkv[r]) + t * a.ld + lane * 8;
+  const int64_t t = (int64_t)blockIdx.x * (kThreads / L) + threadIdx.x / L;
+  if (t >= a.T) return;
+  const int r = blockIdx.z, H = a.Hq + 2 * a.Hk, h0 = blockIdx.y * HPG, i0 = lane * 8;
+  const TIn *src = static_cast<const TIn *>(a.qkv[r]) + t * a.ld + i0;
 
   float x[HPG][8];
 #pragma unroll
   for (int i = 0; i < HPG; ++i)
-    if (h0 + i < H) load8<TIn>(src + (int64_t)(h0 + i) * D, vec_in, x[i]);
+    if (h0 + i < H) load8<TIn>(src + (int64_t)(h0 + i) * D, vec.in, x[i]);
 
-  const int64_t slot = a.slots[t];
-  bool write_kv = slot >= 0;
-  if (slot >= a.pages * a.page) {
-    write_kv = false;
-    if (lane == 0) record_bad_value(a.status);
+  int64_t slot = -1;
+  if (h0 + HPG > a.Hq) {
+    slot = __ldg(a.slots + t);
+    if (slot >= a.pages << a.page_log2) {
+      slot = -1;
+      if (lane == 0) record_bad_value(a.status);
+    }
   }
-  const int64_t pg = write_kv ? slot / a.page : 0;
-  const int off = write_kv ? (int)(slot - pg * a.page) : 0;
+  const int64_t pg = slot >> a.page_log2;
+  const int off = (int)slot & (a.page - 1);
 
   // Rotation: this lane's factors.  Halves: value i < rot/2 pairs with
   // i + rot/2, factor i.  Neighbours: values 2i, 2i + 1, factor i.
-  const int half = a.rot / 2, i0 = lane * 8;
+  const int half = a.rot / 2;
   const bool turns = i0 < a.rot;
   float c[8], s[8];
   if (turns && h0 < a.Hq + a.Hk) {
-    int64_t pos = a.positions[t];
+    int64_t pos = __ldg(a.positions + t);
     if (pos < 0 || pos >= a.rope_rows) {
       pos = 0;
       if (lane == 0) record_bad_value(a.status);
     }
     const float *row = a.rope + pos * a.rot;
     if (a.interleaved) {
+      float c4[4], s4[4];
+      table4(row + i0 / 2, vec.rope, c4);
+      table4(row + half + i0 / 2, vec.rope, s4);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        c[2 * i] = c[2 * i + 1] = __ldg(row + i0 / 2 + i);
-        s[2 * i + 1] = __ldg(row + half + i0 / 2 + i);
-        s[2 * i] = -s[2 * i + 1];
+        c[2 * i] = c[2 * i + 1] = c4[i];
+        s[2 * i] = -s4[i], s[2 * i + 1] = s4[i];
       }
     } else {
       const int f0 = i0 < half ? i0 : i0 - half;
-      const float sign = i0 < half ? -1.0f : 1.0f;
+      table8(row + f0, vec.rope, c);
+      table8(row + half + f0, vec.rope, s);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        c[i] = __ldg(row + f0 + i);
-        s[i] = sign * __ldg(row + half + f0 + i);
-      }
+      for (int i = 0; i < 8; ++i) s[i] = i0 < half ? -s[i] : s[i];
     }
   }
 
+  float gain[8];
+  const float *gain_of = nullptr;  // whose gains are held
 #pragma unroll
   for (int i = 0; i < HPG; ++i) {
     const int h = h0 + i;
     if (h >= H) break;
     float (&y)[8] = x[i];
     if (h < a.Hq + a.Hk) {
-      const float *gain = h < a.Hq ? a.q_norm : a.k_norm;
-      if (gain) {
+      const float *want = h < a.Hq ? a.q_norm : a.k_norm;
+      if (want) {
+        if (want != gain_of) table8(want + i0, vec.gain, gain);
+        gain_of = want;
         float sum = 0.0f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) sum = fmaf(y[j], y[j], sum);
@@ -149,7 +175,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
         for (int m = L / 2; m > 0; m /= 2) sum += __shfl_xor_sync(mask, sum, m);
         const float inv = rsqrtf(sum * (1.0f / D) + a.eps);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] *= inv * __ldg(gain + i0 + j);
+        for (int j = 0; j < 8; ++j) y[j] *= inv * gain[j];
       }
       if (a.rot) {
         float p[8];
@@ -168,11 +194,11 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
         }
       }
       if (h < a.Hq) {
-        store8<T>(static_cast<T *>(a.q[r]) + t * a.ldq + (int64_t)h * D + i0, vec_q, y);
+        store8<T>(static_cast<T *>(a.q[r]) + t * a.ldq + (int64_t)h * D + i0, vec.q, y);
         continue;
       }
     }
-    if (write_kv) {
+    if (slot >= 0) {
       const bool is_k = h < a.Hq + a.Hk;
       const int kh = h - a.Hq - (is_k ? 0 : a.Hk);
       T *page = static_cast<T *>(is_k ? a.k_cache[r] : a.v_cache[r]) + pg * a.ld_page;
@@ -184,22 +210,22 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
 template <typename TIn, typename T, int D>
 int launch(const AppendArgs &a, cudaStream_t s) {
   const int H = a.Hq + 2 * a.Hk;
-  bool vec_in = (a.ld * (int64_t)sizeof(TIn)) % 16 == 0, vec_q = (a.ldq * 2) % 16 == 0;
+  auto aligned = [](const void *p) { return (uintptr_t)p % 16 == 0; };
+  Aligned vec;
+  vec.in = (a.ld * (int64_t)sizeof(TIn)) % 16 == 0, vec.q = (a.ldq * 2) % 16 == 0;
   for (int r = 0; r < a.N; ++r) {
-    vec_in = vec_in && (uintptr_t)a.qkv[r] % 16 == 0;
-    vec_q = vec_q && (uintptr_t)a.q[r] % 16 == 0;
+    vec.in = vec.in && aligned(a.qkv[r]);
+    vec.q = vec.q && aligned(a.q[r]);
   }
-  const bool wide = a.T * a.N * H >= 8192;
+  vec.rope = aligned(a.rope), vec.gain = aligned(a.q_norm) && aligned(a.k_norm);
+  const bool wide = a.T * a.N * H >= 8192;  // fewer: one head a group, for more groups
   const int hpg = wide ? 4 : 1;
-  const int chunks = (H + hpg - 1) / hpg;
-  const int64_t groups = a.T * a.N * chunks;
-  const int64_t blocks = (groups * (D / 8) + kThreads - 1) / kThreads;
-  if (blocks > 0x7fffffff) return set_error(TP_ERR_UNSUPPORTED, "T * N * heads too large for one launch");
-  const cudaError_t e =
-      wide ? launch_pdl(append_kernel<TIn, T, D, 4>, dim3((unsigned)blocks), dim3(kThreads), 0, s, a, chunks, groups,
-                        (int)vec_in, (int)vec_q)
-           : launch_pdl(append_kernel<TIn, T, D, 1>, dim3((unsigned)blocks), dim3(kThreads), 0, s, a, chunks, groups,
-                        (int)vec_in, (int)vec_q);
+  const int64_t blocks = (a.T + kThreads / (D / 8) - 1) / (kThreads / (D / 8)), stretches = (H + hpg - 1) / hpg;
+  if (blocks > 0x7fffffff || stretches > 65535)
+    return set_error(TP_ERR_UNSUPPORTED, "too many tokens or heads for one launch");
+  const dim3 grid((unsigned)blocks, (unsigned)stretches, (unsigned)a.N), block(kThreads);
+  const cudaError_t e = wide ? launch_pdl(append_kernel<TIn, T, D, 4>, grid, block, 0, s, a, vec)
+                             : launch_pdl(append_kernel<TIn, T, D, 1>, grid, block, 0, s, a, vec);
   if (e != cudaSuccess) return cuda_error(e, "append launch");
   note_launch();
   return TP_OK;

@@ -4,11 +4,11 @@
 // Work.  An item is one sequence, rank, key-value head and group of at most
 // 8 * NT query heads of it.  Its visible positions are cut into units of 128
 // (eight chunks of 16); the units of all items, in order, are dealt out to the
-// CTAs in equal consecutive ranges, so every SM streams the same number of bytes
-// however uneven the lengths are.  A CTA's range covers pieces of one or more
-// items; an item that spans CTAs leaves its pieces' unnormalised sums in the
-// workspace and the last CTA to arrive joins them in CTA order (same bytes every
-// time).
+// CTAs in consecutive ranges of equal cost (kUnitCost a unit, kItemCost an item:
+// its warps' parts have to be merged), so every SM has the same work however
+// uneven the lengths are.  A CTA's range covers pieces of one or more items; an
+// item that spans CTAs leaves its pieces' unnormalised sums in the workspace and
+// the last CTA to arrive joins them in CTA order (same bytes every time).
 //
 // A piece.  Warp w takes chunks w, w + 8, ... through a ring of asynchronous
 // copies of its own (no barrier between warps until the piece ends); chunk rows
@@ -42,6 +42,11 @@ struct Shape {
   static constexpr int kMergeBytes = kWarps * kHeads * (kRow + 2) * 4;
   static constexpr int kSmem = kRingBytes + kMergeBytes;
   static constexpr int kSlot = kHeads * (D + 2);                      // floats of a workspace piece
+  // Cost of a unit and of an item (its start and the merge of its parts), in
+  // 0.37 us: a unit streams in 0.73 us at D = 64 and 1.47 at 128, and item
+  // costs of 2..6 gave 106, 102, 99, 96, 97 us for 16 sequences of 100..4096
+  // positions on 32 heads of 128, 36, 33, 32, 32, 32 for 48 windows of 1024 at 64.
+  static constexpr int kUnitCost = D / 32, kItemCost = 5;
 };
 
 struct Plan {
@@ -73,8 +78,8 @@ __device__ __forceinline__ Span span_of(const AttnArgs &a, int64_t b) {
 // A place in the CTA's list of pieces.
 struct Piece {
   int64_t b;
-  int item, units;  // item of sequence b, units of the piece
-  int unit0;        // its first unit within the item
+  int item, unit0, units;  // item of sequence b, the piece's first unit in it, its units
+  long long at;            // where the item begins, in cost
   Span span;
   bool valid;
 };
@@ -85,7 +90,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using Sh = Shape<D, NT>;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ long long s_scan[kWarps + 1];
-  __shared__ long long s_start_b, s_start_rest;
+  __shared__ long long s_start_b, s_start_at;
   __shared__ int s_last;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
   griddep_launch_dependents();
@@ -95,7 +100,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int ips = plan.items_per_seq;
   const int64_t per = (a.B + kThreads - 1) / kThreads, b0 = tid * per, b1 = b0 + per < a.B ? b0 + per : a.B;
   long long mine = 0;
-  for (int64_t b = b0; b < b1; ++b) mine += span_of(a, b).units;
+  constexpr int UC = Sh::kUnitCost, IC = Sh::kItemCost;
+  auto cost = [&](const Span &s) { return s.units ? ips * (IC + (long long)UC * s.units) : 0ll; };
+  for (int64_t b = b0; b < b1; ++b) mine += cost(span_of(a, b));
   long long scan = mine;
 #pragma unroll
   for (int m = 1; m < 32; m *= 2) {
@@ -110,76 +117,97 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (w < warp) before += s_scan[w];
     total += s_scan[w];
   }
-  total *= ips;
-  before *= ips;
-  // no more CTAs than units, so that each has one and an item's CTAs are consecutive
-  const long long grid = total < gridDim.x ? total : gridDim.x, cta = blockIdx.x;
-  const long long u0 = cta < grid ? cta * total / grid : 0, u1 = cta < grid ? (cta + 1) * total / grid : 0;
-  if (u0 < u1 && u0 >= before && u0 < before + mine * ips) {
+  // every CTA's range is at least a unit long: those inside an item then hold a unit of it
+  const long long most = total / UC, grid = most < gridDim.x ? most : gridDim.x, cta = blockIdx.x;
+  const long long x0 = cta < grid ? cta * total / grid : 0, x1 = cta < grid ? (cta + 1) * total / grid : 0;
+  if (x0 < x1 && x0 >= before && x0 < before + mine) {
     long long at = before;
     for (int64_t b = b0; b < b1; ++b) {
-      const long long u = (long long)span_of(a, b).units * ips;
-      if (u0 < at + u) {
+      const long long c = cost(span_of(a, b));
+      if (x0 < at + c) {
         s_start_b = b;
-        s_start_rest = u0 - at;
+        s_start_at = at;
         break;
       }
-      at += u;
+      at += c;
     }
   }
   __syncthreads();
 
-  // Sequences with nothing visible: zeros.
-  for (int64_t b = cta; b < a.B; b += gridDim.x)
-    if (span_of(a, b).units == 0)
-      for (int i = tid; i < a.N * a.Hq * D; i += kThreads)
-        static_cast<T *>(a.o[i / (a.Hq * D)])[b * a.ldo + i % (a.Hq * D)] = static_cast<T>(0.0f);
-  if (u0 == u1) return;
-
-  // ---- the list of pieces, walked twice: by the copies, ahead, and by the products
-  auto first_piece = [&]() {
-    Piece p;
-    p.b = s_start_b;
-    p.span = span_of(a, p.b);
-    p.item = (int)(s_start_rest / p.span.units);
-    p.unit0 = (int)(s_start_rest % p.span.units);
-    const long long left = u1 - u0;
-    p.units = (int)(left < p.span.units - p.unit0 ? left : p.span.units - p.unit0);
-    p.valid = true;
-    return p;
-  };
-  auto next_piece = [&](Piece &p, long long &done) {  // done: units of the pieces up to and with p
-    if (done >= u1 - u0) {
-      p.valid = false;
-      return;
+  // ---- the list of pieces, walked twice: by the copies, ahead, and by the products.
+  // Unit u of an item that begins at `at` belongs to the CTA whose range holds
+  // at + IC + u * UC.
+  auto settle = [&](Piece &p) {  // p is an item: its units in this range, or the next item that has some
+    for (;;) {
+      if (p.at >= x1) {
+        p.valid = false;
+        return;
+      }
+      const long long lo = x0 - p.at - IC + UC - 1, hi = x1 - p.at - IC + UC - 1;
+      p.unit0 = lo > 0 ? (int)(lo / UC) : 0;
+      const int end = hi > 0 ? (hi / UC < p.span.units ? (int)(hi / UC) : p.span.units) : 0;
+      p.units = end - p.unit0;
+      if (p.units > 0) return;
+      p.at += IC + (long long)UC * p.span.units;
+      if (++p.item == ips) {
+        p.item = 0;
+        do {
+          if (++p.b >= a.B) {
+            p.valid = false;
+            return;
+          }
+          p.span = span_of(a, p.b);
+        } while (p.span.units == 0);
+      }
     }
-    p.unit0 = 0;
+  };
+  auto next_piece = [&](Piece &p) {
+    p.at += IC + (long long)UC * p.span.units;
     if (++p.item == ips) {
       p.item = 0;
       do {
-        p.span = span_of(a, ++p.b);
+        if (++p.b >= a.B) {
+          p.valid = false;
+          return;
+        }
+        p.span = span_of(a, p.b);
       } while (p.span.units == 0);
     }
-    const long long left = u1 - u0 - done;
-    p.units = (int)(left < p.span.units ? left : p.span.units);
-    done += p.units;
+    settle(p);
   };
+  Piece p;
+  p.valid = x0 < x1;
+  if (p.valid) {
+    p.b = s_start_b;
+    p.span = span_of(a, p.b);
+    const long long each = IC + (long long)UC * p.span.units;
+    p.item = (int)((x0 - s_start_at) / each);
+    p.at = s_start_at + p.item * each;
+    settle(p);
+  }
 
   const uint32_t ring = smem_u32(smem) + warp * (Sh::kStages * 2 * Sh::kChunkBytes);
   float *merge = reinterpret_cast<float *>(smem + Sh::kRingBytes);
 
   // ---- copies
-  Piece cp = first_piece();
-  long long cp_done = cp.units;
+  Piece cp = p;
   int cp_unit = 0, cp_stage = 0, cp_page_at = -32;
   int cp_pages = 0;  // lane i: the page of this warp's chunk in unit cp_page_at + i
   constexpr int kLanesPerRow = D / 8, kRowsPerCopy = 32 / kLanesPerRow;
   const int c_row = lane / kLanesPerRow, c_col = lane % kLanesPerRow;
+  const T *cp_k = nullptr, *cp_v = nullptr;  // the piece's head in page 0, at this lane's place
+  auto cp_head = [&]() {
+    const int rh = cp.item / plan.groups, r = rh / a.Hk, h = rh - r * a.Hk;
+    const int64_t off = ((int64_t)h * a.page + c_row) * D + c_col * 8;
+    cp_k = static_cast<const T *>(a.k_cache[r]) + off, cp_v = static_cast<const T *>(a.v_cache[r]) + off;
+  };
+  if (cp.valid) cp_head();
   auto issue = [&]() {
     if (cp.valid) {
+      const int j0 = cp.span.from + (cp.unit0 + cp_unit) * kUnit + warp * 16;
       if (cp_unit - cp_page_at >= 32) {
         cp_page_at = cp_unit;
-        const int j = cp.span.from + (cp.unit0 + cp_unit + lane) * kUnit + warp * 16;
+        const int j = j0 + lane * kUnit;
         cp_pages = -1;
         if (cp_unit + lane < cp.units && j < cp.span.to) {
           cp_pages = a.block_table[cp.b * a.ld_table + (j >> a.page_log2)];
@@ -190,22 +218,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       const int pg = __shfl_sync(0xffffffffu, cp_pages, cp_unit - cp_page_at);
-      const int j0 = cp.span.from + (cp.unit0 + cp_unit) * kUnit + warp * 16;
-      const int rh = cp.item / plan.groups, r = rh / a.Hk, h = rh - r * a.Hk;
-      const int64_t base =
-          (int64_t)(pg < 0 ? 0 : pg) * a.ld_page + ((int64_t)h * a.page + (j0 & (a.page - 1))) * D + c_col * 8;
-      const T *k = static_cast<const T *>(a.k_cache[r]) + base, *v = static_cast<const T *>(a.v_cache[r]) + base;
-      const uint32_t dst = ring + cp_stage * (2 * Sh::kChunkBytes);
+      const int64_t base = (int64_t)(pg < 0 ? 0 : pg) * a.ld_page + (j0 & (a.page - 1)) * D;
+      const T *k = cp_k + base, *v = cp_v + base;
+      // visible rows of the chunk, from this lane's first
+      const int lo = cp.span.first - j0 - c_row, hi = pg < 0 ? -1 : cp.span.to - j0 - c_row;
+      const uint32_t dst = ring + cp_stage * (2 * Sh::kChunkBytes) + c_row * (D * 2);
 #pragma unroll
       for (int i = 0; i < 16 / kRowsPerCopy; ++i) {
-        const int row = i * kRowsPerCopy + c_row;
-        const bool ok = pg >= 0 && j0 + row >= cp.span.first && j0 + row < cp.span.to;
-        const uint32_t off = row * (D * 2) + ((c_col ^ (row & 7)) << 4);
+        const int row = i * kRowsPerCopy;
+        const bool ok = row >= lo && row < hi;
+        const uint32_t off = row * (D * 2) + ((c_col ^ ((row + c_row) & 7)) << 4);
         cp_async16(dst + off, k + row * D, ok);
         cp_async16(dst + Sh::kChunkBytes + off, v + row * D, ok);
       }
       if (++cp_unit == cp.units) {
-        next_piece(cp, cp_done);
+        next_piece(cp);
+        if (cp.valid) cp_head();
         cp_unit = 0;
         cp_page_at = -32;
       }
@@ -220,8 +248,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const float to_log2 = 1.4426950408889634f;
   const float qk_scale = a.softcap > 0.0f ? a.scale / a.softcap : a.scale * to_log2;
   const float cap_log2 = a.softcap * to_log2;
-  Piece p = first_piece();
-  long long p_done = p.units, p_at = 0;  // p_at: the piece's first unit within the range
   int stage = 0;
   const int G = a.Hq / a.Hk;
   while (p.valid) {
@@ -354,10 +380,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     __syncthreads();
-    const long long item_first = u0 + p_at - p.unit0, item_end = item_first + p.span.units;  // in units of all items
     const bool whole = p.units == p.span.units;
-    const bool tail = item_first >= u0;  // this CTA holds the item's beginning
-    float *slot = plan.ws + (cta * 2 + (tail ? 1 : 0)) * Sh::kSlot;
+    float *slot = plan.ws + (cta * 2 + (p.unit0 == 0 ? 1 : 0)) * Sh::kSlot;  // an item begins, or goes on, here
     const float *ml = merge + kWarps * Sh::kHeads * Sh::kRow;
     for (int e = tid; e < heads * D; e += kThreads) {
       const int head = e / D, d = e % D;
@@ -381,25 +405,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (!whole) {
-      // the CTAs of this item: c holds unit u where c * total / grid <= u
-      const long long c0 = ((item_first + 1) * grid - 1) / total, c1 = (item_end * grid - 1) / total;
-      __threadfence();
+      // the CTAs of this item: c holds position x where c * total / grid <= x
+      const long long f = p.at + IC, e0 = f + (long long)UC * (p.span.units - 1);
+      const long long c0 = ((f + 1) * grid - 1) / total, c1 = ((e0 + 1) * grid - 1) / total;
       __syncthreads();
-      if (tid == 0) s_last = atomicAdd(plan.counters + c0, 1) == (int)(c1 - c0);
+      if (tid == 0) {
+        __threadfence();  // (the barrier orders the other threads' pieces before it)
+        s_last = atomicAdd(plan.counters + c0, 1) == (int)(c1 - c0);
+        __threadfence();
+      }
       __syncthreads();
       if (s_last) {
         if (tid == 0) plan.counters[c0] = 0;  // ready for the next call
-        __threadfence();
         for (int e = tid; e < heads * D; e += kThreads) {
           const int head = e / D, d = e % D;
           float top = -INFINITY, sum = 0.0f, acc = 0.0f;
+#pragma unroll 4
           for (long long c = c0; c <= c1; ++c) {
             const float *s = plan.ws + (c * 2 + (c == c0 ? 1 : 0)) * Sh::kSlot;
-            const float mc = __ldcg(s + Sh::kHeads * D + head);
+            const float mc = __ldcg(s + Sh::kHeads * D + head), lc = __ldcg(s + Sh::kHeads * (D + 1) + head);
+            const float oc = __ldcg(s + head * D + d);
             const float tn = fmaxf(top, mc), mm = tn == -INFINITY ? 0.0f : tn;
             const float f0 = exp2f(top - mm), f1 = exp2f(mc - mm);
-            sum = sum * f0 + f1 * __ldcg(s + Sh::kHeads * (D + 1) + head);
-            acc = acc * f0 + f1 * __ldcg(s + head * D + d);
+            sum = sum * f0 + f1 * lc;
+            acc = acc * f0 + f1 * oc;
             top = tn;
           }
           const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
@@ -408,10 +437,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncthreads();  // the merge rows are free again
-    p_at += p.units;
-    next_piece(p, p_done);
+    next_piece(p);
   }
   cp_async_wait<0>();
+
+  // Sequences with nothing visible: zeros.
+  for (int64_t b = cta; b < a.B; b += gridDim.x)
+    if (span_of(a, b).units == 0)
+      for (int i = tid; i < a.N * a.Hq * D; i += kThreads)
+        static_cast<T *>(a.o[i / (a.Hq * D)])[b * a.ldo + i % (a.Hq * D)] = static_cast<T>(0.0f);
 }
 
 template <typename T, int D, int NT>

@@ -10,6 +10,12 @@ bool aligned(const void *p, int a) { return ((uintptr_t)p % (uintptr_t)a) == 0; 
 bool is16(int dt) { return dt == TP_BF16 || dt == TP_F16; }
 int elem_size(int dt) { return dt == TP_F32 ? 4 : 2; }
 
+int log2_of(int power) {
+  int n = 0;
+  while (1 << n < power) ++n;
+  return n;
+}
+
 // The checks that the cache of every entry point shares.
 int check_cache(int N, int Hq, int Hk, int D, int64_t pages, int page, int64_t ld_page, tp_dtype dt,
                 void *const *k_cache, void *const *v_cache) {
@@ -73,7 +79,7 @@ int attn_args(AttnArgs &a, int N, const void *const *q, int64_t T, int64_t ldq, 
   a.T = T, a.B = B, a.ldq = ldq, a.ldo = ldo, a.pages = pages, a.ld_page = ld_page;
   a.ld_table = ld_table, a.width = width;
   a.N = N, a.Hq = Hq, a.Hk = Hk, a.D = D, a.page = page;
-  for (a.page_log2 = 4; 1 << a.page_log2 < page;) ++a.page_log2;
+  a.page_log2 = log2_of(page);
   a.dt = dt, a.window = window, a.scale = scale, a.softcap = softcap;
   return TP_OK;
 }
@@ -113,7 +119,7 @@ int tp_qkv_append(int N, const void *const *qkv, int64_t T, int64_t ld, tp_dtype
     a.qkv[r] = qkv[r], a.q[r] = q[r], a.k_cache[r] = k_cache[r], a.v_cache[r] = v_cache[r];
   a.q_norm = q_norm, a.k_norm = k_norm, a.rope = rope, a.positions = positions, a.slots = slots;
   a.T = T, a.ld = ld, a.ldq = ldq, a.pages = pages, a.ld_page = ld_page, a.rope_rows = rope_rows;
-  a.N = N, a.Hq = Hq, a.Hk = Hk, a.D = D, a.page = page, a.rot = rope ? rope_dim : 0, a.interleaved = interleaved != 0;
+  a.N = N, a.Hq = Hq, a.Hk = Hk, a.D = D, a.page = page, a.page_log2 = log2_of(page), a.rot = rope ? rope_dim : 0, a.interleaved = interleaved != 0;
   a.in_dt = in_dt, a.dt = dt, a.eps = eps;
   if (int rc = need_status(&a.status)) return rc;
   return launch_append(a, (cudaStream_t)stream);
