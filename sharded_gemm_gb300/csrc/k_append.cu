@@ -7,80 +7,56 @@
 // in float32, rounded once to the cache's type.  Queries go to q[r][t], keys and
 // values to page slot / page, row slot % page.
 //
-// D/8 lanes hold one head, eight values (16 bytes of a 16-bit type) each, so the
-// mean is a few shuffles and the rotation's partner (rot/2 values away) sits in
-// another lane of the group at the same place.  A group takes HPG heads of one
-// token: their loads are issued together, and the token's cosines and sines are
-// read once for all of them.  Bytes bound it: each value is read and written once.
+// D/8 lanes hold one head, each two quarters of 4 values: a lane below rot/8
+// values 4l.. and rot/2 + 4l.. (with neighbouring pairs 8l.. and 8l + 4..), so
+// that a pair never leaves its lane and every lane of the rotation needs the
+// cosines and sines 4l..; the lanes behind the rotation hold 8l.. and 8l + 4...
+// Only the mean is summed over lanes.
+//
+// Bytes bound it: each value is read and written once.  Two forms:
+//   append_kernel       a group of lanes takes one head of one token: as many
+//                       groups as there are heads, for small calls and rows that
+//                       8-byte copies cannot take;
+//   append_ring_kernel  a group takes four heads of a token after the other, the
+//                       next token's heads, cosines and sines on their way into
+//                       shared memory meanwhile (each lane copies its own
+//                       pieces, so nothing is shared and no barrier is needed).
 #include "attn.cuh"
+#include "mma16.cuh"
 #include "ptx.cuh"
 
 namespace tp {
 namespace {
 
+// Four consecutive values, one access where vec.
 template <typename T>
-__device__ __forceinline__ void load8(const T *p, bool vec, float (&x)[8]);
-
-template <>
-__device__ __forceinline__ void load8<float>(const float *p, bool vec, float (&x)[8]) {
-  if (vec) {
-    const float4 a = __ldcs(reinterpret_cast<const float4 *>(p)), b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = p[i];
-  }
-}
-
-template <typename T>
-__device__ __forceinline__ void load8_16(const T *p, bool vec, float (&x)[8]) {
-  if (vec) {
-    const uint4 a = __ldcs(reinterpret_cast<const uint4 *>(p));
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = Half2<T>::unpack(w[i]);
-      x[2 * i] = f.x, x[2 * i + 1] = f.y;
+__device__ __forceinline__ void load4(const T *p, bool vec, float *x) {
+  if constexpr (sizeof(T) == 4) {
+    if (vec) {
+      const float4 v = __ldcs(reinterpret_cast<const float4 *>(p));
+      x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+      return;
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = static_cast<float>(p[i]);
+  } else if (vec) {
+    const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(p));
+    const float2 lo = Half2<T>::unpack(v.x), hi = Half2<T>::unpack(v.y);
+    x[0] = lo.x, x[1] = lo.y, x[2] = hi.x, x[3] = hi.y;
+    return;
   }
-}
-template <>
-__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16 *p, bool vec, float (&x)[8]) {
-  load8_16(p, vec, x);
-}
-template <>
-__device__ __forceinline__ void load8<__half>(const __half *p, bool vec, float (&x)[8]) {
-  load8_16(p, vec, x);
-}
-
-template <typename T>
-__device__ __forceinline__ void store8(T *p, bool vec, const float (&x)[8]) {
-  uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = Half2<T>::pack(x[2 * i], x[2 * i + 1]);
+  for (int i = 0; i < 4; ++i) x[i] = static_cast<float>(p[i]);
+}
+template <typename T>
+__device__ __forceinline__ void store4(T *p, bool vec, const float *x) {
+  const uint2 v = make_uint2(Half2<T>::pack(x[0], x[1]), Half2<T>::pack(x[2], x[3]));
   if (vec) {
-    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint2 *>(p) = v;
   } else {
     uint16_t *h = reinterpret_cast<uint16_t *>(p);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) h[2 * i] = (uint16_t)w[i], h[2 * i + 1] = (uint16_t)(w[i] >> 16);
+    h[0] = (uint16_t)v.x, h[1] = (uint16_t)(v.x >> 16), h[2] = (uint16_t)v.y, h[3] = (uint16_t)(v.y >> 16);
   }
 }
-
-// 8 consecutive floats of a table, 16-byte aligned where vec.
-__device__ __forceinline__ void table8(const float *p, bool vec, float (&x)[8]) {
-  if (vec) {
-    const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = __ldg(p + i);
-  }
-}
-__device__ __forceinline__ void table4(const float *p, bool vec, float (&x)[4]) {
+__device__ __forceinline__ void table4(const float *p, bool vec, float *x) {
   if (vec) {
     const float4 a = __ldg(reinterpret_cast<const float4 *>(p));
     x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
@@ -93,139 +69,252 @@ __device__ __forceinline__ void table4(const float *p, bool vec, float (&x)[4]) 
 constexpr int kThreads = 256;
 
 struct Aligned {
-  bool in, q, rope, gain;  // 16-byte accesses possible
+  bool in, q, rope, gain;  // one access for four values possible
 };
 
-// Block (x, y, z): x tokens, y a stretch of HPG heads, z a rank.
-template <typename TIn, typename T, int D, int HPG>
+// A lane's place: where its two quarters of a head begin.
+struct Lane {
+  int id, o0, o1;
+  bool turns;     // they are pairs to rotate
+  uint32_t mask;  // the lanes of its group: groups of one warp may take different branches
+};
+template <int D>
+__device__ __forceinline__ Lane lane_of(const AppendArgs &a) {
+  constexpr int L = D / 8;
+  Lane l;
+  l.id = threadIdx.x % L;
+  l.mask = ((1u << L) - 1) << (threadIdx.x % 32 - l.id);
+  l.turns = l.id < a.rot / 8;
+  const bool halves = l.turns && !a.interleaved;
+  l.o0 = halves ? 4 * l.id : 8 * l.id;
+  l.o1 = halves ? a.rot / 2 + 4 * l.id : 8 * l.id + 4;
+  return l;
+}
+
+struct Slot {
+  int64_t page;
+  int row;  // -1: not written
+};
+__device__ __forceinline__ Slot slot_of(const AppendArgs &a, int64_t slot, const Lane &l) {
+  if (slot >= a.pages << a.page_log2) {
+    if (l.id == 0) record_bad_value(a.status);
+    slot = -1;
+  }
+  return Slot{slot >> a.page_log2, slot < 0 ? -1 : (int)slot & (a.page - 1)};
+}
+// The lane's cosines at position pos; its sines are rot/2 behind.
+__device__ __forceinline__ const float *factors_of(const AppendArgs &a, int64_t pos, const Lane &l) {
+  if (pos < 0 || pos >= a.rope_rows) {
+    if (l.id == 0) record_bad_value(a.status);
+    pos = 0;
+  }
+  return a.rope + pos * a.rot + 4 * l.id;
+}
+
+// Norm, rotation and store of heads h0 .. h0 + NH - 1 of token t, step by step
+// for all of them: one head's steps wait for each other.
+template <typename T, int D, int NH>
+__device__ __forceinline__ void put_heads(const AppendArgs &a, const Aligned &vec, const Lane &l, int r, int64_t t, int h0,
+                                          const Slot &slot, const float (&c)[4], const float (&s)[4],
+                                          float (&y)[NH][8]) {
+  const int H = a.Hq + 2 * a.Hk, turned = a.Hq + a.Hk;
+  if (h0 < turned && (a.q_norm || a.k_norm)) {
+    float sum[NH];
+#pragma unroll
+    for (int i = 0; i < NH; ++i) {
+      sum[i] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum[i] = fmaf(y[i][j], y[i][j], sum[i]);
+    }
+#pragma unroll
+    for (int m = D / 16; m > 0; m /= 2)
+#pragma unroll
+      for (int i = 0; i < NH; ++i) sum[i] += __shfl_xor_sync(l.mask, sum[i], m);
+#pragma unroll
+    for (int i = 0; i < NH; ++i) {
+      const float *gains = h0 + i < a.Hq ? a.q_norm : h0 + i < turned ? a.k_norm : nullptr;
+      if (gains) {
+        float g[8];
+        table4(gains + l.o0, vec.gain, g);
+        table4(gains + l.o1, vec.gain, g + 4);
+        const float inv = rsqrtf(sum[i] * (1.0f / D) + a.eps);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[i][j] *= inv * g[j];
+      }
+    }
+  }
+  if (l.turns) {
+#pragma unroll
+    for (int i = 0; i < NH; ++i) {
+      if (h0 + i >= turned) continue;
+      float (&v)[8] = y[i];
+      if (a.interleaved) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float p = v[2 * j], q = v[2 * j + 1];
+          v[2 * j] = p * c[j] - q * s[j], v[2 * j + 1] = q * c[j] + p * s[j];
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float p = v[j], q = v[j + 4];
+          v[j] = p * c[j] - q * s[j], v[j + 4] = q * c[j] + p * s[j];
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NH; ++i) {
+    const int h = h0 + i;
+    if (h >= H) break;
+    if (h < a.Hq) {
+      T *q = static_cast<T *>(a.q[r]) + t * a.ldq + (int64_t)h * D;
+      store4<T>(q + l.o0, vec.q, y[i]);
+      store4<T>(q + l.o1, vec.q, y[i] + 4);
+    } else if (slot.row >= 0) {
+      const int kh = h < turned ? h - a.Hq : h - turned;
+      T *row = static_cast<T *>(h < turned ? a.k_cache[r] : a.v_cache[r]) + slot.page * a.ld_page +
+               ((int64_t)kh * a.page + slot.row) * D;
+      store4<T>(row + l.o0, true, y[i]);
+      store4<T>(row + l.o1, true, y[i] + 4);
+    }
+  }
+}
+
+// Block (x, y, z): x tokens, y a head, z a rank.
+template <typename TIn, typename T, int D>
 __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendArgs a, const Aligned vec) {
   constexpr int L = D / 8;  // lanes of a head
   griddep_launch_dependents();
   griddep_wait();
-  const int lane = threadIdx.x % L;
-  // the lanes of this thread's group: groups of one warp may take different branches
-  const uint32_t mask = ((1u << L) - 1) << (threadIdx.x % 32 - lane);
+  const Lane l = lane_of<D>(a);
   const int64_t t = (int64_t)blockIdx.x * (kThreads / L) + threadIdx.x / L;
   if (t >= a.T) return;
-  const int r = blockIdx.z, H = a.Hq + 2 * a.Hk, h0 = blockIdx.y * HPG, i0 = lane * 8;
-  const TIn *src = static_cast<const TIn *>(a.qkv[r]) + t * a.ld + i0;
-
-  float x[HPG][8];
-#pragma unroll
-  for (int i = 0; i < HPG; ++i)
-    if (h0 + i < H) load8<TIn>(src + (int64_t)(h0 + i) * D, vec.in, x[i]);
-
-  int64_t slot = -1;
-  if (h0 + HPG > a.Hq) {
-    slot = __ldg(a.slots + t);
-    if (slot >= a.pages << a.page_log2) {
-      slot = -1;
-      if (lane == 0) record_bad_value(a.status);
-    }
+  const int r = blockIdx.z, h = blockIdx.y;
+  float x[1][8], c[4], s[4];
+  const TIn *src = static_cast<const TIn *>(a.qkv[r]) + t * a.ld + (int64_t)h * D;
+  load4<TIn>(src + l.o0, vec.in, x[0]);
+  load4<TIn>(src + l.o1, vec.in, x[0] + 4);
+  Slot slot{0, -1};
+  if (h >= a.Hq) slot = slot_of(a, __ldg(a.slots + t), l);
+  if (l.turns && h < a.Hq + a.Hk) {
+    const float *f = factors_of(a, __ldg(a.positions + t), l);
+    table4(f, vec.rope, c);
+    table4(f + a.rot / 2, vec.rope, s);
   }
-  const int64_t pg = slot >> a.page_log2;
-  const int off = (int)slot & (a.page - 1);
+  put_heads<T, D, 1>(a, vec, l, r, t, h, slot, c, s, x);
+}
 
-  // Rotation: this lane's factors.  Halves: value i < rot/2 pairs with
-  // i + rot/2, factor i.  Neighbours: values 2i, 2i + 1, factor i.
-  const int half = a.rot / 2;
-  const bool turns = i0 < a.rot;
-  float c[8], s[8];
-  if (turns && h0 < a.Hq + a.Hk) {
-    int64_t pos = __ldg(a.positions + t);
-    if (pos < 0 || pos >= a.rope_rows) {
-      pos = 0;
-      if (lane == 0) record_bad_value(a.status);
-    }
-    const float *row = a.rope + pos * a.rot;
-    if (a.interleaved) {
-      float c4[4], s4[4];
-      table4(row + i0 / 2, vec.rope, c4);
-      table4(row + half + i0 / 2, vec.rope, s4);
+template <typename TIn>
+struct Ring {
+  static constexpr int kHeads = 4, kStages = 2;
+  static constexpr int kQuarter = 4 * sizeof(TIn);  // bytes
+  static constexpr int kRope = kStages * kHeads * 2 * kQuarter * kThreads;  // where cosines and sines begin
+  static constexpr int kSmem = kRope + kStages * 32 * kThreads;
+};
+
+// Block (x, y, z): token blocks x, x + gridDim.x, ..; y a stretch of four heads, z a rank.
+template <typename TIn, typename T, int D>
+__global__ void __launch_bounds__(kThreads, 3)
+    append_ring_kernel(const __grid_constant__ AppendArgs a, const Aligned vec) {
+  using R = Ring<TIn>;
+  constexpr int L = D / 8, kTokens = kThreads / L, NH = R::kHeads;
+  extern __shared__ __align__(16) uint8_t smem[];
+  griddep_launch_dependents();
+  griddep_wait();
+  const Lane l = lane_of<D>(a);
+  const int r = blockIdx.z, H = a.Hq + 2 * a.Hk, h0 = blockIdx.y * NH;
+  const int64_t first = (int64_t)blockIdx.x * kTokens + threadIdx.x / L, step = (int64_t)gridDim.x * kTokens;
+  const TIn *src = static_cast<const TIn *>(a.qkv[r]) + (int64_t)h0 * D;
+  const bool turns = l.turns && h0 < a.Hq + a.Hk, keeps = h0 + NH > a.Hq;
+  // a piece of one lane lies beside its neighbours': piece 2i, 2i + 1 head i's quarters
+  auto at = [&](int stage, int piece) { return ((stage * NH * 2 + piece) * kThreads + (int)threadIdx.x) * R::kQuarter; };
+  auto rope_at = [&](int stage, int piece) { return R::kRope + ((stage * 2 + piece) * kThreads + (int)threadIdx.x) * 16; };
+  const uint32_t base = smem_u32(smem);
+
+  int64_t ahead = first;  // the token to copy next
+  int next_pos = turns && ahead < a.T ? __ldg(a.positions + ahead) : 0;
+  auto copy = [&](int stage) {
+    if (ahead < a.T) {
+      const TIn *row = src + ahead * a.ld;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        c[2 * i] = c[2 * i + 1] = c4[i];
-        s[2 * i] = -s4[i], s[2 * i + 1] = s4[i];
+      for (int i = 0; i < NH; ++i)
+        if (h0 + i < H) {
+          cp_async<R::kQuarter>(base + at(stage, 2 * i), row + i * D + l.o0);
+          cp_async<R::kQuarter>(base + at(stage, 2 * i + 1), row + i * D + l.o1);
+        }
+      if (turns) {
+        const float *f = factors_of(a, next_pos, l);
+        cp_async<16>(base + rope_at(stage, 0), f);
+        cp_async<16>(base + rope_at(stage, 1), f + a.rot / 2);
       }
+      ahead += step;
+      if (turns && ahead < a.T) next_pos = __ldg(a.positions + ahead);
+    }
+    cp_async_commit();
+  };
+  auto read4 = [&](int at, float *x) {
+    if constexpr (sizeof(TIn) == 4) {
+      const float4 v = *reinterpret_cast<const float4 *>(smem + at);
+      x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
     } else {
-      const int f0 = i0 < half ? i0 : i0 - half;
-      table8(row + f0, vec.rope, c);
-      table8(row + half + f0, vec.rope, s);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s[i] = i0 < half ? -s[i] : s[i];
+      const uint2 v = *reinterpret_cast<const uint2 *>(smem + at);
+      const float2 lo = Half2<TIn>::unpack(v.x), hi = Half2<TIn>::unpack(v.y);
+      x[0] = lo.x, x[1] = lo.y, x[2] = hi.x, x[3] = hi.y;
     }
+  };
+  copy(0);
+  int stage = 0;
+  for (int64_t t = first; t < a.T; t += step) {
+    const int64_t at_slot = keeps ? __ldg(a.slots + t) : -1;
+    copy(stage ^ 1);
+    cp_async_wait<1>();
+    float c[4], s[4], y[NH][8];
+    if (turns) {
+      const float4 fc = *reinterpret_cast<const float4 *>(smem + rope_at(stage, 0));
+      const float4 fs = *reinterpret_cast<const float4 *>(smem + rope_at(stage, 1));
+      c[0] = fc.x, c[1] = fc.y, c[2] = fc.z, c[3] = fc.w;
+      s[0] = fs.x, s[1] = fs.y, s[2] = fs.z, s[3] = fs.w;
+    }
+#pragma unroll
+    for (int i = 0; i < NH; ++i) read4(at(stage, 2 * i), y[i]), read4(at(stage, 2 * i + 1), y[i] + 4);
+    Slot slot{0, -1};
+    if (keeps) slot = slot_of(a, at_slot, l);
+    put_heads<T, D, NH>(a, vec, l, r, t, h0, slot, c, s, y);
+    stage ^= 1;
   }
-
-  float gain[8];
-  const float *gain_of = nullptr;  // whose gains are held
-#pragma unroll
-  for (int i = 0; i < HPG; ++i) {
-    const int h = h0 + i;
-    if (h >= H) break;
-    float (&y)[8] = x[i];
-    if (h < a.Hq + a.Hk) {
-      const float *want = h < a.Hq ? a.q_norm : a.k_norm;
-      if (want) {
-        if (want != gain_of) table8(want + i0, vec.gain, gain);
-        gain_of = want;
-        float sum = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sum = fmaf(y[j], y[j], sum);
-#pragma unroll
-        for (int m = L / 2; m > 0; m /= 2) sum += __shfl_xor_sync(mask, sum, m);
-        const float inv = rsqrtf(sum * (1.0f / D) + a.eps);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] *= inv * gain[j];
-      }
-      if (a.rot) {
-        float p[8];
-        if (a.interleaved) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) p[j] = y[j ^ 1];
-        } else {
-          const int step = half / 8;  // the partner's distance in lanes
-          const int from = (lane < step ? lane + step : lane - step) & (L - 1);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) p[j] = __shfl_sync(mask, y[j], from, L);
-        }
-        if (turns) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) y[j] = fmaf(p[j], s[j], y[j] * c[j]);
-        }
-      }
-      if (h < a.Hq) {
-        store8<T>(static_cast<T *>(a.q[r]) + t * a.ldq + (int64_t)h * D + i0, vec.q, y);
-        continue;
-      }
-    }
-    if (slot >= 0) {
-      const bool is_k = h < a.Hq + a.Hk;
-      const int kh = h - a.Hq - (is_k ? 0 : a.Hk);
-      T *page = static_cast<T *>(is_k ? a.k_cache[r] : a.v_cache[r]) + pg * a.ld_page;
-      store8<T>(page + ((int64_t)kh * a.page + off) * D + i0, true, y);
-    }
-  }
+  cp_async_wait<0>();
 }
 
 template <typename TIn, typename T, int D>
 int launch(const AppendArgs &a, cudaStream_t s) {
   const int H = a.Hq + 2 * a.Hk;
-  auto aligned = [](const void *p) { return (uintptr_t)p % 16 == 0; };
+  constexpr int kTokens = kThreads / (D / 8);
+  auto aligned = [](const void *p, int bytes) { return (uintptr_t)p % bytes == 0; };
+  constexpr int in_bytes = 4 * sizeof(TIn);
   Aligned vec;
-  vec.in = (a.ld * (int64_t)sizeof(TIn)) % 16 == 0, vec.q = (a.ldq * 2) % 16 == 0;
+  vec.in = (a.ld * (int64_t)sizeof(TIn)) % in_bytes == 0, vec.q = (a.ldq * 2) % 8 == 0;
   for (int r = 0; r < a.N; ++r) {
-    vec.in = vec.in && aligned(a.qkv[r]);
-    vec.q = vec.q && aligned(a.q[r]);
+    vec.in = vec.in && aligned(a.qkv[r], in_bytes);
+    vec.q = vec.q && aligned(a.q[r], 8);
   }
-  vec.rope = aligned(a.rope), vec.gain = aligned(a.q_norm) && aligned(a.k_norm);
-  const bool wide = a.T * a.N * H >= 8192;  // fewer: one head a group, for more groups
-  const int hpg = wide ? 4 : 1;
-  const int64_t blocks = (a.T + kThreads / (D / 8) - 1) / (kThreads / (D / 8)), stretches = (H + hpg - 1) / hpg;
-  if (blocks > 0x7fffffff || stretches > 65535)
-    return set_error(TP_ERR_UNSUPPORTED, "too many tokens or heads for one launch");
-  const dim3 grid((unsigned)blocks, (unsigned)stretches, (unsigned)a.N), block(kThreads);
-  const cudaError_t e = wide ? launch_pdl(append_kernel<TIn, T, D, 4>, grid, block, 0, s, a, vec)
-                             : launch_pdl(append_kernel<TIn, T, D, 1>, grid, block, 0, s, a, vec);
+  vec.rope = aligned(a.rope, 16), vec.gain = aligned(a.q_norm, 16) && aligned(a.k_norm, 16);
+  const int64_t blocks = (a.T + kTokens - 1) / kTokens;
+  if (blocks > 0x7fffffff || H > 65535) return set_error(TP_ERR_UNSUPPORTED, "too many tokens or heads for one launch");
+  cudaError_t e;
+  using R = Ring<TIn>;
+  const int stretches = (H + R::kHeads - 1) / R::kHeads;
+  const int64_t resident = (3 * sm_count() + stretches * a.N - 1) / (stretches * a.N);  // token blocks at a time
+  if (vec.in && vec.rope && blocks >= 2 * resident) {
+    auto kern = append_ring_kernel<TIn, T, D>;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, R::kSmem);
+    if (e == cudaSuccess)
+      e = launch_pdl(kern, dim3((unsigned)resident, (unsigned)stretches, (unsigned)a.N), dim3(kThreads), R::kSmem, s, a,
+                     vec);
+  } else {
+    e = launch_pdl(append_kernel<TIn, T, D>, dim3((unsigned)blocks, (unsigned)H, (unsigned)a.N), dim3(kThreads), 0, s, a,
+                   vec);
+  }
   if (e != cudaSuccess) return cuda_error(e, "append launch");
   note_launch();
   return TP_OK;
