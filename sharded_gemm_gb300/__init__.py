@@ -3,7 +3,8 @@
 Argument marshalling only: every function here checks that the tensors it
 is given can be described to the C ABI (device, dtype, row-major strides),
 passes their device pointers and sizes, and enqueues the call on the current
-torch CUDA stream.  All arithmetic runs in the library's CUDA kernels.  There
+torch CUDA stream (through ctypes; the attention-side functions through a small
+extension module, _marshal.so).  All arithmetic runs in the library's CUDA kernels.  There
 is no fallback: if libtp.so is missing or fails to load, every call raises.
 
 Function names are the C names.  Tensors are torch CUDA tensors; bf16 / f16 /
@@ -20,6 +21,7 @@ import threading
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libtp.so")
+MARSHAL_PATH = os.path.join(HERE, "_marshal.so")
 HEADER = os.path.join(os.path.dirname(HERE), "include", "tp_api.h")
 
 TP_OK, TP_ERR_INVALID_ARG, TP_ERR_NOT_DIVISIBLE, TP_ERR_ALIGNMENT = 0, -1, -2, -3
@@ -106,12 +108,12 @@ def _load() -> ctypes.CDLL:
             "tp_q4_quantize": ([vp, i64, i64, i32, vp, vp, vp, vp], i32),
             "tp_q4_all_to_sharded": ([i32, vp, i64, i64, vpp, vpp, vpp, i32, i64, vpp, vpp, i64, i32, vp], i32),
             "tp_q4_sharded_to_all": ([i32, vpp, i64, i64, vpp, vpp, vpp, i32, i64, vp, vp, i64, i32, vp], i32),
-            "tp_qkv_append": ([i32, vpp, i64, i64, i32, i32, i32, i32, vp, vp, f32, vp, i64, i32, i32, vp, vp, vpp,
-                               i64, vpp, vpp, i64, i32, i64, i32, vp], i32),
-            "tp_paged_decode": ([i32, vpp, i64, i64, i32, i32, i32, vpp, vpp, i64, i32, i64, vp, i64, i64, vp, f32,
-                                 f32, i32, i32, vpp, i64, vp], i32),
-            "tp_paged_prefill": ([i32, vpp, i64, i64, i32, i32, i32, vpp, vpp, i64, i32, i64, vp, i64, i64, i64, vp,
-                                  vp, vp, f32, f32, i32, i32, vpp, i64, vp], i32),
+            "tp_qkv_append": ([i32, vp, i64, i64, i32, i32, i32, i32, vp, vp, f32, vp, i64, i32, i32, vp, vp, vp,
+                               i64, vp, vp, i64, i32, i64, i32, vp], i32),
+            "tp_paged_decode": ([i32, vp, i64, i64, i32, i32, i32, vp, vp, i64, i32, i64, vp, i64, i64, vp, f32,
+                                 f32, i32, i32, vp, i64, vp], i32),
+            "tp_paged_prefill": ([i32, vp, i64, i64, i32, i32, i32, vp, vp, i64, i32, i64, vp, i64, i64, i64, vp,
+                                  vp, vp, f32, f32, i32, i32, vp, i64, vp], i32),
             "tp_sample": ([vp, i64, i64, i64, i32, vp, vp, vp, vp, vp, vp, vp, vp], i32),
             "tp_debug_wait_timeout": ([i64, vp], i32),
             "tp_debug_prep_alone": ([i32], i32),
@@ -774,100 +776,39 @@ def tp_mx_sharded_to_all(x, codes, scales, bias=None, out=None, out_dtype=None, 
 
 # ------------------------------------------------------------------ attention side
 # A per-rank argument is a list of N tensors, or one tensor whose first
-# dimension is the ranks (rank r is its slice [r]).  A decode step calls these
-# once a layer on kernels of a few microseconds, so the marshalling reads each
-# tensor attribute once and builds no intermediate objects.
-_array_types = {}
-_dtypes = {}
+# dimension is the ranks (rank r is its slice [r]).  The tensors are checked and
+# turned into the C ABI's arguments by csrc/marshal.c (see there why not here).
+_native = None  # the extension module, once loaded
 
 
-def _pointer_array(n):
-    t = _array_types.get(n)
-    if t is None:
-        t = _array_types[n] = ctypes.c_void_p * n
-    return t
-
-
-def _dtype_code(dtype):
-    if not _dtypes:
+def _marshaller():
+    global _native
+    if _native is None:
+        if not os.path.exists(MARSHAL_PATH):
+            raise RuntimeError("_marshal.so is not built (%s); run `python -m sharded_gemm_gb300.build`" % MARSHAL_PATH)
+        from . import _marshal as m
         torch = _torch()
-        _dtypes.update({torch.float32: TP_F32, torch.bfloat16: TP_BF16, torch.float16: TP_F16})
-    code = _dtypes.get(dtype)
-    if code is None:
-        raise TypeError("unsupported dtype %s" % dtype)
-    return code
+        m.init(torch.float32, torch.bfloat16, torch.float16, torch.int32, torch.int64,
+               getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream))
+        _native = m
+    return _native
 
 
-def _current_stream(stream, dev):
-    """_stream, with the current stream of device `dev` looked up without building a Stream object."""
-    if stream is None:
-        return _torch()._C._cuda_getCurrentRawStream(dev)
-    return stream if isinstance(stream, int) else stream.cuda_stream
+_addresses = {}
 
 
-def _ranks(x, name, dim):
-    """(pointer array, N, shape, strides, index of the rank's first dimension in them, dtype, device index)."""
-    if isinstance(x, (list, tuple)):
-        t = x[0]
-        shape, stride, dtype, dev, first, n = t.shape, t.stride(), t.dtype, t.get_device(), 0, len(x)
-        for o in x:
-            if o.shape != shape or o.stride() != stride or o.dtype != dtype or o.get_device() != dev:
-                raise ValueError("%s: all ranks need one shape, stride, dtype and device" % name)
-        arr = _pointer_array(n)(*[o.data_ptr() for o in x])
-    else:
-        shape, stride, dtype, dev, first = x.shape, x.stride(), x.dtype, x.get_device(), 1
-        n = shape[0] if shape else 0
-        base = x.data_ptr()
-        if n == 1:
-            arr = _pointer_array(1)(base)
-        else:
-            step = stride[0] * x.element_size() if shape else 0
-            arr = _pointer_array(n)(*[base + i * step for i in range(n)])
-    if dev < 0:
-        raise ValueError("%s must be a CUDA tensor" % name)
-    if len(shape) != dim + first:
-        raise ValueError("%s: each rank's tensor must be %d-D" % (name, dim))
-    return arr, n, shape, stride, first, dtype, dev
-
-
-def _ld(shape, stride, first, name):
-    """Row stride of a per-rank matrix."""
-    if stride[first + 1] != 1 and shape[first + 1] > 1:
-        raise ValueError("%s must have unit column stride" % name)
-    return stride[first] if shape[first] > 1 else shape[first + 1]
-
-
-def _param(t, name, dtype, n, dev):
-    """Device pointer of a contiguous 1-D parameter array (None stays None)."""
-    if t is None:
-        return None
-    if t.dtype != dtype:
-        raise TypeError("%s must be %s" % (name, dtype))
-    if t.get_device() != dev:
-        raise ValueError("%s must be on device %d" % (name, dev))
-    if t.shape != (n,) or not t.is_contiguous():
-        raise ValueError("%s must be contiguous with %d elements" % (name, n))
-    return t.data_ptr()
-
-
-def _paged_cache(k_cache, v_cache):
-    """(k pointers, v pointers, N, pages, Hk, page, D, page stride, dtype, device index)."""
-    kp, n, shape, stride, first, dtype, dev = _ranks(k_cache, "k_cache", 4)
-    vp, nv, vshape, vstride, vfirst, vdtype, vdev = _ranks(v_cache, "v_cache", 4)
-    if n != nv or shape[first:] != vshape[vfirst:] or stride[first:] != vstride[vfirst:] or dtype != vdtype \
-            or dev != vdev:
-        raise ValueError("k_cache and v_cache need the same ranks, shape, strides, dtype and device")
-    P, Hk, page, D = shape[first:]
-    ld, ld_head, ld_row, unit = stride[first:]
-    if unit != 1 or ld_row != D or (ld_head != page * D and Hk > 1):
-        raise ValueError("the heads, rows and values of a cache page must be contiguous")
-    return kp, vp, n, P, Hk, page, D, (ld if P > 1 else Hk * page * D), dtype, dev
-
-
-def _heads(cols, D, name):
-    if D < 1 or cols % D:
-        raise ValueError("%s: %d columns are not whole heads of %d" % (name, cols, D))
-    return cols // D
+def _call(name, marshal, *args):
+    """Marshals `args` and calls the library's function `name` (or has prepare() record the call)."""
+    rec = getattr(_rec, "active", None)
+    if rec is not None:
+        _check(getattr(rec, name)(*marshal(0, *args)))
+        return
+    fn = _addresses.get(name)
+    if fn is None:
+        fn = _addresses[name] = ctypes.cast(getattr(lib(), name), ctypes.c_void_p).value
+    rc = marshal(fn, *args)
+    if rc != TP_OK:
+        _check(rc)
 
 
 def tp_qkv_append(qkv, k_cache, v_cache, slots, positions=None, rope=None, q_norm=None, k_norm=None, eps: float = 1e-6,
@@ -877,61 +818,21 @@ def tp_qkv_append(qkv, k_cache, v_cache, slots, positions=None, rope=None, q_nor
     caches (per rank (pages, Hk, page, D)) at ``slots``; returns the queries,
     per rank (T, Hq D) in the cache's dtype (one (N, T, Hq D) tensor unless
     ``out`` is given)."""
-    torch = _torch()
-    kp, vp, N, P, Hk, page, D, ldp, cdtype, dev = _paged_cache(k_cache, v_cache)
-    xp, n, shape, stride, first, dtype, xdev = _ranks(qkv, "qkv", 2)
-    if n != N or xdev != dev:
-        raise ValueError("qkv and the caches need the same ranks on one device")
-    T = shape[first]
-    Hq = _heads(shape[first + 1], D, "qkv") - 2 * Hk
     if out is None:
-        if Hq < 1:
+        x, k = (t[0] if isinstance(t, (list, tuple)) else t for t in (qkv, k_cache))
+        T, cols = x.shape[-2:]
+        Hk, _, D = k.shape[-3:]
+        if cols <= 2 * Hk * D:
             raise ValueError("qkv holds no query heads besides 2 * %d key and value heads" % Hk)
-        out = torch.empty((N, T, Hq * D), dtype=cdtype, device=k_cache[0].device)
-    op, no, oshape, ostride, ofirst, odtype, odev = _ranks(out, "out", 2)
-    if no != N or oshape[ofirst] != T or oshape[ofirst + 1] != Hq * D or odtype != cdtype or odev != dev:
-        raise ValueError("out must be (T, Hq * D) per rank in the cache's dtype")
-    rp, rows, rot = None, 0, 0
-    if rope is not None:
-        if rope.dtype != torch.float32 or rope.dim() != 2 or not rope.is_contiguous() or rope.get_device() != dev:
-            raise ValueError("rope must be a contiguous float32 (positions, rope_dim) tensor on the caches' device")
-        rp, (rows, rot) = rope.data_ptr(), rope.shape
-        if positions is None:
-            raise ValueError("rope needs positions")
-    _check(lib().tp_qkv_append(
-        N, xp, T, _ld(shape, stride, first, "qkv"), _dtype_code(dtype), Hq, Hk, D,
-        _param(q_norm, "q_norm", torch.float32, D, dev), _param(k_norm, "k_norm", torch.float32, D, dev), eps,
-        rp, rows, rot, 1 if interleaved else 0, _param(positions, "positions", torch.int32, T, dev),
-        _param(slots, "slots", torch.int64, T, dev), op, _ld(oshape, ostride, ofirst, "out"), kp, vp, P, page, ldp,
-        _dtype_code(cdtype), _current_stream(stream, dev)))
+        out = k.new_empty((len(qkv), T, cols - 2 * Hk * D))
+    _call("tp_qkv_append", (_native or _marshaller()).append, qkv, k_cache, v_cache, slots, positions, rope, q_norm,
+          k_norm, eps, interleaved, out, stream)
     return out
 
 
-def _attention(q, k_cache, v_cache, block_table, out):
-    """(out, device index, T, D, the arguments up to block_table, (width, ld_table), (dtype, o, ldo))."""
-    torch = _torch()
-    kp, vp, N, P, Hk, page, D, ldp, cdtype, dev = _paged_cache(k_cache, v_cache)
-    qp, n, shape, stride, first, dtype, qdev = _ranks(q, "q", 2)
-    if n != N or qdev != dev:
-        raise ValueError("q and the caches need the same ranks on one device")
-    if dtype != cdtype:
-        raise TypeError("q must have the caches' dtype")
-    T, cols = shape[first], shape[first + 1]
-    if out is None:
-        out = torch.empty((N, T, cols), dtype=dtype, device=block_table.device)
-    op, no, oshape, ostride, ofirst, odtype, odev = _ranks(out, "out", 2)
-    if no != N or oshape[ofirst] != T or oshape[ofirst + 1] != cols or odtype != dtype or odev != dev:
-        raise ValueError("out must have q's shape per rank and its dtype")
-    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.get_device() != dev:
-        raise ValueError("block_table must be a 2-D int32 tensor on the caches' device")
-    rows, width = block_table.shape
-    ldt, unit = block_table.stride()
-    if unit != 1 and width > 1:
-        raise ValueError("block_table must have unit column stride")
-    return (out, dev, T, D,
-            (N, qp, T, _ld(shape, stride, first, "q"), _heads(cols, D, "q"), Hk, D, kp, vp, P, page, ldp,
-             block_table.data_ptr()), (width, ldt if rows > 1 else width),
-            (_dtype_code(dtype), op, _ld(oshape, ostride, ofirst, "out")))
+def _like(q):
+    """An output for per-rank queries: one tensor, the ranks first."""
+    return q[0].new_empty((len(q),) + tuple(q[0].shape)) if isinstance(q, (list, tuple)) else q.new_empty(q.shape)
 
 
 def tp_paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale=None, softcap: float = 0.0, window: int = 0,
@@ -939,13 +840,10 @@ def tp_paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale=None, soft
     """Attention of one new token per sequence over the paged caches: q per rank
     (B, Hq D), seq_lens (B) counts the new token.  Returns o, per rank
     (B, Hq D) (one (N, B, Hq D) tensor unless ``out`` is given)."""
-    out, dev, B, D, head, table, tail = _attention(q, k_cache, v_cache, block_table, out)
-    if block_table.shape[0] != B:
-        raise ValueError("block_table needs one row per sequence")
-    if scale is None:
-        scale = D ** -0.5
-    _check(lib().tp_paged_decode(*head, *table, _param(seq_lens, "seq_lens", _torch().int32, B, dev), scale, softcap,
-                                 window, *tail, _current_stream(stream, dev)))
+    if out is None:
+        out = _like(q)
+    _call("tp_paged_decode", (_native or _marshaller()).decode, q, k_cache, v_cache, block_table, seq_lens, scale,
+          softcap, window, out, stream)
     return out
 
 
@@ -954,15 +852,10 @@ def tp_paged_prefill(q, k_cache, v_cache, block_table, cu_seqlens, seq_lens, pre
     """Causal attention of ragged chunks over the paged caches: rows
     cu_seqlens[b] .. cu_seqlens[b + 1] - 1 of q are the last positions of
     sequence b.  Returns o as tp_paged_decode."""
-    i32 = _torch().int32
-    out, dev, T, D, head, table, tail = _attention(q, k_cache, v_cache, block_table, out)
-    B = block_table.shape[0]
-    if scale is None:
-        scale = D ** -0.5
-    _check(lib().tp_paged_prefill(*head, B, *table, _param(cu_seqlens, "cu_seqlens", i32, B + 1, dev),
-                                  _param(seq_lens, "seq_lens", i32, B, dev),
-                                  _param(prefix_lens, "prefix_lens", i32, B, dev), scale, softcap, window, *tail,
-                                  _current_stream(stream, dev)))
+    if out is None:
+        out = _like(q)
+    _call("tp_paged_prefill", (_native or _marshaller()).prefill, q, k_cache, v_cache, block_table, cu_seqlens,
+          seq_lens, prefix_lens, scale, softcap, window, out, stream)
     return out
 
 
@@ -971,15 +864,10 @@ def tp_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, t
     """Draws one token per row of ``logits`` (B, V) with the given uniform
     numbers ``u`` (B); returns (tokens int64 (B), logprobs float32 (B))."""
     torch = _torch()
-    _rowmajor(logits, "logits")
-    (B, V), dev, f32 = logits.shape, logits.get_device(), torch.float32
     if tokens is None:
-        tokens = torch.empty((B,), dtype=torch.int64, device=logits.device)
+        tokens = logits.new_empty((logits.shape[0],), dtype=torch.int64)
     if logprobs is None:
-        logprobs = torch.empty((B,), dtype=f32, device=logits.device)
-    _check(lib().tp_sample(logits.data_ptr(), B, V, logits.stride(0) if B > 1 else V, _dtype_code(logits.dtype),
-                           _param(u, "u", f32, B, dev), _param(temperature, "temperature", f32, B, dev),
-                           _param(top_k, "top_k", torch.int32, B, dev), _param(top_p, "top_p", f32, B, dev),
-                           _param(min_p, "min_p", f32, B, dev), _param(tokens, "tokens", torch.int64, B, dev),
-                           _param(logprobs, "logprobs", f32, B, dev), _current_stream(stream, dev)))
+        logprobs = logits.new_empty((logits.shape[0],), dtype=torch.float32)
+    _call("tp_sample", (_native or _marshaller()).sample, logits, u, temperature, top_k, top_p, min_p, tokens, logprobs,
+          stream)
     return tokens, logprobs

@@ -1,5 +1,5 @@
 """Build libtp.so in-tree: one nvcc process per translation unit, in parallel,
-then one link.  sm_103a only.
+then one link (sm_103a only), and the binding's extension module _marshal.so.
 
     python -m sharded_gemm_gb300.build [--force] [--verbose]
 """
@@ -11,12 +11,15 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libtp.so")
+MARSHAL_SRC = os.path.join(CSRC, "marshal.c")
+MARSHAL = os.path.join(HERE, "_marshal.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2",
@@ -46,8 +49,25 @@ def _stale(target: str, deps: list[str]) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def build_marshal(force: bool = False) -> str:
+    """The extension module: C against Python's headers, no CUDA."""
+    if force or _stale(MARSHAL, [MARSHAL_SRC] + headers()):
+        cc = os.environ.get("CC") or shutil.which("gcc") or shutil.which("cc")
+        if not cc:
+            raise RuntimeError("no C compiler found for %s" % MARSHAL_SRC)
+        tmp = MARSHAL + ".tmp%d" % os.getpid()
+        r = subprocess.run([cc, "-O2", "-fPIC", "-shared", "-I" + sysconfig.get_paths()["include"], "-I" + INCLUDE,
+                            MARSHAL_SRC, "-o", tmp], capture_output=True, text=True)
+        if r.returncode != 0:
+            sys.stderr.write(r.stdout + r.stderr)
+            raise RuntimeError("compiling %s failed" % MARSHAL_SRC)
+        os.replace(tmp, MARSHAL)
+    return MARSHAL
+
+
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
     os.makedirs(BUILD, exist_ok=True)
+    build_marshal(force)
     cc = nvcc()
     hdrs = headers()
     flags = NVCC_FLAGS + list(extra or [])

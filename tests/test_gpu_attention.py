@@ -571,3 +571,72 @@ def test_sample_distribution():
     prob = torch.softmax(row.double(), 0).cpu().numpy()
     share = np.bincount(tok.cpu().numpy(), minlength=V) / n
     assert (np.abs(share - prob) <= 5 * np.sqrt(prob * (1 - prob) / n)).all()
+
+
+# ------------------------------------------------------------------ the binding
+def test_binding_refusals():
+    B, N, Hq, Hk, D, page = 2, 2, 4, 2, 64, 16
+    cuda = dict(device="cuda")
+    q = torch.zeros((N, B, Hq * D), dtype=BF, **cuda)
+    kc = torch.zeros((N, 3, Hk, page, D), dtype=BF, **cuda)
+    table = torch.zeros((B, 1), dtype=torch.int32, **cuda)
+    lens = torch.ones(B, dtype=torch.int32, **cuda)
+    ok = dict(q=q, k_cache=kc, v_cache=kc.clone(), block_table=table, seq_lens=lens)
+    tp.tp_paged_decode(**ok)
+    for change, error in [
+            (dict(q=q.cpu()), ValueError), (dict(q=q.half()), TypeError), (dict(q=q[:1]), ValueError),
+            (dict(q=[q[0], q[1].float()]), ValueError), (dict(q=q[..., :70]), ValueError), (dict(q=q[0]), ValueError),
+            (dict(q=q.double()), TypeError), (dict(q=q.transpose(1, 2)), ValueError), (dict(q=[]), (ValueError, IndexError)),
+            (dict(k_cache=kc[:, :2]), ValueError), (dict(k_cache=kc.transpose(2, 3)), ValueError),
+            (dict(k_cache=kc[..., ::2], v_cache=kc[..., ::2]), ValueError), (dict(v_cache=kc.half()), ValueError),
+            (dict(block_table=table.long()), ValueError), (dict(block_table=table[:1]), ValueError),
+            (dict(block_table=table.cpu()), ValueError), (dict(seq_lens=lens.long()), TypeError),
+            (dict(seq_lens=lens[:1]), ValueError), (dict(seq_lens=torch.ones(4, dtype=torch.int32, **cuda)[::2]), ValueError),
+            (dict(out=q[:1]), ValueError), (dict(out=q.half()), ValueError), (dict(scale="x"), TypeError),
+            (dict(scale=-1.0), tp.TPError), (dict(window=-3), tp.TPError), (dict(softcap=-1.0), tp.TPError)]:
+        with pytest.raises(error):
+            tp.tp_paged_decode(**{**ok, **change})
+    slots = torch.zeros(B, dtype=torch.int64, **cuda)
+    x = torch.zeros((N, B, (Hq + 2 * Hk) * D), dtype=BF, **cuda)
+    rope = torch.zeros((4, D), **cuda)
+    for args, error in [
+            (dict(rope=rope), ValueError), (dict(rope=rope.half(), positions=lens), ValueError),
+            (dict(q_norm=torch.ones(D + 1, **cuda)), ValueError), (dict(k_norm=torch.ones(D, dtype=BF, **cuda)), TypeError),
+            (dict(out=q.half()), ValueError), (dict(eps=-1.0), tp.TPError)]:
+        with pytest.raises(error):
+            tp.tp_qkv_append(x, kc, kc.clone(), slots, **args)
+    with pytest.raises(ValueError):
+        tp.tp_qkv_append(x[..., :2 * Hk * D], kc, kc.clone(), slots)
+    logits, u = torch.zeros((2, 8), **cuda), torch.zeros(2, **cuda)
+    for args, error in [
+            (dict(logits=logits.double()), TypeError), (dict(logits=logits[0]), ValueError), (dict(u=u.double()), TypeError),
+            (dict(top_k=u), TypeError), (dict(top_p=u[:1]), ValueError), (dict(logits=logits.T), ValueError)]:
+        with pytest.raises(error):
+            tp.tp_sample(**{**dict(logits=logits, u=u), **args})
+    status_ok()
+
+
+def test_prepared_calls_of_every_entry_point():
+    """prepare() records the same calls that run directly."""
+    x = torch.randn((2, 3, 8 * 64), device="cuda").to(BF)
+    kc = torch.zeros((2, 2, 2, 16, 64), dtype=BF, device="cuda")
+    vc = torch.zeros_like(kc)
+    slots, pos = torch.arange(3, device="cuda"), torch.arange(3, dtype=torch.int32, device="cuda")
+    gain = torch.rand(64, device="cuda")
+    call = tp.prepare(tp.tp_qkv_append, x, kc, vc, slots, positions=pos, rope=rope_table(4, 64), q_norm=gain, k_norm=gain,
+                      eps=1e-5, interleaved=True)
+    q = call().clone()
+    k1, v1 = kc.clone(), vc.clone()
+    again = tp.tp_qkv_append(x, kc.zero_(), vc.zero_(), slots, positions=pos, rope=rope_table(4, 64), q_norm=gain,
+                             k_norm=gain, eps=1e-5, interleaved=True)
+    assert torch.equal(q, again) and torch.equal(k1, kc) and torch.equal(v1, vc)
+    table = torch.zeros((1, 1), dtype=torch.int32, device="cuda")
+    cu, n = torch.tensor([0, 3], dtype=torch.int32, device="cuda"), torch.tensor([3], dtype=torch.int32, device="cuda")
+    args = (q, kc, vc, table, cu, n)
+    call = tp.prepare(tp.tp_paged_prefill, *args, prefix_lens=n, softcap=3.0, window=2)
+    assert torch.equal(call(), tp.tp_paged_prefill(*args, prefix_lens=n, softcap=3.0, window=2))
+    logits, u = torch.randn((4, 100), device="cuda"), torch.rand(4, device="cuda")
+    call = tp.prepare(tp.tp_sample, logits, u, temperature=u + 0.5, min_p=u * 0.1)
+    for got, want in zip(call(), tp.tp_sample(logits, u, temperature=u + 0.5, min_p=u * 0.1)):
+        assert torch.equal(got, want)
+    status_ok()
