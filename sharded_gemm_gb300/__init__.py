@@ -824,7 +824,7 @@ def tp_qkv_append(qkv, k_cache, v_cache, slots, positions=None, rope=None, q_nor
         Hk, _, D = k.shape[-3:]
         if cols <= 2 * Hk * D:
             raise ValueError("qkv holds no query heads besides 2 * %d key and value heads" % Hk)
-        out = k.new_empty((len(qkv), T, cols - 2 * Hk * D))
+        out = _torch().empty((len(qkv), T, cols - 2 * Hk * D), dtype=k.dtype, device=k.device)
     _call("tp_qkv_append", (_native or _marshaller()).append, qkv, k_cache, v_cache, slots, positions, rope, q_norm,
           k_norm, eps, interleaved, out, stream)
     return out
@@ -832,7 +832,9 @@ def tp_qkv_append(qkv, k_cache, v_cache, slots, positions=None, rope=None, q_nor
 
 def _like(q):
     """An output for per-rank queries: one tensor, the ranks first."""
-    return q[0].new_empty((len(q),) + tuple(q[0].shape)) if isinstance(q, (list, tuple)) else q.new_empty(q.shape)
+    if isinstance(q, (list, tuple)):
+        return q[0].new_empty((len(q),) + tuple(q[0].shape))
+    return _torch().empty_like(q)
 
 
 def tp_paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale=None, softcap: float = 0.0, window: int = 0,
@@ -865,9 +867,9 @@ def tp_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, t
     numbers ``u`` (B); returns (tokens int64 (B), logprobs float32 (B))."""
     torch = _torch()
     if tokens is None:
-        tokens = logits.new_empty((logits.shape[0],), dtype=torch.int64)
+        tokens = torch.empty((logits.shape[0],), dtype=torch.int64, device=logits.device)
     if logprobs is None:
-        logprobs = logits.new_empty((logits.shape[0],), dtype=torch.float32)
+        logprobs = torch.empty((logits.shape[0],), dtype=torch.float32, device=logits.device)
     _call("tp_sample", (_native or _marshaller()).sample, logits, u, temperature, top_k, top_p, min_p, tokens, logprobs,
           stream)
     return tokens, logprobs

@@ -67,19 +67,32 @@ __device__ unsigned long long block_sum(unsigned long long v, unsigned long long
 // then start in different banks), and sums over runs in order are sums over the
 // row in order.  The end of the last run is padded with -inf.
 //
-// The end of a kept prefix is found with 2048 bins over x: elements are counted
-// (or their weights added up) per bin, the bin that holds the end is picked, and
-// its elements, a few hundred, are sorted on one CTA.
+// The end of a kept prefix is narrowed down until a few hundred elements hold it,
+// which are put in order on one CTA.
+//   top-k: 2048 bins over x count the largest of the threads' runs (of quarters
+//     of them for a large k): the bins in which k of those lie hold at least k
+//     elements, and not many more.
+//   top-p: the exact weights above six values are summed in registers, in the
+//     pass that sums the whole row; then again above six values between the two
+//     that hold the end, over the few elements there (a mask of the run's).
+// (Adding every weight to bins in shared memory took 25 us a row: an addition
+// costs a lane about two cycles of the SM.)
 //
-// What bounds it is arithmetic: about 20 instructions an element for each pass
-// that needs exact weights, two to four passes.
+// What bounds it is arithmetic: about 25 instructions an element for a pass with
+// exact weights (a row needs one, or none for top-k), 20 for the six values.
 
 constexpr int kBins = 2048, kList = 2048;
 constexpr float kBinScale = 64.0f;  // 1/64 of a logit wide, from the largest down
+constexpr int kMarks = 6;  // values above which weights are summed; first kMarkStep, 2 kMarkStep, .. below the largest,
+constexpr float kMarkStep = 2.0f;  // in units of the temperature
+constexpr float kNoWeight = 28.0f;  // so far below the largest a weight is 0
+constexpr int kRanked = 512;  // a list this long is put in order by counting, each element against all
+constexpr int kFew = 256;     // and one for which another round of narrowing does not pay
+constexpr int kMaxRun = 51;   // 51 * 1024 floats and RowShared fill a CTA's shared memory; and bits of a mask
 
 typedef unsigned long long u64;
 
-struct RowShared {
+struct alignas(16) RowShared {  // the row's float4 stores begin behind it
   union {
     uint32_t hist[kBins];
     u64 hist64[kBins];
@@ -88,9 +101,12 @@ struct RowShared {
   u64 warp_a[2][32], warp_b[2][32];
   u64 xa[2], xb[2];  // this CTA's sums, exchanged over the cluster
   uint32_t warp_m[2][32], xm[2];
-  u64 answer;
+  uint32_t mark_hi[kMarks + 1][32], mark_lo[kMarks + 1][32];
+  u64 mark_sums[kMarks + 1], mark_totals[kMarks + 1];
+  u64 answer, before;
+  int drawn;
   uint32_t list_n;
-  int bin0, bin1;
+  int bin;
 };
 
 __device__ __forceinline__ u64 ld_cluster_u64(uint32_t addr) {
@@ -150,6 +166,64 @@ struct Cut {
   __device__ __forceinline__ bool keeps(float v, uint32_t index) const { return v > x || (v == x && index <= i); }
 };
 
+// Which elements of a run are meant, one bit each.
+struct Mask {
+  uint32_t lo = 0, hi = 0;
+  __device__ __forceinline__ int count() const { return __popc(lo) + __popc(hi); }
+  __device__ __forceinline__ bool any() const { return lo | hi; }
+  __device__ __forceinline__ void set(int j, bool on) {
+    const uint32_t bit = on ? 1u << (j & 31) : 0;
+    if (j < 32) lo |= bit; else hi |= bit;
+  }
+};
+template <typename In>
+__device__ __forceinline__ Mask mask_of(int R, In in) {
+  Mask m;
+  const int n = R < 32 ? R : 32;
+#pragma unroll 4
+  for (int j = 0; j < n; ++j) m.lo = __funnelshift_r(m.lo, in(j) ? 1u : 0u, 1);
+  m.lo = n < 32 ? m.lo >> (32 - n) : m.lo;
+#pragma unroll 4
+  for (int j = 32; j < R; ++j) m.hi = __funnelshift_r(m.hi, in(j) ? 1u : 0u, 1);
+  if (R > 32) m.hi >>= 64 - R;
+  return m;
+}
+// f(j, valid) for the elements of each lane's mask, all lanes of the warp in step:
+// a lane that has run out gets j = 0 and valid = false.
+template <typename F>
+__device__ __forceinline__ void for_each(Mask m, F f) {
+  const int most = __reduce_max_sync(0xffffffffu, m.count());
+  for (int i = 0; i < most; ++i) {
+    const bool low = m.lo != 0;
+    const uint32_t w = low ? m.lo : m.hi;
+    const int j = w ? (low ? 0 : 32) + __ffs(w) - 1 : 0;
+    if (low) m.lo &= m.lo - 1; else m.hi &= m.hi - 1;
+    f(j, w != 0);
+  }
+}
+
+// Weights above kMarks values and of all (the last), as upper and lower 20 bits.
+struct MarkSums {
+  float mark[kMarks];
+  uint32_t hi[kMarks + 1], lo[kMarks + 1];
+  __device__ __forceinline__ MarkSums() {
+#pragma unroll
+    for (int i = 0; i <= kMarks; ++i) hi[i] = lo[i] = 0;
+  }
+  __device__ __forceinline__ void add(float v, float e) {
+    WeightSum w;
+    w.add(e);
+    const uint32_t h = w.hi - 0x4B000000u, l = w.lo - 0x4B000000u;
+    hi[kMarks] += h, lo[kMarks] += l;
+#pragma unroll
+    for (int i = 0; i < kMarks; ++i)  // the two additions under one predicate
+      asm("{\n .reg .pred p;\n setp.gt.f32 p, %2, %3;\n @p add.u32 %0, %0, %4;\n @p add.u32 %1, %1, %5;\n}"
+          : "+r"(hi[i]), "+r"(lo[i])
+          : "f"(v), "f"(mark[i]), "r"(h), "r"(l));
+  }
+  __device__ __forceinline__ u64 sum(int i) const { return ((u64)hi[i] << 20) + lo[i]; }
+};
+
 struct Row {
   RowShared &sh;
   const float *run;  // this thread's elements
@@ -162,6 +236,12 @@ struct Row {
     if (C > 1) cluster_sync_all(); else __syncthreads();
   }
   __device__ __forceinline__ uint32_t at0(const void *p) { return mapa_shared(smem_u32(p), 0); }
+  // Where the draw goes, for resolve().
+  u64 share;
+  float min_p, logz;
+  int64_t *token;
+  float *logprob;
+  bool drawn;
   __device__ __forceinline__ float e_of(float x) { return ratio(x, top, inv_t); }
 
   // Sums of a and b over the cluster; every thread gets them, and in before_a
@@ -237,17 +317,45 @@ struct Row {
     return base + run - v;
   }
 
+  // The threads' mark sums over the cluster; every thread gets them.  A thread's
+  // halves are below 2^26 (64 elements of 2^20), a warp's below 2^31.
+  __device__ __forceinline__ void reduce_marks(const MarkSums &m, u64 (&v)[kMarks + 1]) {
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+#pragma unroll
+    for (int i = 0; i <= kMarks; ++i) {
+      const uint32_t h = __reduce_add_sync(0xffffffffu, m.hi[i]), l = __reduce_add_sync(0xffffffffu, m.lo[i]);
+      if (lane == 0) sh.mark_hi[i][warp] = h, sh.mark_lo[i][warp] = l;
+    }
+    __syncthreads();
+    if (warp <= kMarks) {
+      u64 x = ((u64)sh.mark_hi[warp][lane] << 20) + sh.mark_lo[warp][lane];
+#pragma unroll
+      for (int o = 16; o > 0; o /= 2) x += __shfl_xor_sync(0xffffffffu, x, o);
+      if (lane == 0) (C > 1 ? sh.mark_sums : sh.mark_totals)[warp] = x;
+    }
+    sync();
+    if (C > 1) {
+      if (threadIdx.x <= kMarks) {
+        u64 x = 0;
+        for (int c = 0; c < C; ++c) x += ld_cluster_u64(mapa_shared(smem_u32(&sh.mark_sums[threadIdx.x]), c));
+        sh.mark_totals[threadIdx.x] = x;
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i <= kMarks; ++i) v[i] = sh.mark_totals[i];
+  }
+
   // Before bins are added to: the last readers of what they share memory with
   // are a sync behind.
   __device__ __forceinline__ void clear_bins() {
     for (int i = threadIdx.x; i < kBins; i += kThreads) sh.hist64[i] = 0;
-    if (threadIdx.x == 0) sh.list_n = 0, sh.bin0 = sh.bin1 = kBins - 1;
+    if (threadIdx.x == 0) sh.list_n = 0, sh.bin = kBins - 1, sh.before = 0;
     __syncthreads();
   }
-  // The bins over the cluster in which the running total reaches `target`,
-  // where the true totals are (bins << shift) plus less than slack << shift.
+  // The bin over the cluster in which the running total reaches `target`, and the total before it.
   template <typename H>
-  __device__ __forceinline__ void pick_bins(const H *hist, u64 target, int shift, u64 slack, int &b0, int &b1) {
+  __device__ __forceinline__ int pick_bin(const H *hist, u64 target, u64 &below) {
     sync();  // every CTA's bins are complete
     const int per = C == 1 ? 2 : 1, i = rank * (kBins / C) + (int)threadIdx.x * per;
     u64 h0 = 0, h1 = 0;
@@ -267,69 +375,127 @@ struct Row {
       reduce(mine, unused, &base);
     }
     const u64 c0 = base + before, c1 = c0 + h0, c2 = c1 + h1;
-    auto over = [&](u64 cum, u64 more) { return ((cum + more) << shift) >= target; };
     auto mark = [&](u64 from, u64 to, int at) {
-      if (from == to) return;
-      if (over(to, slack) && (from == 0 || !over(from, slack))) st_cluster_u32(at0(&sh.bin0), at);
-      if (over(to, 0) && !over(from, 0)) st_cluster_u32(at0(&sh.bin1), at);
+      if (from < target && to >= target) {
+        st_cluster_u32(at0(&sh.bin), at);
+        st_cluster_u64(at0(&sh.before), from);
+      }
     };
     mark(c0, c1, i);
     mark(c1, c2, i + 1);
     sync();
-    b0 = (int)ld_cluster_u32(at0(&sh.bin0)), b1 = (int)ld_cluster_u32(at0(&sh.bin1));
+    below = ld_cluster_u64(at0(&sh.before));
+    return (int)ld_cluster_u32(at0(&sh.bin));
   }
 
-  // Puts this thread's elements that `in` accepts (n of them) on rank 0's list.
-  template <typename In>
-  __device__ __forceinline__ void gather(int n, In in) {
-    if (n > 0) {
-      uint32_t at = atom_cluster_add(at0(&sh.list_n), n);
-      for (int j = 0; j < R; ++j)
-        if (in(run[j], index0 + j)) st_cluster_u64(at0(&sh.list[at++]), q_of(run[j], index0 + j));
+  // Puts this thread's elements of `mask` on rank 0's list (cleared a sync before).
+  __device__ __forceinline__ void gather(const Mask &mask) {
+    if (__any_sync(0xffffffffu, mask.any())) {
+      uint32_t at = mask.any() ? atom_cluster_add(at0(&sh.list_n), mask.count()) : 0;
+      for_each(mask, [&](int j, bool valid) {
+        if (valid) st_cluster_u64(at0(&sh.list[at++]), q_of(run[j], index0 + j));
+      });
     }
     sync();
+  }
+  __device__ __forceinline__ void clear_list() {
+    if (threadIdx.x == 0) sh.list_n = 0;
+    sync();
+  }
+
+  // Puts rank 0's list in order, the largest first.
+  __device__ __forceinline__ void order_list(int n) {
+    const int tid = threadIdx.x;
+    if (n <= kRanked) {
+      const u64 q = tid < n ? sh.list[tid] : 0;
+      int place = 0;
+      if (tid < n) {
+#pragma unroll 4
+        for (int j = 0; j < n; ++j) place += sh.list[j] > q;
+      }
+      __syncthreads();
+      if (tid < n) sh.list[place] = q;
+      __syncthreads();
+      return;
+    }
+    int size = 2;
+    while (size < n) size *= 2;
+    for (int i = n + tid; i < size; i += kThreads) sh.list[i] = 0;
+    __syncthreads();
+    for (int width = 2; width <= size; width *= 2)
+      for (int step = width / 2; step > 0; step /= 2) {
+        if (tid < size / 2) {
+          const int i = (tid & ~(step - 1)) << 1 | (tid & (step - 1));
+          const u64 x = sh.list[i], y = sh.list[i + step];
+          if ((x < y) == ((i & width) == 0)) sh.list[i] = y, sh.list[i + step] = x;
+        }
+        __syncthreads();
+      }
   }
 
   // Rank 0's list: n elements, all of a stretch of the order behind which
   // `place0` elements of weight `above` lie.  The cut that keeps the first k of
-  // the order and, with p_share < 2^24, of those the ones whose weight before
-  // them is under `want` (found here from p_share where the list starts the order).
-  __device__ __forceinline__ Cut resolve(int n, u64 place0, u64 above, u64 k, bool by_p, u64 want, u64 p_share) {
+  // the order and, by_p, of those the ones whose weight before them is under
+  // `want`.  A list that begins the order (whole): want is part_of(the k's
+  // weight, p_share), and where all that is kept is on the list, few enough, the
+  // token is drawn from it at once (drawn).
+  __device__ __forceinline__ Cut resolve(int n, u64 place0, u64 above, u64 k, bool by_p, u64 want, bool whole = false,
+                                         u64 p_share = 0) {
     if (rank == 0) {
       const int tid = threadIdx.x;
-      int size = 2;
-      while (size < n) size *= 2;
-      for (int i = n + tid; i < size; i += kThreads) sh.list[i] = 0;
       __syncthreads();
-      for (int width = 2; width <= size; width *= 2)
-        for (int step = width / 2; step > 0; step /= 2) {
-          if (tid < size / 2) {
-            const int i = (tid & ~(step - 1)) << 1 | (tid & (step - 1));
-            const u64 x = sh.list[i], y = sh.list[i + step];
-            if ((x < y) == ((i & width) == 0)) sh.list[i] = y, sh.list[i + step] = x;
-          }
-          __syncthreads();
-        }
-      u64 w[2];
+      order_list(n);
+      u64 q[2], w[2];
+      float e[2];
       bool in[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int at = 2 * tid + i;
         in[i] = at < n && place0 + at < k;
-        w[i] = in[i] ? weight(e_of(x_of_key((uint32_t)(sh.list[at] >> 32)))) : 0;
+        q[i] = at < n ? sh.list[at] : 0;
+        e[i] = in[i] ? e_of(x_of_key((uint32_t)(q[i] >> 32))) : 0.0f;
+        w[i] = weight(e[i]);
       }
       u64 total;
       const u64 before = above + scan_before(w[0] + w[1], total);
       par ^= 1;  // as on the other CTAs
       if (by_p) {
-        if (place0 == 0 && above == 0 && p_share) want = part_of(total, p_share - 1);
+        if (whole) want = part_of(total, p_share);
         in[0] = in[0] && (before < want || place0 + 2 * tid == 0);
         in[1] = in[1] && before + w[0] < want;
       }
       const int kept = __syncthreads_count(in[0]) + __syncthreads_count(in[1]);
-      if (tid == 0) sh.answer = sh.list[kept - 1];
+      if (tid == 0) sh.answer = sh.list[kept - 1], sh.drawn = 0;
+      if (whole && n <= kList / 2 && kept <= kRanked) {
+        // the draw: the kept ones' weights beside them, then each sums those of lower index
+        u64 *kept_w = sh.list + kList / 2;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (e[i] < min_p) w[i] = 0;
+          if (!in[i]) w[i] = 0;
+          if (2 * tid + i < kept) kept_w[2 * tid + i] = w[i];
+        }
+        u64 sum;
+        scan_before(w[0] + w[1], sum);
+        par ^= 1;
+        __syncthreads();
+        const u64 r = part_of(sum, share);
+        if (tid < kept) {
+          const u64 mine = sh.list[tid];
+          const uint32_t index = ~(uint32_t)mine;
+          u64 run = 0;
+#pragma unroll 4
+          for (int j = 0; j < kept; ++j) run += ~(uint32_t)sh.list[j] < index ? kept_w[j] : 0;
+          if (run <= r && r < run + kept_w[tid]) {
+            *token = index;
+            if (logprob) *logprob = x_of_key((uint32_t)(mine >> 32)) - top - logz;
+          }
+        }
+        if (tid == 0) sh.drawn = 1;
+      }
     }
     sync();
+    drawn = ld_cluster_u32(at0(&sh.drawn)) != 0;
     const u64 q = ld_cluster_u64(at0(&sh.answer));
     return Cut{x_of_key((uint32_t)(q >> 32)), ~(uint32_t)q};
   }
@@ -348,92 +514,92 @@ struct Row {
         const u64 add = BY_WEIGHT ? weight(e_of(run[j])) : 1;
         if (add) atomicAdd(&sh.hist64[(hi - q) >> shift], add);
       }
-      int b0, b1;
-      pick_bins(sh.hist64, want - above, 0, 0, b0, b1);
-      const u64 new_hi = hi - ((u64)b1 << shift), span = (1ull << shift) - 1;
+      u64 below;
+      const int picked = pick_bin(sh.hist64, want - above, below);
+      above += below;
+      const u64 new_hi = hi - ((u64)picked << shift), span = (1ull << shift) - 1;
       const u64 new_lo = new_hi - lo > span ? new_hi - span : lo;
-      u64 over = 0, n = 0;
-      for (int j = 0; j < R; ++j) {
-        const u64 q = q_of(run[j], index0 + j);
-        if (q >= lo && q <= hi) {
-          if (q > new_hi) over += BY_WEIGHT ? weight(e_of(run[j])) : 1;
-          else if (q >= new_lo) ++n;
-        }
-      }
-      const int mine = (int)n;
-      reduce(over, n);
-      above += over;
       lo = new_lo, hi = new_hi;
+      const Mask mask = mask_of(R, [&](int j) {
+        const u64 q = q_of(run[j], index0 + j);
+        return q >= lo && q <= hi;
+      });
+      u64 n = mask.count(), unused = 0;
+      reduce(n, unused);
       if (n <= kList) {
-        gather(mine, [&](float x, uint32_t i) { return q_of(x, i) >= lo && q_of(x, i) <= hi; });
-        return BY_WEIGHT ? resolve((int)n, 1, above, ~0ull, true, want, 0)
-                         : resolve((int)n, above, 0, want, false, 0, 0);
+        gather(mask);
+        return BY_WEIGHT ? resolve((int)n, 1, above, ~0ull, true, want) : resolve((int)n, above, 0, want, false, 0);
       }
     }
   }
 
   // The first k, and of those with by_p the ones under part_of(their weight, p_share).
   __device__ __forceinline__ Cut select_count(u64 k, bool by_p, u64 p_share, bool &only_first) {
-    // k runs whose largest is in one of the first bins hold k elements in them
-    int limit = kBins - 1, unused;
-    if (k <= (u64)C * kThreads) {
+    // k runs (or quarters) whose largest is in one of the first bins hold k elements in them
+    int limit = kBins - 1;
+    u64 below = 0, unused = 0;
+    auto in_bins = [&](float v) { return limit == kBins - 1 || (top - v) * kBinScale < (float)(limit + 1); };
+    const int parts = k <= (u64)C * kThreads / 4 ? 1 : 4;
+    if (k <= (u64)C * kThreads * parts) {
       clear_bins();
-      atomicAdd(&sh.hist[bin_of(run_top, top)], 1u);
-      pick_bins(sh.hist, k, 0, 0, unused, limit);
+      if (parts == 1) {
+        atomicAdd(&sh.hist[bin_of(run_top, top)], 1u);
+      } else {
+        for (int i = 0; i < 4; ++i) {
+          float most = -INFINITY;
+          for (int j = R * i / 4; j < R * (i + 1) / 4; ++j) most = fmaxf(most, run[j]);
+          if (most > -INFINITY) atomicAdd(&sh.hist[bin_of(most, top)], 1u);
+        }
+      }
+      limit = pick_bin(sh.hist, k, below);
     }
-    u64 n = 0, none = 0;
-    if (bin_of(run_top, top) <= limit)
-      for (int j = 0; j < R; ++j) n += bin_of(run[j], top) <= limit;
-    int mine = (int)n;
-    reduce(n, none);
-    u64 over = 0;
-    int first = 0;  // the list holds bins first..limit
+    Mask mask;
+    if (in_bins(run_top)) mask = mask_of(R, [&](int j) { return in_bins(run[j]); });
+    u64 n = mask.count(), over = 0;
+    reduce(n, unused);
     if (n > kList) {
       clear_bins();
-      if (mine)
-        for (int j = 0; j < R; ++j)
-          if (bin_of(run[j], top) <= limit) atomicAdd(&sh.hist[bin_of(run[j], top)], 1u);
-      pick_bins(sh.hist, k, 0, 0, unused, limit);
-      n = 0;
-      if (bin_of(run_top, top) <= limit)
-        for (int j = 0; j < R; ++j) {
-          const int b = bin_of(run[j], top);
-          n += b == limit;
-          over += b < limit;
-        }
-      mine = (int)n;
-      const int mine_over = (int)over;
-      reduce(n, over);
+      for_each(mask, [&](int j, bool valid) {
+        if (valid) atomicAdd(&sh.hist[bin_of(run[j], top)], 1u);
+      });
+      limit = pick_bin(sh.hist, k, over);
+      Mask equal, under;
+      for_each(mask, [&](int j, bool valid) {
+        const int b = bin_of(run[j], top);
+        equal.set(j, valid && b == limit);
+        under.set(j, valid && b < limit);
+      });
+      n = equal.count();
+      unused = 0;
+      reduce(n, unused);
+      mask = equal;
       if (n + over <= kList) {
-        mine += mine_over;
         n += over, over = 0;
-      } else {
-        first = limit;
+        mask.lo |= under.lo, mask.hi |= under.hi;
       }
     }
     Cut cut;
     if (n <= kList) {
-      if (threadIdx.x == 0) sh.list_n = 0;
-      sync();
-      gather(mine, [&](float x, uint32_t) { return bin_of(x, top) >= first && bin_of(x, top) <= limit; });
-      const bool both = by_p && first == 0;
-      cut = resolve((int)n, over, 0, k, both, 0, p_share + 1);
-      if (both) return cut;
+      clear_list();
+      gather(mask);
+      const bool whole = over == 0;
+      cut = resolve((int)n, over, 0, k, by_p && whole, 0, whole, p_share);
+      if (drawn || (by_p && whole)) return cut;
     } else {
       u64 lo, hi;
-      stretch(limit, limit, lo, hi);
+      stretch(limit, lo, hi);
       cut = select_in<false>(lo, hi, over, k);
     }
-    return by_p ? select_weight(0, p_share, cut, only_first) : cut;
+    u64 run_above = 0;
+    return by_p ? select_weight(0, p_share, cut, top, -INFINITY, 0, only_first, run_above, mask) : cut;
   }
 
-  // The stretch of the order that the elements of bins b0..b1 take.
-  __device__ __forceinline__ void stretch(int b0, int b1, u64 &lo, u64 &hi) {
+  // The stretch of the order that the elements of a bin take.
+  __device__ __forceinline__ void stretch(int bin, u64 &lo, u64 &hi) {
     uint32_t most = 0, not_least = 0;
     for (int j = 0; j < R; ++j) {
-      const int b = bin_of(run[j], top);
       const uint32_t key = order_key(run[j]);
-      if (b < b0 || b > b1) continue;
+      if (bin_of(run[j], top) != bin) continue;
       if (key > most) most = key;
       if (~key > not_least) not_least = ~key;
     }
@@ -441,60 +607,66 @@ struct Row {
     lo = (u64)~reduce_max(not_least) << 32;
   }
 
-  // Of what `from` keeps (weight `total`, 0: not known) the ones whose weight before
-  // them is under part_of(total, p_share).
-  __device__ __noinline__ Cut select_weight(u64 total, u64 p_share, Cut from, bool &only_first) {
-    u64 none = 0;
+  // Of what `from` keeps (weight `total`, 0: not known) the ones whose weight
+  // before them is under part_of(total, p_share).  The end is known to lie among
+  // the values in (low, high], with weight `above` over them, run_above of it
+  // this thread's.  On return `mask` has this thread's elements of the last such
+  // stretch, and run_above fits it.
+  __device__ __noinline__ Cut select_weight(u64 total, u64 p_share, Cut from, float high, float low, u64 above,
+                                            bool &only_first, u64 &run_above, Mask &mask) {
+    u64 unused = 0;
     if (total == 0) {
       WeightSum sum;
       for (int j = 0; j < R; ++j) sum.add(from.keeps(run[j], index0 + j) ? e_of(run[j]) : 0.0f);
       total = sum.total();
-      reduce(total, none);
+      reduce(total, unused);
     }
     const u64 want = part_of(total, p_share);
     if (want == 0) {
       only_first = true;
       return from;
     }
-    // Bins of 32 bits: what the dropped low bits may amount to is the slack.
-    const int bits = 64 - __clzll(total), shift = bits > 31 ? bits - 31 : 0;
-    const u64 slack = shift ? (u64)R * kThreads * C : 0;
-    clear_bins();
-#pragma unroll 4
-    for (int j = 0; j < R; ++j) {
-      const float x = run[j];
-      WeightSum w;
-      w.add(from.keeps(x, index0 + j) ? e_of(x) : 0.0f);
-      const uint32_t add = (uint32_t)(w.total() >> shift);
-      if (add) atomicAdd(&sh.hist[bin_of(x, top)], add);
-    }
-    int b0, b1;
-    pick_bins(sh.hist, want, shift, slack, b0, b1);
-    WeightSum sum;
-    u64 n = 0;
-#pragma unroll 4
-    for (int j = 0; j < R; ++j) {
-      const float x = run[j];
-      const int b = bin_of(x, top);
-      const bool kept = from.keeps(x, index0 + j);
-      sum.add(kept && b < b0 ? e_of(x) : 0.0f);
-      n += kept && b >= b0 && b <= b1;
-    }
-    const int mine = (int)n;
-    u64 above = sum.total();
-    reduce(above, n);
-    if (n <= kList) {
-      if (threadIdx.x == 0) sh.list_n = 0;
-      sync();
-      gather(mine, [&](float x, uint32_t i) {
-        return from.keeps(x, i) && bin_of(x, top) >= b0 && bin_of(x, top) <= b1;
+    if (from.x == -INFINITY) mask = mask_of(R, [&](int j) { return run[j] <= high && run[j] > low; });
+    else mask = mask_of(R, [&](int j) { return run[j] <= high && run[j] > low && from.keeps(run[j], index0 + j); });
+    const float floor_x = __fdiv_rn(-kNoWeight, inv_t) + top;
+    u64 n = mask.count(), was = ~0ull;
+    unused = 0;
+    reduce(n, unused);
+    while (n > kFew && n < was) {
+      // the weights above six values between low and high
+      const float from_x = low > floor_x ? low : floor_x, step = (high - from_x) * (1.0f / (kMarks + 1));
+      MarkSums m;
+#pragma unroll
+      for (int i = 0; i < kMarks; ++i) m.mark[i] = high - (i + 1) * step;
+      for_each(mask, [&](int j, bool valid) {
+        const float x = run[j];
+        m.add(x, valid ? e_of(x) : 0.0f);
       });
-      return resolve((int)n, b0 > 0 || above ? 1 : 0, above, ~0ull, true, want, 0);
+      u64 v[kMarks + 1], over = 0, run_over = 0;
+      reduce_marks(m, v);
+#pragma unroll
+      for (int i = 0; i < kMarks; ++i) {
+        if (above + v[i] < want) high = m.mark[i], over = v[i], run_over = m.sum(i);
+        if (above + v[kMarks - 1 - i] >= want) low = m.mark[kMarks - 1 - i];
+      }
+      above += over, run_above += run_over;
+      Mask kept;
+      for_each(mask, [&](int j, bool valid) { kept.set(j, valid && run[j] <= high && run[j] > low); });
+      mask = kept;
+      was = n;
+      n = mask.count();
+      unused = 0;
+      reduce(n, unused);
     }
-    const u64 floor_q = q_of(from.x, from.i);
-    u64 lo, hi;
-    stretch(b0, b1, lo, hi);
-    return select_in<true>(lo > floor_q ? lo : floor_q, hi, above, want);
+    if (n <= kList) {
+      clear_list();
+      gather(mask);
+      return resolve((int)n, above ? 1 : 0, above, ~0ull, true, want);
+    }
+    u64 lo = ((u64)order_key(low) + 1) << 32;
+    const u64 from_q = q_of(from.x, from.i);
+    if (lo < from_q) lo = from_q;
+    return select_in<true>(lo, (u64)order_key(high) << 32 | 0xffffffffu, above, want);
   }
 };
 
@@ -553,6 +725,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_row_kernel(const __grid_co
     top = fmaxf(top, v);
   }
   Row row{sh, xs + tid * R, R, C, rank, (uint32_t)(rank * slice + tid * R), 0.0f, greedy ? 1.0f : 1.0f / t, -INFINITY, 0, 0};
+  row.drawn = false;
   row.top = top = x_of_key(row.reduce_max(order_key(top)));  // also: the slice is in shared memory
   if (top == -INFINITY) {  // nothing can be drawn
     if (rank == 0 && tid == 0) {
@@ -563,35 +736,86 @@ __global__ void __launch_bounds__(kThreads, 1) sample_row_kernel(const __grid_co
     return;
   }
 
-  // ---- the row's own softmax total, the first of the largest, and the weight of all where top-p asks for it
+  // ---- the row's own softmax total z, and in the same pass the exact weights it is drawn by
+  const bool by_k = k < a.V || k == 1, free_draw = !by_k && !by_p;
   float z = 0.0f;
-  int first = -1;
-  WeightSum all;
-  if (by_p && k == a.V) {
+  WeightSum sum;   // what is kept of the run, where that is known
+  MarkSums marks;  // top-p alone: the run's weight, and above six values
+  auto z_of = [&](float v) { return exp2f((v - top) * 1.4426950408889634f); };
+  if (free_draw) {
 #pragma unroll 4
-    for (int j = R - 1; j >= 0; --j) all.add(row.e_of(row.run[j]));
-  }
+    for (int j = 0; j < R; ++j) {
+      const float v = row.run[j], e = row.e_of(v);
+      z += z_of(v);
+      sum.add(e < min_p ? 0.0f : e);
+    }
+  } else if (!by_k) {
+#pragma unroll
+    for (int i = 0; i < kMarks; ++i) marks.mark[i] = top - (i + 1) * kMarkStep * t;
+#pragma unroll 2
+    for (int j = 0; j < R; ++j) {
+      const float v = row.run[j];
+      z += z_of(v);
+      row.run_top = fmaxf(row.run_top, v);
+      marks.add(v, row.e_of(v));
+    }
+  } else {
 #pragma unroll 4
-  for (int j = R - 1; j >= 0; --j) {
-    const float v = row.run[j];
-    z += exp2f((v - top) * 1.4426950408889634f);
-    row.run_top = fmaxf(row.run_top, v);
-    if (v == top) first = j;
+    for (int j = 0; j < R; ++j) {
+      const float v = row.run[j];
+      z += z_of(v);
+      row.run_top = fmaxf(row.run_top, v);
+    }
   }
   // the threads' sums are joined as whole numbers of 2^-40, which have no order
-  u64 zsum = (u64)(z * 1099511627776.0f), all_w = all.total();
-  row.reduce(zsum, all_w);
+  u64 zsum = (u64)(z * 1099511627776.0f), unused = 0;
+  row.reduce(zsum, unused);
   const float logz = logf((float)zsum * 9.094947017729282e-13f);
+  row.share = u > 0.0f ? (u64)(fminf(u, 1.0f) * 16777216.0f) : 0ull;
+  if (row.share > 16777215ull) row.share = 16777215ull;
+  row.min_p = min_p, row.logz = logz, row.token = a.tokens + b, row.logprob = a.logprobs ? a.logprobs + b : nullptr;
 
   // ---- the kept prefix
   Cut cut{-INFINITY, 0xffffffffu};
   bool only_first = k == 1 || (by_p && p_share == 0);
-  if (!only_first) {
-    if (k < a.V) cut = row.select_count((u64)k, by_p, p_share, only_first);
-    else if (by_p) cut = row.select_weight(all_w, p_share, cut, only_first);
+  u64 mine = sum.total();
+  bool summed = free_draw;
+  if (!only_first && by_k) {
+    cut = row.select_count((u64)k, by_p, p_share, only_first);
+    if (row.drawn) {
+      if (C > 1) cluster_sync_all();
+      return;
+    }
+  } else if (!only_first && by_p) {
+    u64 v[kMarks + 1];
+    row.reduce_marks(marks, v);
+    const u64 want = part_of(v[kMarks], p_share);
+    float high = top, low = -INFINITY;
+    u64 above = 0, run_above = 0;
+#pragma unroll
+    for (int i = 0; i < kMarks; ++i) {
+      if (v[i] < want) high = marks.mark[i], above = v[i], run_above = marks.sum(i);
+      if (v[kMarks - 1 - i] >= want) low = marks.mark[kMarks - 1 - i];
+    }
+    Mask mask;
+    cut = row.select_weight(v[kMarks], p_share, cut, high, low, above, only_first, run_above, mask);
+    if (!(min_p > 0.0f)) {  // all above the last stretch is kept, and of it what the cut keeps
+      summed = true;
+      mine = run_above;
+      for_each(mask, [&](int j, bool valid) {
+        const float x = row.run[j];
+        mine += valid && cut.keeps(x, row.index0 + j) ? weight(row.e_of(x)) : 0;
+      });
+    }
   }
   if (only_first) {
-    const uint32_t best = row.reduce_max(first >= 0 ? ~(row.index0 + first) : 0);
+    uint32_t best = 0;
+    if (row.run_top == top) {
+      int j = 0;
+      while (row.run[j] != top) ++j;
+      best = ~(row.index0 + j);
+    }
+    best = row.reduce_max(best);
     if (rank == 0 && tid == 0) {
       a.tokens[b] = ~best;
       if (a.logprobs) a.logprobs[b] = -logz;
@@ -605,22 +829,22 @@ __global__ void __launch_bounds__(kThreads, 1) sample_row_kernel(const __grid_co
     const float v = row.run[j], e = row.e_of(v);
     return cut.keeps(v, row.index0 + j) && !(e < min_p) ? e : 0.0f;
   };
-  WeightSum sum;
-  if (row.run_top >= cut.x) {
+  if (!summed) {
+    sum = WeightSum();
 #pragma unroll 4
     for (int j = 0; j < R; ++j) sum.add(kept_e(j));
+    mine = sum.total();
   }
-  const u64 mine = sum.total();
-  u64 block, total, unused = 0, before = row.scan_before(mine, block), lower;
+  u64 block, total, before = row.scan_before(mine, block), lower;
   total = tid == 0 ? block : 0;
+  unused = 0;
   if (C > 1) {
     row.reduce(total, unused, &lower);
     before += lower;
   } else {
     total = block;
   }
-  const u64 share = u > 0.0f ? (u64)(fminf(u, 1.0f) * 16777216.0f) : 0ull;
-  const u64 r = part_of(total, share < 16777216ull ? share : 16777215ull);
+  const u64 r = part_of(total, row.share);
   const uint32_t hit = __ballot_sync(0xffffffffu, r >= before && r < before + mine);
   if (hit) {
     // this warp holds the run: its elements 32 at a time
@@ -649,8 +873,6 @@ __global__ void __launch_bounds__(kThreads, 1) sample_row_kernel(const __grid_co
   }
   if (C > 1) cluster_sync_all();  // no CTA leaves while another may still read its shared memory
 }
-
-constexpr int kMaxRun = 51;  // 51 * 1024 floats and RowShared fill a CTA's shared memory
 
 // ---------------------------------------------------------------- longer rows
 template <typename T>
@@ -849,6 +1071,7 @@ __global__ void __launch_bounds__(kThreads) sample_wide_kernel(const __grid_cons
   }
 }
 
+static_assert(sizeof(RowShared) % 16 == 0, "the row begins behind it, 16-byte aligned");
 static_assert(sizeof(RowShared) + kMaxRun * kThreads * 4 <= 232448, "shared memory of a CTA");
 
 template <typename T>
