@@ -100,13 +100,12 @@ struct alignas(16) RowShared {  // the row's float4 stores begin behind it
   };
   u64 warp_a[2][32], warp_b[2][32];
   u64 xa[2], xb[2];  // this CTA's sums, exchanged over the cluster
+  u64 got[2][3];     // what one thread has read of other CTAs, for all of this one
   uint32_t warp_m[2][32], xm[2];
   uint32_t mark_hi[kMarks + 1][32], mark_lo[kMarks + 1][32];
   u64 mark_sums[kMarks + 1], mark_totals[kMarks + 1];
-  u64 answer, before;
-  int drawn;
+  u64 answer, before, drawn, bin;
   uint32_t list_n;
-  int bin;
 };
 
 __device__ __forceinline__ u64 ld_cluster_u64(uint32_t addr) {
@@ -121,9 +120,6 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
 }
 __device__ __forceinline__ void st_cluster_u64(uint32_t addr, u64 v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
-}
-__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 __device__ __forceinline__ uint32_t atom_cluster_add(uint32_t addr, uint32_t v) {
   uint32_t o;
@@ -242,6 +238,17 @@ struct Row {
   int64_t *token;
   float *logprob;
   bool drawn;
+  // What rank 0 left in a and b before a sync, in every thread.
+  __device__ __forceinline__ void from_rank0(const u64 &at_a, const u64 &at_b, u64 &a, u64 &b) {
+    if (C > 1) {
+      if (threadIdx.x == 0) sh.got[xpar][0] = ld_cluster_u64(at0(&at_a)), sh.got[xpar][1] = ld_cluster_u64(at0(&at_b));
+      __syncthreads();
+      a = sh.got[xpar][0], b = sh.got[xpar][1];
+      xpar ^= 1;
+    } else {
+      a = at_a, b = at_b;
+    }
+  }
   __device__ __forceinline__ float e_of(float x) { return ratio(x, top, inv_t); }
 
   // Sums of a and b over the cluster; every thread gets them, and in before_a
@@ -265,12 +272,22 @@ struct Row {
     if (C > 1) {
       if (threadIdx.x == 0) sh.xa[xpar] = a, sh.xb[xpar] = b;
       cluster_sync_all();
-      a = b = 0;
-      for (int c = 0; c < C; ++c) {
-        if (before_a && c == rank) *before_a = a;
-        a += ld_cluster_u64(mapa_shared(smem_u32(&sh.xa[xpar]), c));
-        b += ld_cluster_u64(mapa_shared(smem_u32(&sh.xb[xpar]), c));
+      // one warp reads the other CTAs' (all threads reading took 2 us at 8 CTAs)
+      if (warp == 0) {
+        a = lane < C ? ld_cluster_u64(mapa_shared(smem_u32(&sh.xa[xpar]), lane)) : 0;
+        b = lane < C ? ld_cluster_u64(mapa_shared(smem_u32(&sh.xb[xpar]), lane)) : 0;
+        u64 lower = lane < rank ? a : 0;
+#pragma unroll
+        for (int m = 4; m > 0; m /= 2) {
+          a += __shfl_xor_sync(0xffffffffu, a, m);
+          b += __shfl_xor_sync(0xffffffffu, b, m);
+          lower += __shfl_xor_sync(0xffffffffu, lower, m);
+        }
+        if (lane == 0) sh.got[xpar][0] = a, sh.got[xpar][1] = b, sh.got[xpar][2] = lower;
       }
+      __syncthreads();
+      a = sh.got[xpar][0], b = sh.got[xpar][1];
+      if (before_a) *before_a = sh.got[xpar][2];
       xpar ^= 1;
     }
     par ^= 1;
@@ -284,11 +301,12 @@ struct Row {
     if (C > 1) {
       if (threadIdx.x == 0) sh.xm[xpar] = v;
       cluster_sync_all();
-      v = 0;
-      for (int c = 0; c < C; ++c) {
-        const uint32_t o = ld_cluster_u32(mapa_shared(smem_u32(&sh.xm[xpar]), c));
-        v = o > v ? o : v;
+      if (warp == 0) {
+        v = __reduce_max_sync(0xffffffffu, lane < C ? ld_cluster_u32(mapa_shared(smem_u32(&sh.xm[xpar]), lane)) : 0);
+        if (lane == 0) sh.got[xpar][0] = v;
       }
+      __syncthreads();
+      v = (uint32_t)sh.got[xpar][0];
       xpar ^= 1;
     }
     par ^= 1;
@@ -335,10 +353,11 @@ struct Row {
     }
     sync();
     if (C > 1) {
-      if (threadIdx.x <= kMarks) {
-        u64 x = 0;
-        for (int c = 0; c < C; ++c) x += ld_cluster_u64(mapa_shared(smem_u32(&sh.mark_sums[threadIdx.x]), c));
-        sh.mark_totals[threadIdx.x] = x;
+      if (warp <= kMarks) {
+        u64 x = lane < C ? ld_cluster_u64(mapa_shared(smem_u32(&sh.mark_sums[warp]), lane)) : 0;
+#pragma unroll
+        for (int o = 4; o > 0; o /= 2) x += __shfl_xor_sync(0xffffffffu, x, o);
+        if (lane == 0) sh.mark_totals[warp] = x;
       }
       __syncthreads();
     }
@@ -377,15 +396,16 @@ struct Row {
     const u64 c0 = base + before, c1 = c0 + h0, c2 = c1 + h1;
     auto mark = [&](u64 from, u64 to, int at) {
       if (from < target && to >= target) {
-        st_cluster_u32(at0(&sh.bin), at);
+        st_cluster_u64(at0(&sh.bin), at);
         st_cluster_u64(at0(&sh.before), from);
       }
     };
     mark(c0, c1, i);
     mark(c1, c2, i + 1);
     sync();
-    below = ld_cluster_u64(at0(&sh.before));
-    return (int)ld_cluster_u32(at0(&sh.bin));
+    u64 bin;
+    from_rank0(sh.before, sh.bin, below, bin);
+    return (int)bin;
   }
 
   // Puts this thread's elements of `mask` on rank 0's list (cleared a sync before).
@@ -495,8 +515,9 @@ struct Row {
       }
     }
     sync();
-    drawn = ld_cluster_u32(at0(&sh.drawn)) != 0;
-    const u64 q = ld_cluster_u64(at0(&sh.answer));
+    u64 q, was_drawn;
+    from_rank0(sh.answer, sh.drawn, q, was_drawn);
+    drawn = was_drawn != 0;
     return Cut{x_of_key((uint32_t)(q >> 32)), ~(uint32_t)q};
   }
 
@@ -670,15 +691,45 @@ struct Row {
   }
 };
 
+// The row that cluster `b` takes: the rows whose filters take several passes
+// come first, so that a batch of more rows than the GPU holds at once does not
+// end on them (384 mixed rows of 50272: 126 us in the order given).
+__device__ __forceinline__ int64_t row_of(const SampleArgs &a, RowShared &sh, int64_t b) {
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  auto slow = [&](int64_t row) {
+    const float t = a.temperature ? a.temperature[row] : 1.0f, p = a.top_p ? a.top_p[row] : 1.0f;
+    const int k = a.top_k ? a.top_k[row] : 0;
+    return t >= 9.5367431640625e-7f && (k <= 0 || k > a.V ? p < 1.0f : k > kFew);
+  };
+  int64_t slow_rows = 0;
+  for (int64_t base = 0; base < a.B; base += kThreads)
+    slow_rows += __syncthreads_count(base + tid < a.B && slow(base + tid));
+  const bool of_slow = b < slow_rows;
+  int64_t target = of_slow ? b : b - slow_rows;  // the row's place among its kind
+  for (int64_t base = 0; base < a.B; base += kThreads) {
+    const bool mine = base + tid < a.B && slow(base + tid) == of_slow;
+    const uint32_t ballot = __ballot_sync(0xffffffffu, mine);
+    if (lane == 0) sh.warp_m[0][warp] = __popc(ballot);
+    __syncthreads();
+    const uint32_t n = sh.warp_m[0][lane];
+    const int before = (int)__reduce_add_sync(0xffffffffu, lane < warp ? n : 0) + __popc(ballot & ((1u << lane) - 1));
+    if (mine && before == target) sh.answer = base + tid;
+    target -= (int)__reduce_add_sync(0xffffffffu, n);
+    __syncthreads();
+  }
+  return (int64_t)sh.answer;
+}
+
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 1) sample_row_kernel(const __grid_constant__ SampleArgs a, int C, int R) {
+__global__ void __launch_bounds__(kThreads, 1)
+    sample_row_kernel(const __grid_constant__ SampleArgs a, int C, int R, bool reorder) {
   extern __shared__ __align__(16) uint8_t smem[];
   RowShared &sh = *reinterpret_cast<RowShared *>(smem);
   float *xs = reinterpret_cast<float *>(smem + sizeof(RowShared));
   griddep_launch_dependents();
   griddep_wait();
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  const int64_t b = blockIdx.x / C;
+  const int64_t b = reorder ? row_of(a, sh, blockIdx.x / C) : blockIdx.x / C;
   const int rank = blockIdx.x % C, slice = R * kThreads;
   const T *x = static_cast<const T *>(a.logits) + b * a.ld + (int64_t)rank * slice;
   const int64_t left = a.V - (int64_t)rank * slice;
@@ -741,12 +792,18 @@ __global__ void __launch_bounds__(kThreads, 1) sample_row_kernel(const __grid_co
   float z = 0.0f;
   WeightSum sum;   // what is kept of the run, where that is known
   MarkSums marks;  // top-p alone: the run's weight, and above six values
-  auto z_of = [&](float v) { return exp2f((v - top) * 1.4426950408889634f); };
+  // (where the temperature is 1, z's terms are the weights' own)
+  const bool own = row.inv_t == 1.0f;
+  auto z_of = [&](float v) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"((v - top) * 1.4426950408889634f));
+    return y;
+  };
   if (free_draw) {
 #pragma unroll 4
     for (int j = 0; j < R; ++j) {
       const float v = row.run[j], e = row.e_of(v);
-      z += z_of(v);
+      z += own ? e : z_of(v);
       sum.add(e < min_p ? 0.0f : e);
     }
   } else if (!by_k) {
@@ -754,10 +811,10 @@ __global__ void __launch_bounds__(kThreads, 1) sample_row_kernel(const __grid_co
     for (int i = 0; i < kMarks; ++i) marks.mark[i] = top - (i + 1) * kMarkStep * t;
 #pragma unroll 2
     for (int j = 0; j < R; ++j) {
-      const float v = row.run[j];
-      z += z_of(v);
+      const float v = row.run[j], e = row.e_of(v);
+      z += own ? e : z_of(v);
       row.run_top = fmaxf(row.run_top, v);
-      marks.add(v, row.e_of(v));
+      marks.add(v, e);
     }
   } else {
 #pragma unroll 4
@@ -1105,7 +1162,8 @@ int launch(const SampleArgs &a, cudaStream_t s) {
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, kern, a, C, R);
+    const bool reorder = a.B * C > sm_count() && (a.top_k || a.top_p);
+    e = cudaLaunchKernelEx(&cfg, kern, a, C, R, reorder);
   }
   if (e != cudaSuccess) return cuda_error(e, "sample launch");
   note_launch();

@@ -12,7 +12,8 @@ import numpy as np
 import torch
 
 from . import (tp_all_to_sharded, tp_all_to_sharded_dx, tp_bias_grad, tp_gated_all_to_sharded,
-               tp_mx_all_to_sharded, tp_mx_quantize, tp_mx_sharded_to_all,
+               tp_mx_all_to_sharded, tp_mx_quantize, tp_mx_sharded_to_all, tp_paged_decode, tp_paged_prefill,
+               tp_qkv_append, tp_sample,
                tp_sharded_dw, tp_sharded_to_all_dx, tp_gathered_to_sharded, tp_q4_all_to_sharded,
                tp_q4_quantize,
                tp_q4_sharded_to_all, tp_shard_weight, tp_sharded_to_all, tp_sharded_to_sharded, tp_summa)
@@ -226,6 +227,69 @@ class QKV:
         tp_sharded_to_all(self.x_cols, self.w_o, self.b_o, out=self.attn_out, stream=stream)
         tp_all_to_sharded(self.x, self.w_lm, None, out=self.logit_views, stream=stream)
         return self.qkv, self.attn_out, self.logits
+
+
+class PagedServing:
+    """The attention block and the vocabulary head of ``QKV`` served over a paged
+    cache: fused QKV -> append (rotation, optional head norms) -> attention of the
+    new tokens -> W_o -> logits of each sequence's last token -> a drawn token.
+
+    ``cfg`` is a ``synth.qkv`` workload's (its x is not used); ``heads`` divides
+    its width into heads of 64 or 128, heads / N of them on a rank.  Sequence b's
+    pages are fixed at construction for ``capacity`` positions.  ``step`` takes the
+    new tokens of every sequence: one each (the decode kernel), or ragged chunks."""
+
+    def __init__(self, cfg: dict, heads: int, batch: int, capacity: int, page: int = 64, rope_base: float = 10000.0,
+                 q_norm=None, k_norm=None, device="cuda"):
+        self.N = N = cfg["N"]
+        D, self.V = cfg["D"], cfg["V"]
+        self.page, self.batch, self.capacity = page, batch, capacity
+        self.head = D // heads
+        self.w_qkv = tp_shard_weight(to_device(cfg["w_qkv"], "bf16", device), 0, 3, N)
+        self.b_qkv = tp_shard_weight(to_device(cfg["b_qkv"], "f32", device), 0, 3, N)
+        self.w_o = tp_shard_weight(to_device(cfg["w_o"], "bf16", device), -1, 1, N)
+        self.b_o = to_device(cfg["b_o"], "f32", device)
+        self.w_lm = tp_shard_weight(to_device(cfg["w_lm"], "bf16", device), 0, 1, N)
+        per_seq = -(-capacity // page)
+        shape = (N, batch * per_seq, heads // N, page, self.head)
+        self.k_cache = torch.empty(shape, dtype=torch.bfloat16, device=device)
+        self.v_cache = torch.empty(shape, dtype=torch.bfloat16, device=device)
+        self.block_table = torch.arange(batch * per_seq, dtype=torch.int32, device=device).view(per_seq, batch).T.contiguous()
+        angle = torch.arange(capacity, dtype=torch.float64)[:, None] * \
+            rope_base ** (-torch.arange(self.head // 2, dtype=torch.float64) * 2 / self.head)
+        self.rope = torch.cat([angle.cos(), angle.sin()], 1).float().to(device)
+        self.q_norm, self.k_norm = q_norm, k_norm
+        self.lens = [0] * batch
+
+    def step(self, x, counts, u, temperature=None, top_k=None, top_p=None, min_p=None, stream=None):
+        """x (sum of counts, D) bf16: counts[b] new tokens of each sequence in turn (at least one); u (batch).
+        Returns (tokens (batch), y (sum of counts, D) float32: the attention block's output)."""
+        device, N = x.device, self.N
+        lens = [n + c for n, c in zip(self.lens, counts)]
+        if len(counts) != self.batch or min(counts) < 1 or max(lens) > self.capacity:
+            raise ValueError("every sequence needs at least one new token and room for them")
+        pos = np.concatenate([np.arange(n - c, n) for n, c in zip(lens, counts)]).astype(np.int32)
+        seq = np.repeat(np.arange(self.batch), counts)
+        cu = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+        positions, at = torch.from_numpy(pos).to(device), torch.from_numpy(seq).to(device)
+        slots = self.block_table[at, positions.long() // self.page].long() * self.page + positions % self.page
+        seq_lens = torch.tensor(lens, dtype=torch.int32, device=device)
+        qkv = tp_all_to_sharded(x, self.w_qkv, self.b_qkv, stream=stream)
+        q = tp_qkv_append(qkv, self.k_cache, self.v_cache, slots, positions=positions, rope=self.rope,
+                          q_norm=self.q_norm, k_norm=self.k_norm, stream=stream)
+        if max(counts) == 1:
+            o = tp_paged_decode(q, self.k_cache, self.v_cache, self.block_table, seq_lens, stream=stream)
+        else:
+            o = tp_paged_prefill(q, self.k_cache, self.v_cache, self.block_table, torch.from_numpy(cu).to(device),
+                                 seq_lens, stream=stream)
+        y = tp_sharded_to_all(list(o), self.w_o, self.b_o, stream=stream)
+        last = y[torch.from_numpy(cu[1:].astype(np.int64) - 1).to(device)].to(torch.bfloat16)
+        logits = torch.empty((self.batch, self.V), dtype=torch.float32, device=device)
+        Vn = self.V // N
+        tp_all_to_sharded(last, self.w_lm, None, out=[logits[:, r * Vn:(r + 1) * Vn] for r in range(N)], stream=stream)
+        tokens, self.logprobs = tp_sample(logits, u, temperature, top_k, top_p, min_p, stream=stream)
+        self.lens, self.logits = lens, logits
+        return tokens, y
 
 
 class Q4Pair:

@@ -12,8 +12,12 @@ import numpy as np
 import pytest
 import torch
 
+import oracle
 import sharded_gemm_gb300 as tp
 from sharded_gemm_gb300 import build as tpbuild
+from sharded_gemm_gb300 import synth
+from sharded_gemm_gb300.workloads import PagedServing, to_device, to_host
+from gpu_util import check_close
 
 pytestmark = pytest.mark.gpu
 
@@ -497,6 +501,38 @@ def test_sample(B, V, dt):
         assert abs(lp[b] - ref) <= 1e-5 * (1 + abs(ref))
 
 
+@pytest.mark.parametrize("B,V", [(200, 300), (1500, 77), (170, 60000)])
+def test_sample_more_rows_than_the_gpu_holds(B, V):
+    """Rows are then taken in another order: each must still get its own parameters and place."""
+    rng = np.random.default_rng(B)
+    x = torch.from_numpy(rng.standard_normal((B, V)).astype(np.float32) * 2).cuda()
+    u = rng.random(B, dtype=np.float32)
+    t = rng.choice(np.float32([0, 0.7, 1, 1.5]), B).astype(np.float32)
+    k = rng.choice([0, 1, 20, 300, 5000], B).astype(np.int32)
+    p = rng.choice(np.float32([1, 0.3, 0.9, 0.999]), B).astype(np.float32)
+    m = rng.choice(np.float32([0, 0.01]), B).astype(np.float32)
+    tok, _ = tp.tp_sample(x, *[torch.from_numpy(a).cuda() for a in (u, t, k, p, m)])
+    status_ok()
+    xh, tok = x.double().cpu().numpy(), tok.cpu().numpy()
+    for b in range(B):
+        check_draw(xh[b], int(tok[b]), float(t[b]), int(k[b]), float(p[b]), float(m[b]), float(u[b]))
+
+
+@pytest.mark.parametrize("t", [1e-5, 1e-2, 100.0, 1e30, float("inf")])
+def test_sample_extreme_temperatures(t):
+    """Narrow and flat distributions: top-p ends among few values, or among all of a flat row."""
+    B, V = 4, 40000
+    x = torch.randn((B, V), device="cuda") * 3
+    u = torch.tensor([0.0, 0.3, 0.6, 0.95], device="cuda")
+    p = torch.tensor([0.9, 0.5, 1.0, 0.99], device="cuda")
+    k = torch.tensor([0, 0, 3000, 1500], dtype=torch.int32, device="cuda")
+    tok, _ = tp.tp_sample(x, u, temperature=torch.full((B,), t, device="cuda"), top_k=k, top_p=p)
+    status_ok()
+    for b in range(B):
+        # near a flat row's cut, weights of 2^-24 steps decide: allow what float32 exponentials can differ by
+        check_draw(x[b].double().cpu().numpy(), int(tok[b]), t, int(k[b]), float(p[b]), 0.0, float(u[b]), slack=2e-4)
+
+
 def test_sample_defaults_and_repeat():
     x = torch.randn((33, 777), device="cuda")
     u = torch.rand(33, device="cuda")
@@ -640,3 +676,62 @@ def test_prepared_calls_of_every_entry_point():
     for got, want in zip(call(), tp.tp_sample(logits, u, temperature=u + 0.5, min_p=u * 0.1)):
         assert torch.equal(got, want)
     status_ok()
+
+
+# ------------------------------------------------------------------ together
+def bf16(a):
+    return torch.from_numpy(np.asarray(a, np.float32)).to(BF).double().numpy()
+
+
+def test_serving_steps_against_float64():
+    """Prompts, then decode steps, through the linears, the cache and the draw."""
+    N, D, heads, V = 4, 512, 8, 1000
+    cfg = synth.qkv(seed=9, T=1, D=D, V=V, N=N, bias_std=0.1)
+    gains = [torch.rand(D // heads, device="cuda") + 0.5 for _ in range(2)]
+    serve = PagedServing(cfg, heads, batch=3, capacity=90, page=16, q_norm=gains[0], k_norm=gains[1])
+    w = {n: oracle.bf16_to_f64(cfg[n]) for n in ("w_qkv", "w_o", "w_lm")}
+    rng = np.random.default_rng(2)
+    hd = D // heads
+    past = [[np.zeros((0, heads, hd))] * 2 for _ in range(3)]
+    ang = np.arange(90)[:, None] * 10000.0 ** (-np.arange(hd // 2) * 2.0 / hd)
+    for counts in ([40, 1, 23], [1, 1, 1], [1, 1, 1], [5, 30, 1], [1, 1, 1]):
+        x = to_device(synth.f32_to_bf16_bits(rng.standard_normal((sum(counts), D)).astype(np.float32)), "bf16")
+        u = torch.from_numpy(rng.random(3, dtype=np.float32)).cuda()
+        tokens, y = serve.step(x, counts, u, temperature=torch.full((3,), 0.8, device="cuda"),
+                               top_k=torch.tensor([50, 0, 1], dtype=torch.int32, device="cuda"))
+        status_ok()
+        qkv = bf16(oracle.linear(to_host(x), w["w_qkv"], cfg["b_qkv"])).reshape(-1, 3, heads, hd)
+        out, t0 = [], 0
+        for b, c in enumerate(counts):
+            n = len(past[b][0])
+            cs, sn = np.cos(ang[n:n + c, None]), np.sin(ang[n:n + c, None])
+            qk = []
+            for i in range(2):
+                z = qkv[t0:t0 + c, i]
+                z = z / np.sqrt((z * z).mean(-1, keepdims=True) + 1e-6) * to_host(gains[i])
+                a, d = z[..., :hd // 2], z[..., hd // 2:]
+                qk.append(bf16(np.concatenate([a * cs - d * sn, d * cs + a * sn], -1)))
+            past[b] = [np.concatenate([past[b][0], qk[1]]), np.concatenate([past[b][1], qkv[t0:t0 + c, 2]])]
+            s = np.einsum("ihd,jhd->hij", qk[0], past[b][0]) / np.sqrt(hd)
+            s[:, np.arange(n + c)[None] > n + np.arange(c)[:, None]] = -np.inf
+            p = np.exp(s - s.max(-1, keepdims=True))
+            o = np.einsum("hij,jhd->ihd", p / p.sum(-1, keepdims=True), past[b][1])
+            out.append(bf16(o).reshape(c, D))
+            t0 += c
+        ref = oracle.linear(np.concatenate(out), w["w_o"], cfg["b_o"])
+        check_close(to_host(y), ref, "attention block")
+        last = to_host(y[torch.from_numpy(np.cumsum(counts) - 1).cuda()].to(BF))
+        logits = oracle.linear(last, w["w_lm"], None)
+        check_close(to_host(serve.logits), logits, "logits")
+        for b in range(3):
+            check_draw(to_host(serve.logits)[b], int(tokens[b]), float(np.float32(0.8)), [50, 0, 1][b], 1.0, 0.0, float(u[b]))
+
+
+def test_serving_step_refusals():
+    cfg = synth.qkv(seed=9, T=1, D=128, V=64, N=2)
+    serve = PagedServing(cfg, 2, batch=2, capacity=20, page=16)
+    x = torch.zeros((4, 128), dtype=BF, device="cuda")
+    u = torch.zeros(2, device="cuda")
+    for counts in ([4], [4, 0], [1, 21]):
+        with pytest.raises(ValueError):
+            serve.step(x, counts, u)
