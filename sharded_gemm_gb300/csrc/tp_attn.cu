@@ -59,7 +59,8 @@ int attn_args(AttnArgs &a, int N, const void *const *q, int64_t T, int64_t ldq, 
               const int32_t *block_table, int64_t B, int64_t width, int64_t ld_table, const int32_t *seq_lens,
               float scale, float softcap, int window, tp_dtype dt, void *const *o, int64_t ldo) {
   if (int rc = check_cache(N, Hq, Hk, D, pages, page, ld_page, dt, k_cache, v_cache)) return rc;
-  if (T < 0 || B < 0 || width < 0) return set_error(TP_ERR_INVALID_ARG, "need T, B, width >= 0");
+  if (T < 0 || B < 0 || width < 0 || T > 0x7fffffff || B > 0x7fffffff || width > 0x7fffffff)
+    return set_error(TP_ERR_INVALID_ARG, "T, B and width must be in 0..2^31 - 1");
   if (!(scale > 0.0f) || scale > 3.0e38f) return set_error(TP_ERR_INVALID_ARG, "scale must be positive and finite");
   if (!(softcap >= 0.0f) || softcap > 3.0e38f)
     return set_error(TP_ERR_INVALID_ARG, "softcap must be finite and >= 0 (0: none)");
@@ -99,7 +100,7 @@ int tp_qkv_append(int N, const void *const *qkv, int64_t T, int64_t ld, tp_dtype
                   int64_t ldq, void *const *k_cache, void *const *v_cache, int64_t pages, int page, int64_t ld_page,
                   tp_dtype dt, tp_stream_t stream) {
   if (int rc = check_cache(N, Hq, Hk, D, pages, page, ld_page, dt, k_cache, v_cache)) return rc;
-  if (T < 0) return set_error(TP_ERR_INVALID_ARG, "need T >= 0");
+  if (T < 0 || T > 0x7fffffff) return set_error(TP_ERR_INVALID_ARG, "T must be in 0..2^31 - 1");
   if (in_dt != TP_F32 && !is16(in_dt)) return set_error(TP_ERR_INVALID_ARG, "bad dtype");
   if (!(eps >= 0.0f)) return set_error(TP_ERR_INVALID_ARG, "eps must be >= 0");
   if (rope) {
