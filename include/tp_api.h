@@ -597,7 +597,8 @@ int tp_q4_sharded_to_all_noalloc(int N, const void *const *x, int64_t T, int64_t
  *   all); min_p drops those with e_i < min(min_p, 1).  The token is the lowest
  *   index at which the running weight of the kept, in index order, is above
  *   part(their total, u).  part(W, f) = floor(W * floor(f * 2^24) / 2^24), u
- *   taken into [0, 1).  Temperatures below 2^-20 take the largest logit.
+ *   taken into [0, 1).  Temperatures below 2^-20 take the largest logit, an
+ *   infinite one counts as the largest float.
  *   tokens int64 (B); logprobs NULL or float32 (B): the token's log-probability
  *   under the row's own softmax (temperature 1, unfiltered).  A row without a
  *   logit above -inf gives token -1 and -inf.

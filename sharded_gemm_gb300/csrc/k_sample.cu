@@ -31,6 +31,9 @@ __device__ __forceinline__ float logit(const T *p, int64_t i) {
   return isnan(x) ? -INFINITY : fminf(x, 3.402823466e38f) + 0.0f;  // + 0: one zero
 }
 
+// An infinite temperature as the largest finite one: times 0, a -inf would be NaN.
+__device__ __forceinline__ float finite(float t) { return t > 3.402823466e38f ? 3.402823466e38f : t; }
+
 // Larger x, larger key.
 __device__ __forceinline__ uint32_t order_key(float x) {
   const uint32_t b = __float_as_uint(x);
@@ -72,20 +75,22 @@ __device__ unsigned long long block_sum(unsigned long long v, unsigned long long
 //   top-k: 2048 bins over x count the largest of the threads' runs (of quarters
 //     of them for a large k): the bins in which k of those lie hold at least k
 //     elements, and not many more.
-//   top-p: the exact weights above six values are summed in registers, in the
-//     pass that sums the whole row; then again above six values between the two
+//   top-p: the exact weights above seven values are summed in registers, in the
+//     pass that sums the whole row; then again above seven values between the two
 //     that hold the end, over the few elements there (a mask of the run's).
 // (Adding every weight to bins in shared memory took 25 us a row: an addition
 // costs a lane about two cycles of the SM.)
 //
 // What bounds it is arithmetic: about 25 instructions an element for a pass with
-// exact weights (a row needs one, or none for top-k), 20 for the six values.
+// exact weights (a row needs one, or none for top-k), 20 for the seven values.
 
 constexpr int kBins = 2048, kList = 2048;
 constexpr float kBinScale = 64.0f;  // 1/64 of a logit wide, from the largest down
-constexpr int kMarks = 6;  // values above which weights are summed; first kMarkStep, 2 kMarkStep, .. below the largest,
-constexpr float kMarkStep = 2.0f;  // in units of the temperature
+constexpr int kMarks = 7;  // values above which weights are summed; the first so far below the largest, in temperatures:
+// where top-p of 0.5 to 0.999 ends on rows of 50272 normal logits, closer together where most end
+__device__ constexpr float kMarkAt[kMarks] = {2.0f, 4.0f, 6.0f, 8.0f, 10.0f, 12.5f, 16.0f};
 constexpr float kNoWeight = 28.0f;  // so far below the largest a weight is 0
+constexpr int kSpread = 1536; // a list this long leaves room for 1024 bins beside it
 constexpr int kRanked = 512;  // a list this long is put in order by counting, each element against all
 constexpr int kFew = 256;     // and one for which another round of narrowing does not pay
 constexpr int kMaxRun = 51;   // 51 * 1024 floats and RowShared fill a CTA's shared memory; and bits of a mask
@@ -423,8 +428,9 @@ struct Row {
     sync();
   }
 
-  // Puts rank 0's list in order, the largest first.
-  __device__ __forceinline__ void order_list(int n) {
+  // Puts rank 0's list in order, the largest first.  `reach`: no element is
+  // further below the row's largest than this (infinity: not known).
+  __device__ __forceinline__ void order_list(int n, float reach) {
     const int tid = threadIdx.x;
     if (n <= kRanked) {
       const u64 q = tid < n ? sh.list[tid] : 0;
@@ -435,6 +441,50 @@ struct Row {
       }
       __syncthreads();
       if (tid < n) sh.list[place] = q;
+      __syncthreads();
+      return;
+    }
+    if (n <= kSpread && reach < INFINITY) {
+      // 1024 bins over the reach, elements to their bins, then each among its bin's few
+      uint32_t *bins = reinterpret_cast<uint32_t *>(sh.list + kSpread);
+      const float scale = kThreads / reach;
+      auto bin = [&](u64 q) {
+        const int b = __float2int_rz((top - x_of_key((uint32_t)(q >> 32))) * scale);
+        return b < kThreads - 1 ? b : kThreads - 1;
+      };
+      bins[tid] = 0;
+      __syncthreads();
+      u64 q[2];
+      int b[2], place[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        q[i] = tid + i * kThreads < n ? sh.list[tid + i * kThreads] : 0;
+        b[i] = bin(q[i]);
+        place[i] = 0;
+        if (q[i]) place[i] = atomicAdd(&bins[b[i]], 1u);
+      }
+      __syncthreads();
+      u64 all;
+      const uint32_t mine = bins[tid], before = (uint32_t)scan_before(mine, all);
+      par ^= 1;  // as on the other CTAs
+      __syncthreads();
+      bins[tid] = before << 16 | (before + mine);
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (q[i]) sh.list[(bins[b[i]] >> 16) + place[i]] = q[i];
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int lo = bins[b[i]] >> 16, hi = bins[b[i]] & 0xffff;
+        place[i] = lo;
+        if (q[i])
+          for (int j = lo; j < hi; ++j) place[i] += sh.list[j] > q[i];
+      }
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (q[i]) sh.list[place[i]] = q[i];
       __syncthreads();
       return;
     }
@@ -460,11 +510,11 @@ struct Row {
   // weight, p_share), and where all that is kept is on the list, few enough, the
   // token is drawn from it at once (drawn).
   __device__ __forceinline__ Cut resolve(int n, u64 place0, u64 above, u64 k, bool by_p, u64 want, bool whole = false,
-                                         u64 p_share = 0) {
+                                         u64 p_share = 0, float reach = INFINITY) {
     if (rank == 0) {
       const int tid = threadIdx.x;
       __syncthreads();
-      order_list(n);
+      order_list(n, reach);
       u64 q[2], w[2];
       float e[2];
       bool in[2];
@@ -604,7 +654,8 @@ struct Row {
       clear_list();
       gather(mask);
       const bool whole = over == 0;
-      cut = resolve((int)n, over, 0, k, by_p && whole, 0, whole, p_share);
+      const float reach = whole && limit < kBins - 1 ? (limit + 1) / kBinScale : INFINITY;
+      cut = resolve((int)n, over, 0, k, by_p && whole, 0, whole, p_share, reach);
       if (drawn || (by_p && whole)) return cut;
     } else {
       u64 lo, hi;
@@ -654,7 +705,7 @@ struct Row {
     unused = 0;
     reduce(n, unused);
     while (n > kFew && n < was) {
-      // the weights above six values between low and high
+      // the weights above kMarks values between low and high
       const float from_x = low > floor_x ? low : floor_x, step = (high - from_x) * (1.0f / (kMarks + 1));
       MarkSums m;
 #pragma unroll
@@ -735,7 +786,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int64_t left = a.V - (int64_t)rank * slice;
   const int n = left < 0 ? 0 : left < slice ? (int)left : slice;
 
-  const float t = a.temperature ? a.temperature[b] : 1.0f, u = a.u[b];
+  const float t = a.temperature ? finite(a.temperature[b]) : 1.0f, u = a.u[b];
   const bool greedy = !(t >= 9.5367431640625e-7f);
   long long k = greedy ? 1 : (a.top_k ? a.top_k[b] : 0);
   if (k <= 0 || k > a.V) k = a.V;
@@ -791,7 +842,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool by_k = k < a.V || k == 1, free_draw = !by_k && !by_p;
   float z = 0.0f;
   WeightSum sum;   // what is kept of the run, where that is known
-  MarkSums marks;  // top-p alone: the run's weight, and above six values
+  MarkSums marks;  // top-p alone: the run's weight, and above kMarks values
   // (where the temperature is 1, z's terms are the weights' own)
   const bool own = row.inv_t == 1.0f;
   auto z_of = [&](float v) {
@@ -808,7 +859,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (!by_k) {
 #pragma unroll
-    for (int i = 0; i < kMarks; ++i) marks.mark[i] = top - (i + 1) * kMarkStep * t;
+    for (int i = 0; i < kMarks; ++i) marks.mark[i] = top - kMarkAt[i] * t;
 #pragma unroll 2
     for (int j = 0; j < R; ++j) {
       const float v = row.run[j], e = row.e_of(v);
@@ -887,9 +938,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     return cut.keeps(v, row.index0 + j) && !(e < min_p) ? e : 0.0f;
   };
   if (!summed) {
+    // what may be kept: from the cut up, and nothing clearly below min_p's value (its
+    // logarithm, with a margin above the error of the exponential and of this line)
+    float from = cut.x;
+    if (min_p > 0.0f) from = fmaxf(from, top + (logf(min_p) - 1e-3f) * t - 1e-5f * fabsf(top));
     sum = WeightSum();
-#pragma unroll 4
-    for (int j = 0; j < R; ++j) sum.add(kept_e(j));
+    for_each(mask_of(R, [&](int j) { return row.run[j] >= from; }),
+             [&](int j, bool valid) { sum.add(valid ? kept_e(j) : 0.0f); });
     mine = sum.total();
   }
   u64 block, total, before = row.scan_before(mine, block), lower;
@@ -971,7 +1026,7 @@ __global__ void __launch_bounds__(kThreads) sample_wide_kernel(const __grid_cons
 #pragma unroll
   for (int m = 16; m > 0; m /= 2) z += __shfl_xor_sync(0xffffffffu, z, m);
 
-  const float t = a.temperature ? a.temperature[b] : 1.0f;
+  const float t = a.temperature ? finite(a.temperature[b]) : 1.0f;
   const bool greedy = !(t >= 9.5367431640625e-7f);
   const float inv_t = greedy ? 1.0f : 1.0f / t;
   long long k = greedy ? 1 : (a.top_k ? a.top_k[b] : 0);

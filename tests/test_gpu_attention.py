@@ -598,6 +598,46 @@ def test_sample_masked_and_special_logits():
     assert tok[1] == tok[2] == V - 1 or tok[1] > V - 50
 
 
+def draw_by_definition(x, u, t, k, p, m):
+    """The tokens in whole numbers, from float32 exponentials: every sum exact, the row sorted."""
+    x = x.float()
+    V = x.shape[1]
+    x = torch.where(torch.isnan(x), -float("inf"), x).clamp(max=torch.finfo(torch.float32).max) + 0.0
+    part = lambda total, share: (total >> 24) * share + (((total & 0xFFFFFF) * share) >> 24)  # noqa: E731
+    greedy = t[:, None] < 2.0 ** -20
+    e = torch.exp((x - x.amax(1, keepdim=True)) * torch.where(greedy, 1.0, 1.0 / t[:, None]))
+    w = (e * 2.0 ** 40).long()
+    order = torch.sort(x, dim=1, descending=True, stable=True)[1]
+    rank = torch.arange(V, device=x.device)
+    kk = torch.where(greedy, 1, torch.where((k[:, None] <= 0) | (k[:, None] > V), V, k[:, None]))
+    ws = torch.where(rank < kk, w.gather(1, order), 0)
+    cut = part(ws.sum(1, keepdim=True), (p[:, None] * 2.0 ** 24).long())
+    keep = (rank < kk) & ((p[:, None] >= 1) | (ws.cumsum(1) - ws < cut) | (rank == 0))
+    keep = torch.zeros_like(keep).scatter(1, order, keep) & (e >= m[:, None].clamp(max=1))
+    run = torch.where(keep, w, 0).cumsum(1)
+    return (run <= part(run[:, -1:], (u[:, None] * 2.0 ** 24).long())).sum(1)
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_sample_equals_its_definition(seed):
+    rng = np.random.default_rng(seed)
+    V = int(rng.choice([3, 100, 1024, 5000, 50272, 60000, 130000]))
+    B = int(rng.choice([1, 7, 40, 200]))
+    dt = [torch.float32, torch.bfloat16, torch.float16][seed % 3]
+    x = torch.from_numpy(rng.standard_normal((B, V)).astype(np.float32) * rng.choice([0.01, 0.5, 3, 20])).cuda().to(dt)
+    if seed % 4 == 1:
+        x = (x.float() * 2).round().div(2).to(dt)  # many equal logits
+    if seed % 5 == 2:
+        x[:, ::3] = -float("inf")
+    par = [rng.random(B, dtype=np.float32), rng.choice(np.float32([0, 1e-5, 0.5, 1, 1.3, 100]), B),
+           rng.choice([0, 0, 1, 3, 50, 600, 1500, 3000, 20000], B).astype(np.int32),
+           rng.choice(np.float32([1, 1, 0.5, 0.9, 0.999, 0.9999999]), B), rng.choice(np.float32([0, 0, 0.01, 0.5]), B)]
+    par = [torch.from_numpy(np.ascontiguousarray(a)).cuda() for a in par]
+    tok, _ = tp.tp_sample(x, *par)
+    status_ok()
+    assert torch.equal(tok, draw_by_definition(x, *par))
+
+
 def test_sample_distribution():
     """20000 draws of one row: each share within five standard deviations of its probability."""
     V, n = 12, 20000
