@@ -21,6 +21,11 @@
 //                       next token's heads, cosines and sines on their way into
 //                       shared memory meanwhile (each lane copies its own
 //                       pieces, so nothing is shared and no barrier is needed).
+// Measured: 16384 tokens of 8 ranks x 12 heads of 128, bfloat16, normed and turned,
+// 162 us (5.0 TB/s, 74% of the copy rate); with every head loaded in one piece and
+// the rotation's partners shuffled, 270; one head a group 356.  One token 2.0 us.
+// The ring starts where every resident block has two rounds: with fewer the
+// first form's blocks are all resident at once and its loads overlap as well.
 #include "attn.cuh"
 #include "mma16.cuh"
 #include "ptx.cuh"

