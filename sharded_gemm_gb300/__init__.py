@@ -777,7 +777,9 @@ def tp_mx_sharded_to_all(x, codes, scales, bias=None, out=None, out_dtype=None, 
 # ------------------------------------------------------------------ attention side
 # A per-rank argument is a list of N tensors, or one tensor whose first
 # dimension is the ranks (rank r is its slice [r]).  The tensors are checked and
-# turned into the C ABI's arguments by csrc/marshal.c (see there why not here).
+# turned into the C ABI's arguments by csrc/marshal.c (see there why not here),
+# which also allocates the outputs that are not given: on the current stream, as
+# everywhere in this module, so a caller that names another `stream` orders the two.
 _native = None  # the extension module, once loaded
 
 
@@ -789,7 +791,8 @@ def _marshaller():
         from . import _marshal as m
         torch = _torch()
         m.init(torch.float32, torch.bfloat16, torch.float16, torch.int32, torch.int64,
-               getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream))
+               getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream),
+               torch.empty)
         _native = m
     return _native
 
@@ -797,18 +800,23 @@ def _marshaller():
 _addresses = {}
 
 
+def _address(name):
+    fn = _addresses[name] = ctypes.cast(getattr(lib(), name), ctypes.c_void_p).value
+    return fn
+
+
 def _call(name, marshal, *args):
-    """Marshals `args` and calls the library's function `name` (or has prepare() record the call)."""
+    """Marshals `args`, calls the library's function `name` (or has prepare() record the call) and returns the
+    outputs."""
     rec = getattr(_rec, "active", None)
     if rec is not None:
-        _check(getattr(rec, name)(*marshal(0, *args)))
-        return
-    fn = _addresses.get(name)
-    if fn is None:
-        fn = _addresses[name] = ctypes.cast(getattr(lib(), name), ctypes.c_void_p).value
-    rc = marshal(fn, *args)
-    if rc != TP_OK:
-        _check(rc)
+        out, cargs = marshal(0, *args)
+        _check(getattr(rec, name)(*cargs))
+        return out
+    out = marshal(_addresses.get(name) or _address(name), *args)
+    if out.__class__ is int:
+        _check(out)
+    return out
 
 
 def tp_qkv_append(qkv, k_cache, v_cache, slots, positions=None, rope=None, q_norm=None, k_norm=None, eps: float = 1e-6,
@@ -818,23 +826,8 @@ def tp_qkv_append(qkv, k_cache, v_cache, slots, positions=None, rope=None, q_nor
     caches (per rank (pages, Hk, page, D)) at ``slots``; returns the queries,
     per rank (T, Hq D) in the cache's dtype (one (N, T, Hq D) tensor unless
     ``out`` is given)."""
-    if out is None:
-        x, k = (t[0] if isinstance(t, (list, tuple)) else t for t in (qkv, k_cache))
-        T, cols = x.shape[-2:]
-        Hk, _, D = k.shape[-3:]
-        if cols <= 2 * Hk * D:
-            raise ValueError("qkv holds no query heads besides 2 * %d key and value heads" % Hk)
-        out = _torch().empty((len(qkv), T, cols - 2 * Hk * D), dtype=k.dtype, device=k.device)
-    _call("tp_qkv_append", (_native or _marshaller()).append, qkv, k_cache, v_cache, slots, positions, rope, q_norm,
-          k_norm, eps, interleaved, out, stream)
-    return out
-
-
-def _like(q):
-    """An output for per-rank queries: one tensor, the ranks first."""
-    if isinstance(q, (list, tuple)):
-        return q[0].new_empty((len(q),) + tuple(q[0].shape))
-    return _torch().empty_like(q)
+    return _call("tp_qkv_append", (_native or _marshaller()).append, qkv, k_cache, v_cache, slots, positions, rope,
+                 q_norm, k_norm, eps, interleaved, out, stream)
 
 
 def tp_paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale=None, softcap: float = 0.0, window: int = 0,
@@ -842,11 +835,8 @@ def tp_paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale=None, soft
     """Attention of one new token per sequence over the paged caches: q per rank
     (B, Hq D), seq_lens (B) counts the new token.  Returns o, per rank
     (B, Hq D) (one (N, B, Hq D) tensor unless ``out`` is given)."""
-    if out is None:
-        out = _like(q)
-    _call("tp_paged_decode", (_native or _marshaller()).decode, q, k_cache, v_cache, block_table, seq_lens, scale,
-          softcap, window, out, stream)
-    return out
+    return _call("tp_paged_decode", (_native or _marshaller()).decode, q, k_cache, v_cache, block_table, seq_lens,
+                 scale, softcap, window, out, stream)
 
 
 def tp_paged_prefill(q, k_cache, v_cache, block_table, cu_seqlens, seq_lens, prefix_lens=None, scale=None,
@@ -854,22 +844,13 @@ def tp_paged_prefill(q, k_cache, v_cache, block_table, cu_seqlens, seq_lens, pre
     """Causal attention of ragged chunks over the paged caches: rows
     cu_seqlens[b] .. cu_seqlens[b + 1] - 1 of q are the last positions of
     sequence b.  Returns o as tp_paged_decode."""
-    if out is None:
-        out = _like(q)
-    _call("tp_paged_prefill", (_native or _marshaller()).prefill, q, k_cache, v_cache, block_table, cu_seqlens,
-          seq_lens, prefix_lens, scale, softcap, window, out, stream)
-    return out
+    return _call("tp_paged_prefill", (_native or _marshaller()).prefill, q, k_cache, v_cache, block_table, cu_seqlens,
+                 seq_lens, prefix_lens, scale, softcap, window, out, stream)
 
 
 def tp_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, tokens=None, logprobs=None,
               stream=None):
     """Draws one token per row of ``logits`` (B, V) with the given uniform
     numbers ``u`` (B); returns (tokens int64 (B), logprobs float32 (B))."""
-    torch = _torch()
-    if tokens is None:
-        tokens = torch.empty((logits.shape[0],), dtype=torch.int64, device=logits.device)
-    if logprobs is None:
-        logprobs = torch.empty((logits.shape[0],), dtype=torch.float32, device=logits.device)
-    _call("tp_sample", (_native or _marshaller()).sample, logits, u, temperature, top_k, top_p, min_p, tokens, logprobs,
-          stream)
-    return tokens, logprobs
+    return _call("tp_sample", (_native or _marshaller()).sample, logits, u, temperature, top_k, top_p, min_p, tokens,
+                 logprobs, stream)

@@ -5,9 +5,10 @@
  * a decode step.  Marshalled in Python one took about 20 us; here it takes about
  * as long as the launch.  Nothing is kept between calls.
  *
- * Every function takes the library function's address first.  With 0 it calls
- * nothing and returns the tuple of arguments that it would have passed (pointer
- * arrays as bytes), for prepare(). */
+ * Every function takes the library function's address first and allocates the
+ * outputs that are None.  It returns them, or the library's error code as an int.
+ * With address 0 it calls nothing and returns (outputs, the tuple of arguments
+ * that it would have passed, pointer arrays as bytes), for prepare(). */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 #include <stdint.h>
@@ -18,7 +19,8 @@
 
 static PyObject *s_shape, *s_stride, *s_dtype, *s_get_device, *s_data_ptr, *s_cuda_stream;
 /* set by init() */
-static PyObject *t_f32, *t_bf16, *t_f16, *t_i32, *t_i64, *raw_stream;
+static PyObject *t_f32, *t_bf16, *t_f16, *t_i32, *t_i64, *raw_stream, *torch_empty;
+static PyObject *empty_names; /* ("dtype", "device") */
 
 static int dtype_code(PyObject *dtype) {
   return dtype == t_bf16 ? TP_BF16 : dtype == t_f16 ? TP_F16 : dtype == t_f32 ? TP_F32 : -1;
@@ -216,6 +218,47 @@ static int heads_of(int64_t cols, int D, int *heads, const char *name) {
   return 0;
 }
 
+/* torch.empty(shape, dtype=dtype, device=dev): a new reference. */
+static PyObject *new_tensor(int nd, const int64_t *shape, PyObject *dtype, long dev) {
+  PyObject *size = PyTuple_New(nd), *device = PyLong_FromLong(dev), *t = NULL;
+  int ok = size && device;
+  for (int d = 0; ok && d < nd; ++d) {
+    PyObject *n = PyLong_FromLongLong(shape[d]);
+    if (n) PyTuple_SET_ITEM(size, d, n);
+    else ok = 0;
+  }
+  if (ok) {
+    PyObject *args[3] = {size, dtype, device};
+    t = PyObject_Vectorcall(torch_empty, args, 1, empty_names);
+  }
+  Py_XDECREF(size);
+  Py_XDECREF(device);
+  return t;
+}
+/* The per-rank output `given`, or where it is None a new (n, rows, cols) tensor:
+ * a new reference in *keep, described in *o. */
+static int output_of(PyObject *given, int n, int64_t rows, int64_t cols, PyObject *dtype, long dev, PyObject **keep,
+                     Ranks *o) {
+  if (given == Py_None) {
+    const int64_t shape[3] = {n, rows, cols};
+    *keep = new_tensor(3, shape, dtype, dev);
+  } else {
+    *keep = Py_NewRef(given);
+  }
+  if (!*keep) return -1;
+  if (ranks_of(*keep, o, 2, "out")) {
+    Py_CLEAR(*keep);
+    return -1;
+  }
+  return 0;
+}
+/* What a function returns: its outputs (a new reference, taken), or the error code. */
+static PyObject *answer(PyObject *out, int rc) {
+  if (rc == TP_OK) return out;
+  Py_DECREF(out);
+  return PyLong_FromLong(rc);
+}
+
 static PyObject *bytes_of(const Ranks *o) {
   return PyBytes_FromStringAndSize((const char *)o->ptr, 8 * (o->n < MOST_RANKS ? o->n : MOST_RANKS));
 }
@@ -231,54 +274,62 @@ static PyObject *m_append(PyObject *self, PyObject *const *a, Py_ssize_t na) {
   Cache c;
   Ranks x, out;
   int64_t ld, ldq, rows = 0, rot = 0;
-  int H, Hq;
+  int H, Hq, inter, rc;
+  double eps;
   uint64_t slots, positions, rope = 0, qn, kn, stream;
-  if (cache_of(a[2], a[3], &c) || ranks_of(a[1], &x, 2, "qkv") || ranks_of(a[11], &out, 2, "out")) return NULL;
+  PyObject *keep = NULL;
+  if (cache_of(a[2], a[3], &c) || ranks_of(a[1], &x, 2, "qkv")) return NULL;
   if (x.n != c.k.n || x.dev != c.k.dev) {
     PyErr_SetString(PyExc_ValueError, "qkv and the caches need the same ranks on one device");
     return NULL;
   }
-  if (ld_of(&x, &ld, "qkv") || heads_of(x.shape[1], c.D, &H, "qkv") || ld_of(&out, &ldq, "out")) return NULL;
+  if (ld_of(&x, &ld, "qkv") || heads_of(x.shape[1], c.D, &H, "qkv")) return NULL;
   Hq = H - 2 * c.Hk;
   const int64_t T = x.shape[0];
+  if (Hq < 1)
+    return PyErr_Format(PyExc_ValueError, "qkv holds no query heads besides 2 * %d key and value heads", c.Hk);
+  if (output_of(a[11], c.k.n, T, (int64_t)Hq * c.D, c.k.dtype, c.k.dev, &keep, &out)) return NULL;
+  if (ld_of(&out, &ldq, "out")) goto fail;
   if (out.n != c.k.n || out.shape[0] != T || out.shape[1] != (int64_t)Hq * c.D || out.dtype != c.k.dtype ||
       out.dev != c.k.dev) {
     PyErr_SetString(PyExc_ValueError, "out must be (T, Hq * D) per rank in the cache's dtype");
-    return NULL;
+    goto fail;
   }
   if (a[6] != Py_None) {
     Info f;
-    if (info_of(a[6], &f, "rope")) return NULL;
+    if (info_of(a[6], &f, "rope")) goto fail;
     if (f.dtype != t_f32 || f.nd != 2 || f.dev != c.k.dev || (f.shape[1] > 1 && f.stride[1] != 1) ||
         (f.shape[0] > 1 && f.stride[0] != f.shape[1]) || f.shape[1] > 1 << 20) {
       PyErr_SetString(PyExc_ValueError,
                       "rope must be a contiguous float32 (positions, rope_dim) tensor on the caches' device");
-      return NULL;
+      goto fail;
     }
     if (a[5] == Py_None) {
       PyErr_SetString(PyExc_ValueError, "rope needs positions");
-      return NULL;
+      goto fail;
     }
     rope = f.ptr, rows = f.shape[0], rot = f.shape[1];
   }
-  const double eps = PyFloat_AsDouble(a[9]);
-  const int inter = PyObject_IsTrue(a[10]);
+  eps = PyFloat_AsDouble(a[9]);
+  inter = PyObject_IsTrue(a[10]);
   if (PyErr_Occurred() || param_of(a[4], &slots, t_i64, T, c.k.dev, "slots") ||
       param_of(a[5], &positions, t_i32, T, c.k.dev, "positions") ||
       param_of(a[7], &qn, t_f32, c.D, c.k.dev, "q_norm") || param_of(a[8], &kn, t_f32, c.D, c.k.dev, "k_norm") ||
       stream_of(a[12], c.k.dev, &stream))
-    return NULL;
+    goto fail;
   if (!fn)
-    return Py_BuildValue("iNLLiiiiKKdKLiiKKNLNNLiLiK", x.n, bytes_of(&x), T, ld, x.dt, Hq, c.Hk, c.D, qn, kn, eps, rope,
-                         rows, (int)rot, inter, positions, slots, bytes_of(&out), ldq, bytes_of(&c.k), bytes_of(&c.v),
-                         c.pages, c.page, c.ld, c.k.dt, stream);
-  int rc;
+    return Py_BuildValue("N(iNLLiiiiKKdKLiiKKNLNNLiLiK)", keep, x.n, bytes_of(&x), T, ld, x.dt, Hq, c.Hk, c.D, qn, kn,
+                         eps, rope, rows, (int)rot, inter, positions, slots, bytes_of(&out), ldq, bytes_of(&c.k),
+                         bytes_of(&c.v), c.pages, c.page, c.ld, c.k.dt, stream);
   Py_BEGIN_ALLOW_THREADS;
   rc = ((__typeof__(&tp_qkv_append))fn)(x.n, CA(x), T, ld, (tp_dtype)x.dt, Hq, c.Hk, c.D, P(qn), P(kn), (float)eps,
                                         P(rope), rows, (int)rot, inter, P(positions), P(slots), A(out), ldq, A(c.k),
                                         A(c.v), c.pages, c.page, c.ld, (tp_dtype)c.k.dt, P(stream));
   Py_END_ALLOW_THREADS;
-  return PyLong_FromLong(rc);
+  return answer(keep, rc);
+fail:
+  Py_XDECREF(keep);
+  return NULL;
 }
 
 /* What both attentions share. */
@@ -288,11 +339,14 @@ typedef struct {
   int64_t T, ldq, ldo, B, width, ldt;
   int Hq;
   uint64_t table;
+  PyObject *keep;
 } Attn;
 
+/* On success o->keep is a new reference to the output. */
 static int attn_of(PyObject *q, PyObject *k, PyObject *v, PyObject *table, PyObject *out, Attn *o) {
   Info f;
-  if (cache_of(k, v, &o->c) || ranks_of(q, &o->q, 2, "q") || ranks_of(out, &o->out, 2, "out")) return -1;
+  o->keep = NULL;
+  if (cache_of(k, v, &o->c) || ranks_of(q, &o->q, 2, "q")) return -1;
   if (o->q.n != o->c.k.n || o->q.dev != o->c.k.dev) {
     PyErr_SetString(PyExc_ValueError, "q and the caches need the same ranks on one device");
     return -1;
@@ -301,13 +355,7 @@ static int attn_of(PyObject *q, PyObject *k, PyObject *v, PyObject *table, PyObj
     PyErr_SetString(PyExc_TypeError, "q must have the caches' dtype");
     return -1;
   }
-  if (o->out.n != o->q.n || o->out.shape[0] != o->q.shape[0] || o->out.shape[1] != o->q.shape[1] ||
-      o->out.dtype != o->q.dtype || o->out.dev != o->q.dev) {
-    PyErr_SetString(PyExc_ValueError, "out must have q's shape per rank and its dtype");
-    return -1;
-  }
-  if (ld_of(&o->q, &o->ldq, "q") || ld_of(&o->out, &o->ldo, "out") ||
-      heads_of(o->q.shape[1], o->c.D, &o->Hq, "q") || info_of(table, &f, "block_table"))
+  if (ld_of(&o->q, &o->ldq, "q") || heads_of(o->q.shape[1], o->c.D, &o->Hq, "q") || info_of(table, &f, "block_table"))
     return -1;
   if (f.dtype != t_i32 || f.nd != 2 || f.dev != o->c.k.dev) {
     PyErr_SetString(PyExc_ValueError, "block_table must be a 2-D int32 tensor on the caches' device");
@@ -315,6 +363,17 @@ static int attn_of(PyObject *q, PyObject *k, PyObject *v, PyObject *table, PyObj
   }
   if (f.shape[1] > 1 && f.stride[1] != 1) {
     PyErr_SetString(PyExc_ValueError, "block_table must have unit column stride");
+    return -1;
+  }
+  if (output_of(out, o->q.n, o->q.shape[0], o->q.shape[1], o->q.dtype, o->q.dev, &o->keep, &o->out)) return -1;
+  if (o->out.n != o->q.n || o->out.shape[0] != o->q.shape[0] || o->out.shape[1] != o->q.shape[1] ||
+      o->out.dtype != o->q.dtype || o->out.dev != o->q.dev) {
+    PyErr_SetString(PyExc_ValueError, "out must have q's shape per rank and its dtype");
+    Py_CLEAR(o->keep);
+    return -1;
+  }
+  if (ld_of(&o->out, &o->ldo, "out")) {
+    Py_CLEAR(o->keep);
     return -1;
   }
   o->T = o->q.shape[0], o->B = f.shape[0], o->width = f.shape[1];
@@ -343,23 +402,26 @@ static PyObject *m_decode(PyObject *self, PyObject *const *a, Py_ssize_t na) {
   if (attn_of(a[1], a[2], a[3], a[4], a[9], &o)) return NULL;
   if (o.B != o.T) {
     PyErr_SetString(PyExc_ValueError, "block_table needs one row per sequence");
+    Py_DECREF(o.keep);
     return NULL;
   }
   if (param_of(a[5], &lens, t_i32, o.B, o.c.k.dev, "seq_lens") || scores_of(a + 6, o.c.D, &scale, &cap, &window) ||
-      stream_of(a[10], o.c.k.dev, &stream))
+      stream_of(a[10], o.c.k.dev, &stream)) {
+    Py_DECREF(o.keep);
     return NULL;
+  }
   const Cache *c = &o.c;
   if (!fn)
-    return Py_BuildValue("iNLLiiiNNLiLKLLKddiiNLK", o.q.n, bytes_of(&o.q), o.T, o.ldq, o.Hq, c->Hk, c->D, bytes_of(&c->k),
-                         bytes_of(&c->v), c->pages, c->page, c->ld, o.table, o.width, o.ldt, lens, scale, cap, window,
-                         c->k.dt, bytes_of(&o.out), o.ldo, stream);
+    return Py_BuildValue("N(iNLLiiiNNLiLKLLKddiiNLK)", o.keep, o.q.n, bytes_of(&o.q), o.T, o.ldq, o.Hq, c->Hk, c->D,
+                         bytes_of(&c->k), bytes_of(&c->v), c->pages, c->page, c->ld, o.table, o.width, o.ldt, lens,
+                         scale, cap, window, c->k.dt, bytes_of(&o.out), o.ldo, stream);
   int rc;
   Py_BEGIN_ALLOW_THREADS;
   rc = ((__typeof__(&tp_paged_decode))fn)(o.q.n, CA(o.q), o.T, o.ldq, o.Hq, c->Hk, c->D, A(c->k), A(c->v), c->pages,
                                           c->page, c->ld, P(o.table), o.width, o.ldt, P(lens), (float)scale, (float)cap,
                                           window, (tp_dtype)c->k.dt, A(o.out), o.ldo, P(stream));
   Py_END_ALLOW_THREADS;
-  return PyLong_FromLong(rc);
+  return answer(o.keep, rc);
 }
 
 /* prefill(fn, q, k_cache, v_cache, block_table, cu_seqlens, seq_lens, prefix_lens, scale, softcap, window, out, stream) */
@@ -374,11 +436,13 @@ static PyObject *m_prefill(PyObject *self, PyObject *const *a, Py_ssize_t na) {
   if (param_of(a[5], &cu, t_i32, o.B + 1, o.c.k.dev, "cu_seqlens") ||
       param_of(a[6], &lens, t_i32, o.B, o.c.k.dev, "seq_lens") ||
       param_of(a[7], &prefix, t_i32, o.B, o.c.k.dev, "prefix_lens") ||
-      scores_of(a + 8, o.c.D, &scale, &cap, &window) || stream_of(a[12], o.c.k.dev, &stream))
+      scores_of(a + 8, o.c.D, &scale, &cap, &window) || stream_of(a[12], o.c.k.dev, &stream)) {
+    Py_DECREF(o.keep);
     return NULL;
+  }
   const Cache *c = &o.c;
   if (!fn)
-    return Py_BuildValue("iNLLiiiNNLiLKLLLKKKddiiNLK", o.q.n, bytes_of(&o.q), o.T, o.ldq, o.Hq, c->Hk, c->D,
+    return Py_BuildValue("N(iNLLiiiNNLiLKLLLKKKddiiNLK)", o.keep, o.q.n, bytes_of(&o.q), o.T, o.ldq, o.Hq, c->Hk, c->D,
                          bytes_of(&c->k), bytes_of(&c->v), c->pages, c->page, c->ld, o.table, o.B, o.width, o.ldt, cu,
                          lens, prefix, scale, cap, window, c->k.dt, bytes_of(&o.out), o.ldo, stream);
   int rc;
@@ -388,10 +452,10 @@ static PyObject *m_prefill(PyObject *self, PyObject *const *a, Py_ssize_t na) {
                                            (float)scale, (float)cap, window, (tp_dtype)c->k.dt, A(o.out), o.ldo,
                                            P(stream));
   Py_END_ALLOW_THREADS;
-  return PyLong_FromLong(rc);
+  return answer(o.keep, rc);
 }
 
-/* sample(fn, logits, u, temperature, top_k, top_p, min_p, tokens, logprobs, stream) */
+/* sample(fn, logits, u, temperature, top_k, top_p, min_p, tokens, logprobs, stream) -> (tokens, logprobs) */
 static PyObject *m_sample(PyObject *self, PyObject *const *a, Py_ssize_t na) {
   if (na != 10) return PyErr_Format(PyExc_TypeError, "sample takes 10 arguments");
   void *fn = PyLong_AsVoidPtr(a[0]);
@@ -405,24 +469,34 @@ static PyObject *m_sample(PyObject *self, PyObject *const *a, Py_ssize_t na) {
   const int64_t B = f.shape[0], V = f.shape[1], ld = B > 1 ? f.stride[0] : V;
   if (param_of(a[2], &u, t_f32, B, f.dev, "u") || param_of(a[3], &t, t_f32, B, f.dev, "temperature") ||
       param_of(a[4], &k, t_i32, B, f.dev, "top_k") || param_of(a[5], &p, t_f32, B, f.dev, "top_p") ||
-      param_of(a[6], &m, t_f32, B, f.dev, "min_p") || param_of(a[7], &tokens, t_i64, B, f.dev, "tokens") ||
-      param_of(a[8], &logprobs, t_f32, B, f.dev, "logprobs") || stream_of(a[9], f.dev, &stream))
+      param_of(a[6], &m, t_f32, B, f.dev, "min_p") || stream_of(a[9], f.dev, &stream))
     return NULL;
+  PyObject *tk = a[7] == Py_None ? new_tensor(1, &B, t_i64, f.dev) : Py_NewRef(a[7]);
+  PyObject *lp = !tk ? NULL : a[8] == Py_None ? new_tensor(1, &B, t_f32, f.dev) : Py_NewRef(a[8]);
+  PyObject *out = lp ? PyTuple_Pack(2, tk, lp) : NULL;
+  Py_XDECREF(tk); /* the tuple keeps them */
+  Py_XDECREF(lp);
+  if (!out) return NULL;
+  if (param_of(PyTuple_GET_ITEM(out, 0), &tokens, t_i64, B, f.dev, "tokens") ||
+      param_of(PyTuple_GET_ITEM(out, 1), &logprobs, t_f32, B, f.dev, "logprobs")) {
+    Py_DECREF(out);
+    return NULL;
+  }
   if (!fn)
-    return Py_BuildValue("KLLLiKKKKKKKK", f.ptr, B, V, ld, dt, u, t, k, p, m, tokens, logprobs, stream);
+    return Py_BuildValue("N(KLLLiKKKKKKKK)", out, f.ptr, B, V, ld, dt, u, t, k, p, m, tokens, logprobs, stream);
   int rc;
   Py_BEGIN_ALLOW_THREADS;
   rc = ((__typeof__(&tp_sample))fn)(P(f.ptr), B, V, ld, (tp_dtype)dt, P(u), P(t), P(k), P(p), P(m), P(tokens),
                                     P(logprobs), P(stream));
   Py_END_ALLOW_THREADS;
-  return PyLong_FromLong(rc);
+  return answer(out, rc);
 }
 
-/* init(float32, bfloat16, float16, int32, int64, current raw stream of a device index) */
+/* init(float32, bfloat16, float16, int32, int64, current raw stream of a device index, torch.empty) */
 static PyObject *m_init(PyObject *self, PyObject *args) {
-  PyObject **to[6] = {&t_f32, &t_bf16, &t_f16, &t_i32, &t_i64, &raw_stream}, *v[6];
-  if (!PyArg_ParseTuple(args, "OOOOOO", &v[0], &v[1], &v[2], &v[3], &v[4], &v[5])) return NULL;
-  for (int i = 0; i < 6; ++i) Py_XSETREF(*to[i], Py_NewRef(v[i]));
+  PyObject **to[7] = {&t_f32, &t_bf16, &t_f16, &t_i32, &t_i64, &raw_stream, &torch_empty}, *v[7];
+  if (!PyArg_ParseTuple(args, "OOOOOOO", &v[0], &v[1], &v[2], &v[3], &v[4], &v[5], &v[6])) return NULL;
+  for (int i = 0; i < 7; ++i) Py_XSETREF(*to[i], Py_NewRef(v[i]));
   Py_RETURN_NONE;
 }
 
@@ -444,5 +518,6 @@ PyMODINIT_FUNC PyInit__marshal(void) {
     *names[i].to = PyUnicode_InternFromString(names[i].text);
     if (!*names[i].to) return NULL;
   }
-  return PyModule_Create(&module);
+  empty_names = Py_BuildValue("(ss)", "dtype", "device");
+  return empty_names ? PyModule_Create(&module) : NULL;
 }
