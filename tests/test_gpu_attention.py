@@ -460,8 +460,8 @@ def kept_set(x, t, k, p, m, slack):
 
     def cut(sign):
         keep = np.ones(n, bool) if p >= 1 else before < (p + sign * slack) * total
-        keep[0] = True
         keep &= e[:n] >= min(m, 1.0) * (1 - sign * slack)
+        keep[0] = True  # the largest is always kept
         return set(order[:n][keep].tolist())
     return cut(+1), cut(-1)
 
