@@ -78,24 +78,34 @@ __device__ unsigned long long block_sum(unsigned long long v, unsigned long long
 //   top-k: 2048 bins over x count the largest of the threads' runs (of quarters
 //     of them for a large k): the bins in which k of those lie hold at least k
 //     elements, and not many more.
-//   top-p: the exact weights above seven values are summed in registers, in the
-//     pass that sums the whole row; then again above seven values between the two
-//     that hold the end, over the few elements there (a mask of the run's).
+//   top-p: where it ends is guessed from the row's total as a float and bins that
+//     count 4096 of its elements; then one pass sums the exact weights of all and
+//     above two values around the guess.  They decide: where the end is not between
+//     the two, or too many elements are, weights are summed above seven values
+//     between the closest known ones, over the few elements there (a mask of the
+//     run's), until it is.  (A miss, about one row in 80, costs 7 us.  Seven fixed
+//     values in the first pass and then rounds of seven took 37 to 73 us a wave of
+//     152 rows; the guess takes 35 to 42.)
 // (Adding every weight to bins in shared memory took 25 us a row: an addition
 // costs a lane about two cycles of the SM.)
 //
-// What bounds it is arithmetic: about 25 instructions an element for a pass with
-// exact weights (a row needs one, or none for top-k), 20 for the seven values.
+// What bounds it is arithmetic and the joins: of a top-p row's 33 us, 5.5 are the
+// load, 3 the float pass, 4 the guess, 7 the exact pass (a logit takes 8 and 35
+// instructions), 4 the list, 3 its order, and the rest sums over the block, each a
+// barrier or two and 5 to 20 shuffles a warp.
 
 constexpr int kBins = 2048, kList = 2048;
 constexpr float kBinScale = 64.0f;  // 1/64 of a logit wide, from the largest down
-constexpr int kMarks = 7;  // values above which weights are summed; the first so far below the largest, in temperatures:
-// where top-p of 0.5 to 0.999 ends on rows of 50272 normal logits, closer together where most end
-__device__ constexpr float kMarkAt[kMarks] = {2.0f, 4.0f, 6.0f, 8.0f, 10.0f, 12.5f, 16.0f};
+constexpr int kMarks = 7;  // values above which weights are summed in a round of narrowing
 constexpr float kNoWeight = 28.0f;  // so far below the largest a weight is 0
 constexpr int kSpread = 1536; // a list this long leaves room for 1024 bins beside it
 constexpr int kRanked = 512;  // a list this long is put in order by counting, each element against all
 constexpr int kFew = 256;     // and one for which another round of narrowing does not pay
+// The end of top-p is guessed from 4096 elements, four of a run.  Counted in those the guess
+// is off by up to 15 in the mean square (rows of normal logits, p 0.5 to 0.999); the two
+// values around it are kOff away, 1200 elements of 50272 apart.
+constexpr int kSamples = 4;
+constexpr float kOff = 48.0f;
 constexpr int kMaxRun = 51;   // 51 * 1024 floats and RowShared fill a CTA's shared memory; and bits of a mask
 
 typedef unsigned long long u64;
@@ -206,21 +216,22 @@ __device__ __forceinline__ void for_each(Mask m, F f) {
   }
 }
 
-// Weights above kMarks values and of all (the last), as upper and lower 20 bits.
+// Weights above N values and of all (the last), as upper and lower 20 bits.
+template <int N>
 struct MarkSums {
-  float mark[kMarks];
-  uint32_t hi[kMarks + 1], lo[kMarks + 1];
+  float mark[N];
+  uint32_t hi[N + 1], lo[N + 1];
   __device__ __forceinline__ MarkSums() {
 #pragma unroll
-    for (int i = 0; i <= kMarks; ++i) hi[i] = lo[i] = 0;
+    for (int i = 0; i <= N; ++i) hi[i] = lo[i] = 0;
   }
   __device__ __forceinline__ void add(float v, float e) {
     WeightSum w;
     w.add(e);
     const uint32_t h = w.hi - 0x4B000000u, l = w.lo - 0x4B000000u;
-    hi[kMarks] += h, lo[kMarks] += l;
+    hi[N] += h, lo[N] += l;
 #pragma unroll
-    for (int i = 0; i < kMarks; ++i)  // the two additions under one predicate
+    for (int i = 0; i < N; ++i)  // the two additions under one predicate
       asm("{\n .reg .pred p;\n setp.gt.f32 p, %2, %3;\n @p add.u32 %0, %0, %4;\n @p add.u32 %1, %1, %5;\n}"
           : "+r"(hi[i]), "+r"(lo[i])
           : "f"(v), "f"(mark[i]), "r"(h), "r"(l));
@@ -300,17 +311,23 @@ struct Row {
     }
     par ^= 1;
   }
-  __device__ __forceinline__ uint32_t reduce_max(uint32_t v) {
+  // The largest (or with ADD the sum) of v over the cluster.
+  template <bool ADD>
+  static __device__ __forceinline__ uint32_t of_warp(uint32_t v) {
+    return ADD ? __reduce_add_sync(0xffffffffu, v) : __reduce_max_sync(0xffffffffu, v);
+  }
+  template <bool ADD>
+  __device__ __forceinline__ uint32_t reduce_u32(uint32_t v) {
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    v = __reduce_max_sync(0xffffffffu, v);
+    v = of_warp<ADD>(v);
     if (lane == 0) sh.warp_m[par][warp] = v;
     __syncthreads();
-    v = __reduce_max_sync(0xffffffffu, sh.warp_m[par][lane]);
+    v = of_warp<ADD>(sh.warp_m[par][lane]);
     if (C > 1) {
       if (threadIdx.x == 0) sh.xm[xpar] = v;
       cluster_sync_all();
       if (warp == 0) {
-        v = __reduce_max_sync(0xffffffffu, lane < C ? ld_cluster_u32(mapa_shared(smem_u32(&sh.xm[xpar]), lane)) : 0);
+        v = of_warp<ADD>(lane < C ? ld_cluster_u32(mapa_shared(smem_u32(&sh.xm[xpar]), lane)) : 0);
         if (lane == 0) sh.got[xpar][0] = v;
       }
       __syncthreads();
@@ -320,6 +337,8 @@ struct Row {
     par ^= 1;
     return v;
   }
+  __device__ __forceinline__ uint32_t reduce_max(uint32_t v) { return reduce_u32<false>(v); }
+  __device__ __forceinline__ uint32_t reduce_count(uint32_t v) { return reduce_u32<true>(v); }
   // Sum over the block of the values of lower threads.
   __device__ __forceinline__ u64 scan_before(u64 v, u64 &total) {
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -345,15 +364,16 @@ struct Row {
 
   // The threads' mark sums over the cluster; every thread gets them.  A thread's
   // halves are below 2^26 (64 elements of 2^20), a warp's below 2^31.
-  __device__ __forceinline__ void reduce_marks(const MarkSums &m, u64 (&v)[kMarks + 1]) {
+  template <int N>
+  __device__ __forceinline__ void reduce_marks(const MarkSums<N> &m, u64 (&v)[N + 1]) {
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 #pragma unroll
-    for (int i = 0; i <= kMarks; ++i) {
+    for (int i = 0; i <= N; ++i) {
       const uint32_t h = __reduce_add_sync(0xffffffffu, m.hi[i]), l = __reduce_add_sync(0xffffffffu, m.lo[i]);
       if (lane == 0) sh.mark_hi[i][warp] = h, sh.mark_lo[i][warp] = l;
     }
     __syncthreads();
-    if (warp <= kMarks) {
+    if (warp <= N) {
       u64 x = ((u64)sh.mark_hi[warp][lane] << 20) + sh.mark_lo[warp][lane];
 #pragma unroll
       for (int o = 16; o > 0; o /= 2) x += __shfl_xor_sync(0xffffffffu, x, o);
@@ -361,7 +381,7 @@ struct Row {
     }
     sync();
     if (C > 1) {
-      if (warp <= kMarks) {
+      if (warp <= N) {
         u64 x = lane < C ? ld_cluster_u64(mapa_shared(smem_u32(&sh.mark_sums[warp]), lane)) : 0;
 #pragma unroll
         for (int o = 4; o > 0; o /= 2) x += __shfl_xor_sync(0xffffffffu, x, o);
@@ -370,7 +390,7 @@ struct Row {
       __syncthreads();
     }
 #pragma unroll
-    for (int i = 0; i <= kMarks; ++i) v[i] = sh.mark_totals[i];
+    for (int i = 0; i <= N; ++i) v[i] = sh.mark_totals[i];
   }
 
   // Before bins are added to: the last readers of what they share memory with
@@ -419,7 +439,18 @@ struct Row {
   // Puts this thread's elements of `mask` on rank 0's list (cleared a sync before).
   __device__ __forceinline__ void gather(const Mask &mask) {
     if (__any_sync(0xffffffffu, mask.any())) {
-      uint32_t at = mask.any() ? atom_cluster_add(at0(&sh.list_n), mask.count()) : 0;
+      // the warp's places, then the lane's among them
+      const int lane = threadIdx.x % 32;
+      const uint32_t mine = mask.count();
+      uint32_t at = mine;
+#pragma unroll
+      for (int m = 1; m < 32; m *= 2) {
+        const uint32_t o = __shfl_up_sync(0xffffffffu, at, m);
+        if (lane >= m) at += o;
+      }
+      uint32_t base = 0;
+      if (lane == 31) base = C > 1 ? atom_cluster_add(at0(&sh.list_n), at) : atomicAdd(&sh.list_n, at);
+      at += __shfl_sync(0xffffffffu, base, 31) - mine;
       for_each(mask, [&](int j, bool valid) {
         if (valid) st_cluster_u64(at0(&sh.list[at++]), q_of(run[j], index0 + j));
       });
@@ -431,9 +462,9 @@ struct Row {
     sync();
   }
 
-  // Puts rank 0's list in order, the largest first.  `reach`: no element is
-  // further below the row's largest than this (infinity: not known).
-  __device__ __forceinline__ void order_list(int n, float reach) {
+  // Puts rank 0's list in order, the largest first.  No element is above `from`,
+  // and none further below it than `reach` (infinity: not known).
+  __device__ __forceinline__ void order_list(int n, float from, float reach) {
     const int tid = threadIdx.x;
     if (n <= kRanked) {
       const u64 q = tid < n ? sh.list[tid] : 0;
@@ -452,7 +483,7 @@ struct Row {
       uint32_t *bins = reinterpret_cast<uint32_t *>(sh.list + kSpread);
       const float scale = kThreads / reach;
       auto bin = [&](u64 q) {
-        const int b = __float2int_rz((top - x_of_key((uint32_t)(q >> 32))) * scale);
+        const int b = __float2int_rz((from - x_of_key((uint32_t)(q >> 32))) * scale);
         return b < kThreads - 1 ? b : kThreads - 1;
       };
       bins[tid] = 0;
@@ -512,12 +543,12 @@ struct Row {
   // `want`.  A list that begins the order (whole): want is part_of(the k's
   // weight, p_share), and where all that is kept is on the list, few enough, the
   // token is drawn from it at once (drawn).
-  __device__ __forceinline__ Cut resolve(int n, u64 place0, u64 above, u64 k, bool by_p, u64 want, bool whole = false,
-                                         u64 p_share = 0, float reach = INFINITY) {
+  __device__ __forceinline__ Cut resolve(int n, u64 place0, u64 above, u64 k, bool by_p, u64 want, float from,
+                                         float reach, bool whole = false, u64 p_share = 0) {
     if (rank == 0) {
       const int tid = threadIdx.x;
       __syncthreads();
-      order_list(n, reach);
+      order_list(n, from, reach);
       u64 q[2], w[2];
       float e[2];
       bool in[2];
@@ -598,11 +629,11 @@ struct Row {
         const u64 q = q_of(run[j], index0 + j);
         return q >= lo && q <= hi;
       });
-      u64 n = mask.count(), unused = 0;
-      reduce(n, unused);
+      const uint32_t n = reduce_count(mask.count());
       if (n <= kList) {
         gather(mask);
-        return BY_WEIGHT ? resolve((int)n, 1, above, ~0ull, true, want) : resolve((int)n, above, 0, want, false, 0);
+        return BY_WEIGHT ? resolve((int)n, 1, above, ~0ull, true, want, top, INFINITY)
+                         : resolve((int)n, above, 0, want, false, 0, top, INFINITY);
       }
     }
   }
@@ -611,7 +642,7 @@ struct Row {
   __device__ __forceinline__ Cut select_count(u64 k, bool by_p, u64 p_share, bool &only_first) {
     // k runs (or quarters) whose largest is in one of the first bins hold k elements in them
     int limit = kBins - 1;
-    u64 below = 0, unused = 0;
+    u64 below = 0;
     auto in_bins = [&](float v) { return limit == kBins - 1 || (top - v) * kBinScale < (float)(limit + 1); };
     const int parts = k <= (u64)C * kThreads / 4 ? 1 : 4;
     if (k <= (u64)C * kThreads * parts) {
@@ -629,8 +660,7 @@ struct Row {
     }
     Mask mask;
     if (in_bins(run_top)) mask = mask_of(R, [&](int j) { return in_bins(run[j]); });
-    u64 n = mask.count(), over = 0;
-    reduce(n, unused);
+    u64 n = reduce_count(mask.count()), over = 0;
     if (n > kList) {
       clear_bins();
       for_each(mask, [&](int j, bool valid) {
@@ -643,9 +673,7 @@ struct Row {
         equal.set(j, valid && b == limit);
         under.set(j, valid && b < limit);
       });
-      n = equal.count();
-      unused = 0;
-      reduce(n, unused);
+      n = reduce_count(equal.count());
       mask = equal;
       if (n + over <= kList) {
         n += over, over = 0;
@@ -658,7 +686,7 @@ struct Row {
       gather(mask);
       const bool whole = over == 0;
       const float reach = whole && limit < kBins - 1 ? (limit + 1) / kBinScale : INFINITY;
-      cut = resolve((int)n, over, 0, k, by_p && whole, 0, whole, p_share, reach);
+      cut = resolve((int)n, over, 0, k, by_p && whole, 0, top, reach, whole, p_share);
       if (drawn || (by_p && whole)) return cut;
     } else {
       u64 lo, hi;
@@ -666,7 +694,7 @@ struct Row {
       cut = select_in<false>(lo, hi, over, k);
     }
     u64 run_above = 0;
-    return by_p ? select_weight(0, p_share, cut, top, -INFINITY, 0, only_first, run_above, mask) : cut;
+    return by_p ? select_weight(0, p_share, cut, top, -INFINITY, 0, false, only_first, run_above, mask) : cut;
   }
 
   // The stretch of the order that the elements of a bin take.
@@ -682,15 +710,73 @@ struct Row {
     lo = (u64)~reduce_max(not_least) << 32;
   }
 
+  // Counts the samples, kSamples elements of every C-th thread's run, in rank 0's
+  // bins (cleared a sync before) over the values that have a weight.
+  __device__ __forceinline__ void sample() {
+    if (threadIdx.x % C) return;
+    const float scale = inv_t * (kBins / kNoWeight);
+    const int n = min(R, kSamples), step = R / n;
+    for (int i = 0; i < n; ++i) {
+      const int b = min(__float2int_rz((top - run[i * step]) * scale), kBins - 1);
+      if (C > 1) atom_cluster_add(at0(&sh.hist[b]), 1u); else atomicAdd(&sh.hist[b], 1u);
+    }
+  }
+  // Guesses where the weight below falls to `rest` of a row, by the samples (counted a
+  // sync before): values a little above and below.  All samples of a bin are taken
+  // to weigh what its middle does.
+  __device__ __forceinline__ void guess(u64 rest, float &high, float &low) {
+    if (rank == 0) {
+      const int tid = threadIdx.x;
+      const float width = fminf(__fdiv_rn(kNoWeight / kBins, inv_t), 1e30f);  // times 0 a number
+      const uint32_t n0 = sh.hist[2 * tid], n1 = sh.hist[2 * tid + 1];
+      auto mass = [&](int i, uint32_t n) {
+        const float e = exp2f((i + 0.5f) * (-kNoWeight / kBins * 1.4426950408889634f));
+        return i == kBins - 1 ? 0 : (u64)((float)n * e * 68719476736.0f);
+      };
+      const u64 m0 = mass(2 * tid, n0), m1 = mass(2 * tid + 1, n1);
+      // weights (below 2^48, in units of 2^-36) and counts (up to 4096) in one number
+      u64 both;
+      const u64 both_before = scan_before((m0 + m1) << 13 | (n0 + n1), both);
+      par ^= 1;  // as on the other CTAs
+      const u64 m_before = both_before >> 13, total = both >> 13;
+      const uint32_t before = both_before & 8191, samples = both & 8191;
+      rest = (rest >> 4) / (uint32_t)R * min(R, kSamples) / C;
+      const u64 target = total > rest ? total - rest : 0;
+      if (tid == 0) sh.answer = __float_as_uint((float)samples);
+      __syncthreads();
+      auto at = [&](u64 m_from, u64 m, float n_from, uint32_t n) {
+        if (target >= m_from && target - m_from < m)
+          sh.answer = __float_as_uint(n_from + (float)n * ((float)(target - m_from) / (float)m));
+      };
+      at(m_before, m0, before, n0);
+      at(m_before + m0, m1, before + n0, n1);
+      if (tid == 0) sh.before = __float_as_uint(top), sh.bin = __float_as_uint(top - kBins * width);
+      __syncthreads();
+      const float place = __uint_as_float((uint32_t)sh.answer);
+      auto mark = [&](float rank_at, u64 &to, int i, float n_from, uint32_t n) {
+        if (n && rank_at >= n_from && rank_at < n_from + n)
+          to = __float_as_uint(top - ((float)i + (rank_at - n_from) / (float)n) * width);
+      };
+      mark(place - kOff, sh.before, 2 * tid, before, n0);
+      mark(place - kOff, sh.before, 2 * tid + 1, before + n0, n1);
+      mark(place + kOff, sh.bin, 2 * tid, before, n0);
+      mark(place + kOff, sh.bin, 2 * tid + 1, before + n0, n1);
+    }
+    sync();
+    u64 h, l;
+    from_rank0(sh.before, sh.bin, h, l);
+    high = __uint_as_float((uint32_t)h), low = __uint_as_float((uint32_t)l);
+  }
+
   // Of what `from` keeps (weight `total`, 0: not known) the ones whose weight
   // before them is under part_of(total, p_share).  The end is known to lie among
   // the values in (low, high], with weight `above` over them, run_above of it
-  // this thread's.  On return `mask` has this thread's elements of the last such
-  // stretch, and run_above fits it.
+  // this thread's, and this thread's elements there in `mask` if `masked`.  On
+  // return `mask` has its elements of the last such stretch, and run_above fits it.
   __device__ __noinline__ Cut select_weight(u64 total, u64 p_share, Cut from, float high, float low, u64 above,
-                                            bool &only_first, u64 &run_above, Mask &mask) {
-    u64 unused = 0;
+                                            bool masked, bool &only_first, u64 &run_above, Mask &mask) {
     if (total == 0) {
+      u64 unused = 0;
       WeightSum sum;
       for (int j = 0; j < R; ++j) sum.add(from.keeps(run[j], index0 + j) ? e_of(run[j]) : 0.0f);
       total = sum.total();
@@ -701,16 +787,15 @@ struct Row {
       only_first = true;
       return from;
     }
-    if (from.x == -INFINITY) mask = mask_of(R, [&](int j) { return run[j] <= high && run[j] > low; });
+    if (masked) {
+    } else if (from.x == -INFINITY) mask = mask_of(R, [&](int j) { return run[j] <= high && run[j] > low; });
     else mask = mask_of(R, [&](int j) { return run[j] <= high && run[j] > low && from.keeps(run[j], index0 + j); });
     const float floor_x = __fdiv_rn(-kNoWeight, inv_t) + top;
-    u64 n = mask.count(), was = ~0ull;
-    unused = 0;
-    reduce(n, unused);
-    while (n > kFew && n < was) {
+    uint32_t n = reduce_count(mask.count()), was = ~0u;
+    while (n > (low > -INFINITY ? kSpread : kFew) && n < was) {
       // the weights above kMarks values between low and high
       const float from_x = low > floor_x ? low : floor_x, step = (high - from_x) * (1.0f / (kMarks + 1));
-      MarkSums m;
+      MarkSums<kMarks> m;
 #pragma unroll
       for (int i = 0; i < kMarks; ++i) m.mark[i] = high - (i + 1) * step;
       for_each(mask, [&](int j, bool valid) {
@@ -729,14 +814,12 @@ struct Row {
       for_each(mask, [&](int j, bool valid) { kept.set(j, valid && run[j] <= high && run[j] > low); });
       mask = kept;
       was = n;
-      n = mask.count();
-      unused = 0;
-      reduce(n, unused);
+      n = reduce_count(mask.count());
     }
     if (n <= kList) {
       clear_list();
       gather(mask);
-      return resolve((int)n, above ? 1 : 0, above, ~0ull, true, want);
+      return resolve((int)n, above ? 1 : 0, above, ~0ull, true, want, high, high - low);
     }
     u64 lo = ((u64)order_key(low) + 1) << 32;
     const u64 from_q = q_of(from.x, from.i);
@@ -829,8 +912,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     xs[i] = v;
     top = fmaxf(top, v);
   }
-  Row row{sh, xs + tid * R, R, C, rank, (uint32_t)(rank * slice + tid * R), 0.0f, greedy ? 1.0f : 1.0f / t, -INFINITY, 0, 0};
+  const bool by_k = k < a.V || k == 1, free_draw = !by_k && !by_p, guessed = !by_k && by_p && p_share > 0;
+  Row row{sh, xs + tid * R, R, C, rank, (uint32_t)(rank * slice + tid * R), 0.0f, greedy ? 1.0f : 1.0f / t, -INFINITY, 0,
+          0};
   row.drawn = false;
+  if (guessed) row.clear_bins();
   row.top = top = x_of_key(row.reduce_max(order_key(top)));  // also: the slice is in shared memory
   if (top == -INFINITY) {  // nothing can be drawn
     if (rank == 0 && tid == 0) {
@@ -841,18 +927,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
 
-  // ---- the row's own softmax total z, and in the same pass the exact weights it is drawn by
-  const bool by_k = k < a.V || k == 1, free_draw = !by_k && !by_p;
-  float z = 0.0f;
-  WeightSum sum;   // what is kept of the run, where that is known
-  MarkSums marks;  // top-p alone: the run's weight, and above kMarks values
+  // ---- the row's own softmax total z, and in the same pass the exact weights it is drawn by,
+  // or with top-p alone their total zt as a float and samples
+  float z = 0.0f, zt = 0.0f;
+  WeightSum sum;  // what is kept of the run, where that is known
   // (where the temperature is 1, z's terms are the weights' own)
   const bool own = row.inv_t == 1.0f;
-  auto z_of = [&](float v) {
+  auto exp2_of = [](float v) {
     float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"((v - top) * 1.4426950408889634f));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(v));
     return y;
   };
+  auto z_of = [&](float v) { return exp2_of((v - top) * 1.4426950408889634f); };
   if (free_draw) {
 #pragma unroll 4
     for (int j = 0; j < R; ++j) {
@@ -860,17 +946,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       z += own ? e : z_of(v);
       sum.add(e < min_p ? 0.0f : e);
     }
-  } else if (!by_k) {
-#pragma unroll
-    for (int i = 0; i < kMarks; ++i) marks.mark[i] = top - kMarkAt[i] * t;
-#pragma unroll 2
+  } else if (guessed && !own) {
+    row.sample();
+    const float scale = row.inv_t * 1.4426950408889634f;
+#pragma unroll 4
     for (int j = 0; j < R; ++j) {
-      const float v = row.run[j], e = row.e_of(v);
-      z += own ? e : z_of(v);
+      const float v = row.run[j];
+      z += z_of(v);
+      zt += exp2_of((v - top) * scale);
       row.run_top = fmaxf(row.run_top, v);
-      marks.add(v, e);
     }
   } else {
+    if (guessed) row.sample();
 #pragma unroll 4
     for (int j = 0; j < R; ++j) {
       const float v = row.run[j];
@@ -879,8 +966,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   // the threads' sums are joined as whole numbers of 2^-40, which have no order
-  u64 zsum = (u64)(z * 1099511627776.0f), unused = 0;
-  row.reduce(zsum, unused);
+  u64 zsum = (u64)(z * 1099511627776.0f), ztsum = (u64)(zt * 1099511627776.0f), unused;
+  row.reduce(zsum, ztsum);
+  if (own) ztsum = zsum;
   const float logz = logf((float)zsum * 9.094947017729282e-13f);
   row.share = u > 0.0f ? (u64)(fminf(u, 1.0f) * 16777216.0f) : 0ull;
   if (row.share > 16777215ull) row.share = 16777215ull;
@@ -898,18 +986,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       return;
     }
   } else if (!only_first && by_p) {
-    u64 v[kMarks + 1];
+    float high, low;
+    row.guess((u64)((1.0f - p) * (float)ztsum), high, low);
+    // the exact weights of all, and of what is above the two values; which lie between
+    MarkSums<2> marks;
+    marks.mark[0] = high, marks.mark[1] = low;
+    Mask mask = mask_of(R, [&](int j) {
+      const float v = row.run[j];
+      marks.add(v, row.e_of(v));
+      return v <= high && v > low;
+    });
+    u64 v[3], above = 0, run_above = 0;
     row.reduce_marks(marks, v);
-    const u64 want = part_of(v[kMarks], p_share);
-    float high = top, low = -INFINITY;
-    u64 above = 0, run_above = 0;
-#pragma unroll
-    for (int i = 0; i < kMarks; ++i) {
-      if (v[i] < want) high = marks.mark[i], above = v[i], run_above = marks.sum(i);
-      if (v[kMarks - 1 - i] >= want) low = marks.mark[kMarks - 1 - i];
-    }
-    Mask mask;
-    cut = row.select_weight(v[kMarks], p_share, cut, high, low, above, only_first, run_above, mask);
+    const u64 want = part_of(v[2], p_share);
+    const bool hit = v[0] < want && v[1] >= want;
+    if (hit) above = v[0], run_above = marks.sum(0);
+    else if (v[0] >= want) low = high, high = top;
+    else high = low, low = -INFINITY, above = v[1], run_above = marks.sum(1);
+    cut = row.select_weight(v[2], p_share, cut, high, low, above, hit, only_first, run_above, mask);
     if (!(min_p > 0.0f)) {  // all above the last stretch is kept, and of it what the cut keeps
       summed = true;
       mine = run_above;
