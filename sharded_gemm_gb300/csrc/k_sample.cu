@@ -23,6 +23,8 @@
 #include "attn.cuh"
 #include "ptx.cuh"
 
+#include <atomic>
+
 namespace tp {
 namespace {
 
@@ -1283,6 +1285,36 @@ __global__ void __launch_bounds__(kThreads) sample_wide_kernel(const __grid_cons
 static_assert(sizeof(RowShared) % 16 == 0, "the row begins behind it, 16-byte aligned");
 static_assert(sizeof(RowShared) + kMaxRun * kThreads * 4 <= 232448, "shared memory of a CTA");
 
+// How many clusters of 4 or 8 CTAs run at once: fewer than the SMs hold CTAs, as a
+// cluster stays within a group of SMs (36 and 15 on 152 SMs).  A CTA fills its SM's
+// registers, so it does not depend on the row.
+template <typename T>
+int clusters_at_once(int C) {
+  static std::atomic<int> known[64][2];
+  int dev = 0, n = 0;
+  cudaGetDevice(&dev);
+  std::atomic<int> &was = known[dev & 63][C == 8];
+  if ((n = was.load()) == 0) {
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = C;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg;
+    memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = dim3(C);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = sizeof(RowShared);
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, sample_row_kernel<T>, &cfg) != cudaSuccess || n < 1) {
+      cudaGetLastError();
+      n = 1;
+    }
+    was.store(n);
+  }
+  return n;
+}
+
 template <typename T>
 int launch(const SampleArgs &a, cudaStream_t s) {
   cudaError_t e;
@@ -1290,10 +1322,18 @@ int launch(const SampleArgs &a, cudaStream_t s) {
     // longer than a cluster holds: read again for every pass
     e = launch_pdl(sample_wide_kernel<T>, dim3((unsigned)a.B), dim3(kThreads), 0, s, a);
   } else {
-    // as many CTAs a row as it needs, and more while the batch leaves SMs idle
+    // As many CTAs a row as it needs.  More where the clusters run at once and the longer
+    // joins pay (us, one row of 50272: drawn freely 14.4 on one CTA, 11.5 on 8; top-p 33.7,
+    // 30.6; top-k 17.7, 19.8; of 8000: 8.3, 10.4; 22.6, 26.7; 13.1, 19.3; of 200000, on 4
+    // and on 8: 17.7, 13.8; 50, 47; 23.5, 21.4.  16 rows of 50272 on 8, two turns: 22; 60; 39.)
     int C = 1;
     while ((int64_t)C * kMaxRun * kThreads < a.V) C *= 2;
-    while (C < 8 && a.B * C * 2 <= sm_count() && a.V > (int64_t)C * kThreads) C *= 2;
+    if (C > 1 || (!a.top_k && a.V > (int64_t)kMaxRun / 2 * kThreads))
+      for (int more = 8; more >= 4; more /= 2)
+        if (more > C && a.B <= clusters_at_once<T>(more)) {
+          C = more;
+          break;
+        }
     const int R = (int)((a.V + (int64_t)C * kThreads - 1) / ((int64_t)C * kThreads)) | 1;
     const size_t smem = sizeof(RowShared) + (size_t)R * kThreads * sizeof(float);
     if (a.B * C > 0x7fffffff) return set_error(TP_ERR_UNSUPPORTED, "too many rows for one launch");

@@ -638,6 +638,49 @@ def test_sample_equals_its_definition(seed):
     assert torch.equal(tok, draw_by_definition(x, *par))
 
 
+@pytest.mark.parametrize("B,V", [(1, 25600), (1, 25601), (3, 52224), (3, 52225), (15, 60000), (16, 30000), (36, 60000),
+                                 (37, 60000), (2, 104449), (20, 150000), (40, 110000), (1, 208897)])
+@pytest.mark.parametrize("with_k", [False, True])
+def test_sample_rows_of_every_split(B, V, with_k):
+    """Rows on 1, 2, 4 and 8 CTAs, at the sizes where the number changes."""
+    rng = np.random.default_rng(B + V)
+    x = torch.from_numpy(rng.standard_normal((B, V)).astype(np.float32) * 2.5).cuda()
+    par = [rng.random(B, dtype=np.float32), rng.choice(np.float32([0.5, 0.7, 1, 1.3, 20]), B),
+           rng.choice([0, 40, 2500] if with_k else [0], B).astype(np.int32),
+           rng.choice(np.float32([1, 0.02, 0.5, 0.9, 0.95, 0.999]), B), rng.choice(np.float32([0, 0.02]), B)]
+    par = [torch.from_numpy(np.ascontiguousarray(a)).cuda() for a in par]
+    tok, _ = tp.tp_sample(x, par[0], par[1], par[2] if with_k else None, par[3], par[4])
+    status_ok()
+    assert torch.equal(tok, draw_by_definition(x, *par))
+
+
+@pytest.mark.parametrize("V", [30000, 50272, 120000])
+def test_sample_top_p_where_a_guess_misleads(V):
+    """Every fourth part of the row unlike the rest, a ramp, a spike and two levels: the elements that the end
+    of top-p is guessed from do not stand for the row."""
+    B = 8
+    rng = np.random.default_rng(V)
+    i = np.arange(V)
+    x = rng.standard_normal((B, V)).astype(np.float32)
+    x[0] = 10 - 20 * i / V
+    x[1] = np.where(i % 49 == 0, 8, x[1])
+    x[2] = np.where(i % 49 == 1, 8, x[2])
+    x[3] = -30
+    x[3, V // 3] = 5
+    x[4] = np.where(i < V // 2, 1, 2)
+    x[5] = np.where(i < 700, 6, -6) + x[5] * 1e-3
+    x[6] = x[6] * 1e-6
+    x[7] = np.where(i % 2, -np.inf, x[7] * 4)
+    x = torch.from_numpy(x).cuda()
+    for p in (0.3, 0.9, 0.99999):
+        par = [torch.from_numpy(rng.random(B, dtype=np.float32)).cuda(), torch.full((B,), 0.8, device="cuda"),
+               torch.zeros(B, dtype=torch.int32, device="cuda"), torch.full((B,), p, device="cuda"),
+               torch.zeros(B, device="cuda")]
+        tok, _ = tp.tp_sample(x, par[0], par[1], None, par[3])
+        status_ok()
+        assert torch.equal(tok, draw_by_definition(x, *par))
+
+
 def test_sample_distribution():
     """20000 draws of one row: each share within five standard deviations of its probability."""
     V, n = 12, 20000
