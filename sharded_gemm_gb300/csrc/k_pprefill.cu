@@ -81,18 +81,6 @@ struct Control {
   int abort;
 };
 
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ float rcp_approx(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // mbar_wait without its out-of-line slow path: a call would spill the scores
 // that the softmax warps hold in registers.
 __device__ __forceinline__ bool wait_inline(uint32_t bar, uint32_t parity, uint64_t limit_ns, int *status,
@@ -580,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           for (int c = 0; c < 4; ++c)
 #pragma unroll
             for (int x = 0; x < 32; ++x)
-              s[c][x] = fmaf(-2.0f * cap2, rcp_approx(1.0f + exp2_approx(s[c][x] * scale)), cap2);
+              s[c][x] = capped(s[c][x] * scale, cap2);
         }
         if (!(jt + kTile <= prefix || (jt >= all_lo && jt + kTile <= all_hi))) {
           // one bit a position: compared one by one they cost the registers of the scores

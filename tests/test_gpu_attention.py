@@ -241,6 +241,13 @@ def test_decode(policy, lens, N, Hq, Hk, D, page, dt, cap, window):
     run_decode(lens, N, Hq, Hk, D, page, dt, cap, window)
 
 
+@pytest.mark.parametrize("cap", [0.25, 1e3, 1e4, 1e6, 1e30])
+def test_caps_far_from_the_scores(policy, cap):
+    """Scores far below the cap are themselves; far above it they are the cap."""
+    run_decode([700, 33], 1, 8, 2, 64, 16, F16, cap)
+    run_prefill([(40, 300), (150, 150)], 1, 8, 2, 64, 16, F16, cap)
+
+
 def test_decode_many_sequences(policy):
     rng = np.random.default_rng(3)
     run_decode([int(n) for n in rng.integers(0, 90, 700)], 1, 4, 2, 64, 16, BF)
