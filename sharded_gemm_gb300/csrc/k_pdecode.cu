@@ -23,10 +23,10 @@
 // terms lose nothing to their range.
 //
 // Bytes bound it: every visible key and value is read once.  Measured against the
-// copy rate (6.79 TB/s): 64 sequences of 1000..16384, 8 heads on one of 128, 338 us
-// (99%); 16 of 100..4096 with as many key as query heads 96 us (93%); 48 windows of
-// 1024 on heads of 64, 30 us (44%: 3.7 us to the first bytes, then merges of short
-// pieces); one sequence of 517 8.9 us, a chain of latencies.  The softmax's terms
+// copy rate (6.79 TB/s): 64 sequences of 1000..16384, 8 heads on one of 128, 333 us
+// (101%); 16 of 100..4096 with as many key as query heads 93 us (96%); 48 windows of
+// 1024 on heads of 64, capped, 26 to 28 us (50%: 4 us to the first bytes, then merges of
+// short pieces); one sequence of 517 8.9 us, a chain of latencies.  The softmax's terms
 // are rounded to the 16-bit type for the second product, as its operands are.
 #include "mma16.cuh"
 
@@ -48,10 +48,11 @@ struct Shape {
   static constexpr int kSmem = kRingBytes + kMergeBytes;
   static constexpr int kSlot = kHeads * (D + 2);                      // floats of a workspace piece
   // Cost of a unit and of an item (its start and the merge of its parts), in
-  // 0.37 us: a unit streams in 0.73 us at D = 64 and 1.47 at 128, and item
-  // costs of 2..6 gave 106, 102, 99, 96, 97 us for 16 sequences of 100..4096
-  // positions on 32 heads of 128, 36, 33, 32, 32, 32 for 48 windows of 1024 at 64.
-  static constexpr int kUnitCost = D / 32, kItemCost = 5;
+  // 0.37 us: a unit streams in 0.73 us at D = 64 and 1.47 at 128.  Item costs of
+  // 3, 4, 5, 6, 8 and 10 gave 98, 95, 94, 93, 92 and 92 us for 16 sequences of
+  // 100..4096 positions on 32 heads of 128, and 31, 27.2, 26.5, 25.8, 25.4 and 25.4
+  // for 48 windows of 1024 at 64.
+  static constexpr int kUnitCost = D / 32, kItemCost = 8;
 };
 
 struct Plan {
@@ -80,6 +81,11 @@ __device__ __forceinline__ Span span_of(const AttnArgs &a, int64_t b) {
   return s;
 }
 
+// a / b, both positive; 64-bit divisions only where 32 bits do not hold the numbers.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return (a | b) >> 32 ? a / b : (uint32_t)a / (uint32_t)b;
+}
+
 // A place in the CTA's list of pieces.
 struct Piece {
   int64_t b;
@@ -89,14 +95,23 @@ struct Piece {
   bool valid;
 };
 
+// An item of which this CTA has left a piece in the workspace: CTAs c0 .. c1 share it.
+struct Join {
+  long long c0, c1;
+  int64_t out;  // of its first head, in o[r]
+  int r, heads;
+  int last;     // this CTA came last, and joins
+};
+
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(kThreads, 1)
     decode_kernel(const __grid_constant__ AttnArgs a, const Plan plan) {
   using Sh = Shape<D, NT>;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ long long s_scan[kWarps + 1];
-  __shared__ long long s_start_b, s_start_at;
-  __shared__ int s_last;
+  __shared__ long long s_b[2], s_at[2];
+  __shared__ Join s_join;
+  __shared__ Piece s_first;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
   griddep_launch_dependents();
   griddep_wait();
@@ -123,35 +138,45 @@ __global__ void __launch_bounds__(kThreads, 1)
     total += s_scan[w];
   }
   // every CTA's range is at least a unit long: those inside an item then hold a unit of it
-  const long long most = total / UC, grid = most < gridDim.x ? most : gridDim.x, cta = blockIdx.x;
-  const long long x0 = cta < grid ? cta * total / grid : 0, x1 = cta < grid ? (cta + 1) * total / grid : 0;
-  if (x0 < x1 && x0 >= before && x0 < before + mine) {
-    long long at = before;
-    for (int64_t b = b0; b < b1; ++b) {
-      const long long c = cost(span_of(a, b));
-      if (x0 < at + c) {
-        s_start_b = b;
-        s_start_at = at;
-        break;
+  const long long even = quotient(total + gridDim.x - 1, gridDim.x), share = even > UC ? even : UC, cta = blockIdx.x;
+  const long long x0 = cta * share < total ? cta * share : total, x1 = x0 + share < total ? x0 + share : total;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {  // the sequences that hold the range's first and last place
+    const long long x = i ? x1 - 1 : x0;
+    if (x0 < x1 && x >= before && x < before + mine) {
+      long long at = before;
+      for (int64_t b = b0; b < b1; ++b) {
+        const long long c = cost(span_of(a, b));
+        if (x < at + c) {
+          s_b[i] = b;
+          s_at[i] = at;
+          break;
+        }
+        at += c;
       }
-      at += c;
     }
   }
   __syncthreads();
 
   // ---- the list of pieces, walked twice: by the copies, ahead, and by the products.
   // Unit u of an item that begins at `at` belongs to the CTA whose range holds
-  // at + IC + u * UC.
+  // at + IC + u * UC.  Where the last item goes on in the next CTA its piece is taken
+  // first, so that the join with the others' has the rest of the range to hide under
+  // (16 sequences of 100..4096: 91.9 us; taken last, 93.5; 48 windows 25.4 and 25.2).
+  long long stop = x1;
+  auto cut = [&](Piece &p) {  // p is an item: its units in this range
+    const long long lo = x0 - p.at - IC + UC - 1, hi = x1 - p.at - IC + UC - 1;
+    p.unit0 = lo > 0 ? (int)(lo / UC) : 0;
+    const int end = hi > 0 ? (hi / UC < p.span.units ? (int)(hi / UC) : p.span.units) : 0;
+    p.units = end - p.unit0;
+  };
   auto settle = [&](Piece &p) {  // p is an item: its units in this range, or the next item that has some
     for (;;) {
-      if (p.at >= x1) {
+      if (p.at >= stop) {
         p.valid = false;
         return;
       }
-      const long long lo = x0 - p.at - IC + UC - 1, hi = x1 - p.at - IC + UC - 1;
-      p.unit0 = lo > 0 ? (int)(lo / UC) : 0;
-      const int end = hi > 0 ? (hi / UC < p.span.units ? (int)(hi / UC) : p.span.units) : 0;
-      p.units = end - p.unit0;
+      cut(p);
       if (p.units > 0) return;
       p.at += IC + (long long)UC * p.span.units;
       if (++p.item == ips) {
@@ -166,7 +191,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   };
+  auto item_at = [&](Piece &p, int i, long long x) {  // the item that holds place x, in sequence s_b[i]
+    p.b = s_b[i];
+    p.span = span_of(a, p.b);
+    const long long each = IC + (long long)UC * p.span.units;
+    p.item = (int)quotient(x - s_at[i], each);
+    p.at = s_at[i] + p.item * each;
+  };
+  Piece p;
+  p.valid = x0 < x1;
+  if (p.valid) {
+    item_at(p, 0, x0);
+    settle(p);
+    if (tid == 0) s_first = p;
+    if (p.valid && p.at + IC + (long long)UC * p.span.units < x1) {  // it goes on behind p
+      Piece last;
+      last.valid = true;
+      item_at(last, 1, x1 - 1);
+      cut(last);
+      if (last.units > 0 && last.unit0 + last.units < last.span.units) stop = last.at, p = last;
+    }
+    __syncthreads();  // s_first
+  }
   auto next_piece = [&](Piece &p) {
+    if (p.at >= stop) {
+      p = s_first;
+      return;
+    }
     p.at += IC + (long long)UC * p.span.units;
     if (++p.item == ips) {
       p.item = 0;
@@ -180,16 +231,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     settle(p);
   };
-  Piece p;
-  p.valid = x0 < x1;
-  if (p.valid) {
-    p.b = s_start_b;
-    p.span = span_of(a, p.b);
-    const long long each = IC + (long long)UC * p.span.units;
-    p.item = (int)((x0 - s_start_at) / each);
-    p.at = s_start_at + p.item * each;
-    settle(p);
-  }
 
   const uint32_t ring = smem_u32(smem) + warp * (Sh::kStages * 2 * Sh::kChunkBytes);
   float *merge = reinterpret_cast<float *>(smem + Sh::kRingBytes);
@@ -251,10 +292,48 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // ---- products
   const float to_log2 = 1.4426950408889634f;
-  const float qk_scale = a.softcap > 0.0f ? a.scale / a.softcap : a.scale * to_log2;
+  const float qk_scale = a.softcap > 0.0f ? a.scale / a.softcap * 2.0f * to_log2 : a.scale * to_log2;
   const float cap_log2 = a.softcap * to_log2;
   int stage = 0;
   const int G = a.Hq / a.Hk;
+  // A piece left in the workspace is joined with the others' at the end of the next piece:
+  // until then one warp waits for the count of those that came, not the CTA (2 to 3 us of
+  // round trips; 48 windows of 1024 took 1.0 us longer).
+  bool joins = false;
+  auto join = [&]() {
+    const long long c0 = s_join.c0, c1 = s_join.c1;
+    if (!s_join.last) return;
+    if (tid == 0) plan.counters[c0] = 0;  // ready for the next call
+    for (int e = tid; e < s_join.heads * D; e += kThreads) {
+      const int head = e / D, d = e % D;
+      float top = -INFINITY, sum = 0.0f, acc = 0.0f;
+      for (long long c = c0; c <= c1; c += 8) {  // eight pieces' loads at a time
+        float mc[8], lc[8], oc[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float *s = plan.ws + ((c + i) * 2 + (c + i == c0 ? 1 : 0)) * Sh::kSlot;
+          const bool is = c + i <= c1;
+          mc[i] = is ? __ldcg(s + Sh::kHeads * D + head) : -INFINITY;
+          lc[i] = is ? __ldcg(s + Sh::kHeads * (D + 1) + head) : 0.0f;
+          oc[i] = is ? __ldcg(s + head * D + d) : 0.0f;
+        }
+        float tn = top;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) tn = fmaxf(tn, mc[i]);
+        const float mm = tn == -INFINITY ? 0.0f : tn, f0 = exp2f(top - mm);
+        sum *= f0, acc *= f0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float f1 = exp2f(mc[i] - mm);
+          sum += f1 * lc[i];
+          acc += f1 * oc[i];
+        }
+        top = tn;
+      }
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      static_cast<T *>(a.o[s_join.r])[s_join.out + head * D + d] = static_cast<T>(acc * inv);
+    }
+  };
   while (p.valid) {
     const int rh = p.item / plan.groups, grp = p.item - rh * plan.groups, r = rh / a.Hk, h = rh - r * a.Hk;
     const int heads = G - grp * Sh::kHeads < Sh::kHeads ? G - grp * Sh::kHeads : Sh::kHeads;
@@ -314,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           float x = s[n][i] * qk_scale;
-          if (a.softcap > 0.0f) x = cap_log2 * tanhf(x);
+          if (a.softcap > 0.0f) x = capped(x, cap_log2);  // (tanhf and exp2f: 2.2 us of 31)
           if (edge) {
             const int row = g + (i & 2) * 4;
             if (row < lo || row >= hi) x = -INFINITY;
@@ -331,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int x = 4; x < 32; x *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
             if (top > m[n][c]) {  // the same in all lanes of a head
-              const float keep = exp2f(m[n][c] - top);
+              const float keep = exp2_approx(m[n][c] - top);
               m[n][c] = top;
               l[n][c] *= keep;
 #pragma unroll
@@ -346,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float mm = m[n][i & 1];
-          e[i] = exp2f(s[n][i] - (mm == -INFINITY ? 0.0f : mm));
+          e[i] = exp2_approx(s[n][i] - (mm == -INFINITY ? 0.0f : mm));
         }
         l[n][0] += e[0] + e[2];
         l[n][1] += e[1] + e[3];
@@ -385,6 +464,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     __syncthreads();
+    if (joins) join();
+    joins = false;
     const bool whole = p.units == p.span.units;
     float *slot = plan.ws + (cta * 2 + (p.unit0 == 0 ? 1 : 0)) * Sh::kSlot;  // an item begins, or goes on, here
     const float *ml = merge + kWarps * Sh::kHeads * Sh::kRow;
@@ -409,40 +490,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (d == 0) slot[Sh::kHeads * D + head] = top, slot[Sh::kHeads * (D + 1) + head] = sum;
       }
     }
+    __syncthreads();  // the merge rows are free again, and the piece is written
     if (!whole) {
-      // the CTAs of this item: c holds position x where c * total / grid <= x
-      const long long f = p.at + IC, e0 = f + (long long)UC * (p.span.units - 1);
-      const long long c0 = ((f + 1) * grid - 1) / total, c1 = ((e0 + 1) * grid - 1) / total;
-      __syncthreads();
       if (tid == 0) {
-        __threadfence();  // (the barrier orders the other threads' pieces before it)
-        s_last = atomicAdd(plan.counters + c0, 1) == (int)(c1 - c0);
-        __threadfence();
+        // the CTAs of this item, by the places of its first and last unit
+        const long long f = p.at + IC, e0 = f + (long long)UC * (p.span.units - 1);
+        s_join.c0 = quotient(f, share), s_join.c1 = quotient(e0, share);
+        s_join.out = p.b * a.ldo + head0 * D;
+        s_join.r = r, s_join.heads = heads;
+        // releases the CTA's parts (the barrier orders the other threads' before it), and
+        // acquires those of the CTAs counted before
+        int came;
+        asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;"
+                     : "=r"(came)
+                     : "l"(plan.counters + s_join.c0)
+                     : "memory");
+        s_join.last = came == (int)(s_join.c1 - s_join.c0);
       }
-      __syncthreads();
-      if (s_last) {
-        if (tid == 0) plan.counters[c0] = 0;  // ready for the next call
-        for (int e = tid; e < heads * D; e += kThreads) {
-          const int head = e / D, d = e % D;
-          float top = -INFINITY, sum = 0.0f, acc = 0.0f;
-#pragma unroll 4
-          for (long long c = c0; c <= c1; ++c) {
-            const float *s = plan.ws + (c * 2 + (c == c0 ? 1 : 0)) * Sh::kSlot;
-            const float mc = __ldcg(s + Sh::kHeads * D + head), lc = __ldcg(s + Sh::kHeads * (D + 1) + head);
-            const float oc = __ldcg(s + head * D + d);
-            const float tn = fmaxf(top, mc), mm = tn == -INFINITY ? 0.0f : tn;
-            const float f0 = exp2f(top - mm), f1 = exp2f(mc - mm);
-            sum = sum * f0 + f1 * lc;
-            acc = acc * f0 + f1 * oc;
-            top = tn;
-          }
-          const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-          static_cast<T *>(a.o[r])[p.b * a.ldo + (head0 + head) * D + d] = static_cast<T>(acc * inv);
-        }
-      }
+      joins = true;
     }
-    __syncthreads();  // the merge rows are free again
     next_piece(p);
+  }
+  if (joins) {
+    __syncthreads();
+    join();
   }
   cp_async_wait<0>();
 
