@@ -21,15 +21,20 @@
 //                so one query tile's softmax runs under the other's products;
 //   warps 2, 3   the next unit's queries into shared memory;
 //   warps 4..11  softmax, rescale and output, one warpgroup per query tile.
+// Where whole units would leave SMs idle (a few tokens over a long cache) every CTA
+// takes an equal range of the list of all units' key tiles.  A unit that several CTAs
+// hold leaves each one's O, m and l in the workspace, and the last warp to come joins its
+// rows, in CTA order.  One token over 16384 positions, 32 heads on 8: 167 us whole, 37 so;
+// 64 over 32768: 331, 76; 512 over 8192: 96, 64; 2048 over 16384: 335, 311.
 // Rows of a value tile behind the sequence's end (or in pages that are not
 // read) are written as zeros: stale rows never meet a product.
 //
 // Tensor rate bounds long chunks: 4 D flop per visible pair.  Of it, what holds
 // the kernel back is shared memory: Q K^T reads both operands from there, 128
 // bytes a cycle, which is all there is.  Measured: 8192 tokens, 32 heads of 128,
-// causal, 377 us alone and 408 in a long run (1460 and 1350 TFLOP/s, 76% and 70%
-// of cuBLAS's burst rate); 2 x 1024 tokens over 4000..8192 cached positions, 32
-// heads on 8, 182 us; five prompts of 7..150 tokens 14 us.
+// causal, 375 us alone and 393 to 410 in a long run (1460 and 1350 to 1400 TFLOP/s, 76%
+// and 70 to 73% of cuBLAS's burst rate); 2 x 1024 tokens over 4000..8192 cached positions,
+// 32 heads on 8, 182 us; five prompts of 7..150 tokens 14 us.
 #include "attn.cuh"
 #include "mma16.cuh"
 #include "ptx.cuh"
@@ -40,6 +45,8 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kTile = 128;  // rows of a query tile, positions of a key tile
 constexpr float kSlack = 8.0f;
+constexpr int kUnitTiles = 2;  // what a unit costs besides its tiles, in tiles (1.75 us at D = 128)
+constexpr int kJoinTiles = 6;  // and what a CTA's two shared ones cost more
 // Registers a thread: 384 * 168 at launch = 128 * 88 + 256 * 208.
 constexpr int kRegsFew = 88, kRegsMany = 208;
 
@@ -59,7 +66,9 @@ struct PrefillArgs {
   int groups, gsize, tpt;  // head groups of a key-value head, heads of a group, tokens of a query tile
   int box;                 // rows of a page copy
   int vec_q, vec_o;
-  int *counters;
+  int *counters;  // units dealt, CTAs at the end; with few units, of every CTA's shared one, parts come by warp
+  float *ws;      // parts of shared units: of a CTA two, of those each query tile's D + 2 values of 128 rows
+  int few;        // so few units that their tiles may be shared
   uint64_t wait_ns;
 };
 
@@ -71,12 +80,25 @@ struct Unit {
   int seen0;       // no row of the unit sees a position below this
   int j0;          // first key tile's position
   int n[2];        // key tiles of the query tiles
+  // where the unit's key tiles are shared with other CTAs:
+  int shared, c0, others;  // the first of them, how many besides this one
+};
+
+// A CTA's range in the list of all units' key tiles, and the unit it has come to.
+struct Walk {
+  long long x0, x1, share;  // from, to, of every CTA; in tiles, each unit counted kUnitTiles more
+  long long at;             // where the unit begins
+  int64_t b, t0;
+  int tokens, to, prefix;   // of sequence b
+  int blocks, rank, hu, n;  // its blocks, the unit's place among them and among the heads, its tiles
+  int ranged;
 };
 
 struct Control {
   uint64_t unit_full[2], unit_free[2], q_full[2], q_free[2], s_full[2], p_full[2][2], o_done[2], drain;
   uint64_t kv_full[10], kv_free[10];
   Unit unit[2];
+  Walk walk;
   uint32_t tmem;
   int abort;
 };
@@ -210,60 +232,208 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       unsigned fills = 0;  // ring slots filled so far
       uint32_t kv_phase = 0;
       bool ok = true;
-      for (;; ++seq) {
-        // find unit u: 32 sequences at a time from the cursor
-        int64_t b = -1;
-        long long base = 0;
-        int64_t t0 = 0, t1 = 0;
-        while (cur_b < a.B) {
-          int64_t x0 = 0, x1 = 0;
-          if (cur_b + lane < a.B) token_range(a, cur_b + lane, x0, x1);
-          long long mine = (x1 - x0 + block - 1) / block * heads_units, run = mine;
-#pragma unroll
-          for (int m = 1; m < 32; m *= 2) {
-            const long long o = __shfl_up_sync(0xffffffffu, run, m);
-            if (lane >= m) run += o;
-          }
-          const uint32_t hit = __ballot_sync(0xffffffffu, cur_base + run > u);
-          if (hit) {
-            const int l = __ffs(hit) - 1;
-            b = cur_b + l;
-            base = cur_base + __shfl_sync(0xffffffffu, run - mine, l);
-            t0 = __shfl_sync(0xffffffffu, x0, l);
-            t1 = __shfl_sync(0xffffffffu, x1, l);
-            break;
-          }
-          cur_base += __shfl_sync(0xffffffffu, run, 31);
-          cur_b += 32;
+      Walk &wk = ctl.walk;
+      // a sequence's length and bidirectional part, inside what the table can hold
+      auto lengths = [&](int64_t b, int &to, int &prefix) {
+        const int64_t cap = a.width << a.page_log2;
+        int64_t n = a.seq_lens[b];
+        if (n > cap) {
+          n = cap;
+          record_bad_value(a.status);
         }
+        to = n < 0 ? 0 : (int)n;
+        const int pre = a.prefix_lens ? a.prefix_lens[b] : 0;
+        prefix = pre < 0 ? 0 : pre > to ? to : pre;
+      };
+      // the first position that a block whose first is pos0 may see
+      auto seen_from = [&](int pos0, int prefix) {
+        const int lo = a.window && prefix == 0 ? pos0 - a.window + 1 : 0;
+        return lo < 0 ? 0 : lo;
+      };
+      // key tiles of block qb of a sequence
+      auto tiles_of = [&](int tokens, int to, int prefix, int qb) {
+        const int pos0 = to - tokens + qb * block;
+        int hi = tokens - qb * block < block ? to : pos0 + block;
+        if (hi < prefix) hi = prefix;
+        const int j0 = seen_from(pos0, prefix) & ~(kTile - 1);
+        return hi > j0 ? (hi - j0 + kTile - 1) / kTile : 0;
+      };
+      wk.ranged = 0;
+      if (pa.few) {
+        // Few units: their lengths, and whether equal ranges of tiles are likely to end before whole
+        // units would.  (Ranges are not shorter than an eighth of the longest unit: all its
+        // parts are read back by one CTA.  An eighth over the even share and a join are allowed
+        // for: 2 x 1024 tokens over 4000..8192 took 182 us in ranges, 177 whole.)
+        auto cost_of = [&](int64_t b, long long &units, int &longest) {
+          int64_t t0 = 0, t1 = 0;
+          int to, prefix;
+          long long sum = 0;
+          if (b >= a.B) return sum;
+          token_range(a, b, t0, t1);
+          lengths(b, to, prefix);
+          const int blocks = (int)((t1 - t0 + block - 1) / block);
+          for (int qb = 0; qb < blocks; ++qb) {
+            const int n = tiles_of((int)(t1 - t0), to, prefix, qb);
+            sum += kUnitTiles + n;
+            longest = n > longest ? n : longest;
+          }
+          units += (long long)blocks * heads_units;
+          return sum * heads_units;
+        };
+        long long total = 0, units = 0;
+        int longest = 0;
+        for (int64_t b = lane; b < a.B + lane; b += 32) total += cost_of(b, units, longest);
+#pragma unroll
+        for (int m = 16; m > 0; m /= 2) {
+          total += __shfl_xor_sync(0xffffffffu, total, m);
+          units += __shfl_xor_sync(0xffffffffu, units, m);
+          longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, m));
+        }
+        const long long even = (total + gridDim.x - 1) / gridDim.x;
+        const int least = max(4, (longest + 7) / 8);
+        const long long share = even > least ? even : least;
+        // whole units: the longest, or as many turns as it takes of average ones.  (Full turns
+        // are no loss: with every SM busy a tile takes 1.95 us, with five of six 1.75.)
+        const long long turns = (units + gridDim.x - 1) / gridDim.x;
+        const long long whole = turns <= 1 ? longest + kUnitTiles : turns * total / units;
+        if (whole > share + share / 8 + kJoinTiles) {
+          const long long x0 = blockIdx.x * share < total ? blockIdx.x * share : total;
+          // the sequence that holds x0
+          long long base = 0;
+          int64_t b = a.B;
+          for (int64_t b32 = 0; b32 < a.B; b32 += 32) {
+            const long long mine = cost_of(b32 + lane, units, longest);
+            long long run = mine;
+#pragma unroll
+            for (int m = 1; m < 32; m *= 2) {
+              const long long o = __shfl_up_sync(0xffffffffu, run, m);
+              if (lane >= m) run += o;
+            }
+            const uint32_t hit = __ballot_sync(0xffffffffu, base + run > x0);
+            if (hit) {
+              const int l = __ffs(hit) - 1;
+              b = b32 + l;
+              base += __shfl_sync(0xffffffffu, run - mine, l);
+              break;
+            }
+            base += __shfl_sync(0xffffffffu, run, 31);
+          }
+          if (lane == 0) {
+            wk.ranged = 1;
+            wk.share = share;
+            wk.x0 = x0;
+            wk.x1 = x0 + share < total ? x0 + share : total;
+            wk.at = base;
+            wk.b = b - 1;
+            wk.blocks = wk.rank = wk.n = 0;
+            wk.hu = heads_units - 1;
+          }
+        }
+      }
+      __syncwarp();
+      // the walk's next unit (lane 0)
+      auto step = [&](bool begin) {
+        if (!begin) wk.at += kUnitTiles + wk.n;
+        if (++wk.hu < heads_units) return;
+        wk.hu = 0;
+        if (++wk.rank >= wk.blocks) {
+          wk.rank = 0;
+          do {
+            if (++wk.b >= a.B) return;
+            int64_t t0, t1;
+            token_range(a, wk.b, t0, t1);
+            wk.t0 = t0;
+            wk.tokens = (int)(t1 - t0);
+            wk.blocks = (wk.tokens + block - 1) / block;
+          } while (wk.blocks == 0);
+          lengths(wk.b, wk.to, wk.prefix);
+        }
+        wk.n = tiles_of(wk.tokens, wk.to, wk.prefix, wk.blocks - 1 - wk.rank);
+      };
+      if (lane == 0 && wk.ranged) {
+        step(true);
+        // to the block, and the head, that hold x0
+        while (wk.b < a.B && wk.at + (long long)heads_units * (kUnitTiles + wk.n) <= wk.x0) {
+          wk.at += (long long)heads_units * (kUnitTiles + wk.n);
+          ++wk.rank;
+          wk.n = tiles_of(wk.tokens, wk.to, wk.prefix, wk.blocks - 1 - wk.rank);
+        }
+        if (wk.b < a.B) {
+          wk.hu = (int)((wk.x0 - wk.at) / (kUnitTiles + wk.n));
+          wk.at += (long long)wk.hu * (kUnitTiles + wk.n);
+        }
+      }
+      __syncwarp();
+      for (;; ++seq) {
+        int64_t b = -1, t0 = 0;
+        int tokens = 0, qb = 0, hu = 0, from = 0, to_tile = 0x7fffffff;
         Unit w;
+        w.shared = 0;
+        if (wk.ranged) {
+          // the next unit of which a tile is in the range, or that has none and begins in it
+          if (lane == 0) {
+            for (; wk.b < a.B && wk.at < wk.x1; step(false)) {
+              const long long f = wk.at + kUnitTiles;
+              const long long lo = wk.x0 > f ? wk.x0 - f : 0, hi = wk.x1 - f < wk.n ? wk.x1 - f : wk.n;
+              if (wk.n == 0 ? wk.at < wk.x0 : hi <= lo) continue;
+              b = wk.b, t0 = wk.t0, tokens = wk.tokens;
+              qb = wk.blocks - 1 - wk.rank, hu = wk.hu;
+              from = (int)lo, to_tile = wk.n ? (int)hi : 0;
+              if (to_tile - from < wk.n) {
+                w.shared = 1;
+                w.c0 = (int)(f / wk.share);
+                w.others = (int)((f + wk.n - 1) / wk.share) - w.c0;
+              }
+              step(false);
+              break;
+            }
+          }
+          b = __shfl_sync(0xffffffffu, b, 0);
+          t0 = __shfl_sync(0xffffffffu, t0, 0);
+          tokens = __shfl_sync(0xffffffffu, tokens, 0);
+          qb = __shfl_sync(0xffffffffu, qb, 0);
+          hu = __shfl_sync(0xffffffffu, hu, 0);
+          from = __shfl_sync(0xffffffffu, from, 0);
+          to_tile = __shfl_sync(0xffffffffu, to_tile, 0);
+        } else {
+          // find unit u: 32 sequences at a time from the cursor
+          while (cur_b < a.B) {
+            int64_t x0 = 0, x1 = 0;
+            if (cur_b + lane < a.B) token_range(a, cur_b + lane, x0, x1);
+            long long mine = (x1 - x0 + block - 1) / block * heads_units, run = mine;
+#pragma unroll
+            for (int m = 1; m < 32; m *= 2) {
+              const long long o = __shfl_up_sync(0xffffffffu, run, m);
+              if (lane >= m) run += o;
+            }
+            const uint32_t hit = __ballot_sync(0xffffffffu, cur_base + run > u);
+            if (hit) {
+              const int l = __ffs(hit) - 1;
+              b = cur_b + l;
+              const long long local = u - (cur_base + __shfl_sync(0xffffffffu, run - mine, l));
+              t0 = __shfl_sync(0xffffffffu, x0, l);
+              tokens = (int)(__shfl_sync(0xffffffffu, x1, l) - t0);
+              // longest first, a block's heads side by side: the CTAs then walk the
+              // same key tiles of a head at about the same time
+              hu = (int)(local % heads_units);
+              qb = (tokens + block - 1) / block - 1 - (int)(local / heads_units);
+              break;
+            }
+            cur_base += __shfl_sync(0xffffffffu, run, 31);
+            cur_b += 32;
+          }
+        }
         w.valid = b >= 0;
         if (w.valid) {
-          const long long local = u - base;
-          const int blocks = (int)((t1 - t0 + block - 1) / block);
-          // longest first, a block's heads side by side: the CTAs then walk the
-          // same key tiles of a head at about the same time
-          const int hu = (int)(local % heads_units);
-          const int qb = blocks - 1 - (int)(local / heads_units);
           w.b = (int)b;
           w.grp = hu % pa.groups;
           w.h = hu / pa.groups % a.Hk;
           w.r = hu / pa.groups / a.Hk;
           w.tok0 = (int)t0 + qb * block;
-          w.ntok = (int)(t1 - w.tok0 < block ? t1 - w.tok0 : block);
-          const int64_t cap = a.width << a.page_log2;
-          int64_t n = a.seq_lens[b];
-          if (n > cap) {
-            n = cap;
-            if (lane == 0) record_bad_value(a.status);
-          }
-          if (n < 0) n = 0;
-          w.to = (int)n;
-          int pre = a.prefix_lens ? a.prefix_lens[b] : 0;
-          w.prefix = pre < 0 ? 0 : pre > w.to ? w.to : pre;
-          w.pos0 = w.to - (int)(t1 - t0) + qb * block;
-          int lo = a.window && w.prefix == 0 ? w.pos0 - a.window + 1 : 0;
-          w.seen0 = lo < 0 ? 0 : lo;
+          w.ntok = tokens - qb * block < block ? tokens - qb * block : block;
+          lengths(b, w.to, w.prefix);
+          w.pos0 = w.to - tokens + qb * block;
+          w.seen0 = seen_from(w.pos0, w.prefix);
           w.j0 = w.seen0 & ~(kTile - 1);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
@@ -271,8 +441,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             int hi = w.pos0 + i * pa.tpt + rows;  // behind the last row's position
             if (hi < w.prefix) hi = w.prefix;
             if (hi > w.to) hi = w.to;
-            w.n[i] = rows > 0 && hi > w.j0 ? (hi - w.j0 + kTile - 1) / kTile : 0;
+            const int n = rows > 0 && hi > w.j0 ? (hi - w.j0 + kTile - 1) / kTile : 0;
+            w.n[i] = n < from ? 0 : (n < to_tile ? n : to_tile) - from;  // of the part
           }
+          w.j0 += from * kTile;
         }
         const int us = seq & 1;
         if (seq >= 2) ok = wait(ctl.unit_free[us], ((seq >> 1) - 1) & 1);
@@ -282,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           mbar_arrive(smem_u32(&ctl.unit_full[us]));
         }
         if (!w.valid) {
-          if (lane == 0) {
+          if (lane == 0 && !wk.ranged) {
             // out of units: the last CTA to see that clears the counters for the next call
             // (every CTA's additions to the first are done before its one to the second)
             __threadfence();
@@ -352,8 +524,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         if (!ok) break;
         // The next unit is asked for only now, a ring of tiles before this one's
         // products end: asked for earlier, units went to CTAs that were still busy.
-        if (lane == 0) u = (long long)gridDim.x + atomicAdd(pa.counters, 1);
-        u = __shfl_sync(0xffffffffu, u, 0);
+        if (!wk.ranged) {
+          if (lane == 0) u = (long long)gridDim.x + atomicAdd(pa.counters, 1);
+          u = __shfl_sync(0xffffffffu, u, 0);
+        }
       }
       if (!ok) {
         // gave up: the copies in flight still land in this CTA's shared memory
@@ -465,6 +639,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     } else {
       // ---------------------------------------------------------------- queries
       const int th = threadIdx.x - 64, G = a.Hq / a.Hk;
+      const int row0 = th / (D / 8), tk0 = row0 / pa.gsize, hd0 = row0 - tk0 * pa.gsize;
+      const int step_tk = 64 / (D / 8) / pa.gsize, step_hd = 64 / (D / 8) - step_tk * pa.gsize;
+      const int64_t step_src = step_tk * a.ldq + (int64_t)step_hd * D, wrap_src = a.ldq - (int64_t)pa.gsize * D;
       for (int seq = 0;; ++seq) {
         const int us = seq & 1;
         if (!wait(ctl.unit_full[us], (seq >> 1) & 1)) break;
@@ -491,14 +668,20 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         for (int i = 0; i < 2; ++i) {
           if (seq > 0) ok = wait(ctl.q_free[i], (seq - 1) & 1);
           if (!ok) break;
-          const uint32_t base = i * S::kTileBytes;
-          for (int e = th; e < kTile * (D / 8); e += 64) {
-            const int row = e / (D / 8), c = e % (D / 8), tk = row / pa.gsize, hd = row - tk * pa.gsize;
-            const bool live = tk < pa.tpt && i * pa.tpt + tk < w.ntok && hd < heads;
-            const T *src = q + (live ? (int64_t)(i * pa.tpt + tk) * a.ldq + (int64_t)hd * D + c * 8 : 0);
-            const uint32_t off = base + (c >> 3) * S::kHalf + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+          // this thread's column of 8 values, in every kStep-th row; the row's token and head
+          // go along without divisions (with them a unit's queries took 2 us longer)
+          constexpr int kStep = 64 / (D / 8);
+          const int c = th % (D / 8);
+          const uint32_t base = i * S::kTileBytes + (c >> 3) * S::kHalf;
+          const int tokens = w.ntok - i * pa.tpt < pa.tpt ? w.ntok - i * pa.tpt : pa.tpt;
+          int tk = tk0, hd = hd0;
+          const T *src = q + (int64_t)(i * pa.tpt + tk) * a.ldq + (int64_t)hd * D + c * 8;
+#pragma unroll 4
+          for (int row = th / (D / 8); row < kTile; row += kStep) {
+            const bool live = tk < tokens && hd < heads;
+            const uint32_t off = base + row * 128 + (((c & 7) ^ (row & 7)) << 4);
             if (pa.vec_q) {
-              cp_async16(q_smem + off, src, live);
+              cp_async16(q_smem + off, live ? src : q, live);
             } else {
               uint16_t x[8];
 #pragma unroll
@@ -506,6 +689,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
               *reinterpret_cast<uint4 *>(smem_gen + off) =
                   make_uint4(x[0] | x[1] << 16, x[2] | x[3] << 16, x[4] | x[5] << 16, x[6] | x[7] << 16);
             }
+            tk += step_tk, hd += step_hd, src += step_src;
+            if (hd >= pa.gsize) hd -= pa.gsize, ++tk, src += wrap_src;
           }
           cp_async_commit();
           cp_async_wait<0>();
@@ -655,10 +840,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         if (!ok) break;
         tc_fence_after();
       }
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        float o[32];
+      auto sums = [&](int c, float (&o)[32]) {  // this row's O, 32 values of it
         if (tiles > 0) {
           tmem_ld32(o_tmem + c * 32, o);
           tmem_wait_ld();
@@ -666,7 +848,104 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 #pragma unroll
           for (int x = 0; x < 32; ++x) o[x] = 0.0f;
         }
-        if (out) {
+      };
+      // the part left by CTA c, from a row on: value x at x * kTile
+      auto part = [&](int c, int of) {
+        return pa.ws + (size_t)((c * 2 + (c == w.c0)) * 2 + i) * ((D + 2) * kTile) + of;
+      };
+      auto factor = [](float mc, float to) { return mc == -INFINITY ? 0.0f : exp2_approx(mc - to); };
+      bool joins = false;
+      // In a join of few rows, the first `rows` of the warp (8 or 16), several lanes share a
+      // row's values: lane g * rows + r has values of row r.
+      int rows = 32, g = 0, jrow = row;
+      bool mine_too = live;  // this lane has values to join
+      float top = m;
+      if (w.shared) {
+        float *mine = part(blockIdx.x, row);
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          float o[32];
+          sums(c, o);
+          if (live) {
+#pragma unroll
+            for (int x = 0; x < 32; ++x) mine[(c * 32 + x) * kTile] = o[x];
+          }
+          __syncwarp();
+        }
+        if (live) mine[D * kTile] = m, mine[(D + 1) * kTile] = l;
+        __syncwarp();
+        int came = 0;
+        if (lane == 0) {
+          // releases the warp's rows, and acquires those of the CTAs counted before
+          int *count = pa.counters + 2 + w.c0 * 8 + (warp - 4);
+          asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(came) : "l"(count) : "memory");
+          if (came == w.others) *count = 0;  // ready for the next call
+        }
+        joins = __shfl_sync(0xffffffffu, came, 0) == w.others;
+        if (!joins) {
+          tc_fence_before();
+          continue;
+        }
+        const uint32_t alive = __ballot_sync(0xffffffffu, live);
+        rows = alive >> 8 == 0 ? 8 : alive >> 16 == 0 ? 16 : 32;
+        g = lane / rows;
+        const int from = lane % rows;
+        jrow = row - lane + from;
+        mine_too = alive >> from & 1;
+        out = reinterpret_cast<T *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(out), from));
+        const int end = mine_too ? w.c0 + w.others + 1 : 0;
+        float sum = 0.0f;
+        top = -INFINITY;
+        for (int c0 = w.c0; c0 < end; c0 += 4) {
+          float mc[4], lc[4], mx = top;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            mc[k] = c0 + k < end ? __ldcg(part(c0 + k, jrow) + D * kTile) : -INFINITY;
+            lc[k] = c0 + k < end ? __ldcg(part(c0 + k, jrow) + (D + 1) * kTile) : 0.0f;
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mx = fmaxf(mx, mc[k]);
+          sum *= factor(top, mx);
+          top = mx;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) sum = fmaf(factor(mc[k], top), lc[k], sum);
+        }
+        l = sum;
+      }
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll 1
+      for (int c0 = 0; c0 < D / 32; c0 += 32 / rows) {
+        const int c = c0 + g;
+        float o[32];
+        if (!joins) {
+          sums(c, o);
+        } else {
+#pragma unroll
+          for (int x = 0; x < 32; ++x) o[x] = 0.0f;
+          // in CTA order, so that who came last changes no rounding; two parts' loads at a time
+          float own[32];
+          sums(c0, own);
+          // (its own part too is read back where lanes share rows)
+          const int end = mine_too && c < D / 32 ? w.c0 + w.others + 1 : 0, me = rows == 32 ? (int)blockIdx.x : -1;
+          for (int k0 = w.c0; k0 < end; k0 += 2) {
+            float v[2][32], f[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const bool is = k0 + k < end && k0 + k != me;
+              const float *p = part(is ? k0 + k : w.c0, jrow);
+              f[k] = k0 + k == me ? m : is ? __ldcg(p + D * kTile) : -INFINITY;
+#pragma unroll
+              for (int x = 0; x < 32; ++x) v[k][x] = is ? __ldcg(p + (c * 32 + x) * kTile) : own[x];
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const float e = factor(f[k], top);
+#pragma unroll
+              for (int x = 0; x < 32; ++x) o[x] = fmaf(e, v[k][x], o[x]);
+            }
+          }
+        }
+        if (out && c < D / 32) {
           uint32_t pk[16];
 #pragma unroll
           for (int x = 0; x < 16; ++x) pk[x] = Half2<T>::pack(o[2 * x] * inv, o[2 * x + 1] * inv);
@@ -719,10 +998,16 @@ int launch(const AttnArgs &a, cudaStream_t s) {
     if (int rc = make_tmap_2d(&p.k[r], kc, mt, 2, D, rows, D, 64, p.box, CU_TENSOR_MAP_SWIZZLE_128B)) return rc;
     if (int rc = make_tmap_2d(&p.v[r], vc, mt, 2, D, rows, D, 64, p.box, CU_TENSOR_MAP_SWIZZLE_128B)) return rc;
   }
-  float *ws;
-  if (int rc = split_workspace(s, 0, 2, &ws, &p.counters)) return rc;
-  const int64_t most = (a.T / (2 * p.tpt) + a.B) * a.N * a.Hk * p.groups;
-  const int grid = most < sm_count() ? (int)most : sm_count();
+  // Tiles are never shared with four units an SM or more: a fifth, unfinished turn costs
+  // less than sharing saves.
+  const int64_t heads = (int64_t)a.N * a.Hk * p.groups, blocks = a.T / (2 * p.tpt);
+  const int64_t sure = (blocks > a.B ? blocks : a.B < a.T ? a.B : a.T) * heads;
+  p.few = sure < 4ll * sm_count();
+  const int64_t most = (blocks + a.B) * heads;
+  const int grid = p.few || most > sm_count() ? sm_count() : (int)most;
+  const size_t part = 2 * (D + 2) * kTile * sizeof(float);
+  if (int rc = split_workspace(s, p.few ? grid * 2 * part : 0, 2 + (p.few ? grid * 8 : 0), &p.ws, &p.counters))
+    return rc;
   auto kern = prefill_kernel<T, D, MAXN>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh<D>::kSmem);
   if (e == cudaSuccess) e = launch_pdl(kern, dim3(grid), dim3(kThreads), Sh<D>::kSmem, s, p);

@@ -426,6 +426,29 @@ def test_prefill_of_one_token_is_decode():
     assert ((o - o2).float().abs() <= 2 * U[BF] * (o.float().abs() + 1)).all()
 
 
+@pytest.mark.parametrize("chunks,N,Hq,Hk,D,page,dt,cap,window", [
+    ([(1, 9000)], 1, 8, 2, 128, 16, BF, 0.0, 0),
+    ([(4, 16000)], 1, 32, 8, 128, 64, F16, 0.0, 0),
+    ([(5, 5000), (0, 700), (3, 12), (17, 4097), (2, 1)], 2, 6, 2, 64, 32, BF, 20.0, 0),
+    ([(64, 8192)], 1, 4, 4, 128, 128, BF, 0.0, 0),
+    ([(300, 6000), (700, 700)], 1, 8, 1, 128, 16, F16, 0.0, 3000),
+    ([(1100, 1100)], 1, 2, 2, 128, 16, BF, 0.0, 0),
+    ([(129, 3000), (40, 2999), (1, 3001)], 4, 3, 3, 64, 256, F16, 0.0, 0),
+    ([(16, 4000)], 1, 150, 1, 64, 16, BF, 0.0, 0),
+    ([(2, 300)] * 40 + [(3, 9000)], 1, 4, 2, 64, 16, BF, 0.0, 0)])
+def test_prefill_tiles_shared_between_ctas(policy, chunks, N, Hq, Hk, D, page, dt, cap, window):
+    """Few rows over long caches: the key tiles of a block are divided, and joined."""
+    chunks = [(min(a, b), b) for a, b in chunks]
+    run_prefill(chunks, N, Hq, Hk, D, page, dt, cap, window)
+    run_prefill(chunks, N, Hq, Hk, D, page, dt, cap, window, seed=5)  # the counters are clear again
+
+
+def test_prefill_shared_tiles_repeat_bitwise():
+    o, args = run_prefill([(33, 7000), (90, 2500)], 1, 8, 2, 128, 32, BF)
+    for _ in range(5):
+        assert torch.equal(tp.tp_paged_prefill(*args), o)
+
+
 def test_prefill_strides_other_stream():
     o, (q, kc, vc, table, cu, seq, _) = run_prefill([(50, 20), (200, 0)], 2, 4, 2, 128, 16, F16)
     N, T, C = q.shape
