@@ -17,9 +17,9 @@
 // value needs one division.  min-p drops the kept ones with e_i < min_p.
 // The token is the first, in index order, whose running weight passes
 // floor(u * W).
-// Measured: 384 rows of 50272 float32 logits with mixed settings 77 us (floor by
-// bytes 11); 152 rows, one an SM: greedy 12, free 15, top-k 50 19, top-k 1000 with
-// top-p 25, top-p 0.95 59 us; a single row 9 to 37.
+// Measured: 384 rows of 50272 float32 logits with mixed settings 68 us (floor by
+// bytes 11); 152 rows, one an SM: greedy 12, free 15, top-k 50 18, top-k 1000 with
+// top-p 25, top-p 36 to 42 us; a single row 9 to 31.
 #include "attn.cuh"
 #include "ptx.cuh"
 
