@@ -583,6 +583,9 @@ int tp_q4_sharded_to_all_noalloc(int N, const void *const *x, int64_t T, int64_t
  *   positions of sequence b (whose keys and values are in the cache already).
  *   The token at position p sees position j < seq_lens[b] where
  *     j <= p and (window = 0 or j > p - window), or j < prefix_lens[b].
+ *   With few tokens the key tiles of a block of them are shared between SMs and
+ *   the parts joined in a fixed order (the same call gives the same bytes);
+ *   that uses the per-(device, stream) workspace, 512 * (D + 2) * 4 bytes an SM.
  *   cu_seqlens int32 (B + 1), ascending; prefix_lens NULL or int32 (B).  A row
  *   that sees nothing is zero, and so is a row of no sequence.
  *

@@ -449,6 +449,26 @@ def test_prefill_shared_tiles_repeat_bitwise():
         assert torch.equal(tp.tp_paged_prefill(*args), o)
 
 
+def test_prefill_shared_tiles_in_a_graph():
+    """Replayed on new queries: the arrival counts are clear after every run."""
+    o, args = run_prefill([(4, 9000), (20, 300)], 1, 8, 2, 128, 64, F16)
+    q, out = args[0].clone(), torch.empty_like(o)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    tp.tp_paged_prefill(q, *args[1:], out=out, stream=s)  # the stream's workspace
+    s.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        tp.tp_paged_prefill(q, *args[1:], out=out, stream=s)
+    for seed in range(3):
+        q.copy_(torch.randn(q.shape, device="cuda", generator=torch.Generator(device="cuda").manual_seed(seed)))
+        out.fill_(7.0)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, tp.tp_paged_prefill(q, *args[1:]))
+    status_ok()
+
+
 def test_prefill_strides_other_stream():
     o, (q, kc, vc, table, cu, seq, _) = run_prefill([(50, 20), (200, 0)], 2, 4, 2, 128, 16, F16)
     N, T, C = q.shape
