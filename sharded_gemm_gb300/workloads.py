@@ -263,7 +263,27 @@ class PagedServing:
 
     def step(self, x, counts, u, temperature=None, top_k=None, top_p=None, min_p=None, stream=None):
         """x (sum of counts, D) bf16: counts[b] new tokens of each sequence in turn (at least one); u (batch).
-        Returns (tokens (batch), y (sum of counts, D) float32: the attention block's output)."""
+        Returns (tokens (batch), y (sum of counts, D) float32: the attention block's output).
+
+        With ``stream`` (a torch stream or a raw handle) everything runs there, torch's own copies and gathers
+        too: behind what the current stream holds now, and the current stream waits for it."""
+        args = (x, counts, u, temperature, top_k, top_p, min_p)
+        if stream is None:
+            return self._step(*args)
+        here = torch.cuda.current_stream(x.device)
+        side = torch.cuda.ExternalStream(stream, x.device) if isinstance(stream, int) else stream
+        side.wait_stream(here)
+        try:
+            with torch.cuda.stream(side):
+                out = self._step(*args)
+        finally:
+            here.wait_stream(side)
+        # allocated on `side`: not handed out again there while the caller's stream still uses them
+        for t in (*out, self.logits, self.logprobs):
+            t.record_stream(here)
+        return out
+
+    def _step(self, x, counts, u, temperature, top_k, top_p, min_p):
         device, N = x.device, self.N
         lens = [n + c for n, c in zip(self.lens, counts)]
         if len(counts) != self.batch or min(counts) < 1 or max(lens) > self.capacity:
@@ -274,20 +294,20 @@ class PagedServing:
         positions, at = torch.from_numpy(pos).to(device), torch.from_numpy(seq).to(device)
         slots = self.block_table[at, positions.long() // self.page].long() * self.page + positions % self.page
         seq_lens = torch.tensor(lens, dtype=torch.int32, device=device)
-        qkv = tp_all_to_sharded(x, self.w_qkv, self.b_qkv, stream=stream)
+        qkv = tp_all_to_sharded(x, self.w_qkv, self.b_qkv)
         q = tp_qkv_append(qkv, self.k_cache, self.v_cache, slots, positions=positions, rope=self.rope,
-                          q_norm=self.q_norm, k_norm=self.k_norm, stream=stream)
+                          q_norm=self.q_norm, k_norm=self.k_norm)
         if max(counts) == 1:
-            o = tp_paged_decode(q, self.k_cache, self.v_cache, self.block_table, seq_lens, stream=stream)
+            o = tp_paged_decode(q, self.k_cache, self.v_cache, self.block_table, seq_lens)
         else:
             o = tp_paged_prefill(q, self.k_cache, self.v_cache, self.block_table, torch.from_numpy(cu).to(device),
-                                 seq_lens, stream=stream)
-        y = tp_sharded_to_all(list(o), self.w_o, self.b_o, stream=stream)
+                                 seq_lens)
+        y = tp_sharded_to_all(list(o), self.w_o, self.b_o)
         last = y[torch.from_numpy(cu[1:].astype(np.int64) - 1).to(device)].to(torch.bfloat16)
         logits = torch.empty((self.batch, self.V), dtype=torch.float32, device=device)
         Vn = self.V // N
-        tp_all_to_sharded(last, self.w_lm, None, out=[logits[:, r * Vn:(r + 1) * Vn] for r in range(N)], stream=stream)
-        tokens, self.logprobs = tp_sample(logits, u, temperature, top_k, top_p, min_p, stream=stream)
+        tp_all_to_sharded(last, self.w_lm, None, out=[logits[:, r * Vn:(r + 1) * Vn] for r in range(N)])
+        tokens, self.logprobs = tp_sample(logits, u, temperature, top_k, top_p, min_p)
         self.lens, self.logits = lens, logits
         return tokens, y
 

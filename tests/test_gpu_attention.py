@@ -868,3 +868,34 @@ def test_serving_step_refusals():
     for counts in ([4], [4, 0], [1, 21]):
         with pytest.raises(ValueError):
             serve.step(x, counts, u)
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_serving_steps_on_a_busy_side_stream(raw):
+    """Both streams have work queued when a step on another stream is asked for: its inputs are written
+    late on the caller's, and its results are read there at once."""
+    cfg = synth.qkv(seed=9, T=1, D=512, V=1000, N=4, bias_std=0.1)
+    plain, moved = (PagedServing(cfg, 8, batch=3, capacity=90, page=16) for _ in range(2))
+    side = torch.cuda.Stream()
+    rng = np.random.default_rng(7)
+    for counts in ([40, 1, 23], [1, 1, 1], [5, 30, 1], [1, 1, 1]):
+        xs = to_device(synth.f32_to_bf16_bits(rng.standard_normal((sum(counts), 512)).astype(np.float32)), "bf16")
+        us = torch.from_numpy(rng.random(3, dtype=np.float32)).cuda()
+        want = [t.clone() for t in (*plain.step(xs, counts, us), plain.logits, plain.logprobs)]
+        torch.cuda.synchronize()
+        x, u = torch.zeros_like(xs), torch.zeros_like(us)
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(3000000)
+        torch.cuda._sleep(3000000)
+        x.copy_(xs)
+        u.copy_(us)
+        tokens, y = moved.step(x, counts, u, stream=side.cuda_stream if raw else side)
+        got = [t.clone() for t in (tokens, y, moved.logits, moved.logprobs)]
+        # what the step freed may be handed out again on either stream
+        for s in (torch.cuda.current_stream(), side):
+            with torch.cuda.stream(s):
+                junk = [torch.full_like(y, NAN) for _ in range(8)]
+        del tokens, y, junk
+        status_ok()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
