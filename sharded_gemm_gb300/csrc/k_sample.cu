@@ -1283,7 +1283,8 @@ __global__ void __launch_bounds__(kThreads) sample_wide_kernel(const __grid_cons
 }
 
 static_assert(sizeof(RowShared) % 16 == 0, "the row begins behind it, 16-byte aligned");
-static_assert(sizeof(RowShared) + kMaxRun * kThreads * 4 <= 232448, "shared memory of a CTA");
+constexpr int kMaxSmem = (int)sizeof(RowShared) + kMaxRun * kThreads * 4;
+static_assert(kMaxSmem <= 232448, "shared memory of a CTA");
 
 // How many clusters of 4 or 8 CTAs run at once: fewer than the SMs hold CTAs, as a
 // cluster stays within a group of SMs (36 and 15 on 152 SMs).  A CTA fills its SM's
@@ -1338,7 +1339,9 @@ int launch(const SampleArgs &a, cudaStream_t s) {
     const size_t smem = sizeof(RowShared) + (size_t)R * kThreads * sizeof(float);
     if (a.B * C > 0x7fffffff) return set_error(TP_ERR_UNSUPPORTED, "too many rows for one launch");
     auto kern = sample_row_kernel<T>;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // The limit belongs to the function, not to this call: always the largest, so that a thread
+    // with shorter rows does not lower it between another's setting and launch.
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
     if (e != cudaSuccess) return cuda_error(e, "sample launch");
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof(cfg));

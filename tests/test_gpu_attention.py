@@ -811,6 +811,48 @@ def test_prepared_calls_of_every_entry_point():
     status_ok()
 
 
+def test_calls_from_two_threads():
+    """Draws of different lengths, appends and both attentions from two threads at once, a stream each: no call is
+    refused, and every one gives what it gives alone."""
+    import threading
+    jobs, want, errors = [], [], []
+    for i, V in enumerate((1000, 50272)):
+        g = torch.Generator(device="cuda").manual_seed(V)
+        logits = torch.randn((3, V), generator=g, device="cuda")
+        u = torch.rand(3, generator=g, device="cuda")
+        kc, vc, table, _ = paged([70 + 300 * i, 33], 1, 2, 64 << i, 16, BF, seed=i, fill=0.0)
+        q = torch.randn((1, 2, 8 * (64 << i)), generator=g, device="cuda").to(BF)
+        lens = torch.tensor([70 + 300 * i, 33], dtype=torch.int32, device="cuda")
+        cu = torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda")
+        x = torch.randn((1, 2, 12 * (64 << i)), generator=g, device="cuda").to(BF)
+        ka, va, slots = torch.zeros_like(kc), torch.zeros_like(vc), torch.arange(2, device="cuda")
+
+        def work(logits=logits, u=u, kc=kc, vc=vc, table=table, q=q, lens=lens, cu=cu, x=x, ka=ka, va=va, slots=slots):
+            return (*tp.tp_sample(logits, u, top_p=u), tp.tp_paged_decode(q, kc, vc, table, lens),
+                    tp.tp_paged_prefill(q, kc, vc, table, cu, lens), tp.tp_qkv_append(x, ka, va, slots))
+        jobs.append(work)
+        want.append(work())
+    torch.cuda.synchronize()
+
+    def loop(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(300):
+                    got = jobs[i]()
+                torch.cuda.current_stream().synchronize()
+            for a, b in zip(got, want[i]):
+                assert torch.equal(a, b)
+        except BaseException as e:  # noqa: BLE001 - reported by the test's thread
+            errors.append(e)
+    threads = [threading.Thread(target=loop, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    status_ok()
+
+
 # ------------------------------------------------------------------ together
 def bf16(a):
     return torch.from_numpy(np.asarray(a, np.float32)).to(BF).double().numpy()
