@@ -304,7 +304,8 @@ static int launch_mx_gemv(const Problem &p, cudaStream_t s, bool *handled) {
     }
   }
   const size_t smem = (size_t)floats * 4;
-  if (smem > 200 * 1024) return TP_OK;  // inputs too large to stage: the CUDA-core GEMM takes it
+  constexpr int kMostSmem = 200 * 1024;
+  if (smem > (size_t)kMostSmem) return TP_OK;  // inputs too large to stage: the CUDA-core GEMM takes it
   args.njobs = p.njobs;
   args.T = (int)maxT;
   args.xvec = 1;
@@ -315,9 +316,10 @@ static int launch_mx_gemv(const Problem &p, cudaStream_t s, bool *handled) {
   args.out_dt = p.out_dt;
   const int grid = std::min(sm_count(), (ntasks + kMxWarps - 1) / kMxWarps);
   cudaError_t e = cudaSuccess;
+  // the limit is the function's, shared by all threads: always the largest
 #define TP_MX_CASE(TTV)                                                                                   \
   if (maxT == TTV) {                                                                                      \
-    e = cudaFuncSetAttribute(mx_gemv_kernel<TTV>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem); \
+    e = cudaFuncSetAttribute(mx_gemv_kernel<TTV>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem); \
     if (e == cudaSuccess) e = launch_pdl(mx_gemv_kernel<TTV>, dim3(grid), dim3(kMxWarps * 32), smem, s, args); \
   }
   TP_MX_CASE(1)

@@ -383,6 +383,36 @@ def test_mx_pair_small_repeatable():
     check_close(to_host(w.y), ref, "down")
 
 
+def test_mx_gemv_of_two_widths_from_two_threads():
+    """Inputs of 2 and of 192 KB in shared memory, a thread and a stream each: no launch is refused."""
+    import threading
+    T, jobs, want, errors = 4, [], [], []
+    for K in (128, 12288):
+        w = tp.tp_mx_quantize(torch.randn((256, K), device="cuda"))
+        cs, ss = (tp.tp_shard_weight(t, 0, 1, 2) for t in w)
+        x = torch.randn((T, K), device="cuda").to(torch.bfloat16)
+        jobs.append((x, cs, ss))
+        want.append(tp.tp_mx_all_to_sharded(*jobs[-1]))
+    torch.cuda.synchronize()
+
+    def loop(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(1000):
+                    got = tp.tp_mx_all_to_sharded(*jobs[i])
+                torch.cuda.current_stream().synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got, want[i]))
+        except BaseException as e:  # noqa: BLE001 - reported by the test's thread
+            errors.append(e)
+    threads = [threading.Thread(target=loop, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    _status_ok()
+
+
 # ------------------------------------------------------------------ f3 backward
 @pytest.mark.parametrize("T,On,K,N", [(1, 64, 128, 2), (5, 40, 192, 4), (130, 320, 600, 2),
                                       (300, 264, 200, 3), (64, 256, 512, 8), (129, 128, 129, 1),
