@@ -882,6 +882,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           if (came == w.others) *count = 0;  // ready for the next call
         }
         joins = __shfl_sync(0xffffffffu, came, 0) == w.others;
+        __syncwarp();  // what lane 0 has acquired, for the other lanes: the shuffle orders no memory
         if (!joins) {
           tc_fence_before();
           continue;

@@ -443,6 +443,23 @@ def test_prefill_tiles_shared_between_ctas(policy, chunks, N, Hq, Hk, D, page, d
     run_prefill(chunks, N, Hq, Hk, D, page, dt, cap, window, seed=5)  # the counters are clear again
 
 
+@pytest.mark.parametrize("tokens,Hq,Hk,D", [(1, 8, 2, 128), (1, 8, 1, 64), (3, 8, 2, 64), (2, 8, 1, 128), (9, 8, 2, 64),
+                                            (40, 8, 1, 128)])
+def test_prefill_joins_of_few_and_many_rows_repeat(tokens, Hq, Hk, D):
+    """Joins where 8, 16 or all 32 lanes of a warp have rows of their own, again and again with other work between:
+    each reads every part that other CTAs have left."""
+    o, args = run_prefill([(tokens, 6000), (1, 40)], 2, Hq, Hk, D, 16, BF)
+    other = torch.randn((1 << 24,), device="cuda")
+    outs = []
+    for i in range(40):
+        outs.append(tp.tp_paged_prefill(*args))
+        if i % 4 == 0:
+            other.mul_(1.0)
+    status_ok()
+    for x in outs:
+        assert torch.equal(x, o)
+
+
 def test_prefill_shared_tiles_repeat_bitwise():
     o, args = run_prefill([(33, 7000), (90, 2500)], 1, 8, 2, 128, 32, BF)
     for _ in range(5):
