@@ -542,10 +542,11 @@ int tp_q4_sharded_to_all_noalloc(int N, const void *const *x, int64_t T, int64_t
  * block_table[b * ld_table + i / page]; entries behind a sequence's last page
  * are not read, and rows that hold no position of a sequence may hold anything
  * (NaN too).
- * Page numbers, slots, positions and lengths are device data: one that is out
- * of range records TP_ERR_INVALID_ARG in the device status word
- * (tp_query_status); nothing outside the arrays is then read or written, and
- * the results of that token or sequence are unspecified.
+ * Page numbers, slots, positions, lengths and offsets are device data: one
+ * that is out of range (a length below 0 or above width * page; offsets that
+ * do not ascend within 0..T) records TP_ERR_INVALID_ARG in the device status
+ * word (tp_query_status); nothing outside the arrays is then read or written,
+ * and the results of that token or sequence are unspecified.
  *
  * tp_qkv_append: per-head norms, rotation, and the write into the cache, for T
  *   tokens of the fused projection's output.
@@ -586,7 +587,8 @@ int tp_q4_sharded_to_all_noalloc(int N, const void *const *x, int64_t T, int64_t
  *   With few tokens the key tiles of a block of them are shared between SMs and
  *   the parts joined in a fixed order (the same call gives the same bytes);
  *   that uses the per-(device, stream) workspace, 512 * (D + 2) * 4 bytes an SM.
- *   cu_seqlens int32 (B + 1), ascending; prefix_lens NULL or int32 (B).  A row
+ *   cu_seqlens int32 (B + 1), ascending; prefix_lens NULL or int32 (B): one
+ *   below 0 is none, one above its sequence's length the whole of it.  A row
  *   that sees nothing is zero, and so is a row of no sequence.
  *
  * tp_sample: one token per row of logits (B, V) in_dt (any tp_dtype), row

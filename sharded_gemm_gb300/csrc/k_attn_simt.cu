@@ -18,6 +18,11 @@ __global__ void __launch_bounds__(kWarps * 32) attn_simt_kernel(const __grid_con
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int64_t w = (int64_t)blockIdx.x * kWarps + warp;
   const int64_t rows = a.T * a.N * a.Hq;
+  if (a.cu_seqlens && lane == 0)
+    for (int64_t i = w; i < a.B; i += (int64_t)gridDim.x * kWarps) {
+      const int c0 = a.cu_seqlens[i], c1 = a.cu_seqlens[i + 1];
+      if (c0 < 0 || c1 < c0 || c1 > a.T) record_bad_value(a.status);
+    }
   if (w >= rows) return;
   const int hq = (int)(w % a.Hq);
   const int r = (int)(w / a.Hq % a.N);
@@ -41,8 +46,8 @@ __global__ void __launch_bounds__(kWarps * 32) attn_simt_kernel(const __grid_con
     n = a.seq_lens[b];
     pos = n - 1;
   }
-  if (n > a.width * a.page) {
-    n = a.width * a.page;
+  if (n < 0 || n > a.width * a.page) {
+    n = n < 0 ? 0 : a.width * a.page;
     if (lane == 0) record_bad_value(a.status);
   }
   const int64_t prefix = a.prefix_lens ? a.prefix_lens[b] : 0;

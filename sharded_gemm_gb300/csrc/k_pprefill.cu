@@ -237,11 +237,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       auto lengths = [&](int64_t b, int &to, int &prefix) {
         const int64_t cap = a.width << a.page_log2;
         int64_t n = a.seq_lens[b];
-        if (n > cap) {
-          n = cap;
+        if (n < 0 || n > cap) {
           record_bad_value(a.status);
+          n = n < 0 ? 0 : cap;
         }
-        to = n < 0 ? 0 : (int)n;
+        to = (int)n;
         const int pre = a.prefix_lens ? a.prefix_lens[b] : 0;
         prefix = pre < 0 ? 0 : pre > to ? to : pre;
       };

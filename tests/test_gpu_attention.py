@@ -335,6 +335,40 @@ def test_decode_bad_page_and_length_are_recorded(policy):
     assert tp.tp_query_status() == 0
 
 
+def test_negative_lengths_and_disordered_offsets_are_recorded(policy):
+    """A negative length is out of range, and counts as an empty sequence; so are offsets that do not ascend."""
+    _, (q, kc, vc, table, seq) = run_decode([40, 20, 33], 1, 2, 1, 64, 16, BF)
+    for n in (-1, -100000, -2 ** 31):
+        bad = seq.clone()
+        bad[1] = n
+        o = tp.tp_paged_decode(q, kc, vc, table, bad)
+        assert tp.tp_query_status() == tp.TP_ERR_INVALID_ARG
+        assert (o[0, 1] == 0).all()
+    o, (q, kc, vc, table, cu, seq, _) = run_prefill([(40, 0), (20, 4), (33, 50)], 1, 2, 1, 64, 16, BF)
+    for n in (-1, -100000, -2 ** 31):
+        bad = seq.clone()
+        bad[1] = n
+        got = tp.tp_paged_prefill(q, kc, vc, table, cu, bad)
+        assert tp.tp_query_status() == tp.TP_ERR_INVALID_ARG
+        assert (got[0, 40:60] == 0).all()
+    for at, n in ((0, -1), (1, 61), (3, 94), (2, 1000)):
+        bad = cu.clone()
+        bad[at] = n
+        tp.tp_paged_prefill(q, kc, vc, table, bad, seq)
+        assert tp.tp_query_status() == tp.TP_ERR_INVALID_ARG, (at, n)
+    assert torch.equal(tp.tp_paged_prefill(q, kc, vc, table, cu, seq), o)
+    status_ok()
+
+
+def test_prefix_lengths_beyond_the_sequence(policy):
+    """A prefix longer than its sequence is the whole of it, one below zero is none: no error."""
+    chunks = [(40, 30), (20, 4), (33, 50)]
+    same, args = run_prefill(chunks, 1, 4, 2, 64, 16, F16, prefix=[70, 0, 83])
+    over = torch.tensor([2 ** 31 - 1, -2 ** 31, 1000], dtype=torch.int32, device="cuda")
+    assert torch.equal(tp.tp_paged_prefill(*args[:6], over), same)
+    status_ok()
+
+
 def test_a_cache_beyond_32_bit_offsets():
     """Pages whose byte and element offsets pass 2^32 (a 17 GB key cache)."""
     Hk, page, D = 8, 256, 128
