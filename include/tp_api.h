@@ -543,8 +543,8 @@ int tp_q4_sharded_to_all_noalloc(int N, const void *const *x, int64_t T, int64_t
  * are not read, and rows that hold no position of a sequence may hold anything
  * (NaN too).
  * Page numbers, slots, positions, lengths and offsets are device data: one
- * that is out of range (a length below 0 or above width * page; offsets that
- * do not ascend within 0..T) records TP_ERR_INVALID_ARG in the device status
+ * that is out of range (a length below 0, above width * page or above 2^30;
+ * offsets that do not ascend within 0..T) records TP_ERR_INVALID_ARG in the device status
  * word (tp_query_status); nothing outside the arrays is then read or written,
  * and the results of that token or sequence are unspecified.
  *
@@ -608,7 +608,8 @@ int tp_q4_sharded_to_all_noalloc(int N, const void *const *x, int64_t T, int64_t
  *   under the row's own softmax (temperature 1, unfiltered).  A row without a
  *   logit above -inf gives token -1 and -inf.
  * Errors: TP_ERR_NOT_DIVISIBLE if Hq % Hk != 0; TP_ERR_UNSUPPORTED for a D,
- * page, rope_dim or V this build does not take; TP_ERR_ALIGNMENT for a pointer
+ * page, rope_dim or V this build does not take, or more than 2^30 rows of q in
+ * an attention; TP_ERR_ALIGNMENT for a pointer
  * not aligned to its element size (caches: 16 bytes); TP_ERR_INVALID_ARG for
  * null pointers, a row stride below the row, N outside 1..64, scale <= 0,
  * softcap < 0, window < 0.  T = 0 or B = 0 launches nothing.

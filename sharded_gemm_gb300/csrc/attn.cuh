@@ -15,6 +15,10 @@
 
 namespace tp {
 
+// Positions of a sequence and rows of q at most: sums of two of them, a tile's
+// end and a window's beginning stay inside 32 bits.
+constexpr int64_t kMostPositions = 1 << 30;
+
 struct AppendArgs {
   const void *qkv[kMaxShards];
   void *q[kMaxShards], *k_cache[kMaxShards], *v_cache[kMaxShards];
@@ -37,6 +41,7 @@ struct AttnArgs {
   const int32_t *cu_seqlens;   // (B + 1), or null: one query token per sequence
   const int32_t *prefix_lens;  // nullable, (B)
   int64_t T, B, ldq, ldo, pages, ld_page, ld_table, width;
+  int64_t cap;                 // positions that a row of the table holds, kMostPositions at most
   int N, Hq, Hk, D, page, page_log2;
   int dt, window;              // window 0: none
   float scale, softcap;        // softcap 0: none

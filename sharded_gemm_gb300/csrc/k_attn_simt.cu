@@ -46,8 +46,8 @@ __global__ void __launch_bounds__(kWarps * 32) attn_simt_kernel(const __grid_con
     n = a.seq_lens[b];
     pos = n - 1;
   }
-  if (n < 0 || n > a.width * a.page) {
-    n = n < 0 ? 0 : a.width * a.page;
+  if (n < 0 || n > a.cap) {
+    n = n < 0 ? 0 : a.cap;
     if (lane == 0) record_bad_value(a.status);
   }
   const int64_t prefix = a.prefix_lens ? a.prefix_lens[b] : 0;

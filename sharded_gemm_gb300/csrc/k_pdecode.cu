@@ -67,11 +67,10 @@ struct Span {
 };
 __device__ __forceinline__ Span span_of(const AttnArgs &a, int64_t b) {
   Span s;
-  const int64_t cap = a.width << a.page_log2;
   int64_t n = a.seq_lens[b];
-  if (n < 0 || n > cap) {
+  if (n < 0 || n > a.cap) {
     record_bad_value(a.status);
-    n = n < 0 ? 0 : cap;
+    n = n < 0 ? 0 : a.cap;
   }
   s.to = (int)n;
   s.first = a.window && s.to > a.window ? s.to - a.window : 0;

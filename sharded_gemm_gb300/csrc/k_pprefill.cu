@@ -235,11 +235,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       Walk &wk = ctl.walk;
       // a sequence's length and bidirectional part, inside what the table can hold
       auto lengths = [&](int64_t b, int &to, int &prefix) {
-        const int64_t cap = a.width << a.page_log2;
         int64_t n = a.seq_lens[b];
-        if (n < 0 || n > cap) {
+        if (n < 0 || n > a.cap) {
           record_bad_value(a.status);
-          n = n < 0 ? 0 : cap;
+          n = n < 0 ? 0 : a.cap;
         }
         to = (int)n;
         const int pre = a.prefix_lens ? a.prefix_lens[b] : 0;

@@ -61,6 +61,7 @@ int attn_args(AttnArgs &a, int N, const void *const *q, int64_t T, int64_t ldq, 
   if (int rc = check_cache(N, Hq, Hk, D, pages, page, ld_page, dt, k_cache, v_cache)) return rc;
   if (T < 0 || B < 0 || width < 0 || T > 0x7fffffff || B > 0x7fffffff || width > 0x7fffffff)
     return set_error(TP_ERR_INVALID_ARG, "T, B and width must be in 0..2^31 - 1");
+  if (T > kMostPositions) return set_error(TP_ERR_UNSUPPORTED, "T (%lld) above 2^30", (long long)T);
   if (!(scale > 0.0f) || scale > 3.0e38f) return set_error(TP_ERR_INVALID_ARG, "scale must be positive and finite");
   if (!(softcap >= 0.0f) || softcap > 3.0e38f)
     return set_error(TP_ERR_INVALID_ARG, "softcap must be finite and >= 0 (0: none)");
@@ -81,7 +82,10 @@ int attn_args(AttnArgs &a, int N, const void *const *q, int64_t T, int64_t ldq, 
   a.ld_table = ld_table, a.width = width;
   a.N = N, a.Hq = Hq, a.Hk = Hk, a.D = D, a.page = page;
   a.page_log2 = log2_of(page);
-  a.dt = dt, a.window = window, a.scale = scale, a.softcap = softcap;
+  const int64_t held = width << a.page_log2, most = kMostPositions;
+  a.cap = held < most ? held : most;
+  // a window of as many positions as there can be hides none
+  a.dt = dt, a.window = window < most ? window : (int)most, a.scale = scale, a.softcap = softcap;
   return TP_OK;
 }
 

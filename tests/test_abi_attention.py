@@ -120,3 +120,9 @@ def test_empty_calls_launch_nothing(L):
     assert _attn(L, True, T=0, B=0) == tp.TP_OK
     assert _sample(L, B=0) == tp.TP_OK
     assert L.tp_launch_count() == before
+
+
+@pytest.mark.parametrize("prefill", [False, True])
+def test_attention_of_more_than_2_to_30_rows_is_refused(L, prefill):
+    assert _attn(L, prefill, T=(1 << 30) + 1) == tp.TP_ERR_UNSUPPORTED
+    assert tp.tp_last_error()

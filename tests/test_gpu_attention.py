@@ -369,6 +369,46 @@ def test_prefix_lengths_beyond_the_sequence(policy):
     status_ok()
 
 
+def test_the_longest_sequences(policy):
+    """Positions up to 2^30 (a table of one page repeated, the window at the end); one more is out of range."""
+    page, D, W = 256, 64, 40
+    kc = torch.randn((1, 1, 1, page, D), device="cuda").to(BF)
+    vc = torch.randn((1, 1, 1, page, D), device="cuda").to(BF)
+    table = torch.zeros((1, 1 << 23), dtype=torch.int32, device="cuda")
+    q = torch.randn((1, 5, 2 * D), device="cuda").to(BF)
+    cu = torch.tensor([0, 5], dtype=torch.int32, device="cuda")
+    for n in (1 << 30, (1 << 30) - 77):
+        seq = torch.tensor([n], dtype=torch.int32, device="cuda")
+        o = tp.tp_paged_prefill(q, kc, vc, table, cu, seq, window=W)
+        d = tp.tp_paged_decode(q[:, 4:], kc, vc, table, seq, window=W)
+        status_ok()
+        at = torch.arange(n - 4 - W, n, device="cuda") % page  # what the five rows can see
+        kv = [(kc[:, 0][:, :, at], vc[:, 0][:, :, at])]
+        check_attention(o, q, kv, [(0, 5)], [W + 4], 2, 1, D, BF, D ** -0.5, 0.0, W)
+        check_attention(d, q[:, 4:], kv, [(0, 1)], [W + 4], 2, 1, D, BF, D ** -0.5, 0.0, W)
+    for n in ((1 << 30) + 1, (1 << 31) - 1):
+        seq = torch.tensor([n], dtype=torch.int32, device="cuda")
+        tp.tp_paged_prefill(q, kc, vc, table, cu, seq, window=W)
+        assert tp.tp_query_status() == tp.TP_ERR_INVALID_ARG
+        tp.tp_paged_decode(q[:, 4:], kc, vc, table, seq, window=W)
+        assert tp.tp_query_status() == tp.TP_ERR_INVALID_ARG
+
+
+def test_the_widest_window_hides_nothing(policy):
+    """A window of 2^31 - 1, with rows before the first position too, is no window."""
+    kc, vc, table, kv = paged([10, 300], 1, 1, 64, 16, BF, seed=8)
+    q = torch.randn((1, 320, 128), device="cuda").to(BF)
+    cu = torch.tensor([0, 17, 320], dtype=torch.int32, device="cuda")
+    seq = torch.tensor([10, 300], dtype=torch.int32, device="cuda")
+    for window in (2 ** 31 - 1, 2 ** 31 - 20, 2 ** 30):
+        o = tp.tp_paged_prefill(q, kc, vc, table, cu, seq, window=window)
+        status_ok()
+        assert torch.equal(o, tp.tp_paged_prefill(q, kc, vc, table, cu, seq))
+        check_attention(o, q, kv, [(0, 17), (17, 303)], [10, 300], 2, 1, 64, BF, 0.125, 0.0, 0)
+        d = tp.tp_paged_decode(q[:, :2], kc, vc, table, seq, window=window)
+        assert torch.equal(d, tp.tp_paged_decode(q[:, :2], kc, vc, table, seq))
+
+
 def test_a_cache_beyond_32_bit_offsets():
     """Pages whose byte and element offsets pass 2^32 (a 17 GB key cache)."""
     Hk, page, D = 8, 256, 128
