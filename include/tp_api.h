@@ -608,8 +608,8 @@ int tp_q4_sharded_to_all_noalloc(int N, const void *const *x, int64_t T, int64_t
  *   under the row's own softmax (temperature 1, unfiltered).  A row without a
  *   logit above -inf gives token -1 and -inf.
  * Errors: TP_ERR_NOT_DIVISIBLE if Hq % Hk != 0; TP_ERR_UNSUPPORTED for a D,
- * page, rope_dim or V this build does not take, or more than 2^30 rows of q in
- * an attention; TP_ERR_ALIGNMENT for a pointer
+ * page, rope_dim or V this build does not take, more than 2^30 rows of q in an
+ * attention or Hq + 2 Hk above 65535; TP_ERR_ALIGNMENT for a pointer
  * not aligned to its element size (caches: 16 bytes); TP_ERR_INVALID_ARG for
  * null pointers, a row stride below the row, N outside 1..64, scale <= 0,
  * softcap < 0, window < 0.  T = 0 or B = 0 launches nothing.

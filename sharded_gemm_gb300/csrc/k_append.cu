@@ -305,7 +305,7 @@ int launch(const AppendArgs &a, cudaStream_t s) {
   }
   vec.rope = aligned(a.rope, 16), vec.gain = aligned(a.q_norm, 16) && aligned(a.k_norm, 16);
   const int64_t blocks = (a.T + kTokens - 1) / kTokens;
-  if (blocks > 0x7fffffff || H > 65535) return set_error(TP_ERR_UNSUPPORTED, "too many tokens or heads for one launch");
+  if (blocks > 0x7fffffff) return set_error(TP_ERR_UNSUPPORTED, "too many tokens for one launch");
   cudaError_t e;
   using R = Ring<TIn>;
   const int stretches = (H + R::kHeads - 1) / R::kHeads;

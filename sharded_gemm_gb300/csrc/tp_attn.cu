@@ -22,6 +22,8 @@ int check_cache(int N, int Hq, int Hk, int D, int64_t pages, int page, int64_t l
   if (N < 1 || N > kMaxShards) return set_error(TP_ERR_INVALID_ARG, "N must be in 1..%d", kMaxShards);
   if (!is16(dt)) return set_error(TP_ERR_INVALID_ARG, "the cache holds TP_BF16 or TP_F16");
   if (Hq < 1 || Hk < 1) return set_error(TP_ERR_INVALID_ARG, "need Hq >= 1, Hk >= 1");
+  if ((int64_t)Hq + 2ll * Hk > 65535)  // a launch's second dimension; N * Hq * D then fits 32 bits too
+    return set_error(TP_ERR_UNSUPPORTED, "%d query and %d key-value heads: Hq + 2 Hk must be at most 65535", Hq, Hk);
   if (Hq % Hk)
     return set_error(TP_ERR_NOT_DIVISIBLE, "%d query heads cannot share %d key-value heads evenly", Hq, Hk);
   if (D != 64 && D != 128) return set_error(TP_ERR_UNSUPPORTED, "head size %d: only 64 and 128 are supported", D);

@@ -126,3 +126,13 @@ def test_empty_calls_launch_nothing(L):
 def test_attention_of_more_than_2_to_30_rows_is_refused(L, prefill):
     assert _attn(L, prefill, T=(1 << 30) + 1) == tp.TP_ERR_UNSUPPORTED
     assert tp.tp_last_error()
+
+
+@pytest.mark.parametrize("heads", [dict(Hq=65534, Hk=1), dict(Hq=1 << 30, Hk=1 << 30), dict(Hq=(1 << 31) - 1, Hk=1),
+                                   dict(Hq=65536, Hk=4)])
+def test_too_many_heads_are_refused(L, heads):
+    """Before any product of them is taken in 32 bits."""
+    wide = dict(ldp=1 << 45)
+    assert _append(L, ld=1 << 40, ldq=1 << 40, **heads, **wide) == tp.TP_ERR_UNSUPPORTED
+    for prefill in (False, True):
+        assert _attn(L, prefill, ldq=1 << 40, ldo=1 << 40, **heads, **wide) == tp.TP_ERR_UNSUPPORTED
