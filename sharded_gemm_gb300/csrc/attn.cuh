@@ -70,6 +70,7 @@ template <typename T>
 struct Half2;  // packed pairs of the 16-bit types
 template <>
 struct Half2<__nv_bfloat16> {
+  typedef __nv_bfloat162 Pair;
   static constexpr bool kBf16 = true;
   static __device__ __forceinline__ uint32_t pack(float a, float b) {
     __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
@@ -81,6 +82,7 @@ struct Half2<__nv_bfloat16> {
 };
 template <>
 struct Half2<__half> {
+  typedef __half2 Pair;
   static constexpr bool kBf16 = false;
   static __device__ __forceinline__ uint32_t pack(float a, float b) {
     __half2 v = __floats2half2_rn(a, b);

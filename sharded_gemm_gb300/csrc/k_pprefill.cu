@@ -27,7 +27,9 @@
 // rows, in CTA order.  One token over 16384 positions, 32 heads on 8: 167 us whole, 37 so;
 // 64 over 32768: 331, 76; 512 over 8192: 96, 64; 2048 over 16384: 335, 311.
 // Rows of a value tile behind the sequence's end (or in pages that are not
-// read) are written as zeros: stale rows never meet a product.
+// read) are written as zeros: stale rows never meet a product.  A value within the
+// sequence that is not finite does, with the terms 0 of rows that do not see it:
+// their sums are NaN, which is noticed, and these rows are computed again (redo_rows).
 //
 // Tensor rate bounds long chunks: 4 D flop per visible pair.  Of it, what holds
 // the kernel back is shared memory: Q K^T reads both operands from there, 128
@@ -169,6 +171,157 @@ __device__ __forceinline__ void token_range(const AttnArgs &a, int64_t b, int64_
   t0 = c0 < 0 ? 0 : c0 > a.T ? a.T : c0;
   t1 = c1 < t0 ? t0 : c1 > a.T ? a.T : c1;
   if (c0 != t0 || c1 != t1) record_bad_value(a.status);
+}
+
+// Outputs of a warp's rows again (those of the lanes set in `rows`, of one sequence and key-value
+// head), on the CUDA cores, each from the positions that it sees alone.  Four rows at a time: a lane
+// has their scores with one of 32 positions, and every 32nd of their values.  A row is known by its
+// output's address, and all else found again from that: the softmax warps, whose registers are full,
+// would have to keep it (2 x 1024 tokens over 4000..8192 took 179 us so, 175 as it is, 173 without any
+// of this).  Rare, and slow: 512 tokens over 65536 positions, 8 heads of 128, take 0.14 ms and with a
+// last value that is not finite 278.
+template <typename T, int D>
+__device__ __noinline__ void redo_rows(const AttnArgs &a, bool vec_q, uint32_t rows, T *out) {
+  constexpr int E = D / 32, R = 4;
+  const int lane = threadIdx.x % 32, first = __ffs(rows) - 1;
+  // the rank whose output the rows are in (the ranks' may be column blocks of one matrix), token and head
+  int r = 0, hq = 0;
+  int64_t tok = 0;
+  for (; r < a.N; ++r) {
+    const int64_t off = out - static_cast<const T *>(a.o[r]);
+    tok = off / a.ldo;
+    const int64_t col = off - tok * a.ldo;
+    hq = (int)(col / D);
+    if (__shfl_sync(0xffffffffu, off >= 0 && tok < a.T && col < (int64_t)a.Hq * D, first)) break;
+  }
+  if (r == a.N) return;
+  const T *k_cache = static_cast<const T *>(a.k_cache[r]), *v_cache = static_cast<const T *>(a.v_cache[r]);
+  const int h = __shfl_sync(0xffffffffu, hq, first) / (a.Hq / a.Hk);
+  int64_t b = 0;  // the last sequence whose first token is not behind the rows'
+  for (int64_t top = a.B, t0 = __shfl_sync(0xffffffffu, tok, first); top - b > 1;) {
+    const int64_t mid = (b + top) / 2;
+    if (a.cu_seqlens[mid] <= t0) b = mid; else top = mid;
+  }
+  // the lane's row sees [lo, hi) and [0, prefix)
+  const int64_t len = a.seq_lens[b], n = len < 0 ? 0 : len > a.cap ? a.cap : len;
+  const int64_t pos = n - a.cu_seqlens[b + 1] + tok, pre = a.prefix_lens ? a.prefix_lens[b] : 0;
+  const int prefix = (int)(pre < 0 ? 0 : pre > n ? n : pre);
+  const int lo = (int)(a.window && pos - a.window + 1 > 0 ? pos - a.window + 1 : 0), hi = (int)(pos + 1 < n ? pos + 1 : n);
+  const uint16_t *q = static_cast<const uint16_t *>(a.q[r]) + tok * a.ldq + (int64_t)hq * D;
+  for (int f0 = 0; f0 < 32; f0 += R) {
+    const uint32_t some = rows >> f0 & ((1u << R) - 1);
+    if (!some) continue;
+    const bool mine = rows >> lane & 1 && lane / R == f0 / R;
+    const int from = (int)__reduce_min_sync(0xffffffffu, mine ? (prefix > 0 ? 0 : lo) : 0x7fffffff) & ~31;
+    const int end = __reduce_max_sync(0xffffffffu, mine ? max(hi, prefix) : 0);
+    const uint16_t *qr[R];
+    float m[R], l[R], acc[R][E];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      qr[i] = reinterpret_cast<const uint16_t *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(q), f0 + i));
+      m[i] = -INFINITY, l[i] = 0.0f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[i][e] = 0.0f;
+    }
+#pragma unroll 1
+    for (int j0 = from; j0 < end; j0 += 32) {
+      const int j = j0 + lane;
+      int64_t row = -1;
+      if (j < end) {
+        const int pg = a.block_table[b * a.ld_table + (j >> a.page_log2)];
+        if (pg >= 0 && pg < a.pages) row = pg * a.ld_page + ((int64_t)h * a.page + (j & (a.page - 1))) * D;
+      }
+      float p[R];
+#pragma unroll
+      for (int i = 0; i < R; ++i) p[i] = 0.0f;
+      if (row >= 0) {
+#pragma unroll 4
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 x = *reinterpret_cast<const uint4 *>(k_cache + row + c * 8);
+          const uint32_t k[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int i = 0; i < R; ++i) {
+            if (!(some >> i & 1)) continue;
+            uint32_t qq[4];
+            if (vec_q) {
+              const uint4 y = __ldg(reinterpret_cast<const uint4 *>(qr[i] + c * 8));
+              qq[0] = y.x, qq[1] = y.y, qq[2] = y.z, qq[3] = y.w;
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                qq[e] = (uint32_t)__ldg(qr[i] + c * 8 + 2 * e) | (uint32_t)__ldg(qr[i] + c * 8 + 2 * e + 1) << 16;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 kf = Half2<T>::unpack(k[e]), qf = Half2<T>::unpack(qq[e]);
+              p[i] = fmaf(qf.x, kf.x, fmaf(qf.y, kf.y, p[i]));
+            }
+          }
+        }
+      }
+      uint32_t seen[R], any = 0;
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const int lo_i = __shfl_sync(0xffffffffu, lo, f0 + i), hi_i = __shfl_sync(0xffffffffu, hi, f0 + i);
+        const float log2e = 1.4426950408889634f;
+        const bool is = row >= 0 && (some >> i & 1) && ((j >= lo_i && j < hi_i) || j < prefix);
+        seen[i] = __ballot_sync(0xffffffffu, is);
+        any |= seen[i];
+        float s = a.softcap > 0.0f ? capped(p[i] * (2.0f * log2e * a.scale / a.softcap), a.softcap * log2e)
+                                   : p[i] * (a.scale * log2e);
+        if (!is) s = -INFINITY;
+        float top = s, sum;
+#pragma unroll
+        for (int x = 16; x > 0; x /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+        top = fmaxf(top, m[i]);
+        const float to = top == -INFINITY ? 0.0f : top, keep = exp2_approx(m[i] - to);
+        m[i] = top;
+        sum = p[i] = exp2_approx(s - to);
+#pragma unroll
+        for (int x = 16; x > 0; x /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+        l[i] = fmaf(l[i], keep, sum);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[i][e] *= keep;
+      }
+      if (!any) continue;
+#pragma unroll 1
+      for (int x0 = 0; x0 < 32; x0 += 8) {
+        // eight positions' values at a time, loaded whether seen or not (position 0 of page 0 where
+        // there is no page), and used where seen
+        T v[8][E];
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          const int64_t at = __shfl_sync(0xffffffffu, row < 0 ? 0 : row, x0 + x);
+#pragma unroll
+          for (int e = 0; e < E; ++e) v[x][e] = v_cache[at + lane + 32 * e];
+        }
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+#pragma unroll
+          for (int i = 0; i < R; ++i) {
+            const float pi = __shfl_sync(0xffffffffu, p[i], x0 + x);
+            const bool is = seen[i] >> (x0 + x) & 1;
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[i][e] = is ? fmaf(pi, static_cast<float>(v[x][e]), acc[i][e]) : acc[i][e];
+          }
+      }
+      bool lost = true;  // nothing behind this changes the rows any more
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int e = 0; e < E; ++e) lost = lost && (isnan(acc[i][e]) || !(some >> i & 1));
+      if (__all_sync(0xffffffffu, lost)) break;
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      T *o = reinterpret_cast<T *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(out), f0 + i));
+      const float inv = l[i] == 0.0f ? 0.0f : 1.0f / l[i];
+      if (some >> i & 1) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[lane + 32 * e] = static_cast<T>(acc[i][e] * inv);
+      }
+    }
+  }
 }
 
 template <typename T, int D, int MAXN>
@@ -913,6 +1066,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         l = sum;
       }
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      bool nan = false;
 #pragma unroll 1
       for (int c0 = 0; c0 < D / 32; c0 += 32 / rows) {
         const int c = c0 + g;
@@ -949,6 +1103,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           uint32_t pk[16];
 #pragma unroll
           for (int x = 0; x < 16; ++x) pk[x] = Half2<T>::pack(o[2 * x] * inv, o[2 * x + 1] * inv);
+          auto as2 = [](const uint32_t &u) { return *reinterpret_cast<const typename Half2<T>::Pair *>(&u); };
+          auto top2 = as2(pk[0]), low2 = as2(pk[1]);
+#pragma unroll
+          for (int x = 2; x < 16; x += 2) top2 = __hmax2_nan(top2, as2(pk[x])), low2 = __hmax2_nan(low2, as2(pk[x + 1]));
+          top2 = __hmax2_nan(top2, low2);
+          nan |= __hisnan(top2.x) || __hisnan(top2.y);
           if (pa.vec_o) {
 #pragma unroll
             for (int x = 0; x < 4; ++x)
@@ -960,6 +1120,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             for (int x = 0; x < 16; ++x) p[2 * x] = (uint16_t)pk[x], p[2 * x + 1] = (uint16_t)(pk[x] >> 16);
           }
         }
+        __syncwarp();
+      }
+      // A value of the tile that is not finite gives NaN in rows that do not see it as well (0 times
+      // it): rows whose scores are numbers and whose sums are not are taken again.  (The check costs
+      // 1 us of 173, packed and with the maximum that keeps NaN; a chain of compares, 3.)
+      uint32_t redo = __ballot_sync(0xffffffffu, nan && !isnan(inv));
+      if (redo) {
+        if (rows <= 16) redo |= redo >> 16;
+        if (rows == 8) redo |= redo >> 8;
+        redo_rows<T, D>(a, pa.vec_q, rows < 32 ? redo & ((1u << rows) - 1) : redo, out);
         __syncwarp();
       }
       tc_fence_before();

@@ -534,6 +534,66 @@ def test_prefill_joins_of_few_and_many_rows_repeat(tokens, Hq, Hk, D):
         assert torch.equal(x, o)
 
 
+@pytest.mark.parametrize("chunks,N,Hq,Hk,D,page,dt,cap,window,prefix", [
+    ([(1, 0), (130, 0), (37, 200)], 1, 4, 2, 64, 16, BF, 0.0, 0, None),
+    ([(600, 100), (3, 500)], 2, 6, 2, 128, 32, F16, 0.0, 90, None),
+    ([(300, 100), (90, 0)], 1, 7, 1, 128, 128, BF, 20.0, 0, [150, 20]),
+    ([(260, 40)], 1, 130, 1, 64, 16, BF, 0.0, 33, [60]),
+    ([(5, 6000)], 2, 8, 2, 128, 64, BF, 0.0, 0, None),  # from here on key tiles shared between CTAs
+    ([(40, 5000), (9, 700)], 1, 4, 1, 64, 16, F16, 0.0, 0, None),
+    ([(64, 8192)], 1, 4, 4, 128, 128, BF, 30.0, 3000, None)])
+def test_prefill_values_that_are_not_finite(policy, chunks, N, Hq, Hk, D, page, dt, cap, window, prefix):
+    """Infinities and NaN in the values (whole rows, and single columns) and keys of single positions: a row that
+    does not see the position is as without it."""
+    chunks = [(min(a, b) if b > 1000 else a, b) for a, b in chunks]
+    lens = [m + c for m, c in chunks]
+    kc, vc, table, kv = paged(lens, N, Hk, D, page, dt, seed=3)
+    g = torch.Generator().manual_seed(len(chunks) + Hq)
+    poison = []  # of each sequence: (n, D), which values are not finite
+    for b, n in enumerate(lens):
+        mark = torch.zeros((n, D), dtype=torch.bool, device="cuda")
+        # the last positions, which most of the chunk's rows do not see, and some others
+        for i, j in enumerate({n - 1, max(0, n - 3), min(n - 1, n - chunks[b][0] // 2), int(torch.randint(n, (1,), generator=g))}):
+            cols = slice(None) if i % 2 else slice(5, 6)
+            at = int(table[b, j // page])
+            row = vc[:, at, :, j % page]  # a view: (N, Hk, D)
+            row[..., cols] = [NAN, float("inf"), -float("inf")][i % 3]
+            kv[b][1][:, :, j, cols] = 0.0
+            mark[j, cols] = True
+            if i % 2 and j == n - 1 and chunks[b][0] > 1:  # its key too: rows that see it are NaN all over
+                kc[:, at, :, j % page] = NAN
+                mark[j] = True
+                kv[b][0][:, :, j] = 0.0
+        poison.append(mark)
+    cu = np.concatenate([[0], np.cumsum([m for m, _ in chunks])]).astype(np.int32)
+    q = torch.randn((N, int(cu[-1]), Hq * D), device="cuda", generator=torch.Generator(device="cuda").manual_seed(1)).to(dt)
+    wide = torch.empty((N, int(cu[-1]), Hq * D + 1), dtype=dt, device="cuda")
+    seq = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    pre = torch.tensor(prefix, dtype=torch.int32, device="cuda") if prefix else None
+    for out in (torch.empty_like(q), wide[..., 1:]):
+        o = tp.tp_paged_prefill(q, kc, vc, table, torch.from_numpy(cu).cuda(), seq, pre, softcap=cap, window=window, out=out)
+        status_ok()
+        clean, hit = o.clone(), torch.zeros(q.shape, dtype=torch.bool, device="cuda")
+        for b, n in enumerate(lens):
+            m, t0 = chunks[b][0], int(cu[b])
+            pos, j = n - m + torch.arange(m, device="cuda")[:, None], torch.arange(n, device="cuda")[None]
+            seen = (j <= pos) & (j > pos - window if window else j >= 0) | (j < (prefix[b] if prefix else 0))
+            bad = (seen.double() @ poison[b].double()) > 0  # (m, D)
+            hit[:, t0:t0 + m] = bad.repeat(1, Hq)
+            # what sees a poisoned position is not compared with the reference, which lacks it
+            for r in range(N):
+                for h in range(Hk):
+                    G = Hq // Hk
+                    ref, mass = attn_ref(q[r, t0:t0 + m].reshape(m, Hq, D)[:, h * G:(h + 1) * G], kv[b][0][r, h],
+                                         kv[b][1][r, h], seen, D ** -0.5, cap)
+                    got = clean[r, t0:t0 + m].reshape(m, Hq, D)[:, h * G:(h + 1) * G].double()
+                    tol = U[dt] * ref.abs() + (U[dt] + 2.0 ** -13) * mass + 2.0 ** -24
+                    if dt == torch.float16:
+                        tol = tol + n * 2.0 ** -25 * 6
+                    assert (((got - ref).abs() <= tol) | bad[:, None]).all(), (b, r, h)
+        assert torch.isfinite(o[~hit]).all() and not torch.isfinite(o[hit]).any()
+
+
 def test_prefill_shared_tiles_repeat_bitwise():
     o, args = run_prefill([(33, 7000), (90, 2500)], 1, 8, 2, 128, 32, BF)
     for _ in range(5):
