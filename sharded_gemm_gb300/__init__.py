@@ -4,7 +4,7 @@ Argument marshalling only: every function here checks that the tensors it
 is given can be described to the C ABI (device, dtype, row-major strides),
 passes their device pointers and sizes, and enqueues the call on the current
 torch CUDA stream (through ctypes; the attention-side functions through a small
-extension module, _marshal.so).  All arithmetic runs in the library's CUDA kernels.  There
+extension module, _marshal).  All arithmetic runs in the library's CUDA kernels.  There
 is no fallback: if libtp.so is missing or fails to load, every call raises.
 
 Function names are the C names.  Tensors are torch CUDA tensors; bf16 / f16 /
@@ -15,13 +15,14 @@ quantization biases are float16.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
 import os
 import re
 import threading
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libtp.so")
-MARSHAL_PATH = os.path.join(HERE, "_marshal.so")
+MARSHAL_PATH = os.path.join(HERE, "_marshal" + importlib.machinery.EXTENSION_SUFFIXES[0])
 HEADER = os.path.join(os.path.dirname(HERE), "include", "tp_api.h")
 
 TP_OK, TP_ERR_INVALID_ARG, TP_ERR_NOT_DIVISIBLE, TP_ERR_ALIGNMENT = 0, -1, -2, -3
@@ -787,7 +788,8 @@ def _marshaller():
     global _native
     if _native is None:
         if not os.path.exists(MARSHAL_PATH):
-            raise RuntimeError("_marshal.so is not built (%s); run `python -m sharded_gemm_gb300.build`" % MARSHAL_PATH)
+            raise RuntimeError("_marshal is not built (%s); run `python -m sharded_gemm_gb300.build` (it needs Python's "
+                               "headers)" % MARSHAL_PATH)
         from . import _marshal as m
         torch = _torch()
         m.init(torch.float32, torch.bfloat16, torch.float16, torch.int32, torch.int64,

@@ -1,5 +1,6 @@
 """Build libtp.so in-tree: one nvcc process per translation unit, in parallel,
-then one link (sm_103a only), and the binding's extension module _marshal.so.
+then one link (sm_103a only), and the binding's extension module _marshal,
+named for the interpreter that it is built against.
 
     python -m sharded_gemm_gb300.build [--force] [--verbose]
 """
@@ -7,6 +8,7 @@ from __future__ import annotations
 
 import argparse
 import concurrent.futures as cf
+import importlib.machinery
 import os
 import shutil
 import subprocess
@@ -19,7 +21,8 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libtp.so")
 MARSHAL_SRC = os.path.join(CSRC, "marshal.c")
-MARSHAL = os.path.join(HERE, "_marshal.so")
+# one file for each Python version: another one's is not imported
+MARSHAL = os.path.join(HERE, "_marshal" + importlib.machinery.EXTENSION_SUFFIXES[0])
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2",
@@ -49,14 +52,21 @@ def _stale(target: str, deps: list[str]) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
-def build_marshal(force: bool = False) -> str:
-    """The extension module: C against Python's headers, no CUDA."""
+def build_marshal(force: bool = False) -> str | None:
+    """The extension module: C against Python's headers, no CUDA.  Where they are not installed, None: the
+    library works without it, and the attention-side functions of the binding say what is missing."""
     if force or _stale(MARSHAL, [MARSHAL_SRC] + headers()):
+        include = sysconfig.get_paths()["include"]
+        if not os.path.exists(os.path.join(include, "Python.h")):
+            sys.stderr.write("no Python.h in %s: %s is not built\n" % (include, os.path.basename(MARSHAL)))
+            if os.path.exists(MARSHAL):  # of older sources
+                os.remove(MARSHAL)
+            return None
         cc = os.environ.get("CC") or shutil.which("gcc") or shutil.which("cc")
         if not cc:
             raise RuntimeError("no C compiler found for %s" % MARSHAL_SRC)
         tmp = MARSHAL + ".tmp%d" % os.getpid()
-        r = subprocess.run([cc, "-O2", "-fPIC", "-shared", "-I" + sysconfig.get_paths()["include"], "-I" + INCLUDE,
+        r = subprocess.run([cc, "-O2", "-fPIC", "-shared", "-I" + include, "-I" + INCLUDE,
                             MARSHAL_SRC, "-o", tmp], capture_output=True, text=True)
         if r.returncode != 0:
             sys.stderr.write(r.stdout + r.stderr)
@@ -67,7 +77,6 @@ def build_marshal(force: bool = False) -> str:
 
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    build_marshal(force)
     cc = nvcc()
     hdrs = headers()
     flags = NVCC_FLAGS + list(extra or [])
@@ -95,6 +104,7 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
             sys.stderr.write(r.stdout + r.stderr)
             raise RuntimeError("link of libtp.so failed")
         os.replace(tmp, LIB)
+    build_marshal(force)
     return LIB
 
 
