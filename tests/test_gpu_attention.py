@@ -113,6 +113,99 @@ def test_append(T, N, Hq, Hk, D, page, rot, inter, norm, in_dt, dt):
     assert torch.equal(kc, k0) and torch.equal(vc, v0)  # nothing else was written
 
 
+F32 = torch.float32
+
+
+def takes_ring(T, N, Hq, Hk, D):
+    """Whether an append of aligned rows is a prompt batch: its blocks of tokens fill the GPU twice."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    tokens, stretches = 256 // (D // 8), -(-(Hq + 2 * Hk) // 4)
+    return -(-T // tokens) >= 2 * -(-3 * sms // (stretches * N))
+
+
+@pytest.mark.parametrize("T,N,Hq,Hk,D,page,rot,inter,norms,in_dt,dt", [
+    (16391, 1, 6, 2, 64, 16, 64, False, "qk", F32, torch.bfloat16),
+    (8209, 1, 2, 2, 128, 64, 128, True, "qk", torch.bfloat16, torch.bfloat16),
+    (3001, 8, 7, 1, 128, 256, 16, True, "qk", torch.float16, torch.bfloat16),
+    (3001, 8, 5, 1, 64, 32, 48, False, "q", F32, torch.float16),
+    (3000, 8, 2, 1, 128, 16, 128, False, "k", F32, torch.bfloat16),
+    (8199, 4, 1, 1, 64, 16, 0, False, "", torch.bfloat16, torch.float16),
+    (4099, 4, 4, 4, 64, 128, 32, True, "qk", F32, torch.bfloat16),
+    (1500, 64, 1, 1, 128, 64, 128, False, "qk", torch.float16, torch.float16),
+    (5003, 2, 9, 3, 128, 64, 0, False, "k", F32, torch.float16)])
+@pytest.mark.parametrize("odd_out", [False, True])
+def test_append_prompt_batches(T, N, Hq, Hk, D, page, rot, inter, norms, in_dt, dt, odd_out):
+    """Prompt batches, which the ring kernel takes: stretches of four heads that mix queries, keys and values and
+    do not end with them, tokens that do not end with a block, padding, and query rows without alignment."""
+    assert takes_ring(T, N, Hq, Hk, D)
+    g = torch.Generator(device="cuda").manual_seed(T + N)
+    rng = np.random.default_rng(T * N)
+    pages = -(-T // page) + 3
+    wide = (Hq + 2 * Hk) * D
+    qkv = [torch.randn((T, wide + 8), generator=g, device="cuda").to(in_dt)[:, :wide] for _ in range(N)]
+    kc = torch.randn((N, pages, Hk, page, D), generator=g, device="cuda").to(dt)
+    vc = torch.randn((N, pages, Hk, page, D), generator=g, device="cuda").to(dt)
+    slots = torch.from_numpy(rng.permutation(pages * page)[:T].astype(np.int64)).cuda()
+    slots[torch.from_numpy(rng.integers(0, T, 20)).cuda()] = -1
+    slots[T - 1] = -(1 << 40)
+    pos = torch.from_numpy(rng.integers(0, 500, T).astype(np.int32)).cuda()
+    rope = rope_table(500, rot) if rot else None
+    qn = torch.rand(D, generator=g, device="cuda") + 0.5 if "q" in norms else None
+    kn = torch.rand(D, generator=g, device="cuda") + 0.5 if "k" in norms else None
+    k0, v0 = kc.clone(), vc.clone()
+    obuf = torch.full((N, T, Hq * D + 6), 7.0, device="cuda").to(dt)
+    lo = 3 if odd_out else 0
+    tp.tp_qkv_append(qkv, kc, vc, slots, positions=pos, rope=rope, q_norm=qn, k_norm=kn, eps=1e-5, interleaved=inter,
+                     out=obuf[:, :, lo:lo + Hq * D])
+    status_ok()
+    live = slots >= 0
+    at, off = slots[live] // page, slots[live] % page
+    for r in range(N):
+        rq, rk, rv = append_ref(qkv[r], Hq, Hk, D, qn, kn, 1e-5, rope, pos, inter)
+        got = obuf[r, :, lo:lo + Hq * D].double().cpu().reshape(T, Hq, D)
+        big = rq.abs().amax(-1, keepdim=True)
+        assert ((got - rq).abs() <= U[dt] * rq.abs() + 2.0 ** -20 * big + 2.0 ** -24).all()
+        gk = kc[r][at, :, off].double().cpu()
+        rk, rv = rk[live.cpu()], rv[live.cpu()]
+        assert ((gk - rk).abs() <= U[dt] * rk.abs() + 2.0 ** -20 * rk.abs().amax(-1, keepdim=True) + 2.0 ** -24).all()
+        assert torch.equal(vc[r][at, :, off].cpu(), rv.to(dt))
+        k0[r][at, :, off], v0[r][at, :, off] = kc[r][at, :, off], vc[r][at, :, off]
+    assert torch.equal(kc, k0) and torch.equal(vc, v0)  # nothing else was written
+    assert (obuf[:, :, :lo] == 7).all() and (obuf[:, :, lo + Hq * D:] == 7).all()
+
+
+@pytest.mark.parametrize("in_dt", [F32, torch.bfloat16])
+def test_append_prompt_batch_with_bad_slots_and_positions(in_dt):
+    """They are recorded; every other token is as without them."""
+    T, N, Hq, Hk, D, page = 4099, 2, 6, 1, 128, 16
+    assert takes_ring(T, N, Hq, Hk, D)
+    pages = -(-T // page) + 1
+    qkv = torch.randn((N, T, (Hq + 2 * Hk) * D), device="cuda").to(in_dt)
+    kc = torch.zeros((N, pages, Hk, page, D), dtype=torch.bfloat16, device="cuda")
+    vc = torch.zeros_like(kc)
+    slots, pos = torch.arange(T, device="cuda"), torch.arange(T, dtype=torch.int32, device="cuda") % 90
+    rope = rope_table(90, D)
+    q = tp.tp_qkv_append(qkv, kc, vc, slots, positions=pos, rope=rope)
+    status_ok()
+    for bad_slot, bad_pos in ((pages * page, None), (1 << 60, None), (None, 90), (None, -1), (None, 2 ** 31 - 1)):
+        k2, v2, s2, p2 = torch.zeros_like(kc), torch.zeros_like(vc), slots.clone(), pos.clone()
+        if bad_slot is not None:
+            s2[[5, T - 1]] = bad_slot
+        else:
+            p2[[5, T - 1]] = bad_pos
+        q2 = tp.tp_qkv_append(qkv, k2, v2, s2, positions=p2, rope=rope)
+        assert tp.tp_query_status() == tp.TP_ERR_INVALID_ARG
+        rest = torch.ones(T, dtype=torch.bool, device="cuda")
+        rest[[5, T - 1]] = False
+        at, off = slots[rest] // page, slots[rest] % page
+        assert torch.equal(q2[:, rest], q[:, rest])
+        assert torch.equal(k2[:, at, :, off], kc[:, at, :, off]) and torch.equal(v2[:, at, :, off], vc[:, at, :, off])
+        if bad_slot is not None:  # and nothing is written for them
+            lost = slots[~rest]
+            assert (k2[:, lost // page, :, lost % page] == 0).all() and (v2[:, lost // page, :, lost % page] == 0).all()
+    status_ok()
+
+
 def test_append_strides_and_unaligned_rows():
     T, Hq, Hk, D, page = 19, 3, 1, 64, 16
     g = torch.Generator(device="cuda").manual_seed(5)
