@@ -563,6 +563,15 @@ def test_prefill(policy, chunks, N, Hq, Hk, D, page, dt, cap, window, prefix):
     run_prefill(chunks, N, Hq, Hk, D, page, dt, cap, window, prefix)
 
 
+@pytest.mark.parametrize("N,Hq,Hk,D,chunks", [(9, 2, 1, 64, [(40, 3), (1, 100)]), (64, 1, 1, 128, [(130, 0)]),
+                                              (64, 3, 1, 64, [(3, 4000), (2, 17)]), (33, 2, 2, 128, [(300, 200)])])
+@pytest.mark.parametrize("dt", [BF, F16])
+def test_attention_of_many_ranks(policy, N, Hq, Hk, D, chunks, dt):
+    """More than eight ranks in one call, up to 64: prefill has a form of its own for them."""
+    run_prefill(chunks, N, Hq, Hk, D, 16, dt, prefix=[20] * len(chunks))
+    run_decode([m + c for m, c in chunks], N, Hq, Hk, D, 16, dt)
+
+
 def test_prefill_large_scores(policy):
     run_prefill([(260, 100), (33, 0)], 1, 8, 2, 128, 16, BF, std=30.0)
 
