@@ -752,6 +752,58 @@ def test_prefill_bad_page_and_length_are_recorded(policy):
     assert tp.tp_query_status() == 0
 
 
+# ------------------------------------------------------------------ float16 over long rows
+def float16_reference(q, k, v, seen, scale):
+    """q (R, G, D), k / v (n, D), seen (R, n) in float64: the output, its tolerance, and the smallest of any 128
+    consecutive positions' largest share of the tolerance, were they left out.
+
+    A term e = 2^(s - m) is rounded by 2^-11 of itself, or by 2^-25 where it is below 2^-14.  Every m is a score of
+    the row (that of a part of it), so relative to the row's largest score the latter is 2^-25 at most, and 2^-25
+    sum |v_j| / L of the output, L being the softmax's sum relative to that score."""
+    u = U[torch.float16]
+    s = torch.einsum("rgd,nd->rgn", q.double(), k.double()) * scale
+    s = s.masked_fill(~seen[:, None], -float("inf"))
+    e = torch.exp(s - s.amax(-1, keepdim=True))
+    L = e.sum(-1, keepdim=True)
+    v = v.double()
+    sums = torch.einsum("rgn,nd->rgd", e, v)
+    ref, mass = sums / L, torch.einsum("rgn,nd->rgd", e, v.abs()) / L
+    small = torch.einsum("rn,nd->rd", seen.double(), v.abs())[:, None] * 2.0 ** -25 / L
+    tol = u * ref.abs() + (u + 2.0 ** -13) * mass + small + 2.0 ** -25
+    least = float("inf")
+    for j in range(0, k.shape[0], 128):
+        part = torch.einsum("rgn,nd->rgd", e[..., j:j + 128], v[j:j + 128])
+        rest = L - e[..., j:j + 128].sum(-1, keepdim=True)
+        without = torch.where(rest > 0, (sums - part) / rest, 0.0)
+        least = min(least, float(((without - ref).abs() / tol).max()))
+    return ref, tol, least
+
+
+@pytest.mark.parametrize("tokens,n,Hq,Hk,D,page", [(1, 20060, 8, 1, 64, 16), (1, 9061, 4, 2, 128, 64),
+                                                   (1, 4190, 32, 8, 128, 16), (4, 16100, 8, 2, 128, 64),
+                                                   (40, 5080, 4, 1, 64, 16), (3, 20063, 4, 2, 64, 256)])
+def test_float16_long_rows(policy, tokens, n, Hq, Hk, D, page):
+    """Close enough to see any 128 positions left out."""
+    kc, vc, table, kv = paged([n], 1, Hk, D, page, F16, seed=n)
+    g = torch.Generator(device="cuda").manual_seed(n + 1)  # not the keys' own
+    q = torch.randn((1, tokens, Hq * D), generator=g, device="cuda").to(F16)
+    seq = torch.tensor([n], dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, tokens], dtype=torch.int32, device="cuda")
+    outs = [tp.tp_paged_prefill(q, kc, vc, table, cu, seq)]
+    if tokens == 1:
+        outs.append(tp.tp_paged_decode(q, kc, vc, table, seq))
+    status_ok()
+    G = Hq // Hk
+    seen = torch.arange(n, device="cuda")[None] <= n - tokens + torch.arange(tokens, device="cuda")[:, None]
+    for h in range(Hk):
+        part = slice(h * G, (h + 1) * G)
+        ref, tol, least = float16_reference(q[0].reshape(tokens, Hq, D)[:, part], kv[0][0][0, h], kv[0][1][0, h], seen,
+                                            D ** -0.5)
+        assert least > 1
+        for o in outs:
+            assert ((o[0].reshape(tokens, Hq, D)[:, part].double() - ref).abs() <= tol).all()
+
+
 # ------------------------------------------------------------------ sampling
 def kept_set(x, t, k, p, m, slack):
     """Indices that may be kept and those that must be, in float64, `slack` the allowed relative error of a share."""
