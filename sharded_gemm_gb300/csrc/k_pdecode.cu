@@ -25,8 +25,8 @@
 // Bytes bound it: every visible key and value is read once.  Measured against the
 // copy rate (6.79 TB/s): 64 sequences of 1000..16384, 8 heads on one of 128, 333 us
 // (101%); 16 of 100..4096 with as many key as query heads 93 us (96%); 48 windows of
-// 1024 on heads of 64, capped, 26 to 28 us (50%: 4 us to the first bytes, then merges of
-// short pieces); one sequence of 517 8.9 us, a chain of latencies.  The softmax's terms
+// 1024 on heads of 64, capped, 26 to 28 us (50%: 4 us to the first bytes, then about 3 us
+// a piece besides its units, of which a CTA has 20 in 3.1 pieces); one sequence of 517 8.9 us, a chain of latencies.  The softmax's terms
 // are rounded to the 16-bit type for the second product, as its operands are.
 #include "mma16.cuh"
 

@@ -25,7 +25,7 @@
 // takes an equal range of the list of all units' key tiles.  A unit that several CTAs
 // hold leaves each one's O, m and l in the workspace, and the last warp to come joins its
 // rows, in CTA order.  One token over 16384 positions, 32 heads on 8: 167 us whole, 37 so;
-// 64 over 32768: 331, 76; 512 over 8192: 96, 64; 2048 over 16384: 335, 311.
+// 64 over 32768: 331, 78; 512 over 8192: 96, 65; 2048 over 16384: 335, 317.
 // Rows of a value tile behind the sequence's end (or in pages that are not
 // read) are written as zeros: stale rows never meet a product.  A value within the
 // sequence that is not finite does, with the terms 0 of rows that do not see it:
@@ -34,9 +34,9 @@
 // Tensor rate bounds long chunks: 4 D flop per visible pair.  Of it, what holds
 // the kernel back is shared memory: Q K^T reads both operands from there, 128
 // bytes a cycle, which is all there is.  Measured: 8192 tokens, 32 heads of 128,
-// causal, 375 us alone and 393 to 410 in a long run (1460 and 1350 to 1400 TFLOP/s, 76%
-// and 70 to 73% of cuBLAS's burst rate); 2 x 1024 tokens over 4000..8192 cached positions,
-// 32 heads on 8, 182 us; five prompts of 7..150 tokens 14 us.
+// causal, 371 to 387 us a call in a graph of 20 and 393 to 410 in a long run (1350 to 1480
+// TFLOP/s, 70 to 77% of cuBLAS's burst rate); 2 x 1024 tokens over 4000..8192 cached positions,
+// 32 heads on 8, 175 and 186 us; five prompts of 7..150 tokens 14 us.
 #include "attn.cuh"
 #include "mma16.cuh"
 #include "ptx.cuh"
@@ -47,7 +47,7 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kTile = 128;  // rows of a query tile, positions of a key tile
 constexpr float kSlack = 8.0f;
-constexpr int kUnitTiles = 2;  // what a unit costs besides its tiles, in tiles (1.75 us at D = 128)
+constexpr int kUnitTiles = 2;  // what a unit costs besides its tiles, in tiles (1.6 to 1.9 us at D = 128)
 constexpr int kJoinTiles = 6;  // and what a CTA's two shared ones cost more
 // Registers a thread: 384 * 168 at launch = 128 * 88 + 256 * 208.
 constexpr int kRegsFew = 88, kRegsMany = 208;
@@ -444,8 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         const long long even = (total + gridDim.x - 1) / gridDim.x;
         const int least = max(4, (longest + 7) / 8);
         const long long share = even > least ? even : least;
-        // whole units: the longest, or as many turns as it takes of average ones.  (Full turns
-        // are no loss: with every SM busy a tile takes 1.95 us, with five of six 1.75.)
+        // whole units: the longest, or as many turns as it takes of average ones
         const long long turns = (units + gridDim.x - 1) / gridDim.x;
         const long long whole = turns <= 1 ? longest + kUnitTiles : turns * total / units;
         if (whole > share + share / 8 + kJoinTiles) {
@@ -862,7 +861,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     const bool cap = a.softcap > 0.0f;
     const float log2e = 1.4426950408889634f;
     // log2 scores: s * scale * log2e, or with a cap c: c * log2e * tanh(s * scale / c),
-    // tanh y = 1 - 2 / (1 + 2^(2 y log2e)), whose error is absolute and so is the score's
+    // from 2 s * scale / c * log2e by capped()
     const float scale = cap ? 2.0f * log2e * a.scale / a.softcap : a.scale * log2e;
     const float cap2 = a.softcap * log2e;
     uint32_t s_phase = 0, o_count = 0;
