@@ -24,12 +24,13 @@
  *  - Bias vectors are float32.  Accumulation is float32 everywhere.
  *  - The device-side waits of the kernels are bounded; a wait that runs out
  *    makes the kernel record TP_ERR_TIMEOUT in a device status word and
- *    return.  tp_query_status() reads (and clears) that word.
+ *    return.  tp_query_status() reads (and clears) that word, in which the
+ *    attention-side calls also record device data that is out of range.
  *  - The library allocates one 4-byte device status word per device on
  *    first use and caches host-side TMA descriptors.  Calls whose kernel
  *    splits a sum across CTAs (the row-parallel 4-bit linears, split-K 4-bit
- *    and MXFP8 tiles, and 16-bit linears of at most 16 tokens whose output
- *    has fewer 128-row tiles than the GPU has SMs) use a per-(device, stream)
+ *    and MXFP8 tiles, 16-bit linears of at most 16 tokens whose output has
+ *    fewer 128-row tiles than the GPU has SMs, and both paged attentions) use a per-(device, stream)
  *    float32 workspace with zeroed counters, allocated (cudaMalloc) on first
  *    need and grown when a larger call needs more; the counters are back at
  *    zero when each kernel ends.  A workspace that grows keeps its old
@@ -88,10 +89,13 @@ int64_t tp_launch_count(void);
  * *device_status (0 = no error, else a tp_status such as TP_ERR_TIMEOUT)
  * and resets them to 0.  Two words are read: the library's own (written by
  * every entry point but the next) and the one inside the fixed buffer of
- * tp_q4_sharded_to_all_noalloc; the first nonzero one is reported.  After a
- * nonzero word the split counters it concerns are cleared as well.  Allocates
- * nothing (a word that was never created reads as 0).  Returns TP_OK or
- * TP_ERR_CUDA. */
+ * tp_q4_sharded_to_all_noalloc; the first nonzero one is reported.  After
+ * TP_ERR_TIMEOUT in the first the whole device is waited for and the split
+ * counters are cleared, after a nonzero second word the array's.  (The other
+ * value of the first word is TP_ERR_INVALID_ARG, a page number, slot, position
+ * or length out of range: calls on other streams go on undisturbed.)
+ * Allocates nothing (a word that was never created reads as 0).  Returns TP_OK
+ * or TP_ERR_CUDA. */
 int tp_query_status(tp_stream_t stream, int *device_status);
 
 /* Selects the kernel family for the calling process (default AUTO).  The SIMT
@@ -544,9 +548,9 @@ int tp_q4_sharded_to_all_noalloc(int N, const void *const *x, int64_t T, int64_t
  * (NaN too).
  * Page numbers, slots, positions, lengths and offsets are device data: one
  * that is out of range (a length below 0, above width * page or above 2^30;
- * offsets that do not ascend within 0..T) records TP_ERR_INVALID_ARG in the device status
- * word (tp_query_status); nothing outside the arrays is then read or written,
- * and the results of that token or sequence are unspecified.
+ * offsets that do not ascend within 0..T) records TP_ERR_INVALID_ARG in the
+ * device status word (tp_query_status); nothing outside the arrays is then
+ * read or written, and the results of that token or sequence are unspecified.
  *
  * tp_qkv_append: per-head norms, rotation, and the write into the cache, for T
  *   tokens of the fused projection's output.

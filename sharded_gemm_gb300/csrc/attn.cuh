@@ -94,7 +94,7 @@ struct Half2<__half> {
 };
 
 // Records a bad value found in device memory (a page, slot or position out of
-// range); the first error wins and tp_query_status() reports it.
+// range), which tp_query_status() reports.  The kernel goes on to its end.
 __device__ __forceinline__ void record_bad_value(int *status) { atomicCAS(status, 0, TP_ERR_INVALID_ARG); }
 
 #endif  // __CUDACC__

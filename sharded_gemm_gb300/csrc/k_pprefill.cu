@@ -117,7 +117,7 @@ __device__ __forceinline__ bool wait_inline(uint32_t bar, uint32_t parity, uint6
       if (done || (i & 31)) continue;
       if (*abort) break;
       if (globaltimer_ns() - t0 > limit_ns) {
-        atomicCAS(status, 0, TP_ERR_TIMEOUT);
+        atomicMin(status, TP_ERR_TIMEOUT);
         *abort = 1;
       }
     }

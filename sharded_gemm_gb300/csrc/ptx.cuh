@@ -60,8 +60,8 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
 
 // Slow path of mbar_wait: spins with try_wait until the phase completes,
 // `limit_ns` of wall time passes, or *abort (shared memory) is set by another
-// thread of the CTA.  Running out of time records TP_ERR_TIMEOUT (-6) in
-// *status (first error wins) and sets *abort.
+// thread of the CTA.  Running out of time records TP_ERR_TIMEOUT (-6, the
+// lowest code: it stays over any other) in *status and sets *abort.
 static __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, uint64_t limit_ns,
                                             int *status, volatile int *abort) {
   const uint64_t t0 = globaltimer_ns();
@@ -70,7 +70,7 @@ static __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity
     if ((i & 31) == 0) {
       if (abort && *abort) return false;
       if (globaltimer_ns() - t0 > limit_ns) {
-        if (status) atomicCAS(status, 0, -6);
+        if (status) atomicMin(status, -6);
         if (abort) *abort = 1;
         return false;
       }

@@ -139,7 +139,13 @@ int tp_query_status(tp_stream_t stream, int *device_status) {
     if (v != 0) {
       e = cudaMemset(w, 0, sizeof(int));
       if (e != cudaSuccess) return cuda_error(e, "clear status word");
-      split_workspace_reset();  // a kernel may have stopped mid-reduction
+    }
+    if (v == TP_ERR_TIMEOUT) {
+      // A kernel may have stopped mid-reduction.  Kernels of other streams still count, so they end
+      // first.  (After a bad value every kernel runs to its end, and the counters are as they should be.)
+      e = cudaDeviceSynchronize();
+      if (e != cudaSuccess) return cuda_error(e, "cudaDeviceSynchronize");
+      split_workspace_reset();
     }
   }
   int v2 = 0;

@@ -502,6 +502,44 @@ def test_the_widest_window_hides_nothing(policy):
         assert torch.equal(d, tp.tp_paged_decode(q[:, :2], kc, vc, table, seq))
 
 
+def test_a_bad_value_on_one_stream_leaves_others_alone():
+    """Asking for the status while other streams' kernels join their parts: they count on, and leave no count behind."""
+    d, dargs = run_decode([9000, 1, 700, 64], 1, 8, 2, 128, 64, BF)
+    p, pargs = run_prefill([(4, 9000), (20, 300)], 1, 8, 2, 128, 64, BF)
+    qkv = torch.ones((2, 3 * 64), dtype=BF, device="cuda")
+    kc = torch.zeros((2, 1, 16, 64), dtype=BF, device="cuda")
+    bad = torch.tensor([0, 32], device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    outs, seen = [], 0
+    for _ in range(60):
+        with torch.cuda.stream(side):
+            for _ in range(8):
+                outs.append((tp.tp_paged_decode(*dargs), tp.tp_paged_prefill(*pargs)))
+        tp.tp_qkv_append([qkv], [kc], [kc.clone()], bad)
+        seen += tp.tp_query_status() == tp.TP_ERR_INVALID_ARG
+    assert seen == 60
+    side.synchronize()
+    for a, b in outs:
+        assert torch.equal(a, d) and torch.equal(b, p)
+    status_ok()
+
+
+def test_timeouts_stay_over_bad_values():
+    """Both in the status word: the timeout is reported, as the counters have to be cleared after it."""
+    qkv = torch.ones((2, 3 * 64), dtype=BF, device="cuda")
+    kc = torch.zeros((2, 1, 16, 64), dtype=BF, device="cuda")
+    bad = torch.tensor([0, 32], device="cuda")
+    for first in (True, False):
+        if first:
+            tp.tp_qkv_append([qkv], [kc], [kc.clone()], bad)
+        tp.tp_debug_wait_timeout(2000000)
+        if not first:
+            tp.tp_qkv_append([qkv], [kc], [kc.clone()], bad)
+        assert tp.tp_query_status() == tp.TP_ERR_TIMEOUT
+        assert tp.tp_query_status() == 0
+
+
 def test_a_cache_beyond_32_bit_offsets():
     """Pages whose byte and element offsets pass 2^32 (a 17 GB key cache)."""
     Hk, page, D = 8, 256, 128
