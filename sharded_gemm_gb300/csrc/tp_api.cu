@@ -147,6 +147,12 @@ int tp_query_status(tp_stream_t stream, int *device_status) {
       if (e != cudaSuccess) return cuda_error(e, "cudaDeviceSynchronize");
       split_workspace_reset();
     }
+    if (v != 0) {
+      // clears are not waited for by streams that do not wait for the default one: a call that follows
+      // on such a stream has to find them done
+      e = cudaStreamSynchronize(nullptr);
+      if (e != cudaSuccess) return cuda_error(e, "cudaStreamSynchronize");
+    }
   }
   int v2 = 0;
   int rc = noalloc_status_take((cudaStream_t)stream, &v2);

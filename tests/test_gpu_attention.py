@@ -525,6 +525,23 @@ def test_a_bad_value_on_one_stream_leaves_others_alone():
     status_ok()
 
 
+def test_errors_behind_a_cleared_status_are_kept():
+    """The word is clear when the query returns: a call on another stream right behind it may set it again."""
+    qkv = torch.ones((2, 3 * 64), dtype=BF, device="cuda")
+    kc, vc = (torch.zeros((2, 1, 16, 64), dtype=BF, device="cuda") for _ in range(2))
+    bad = torch.tensor([0, 32], device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    tp.tp_qkv_append([qkv], [kc], [vc], bad)
+    for _ in range(200):
+        assert tp.tp_query_status() == tp.TP_ERR_INVALID_ARG
+        with torch.cuda.stream(side):
+            tp.tp_qkv_append([qkv], [kc], [vc], bad)
+        side.synchronize()
+    assert tp.tp_query_status() == tp.TP_ERR_INVALID_ARG
+    status_ok()
+
+
 def test_timeouts_stay_over_bad_values():
     """Both in the status word: the timeout is reported, as the counters have to be cleared after it."""
     qkv = torch.ones((2, 3 * 64), dtype=BF, device="cuda")
