@@ -187,6 +187,11 @@ def prepare(case, seed):
                    rejected=dev(back.astype(np.int32)) if case["rejected"] else None)
         n = case["adapters"]
         st["adapters"] = dev(rng.integers(-1, n, B).astype(np.int32)) if n else None
+        # what a program writes each step into: lengths, pages, pool, what lacks, offsets, positions, slots
+        T = st["tokens"]
+        st["step"] = [torch.empty(m, dtype=torch.int32, device="cuda") for m in (B, B, 1, 1, B + 1, T)]
+        st["step"] += [torch.empty(T, dtype=torch.int64, device="cuda")]
+        st["groups"] = torch.empty(4 + 4 * min(T, n + 1) + T, dtype=torch.int32, device="cuda") if n else None
         return st
 
     if case["op"] == "lora":
@@ -244,12 +249,13 @@ def run(st):
         import sharded_gemm_gb300 as tp
         if c["op"] == "plan":
             p = tp.tp_paged_plan(st["counts"], st["seq_lens"], st["owned"], st["block_table"], st["free_pages"],
-                                 st["free_count"], c["page"], st["tokens"], rejected=st["rejected"])
+                                 st["free_count"], c["page"], st["tokens"], rejected=st["rejected"], out=st["step"])
             out = {"seq_lens": p.seq_lens, "owned": p.owned, "free_count": p.free_count, "missing": p.missing,
                    "cu_seqlens": p.cu_seqlens, "positions": p.positions, "slots": p.slots,
                    "block_table": st["block_table"], "free_pages": st["free_pages"]}
             if st["adapters"] is not None:
-                out["groups"] = tp.tp_lora_plan(st["adapters"], st["tokens"], c["adapters"], cu_seqlens=p.cu_seqlens)
+                out["groups"] = tp.tp_lora_plan(st["adapters"], st["tokens"], c["adapters"], cu_seqlens=p.cu_seqlens,
+                                                out=st["groups"])
             return out
         if c["op"] == "lora":
             if c["form"] == "column":
