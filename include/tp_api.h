@@ -640,6 +640,130 @@ int tp_sample(const void *logits, int64_t B, int64_t V, int64_t ld, tp_dtype in_
               const float *min_p, int64_t *tokens, float *logprobs, tp_stream_t stream);
 
 /*
+ * The operators that serve many requests at once over one paged cache.
+ *
+ * tp_paged_plan: what a step needs to know of its tokens, from the requests'
+ *   lengths, for B sequences (at most 8192) that share a pool of `pages` pages.
+ *   All arrays are device data.
+ *     counts       int32 (B): the new tokens of each sequence, 0: none this
+ *                  step, below 0: the sequence has ended;
+ *     rejected     NULL or int32 (B): cached positions at its end that do not
+ *                  count (tp_verify's refused drafts);
+ *     seq_lens     int32 (B): the positions cached before this step;
+ *     owned        int32 (B): the pages that each sequence holds, the first
+ *                  owned[b] entries of its row of block_table (int32
+ *                  (B, width), row stride ld_table), enough for
+ *                  seq_lens[b] - rejected[b] positions;
+ *     free_pages   int32 (pages), free_count int32 (1): the pool's free pages
+ *                  are its first free_count entries.
+ *   The pages of ended sequences go on top of the pool, in the order of the
+ *   sequences and their pages; then each sequence in turn takes the pages that
+ *   it lacks from the top: block_table's entries behind its own are written.
+ *   Out: new_seq_lens, new_owned (B), new_free_count (1), each of which may be
+ *   the array it follows from; cu_seqlens (B + 1), the running sum of the new
+ *   tokens; and for each of T rows the position (int32) and the slot (int64)
+ *   that tp_qkv_append takes: row cu_seqlens[b] + i is the i-th new token of
+ *   sequence b.  Rows behind the last token have position 0 and slot -1.
+ *   missing (1) is 0, or: the pages that the pool lacks (> 0), or -1 for a value
+ *   out of range (a length or a count of pages below 0, above width * page or
+ *   above 2^30, fewer pages than positions, free_count outside 0..pages) and
+ *   for more than T tokens, which also record TP_ERR_INVALID_ARG in the status
+ *   word.  Then the step is empty: lengths, pages and pool stay as they were,
+ *   cu_seqlens is 0 and no row has a slot.  A page number outside 0..pages - 1
+ *   is recorded and gives its tokens slot -1.
+ *   With the inputs kept apart from the outputs, the same call gives the same
+ *   step again.
+ *
+ * tp_lora_plan: a step's tokens grouped by adapter.  adapters int32 (B): each
+ *   sequence's of n (at most 16384), -1: none.  cu_seqlens int32 (B + 1), from 0,
+ *   ascending to at most T, or NULL: one token each (B = T).  plan, 16-byte
+ *   aligned, int32 (tp_lora_plan_ints(T, n)):
+ *     4 values: the groups G, the tokens with an adapter, 0, 0;
+ *     min(T, n + 1) groups of 4: adapter, first place, tokens, 0, by adapter,
+ *       those without one last (-1); -1 in what is behind the last group;
+ *     T places: the tokens by adapter, each adapter's ascending, -1 behind the
+ *       last.
+ *   An adapter of n or more is recorded in the status word and counts as none;
+ *   offsets out of range are recorded and give a plan of no tokens.
+ *
+ * tp_lora_all_to_sharded, tp_lora_sharded_to_all: the low-rank adapters of a
+ *   step's tokens beside a column-parallel and a row-parallel projection.  For a
+ *   token t of adapter i = 0..n-1 (the plan's):
+ *     out[r][t] = y[r][t] + (scale_i * x[t] A_i^T) B_i[r]^T
+ *     out[t]    = y[t] + (scale_i * sum_r x[r][t] A_i[r]^T) B_i^T
+ *   and out = y for a token without an adapter; rows of no sequence stay as they
+ *   were.  x, A and B are of one dt, TP_BF16 or TP_F16, y and out of any.
+ *     x      (T, K), or x[r] (T, K / N), row stride ldx;
+ *     a      (n, R, K), or a[r] (n, R, K / N), contiguous; R at most 128;
+ *     b[r]   (n, O / N, R), or b (n, O, R), contiguous;
+ *     scales NULL (1) or float32 (n);
+ *     y[r], out[r]  (T, O / N), or (T, O); out may be y (one row stride then),
+ *            else they do not overlap.
+ *   The products are summed in float32; the sum over x meets B as two terms of
+ *   dt, which keep 16 of its bits (22 for TP_F16), and the result is rounded once.
+ *   The ranks' parts are added in a fixed order: the same call gives the same
+ *   bytes.  plan_size counts plan's values: a plan of another T or n is refused
+ *   (TP_ERR_INVALID_ARG); one that is not a plan is recorded in the status word.
+ *
+ * tp_verify: drafted tokens checked against the target's probabilities.  Rows
+ *   cu_rows[b] .. cu_rows[b + 1] - 1 of logits (T, V) in_dt, row stride ld,
+ *   V <= 417792, are the target's after each of sequence b's m drafted tokens in
+ *   turn and, the first, before them: m + 1 rows, or none.  cu_rows int32
+ *   (seqs + 1), ascending within 0..T.
+ *     drafts       int64 (T): row i's drafted token; below 0: none, which ends the
+ *                  sequence's drafts.  A sequence's last row has none;
+ *     draft_probs  NULL (a drafted token's probability is 1) or q_dt (T, V), row
+ *                  stride ldq: the distribution that row i's token was drawn
+ *                  from, taken into [0, 1];
+ *     u            float32 (T): row i's random number for the test of its draft,
+ *                  the last row's for the draw;
+ *     temperature, top_k, top_p, min_p: NULL or (seqs), as in tp_sample.
+ *   With e_i, w_i and what is kept of the row as in tp_sample, W the kept
+ *   weights' total and s = 1 / (W as a float * 2^-40): p_i = e_i * s of the kept,
+ *   else 0.  Draft d of row i is accepted if u * q_d < p_d (in float32, u taken
+ *   into [0, 1)).  Behind the accepted ones one token is drawn, by tp_sample's
+ *   rule with the last row's u: where a draft was refused by the weights
+ *   floor(max(p_i - q_i, 0) * 2^40), else, or if those are all 0, by w_i.
+ *   tokens int64 (T): row cu_rows[b] + i the i-th new token of sequence b, -1
+ *   behind the drawn one; logprobs NULL or float32 (T): their log-probabilities
+ *   as in tp_sample, 0 behind.  accepted, rejected NULL or int32 (seqs): the
+ *   drafts accepted, and the rows behind the drawn token (0 and 0 for a sequence
+ *   of no rows).  Rows of no sequence stay as they were.  A row without a logit
+ *   above -inf accepts nothing and gives token -1 and -inf.  A draft of V or more
+ *   and offsets out of range are recorded in the status word: the draft counts as
+ *   none, the sequence has no rows.
+ * Errors: TP_ERR_UNSUPPORTED for more sequences or adapters than these, R above
+ * 128, a page or V this build does not take; TP_ERR_NOT_DIVISIBLE if K (of the
+ * row-parallel) or O (of the column-parallel) does not divide by N;
+ * TP_ERR_ALIGNMENT for a pointer not aligned to its element size (plan: 16
+ * bytes); TP_ERR_INVALID_ARG for null pointers, a row stride below the row, N
+ * outside 1..64, a negative size.  An adapter call of no rows and a verification
+ * of no sequences launch nothing; a plan of none is still written.
+ */
+int tp_paged_plan(int64_t B, const int32_t *counts, const int32_t *rejected, const int32_t *seq_lens,
+                  const int32_t *owned, int32_t *block_table, int64_t width, int64_t ld_table,
+                  int32_t *free_pages, int64_t pages, const int32_t *free_count, int page, int64_t T,
+                  int32_t *new_seq_lens, int32_t *new_owned, int32_t *new_free_count, int32_t *missing,
+                  int32_t *cu_seqlens, int32_t *positions, int64_t *slots, tp_stream_t stream);
+int64_t tp_lora_plan_ints(int64_t T, int64_t n);
+int tp_lora_plan(int64_t B, const int32_t *adapters, const int32_t *cu_seqlens, int64_t T, int64_t n,
+                 int32_t *plan, tp_stream_t stream);
+int tp_lora_all_to_sharded(int N, const void *x, int64_t T, int64_t K, int64_t ldx, const void *a,
+                           const void *const *b, int64_t n, int R, int64_t O, const float *scales,
+                           const int32_t *plan, int64_t plan_size, tp_dtype dt, const void *const *y,
+                           int64_t ldy, void *const *out, int64_t ldo, tp_dtype out_dt, tp_stream_t stream);
+int tp_lora_sharded_to_all(int N, const void *const *x, int64_t T, int64_t K, int64_t ldx,
+                           const void *const *a, const void *b, int64_t n, int R, int64_t O,
+                           const float *scales, const int32_t *plan, int64_t plan_size, tp_dtype dt,
+                           const void *y, int64_t ldy, void *out, int64_t ldo, tp_dtype out_dt,
+                           tp_stream_t stream);
+int tp_verify(const void *logits, int64_t T, int64_t V, int64_t ld, tp_dtype in_dt, const int64_t *drafts,
+              const void *draft_probs, int64_t ldq, tp_dtype q_dt, int64_t seqs, const int32_t *cu_rows,
+              const float *u, const float *temperature, const int32_t *top_k, const float *top_p,
+              const float *min_p, int64_t *tokens, float *logprobs, int32_t *accepted, int32_t *rejected,
+              tp_stream_t stream);
+
+/*
  * Fault check of the bounded waits (no counterpart on the pages): launches a
  * one-block kernel that waits on a shared-memory barrier nothing ever
  * arrives at, with the given limit (1e6 .. 6e10 ns).  The wait runs out,

@@ -19,6 +19,7 @@ import importlib.machinery
 import os
 import re
 import threading
+from typing import NamedTuple
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libtp.so")
@@ -116,6 +117,16 @@ def _load() -> ctypes.CDLL:
             "tp_paged_prefill": ([i32, vp, i64, i64, i32, i32, i32, vp, vp, i64, i32, i64, vp, i64, i64, i64, vp,
                                   vp, vp, f32, f32, i32, i32, vp, i64, vp], i32),
             "tp_sample": ([vp, i64, i64, i64, i32, vp, vp, vp, vp, vp, vp, vp, vp], i32),
+            "tp_paged_plan": ([i64, vp, vp, vp, vp, vp, i64, i64, vp, i64, vp, i32, i64, vp, vp, vp, vp, vp, vp, vp,
+                               vp], i32),
+            "tp_lora_plan_ints": ([i64, i64], i64),
+            "tp_lora_plan": ([i64, vp, vp, i64, i64, vp, vp], i32),
+            "tp_lora_all_to_sharded": ([i32, vp, i64, i64, i64, vp, vp, i64, i32, i64, vp, vp, i64, i32, vp, i64, vp,
+                                        i64, i32, vp], i32),
+            "tp_lora_sharded_to_all": ([i32, vp, i64, i64, i64, vp, vp, i64, i32, i64, vp, vp, i64, i32, vp, i64, vp,
+                                        i64, i32, vp], i32),
+            "tp_verify": ([vp, i64, i64, i64, i32, vp, vp, i64, i32, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp],
+                          i32),
             "tp_debug_wait_timeout": ([i64, vp], i32),
             "tp_debug_prep_alone": ([i32], i32),
             "tp_set_trace": ([vp, i64], i32),
@@ -856,3 +867,61 @@ def tp_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, t
     numbers ``u`` (B); returns (tokens int64 (B), logprobs float32 (B))."""
     return _call("tp_sample", (_native or _marshaller()).sample, logits, u, temperature, top_k, top_p, min_p, tokens,
                  logprobs, stream)
+
+
+# ------------------------------------------------------------------ many requests at once
+class PagedPlan(NamedTuple):
+    """What tp_paged_plan gives, in its order: `seq_lens`, `owned` and `free_count` are the next call's."""
+    seq_lens: object
+    owned: object
+    free_count: object
+    missing: object
+    cu_seqlens: object
+    positions: object
+    slots: object
+
+
+def tp_paged_plan(counts, seq_lens, owned, block_table, free_pages, free_count, page: int, tokens: int, rejected=None,
+                  out=None, stream=None) -> PagedPlan:
+    """A step's plan for sequences that share a pool of pages: ``counts`` (B) new
+    tokens each (below 0: the sequence has ended and gives its pages back), for
+    ``tokens`` rows at most.  Takes the pages that lack from the pool
+    (``block_table`` and ``free_pages`` are written in place) and returns a
+    PagedPlan; ``out``, the seven outputs, may hold the inputs themselves."""
+    return PagedPlan(*_call("tp_paged_plan", (_native or _marshaller()).plan, counts, seq_lens, owned, block_table,
+                            free_pages, free_count, page, tokens, rejected, out, stream))
+
+
+def tp_lora_plan(adapters, tokens: int, n: int, cu_seqlens=None, out=None, stream=None):
+    """A step's ``tokens`` rows grouped by adapter: ``adapters`` (B) each sequence's
+    of n, -1 for none; ``cu_seqlens`` (B + 1) its rows (None: one each).  Returns
+    the int32 plan that the adapter calls of the step take."""
+    return _call("tp_lora_plan", (_native or _marshaller()).groups, adapters, tokens, n, cu_seqlens, out, stream)
+
+
+def tp_lora_all_to_sharded(x, a, b, plan, y, scales=None, out=None, stream=None):
+    """Adapters beside a column-parallel projection: out[r] = y[r] + scale (x A^T) B[r]^T
+    by each token's adapter; x (T, K), a (n, R, K), b per rank (n, O / N, R), y
+    per rank (T, O / N).  Written to y unless ``out`` is given; returns that."""
+    return _call("tp_lora_all_to_sharded", (_native or _marshaller()).lora, True, x, a, b, plan, y, scales, out, stream)
+
+
+def tp_lora_sharded_to_all(x, a, b, plan, y, scales=None, out=None, stream=None):
+    """Adapters beside a row-parallel projection: out = y + scale (sum_r x[r] A[r]^T) B^T
+    by each token's adapter; x per rank (T, K / N), a per rank (n, R, K / N), b
+    (n, O, R), y (T, O).  Written to y unless ``out`` is given; returns that."""
+    return _call("tp_lora_sharded_to_all", (_native or _marshaller()).lora, False, x, a, b, plan, y, scales, out,
+                 stream)
+
+
+def tp_verify(logits, drafts, cu_rows, u, draft_probs=None, temperature=None, top_k=None, top_p=None, min_p=None,
+              tokens=None, logprobs=None, accepted=None, rejected=None, stream=None):
+    """Checks drafted tokens against the target's probabilities and draws the token
+    that follows the accepted ones: rows cu_rows[b] .. of ``logits`` (T, V) are
+    sequence b's, row i's draft ``drafts[i]`` of the distribution
+    ``draft_probs[i]`` (None: drafts of probability 1), ``u`` (T) the random
+    numbers; the settings are the sequences'.  Returns (tokens int64 (T), -1
+    behind each sequence's drawn one, logprobs float32 (T), accepted and rejected
+    int32 (sequences))."""
+    return _call("tp_verify", (_native or _marshaller()).verify, logits, drafts, cu_rows, u, draft_probs, temperature,
+                 top_k, top_p, min_p, tokens, logprobs, accepted, rejected, stream)

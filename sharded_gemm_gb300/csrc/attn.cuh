@@ -58,11 +58,27 @@ struct SampleArgs {
   int in_dt;
 };
 
+// The longest row of logits that a verification takes: what 8 CTAs hold on chip.
+constexpr int64_t kMostVerified = 417792;
+
+// Rows of logits of a batch of sequences, row cu[b] + i the target's after i drafted
+// tokens of sequence b.  B counts the rows; the settings are the sequences'.
+struct VerifyArgs : SampleArgs {
+  const int32_t *cu;      // (seqs + 1)
+  const int64_t *drafts;  // (B)
+  const void *q;          // nullable, (B, V), row stride ldq
+  int32_t *accepted, *rejected;  // (seqs), each nullable
+  int64_t seqs, ldq;
+  int q_dt;
+  int *status;
+};
+
 int launch_append(const AppendArgs &a, cudaStream_t s);
 int launch_decode(const AttnArgs &a, cudaStream_t s);
 int launch_prefill(const AttnArgs &a, cudaStream_t s);
 int launch_attn_simt(const AttnArgs &a, cudaStream_t s);
 int launch_sample(const SampleArgs &a, cudaStream_t s);
+int launch_verify(const VerifyArgs &a, cudaStream_t s);
 
 #ifdef __CUDACC__
 

@@ -492,6 +492,263 @@ static PyObject *m_sample(PyObject *self, PyObject *const *a, Py_ssize_t na) {
   return answer(out, rc);
 }
 
+/* ---- the operators that serve many requests at once */
+
+/* A 2-D int32 matrix: pointer, rows, columns and row stride. */
+static int table_of(PyObject *t, long dev, uint64_t *ptr, int64_t *rows, int64_t *cols, int64_t *ld, const char *name) {
+  Info f;
+  if (info_of(t, &f, name)) return -1;
+  if (f.dtype != t_i32 || f.nd != 2 || f.dev != dev || (f.shape[0] > 0 && f.shape[1] > 1 && f.stride[1] != 1)) {
+    PyErr_Format(PyExc_ValueError, "%s must be a 2-D int32 tensor with unit column stride on device %ld", name, dev);
+    return -1;
+  }
+  *ptr = f.ptr, *rows = f.shape[0], *cols = f.shape[1], *ld = f.shape[0] > 1 ? f.stride[0] : f.shape[1];
+  return 0;
+}
+
+static int length_of(PyObject *t, int64_t *n, long *dev, const char *name) {
+  Info f;
+  if (info_of(t, &f, name)) return -1;
+  if (f.nd != 1) {
+    PyErr_Format(PyExc_ValueError, "%s must be 1-D", name);
+    return -1;
+  }
+  *n = f.shape[0], *dev = f.dev;
+  return 0;
+}
+
+/* The tensor `given`, or where it is None a new one of n values: a new reference. */
+static PyObject *vector_or_new(PyObject *given, int64_t n, PyObject *dtype, long dev) {
+  return given == Py_None ? new_tensor(1, &n, dtype, dev) : Py_NewRef(given);
+}
+
+/* plan(fn, counts, seq_lens, owned, block_table, free_pages, free_count, page, tokens, rejected, out, stream) -> the
+ * seven outputs: lengths, pages, free count, missing, offsets, positions, slots */
+static PyObject *m_plan(PyObject *self, PyObject *const *a, Py_ssize_t na) {
+  if (na != 12) return PyErr_Format(PyExc_TypeError, "plan takes 12 arguments");
+  void *fn = PyLong_AsVoidPtr(a[0]);
+  int64_t B, rows, width, ld, pages;
+  long dev, pool_dev;
+  uint64_t counts, lens, owned, table, pool, free_n, rejected, stream, to[7];
+  if (length_of(a[1], &B, &dev, "counts") || param_of(a[1], &counts, t_i32, B, dev, "counts") ||
+      param_of(a[2], &lens, t_i32, B, dev, "seq_lens") || param_of(a[3], &owned, t_i32, B, dev, "owned") ||
+      table_of(a[4], dev, &table, &rows, &width, &ld, "block_table"))
+    return NULL;
+  if (rows != B) return PyErr_Format(PyExc_ValueError, "block_table needs one row per sequence");
+  if (length_of(a[5], &pages, &pool_dev, "free_pages") || param_of(a[5], &pool, t_i32, pages, dev, "free_pages") ||
+      param_of(a[6], &free_n, t_i32, 1, dev, "free_count") || param_of(a[9], &rejected, t_i32, B, dev, "rejected") ||
+      stream_of(a[11], dev, &stream))
+    return NULL;
+  const long page = PyLong_AsLong(a[7]);
+  const int64_t T = PyLong_AsLongLong(a[8]);
+  if (PyErr_Occurred()) return NULL;
+  if (T < 0 || T > 0x7fffffff) return PyErr_Format(PyExc_ValueError, "tokens must be in 0..2^31 - 1");
+  if (a[10] != Py_None && (!(PyTuple_Check(a[10]) || PyList_Check(a[10])) || PySequence_Fast_GET_SIZE(a[10]) != 7))
+    return PyErr_Format(PyExc_ValueError, "out must be the seven outputs");
+  static const char *const names[7] = {"out.seq_lens",   "out.owned",     "out.free_count", "out.missing",
+                                       "out.cu_seqlens", "out.positions", "out.slots"};
+  const int64_t sizes[7] = {B, B, 1, 1, B + 1, T, T};
+  PyObject *out = PyTuple_New(7);
+  if (!out) return NULL;
+  for (int i = 0; i < 7; ++i) {
+    PyObject *dtype = i == 6 ? t_i64 : t_i32;
+    PyObject *t = a[10] == Py_None ? new_tensor(1, &sizes[i], dtype, dev) : Py_NewRef(PySequence_Fast_GET_ITEM(a[10], i));
+    if (!t) goto fail;
+    PyTuple_SET_ITEM(out, i, t);
+    if (t == Py_None) {
+      PyErr_Format(PyExc_ValueError, "%s is None", names[i]);
+      goto fail;
+    }
+    if (param_of(t, &to[i], dtype, sizes[i], dev, names[i])) goto fail;
+  }
+  if (!fn)
+    return Py_BuildValue("N(LKKKKKLLKLKiLKKKKKKKK)", out, B, counts, rejected, lens, owned, table, width, ld, pool, pages,
+                         free_n, (int)page, T, to[0], to[1], to[2], to[3], to[4], to[5], to[6], stream);
+  int rc;
+  Py_BEGIN_ALLOW_THREADS;
+  rc = ((__typeof__(&tp_paged_plan))fn)(B, P(counts), P(rejected), P(lens), P(owned), P(table), width, ld, P(pool), pages,
+                                        P(free_n), (int)page, T, P(to[0]), P(to[1]), P(to[2]), P(to[3]), P(to[4]),
+                                        P(to[5]), P(to[6]), P(stream));
+  Py_END_ALLOW_THREADS;
+  return answer(out, rc);
+fail:
+  Py_DECREF(out);
+  return NULL;
+}
+
+static int64_t group_ints(int64_t T, int64_t n) { return 4 + 4 * (T < n + 1 ? T : n + 1) + T; }
+
+/* groups(fn, adapters, tokens, n, cu_seqlens, out, stream) -> the plan */
+static PyObject *m_groups(PyObject *self, PyObject *const *a, Py_ssize_t na) {
+  if (na != 7) return PyErr_Format(PyExc_TypeError, "groups takes 7 arguments");
+  void *fn = PyLong_AsVoidPtr(a[0]);
+  int64_t B;
+  long dev;
+  uint64_t ids, cu, plan, stream;
+  const int64_t T = PyLong_AsLongLong(a[2]), n = PyLong_AsLongLong(a[3]);
+  if (PyErr_Occurred()) return NULL;
+  if (T < 0 || T > 0x7fffffff || n < 1 || n > 0x7fffffff)
+    return PyErr_Format(PyExc_ValueError, "tokens must be in 0..2^31 - 1, n in 1..2^31 - 1");
+  if (length_of(a[1], &B, &dev, "adapters") || param_of(a[1], &ids, t_i32, B, dev, "adapters") ||
+      param_of(a[4], &cu, t_i32, B + 1, dev, "cu_seqlens") || stream_of(a[6], dev, &stream))
+    return NULL;
+  PyObject *out = vector_or_new(a[5], group_ints(T, n), t_i32, dev);
+  if (!out) return NULL;
+  if (param_of(out, &plan, t_i32, group_ints(T, n), dev, "out")) {
+    Py_DECREF(out);
+    return NULL;
+  }
+  if (!fn) return Py_BuildValue("N(LKKLLKK)", out, B, ids, cu, T, n, plan, stream);
+  int rc;
+  Py_BEGIN_ALLOW_THREADS;
+  rc = ((__typeof__(&tp_lora_plan))fn)(B, P(ids), P(cu), T, n, P(plan), P(stream));
+  Py_END_ALLOW_THREADS;
+  return answer(out, rc);
+}
+
+/* A pool of adapters (n, rows, cols): contiguous, in x's 16-bit dtype. */
+static int pool_of(const Ranks *o, PyObject *dtype, long dev, const char *name) {
+  if (o->dtype != dtype || o->dev != dev || dtype == t_f32) {
+    PyErr_Format(PyExc_ValueError, "%s must have x's 16-bit dtype and its device", name);
+    return -1;
+  }
+  if ((o->shape[2] > 1 && o->stride[2] != 1) || (o->shape[1] > 1 && o->stride[1] != o->shape[2]) ||
+      (o->shape[0] > 1 && o->stride[0] != o->shape[1] * o->shape[2])) {
+    PyErr_Format(PyExc_ValueError, "%s must be contiguous", name);
+    return -1;
+  }
+  return 0;
+}
+
+/* An argument that is one tensor, as a list of one. */
+static int one_of(PyObject *t, Ranks *o, int dim, const char *name) {
+  if (PyList_Check(t) || PyTuple_Check(t)) {
+    PyErr_Format(PyExc_ValueError, "%s must be one tensor", name);
+    return -1;
+  }
+  PyObject *list = PyTuple_Pack(1, t);
+  if (!list) return -1;
+  const int rc = ranks_of(list, o, dim, name);
+  Py_DECREF(list);
+  return rc;
+}
+
+/* lora(fn, column, x, a, b, plan, y, scales, out, stream) -> out */
+static PyObject *m_lora(PyObject *self, PyObject *const *a, Py_ssize_t na) {
+  if (na != 10) return PyErr_Format(PyExc_TypeError, "lora takes 10 arguments");
+  void *fn = PyLong_AsVoidPtr(a[0]);
+  const int column = PyObject_IsTrue(a[1]);
+  Ranks x, A_, B_, y, out;
+  int64_t ldx, ldy, ldo, size;
+  uint64_t plan, scales, stream;
+  long dev;
+  PyObject *to = a[8] == Py_None ? a[6] : a[8];
+  if (column ? one_of(a[2], &x, 2, "x") || one_of(a[3], &A_, 3, "a") || ranks_of(a[4], &B_, 3, "b") ||
+                   ranks_of(a[6], &y, 2, "y") || ranks_of(to, &out, 2, "out")
+             : ranks_of(a[2], &x, 2, "x") || ranks_of(a[3], &A_, 3, "a") || one_of(a[4], &B_, 3, "b") ||
+                   one_of(a[6], &y, 2, "y") || one_of(to, &out, 2, "out"))
+    return NULL;
+  if (pool_of(&A_, x.dtype, x.dev, "a") || pool_of(&B_, x.dtype, x.dev, "b")) return NULL;
+  if (A_.n != x.n || B_.n != y.n) {
+    PyErr_SetString(PyExc_ValueError, column ? "b and y need the same ranks" : "x and a need the same ranks");
+    return NULL;
+  }
+  const int64_t T = x.shape[0], K = x.shape[1], n = A_.shape[0], R = A_.shape[1], O = B_.shape[1];
+  if (A_.shape[2] != K || B_.shape[0] != n || B_.shape[2] != R || y.shape[0] != T || y.shape[1] != O || y.dev != x.dev) {
+    PyErr_SetString(PyExc_ValueError, "per rank x (T, K), a (n, R, K), b (n, O, R), y (T, O): the shapes do not fit");
+    return NULL;
+  }
+  if (out.n != y.n || out.shape[0] != T || out.shape[1] != O || out.dtype != y.dtype || out.dev != y.dev) {
+    PyErr_SetString(PyExc_ValueError, "out must have y's ranks, shape, dtype and device");
+    return NULL;
+  }
+  if (R > 1 << 20 || ld_of(&x, &ldx, "x") || ld_of(&y, &ldy, "y") || ld_of(&out, &ldo, "out")) {
+    if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "the adapters' rank is too large");
+    return NULL;
+  }
+  if (length_of(a[5], &size, &dev, "plan") || param_of(a[5], &plan, t_i32, size, x.dev, "plan") ||
+      param_of(a[7], &scales, t_f32, n, x.dev, "scales") || stream_of(a[9], x.dev, &stream))
+    return NULL;
+  PyObject *keep = Py_NewRef(to);
+  if (!fn) {
+    if (column)
+      return Py_BuildValue("N(iKLLLKNLiLKKLiNLNLiK)", keep, y.n, x.ptr[0], T, K, ldx, A_.ptr[0], bytes_of(&B_), n, (int)R,
+                           O * y.n, scales, plan, size, x.dt, bytes_of(&y), ldy, bytes_of(&out), ldo, y.dt, stream);
+    return Py_BuildValue("N(iNLLLNKLiLKKLiKLKLiK)", keep, x.n, bytes_of(&x), T, K * x.n, ldx, bytes_of(&A_), B_.ptr[0], n,
+                         (int)R, O, scales, plan, size, x.dt, y.ptr[0], ldy, out.ptr[0], ldo, y.dt, stream);
+  }
+  int rc;
+  Py_BEGIN_ALLOW_THREADS;
+  if (column)
+    rc = ((__typeof__(&tp_lora_all_to_sharded))fn)(y.n, P(x.ptr[0]), T, K, ldx, P(A_.ptr[0]), CA(B_), n, (int)R, O * y.n,
+                                                   P(scales), P(plan), size, (tp_dtype)x.dt, CA(y), ldy, A(out), ldo,
+                                                   (tp_dtype)y.dt, P(stream));
+  else
+    rc = ((__typeof__(&tp_lora_sharded_to_all))fn)(x.n, CA(x), T, K * x.n, ldx, CA(A_), P(B_.ptr[0]), n, (int)R, O,
+                                                   P(scales), P(plan), size, (tp_dtype)x.dt, P(y.ptr[0]), ldy,
+                                                   P(out.ptr[0]), ldo, (tp_dtype)y.dt, P(stream));
+  Py_END_ALLOW_THREADS;
+  return answer(keep, rc);
+}
+
+/* verify(fn, logits, drafts, cu_rows, u, draft_probs, temperature, top_k, top_p, min_p, tokens, logprobs, accepted,
+ * rejected, stream) -> (tokens, logprobs, accepted, rejected) */
+static PyObject *m_verify(PyObject *self, PyObject *const *a, Py_ssize_t na) {
+  if (na != 15) return PyErr_Format(PyExc_TypeError, "verify takes 15 arguments");
+  void *fn = PyLong_AsVoidPtr(a[0]);
+  Info f, q;
+  long dev;
+  int64_t seqs, ldq = 0;
+  uint64_t drafts, cu, u, t, k, p, m, stream, to[4];
+  if (info_of(a[1], &f, "logits")) return NULL;
+  const int dt = dtype_code(f.dtype);
+  if (dt < 0) return PyErr_Format(PyExc_TypeError, "logits: unsupported dtype %S", f.dtype);
+  if (f.nd != 2 || (f.shape[1] > 1 && f.stride[1] != 1))
+    return PyErr_Format(PyExc_ValueError, "logits must be 2-D with unit column stride");
+  const int64_t T = f.shape[0], V = f.shape[1], ld = T > 1 ? f.stride[0] : V;
+  int q_dt = TP_F32;
+  q.ptr = 0;
+  if (a[5] != Py_None) {
+    if (info_of(a[5], &q, "draft_probs")) return NULL;
+    q_dt = dtype_code(q.dtype);
+    if (q_dt < 0) return PyErr_Format(PyExc_TypeError, "draft_probs: unsupported dtype %S", q.dtype);
+    if (q.nd != 2 || q.dev != f.dev || q.shape[0] != T || q.shape[1] != V || (V > 1 && q.stride[1] != 1))
+      return PyErr_Format(PyExc_ValueError, "draft_probs must have logits' shape and device and unit column stride");
+    ldq = T > 1 ? q.stride[0] : V;
+  }
+  if (length_of(a[3], &seqs, &dev, "cu_rows")) return NULL;
+  if (--seqs < 0) return PyErr_Format(PyExc_ValueError, "cu_rows needs one value more than there are sequences");
+  if (param_of(a[3], &cu, t_i32, seqs + 1, f.dev, "cu_rows") || param_of(a[2], &drafts, t_i64, T, f.dev, "drafts") ||
+      param_of(a[4], &u, t_f32, T, f.dev, "u") || param_of(a[6], &t, t_f32, seqs, f.dev, "temperature") ||
+      param_of(a[7], &k, t_i32, seqs, f.dev, "top_k") || param_of(a[8], &p, t_f32, seqs, f.dev, "top_p") ||
+      param_of(a[9], &m, t_f32, seqs, f.dev, "min_p") || stream_of(a[14], f.dev, &stream))
+    return NULL;
+  static const char *const names[4] = {"tokens", "logprobs", "accepted", "rejected"};
+  PyObject *const types[4] = {t_i64, t_f32, t_i32, t_i32};
+  PyObject *out = PyTuple_New(4);
+  if (!out) return NULL;
+  for (int i = 0; i < 4; ++i) {
+    const int64_t n = i < 2 ? T : seqs;
+    PyObject *v = vector_or_new(a[10 + i], n, types[i], f.dev);
+    if (!v) goto fail;
+    PyTuple_SET_ITEM(out, i, v);
+    if (param_of(v, &to[i], types[i], n, f.dev, names[i])) goto fail;
+  }
+  if (!fn)
+    return Py_BuildValue("N(KLLLiKKLiLKKKKKKKKKKK)", out, f.ptr, T, V, ld, dt, drafts, q.ptr, ldq, q_dt, seqs, cu, u, t, k,
+                         p, m, to[0], to[1], to[2], to[3], stream);
+  int rc;
+  Py_BEGIN_ALLOW_THREADS;
+  rc = ((__typeof__(&tp_verify))fn)(P(f.ptr), T, V, ld, (tp_dtype)dt, P(drafts), P(q.ptr), ldq, (tp_dtype)q_dt, seqs,
+                                    P(cu), P(u), P(t), P(k), P(p), P(m), P(to[0]), P(to[1]), P(to[2]), P(to[3]),
+                                    P(stream));
+  Py_END_ALLOW_THREADS;
+  return answer(out, rc);
+fail:
+  Py_DECREF(out);
+  return NULL;
+}
+
 /* init(float32, bfloat16, float16, int32, int64, current raw stream of a device index, torch.empty) */
 static PyObject *m_init(PyObject *self, PyObject *args) {
   PyObject **to[7] = {&t_f32, &t_bf16, &t_f16, &t_i32, &t_i64, &raw_stream, &torch_empty}, *v[7];
@@ -505,6 +762,10 @@ static PyMethodDef methods[] = {{"init", m_init, METH_VARARGS, NULL},
                                 {"decode", (PyCFunction)(void (*)(void))m_decode, METH_FASTCALL, NULL},
                                 {"prefill", (PyCFunction)(void (*)(void))m_prefill, METH_FASTCALL, NULL},
                                 {"sample", (PyCFunction)(void (*)(void))m_sample, METH_FASTCALL, NULL},
+                                {"plan", (PyCFunction)(void (*)(void))m_plan, METH_FASTCALL, NULL},
+                                {"groups", (PyCFunction)(void (*)(void))m_groups, METH_FASTCALL, NULL},
+                                {"lora", (PyCFunction)(void (*)(void))m_lora, METH_FASTCALL, NULL},
+                                {"verify", (PyCFunction)(void (*)(void))m_verify, METH_FASTCALL, NULL},
                                 {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", NULL, -1, methods, NULL, NULL, NULL, NULL};
 

@@ -1,0 +1,51 @@
+// serve.cuh -- the arguments of the operators that serve many requests at once: the
+// step's plan over a shared pool of pages, the grouping of its tokens by adapter, and
+// the adapters' products.
+#pragma once
+
+#include "attn.cuh"
+
+namespace tp {
+
+constexpr int64_t kMostSequences = 8192;  // their offsets are held in shared memory
+constexpr int64_t kMostAdapters = 16384;  // and the adapters' token counts
+
+struct PlanArgs {
+  const int32_t *counts, *rejected, *seq_lens, *owned, *free_count;  // rejected nullable
+  int32_t *table, *free_pages;
+  int32_t *new_lens, *new_owned, *new_free_count, *missing, *cu, *positions;
+  int64_t *slots;
+  int64_t B, width, ld_table, pages, T, cap;
+  int page_log2;
+  int *status;
+};
+
+// The plan of a step's adapters: a header of 4, the groups of 4, the tokens in their order.
+struct GroupArgs {
+  const int32_t *adapters, *cu;  // cu nullable: one token each
+  int32_t *plan;
+  int64_t B, T, n, most;  // most: groups there is room for
+  int *status;
+};
+inline int64_t most_groups(int64_t T, int64_t n) { return T < n + 1 ? T : n + 1; }
+inline int64_t plan_ints(int64_t T, int64_t n) { return 4 + 4 * most_groups(T, n) + T; }
+
+struct LoraArgs {
+  const void *x[kMaxShards], *a[kMaxShards];  // nx parts of the contraction
+  const void *b[kMaxShards], *y[kMaxShards];  // ny parts of the output
+  void *out[kMaxShards];
+  const int32_t *plan;
+  const float *scales;  // nullable, (n)
+  int64_t T, n, K, O, ldx, ldy, ldo, most;  // K, O: of a part
+  int nx, ny, R;
+  int dt, out_dt;
+  int in_place;  // out is y: tokens without an adapter are left alone
+  int *status;
+};
+
+int launch_plan(const PlanArgs &a, cudaStream_t s);
+int launch_groups(const GroupArgs &a, cudaStream_t s);
+int launch_lora(const LoraArgs &a, cudaStream_t s);
+int launch_lora_simt(const LoraArgs &a, cudaStream_t s);
+
+}  // namespace tp

@@ -1,0 +1,650 @@
+"""GPU parity of the operators that serve many requests at once: the step's plan over a shared pool of
+pages, the adapters beside the projections, the verification of drafted tokens, and all of them together.
+
+Whole numbers have one right answer and are compared as such.  Tolerances of the adapters: with u the unit
+roundoff of the output's type (2^-8 for bfloat16, 2^-11 for float16, 2^-24 for float32) an output is rounded
+once (u |out|); the sum over x meets B as two terms, which lose at most 2^-16 of it (bfloat16: 8 + 8 bits) or
+2^-21 (float16: 11 + 11 bits, less what falls below the smallest), and the two products are summed in float32,
+(K + R) adds of at most 2^-23 of the sum of their terms' sizes.
+"""
+import numpy as np
+import pytest
+import torch
+
+import sharded_gemm_gb300 as tp
+from sharded_gemm_gb300 import build as tpbuild
+
+pytestmark = pytest.mark.gpu
+
+BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
+U = {BF16: 2.0 ** -8, F16: 2.0 ** -11, F32: 2.0 ** -24}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    tpbuild.build()
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    yield
+    tp.tp_set_policy(tp.TP_POLICY_AUTO)
+
+
+def status():
+    torch.cuda.synchronize()
+    return tp.tp_query_status()
+
+
+def dev(a, dtype=None):
+    t = torch.from_numpy(np.ascontiguousarray(a))
+    return (t if dtype is None else t.to(dtype)).cuda()
+
+
+def i32(a):
+    return dev(np.asarray(a, np.int32))
+
+
+# ------------------------------------------------------------------ the step's plan
+def plan_ref(counts, rejected, lens, owned, table, pool, free, page, T):
+    """The definition, one sequence and one page after the other: (lens, owned, free, missing, cu, positions,
+    slots, table, pool)."""
+    table, pool = [list(r) for r in table], list(pool)
+    B, width, pages = len(counts), len(table[0]) if len(table) else 0, len(pool)
+    cap = min(width * page, 1 << 30)
+    empty = (list(lens), list(owned), free, [0] * (B + 1), [0] * T, [-1] * T, table, pool)
+
+    def given_up(missing):
+        return (*empty[:3], missing, *empty[3:])
+    bad = free < 0 or free > pages or sum(max(c, 0) for c in counts) > T
+    need = back = 0
+    for b in range(B):
+        own = owned[b]
+        if own < 0 or own > width:
+            bad = True
+        elif counts[b] < 0:
+            back += own
+        else:
+            end = lens[b] - rejected[b] + counts[b]
+            if lens[b] < 0 or rejected[b] < 0 or rejected[b] > lens[b] or end > cap or own * page < lens[b] - rejected[b]:
+                bad = True
+            need += max(0, -(-end // page) - own)
+    if bad or free + back > pages:
+        return given_up(-1)
+    if need > free + back:
+        return given_up(need - free - back)
+    for b in range(B):
+        if counts[b] < 0:
+            for j in range(owned[b]):
+                pool[free] = table[b][j]
+                free += 1
+    lens2, owned2, cu, positions, slots = [], [], [0], [], []
+    for b in range(B):
+        if counts[b] < 0:
+            lens2.append(0), owned2.append(0), cu.append(cu[-1])
+            continue
+        start, own = lens[b] - rejected[b], owned[b]
+        end = start + counts[b]
+        while own * page < end:
+            free -= 1
+            table[b][own] = pool[free]
+            own += 1
+        for i in range(start, end):
+            positions.append(i)
+            p = table[b][i // page]
+            slots.append(p * page + i % page if 0 <= p < pages else -1)
+        lens2.append(end), owned2.append(own), cu.append(cu[-1] + counts[b])
+    pad = T - len(positions)
+    return lens2, owned2, free, 0, cu, positions + [0] * pad, slots + [-1] * pad, table, pool
+
+
+def run_plan(counts, rejected, lens, owned, table, pool, free, page, T, in_place=False, stream=None):
+    t = i32(table)
+    args = [i32(counts), i32(lens), i32(owned), t, i32(pool), i32([free])]
+    out = None
+    if in_place:
+        out = [args[1], args[2], args[5], torch.empty(1, dtype=torch.int32, device="cuda"),
+               torch.empty(len(counts) + 1, dtype=torch.int32, device="cuda"),
+               torch.empty(T, dtype=torch.int32, device="cuda"), torch.empty(T, dtype=torch.int64, device="cuda")]
+    p = tp.tp_paged_plan(*args, page, T, rejected=None if rejected is None else i32(rejected), out=out, stream=stream)
+    torch.cuda.synchronize()
+    return (p.seq_lens.tolist(), p.owned.tolist(), int(p.free_count), int(p.missing), p.cu_seqlens.tolist(),
+            p.positions.tolist(), p.slots.tolist(), t.tolist(), args[4].tolist())
+
+
+def some_step(B, page, hi, most, ends, seed, short=False, rejects=True):
+    rng = np.random.default_rng(seed)
+    lens = rng.integers(0, hi + 1, B)
+    counts = rng.integers(0, most + 1, B)
+    back = np.minimum(rng.integers(0, 5, B), lens) if rejects else np.zeros(B, int)
+    held = -(-lens // page)
+    ended = rng.random(B) < ends
+    need = np.where(ended, 0, np.maximum(0, -(-(lens - back + counts) // page) - held))
+    width = max(1, -(-(hi + most) // page))
+    total = int(need.sum())
+    spare = max(0, total - int(held[ended].sum()) - 1) if short else total + 3
+    pages = int(held.sum()) + spare
+    names = rng.permutation(pages)
+    table = np.full((B, width), -1)
+    table[np.arange(width)[None] < held[:, None]] = names[:held.sum()]
+    pool = np.full(pages, -1)
+    pool[:spare] = names[held.sum():]
+    counts = np.where(ended, -1 - rng.integers(0, 3, B), counts)
+    T = int(np.maximum(counts, 0).sum()) + seed % 4
+    return (counts.tolist(), back.tolist(), lens.tolist(), held.tolist(), table.tolist(), pool.tolist(), spare, page, T)
+
+
+@pytest.mark.parametrize("B,page,hi,most,ends", [
+    (1, 16, 0, 1, 0.0), (1, 16, 40, 1, 0.0), (3, 16, 31, 5, 0.0), (33, 32, 100, 8, 0.2), (256, 16, 700, 8, 0.1),
+    (1023, 16, 50, 2, 0.3), (1025, 64, 300, 1, 0.1), (40, 128, 1000, 600, 0.1), (70, 16, 300, 300, 0.4),
+    (8192, 16, 20, 1, 0.2), (5, 256, 3000, 4000, 0.0)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_plan(B, page, hi, most, ends, in_place):
+    for seed in range(3):
+        step = some_step(B, page, hi, most, ends, seed)
+        assert run_plan(*step, in_place=in_place) == plan_ref(*step)
+    assert status() == 0
+
+
+@pytest.mark.parametrize("B,most", [(4, 40), (300, 3), (64, 200)])
+def test_plan_without_enough_pages_is_empty(B, most):
+    steps = (some_step(B, 16, 100, most, 0.0, seed, short=True) for seed in range(5, 50))
+    step = next(s for s in steps if plan_ref(*s)[3] > 0)
+    ref = plan_ref(*step)
+    assert run_plan(*step) == ref and run_plan(*step, in_place=True) == ref
+    assert status() == 0  # the caller is told by `missing`
+
+
+def test_plan_takes_the_last_page_and_pages_given_back_just_now():
+    # 0 ends and gives back 5, 6; 1 needs two pages: 6 and 5; the pool of one page keeps it
+    step = ([-1, 20], [0, 0], [32, 0], [2, 0], [[5, 6], [-1, -1]], [3, -1, -1, -1, -1, -1, -1], 1, 16, 20)
+    got = run_plan(*step)
+    assert got == plan_ref(*step)
+    assert got[1] == [0, 2] and got[2] == 1 and got[7][1] == [6, 5]
+    # the same with an empty pool and exactly what is needed
+    step = ([-1, 20], [0, 0], [32, 0], [2, 0], [[5, 6], [-1, -1]], [-1] * 7, 0, 16, 20)
+    assert run_plan(*step)[2:4] == (0, 0)
+    assert status() == 0
+
+
+def test_plan_rejected_tokens_keep_their_pages():
+    # 17 positions on two pages, two refused: the next token is position 15, on a page held already
+    step = ([3], [2], [17], [2], [[4, 9, -1]], list(range(12)), 2, 16, 3)
+    got = run_plan(*step)
+    assert got == plan_ref(*step)
+    assert got[5] == [15, 16, 17] and got[6] == [4 * 16 + 15, 9 * 16, 9 * 16 + 1] and got[2] == 2
+
+
+@pytest.mark.parametrize("change", [
+    dict(lens=[-1, 3]), dict(rejected=[4, 0]), dict(rejected=[-1, 0]), dict(owned=[-1, 1]), dict(owned=[5, 1]),
+    dict(counts=[62, 1]), dict(counts=[2 ** 31 - 1, 2 ** 31 - 1]), dict(owned=[0, 1]), dict(free=-1), dict(free=9),
+    dict(T=3), dict(counts=[-1, 1], free=8)])
+def test_plan_of_values_out_of_range_is_empty_and_recorded(change):
+    step = dict(counts=[2, 3], rejected=[0, 0], lens=[3, 16], owned=[1, 1], table=[[1, -1, -1, -1], [2, -1, -1, -1]],
+                pool=[0, 3, 4, 5, 6, 7, -1, -1], free=6, page=16, T=8)
+    assert plan_ref(*step.values())[3] == 0
+    step.update(change)
+    ref = plan_ref(*step.values())
+    assert ref[3] == -1
+    assert run_plan(*step.values()) == ref
+    assert status() == tp.TP_ERR_INVALID_ARG
+
+
+def test_plan_page_numbers_out_of_range_give_no_slot():
+    step = ([2, 1], [0, 0], [15, 0], [1, 0], [[70000, -1], [-1, -1]], [3, 2, -9], 3, 16, 4)
+    ref = plan_ref(*step)
+    assert ref[6] == [-1, -1, 2 * 16, -1]
+    assert run_plan(*step) == ref
+    assert status() == tp.TP_ERR_INVALID_ARG
+
+
+def test_plan_of_no_sequences():
+    got = run_plan([], None, [], [], np.zeros((0, 3)), [0, 1], 2, 16, 3)
+    assert got == ([], [], 2, 0, [0], [0] * 3, [-1] * 3, [], [0, 1])
+    assert status() == 0
+
+
+# ------------------------------------------------------------------ tokens by adapter
+def groups_ref(ids, cu, T, n):
+    """The plan's values."""
+    kind = [-2] * T
+    for b, i in enumerate(ids):
+        for t in range(cu[b], cu[b + 1]):
+            kind[t] = i if 0 <= i < n else -1
+    order, groups = [], []
+    for i in [*range(n), -1]:
+        mine = [t for t in range(T) if kind[t] == i]
+        if mine:
+            groups.append((i, len(order), len(mine), 0))
+        order += mine
+    most = min(T, n + 1)
+    head = [len(groups), sum(g[2] for g in groups if g[0] >= 0), 0, 0]
+    return head + [v for g in groups for v in g] + [-1] * (4 * (most - len(groups))) + order + [-1] * (T - len(order))
+
+
+@pytest.mark.parametrize("B,most,n", [(1, 1, 1), (1, 9, 4), (5, 4, 3), (64, 1, 200), (100, 3, 7), (1000, 2, 33),
+                                      (1025, 9, 1000), (8192, 1, 16384), (30, 400, 5)])
+def test_adapter_plan(B, most, n):
+    rng = np.random.default_rng(B + n)
+    for pad in (0, 3):
+        ids = rng.integers(-1, n, B)
+        lens = rng.integers(0, most + 1, B) if most > 1 else np.ones(B, int)
+        cu = np.concatenate([[0], np.cumsum(lens)])
+        T = int(cu[-1]) + pad
+        got = tp.tp_lora_plan(i32(ids), T, n, cu_seqlens=i32(cu))
+        assert got.tolist() == groups_ref(ids.tolist(), cu.tolist(), T, n)
+        if most == 1:
+            assert tp.tp_lora_plan(i32(ids), B, n).tolist() == groups_ref(ids.tolist(), cu.tolist(), B, n)
+    assert status() == 0
+
+
+def test_adapter_plan_of_bad_values():
+    got = tp.tp_lora_plan(i32([1, 5, -7]), 3, 2)  # an adapter there is none of: none
+    assert got.tolist() == groups_ref([1, -1, -1], [0, 1, 2, 3], 3, 2)
+    assert status() == tp.TP_ERR_INVALID_ARG
+    for cu in ([0, 3, 2, 4], [0, 1, 2, 9], [1, 2, 3, 4], [-1, 0, 1, 2]):
+        got = tp.tp_lora_plan(i32([0, 1, 0]), 4, 2, cu_seqlens=i32(cu))
+        assert got.tolist() == [0] * 4 + [-1] * 12 + [-1] * 4
+        assert status() == tp.TP_ERR_INVALID_ARG
+
+
+# ------------------------------------------------------------------ the adapters
+def lora_ref(x, a, b, ids, scales, y):
+    """(outputs, sizes of what was summed) in float64, per rank; ids per token, -2: no sequence's."""
+    x, a, b = ([t.double() for t in v] for v in (x, a, b))
+    out, big = [t.double().clone() for t in y], [torch.zeros_like(t, dtype=torch.float64) for t in y]
+    for i in set(ids.tolist()) - {-1, -2}:
+        rows = (ids == i).nonzero()[:, 0]
+        s = 1.0 if scales is None else float(scales[i])
+        h = s * sum(xr[rows] @ ar[i].T for xr, ar in zip(x, a))
+        hb = abs(s) * sum(xr[rows].abs() @ ar[i].abs().T for xr, ar in zip(x, a))
+        for r in range(len(b)):
+            out[r][rows] += h @ b[r][i].T
+            big[r][rows] += hb @ b[r][i].abs().T
+    return out, big
+
+
+def check_lora(got, x, a, b, ids, scales, y, dt):
+    ref, big = lora_ref(x, a, b, ids, scales, y)
+    K, R = sum(t.shape[1] for t in x), a[0].shape[1]
+    lost = (2.0 ** -16 if dt == BF16 else 2.0 ** -20) + (K + R) * 2.0 ** -23
+    live = ids > -2
+    for g, f, s, start in zip(got, ref, big, y):
+        assert torch.equal(g[~live], start[~live])
+        d = (g.double() - f).abs()[live]
+        tol = (U[g.dtype] * f.abs() + lost * s)[live] + 2.0 ** -24
+        assert (d <= tol).all(), float((d / tol).max())
+        none = ids == -1
+        assert torch.equal(g[none], start[none])
+
+
+def lora_data(form, T, N, K, O, R, n, dt, out_dt, seed, some_without=True):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    nx, ny = (N, 1) if form == "row" else (1, N)
+
+    def normal(shape, std, d):
+        return (torch.randn(shape, generator=g, device="cuda") * std).to(d)
+    x = [normal((T, K // nx), 1, dt) for _ in range(nx)]
+    a = [normal((n, R, K // nx), K ** -0.5, dt) for _ in range(nx)]
+    b = [normal((n, O // ny, R), R ** -0.5, dt) for _ in range(ny)]
+    y = [normal((T, O // ny), 1, out_dt) for _ in range(ny)]
+    scales = torch.rand(n, generator=g, device="cuda") * 2
+    return x, a, b, y, scales
+
+
+def call_lora(form, x, a, b, plan, y, **kw):
+    if form == "column":
+        return tp.tp_lora_all_to_sharded(x[0], a[0], b, plan, y, **kw)
+    out = kw.pop("out", None)
+    return [tp.tp_lora_sharded_to_all(x, a, b[0], plan, y[0], out=None if out is None else out[0], **kw)]
+
+
+@pytest.fixture(params=[tp.TP_POLICY_AUTO, tp.TP_POLICY_SIMT], ids=["auto", "simt"])
+def policy(request):
+    tp.tp_set_policy(request.param)
+    yield request.param
+    tp.tp_set_policy(tp.TP_POLICY_AUTO)
+
+
+@pytest.mark.parametrize("form", ["column", "row"])
+@pytest.mark.parametrize("T,N,K,O,R,n,dt,out_dt", [
+    (1, 1, 64, 64, 16, 1, BF16, BF16), (1, 8, 4096, 4096, 16, 3, BF16, F32), (3, 2, 96, 40, 8, 2, F16, F16),
+    (17, 4, 512, 256, 4, 20, BF16, BF16), (64, 1, 1000, 333, 16, 64, BF16, F32), (33, 3, 333, 99, 5, 4, F16, BF16),
+    (100, 2, 2048, 1024, 64, 7, F16, F32), (50, 8, 640, 128, 128, 5, BF16, F16), (40, 1, 72, 200, 33, 3, BF16, BF16),
+    (1025, 2, 256, 320, 32, 9, BF16, BF16), (1500, 4, 128, 96, 16, 3, F16, F32), (1100, 1, 520, 72, 128, 2, BF16, F32),
+    (2000, 1, 100, 64, 64, 1, F16, BF16), (1030, 2, 30, 10, 1, 50, BF16, F32)])
+def test_adapters(policy, form, T, N, K, O, R, n, dt, out_dt):
+    if (K if form == "row" else O) % N:
+        K, O = -(-K // N) * N, -(-O // N) * N
+    x, a, b, y, scales = lora_data(form, T, N, K, O, R, n, dt, out_dt, T + R)
+    rng = np.random.default_rng(T)
+    for pad, s, in_place in ((0, None, False), (min(5, T - 1), scales, True)):
+        ids = rng.integers(-1, n, T)
+        ids[T - pad:] = -2
+        plan = tp.tp_lora_plan(i32(ids[:T - pad]), T, n, cu_seqlens=i32(np.arange(T - pad + 1)))
+        y0 = [t.clone() for t in y]
+        if in_place:
+            got = call_lora(form, x, a, b, plan, y, scales=s)
+            assert all(p.data_ptr() == t.data_ptr() for p, t in zip(got, y))
+        else:
+            out = [torch.full_like(t, 7) for t in y]
+            got = call_lora(form, x, a, b, plan, y, scales=s, out=out)
+            assert all(torch.equal(p, t) for p, t in zip(y, y0))
+        check_lora(got, x, a, b, dev(ids), s, y0, dt)
+    assert status() == 0
+
+
+@pytest.mark.parametrize("T", [40, 1200])
+@pytest.mark.parametrize("form", ["column", "row"])
+def test_adapters_of_strided_and_unaligned_rows(form, T):
+    """Rows with a stride, that begin at any element; outputs that are columns of one buffer."""
+    N, K, O, R, n = 2, 256, 128, 16, 4
+    x, a, b, y, s = lora_data(form, T, N, K, O, R, n, BF16, F32, 3)
+    ids = np.random.default_rng(1).integers(-1, n, T)
+    plan = tp.tp_lora_plan(i32(ids), T, n)
+    for off in (0, 1):
+        xs = []
+        for t in x:
+            wide = torch.zeros((T, t.shape[1] + 24), dtype=BF16, device="cuda")
+            wide[:, off:off + t.shape[1]] = t
+            xs.append(wide[:, off:off + t.shape[1]])
+        cols = y[0].shape[1]
+        one = torch.full((T, cols * len(y) + 8), 9.0, device="cuda")
+        out = [one[:, off + r * cols:off + (r + 1) * cols] for r in range(len(y))]
+        got = call_lora(form, xs, a, b, plan, y, scales=s, out=out)
+        check_lora(got, x, a, b, dev(ids), s, y, BF16)
+        assert bool((one[:, :off] == 9).all()) and bool((one[:, off + cols * len(y):] == 9).all())
+    assert status() == 0
+
+
+def test_adapters_give_the_same_bytes_again_and_alone():
+    """Twice the same, and a token's outputs do not depend on the tokens beside it."""
+    T, N, K, O, R, n = 200, 2, 1024, 512, 16, 5
+    x, a, b, y, s = lora_data("column", T, N, K, O, R, n, BF16, BF16, 8)
+    ids = np.random.default_rng(2).integers(0, n, T)
+    plan = tp.tp_lora_plan(i32(ids), T, n)
+    outs = [call_lora("column", x, a, b, plan, y, scales=s, out=[torch.empty_like(t) for t in y]) for _ in range(2)]
+    assert all(torch.equal(p, q) for p, q in zip(*outs))
+    for t in (0, 77, 199):
+        alone = tp.tp_lora_plan(i32(ids[t:t + 1]), 1, n)
+        got = call_lora("column", [x[0][t:t + 1]], a, b, alone, [v[t:t + 1] for v in y], scales=s,
+                        out=[torch.empty_like(v[t:t + 1]) for v in y])
+        assert all(torch.equal(g[0], o[t]) for g, o in zip(got, outs[0]))
+
+
+@pytest.mark.parametrize("dt", [BF16, F16])
+@pytest.mark.parametrize("T", [30, 1100])
+def test_adapters_not_finite_and_extreme(dt, T):
+    """What is not finite stays in its token and its adapter; sizes from one end of the type to the other."""
+    K, O, R, n = 128, 64, 16, 3
+    x, a, b, y, _ = lora_data("column", T, 1, K, O, R, n, dt, F32, 4)
+    ids = np.arange(T) % n
+    ids[9] = 0
+    big = 2.0 ** 60 if dt == BF16 else 6e4
+    for t, v in ((3, big), (4, 1 / big), (6, 2.0 ** -20)):
+        x[0][t] = (x[0][t].float() * v).to(dt).clamp(-6e4 if dt == F16 else -big * 8, 6e4 if dt == F16 else big * 8)
+    plan = tp.tp_lora_plan(i32(ids), T, n)
+    clean = call_lora("column", x, a, b, plan, y, out=[torch.empty_like(t) for t in y])
+    check_lora(clean, x, a, b, dev(ids), None, y, dt)
+    x2, a2 = [x[0].clone()], [a[0].clone()]
+    x2[0][9, 5] = float("nan")
+    x2[0][12, 7] = float("inf")
+    a2[0][1, 3, 2] = float("nan")
+    got = call_lora("column", x2, a2, b, plan, y, out=[torch.empty_like(t) for t in y])[0]
+    assert torch.isnan(got[9]).all() and not torch.isfinite(got[12]).any()
+    assert torch.isnan(got[dev(ids == 1)]).all()
+    same = dev((ids != 1) & (np.arange(T) != 9) & (np.arange(T) != 12))
+    assert torch.equal(got[same], clean[0][same])
+
+
+def test_adapters_infinite_sums():
+    """An infinite sum gives infinite outputs of its sign, as in float32, not NaN."""
+    x = torch.ones((2, 32), dtype=BF16, device="cuda")
+    x[1, 0] = float("inf")
+    a = torch.ones((1, 16, 32), dtype=BF16, device="cuda")
+    b = torch.ones((1, 24, 16), dtype=BF16, device="cuda")
+    b[0, 1::2] = -1
+    y = torch.zeros((2, 24), device="cuda")
+    got = tp.tp_lora_all_to_sharded(x, a, [b], tp.tp_lora_plan(i32([0, 0]), 2, 1), [y])[0]
+    assert got[0, 0] == 512 and got[0, 1] == -512
+    assert (got[1, 0::2] == float("inf")).all() and (got[1, 1::2] == -float("inf")).all()
+
+
+def test_adapters_of_plans_that_are_none():
+    """Values that no plan holds are recorded; nothing outside the tensors is touched."""
+    T, n = 8, 2
+    x, a, b, y, _ = lora_data("column", T, 1, 64, 64, 16, n, BF16, F32, 4)
+    good = tp.tp_lora_plan(i32([0, 1, 0, 1, 0, 1, -1, 0]), T, n)
+    for at, v in ((0, 1000), (0, -3), (4, 7), (5, -1), (5, 9), (6, 100), (6, -2), (4 + 4 * 3, 8), (4 + 4 * 3 + 2, -5)):
+        bad = good.clone()
+        bad[at] = v
+        call_lora("column", x, a, b, bad, y, out=[torch.empty_like(t) for t in y])
+        assert status() == tp.TP_ERR_INVALID_ARG, (at, v)
+
+
+# ------------------------------------------------------------------ verification
+def part(total, share):
+    return (int(total) * int(share)) >> 24
+
+
+def f32(v):
+    return np.float32(v)
+
+
+def verify_ref(logits, drafts, cu, u, q=None, temperature=None, top_k=None, top_p=None, min_p=None):
+    """The definition with whole numbers of any size: tokens, accepted, rejected, logprobs (float64)."""
+    T, V = logits.shape
+    x = logits.float()
+    x = torch.where(torch.isnan(x), -torch.inf, x).clamp(max=float(np.finfo(np.float32).max)) + 0.0
+    seq = torch.zeros(T, dtype=torch.long)
+    for b in range(len(cu) - 1):
+        seq[cu[b]:cu[b + 1]] = b
+    t = np.ones(len(cu) - 1, np.float32) if temperature is None else temperature.cpu().numpy()
+    greedy = ~(t >= np.float32(2.0 ** -20))
+    inv = torch.ones_like(torch.from_numpy(t)).cuda()
+    inv = torch.where(dev(greedy), inv, 1.0 / dev(np.minimum(t, np.finfo(np.float32).max)))
+    top = x.amax(1, keepdim=True)
+    e_all = torch.exp((x - top) * inv[seq.cuda()][:, None]).cpu().numpy()  # the device's exponential
+    xs, us = x.cpu().numpy(), u.cpu().numpy()
+    qs = None if q is None else np.clip(np.nan_to_num(q.float().cpu().numpy(), nan=0.0, posinf=1.0, neginf=0.0), 0, 1)
+    d_all = drafts.cpu().numpy()
+    tokens, logprobs = np.full(T, -1), np.zeros(T)
+    accepted, rejected = [], []
+    for b in range(len(cu) - 1):
+        r0, r1 = cu[b], cu[b + 1]
+        accepted.append(0), rejected.append(0)
+        for i in range(r0, r1):
+            row = xs[i]
+            if row.max() == -np.inf:
+                logprobs[i], rejected[b] = -np.inf, r1 - 1 - i
+                break
+            e = e_all[i]
+            w = [int(v) for v in np.floor(e.astype(np.float64) * 2.0 ** 40)]
+            order = np.argsort(-row, kind="stable")
+            k = 1 if greedy[b] else int(top_k[b]) if top_k is not None and 0 < int(top_k[b]) < V else V
+            kept = list(order[:k])
+            p = 1.0 if top_p is None else float(top_p[b])
+            if p < 1 and not (greedy[b] or k == 1):
+                cut, before, n = part(sum(w[j] for j in kept), int(f32(max(p, 0)) * f32(2 ** 24))), 0, 0
+                for j in kept:
+                    if n and before >= cut:
+                        break
+                    before, n = before + w[j], n + 1
+                kept = kept[:n]
+            m = 0.0 if min_p is None else float(min_p[b])
+            m = min(m, 1.0) if m > 0 else 0.0
+            kept = [j for j in kept if not e[j] < f32(m)]
+            W = sum(w[j] for j in kept)
+            s = f32(1) / (f32(W) * f32(2.0 ** -40))
+            prob = np.zeros(V, np.float32)
+            prob[kept] = e[kept] * s
+            wk = np.zeros(V, object)
+            wk[kept] = [w[j] for j in kept]
+            d = int(d_all[i]) if i < r1 - 1 else -1
+            z = np.log(np.sum(np.exp(row.astype(np.float64) - row.max())))
+            if d >= 0:
+                theirs = qs[i] if qs is not None else (np.arange(V) == d).astype(np.float32)
+                ui = min(f32(us[i]), f32(1 - 2.0 ** -24)) if us[i] > 0 else f32(0)
+                if ui * theirs[d] < prob[d]:
+                    tokens[i], logprobs[i] = d, float(row[d]) - row.max() - z
+                    accepted[b] += 1
+                    continue
+                rest = np.floor(np.maximum(prob - theirs, f32(0)).astype(np.float64) * 2.0 ** 40)
+                if rest.sum() > 0:
+                    wk = np.array([int(v) for v in rest], object)
+            ul = us[r1 - 1]
+            share = min(int(min(f32(ul), f32(1)) * f32(2 ** 24)), 2 ** 24 - 1) if ul > 0 else 0
+            run, r = np.cumsum(wk), part(sum(wk), share)
+            tokens[i] = int(np.argmax(run > r))
+            logprobs[i] = float(row[tokens[i]]) - row.max() - z
+            rejected[b] = r1 - 1 - i
+            break
+    return tokens, logprobs, accepted, rejected
+
+
+def check_verify(got, ref):
+    tokens, logprobs, accepted, rejected = got
+    torch.cuda.synchronize()
+    assert accepted.tolist() == ref[2]
+    assert rejected.tolist() == ref[3]
+    assert tokens.tolist() == ref[0].tolist()
+    lp = logprobs.double().cpu().numpy()
+    assert np.array_equal(np.isinf(lp), np.isinf(ref[1]))
+    # float32 subtraction of logits, and a logarithm of a sum whose terms are 2^-20 off at most
+    live = np.isfinite(lp)
+    assert np.all(np.abs(lp[live] - ref[1][live]) <= 2.0 ** -18 * (1 + np.abs(ref[1][live])))
+
+
+def drafted(B, lo, hi, V, dt, q_dt, seed, std=2.5, noise=0.7):
+    """Logits, drafts of a nearby distribution, offsets, random numbers, the distribution."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    rng = np.random.default_rng(seed)
+    n = rng.integers(lo, hi + 1, B)
+    cu = np.concatenate([[0], np.cumsum(n + 1)])
+    T = int(cu[-1])
+    x = torch.randn((T, V), generator=g, device="cuda") * std
+    q = torch.softmax(x + noise * torch.randn((T, V), generator=g, device="cuda"), 1)
+    pick = torch.rand((T, 1), generator=g, device="cuda", dtype=torch.float64)
+    d = (q.double().cumsum(1) < pick).sum(1).clamp(max=V - 1)
+    u = torch.rand(T, generator=g, device="cuda")
+    return x.to(dt), d, cu.tolist(), u, None if q_dt is None else q.to(q_dt)
+
+
+def settings_of(B, seed):
+    rng = np.random.default_rng(seed)
+    return dict(temperature=dev(rng.choice(np.float32([0, 0.3, 0.7, 1, 1, 1.5]), B)),
+                top_k=i32(rng.choice([0, 0, 1, 2, 20, 700], B)), top_p=dev(rng.choice(np.float32([1, 0.999, 0.9, 0.5, 0], ), B)),
+                min_p=dev(rng.choice(np.float32([0, 0, 0.05, 1]), B)))
+
+
+@pytest.mark.parametrize("B,lo,hi,V,dt,q_dt", [
+    (1, 0, 0, 1, F32, F32), (1, 4, 4, 50, F32, F32), (5, 0, 6, 1000, F32, None), (7, 1, 3, 4097, BF16, F32),
+    (3, 2, 2, 50272, F32, BF16), (40, 0, 5, 333, F16, F16), (200, 1, 1, 30, F32, F32), (2, 1, 1, 60001, BF16, None),
+    (1, 40, 40, 517, F32, F32)])
+@pytest.mark.parametrize("filters", [False, True])
+def test_verify(B, lo, hi, V, dt, q_dt, filters):
+    x, d, cu, u, q = drafted(B, lo, hi, V, dt, q_dt, B + V)
+    s = settings_of(B, V) if filters else {}
+    got = tp.tp_verify(x, d, i32(cu), u, draft_probs=q, **s)
+    check_verify(got, verify_ref(x, d, cu, u, q, **s))
+    assert status() == 0
+
+
+def test_verify_more_rows_than_the_gpu_holds():
+    """Rows whose filters take several passes come first; the results keep their places."""
+    x, d, cu, u, q = drafted(90, 0, 4, 2000, F32, F32, 1)
+    s = settings_of(90, 3)
+    check_verify(tp.tp_verify(x, d, i32(cu), u, draft_probs=q, **s), verify_ref(x, d, cu, u, q, **s))
+
+
+@pytest.mark.parametrize("C_rows", [1, 3])
+def test_verify_long_rows_of_several_ctas(C_rows):
+    x, d, cu, u, q = drafted(C_rows, 1, 2, 130003, F16, F16, 5, std=1.0)
+    for s in ({}, settings_of(C_rows, 2)):
+        check_verify(tp.tp_verify(x, d, i32(cu), u, draft_probs=q, **s), verify_ref(x, d, cu, u, q, **s))
+
+
+def test_verify_strides_and_given_outputs():
+    x, d, cu, u, q = drafted(6, 0, 3, 77, F32, F16, 9)
+    T = len(d)
+    wide, wide_q = torch.zeros((T, 100), device="cuda"), torch.zeros((T, 83), dtype=F16, device="cuda")
+    wide[:, 3:80], wide_q[:, 1:78] = x, q
+    out = [torch.empty(T, dtype=torch.int64, device="cuda"), torch.empty(T, device="cuda"),
+           torch.empty(6, dtype=torch.int32, device="cuda"), torch.empty(6, dtype=torch.int32, device="cuda")]
+    got = tp.tp_verify(wide[:, 3:80], d, i32(cu), u, draft_probs=wide_q[:, 1:78], tokens=out[0], logprobs=out[1],
+                       accepted=out[2], rejected=out[3])
+    assert all(a is b for a, b in zip(got, out))
+    check_verify(got, verify_ref(x, d, cu, u, q))
+
+
+def test_verify_borders():
+    """Random numbers at both ends, drafts that are certain or impossible, nothing left over, no draft, equal logits."""
+    V = 12
+    x = torch.zeros((24, V), device="cuda")
+    x[8:12, 3:] = -float("inf")
+    x[12:14] = -float("inf")
+    x[14:16, 5] = float("inf")
+    x[16:18, 2] = float("nan")
+    d = torch.tensor([0, 5, 11, 0, 3, -1, 4, 0, 1, 7, 2, 0, 3, 0, 5, 0, 2, 0, 9, 9, 9, 9, 9, 0], device="cuda")
+    cu = [0, 4, 8, 12, 14, 16, 18, 24]
+    u = torch.tensor([0, 0.999, 1.0, 0, 0, 0.5, 0, 0.999999, 0.5, 0, 0, 0.3, 0, 0.5, 0.9, 0.5, 0, 1.0, float("nan"), -1, 0,
+                      0.01, 0.02, 2.0], device="cuda")
+    q = torch.softmax(x.nan_to_num(0, 1, -50), 1)  # as the target itself: nothing left over
+    q[20] = float("nan")
+    q[21] = -1
+    q[22] = float("inf")
+    for probs in (q, None, torch.zeros_like(q), torch.ones_like(q)):
+        check_verify(tp.tp_verify(x, d, i32(cu), u, draft_probs=probs), verify_ref(x, d, cu, u, probs))
+        s = dict(temperature=dev(np.float32([0, 1, np.inf, 1, 1, 0.5, 1])), top_k=i32([0, 3, 2, 1, 0, 500, 4]),
+                 top_p=dev(np.float32([1, 0.5, 1, 0, 0.9, 2, -1])), min_p=dev(np.float32([0, 1, 5, 0, 0.5, -1, 0])))
+        check_verify(tp.tp_verify(x, d, i32(cu), u, draft_probs=probs, **s), verify_ref(x, d, cu, u, probs, **s))
+    assert status() == 0
+
+
+def test_verify_empty_sequences_and_rows_of_none():
+    x, d, _, u, q = drafted(4, 1, 1, 40, F32, F32, 2)
+    cu = [0, 0, 3, 3, 5, 5]
+    keep = torch.full((len(d),), 77, dtype=torch.int64, device="cuda")
+    got = tp.tp_verify(x, d, i32(cu), u, draft_probs=q, tokens=keep)
+    ref = verify_ref(x, d, cu, u, q)
+    assert got[0][5:].tolist() == [77] * 3  # rows of no sequence are left alone
+    assert got[0][:5].tolist() == ref[0][:5].tolist()
+    assert got[2].tolist() == ref[2] and got[3].tolist() == ref[3]
+    none = tp.tp_verify(x[:0], d[:0], i32([0, 0, 0]), u[:0])
+    assert none[2].tolist() == [0, 0] and none[3].tolist() == [0, 0]
+    assert status() == 0
+
+
+def test_verify_bad_values_are_recorded():
+    x, d, cu, u, q = drafted(3, 2, 2, 40, F32, F32, 2)
+    bad = d.clone()
+    bad[1] = 40
+    got = tp.tp_verify(x, bad, i32(cu), u, draft_probs=q)
+    assert status() == tp.TP_ERR_INVALID_ARG
+    ended = d.clone()
+    ended[1] = -1
+    ref = verify_ref(x, ended, cu, u, q)
+    assert got[0].tolist() == ref[0].tolist()
+    for off in ([0, 3, 2, 9], [0, 3, 6, 10], [-1, 3, 6, 9]):
+        got = tp.tp_verify(x, d, i32(off), u, draft_probs=q)
+        assert status() == tp.TP_ERR_INVALID_ARG
+        assert got[2].min() >= 0
+
+
+@pytest.mark.parametrize("with_q", [True, False])
+def test_verified_tokens_follow_the_target(with_q):
+    """Whatever the draft is, the first token is distributed as the target says: 200000 sequences, 5 deviations."""
+    V, B = 6, 200000
+    logits = torch.tensor([0.5, -1.0, 2.0, 0.0, 1.0, -3.0], device="cuda")
+    draft = torch.tensor([0.3, 0.25, 0.05, 0.2, 0.1, 0.1], device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(3)
+    d = torch.zeros((B, 2), dtype=torch.int64, device="cuda")
+    d[:, 0] = torch.multinomial(draft, B, replacement=True, generator=g)
+    if not with_q:
+        d[:, 0] = 4
+    u = torch.rand((B, 2), generator=g, device="cuda").flatten()
+    x = logits.expand(2 * B, V).contiguous()
+    q = draft.expand(2 * B, V).contiguous() if with_q else None
+    tokens, _, accepted, _ = tp.tp_verify(x, d.flatten(), i32(np.arange(B + 1) * 2), u, draft_probs=q)
+    p = torch.softmax(logits.double(), 0).cpu().numpy()
+    seen = np.bincount(tokens.view(B, 2)[:, 0].cpu().numpy(), minlength=V) / B
+    assert np.all(np.abs(seen - p) <= 5 * np.sqrt(p * (1 - p) / B))
+    rate = np.minimum(p, draft.double().cpu().numpy()).sum() if with_q else p[4]
+    assert abs(float(accepted.double().mean()) - rate) <= 5 * np.sqrt(rate * (1 - rate) / B)
