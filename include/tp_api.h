@@ -699,10 +699,13 @@ int tp_sample(const void *logits, int64_t B, int64_t V, int64_t ld, tp_dtype in_
  *     scales NULL (1) or float32 (n);
  *     y[r], out[r]  (T, O / N), or (T, O); out may be y (one row stride then),
  *            else they do not overlap.
- *   The products are summed in float32; the sum over x meets B as two terms of
- *   dt, which keep 16 of its bits (22 for TP_F16), and the result is rounded once.
- *   The ranks' parts are added in a fixed order: the same call gives the same
- *   bytes.  plan_size counts plan's values: a plan of another T or n is refused
+ *     workspace  NULL or float32 (tp_lora_workspace_floats(T, R)), 16-byte
+ *            aligned, the call's own until it has ended on the stream: with it,
+ *            steps of more than 1024 tokens take two faster passes.
+ *   The products are summed in float32; the sum over x meets B as terms of dt that
+ *   keep 16 of its bits, 22 or more for TP_F16 and for float32 outputs, and the
+ *   result is rounded once.  The ranks' parts are added in a fixed order: the
+ *   same call gives the same bytes.  plan_size counts plan's values: a plan of another T or n is refused
  *   (TP_ERR_INVALID_ARG); one that is not a plan is recorded in the status word.
  *
  * tp_verify: drafted tokens checked against the target's probabilities.  Rows
@@ -735,8 +738,8 @@ int tp_sample(const void *logits, int64_t B, int64_t V, int64_t ld, tp_dtype in_
  * Errors: TP_ERR_UNSUPPORTED for more sequences or adapters than these, R above
  * 128, a page or V this build does not take; TP_ERR_NOT_DIVISIBLE if K (of the
  * row-parallel) or O (of the column-parallel) does not divide by N;
- * TP_ERR_ALIGNMENT for a pointer not aligned to its element size (plan: 16
- * bytes); TP_ERR_INVALID_ARG for null pointers, a row stride below the row, N
+ * TP_ERR_ALIGNMENT for a pointer not aligned to its element size (plan and
+ * workspace: 16 bytes); TP_ERR_INVALID_ARG for null pointers, a row stride below the row, N
  * outside 1..64, a negative size.  An adapter call of no rows and a verification
  * of no sequences launch nothing; a plan of none is still written.
  */
@@ -746,17 +749,19 @@ int tp_paged_plan(int64_t B, const int32_t *counts, const int32_t *rejected, con
                   int32_t *new_seq_lens, int32_t *new_owned, int32_t *new_free_count, int32_t *missing,
                   int32_t *cu_seqlens, int32_t *positions, int64_t *slots, tp_stream_t stream);
 int64_t tp_lora_plan_ints(int64_t T, int64_t n);
+int64_t tp_lora_workspace_floats(int64_t T, int R);
 int tp_lora_plan(int64_t B, const int32_t *adapters, const int32_t *cu_seqlens, int64_t T, int64_t n,
                  int32_t *plan, tp_stream_t stream);
 int tp_lora_all_to_sharded(int N, const void *x, int64_t T, int64_t K, int64_t ldx, const void *a,
                            const void *const *b, int64_t n, int R, int64_t O, const float *scales,
-                           const int32_t *plan, int64_t plan_size, tp_dtype dt, const void *const *y,
-                           int64_t ldy, void *const *out, int64_t ldo, tp_dtype out_dt, tp_stream_t stream);
+                           const int32_t *plan, int64_t plan_size, float *workspace, tp_dtype dt,
+                           const void *const *y, int64_t ldy, void *const *out, int64_t ldo,
+                           tp_dtype out_dt, tp_stream_t stream);
 int tp_lora_sharded_to_all(int N, const void *const *x, int64_t T, int64_t K, int64_t ldx,
                            const void *const *a, const void *b, int64_t n, int R, int64_t O,
-                           const float *scales, const int32_t *plan, int64_t plan_size, tp_dtype dt,
-                           const void *y, int64_t ldy, void *out, int64_t ldo, tp_dtype out_dt,
-                           tp_stream_t stream);
+                           const float *scales, const int32_t *plan, int64_t plan_size, float *workspace,
+                           tp_dtype dt, const void *y, int64_t ldy, void *out, int64_t ldo,
+                           tp_dtype out_dt, tp_stream_t stream);
 int tp_verify(const void *logits, int64_t T, int64_t V, int64_t ld, tp_dtype in_dt, const int64_t *drafts,
               const void *draft_probs, int64_t ldq, tp_dtype q_dt, int64_t seqs, const int32_t *cu_rows,
               const float *u, const float *temperature, const int32_t *top_k, const float *top_p,

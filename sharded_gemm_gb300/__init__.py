@@ -51,6 +51,7 @@ class _Recording:
     def __init__(self, real):
         self.real = real
         self.calls = []
+        self.keep = []  # tensors that the entry point made for the call
 
     def __getattr__(self, name):
         if not name.startswith("tp_") or name in ("tp_last_error",):
@@ -121,10 +122,11 @@ def _load() -> ctypes.CDLL:
                                vp], i32),
             "tp_lora_plan_ints": ([i64, i64], i64),
             "tp_lora_plan": ([i64, vp, vp, i64, i64, vp, vp], i32),
-            "tp_lora_all_to_sharded": ([i32, vp, i64, i64, i64, vp, vp, i64, i32, i64, vp, vp, i64, i32, vp, i64, vp,
-                                        i64, i32, vp], i32),
-            "tp_lora_sharded_to_all": ([i32, vp, i64, i64, i64, vp, vp, i64, i32, i64, vp, vp, i64, i32, vp, i64, vp,
-                                        i64, i32, vp], i32),
+            "tp_lora_workspace_floats": ([i64, i32], i64),
+            "tp_lora_all_to_sharded": ([i32, vp, i64, i64, i64, vp, vp, i64, i32, i64, vp, vp, i64, vp, i32, vp, i64,
+                                        vp, i64, i32, vp], i32),
+            "tp_lora_sharded_to_all": ([i32, vp, i64, i64, i64, vp, vp, i64, i32, i64, vp, vp, i64, vp, i32, vp, i64,
+                                        vp, i64, i32, vp], i32),
             "tp_verify": ([vp, i64, i64, i64, i32, vp, vp, i64, i32, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp],
                           i32),
             "tp_debug_wait_timeout": ([i64, vp], i32),
@@ -178,7 +180,7 @@ def prepare(entry, *args, **kwargs) -> Prepared:
         raise ValueError("%s made %d library calls; prepare() takes entry points that make one"
                          % (getattr(entry, "__name__", entry), len(rec.calls)))
     fn, cargs = rec.calls[0]
-    return Prepared(fn, cargs, (args, kwargs), result)
+    return Prepared(fn, cargs, (args, kwargs, rec.keep), result)
 
 
 def declared_functions() -> list[str]:
@@ -899,19 +901,41 @@ def tp_lora_plan(adapters, tokens: int, n: int, cu_seqlens=None, out=None, strea
     return _call("tp_lora_plan", (_native or _marshaller()).groups, adapters, tokens, n, cu_seqlens, out, stream)
 
 
+def _lora_workspace(x, a, stream):
+    """The memory of a call of many tokens for the sums over x, None for few.  Of the stream that the call runs on:
+    given back after the call, it is not handed out elsewhere before that stream is done with it."""
+    xs, pool = (t[0] if isinstance(t, (list, tuple)) else t for t in (x, a))
+    if xs.dim() < 2 or pool.dim() < 2 or xs.shape[-2] <= 1024:  # the call says what is wrong
+        return None
+    T, R = xs.shape[-2], pool.shape[-2]
+    rec = getattr(_rec, "active", None)
+    floats = (rec.real if rec is not None else _load()).tp_lora_workspace_floats(T, R)
+    torch = _torch()
+    if stream is None:
+        ws = torch.empty(floats, dtype=torch.float32, device=xs.device)
+    else:
+        side = torch.cuda.ExternalStream(stream, xs.device) if isinstance(stream, int) else stream
+        with torch.cuda.stream(side):
+            ws = torch.empty(floats, dtype=torch.float32, device=xs.device)
+    if rec is not None:
+        rec.keep.append(ws)
+    return ws
+
+
 def tp_lora_all_to_sharded(x, a, b, plan, y, scales=None, out=None, stream=None):
     """Adapters beside a column-parallel projection: out[r] = y[r] + scale (x A^T) B[r]^T
     by each token's adapter; x (T, K), a (n, R, K), b per rank (n, O / N, R), y
     per rank (T, O / N).  Written to y unless ``out`` is given; returns that."""
-    return _call("tp_lora_all_to_sharded", (_native or _marshaller()).lora, True, x, a, b, plan, y, scales, out, stream)
+    return _call("tp_lora_all_to_sharded", (_native or _marshaller()).lora, True, x, a, b, plan,
+                 _lora_workspace(x, a, stream), y, scales, out, stream)
 
 
 def tp_lora_sharded_to_all(x, a, b, plan, y, scales=None, out=None, stream=None):
     """Adapters beside a row-parallel projection: out = y + scale (sum_r x[r] A[r]^T) B^T
     by each token's adapter; x per rank (T, K / N), a per rank (n, R, K / N), b
     (n, O, R), y (T, O).  Written to y unless ``out`` is given; returns that."""
-    return _call("tp_lora_sharded_to_all", (_native or _marshaller()).lora, False, x, a, b, plan, y, scales, out,
-                 stream)
+    return _call("tp_lora_sharded_to_all", (_native or _marshaller()).lora, False, x, a, b, plan,
+                 _lora_workspace(x, a, stream), y, scales, out, stream)
 
 
 def tp_verify(logits, drafts, cu_rows, u, draft_probs=None, temperature=None, top_k=None, top_p=None, min_p=None,

@@ -1,0 +1,145 @@
+// lora.cuh -- what the adapters' kernels share: a call's tiles out of its plan, h as sums
+// of 16-bit numbers, the loads of fragments.
+//
+// A warp-level m16n8k16 product takes its fragments straight from memory, 16 bytes a lane,
+// because a contraction may go through its index in any order that both operands share: a
+// quad's four lanes hold 8 neighbouring elements each, which feed two products (with R of
+// 16 four, for one).  Output columns are dealt to four products so that a lane ends with 8
+// neighbouring ones: column 8 (g / 2) + 2 j + g % 2 of 32 is row g of product j's B.
+#pragma once
+
+#include "mma16.cuh"
+#include "serve.cuh"
+
+namespace tp {
+
+int launch_lora_prompt(const LoraArgs &a, int RP, cudaStream_t s);
+
+namespace {
+
+constexpr int kWarps = 8, kLoraThreads = kWarps * 32;
+
+__device__ __forceinline__ float4 add4(float4 a, float4 b) {
+  return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+}
+
+// Two values as sums of N 16-bit numbers each.  A finite value stays one (bfloat16's
+// rounding may pass its largest), and behind an infinite one come zeros, not NaN.
+template <typename T, int N>
+__device__ __forceinline__ void terms_of(float a, float b, uint32_t *to, int step) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    uint32_t t = Half2<T>::pack(a, b);
+    float2 h = Half2<T>::unpack(t);
+    if (isinf(h.x) || isinf(h.y)) {
+      if (Half2<T>::kBf16) {  // cut instead
+        if (isinf(h.x) && !isinf(a)) t = (t & 0xffff0000u) | __float_as_uint(a) >> 16;
+        if (isinf(h.y) && !isinf(b)) t = (t & 0xffffu) | (__float_as_uint(b) & 0xffff0000u);
+        h = Half2<T>::unpack(t);
+      }
+      a = isinf(h.x) ? 0.0f : a - h.x, b = isinf(h.y) ? 0.0f : b - h.y;
+    } else {
+      a -= h.x, b -= h.y;
+    }
+    to[i * step] = t;
+  }
+}
+
+// Tile `tile` of the plan, counting on from group `base` (tiles `before` it): its adapter,
+// first place and tokens; false behind the last.  The same in all lanes.
+__device__ __forceinline__ bool find_tile(const LoraArgs &a, int groups, int rows, int64_t tile, int &base,
+                                          int64_t &before, int4 &found) {
+  const int lane = threadIdx.x % 32;
+  const int4 *list = reinterpret_cast<const int4 *>(a.plan + 4);
+  for (; base < groups; base += 32) {
+    int4 g = make_int4(-1, 0, 0, 0);
+    if (base + lane < groups) {
+      g = __ldg(list + base + lane);
+      if (g.x >= a.n || g.y < 0 || g.z < 0 || (int64_t)g.y + g.z > a.T) {  // not a plan of this call
+        g = make_int4(-1, 0, 0, 0);
+        record_bad_value(a.status);
+      }
+    }
+    const int mine = g.x < 0 && a.in_place ? 0 : (g.z + rows - 1) / rows;
+    int run = mine;
+#pragma unroll
+    for (int m = 1; m < 32; m *= 2) {
+      const int o = __shfl_up_sync(0xffffffffu, run, m);
+      if (lane >= m) run += o;
+    }
+    const int all = __shfl_sync(0xffffffffu, run, 31);
+    if (tile < before + all) {
+      const int at = (int)(tile - before);
+      const uint32_t in = __ballot_sync(0xffffffffu, at >= run - mine && at < run);
+      const int l = __ffs(in) - 1, skip = (at - __shfl_sync(0xffffffffu, run - mine, l)) * rows;
+      found.x = __shfl_sync(0xffffffffu, g.x, l);
+      found.y = __shfl_sync(0xffffffffu, g.y, l) + skip;
+      found.z = min(rows, __shfl_sync(0xffffffffu, g.z, l) - skip);
+      return true;
+    }
+    before += all;
+  }
+  return false;
+}
+
+// The exponent that takes the largest finite value of a row of h to 2^14..2^15, below
+// float16's largest; the same in all lanes.
+template <int RP>
+__device__ __forceinline__ int row_exponent(const float *row) {
+  float most = 0.0f;
+  for (int c = threadIdx.x % 32; c < RP; c += 32) {
+    const float v = fabsf(row[c]);
+    most = fmaxf(most, v <= 3.402823466e38f ? v : 0.0f);
+  }
+  most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));
+  return most > 0.0f ? max(-100, min(100, 14 - ilogbf(most))) : 0;
+}
+
+// h (rows of a stride of STRIDE floats, float16's scaled) as fragments of N terms.
+template <typename T, int RP, int MT, int N, int STRIDE>
+__device__ __forceinline__ void make_fragments(const float *h, uint4 (*frag)[MT][RP / 16][32]) {
+  constexpr int KS = RP / 16;
+  for (int i = threadIdx.x; i < MT * KS * 32; i += kLoraThreads) {
+    const int l = i % 32, ks = i / 32 % KS, m = i / (32 * KS);
+    const int c = RP == 16 ? l % 4 * 4 : ks / 2 * 32 + l % 4 * 8 + ks % 2 * 4;
+    const float4 v0 = *reinterpret_cast<const float4 *>(h + (m * 16 + l / 4) * STRIDE + c);
+    const float4 v1 = *reinterpret_cast<const float4 *>(h + (m * 16 + l / 4 + 8) * STRIDE + c);
+    uint32_t f[N][4];
+    terms_of<T, N>(v0.x, v0.y, &f[0][0], 4);
+    terms_of<T, N>(v1.x, v1.y, &f[0][1], 4);
+    terms_of<T, N>(v0.z, v0.w, &f[0][2], 4);
+    terms_of<T, N>(v1.z, v1.w, &f[0][3], 4);
+#pragma unroll
+    for (int n = 0; n < N; ++n) frag[n][m][ks][l] = make_uint4(f[n][0], f[n][1], f[n][2], f[n][3]);
+  }
+}
+
+// Part p of the parts of `per` units, and the unit in it.
+struct Cursor {
+  int p, i;
+  __device__ __forceinline__ Cursor(int at, int per) : p(at / per), i(at % per) {}
+  __device__ __forceinline__ void next(int step, int per) {
+    for (i += step; i >= per; i -= per) ++p;
+  }
+};
+
+__device__ __forceinline__ void read_tokens(const LoraArgs &a, const int4 &tile, int rows, int *to) {
+  const int tid = threadIdx.x;
+  if (tid < rows) {
+    int t = tid < tile.z ? __ldg(a.plan + 4 + 4 * a.most + tile.y + tid) : -1;
+    if (tid < tile.z && (t < 0 || t >= a.T)) {
+      record_bad_value(a.status);
+      t = -1;
+    }
+    to[tid] = t;
+  }
+}
+__device__ __forceinline__ int groups_of(const LoraArgs &a) {
+  const int groups = __ldg(a.plan);
+  if (groups >= 0 && groups <= a.most) return groups;
+  record_bad_value(a.status);
+  return 0;
+}
+
+}  // namespace
+}  // namespace tp

@@ -633,20 +633,21 @@ static int one_of(PyObject *t, Ranks *o, int dim, const char *name) {
   return rc;
 }
 
-/* lora(fn, column, x, a, b, plan, y, scales, out, stream) -> out */
+/* lora(fn, column, x, a, b, plan, workspace, y, scales, out, stream) -> out */
 static PyObject *m_lora(PyObject *self, PyObject *const *a, Py_ssize_t na) {
-  if (na != 10) return PyErr_Format(PyExc_TypeError, "lora takes 10 arguments");
+  if (na != 11) return PyErr_Format(PyExc_TypeError, "lora takes 11 arguments");
   void *fn = PyLong_AsVoidPtr(a[0]);
   const int column = PyObject_IsTrue(a[1]);
   Ranks x, A_, B_, y, out;
   int64_t ldx, ldy, ldo, size;
-  uint64_t plan, scales, stream;
+  uint64_t plan, room = 0, scales, stream;
+  int64_t floats;
   long dev;
-  PyObject *to = a[8] == Py_None ? a[6] : a[8];
+  PyObject *to = a[9] == Py_None ? a[7] : a[9];
   if (column ? one_of(a[2], &x, 2, "x") || one_of(a[3], &A_, 3, "a") || ranks_of(a[4], &B_, 3, "b") ||
-                   ranks_of(a[6], &y, 2, "y") || ranks_of(to, &out, 2, "out")
+                   ranks_of(a[7], &y, 2, "y") || ranks_of(to, &out, 2, "out")
              : ranks_of(a[2], &x, 2, "x") || ranks_of(a[3], &A_, 3, "a") || one_of(a[4], &B_, 3, "b") ||
-                   one_of(a[6], &y, 2, "y") || one_of(to, &out, 2, "out"))
+                   one_of(a[7], &y, 2, "y") || one_of(to, &out, 2, "out"))
     return NULL;
   if (pool_of(&A_, x.dtype, x.dev, "a") || pool_of(&B_, x.dtype, x.dev, "b")) return NULL;
   if (A_.n != x.n || B_.n != y.n) {
@@ -667,25 +668,27 @@ static PyObject *m_lora(PyObject *self, PyObject *const *a, Py_ssize_t na) {
     return NULL;
   }
   if (length_of(a[5], &size, &dev, "plan") || param_of(a[5], &plan, t_i32, size, x.dev, "plan") ||
-      param_of(a[7], &scales, t_f32, n, x.dev, "scales") || stream_of(a[9], x.dev, &stream))
+      param_of(a[8], &scales, t_f32, n, x.dev, "scales") || stream_of(a[10], x.dev, &stream) ||
+      (a[6] != Py_None &&
+       (length_of(a[6], &floats, &dev, "workspace") || param_of(a[6], &room, t_f32, floats, x.dev, "workspace"))))
     return NULL;
   PyObject *keep = Py_NewRef(to);
   if (!fn) {
     if (column)
-      return Py_BuildValue("N(iKLLLKNLiLKKLiNLNLiK)", keep, y.n, x.ptr[0], T, K, ldx, A_.ptr[0], bytes_of(&B_), n, (int)R,
-                           O * y.n, scales, plan, size, x.dt, bytes_of(&y), ldy, bytes_of(&out), ldo, y.dt, stream);
-    return Py_BuildValue("N(iNLLLNKLiLKKLiKLKLiK)", keep, x.n, bytes_of(&x), T, K * x.n, ldx, bytes_of(&A_), B_.ptr[0], n,
-                         (int)R, O, scales, plan, size, x.dt, y.ptr[0], ldy, out.ptr[0], ldo, y.dt, stream);
+      return Py_BuildValue("N(iKLLLKNLiLKKLKiNLNLiK)", keep, y.n, x.ptr[0], T, K, ldx, A_.ptr[0], bytes_of(&B_), n, (int)R,
+                           O * y.n, scales, plan, size, room, x.dt, bytes_of(&y), ldy, bytes_of(&out), ldo, y.dt, stream);
+    return Py_BuildValue("N(iNLLLNKLiLKKLKiKLKLiK)", keep, x.n, bytes_of(&x), T, K * x.n, ldx, bytes_of(&A_), B_.ptr[0], n,
+                         (int)R, O, scales, plan, size, room, x.dt, y.ptr[0], ldy, out.ptr[0], ldo, y.dt, stream);
   }
   int rc;
   Py_BEGIN_ALLOW_THREADS;
   if (column)
     rc = ((__typeof__(&tp_lora_all_to_sharded))fn)(y.n, P(x.ptr[0]), T, K, ldx, P(A_.ptr[0]), CA(B_), n, (int)R, O * y.n,
-                                                   P(scales), P(plan), size, (tp_dtype)x.dt, CA(y), ldy, A(out), ldo,
+                                                   P(scales), P(plan), size, P(room), (tp_dtype)x.dt, CA(y), ldy, A(out), ldo,
                                                    (tp_dtype)y.dt, P(stream));
   else
     rc = ((__typeof__(&tp_lora_sharded_to_all))fn)(x.n, CA(x), T, K * x.n, ldx, CA(A_), P(B_.ptr[0]), n, (int)R, O,
-                                                   P(scales), P(plan), size, (tp_dtype)x.dt, P(y.ptr[0]), ldy,
+                                                   P(scales), P(plan), size, P(room), (tp_dtype)x.dt, P(y.ptr[0]), ldy,
                                                    P(out.ptr[0]), ldo, (tp_dtype)y.dt, P(stream));
   Py_END_ALLOW_THREADS;
   return answer(keep, rc);

@@ -30,6 +30,13 @@ struct GroupArgs {
 inline int64_t most_groups(int64_t T, int64_t n) { return T < n + 1 ? T : n + 1; }
 inline int64_t plan_ints(int64_t T, int64_t n) { return 4 + 4 * most_groups(T, n) + T; }
 
+// Steps of more tokens take two passes with h between them in memory.  (A tile of 16 reads
+// an adapter for every 16 tokens; up to here the second launch costs more.)
+constexpr int64_t kFewTokens = 1024;
+inline int64_t lora_workspace(int64_t T, int R) {
+  return T <= kFewTokens ? 0 : T * (R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 ? 64 : 128);
+}
+
 struct LoraArgs {
   const void *x[kMaxShards], *a[kMaxShards];  // nx parts of the contraction
   const void *b[kMaxShards], *y[kMaxShards];  // ny parts of the output
@@ -40,6 +47,7 @@ struct LoraArgs {
   int nx, ny, R;
   int dt, out_dt;
   int in_place;  // out is y: tokens without an adapter are left alone
+  float *workspace;  // many tokens: (T, R rounded up to 16, 32, 64 or 128); else null
   int *status;
 };
 

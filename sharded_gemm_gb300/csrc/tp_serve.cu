@@ -32,11 +32,18 @@ int check_ranks(int N) {
   return N < 1 || N > kMaxShards ? set_error(TP_ERR_INVALID_ARG, "N must be in 1..%d", kMaxShards) : TP_OK;
 }
 
+int check_widths(int64_t K, int64_t O) {
+  if (K < 1 || O < 1) return set_error(TP_ERR_INVALID_ARG, "need K >= 1, O >= 1");
+  if (K > 1 << 30 || O > 1 << 30)  // counted in 32 bits, a block of 32 behind the end too
+    return set_error(TP_ERR_UNSUPPORTED, "K (%lld) and O (%lld) must be at most 2^30", (long long)K, (long long)O);
+  return TP_OK;
+}
+
 // K and O those of a part.
 int lora(int nx, const void *const *x, int64_t T, int64_t K, int64_t ldx, const void *const *a, int ny,
          const void *const *b, int64_t n, int R, int64_t O, const float *scales, const int32_t *plan,
-         int64_t plan_size, tp_dtype dt, const void *const *y, int64_t ldy, void *const *out, int64_t ldo,
-         tp_dtype out_dt, tp_stream_t stream) {
+         int64_t plan_size, float *workspace, tp_dtype dt, const void *const *y, int64_t ldy, void *const *out,
+         int64_t ldo, tp_dtype out_dt, tp_stream_t stream) {
   if (!is16(dt)) return set_error(TP_ERR_INVALID_ARG, "the adapters hold TP_BF16 or TP_F16");
   if (out_dt != TP_F32 && !is16(out_dt)) return set_error(TP_ERR_INVALID_ARG, "bad dtype");
   if (T < 0 || T > kMost32 || n < 1) return set_error(TP_ERR_INVALID_ARG, "need T in 0..2^31 - 1, n >= 1");
@@ -52,8 +59,8 @@ int lora(int nx, const void *const *x, int64_t T, int64_t K, int64_t ldx, const 
   if (int rc = check_rows(ny, y, T, ldy, O, es, "y")) return rc;
   if (int rc = check_rows(ny, out, T, ldo, O, es, "out")) return rc;
   if (!plan) return set_error(TP_ERR_INVALID_ARG, "null pointer");
-  if (!aligned(plan, 16) || !aligned(scales, 4))
-    return set_error(TP_ERR_ALIGNMENT, "plan not aligned to 16 bytes, or scales not to 4");
+  if (!aligned(plan, 16) || !aligned(workspace, 16) || !aligned(scales, 4))
+    return set_error(TP_ERR_ALIGNMENT, "plan or workspace not aligned to 16 bytes, or scales not to 4");
   if (plan_size != plan_ints(T, n))
     return set_error(TP_ERR_INVALID_ARG, "a plan of %lld values: %lld rows and %lld adapters have %lld",
                      (long long)plan_size, (long long)T, (long long)n, (long long)plan_ints(T, n));
@@ -67,7 +74,7 @@ int lora(int nx, const void *const *x, int64_t T, int64_t K, int64_t ldx, const 
   }
   if (same && (same < ny || (T > 1 && ldy != ldo)))
     return set_error(TP_ERR_INVALID_ARG, "out must be y for all ranks, with one row stride, or for none");
-  l.plan = plan, l.scales = scales;
+  l.plan = plan, l.scales = scales, l.workspace = lora_workspace(T, R) > 0 ? workspace : nullptr;
   l.T = T, l.n = n, l.K = K, l.O = O, l.ldx = ldx, l.ldy = ldy, l.ldo = ldo, l.most = most_groups(T, n);
   l.nx = nx, l.ny = ny, l.R = R, l.dt = dt, l.out_dt = out_dt, l.in_place = same != 0;
   if (int rc = need_status(&l.status)) return rc;
@@ -115,6 +122,8 @@ int tp_paged_plan(int64_t B, const int32_t *counts, const int32_t *rejected, con
 
 int64_t tp_lora_plan_ints(int64_t T, int64_t n) { return T < 0 || n < 0 ? 0 : plan_ints(T, n); }
 
+int64_t tp_lora_workspace_floats(int64_t T, int R) { return T < 0 || R < 1 || R > 128 ? 0 : lora_workspace(T, R); }
+
 int tp_lora_plan(int64_t B, const int32_t *adapters, const int32_t *cu_seqlens, int64_t T, int64_t n, int32_t *plan,
                  tp_stream_t stream) {
   if (B < 0 || T < 0 || T > kMost32 || n < 1) return set_error(TP_ERR_INVALID_ARG, "need B >= 0, T >= 0, n >= 1");
@@ -134,23 +143,25 @@ int tp_lora_plan(int64_t B, const int32_t *adapters, const int32_t *cu_seqlens, 
 
 int tp_lora_all_to_sharded(int N, const void *x, int64_t T, int64_t K, int64_t ldx, const void *a,
                            const void *const *b, int64_t n, int R, int64_t O, const float *scales,
-                           const int32_t *plan, int64_t plan_size, tp_dtype dt, const void *const *y, int64_t ldy,
-                           void *const *out, int64_t ldo, tp_dtype out_dt, tp_stream_t stream) {
+                           const int32_t *plan, int64_t plan_size, float *workspace, tp_dtype dt,
+                           const void *const *y, int64_t ldy, void *const *out, int64_t ldo, tp_dtype out_dt,
+                           tp_stream_t stream) {
   if (int rc = check_ranks(N)) return rc;
-  if (K < 1 || O < 1) return set_error(TP_ERR_INVALID_ARG, "need K >= 1, O >= 1");
+  if (int rc = check_widths(K, O)) return rc;
   if (O % N) return set_error(TP_ERR_NOT_DIVISIBLE, "Cannot shard %lld outputs over %d ranks", (long long)O, N);
-  return lora(1, &x, T, K, ldx, &a, N, b, n, R, O / N, scales, plan, plan_size, dt, y, ldy, out, ldo, out_dt, stream);
+  return lora(1, &x, T, K, ldx, &a, N, b, n, R, O / N, scales, plan, plan_size, workspace, dt, y, ldy, out, ldo, out_dt,
+              stream);
 }
 
 int tp_lora_sharded_to_all(int N, const void *const *x, int64_t T, int64_t K, int64_t ldx, const void *const *a,
                            const void *b, int64_t n, int R, int64_t O, const float *scales, const int32_t *plan,
-                           int64_t plan_size, tp_dtype dt, const void *y, int64_t ldy, void *out, int64_t ldo,
-                           tp_dtype out_dt, tp_stream_t stream) {
+                           int64_t plan_size, float *workspace, tp_dtype dt, const void *y, int64_t ldy, void *out,
+                           int64_t ldo, tp_dtype out_dt, tp_stream_t stream) {
   if (int rc = check_ranks(N)) return rc;
-  if (K < 1 || O < 1) return set_error(TP_ERR_INVALID_ARG, "need K >= 1, O >= 1");
+  if (int rc = check_widths(K, O)) return rc;
   if (K % N) return set_error(TP_ERR_NOT_DIVISIBLE, "Cannot shard %lld inputs over %d ranks", (long long)K, N);
-  return lora(N, x, T, K / N, ldx, a, 1, &b, n, R, O, scales, plan, plan_size, dt, &y, ldy, &out, ldo, out_dt,
-              stream);
+  return lora(N, x, T, K / N, ldx, a, 1, &b, n, R, O, scales, plan, plan_size, workspace, dt, &y, ldy, &out, ldo,
+              out_dt, stream);
 }
 
 int tp_verify(const void *logits, int64_t T, int64_t V, int64_t ld, tp_dtype in_dt, const int64_t *drafts,

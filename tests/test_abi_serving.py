@@ -39,14 +39,14 @@ def _column(L, **kw):
     size = L.tp_lora_plan_ints(kw.get("T", 4), kw.get("n", 3))
     return _of(L.tp_lora_all_to_sharded, dict(
         N=2, x=FAKE, T=4, K=64, ldx=64, a=FAKE, b=_arr(2), n=3, R=8, O=32, scales=None, plan=FAKE, size=size,
-        dt=tp.TP_BF16, y=_arr(2), ldy=16, out=_arr(2), ldo=16, odt=tp.TP_BF16, stream=None), kw)
+        ws=None, dt=tp.TP_BF16, y=_arr(2), ldy=16, out=_arr(2), ldo=16, odt=tp.TP_BF16, stream=None), kw)
 
 
 def _row(L, **kw):
     size = L.tp_lora_plan_ints(kw.get("T", 4), kw.get("n", 3))
     return _of(L.tp_lora_sharded_to_all, dict(
         N=2, x=_arr(2), T=4, K=64, ldx=32, a=_arr(2), b=FAKE, n=3, R=8, O=32, scales=None, plan=FAKE, size=size,
-        dt=tp.TP_F16, y=FAKE, ldy=32, out=FAKE, ldo=32, odt=tp.TP_F32, stream=None), kw)
+        ws=None, dt=tp.TP_F16, y=FAKE, ldy=32, out=FAKE, ldo=32, odt=tp.TP_F32, stream=None), kw)
 
 
 def _verify(L, **kw):
@@ -82,7 +82,7 @@ def test_adapter_plan_refusals(L, kw, code):
 BOTH = [(dict(N=0), BAD), (dict(N=65), BAD), (dict(T=-1), BAD), (dict(K=0), BAD), (dict(O=0), BAD), (dict(n=0), BAD),
         (dict(n=16385), UNSUP), (dict(R=0), BAD), (dict(R=129), UNSUP), (dict(dt=tp.TP_F32), BAD), (dict(odt=5), BAD),
         (dict(ldx=31), BAD), (dict(ldy=15), BAD), (dict(ldo=15), BAD), (dict(plan=None), BAD), (dict(plan=FAKE + 8), ALIGN),
-        (dict(scales=FAKE + 2), ALIGN), (dict(size=4), BAD), (dict(x=None), BAD), (dict(a=None), BAD), (dict(b=None), BAD),
+        (dict(scales=FAKE + 2), ALIGN), (dict(size=4), BAD), (dict(ws=FAKE + 8), ALIGN), (dict(x=None), BAD), (dict(a=None), BAD), (dict(b=None), BAD),
         (dict(y=None), BAD), (dict(out=None), BAD)]
 
 
@@ -115,6 +115,12 @@ def test_sizes_of_adapter_plans(L):
     assert L.tp_lora_plan_ints(0, 5) == 4
     assert L.tp_lora_plan_ints(3, 5) == 4 + 12 + 3
     assert L.tp_lora_plan_ints(100, 5) == 4 + 24 + 100
+
+
+def test_sizes_of_adapter_workspaces(L):
+    assert L.tp_lora_workspace_floats(1024, 16) == 0
+    assert [L.tp_lora_workspace_floats(1025, r) for r in (1, 16, 17, 64, 65, 128)] == [1025 * r for r in (16, 16, 32, 64, 128, 128)]
+    assert L.tp_lora_workspace_floats(2000, 129) == 0 and L.tp_lora_workspace_floats(-1, 8) == 0
 
 
 def test_empty_calls_launch_nothing(L):
