@@ -9,6 +9,8 @@
 // no barrier between the copy and its use.  (As one kernel, h exchanged within a cluster, the
 // barriers between the products stood in the way of the streams, and registers for both were
 // too many: 309 us for 8192 tokens, R = 64, 4096 x 11008, where 66 us of bytes move.)
+#include <type_traits>
+
 #include "lora.cuh"
 
 namespace tp {
@@ -17,20 +19,22 @@ namespace {
 constexpr int kTile = 64;
 
 // ---------------------------------------------------------------- the first pass
-// Eight warps: kM groups of MW blocks of 16 tokens, kG stretches of the contraction.
+// Eight warps: kM groups of MW blocks of 16 tokens, kG stretches of the contraction.  A ring
+// holds units of 32 elements of the contraction: the tokens' rows, then the adapter's.
 template <int RP>
 struct ShrinkShared {
   static constexpr int MW = RP == 128 ? 1 : 2, kM = 4 / MW, kG = kWarps / kM, kStride = RP + 4;
-  static constexpr int kAhead = 4;  // units
+  static constexpr int kAhead = RP == 16 ? 4 : 3, kRows = 2 * MW + RP / 8;  // pieces of 512 bytes a unit
+  static constexpr int kCtas = RP <= 32 ? 2 : 1;                            // of an SM
   union {
-    uint4 ring[kWarps][kAhead][MW * 2][32];
+    uint4 ring[kWarps][kAhead][kRows][32];
     float part[kG][kTile][kStride];  // [0] in the end: this CTA's sums, read by the others
   };
   int token[kTile];
 };
 
 template <typename T, int RP>
-__global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
+__global__ void __launch_bounds__(kLoraThreads, ShrinkShared<RP>::kCtas)
     lora_shrink_kernel(const __grid_constant__ LoraArgs a, int C) {
   typedef ShrinkShared<RP> Shared;
   constexpr int NT = RP / 8, MW = Shared::MW, kG = Shared::kG, kAhead = Shared::kAhead, kStride = Shared::kStride;
@@ -40,7 +44,6 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
   const int rank = blockIdx.x % C, K = (int)a.K, per = (K + 31) / 32, units = per * a.nx;
   const int m0 = warp % Shared::kM * MW, slot = rank * kG + warp / Shared::kM;
   const int u0 = (int)((int64_t)units * slot / (C * kG)), u1 = (int)((int64_t)units * (slot + 1) / (C * kG));
-  uint4 *const ring = &sh.ring[warp][0][0][lane];
   griddep_launch_dependents();
   griddep_wait();
   const int groups = groups_of(a);
@@ -53,24 +56,38 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
     if (C > 1) cluster_sync_all(); else __syncthreads();  // the last tile's sums are read
     read_tokens(a, tile, kTile, sh.token);
     __syncthreads();
-    int t[MW][2];
+    int64_t row[2 * MW];  // where the lane's rows of x begin; without a token, -1
 #pragma unroll
-    for (int m = 0; m < MW; ++m) t[m][0] = sh.token[(m0 + m) * 16 + g], t[m][1] = sh.token[(m0 + m) * 16 + g + 8];
-    Cursor cx(u0, per), ca(u0, per);
-    int ux = u0, x_slot = 0, slot_at = 0;
+    for (int i = 0; i < 2 * MW; ++i) {
+      const int t = sh.token[(m0 + i / 2) * 16 + i % 2 * 8 + g];
+      row[i] = t < 0 ? -1 : t * a.ldx;
+    }
+    Cursor c(u0, per);
+    int ahead = u0, x_slot = 0, slot_at = 0;
+    const uint16_t *x = nullptr, *w = nullptr;
+    auto part = [&]() {
+      x = static_cast<const uint16_t *>(a.x[c.p]);
+      w = static_cast<const uint16_t *>(a.a[c.p]) + ((int64_t)id * a.R + g) * K;
+    };
+    if (u0 < u1) part();
     auto fetch = [&]() {
-      if (ux < u1) {
-        const int k = cx.i * 32 + q * 8;
-        const uint16_t *x = static_cast<const uint16_t *>(a.x[cx.p]);
+      if (ahead < u1) {
+        const int k = c.i * 32 + q * 8;
+        const bool in = k < K;
+        const uint32_t to = smem_u32(&sh.ring[warp][x_slot][0][lane]);
 #pragma unroll
-        for (int i = 0; i < 2 * MW; ++i) {
-          const int row = t[i / 2][i % 2];
-          const bool valid = row >= 0 && k < K;
-          cp_async16(smem_u32(ring + (x_slot * 2 * MW + i) * 32), valid ? x + row * a.ldx + k : x, valid);
+        for (int i = 0; i < 2 * MW; ++i)
+          cp_async16(to + i * 512, row[i] >= 0 && in ? x + row[i] + k : x, row[i] >= 0 && in);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const bool valid = in && j * 8 + g < a.R;
+          cp_async16(to + (2 * MW + j) * 512, valid ? w + (int64_t)j * 8 * K + k : x, valid);
         }
-        cx.next(1, per);
+        const int p = c.p;
+        c.next(1, per);
+        if (c.p != p && ahead + 1 < u1) part();
       }
-      ++ux;
+      ++ahead;
       x_slot = x_slot + 1 == kAhead ? 0 : x_slot + 1;
       cp_async_commit();
     };
@@ -82,29 +99,24 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
 #pragma unroll
       for (int j = 0; j < NT; ++j) acc[m][j][0] = acc[m][j][1] = acc[m][j][2] = acc[m][j][3] = 0.0f;
     for (int u = u0; u < u1; ++u) {
-      const int k = ca.i * 32 + q * 8;
-      const uint16_t *w = static_cast<const uint16_t *>(a.a[ca.p]) + ((int64_t)id * a.R + g) * K + k;
-      uint4 v[NT];
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-        v[j] = j * 8 + g < a.R && k < K ? __ldg(reinterpret_cast<const uint4 *>(w + (int64_t)j * 8 * K)) : make_uint4(0, 0, 0, 0);
-      ca.next(1, per);
       cp_async_wait<kAhead - 2>();
-      uint4 r[MW][2];
+      const uint4(*const ring)[32] = sh.ring[warp][slot_at];
+      uint4 r[2 * MW];
 #pragma unroll
-      for (int i = 0; i < 2 * MW; ++i) r[i / 2][i % 2] = ring[(slot_at * 2 * MW + i) * 32];
-      slot_at = slot_at + 1 == kAhead ? 0 : slot_at + 1;
+      for (int i = 0; i < 2 * MW; ++i) r[i] = ring[i][lane];
       fetch();
 #pragma unroll
-      for (int m = 0; m < MW; ++m) {
-        const uint32_t f0[4] = {r[m][0].x, r[m][1].x, r[m][0].y, r[m][1].y};
-        const uint32_t f1[4] = {r[m][0].z, r[m][1].z, r[m][0].w, r[m][1].w};
+      for (int j = 0; j < NT; ++j) {
+        const uint4 v = ring[2 * MW + j][lane];
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          mma16816<T>(acc[m][j], f0, v[j].x, v[j].y);
-          mma16816<T>(acc[m][j], f1, v[j].z, v[j].w);
+        for (int m = 0; m < MW; ++m) {
+          const uint32_t f0[4] = {r[2 * m].x, r[2 * m + 1].x, r[2 * m].y, r[2 * m + 1].y};
+          const uint32_t f1[4] = {r[2 * m].z, r[2 * m + 1].z, r[2 * m].w, r[2 * m + 1].w};
+          mma16816<T>(acc[m][j], f0, v.x, v.y);
+          mma16816<T>(acc[m][j], f1, v.z, v.w);
         }
       }
+      slot_at = slot_at + 1 == kAhead ? 0 : slot_at + 1;
     }
     cp_async_wait<0>();
     __syncthreads();  // the rings are read
@@ -121,27 +133,27 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
     constexpr int kQuads = kTile * RP / 4;
     if (C > 1) {
       for (int i = tid; i < kQuads; i += kLoraThreads) {
-        const int row = i / (RP / 4), c = i % (RP / 4) * 4;
-        float4 sum = *reinterpret_cast<const float4 *>(&sh.part[0][row][c]);
+        const int r = i / (RP / 4), col = i % (RP / 4) * 4;
+        float4 sum = *reinterpret_cast<const float4 *>(&sh.part[0][r][col]);
 #pragma unroll
-        for (int j = 1; j < kG; ++j) sum = add4(sum, *reinterpret_cast<const float4 *>(&sh.part[j][row][c]));
-        *reinterpret_cast<float4 *>(&sh.part[0][row][c]) = sum;
+        for (int j = 1; j < kG; ++j) sum = add4(sum, *reinterpret_cast<const float4 *>(&sh.part[j][r][col]));
+        *reinterpret_cast<float4 *>(&sh.part[0][r][col]) = sum;
       }
       cluster_sync_all();
     }
     const float scale = a.scales ? __ldg(a.scales + id) : 1.0f;
     for (int i = kQuads / C * rank + tid; i < kQuads / C * (rank + 1); i += kLoraThreads) {
-      const int row = i / (RP / 4), c = i % (RP / 4) * 4;
+      const int r = i / (RP / 4), col = i % (RP / 4) * 4;
       float4 sum = make_float4(0, 0, 0, 0);
       if (C > 1) {
-        const uint32_t mine = smem_u32(&sh.part[0][row][c]);
-        for (int r = 0; r < C; ++r) sum = add4(sum, ld_cluster_f4(mapa_shared(mine, r)));
+        const uint32_t mine = smem_u32(&sh.part[0][r][col]);
+        for (int o = 0; o < C; ++o) sum = add4(sum, ld_cluster_f4(mapa_shared(mine, o)));
       } else {
 #pragma unroll
-        for (int j = 0; j < kG; ++j) sum = add4(sum, *reinterpret_cast<const float4 *>(&sh.part[j][row][c]));
+        for (int j = 0; j < kG; ++j) sum = add4(sum, *reinterpret_cast<const float4 *>(&sh.part[j][r][col]));
       }
-      if (row < tile.z)
-        *reinterpret_cast<float4 *>(a.workspace + (int64_t)(tile.y + row) * RP + c) =
+      if (r < tile.z)
+        *reinterpret_cast<float4 *>(a.workspace + (int64_t)(tile.y + r) * RP + col) =
             make_float4(sum.x * scale, sum.y * scale, sum.z * scale, sum.w * scale);
     }
   }
@@ -149,46 +161,57 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
 }
 
 // ---------------------------------------------------------------- the second pass
+// A warp takes 32 columns of a tile at a time, its lane the rows g and g + 8 of each of the
+// four blocks of 16 tokens, 8 columns of each.  A block's old values are fetched while the
+// one before it is worked on, into the place that was just read.
 template <typename T, int RP, bool OUT32>
 struct ExpandShared {
   static constexpr int kTerms = Half2<T>::kBf16 && OUT32 ? 3 : 2, kStride = RP + 4;
-  static constexpr int kWords = OUT32 ? 2 : 1, kAhead = 6 / kWords;  // of a block of 16 tokens and 32 columns
+  static constexpr int kWords = OUT32 ? 2 : 1;
   union {
-    uint4 ring[kWarps][kAhead][2 * kWords][32];
+    uint4 ring[kWarps][4][2 * kWords][32];
     float h[kTile][kStride];
   };
   uint4 frag[kTerms][4][RP / 16][32];
+  int64_t y_row[kTile], out_row[kTile];  // where the rows begin, in bytes; out: without a token, -1
   int token[kTile];
   float unscale[kTile];
 };
 
-template <typename T>
-__device__ __forceinline__ uint4 add_pairs(uint4 y, const float *d) {
-  uint32_t v[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = Half2<T>::unpack(v[i]);
-    v[i] = Half2<T>::pack(f.x + d[2 * i], f.y + d[2 * i + 1]);
-  }
-  return make_uint4(v[0], v[1], v[2], v[3]);
-}
 __device__ __forceinline__ uint4 add_floats(uint4 y, const float *d) {
   return make_uint4(__float_as_uint(__uint_as_float(y.x) + d[0]), __float_as_uint(__uint_as_float(y.y) + d[1]),
                     __float_as_uint(__uint_as_float(y.z) + d[2]), __float_as_uint(__uint_as_float(y.w) + d[3]));
 }
+template <typename O>
+__device__ __forceinline__ uint4 pack8(const float *d) {
+  return make_uint4(Half2<O>::pack(d[0], d[1]), Half2<O>::pack(d[2], d[3]), Half2<O>::pack(d[4], d[5]),
+                    Half2<O>::pack(d[6], d[7]));
+}
+template <typename O>
+__device__ __forceinline__ void unpack8(const uint4 &v, float *d) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = Half2<O>::unpack(w[i]);
+    d[2 * i] = f.x, d[2 * i + 1] = f.y;
+  }
+}
 
-template <typename T, int RP, bool OUT32>
+// O: the outputs' type.
+template <typename T, int RP, typename O>
 __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
     lora_expand_kernel(const __grid_constant__ LoraArgs a, int S) {
+  constexpr bool OUT32 = sizeof(O) == 4;
   typedef ExpandShared<T, RP, OUT32> Shared;
-  constexpr int KS = RP / 16, kAhead = Shared::kAhead, kTerms = Shared::kTerms, kStride = Shared::kStride;
-  constexpr int kWords = Shared::kWords, kSize = OUT32 ? 4 : 2;
+  constexpr int KS = RP / 16, kTerms = Shared::kTerms, kStride = Shared::kStride, kWords = Shared::kWords;
+  // 16-bit outputs: the products are added to the old values, whose sums lose less than the
+  // rounding does; float32 ones keep the old values out of the products' sums
+  constexpr bool kSeed = !OUT32 && Half2<T>::kBf16;
   extern __shared__ __align__(16) uint8_t smem[];
   Shared &sh = *reinterpret_cast<Shared *>(smem);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, q = lane % 4;
-  const int O = (int)a.O, per = (O + 31) / 32, blocks = per * a.ny, step = S * kWarps;
+  const int cols = (int)a.O, per = (cols + 31) / 32, blocks = per * a.ny, step = S * kWarps;
   const int blk0 = blockIdx.x % S * kWarps + warp;
-  const bool out_bf16 = a.out_dt == TP_BF16;
   uint4 *const ring = &sh.ring[warp][0][0][lane];
   griddep_launch_dependents();
   griddep_wait();
@@ -200,20 +223,25 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
     const int id = tile.x;
     __syncthreads();
     read_tokens(a, tile, kTile, sh.token);
+    if (tid < kTile) {  // read_tokens' own thread
+      const int t = sh.token[tid];
+      sh.y_row[tid] = max(t, 0) * a.ldy * (int64_t)sizeof(O);
+      sh.out_row[tid] = t < 0 ? -1 : t * a.ldo * (int64_t)sizeof(O);
+    }
     if (id >= 0) {
       for (int i = tid; i < kTile * RP / 4; i += kLoraThreads) {
-        const int row = i / (RP / 4), c = i % (RP / 4) * 4;
+        const int r = i / (RP / 4), c = i % (RP / 4) * 4;
         float4 v = make_float4(0, 0, 0, 0);
-        if (row < tile.z) v = __ldcg(reinterpret_cast<const float4 *>(a.workspace + (int64_t)(tile.y + row) * RP + c));
-        *reinterpret_cast<float4 *>(&sh.h[row][c]) = v;
+        if (r < tile.z) v = __ldcg(reinterpret_cast<const float4 *>(a.workspace + (int64_t)(tile.y + r) * RP + c));
+        *reinterpret_cast<float4 *>(&sh.h[r][c]) = v;
       }
       __syncthreads();
       if (!Half2<T>::kBf16) {
-        for (int row = warp; row < kTile; row += kWarps) {
-          const int e = row_exponent<RP>(sh.h[row]);
+        for (int r = warp; r < kTile; r += kWarps) {
+          const int e = row_exponent<RP>(sh.h[r]);
           __syncwarp();
-          for (int c = lane; c < RP; c += 32) sh.h[row][c] = ldexpf(sh.h[row][c], e);
-          if (lane == 0) sh.unscale[row] = ldexpf(1.0f, -e);
+          for (int c = lane; c < RP; c += 32) sh.h[r][c] = ldexpf(sh.h[r][c], e);
+          if (lane == 0) sh.unscale[r] = ldexpf(1.0f, -e);
         }
         __syncthreads();
       }
@@ -221,39 +249,31 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
     }
     __syncthreads();
 
-    // ---- the old outputs ahead of their use
     Cursor cy(blk0, per), c(blk0, per);
-    int y_blk = blk0, y_m = 0, y_slot = 0, at_slot = 0;
-    auto fetch = [&]() {
-      if (y_blk < blocks) {
+    // the old values of block m of the columns that cy names
+    auto fetch = [&](int m, bool any) {
+      if (any) {
         const int col = cy.i * 32 + q * 8;
-        const char *y = static_cast<const char *>(a.y[cy.p]);
+        const char *y = static_cast<const char *>(a.y[cy.p]) + (col < cols ? col : 0) * (int)sizeof(O);
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int t = sh.token[y_m * 16 + r * 8 + g];
-          const bool valid = t >= 0 && col < O;
-          const char *from = valid ? y + (t * a.ldy + col) * kSize : y;
+        for (int r = 0; r < 2; ++r)
 #pragma unroll
           for (int i = 0; i < kWords; ++i)
-            cp_async16(smem_u32(ring + ((y_slot * 2 + r) * kWords + i) * 32), from + 16 * i * valid, valid);
-        }
-        if (++y_m == 4) {
-          y_m = 0, y_blk += step;
-          cy.next(step, per);
-        }
+            cp_async16(smem_u32(ring + ((m * 2 + r) * kWords + i) * 32), y + sh.y_row[m * 16 + r * 8 + g] + 16 * i, true);
       }
-      y_slot = y_slot + 1 == kAhead ? 0 : y_slot + 1;
       cp_async_commit();
     };
-    for (int i = 0; i < kAhead - 1; ++i) fetch();
+#pragma unroll
+    for (int m = 0; m < 4; ++m) fetch(m, blk0 < blocks);
+    cy.next(step, per);
 
     uint4 w[4][RP == 16 ? 1 : KS / 2];
     auto load_b = [&](const Cursor &at) {
-      const uint16_t *b = static_cast<const uint16_t *>(a.b[at.p]) + ((int64_t)id * O + at.i * 32) * a.R;
+      const uint16_t *b = static_cast<const uint16_t *>(a.b[at.p]) + ((int64_t)id * cols + at.i * 32) * a.R;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int r = (g >> 1) * 8 + 2 * j + (g & 1);
-        const bool in = at.i * 32 + r < O;
+        const bool in = at.i * 32 + r < cols;
         const uint16_t *row = b + r * a.R;
         if (RP == 16) {
           const uint2 v = in && q * 4 < a.R ? __ldg(reinterpret_cast<const uint2 *>(row + q * 4)) : make_uint2(0, 0);
@@ -267,13 +287,32 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
     };
     if (id >= 0 && blk0 < blocks) load_b(c);
     for (int blk = blk0; blk < blocks; blk += step) {
-      const int p = c.p, col = c.i * 32 + q * 8;
+      const int col = c.i * 32 + q * 8;
+      char *const out = static_cast<char *>(a.out[c.p]) + col * (int)sizeof(O);
+      const bool in = col < cols, more = blk + step < blocks;
       c.next(step, per);
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
-        float d[4][4];
+        uint4 y[2][kWords];
+        float d[4][4], add[2][8];
+        auto take = [&]() {  // the old values, and the fetch of the next into their place
+          cp_async_wait<3>();
 #pragma unroll
-        for (int j = 0; j < 4; ++j) d[j][0] = d[j][1] = d[j][2] = d[j][3] = 0.0f;
+          for (int i = 0; i < 2 * kWords; ++i) y[i / kWords][i % kWords] = ring[(m * 2 * kWords + i) * 32];
+          fetch(m, more);
+        };
+        if (kSeed) {
+          take();
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            unpack8<typename std::conditional<OUT32, __half, O>::type>(y[r][0], add[r]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) d[j][2 * r] = add[r][2 * j], d[j][2 * r + 1] = add[r][2 * j + 1];
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) d[j][0] = d[j][1] = d[j][2] = d[j][3] = 0.0f;
+        }
         if (id >= 0) {
 #pragma unroll
           for (int s = 0; s < KS; ++s)
@@ -287,36 +326,34 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
                 mma16816<T>(d[j], hf, s % 2 ? b.z : b.x, s % 2 ? b.w : b.y);
               }
             }
-          if (m == 3 && blk + step < blocks) load_b(c);
+          if (m == 3 && more) load_b(c);
         }
-        cp_async_wait<kAhead - 2>();
-        uint4 y[2][kWords];
-#pragma unroll
-        for (int i = 0; i < 2 * kWords; ++i) y[i / kWords][i % kWords] = ring[(at_slot * 2 * kWords + i) * 32];
-        at_slot = at_slot + 1 == kAhead ? 0 : at_slot + 1;
-        fetch();
+        if (!kSeed) take();
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const int t = sh.token[m * 16 + r * 8 + g];
-          if (id >= 0) {
-            const float f = Half2<T>::kBf16 ? 1.0f : sh.unscale[m * 16 + r * 8 + g];
-            float add[8];
+          const float f = Half2<T>::kBf16 || id < 0 ? 1.0f : sh.unscale[m * 16 + r * 8 + g];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) add[2 * j] = d[j][2 * r] * f, add[2 * j + 1] = d[j][2 * r + 1] * f;
-            if (OUT32) {
-              y[r][0] = add_floats(y[r][0], add);
-              y[r][kWords - 1] = add_floats(y[r][kWords - 1], add + 4);
-            } else {
-              y[r][0] = out_bf16 ? add_pairs<__nv_bfloat16>(y[r][0], add) : add_pairs<__half>(y[r][0], add);
-            }
+          for (int j = 0; j < 4; ++j) add[r][2 * j] = d[j][2 * r] * f, add[r][2 * j + 1] = d[j][2 * r + 1] * f;
+          if constexpr (OUT32) {
+            if (id >= 0) y[r][0] = add_floats(y[r][0], add[r]), y[r][1] = add_floats(y[r][1], add[r] + 4);
+          } else if constexpr (kSeed) {
+            if (id >= 0) y[r][0] = pack8<O>(add[r]);
+          } else if (id >= 0) {
+            float old[8];
+            unpack8<O>(y[r][0], old);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) add[r][i] += old[i];
+            y[r][0] = pack8<O>(add[r]);
           }
-          if (t >= 0 && col < O) {
-            uint4 *to = reinterpret_cast<uint4 *>(static_cast<char *>(a.out[p]) + (t * a.ldo + col) * kSize);
+          const int64_t row = sh.out_row[m * 16 + r * 8 + g];
+          if (row >= 0 && in) {
+            uint4 *to = reinterpret_cast<uint4 *>(out + row);
 #pragma unroll
             for (int i = 0; i < kWords; ++i) to[i] = y[r][i];
           }
         }
       }
+      cy.next(step, per);
     }
     cp_async_wait<0>();
   }
@@ -350,16 +387,17 @@ template <typename T, int RP>
 int launch(const LoraArgs &a, cudaStream_t s) {
   int64_t tiles = a.T / kTile + a.most;  // at most
   if (tiles > (1 << 20)) tiles = 1 << 20;
-  const int64_t slots = 2 * sm_count();
+  const int64_t room = (int64_t)ShrinkShared<RP>::kCtas * sm_count();
   int C = 1;
-  while (C < 8 && tiles * C * 2 <= slots) C *= 2;
+  while (C < 8 && tiles * C * 2 <= room) C *= 2;
   if (int rc = launch_one(lora_shrink_kernel<T, RP>, tiles * C, sizeof(ShrinkShared<RP>), C, s, a, C)) return rc;
   const int64_t blocks = (a.O + 31) / 32 * a.ny, most = (blocks + kWarps - 1) / kWarps;
-  int64_t S = (4 * slots + tiles - 1) / tiles;
+  int64_t S = (8 * (int64_t)sm_count() + tiles - 1) / tiles;
   S = S < 1 ? 1 : S < most ? S : most;
-  if (a.out_dt == TP_F32)
-    return launch_one(lora_expand_kernel<T, RP, true>, tiles * S, sizeof(ExpandShared<T, RP, true>), 1, s, a, (int)S);
-  return launch_one(lora_expand_kernel<T, RP, false>, tiles * S, sizeof(ExpandShared<T, RP, false>), 1, s, a, (int)S);
+  const size_t smem = a.out_dt == TP_F32 ? sizeof(ExpandShared<T, RP, true>) : sizeof(ExpandShared<T, RP, false>);
+  if (a.out_dt == TP_F32) return launch_one(lora_expand_kernel<T, RP, float>, tiles * S, smem, 1, s, a, (int)S);
+  if (a.out_dt == TP_F16) return launch_one(lora_expand_kernel<T, RP, __half>, tiles * S, smem, 1, s, a, (int)S);
+  return launch_one(lora_expand_kernel<T, RP, __nv_bfloat16>, tiles * S, smem, 1, s, a, (int)S);
 }
 
 template <typename T>
