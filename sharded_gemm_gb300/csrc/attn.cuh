@@ -70,6 +70,7 @@ struct VerifyArgs : SampleArgs {
   int32_t *accepted, *rejected;  // (seqs), each nullable
   int64_t seqs, ldq;
   int q_dt;
+  int ordered;  // the upper words of tokens say which row a cluster takes
   int *status;
 };
 

@@ -242,7 +242,7 @@ int launch(const SampleArgs &a, cudaStream_t s) {
     // longer than a cluster holds: read again for every pass
     e = launch_pdl(sample_wide_kernel<T>, dim3((unsigned)a.B), dim3(kThreads), 0, s, a);
   } else {
-    return launch_rows<T, false>(a, s);
+    return launch_rows<T, false>(a, ctas_a_row<T, false>(a), s);
   }
   if (e != cudaSuccess) return cuda_error(e, "sample launch");
   note_launch();

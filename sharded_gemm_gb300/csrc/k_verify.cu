@@ -13,10 +13,72 @@
 // a second kernel, a warp a sequence, ends the sequence at its first marked row.  (One
 // cluster for the rows of a sequence, one after the other, would read no row in vain, but
 // take as many times the latency as tokens were accepted.)
+//
+// More rows than the GPU holds are put in order first: the first rows of all sequences,
+// then the second ones and so on, those whose filters take several passes before the
+// others.  A row whose sequence an earlier one has ended by then is left out.
 #include "sample_row.cuh"
 
 namespace tp {
 namespace {
+
+// The order of the rows (one block): by their place in their sequences up to kLevels, then
+// the others as they lie.
+constexpr int kLevels = 32;
+__global__ void __launch_bounds__(kThreads) verify_order_kernel(const __grid_constant__ VerifyArgs a) {
+  __shared__ uint64_t sums[32];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int64_t first = a.cu[0], end = a.cu[a.seqs];  // rows of no sequence are not touched
+  if (first < 0 || end > a.B) return;                 // recorded by the rows' kernel
+  for (int64_t i = first + tid; i < end; i += kThreads) row_words(a, i)[0] = kPending, row_words(a, i)[1] = -1;
+  __syncthreads();
+  auto put = [&](int64_t at, int64_t row) {  // sequences that claim each other's rows may be more than there are
+    if (first + at < end) row_words(a, first + at)[1] = (int32_t)row;
+  };
+  int64_t at = 0, r0 = 0, n = 0;
+  bool slow = false, known = false;
+  for (int level = 0; level <= kLevels; ++level) {
+    bool more = false;
+    for (int64_t base = 0; base < a.seqs; base += kThreads) {  // of 1024 sequences the slow ones first
+      const int64_t s = base + tid;
+      if (!known) {
+        n = 0;
+        if (s < a.seqs) {
+          r0 = a.cu[s];
+          const int64_t r1 = a.cu[s + 1];
+          if (r0 >= 0 && r0 <= r1 && r1 <= a.B) n = r1 - r0;
+          slow = slow_row(a, s);
+        }
+        known = a.seqs <= kThreads;
+      }
+      const uint64_t left = n > level ? n - level : 0, count = level < kLevels ? left > 0 : left;
+      // how many lower threads of its kind put, and of each kind all do
+      uint64_t run = slow ? count << 32 : count;
+      const uint64_t mine = run;
+#pragma unroll
+      for (int m = 1; m < 32; m *= 2) {
+        const uint64_t o = __shfl_up_sync(0xffffffffu, run, m);
+        if (lane >= m) run += o;
+      }
+      if (lane == 31) sums[warp] = run;
+      more = __syncthreads_or(left > 1) || more;
+      uint64_t lower = lane < warp ? sums[lane] : 0, all = sums[lane];
+#pragma unroll
+      for (int m = 16; m > 0; m /= 2) {
+        lower += __shfl_xor_sync(0xffffffffu, lower, m);
+        all += __shfl_xor_sync(0xffffffffu, all, m);
+      }
+      lower += run - mine;
+      const int64_t place = at + (slow ? lower >> 32 : (all >> 32) + (lower & 0xffffffffu));
+      for (uint64_t i = 0; i < count; ++i) put(place + i, r0 + level + i);
+      at += (int64_t)((all >> 32) + (all & 0xffffffffu));
+      __syncthreads();
+    }
+    if (!more) break;
+  }
+}
 
 __global__ void __launch_bounds__(256) verify_end_kernel(const __grid_constant__ VerifyArgs a) {
   griddep_wait();
@@ -30,14 +92,12 @@ __global__ void __launch_bounds__(256) verify_end_kernel(const __grid_constant__
   } else {
     bool ended = false;
     for (int64_t i0 = r0; i0 < r1; i0 += 32) {
-      const int64_t i = i0 + lane, token = i < r1 ? a.tokens[i] : 0;
-      const uint32_t marked = __ballot_sync(0xffffffffu, i < r1 && token < 0);
+      const int64_t i = i0 + lane;
+      const int32_t word = i < r1 ? row_words(a, i)[0] : 0;
+      const uint32_t marked = __ballot_sync(0xffffffffu, i < r1 && word < 0);
       const int end = ended ? -1 : marked ? __ffs(marked) - 1 : 32;
-      if (i < r1 && lane == end) a.tokens[i] = drawn_mark(token);
-      if (i < r1 && lane > end) {
-        a.tokens[i] = -1;
-        if (a.logprobs) a.logprobs[i] = 0.0f;
-      }
+      if (i < r1) a.tokens[i] = lane < end ? word : lane == end ? drawn_mark(word) : -1;
+      if (i < r1 && lane > end && a.logprobs) a.logprobs[i] = 0.0f;
       if (!ended && marked) accepted = i0 + end - r0, ended = true;
     }
   }
@@ -50,10 +110,19 @@ __global__ void __launch_bounds__(256) verify_end_kernel(const __grid_constant__
 static_assert(kMostVerified == kMostOnChip, "the argument check");
 
 template <typename T>
-int launch(const VerifyArgs &a, cudaStream_t s) {
-  if (a.B > 0)
-    if (int rc = launch_rows<T, true>(a, s)) return rc;
-  const cudaError_t e = launch_pdl(verify_end_kernel, dim3((unsigned)((a.seqs + 7) / 8)), dim3(256), 0, s, a);
+int launch(VerifyArgs a, cudaStream_t s) {
+  cudaError_t e;
+  if (a.B > 0) {
+    const int C = ctas_a_row<T, true>(a);
+    a.ordered = a.B * C > sm_count();
+    if (a.ordered) {
+      e = launch_pdl(verify_order_kernel, dim3(1), dim3(kThreads), 0, s, a);
+      if (e != cudaSuccess) return cuda_error(e, "verify launch");
+      note_launch();
+    }
+    if (int rc = launch_rows<T, true>(a, C, s)) return rc;
+  }
+  e = launch_pdl(verify_end_kernel, dim3((unsigned)((a.seqs + 7) / 8)), dim3(256), 0, s, a);
   if (e != cudaSuccess) return cuda_error(e, "verify launch");
   note_launch();
   return TP_OK;

@@ -835,54 +835,55 @@ __device__ __forceinline__ int64_t row_of(const SampleArgs &a, RowShared &sh, in
   return (int64_t)sh.answer;
 }
 
-// Which row of which sequence cluster `b` of a verification takes; false: none.  With
-// reorder, the sequences whose filters take several passes come first, as in row_of.
+// The token of row i while a verification runs, two 32-bit words: the lower the row's
+// result (an accepted draft, or a drawn token's mark below 0), the upper, where the rows
+// were put in order, the row that the cluster of its number takes, counted from the first
+// sequence's first row.
+constexpr int32_t kPending = -0x7fffffff - 1;
+__device__ __forceinline__ int32_t *row_words(const VerifyArgs &a, int64_t i) {
+  return reinterpret_cast<int32_t *>(a.tokens + i);
+}
+// A drawn token's mark: where the accepted drafts of a sequence end.  Its own inverse.
+__device__ __forceinline__ int32_t drawn_mark(int32_t token) { return -2 - token; }
+
+// Which row of which sequence the `b`-th cluster of a verification takes; false: none.
 // Offsets that do not ascend within the rows are recorded, and their sequence has no rows.
-__device__ __forceinline__ bool verify_place(const VerifyArgs &a, RowShared &sh, int64_t b, bool reorder, int64_t &row,
-                                             int64_t &seq, int64_t &last) {
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+// Where the rows were put in order, one behind a row of its sequence that has ended it is
+// none either: nothing of it would be used.
+__device__ __forceinline__ bool verify_place(const VerifyArgs &a, RowShared &sh, int64_t b, int rank, int C,
+                                             int64_t &row, int64_t &seq, int64_t &last) {
+  const int tid = threadIdx.x;
   if (tid == 0) sh.answer = ~0ull;
-  __syncthreads();
-  int64_t from = 0;  // rows of the sequences passed
-  for (int kind = 0; kind < (reorder ? 2 : 1); ++kind) {
-    for (int64_t base = 0; base < a.seqs; base += kThreads) {
-      const int64_t s = base + tid;
-      int64_t r0 = 0, n = 0;
-      if (s < a.seqs) {
-        const int64_t r1 = a.cu[s + 1];
-        r0 = a.cu[s];
-        if (r0 >= 0 && r0 <= r1 && r1 <= a.B) n = r1 - r0;
-        else record_bad_value(a.status);
-        if (reorder && slow_row(a, s) != (kind == 0)) n = 0;
-      }
-      if (!reorder) {  // the rows in their own order
-        if (b >= r0 && b < r0 + n) sh.answer = s, sh.before = b, sh.bin = r0 + n - 1;
-        continue;
-      }
-      u64 run = n;
-#pragma unroll
-      for (int m = 1; m < 32; m *= 2) {
-        const u64 o = __shfl_up_sync(0xffffffffu, run, m);
-        if (lane >= m) run += o;
-      }
-      if (lane == 31) sh.warp_a[0][warp] = run;
-      __syncthreads();
-      const u64 w = sh.warp_a[0][lane];
-      u64 lower = lane < warp ? w : 0, all = w;
-#pragma unroll
-      for (int m = 16; m > 0; m /= 2) {
-        lower += __shfl_xor_sync(0xffffffffu, lower, m);
-        all += __shfl_xor_sync(0xffffffffu, all, m);
-      }
-      const int64_t first = from + (int64_t)(lower + run) - n;
-      if (b >= first && b < first + n) sh.answer = s, sh.before = r0 + b - first, sh.bin = r0 + n - 1;
-      from += (int64_t)all;
-      __syncthreads();
-    }
+  row = b;
+  if (a.ordered) {
+    const int64_t r0 = a.cu[0], r1 = a.cu[a.seqs];
+    row = r0 >= 0 && r1 <= a.B && b < r1 - r0 ? row_words(a, r0 + b)[1] : -1;
   }
   __syncthreads();
-  const bool found = sh.answer != ~0ull;
-  seq = (int64_t)sh.answer, row = (int64_t)sh.before, last = (int64_t)sh.bin;
+  for (int64_t s = tid; s < a.seqs; s += kThreads) {
+    const int64_t r0 = a.cu[s], r1 = a.cu[s + 1];
+    if (r0 < 0 || r0 > r1 || r1 > a.B) record_bad_value(a.status);
+    else if (row >= r0 && row < r1) sh.answer = s, sh.before = r0, sh.bin = r1 - 1;
+  }
+  __syncthreads();
+  bool found = sh.answer != ~0ull;
+  seq = (int64_t)sh.answer, last = (int64_t)sh.bin;
+  if (a.ordered && found) {  // the same in all CTAs of the cluster, but for what they read next
+    bool ended = false;
+    if (rank == 0)
+      for (int64_t i = (int64_t)sh.before + tid; i < row; i += kThreads) {
+        const int32_t word = __ldcg(row_words(a, i));
+        ended = ended || (word < 0 && word != kPending);
+      }
+    ended = __syncthreads_or(ended);
+    if (C > 1) {
+      if (tid == 0) sh.got[0][0] = ended;
+      cluster_sync_all();
+      ended = ld_cluster_u64(mapa_shared(smem_u32(&sh.got[0][0]), 0)) != 0;
+      cluster_sync_all();  // read by all before it is used again
+    }
+    found = !ended;
+  }
   __syncthreads();  // read by all before they are used again
   return found;
 }
@@ -892,16 +893,26 @@ struct RowArgs { typedef SampleArgs type; };
 template <>
 struct RowArgs<true> { typedef VerifyArgs type; };
 
-// A drawn token as the verification's first kernel leaves it, below 0: where the accepted
-// drafts of a sequence end.  Its own inverse.
-__device__ __forceinline__ int64_t drawn_mark(int64_t token) { return -2 - token; }
-
-// What is read of the draft's probabilities: whole rows, or single values.
+// The draft's probabilities, taken into [0, 1] (NaN: 0): one, or four neighbours.
+__device__ __forceinline__ float as_prob(float v) { return fminf(fmaxf(v, 0.0f), 1.0f); }
 __device__ __forceinline__ float draft_prob(const void *q, int dt, int64_t i) {
-  const float v = dt == TP_F32 ? static_cast<const float *>(q)[i]
-                  : dt == TP_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(q)[i])
-                                  : __half2float(static_cast<const __half *>(q)[i]);
-  return fminf(fmaxf(v, 0.0f), 1.0f);  // NaN: 0
+  return as_prob(dt == TP_F32    ? static_cast<const float *>(q)[i]
+                 : dt == TP_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(q)[i])
+                                 : __half2float(static_cast<const __half *>(q)[i]));
+}
+__device__ __forceinline__ uint4 draft_words(const void *q, int dt, int64_t i) {
+  if (dt == TP_F32) return __ldcs(reinterpret_cast<const uint4 *>(static_cast<const float *>(q) + i));
+  const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(q) + i));
+  return make_uint4(v.x, v.y, 0, 0);
+}
+__device__ __forceinline__ float4 draft_probs(const uint4 &w, int dt) {
+  float4 v = make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w));
+  if (dt != TP_F32) {
+    const float2 a = dt == TP_BF16 ? Half2<__nv_bfloat16>::unpack(w.x) : Half2<__half>::unpack(w.x);
+    const float2 b = dt == TP_BF16 ? Half2<__nv_bfloat16>::unpack(w.y) : Half2<__half>::unpack(w.y);
+    v = make_float4(a.x, a.y, b.x, b.y);
+  }
+  return make_float4(as_prob(v.x), as_prob(v.y), as_prob(v.z), as_prob(v.w));
 }
 
 // A row's draw, or with VERIFY the test of its drafted token and, where that is refused
@@ -917,7 +928,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   int64_t b, at, last = 0;  // the row, and whose settings it has
   if constexpr (VERIFY) {
-    if (!verify_place(a, sh, blockIdx.x / C, reorder, b, at, last)) return;  // all CTAs of the cluster
+    if (!verify_place(a, sh, blockIdx.x / C, blockIdx.x % C, C, b, at, last)) return;  // all CTAs of the cluster
   } else {
     at = b = reorder ? row_of(a, sh, blockIdx.x / C) : blockIdx.x / C;
   }
@@ -992,7 +1003,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   row.top = top = x_of_key(row.reduce_max(order_key(top)));  // also: the slice is in shared memory
   if (top == -INFINITY) {  // nothing can be drawn
     if (rank == 0 && tid == 0) {
-      a.tokens[b] = VERIFY ? drawn_mark(-1) : -1;
+      if constexpr (VERIFY) row_words(a, b)[0] = drawn_mark(-1);
+      else a.tokens[b] = -1;
       if (a.logprobs) a.logprobs[b] = -INFINITY;
     }
     if (C > 1) cluster_sync_all();
@@ -1135,24 +1147,56 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (d >= 0) {
       const float share = __fdiv_rn(1.0f, __ull2float_rn(total) * 9.094947017729282e-13f);
       auto prob_of = [&](float v, uint32_t i) {
+        if (!cut.keeps(v, i)) return 0.0f;
         const float e = row.e_of(v);
-        return cut.keeps(v, i) && !(e < min_p) ? __fmul_rn(e, share) : 0.0f;
+        return e < min_p ? 0.0f : __fmul_rn(e, share);
       };
       if (__fmul_rn(u_d, q_d) < prob_of(x_d, (uint32_t)d)) {  // the same in every thread
         if (rank == 0 && tid == 0) {
-          a.tokens[b] = d;
+          row_words(a, b)[0] = (int32_t)d;
           if (a.logprobs) a.logprobs[b] = x_d - top - logz;
         }
         if (C > 1) cluster_sync_all();
         return;
       }
-      // what is left, in place of the logits
+      if (a.ordered && rank == 0 && tid == 0) __stcg(row_words(a, b), drawn_mark(0));  // later rows need not begin
+      // What is left, in place of the logits: four neighbours a thread, two of those at a
+      // time; what is not kept needs no exponential and nothing of the draft's.
       __syncthreads();
+      const int64_t q0 = b * a.ldq + (int64_t)rank * slice;
       const uint32_t first = (uint32_t)rank * slice;
-      for (int i = tid; i < slice; i += kThreads) {
-        const uint32_t index = first + i;
-        const float q = a.q ? (i < n ? draft_prob(a.q, a.q_dt, b * a.ldq + index) : 0.0f) : index == (uint32_t)d;
-        xs[i] = fmaxf(__fsub_rn(prob_of(xs[i], index), q), 0.0f);
+      const int es = a.q_dt == TP_F32 ? 4 : 2;
+      const int quads = a.q && ((uintptr_t)a.q + q0 * es) % (4 * es) ? 0 : n / 4;
+      auto left = [&](float v, uint32_t i, float q) { return fmaxf(__fsub_rn(prob_of(v, i), q), 0.0f); };
+      auto left4 = [&](int i, const float4 &v, const float4 &q) {
+        const uint32_t at = first + 4 * i;
+        reinterpret_cast<float4 *>(xs)[i] =
+            make_float4(left(v.x, at, q.x), left(v.y, at + 1, q.y), left(v.z, at + 2, q.z), left(v.w, at + 3, q.w));
+      };
+      auto any4 = [&](const float4 &v) { return v.x >= cut.x || v.y >= cut.x || v.z >= cut.x || v.w >= cut.x; };
+      auto one_hot = [&](int i) {
+        const uint32_t at = (uint32_t)d - (first + 4 * i);
+        return make_float4(at == 0, at == 1, at == 2, at == 3);
+      };
+      const float4 none = make_float4(0, 0, 0, 0);
+      for (int i = tid; i < quads; i += 2 * kThreads) {
+        const int i2 = i + kThreads;
+        const bool in2 = i2 < quads;
+        const float4 v = reinterpret_cast<const float4 *>(xs)[i], v2 = in2 ? reinterpret_cast<const float4 *>(xs)[i2] : none;
+        const bool any = any4(v), any2 = in2 && any4(v2);
+        uint4 w = make_uint4(0, 0, 0, 0), w2 = w;
+        if (any && a.q) w = draft_words(a.q, a.q_dt, q0 + 4 * i);
+        if (any2 && a.q) w2 = draft_words(a.q, a.q_dt, q0 + 4 * i2);
+        if (any) left4(i, v, a.q ? draft_probs(w, a.q_dt) : one_hot(i));
+        else reinterpret_cast<float4 *>(xs)[i] = none;
+        if (any2) left4(i2, v2, a.q ? draft_probs(w2, a.q_dt) : one_hot(i2));
+        else if (in2) reinterpret_cast<float4 *>(xs)[i2] = none;
+      }
+      for (int i = quads * 4 + tid; i < slice; i += kThreads) {
+        const float v = xs[i];
+        float q = 0.0f;
+        if (v >= cut.x && i < n) q = a.q ? draft_prob(a.q, a.q_dt, q0 + i) : first + i == (uint32_t)d;
+        xs[i] = v >= cut.x ? left(v, first + i, q) : 0.0f;
       }
       __syncthreads();
       WeightSum rest;
@@ -1195,7 +1239,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == __ffs(found) - 1) {
           const int64_t token = row.index0 + j;
           if constexpr (VERIFY) {
-            a.tokens[b] = drawn_mark(token);
+            row_words(a, b)[0] = drawn_mark((int32_t)token);
             if (a.logprobs) a.logprobs[b] = clean(static_cast<float>(x[token - (int64_t)rank * slice])) - top - logz;
           } else {
             a.tokens[b] = token;
@@ -1245,21 +1289,24 @@ int clusters_at_once(int C) {
   return n;
 }
 
-// The rows of `a` in one launch, a cluster each.
+// How many CTAs a row takes: as many as it needs.  More where the clusters run at once and
+// the longer joins pay (us, one row of 50272: drawn freely 14.4 on one CTA, 11.5 on 8; top-p
+// 33.7, 30.6; top-k 17.7, 19.8; of 8000: 8.3, 10.4; 22.6, 26.7; 13.1, 19.3; of 200000, on 4
+// and on 8: 17.7, 13.8; 50, 47; 23.5, 21.4.  16 rows of 50272 on 8, two turns: 22; 60; 39.
+// A verification's pass over the draft's row pays for them with top-k too.)
 template <typename T, bool VERIFY>
-int launch_rows(const typename RowArgs<VERIFY>::type &a, cudaStream_t s) {
-  // As many CTAs a row as it needs.  More where the clusters run at once and the longer
-  // joins pay (us, one row of 50272: drawn freely 14.4 on one CTA, 11.5 on 8; top-p 33.7,
-  // 30.6; top-k 17.7, 19.8; of 8000: 8.3, 10.4; 22.6, 26.7; 13.1, 19.3; of 200000, on 4
-  // and on 8: 17.7, 13.8; 50, 47; 23.5, 21.4.  16 rows of 50272 on 8, two turns: 22; 60; 39.)
+int ctas_a_row(const SampleArgs &a) {
   int C = 1;
   while ((int64_t)C * kMaxRun * kThreads < a.V) C *= 2;
-  if (C > 1 || (!a.top_k && a.V > (int64_t)kMaxRun / 2 * kThreads))
+  if (C > 1 || ((VERIFY || !a.top_k) && a.V > (int64_t)kMaxRun / 2 * kThreads))
     for (int more = 8; more >= 4; more /= 2)
-      if (more > C && a.B <= clusters_at_once<T, VERIFY>(more)) {
-        C = more;
-        break;
-      }
+      if (more > C && a.B <= clusters_at_once<T, VERIFY>(more)) return more;
+  return C;
+}
+
+// The rows of `a` in one launch, a cluster of C CTAs each.
+template <typename T, bool VERIFY>
+int launch_rows(const typename RowArgs<VERIFY>::type &a, int C, cudaStream_t s) {
   const int R = (int)((a.V + (int64_t)C * kThreads - 1) / ((int64_t)C * kThreads)) | 1;
   const size_t smem = sizeof(RowShared) + (size_t)R * kThreads * sizeof(float);
   if (a.B * C > 0x7fffffff) return set_error(TP_ERR_UNSUPPORTED, "too many rows for one launch");
@@ -1282,7 +1329,7 @@ int launch_rows(const typename RowArgs<VERIFY>::type &a, cudaStream_t s) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  const bool reorder = a.B * C > sm_count() && (a.top_k || a.top_p);
+  const bool reorder = !VERIFY && a.B * C > sm_count() && (a.top_k || a.top_p);
   e = cudaLaunchKernelEx(&cfg, kern, a, C, R, reorder);
   if (e != cudaSuccess) return cuda_error(e, "row launch");
   note_launch();

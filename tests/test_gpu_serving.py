@@ -547,11 +547,34 @@ def test_verify(B, lo, hi, V, dt, q_dt, filters):
     assert status() == 0
 
 
-def test_verify_more_rows_than_the_gpu_holds():
-    """Rows whose filters take several passes come first; the results keep their places."""
-    x, d, cu, u, q = drafted(90, 0, 4, 2000, F32, F32, 1)
-    s = settings_of(90, 3)
+@pytest.mark.parametrize("B,lo,hi", [(90, 0, 4), (200, 0, 1), (5, 60, 80), (1100, 0, 2), (1, 400, 400)])
+def test_verify_more_rows_than_the_gpu_holds(B, lo, hi):
+    """Rows are taken in another order, and those behind an ended one left out; the results keep their places."""
+    V = 2000 if B == 90 else 100
+    x, d, cu, u, q = drafted(B, lo, hi, V, F32, F32, B, noise=0.1 if hi > 50 else 0.7)
+    for s in ({}, settings_of(B, 3)):
+        ref = verify_ref(x, d, cu, u, q, **s)
+        for _ in range(3):
+            check_verify(tp.tp_verify(x, d, i32(cu), u, draft_probs=q, **s), ref)
+    assert status() == 0
+
+
+def test_verify_more_long_rows_than_the_gpu_holds():
+    x, d, cu, u, q = drafted(40, 1, 3, 60007, BF16, BF16, 7)
+    s = settings_of(40, 5)
     check_verify(tp.tp_verify(x, d, i32(cu), u, draft_probs=q, **s), verify_ref(x, d, cu, u, q, **s))
+
+
+def test_verify_many_rows_between_rows_of_none():
+    """Rows in front of the first sequence and behind the last are left alone, in any order of the others."""
+    x, d, _, u, q = drafted(100, 3, 3, 50, F32, F32, 2)
+    cu = np.arange(5, 391, 4).tolist()
+    keep = torch.full((len(d),), 77, dtype=torch.int64, device="cuda")
+    got = tp.tp_verify(x, d, i32(cu), u, draft_probs=q, tokens=keep)
+    ref = verify_ref(x, d, cu, u, q)
+    assert got[0][:5].tolist() == [77] * 5 and got[0][cu[-1]:].tolist() == [77] * (400 - cu[-1])
+    assert got[0][5:cu[-1]].tolist() == ref[0][5:cu[-1]].tolist()
+    assert got[2].tolist() == ref[2] and got[3].tolist() == ref[3]
 
 
 @pytest.mark.parametrize("C_rows", [1, 3])
@@ -626,6 +649,12 @@ def test_verify_bad_values_are_recorded():
         got = tp.tp_verify(x, d, i32(off), u, draft_probs=q)
         assert status() == tp.TP_ERR_INVALID_ARG
         assert got[2].min() >= 0
+    x, d, cu, u, q = drafted(100, 3, 3, 20, F32, F32, 2)
+    for at, v in ((0, -4), (100, 401), (40, 10), (40, 390), (1, -1)):
+        off = np.array(cu)
+        off[at] = v
+        tp.tp_verify(x, d, i32(off), u, draft_probs=q)
+        assert status() == tp.TP_ERR_INVALID_ARG, (at, v)
 
 
 @pytest.mark.parametrize("with_q", [True, False])
