@@ -4,18 +4,20 @@
 // tp_paged_plan.  Three running sums over the sequences (tokens, pages that ended ones
 // give back, pages needed) place everything: token i of sequence b in row cu[b] + i, the
 // i-th page given back on top of the pool, the i-th page needed taken from the top.  One
-// cluster does it in one launch: every CTA reads the sequences and takes the sums for
-// itself, a barrier lies between that and the first write (outputs may be the inputs
-// themselves), and the rows and pages are dealt to the threads of all CTAs, each of which
-// finds its sequence by bisection of the sums in shared memory.
+// CTA takes the sums; a barrier lies between its last read of what the outputs may be and
+// the first write.  Then pages given back, pages taken and rows are dealt to its threads,
+// each of which finds its sequence by bisection of the sums in shared memory and needs
+// nothing that another thread has just written.  The rows of a large step are a second
+// kernel's.
 //
 // tp_lora_plan.  A stable counting sort by adapter: tokens of each adapter counted in
 // shared memory, their running sum, and then one warp walks the sequences in order, 32 at
 // a time, and gives each the place behind the earlier ones of its adapter.  The tokens are
-// then dealt to all threads.  Every CTA of the cluster does the counting for itself.
+// then dealt to all threads.  Of a large step's several CTAs each does the counting for
+// itself.
 //
 // Both are bound by latency: two or three dependent loads, the sums' barriers, the
-// bisections.  A step of few tokens takes one CTA.
+// bisections.
 #include "ptx.cuh"
 #include "serve.cuh"
 
@@ -65,36 +67,46 @@ __device__ __forceinline__ int holder(const int32_t *sums, int n, int32_t at) {
   return lo;
 }
 
-__global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ PlanArgs a, int C) {
+// Rows that one CTA takes itself.  (Four turns of its threads, 3 us; a second launch costs 2.)
+constexpr int64_t kOwnRows = 4096;
+
+__global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ PlanArgs a) {
   extern __shared__ int32_t smem[];
   __shared__ int64_t buf[96];
-  const int B = (int)a.B, tid = threadIdx.x, rank = blockIdx.x;
+  const int B = (int)a.B, tid = threadIdx.x;
   int32_t *cu = smem, *need_at = cu + B, *back_at = need_at + B, *after = back_at + B, *held = after + B;
   griddep_launch_dependents();
   griddep_wait();
-  const int64_t F = a.free_count[0], page = 1ll << a.page_log2;
 
   // ---- a run of sequences a thread, and the sums before them
+  struct Sequence {
+    int64_t tokens, need, back, end, own, len;
+    bool ok;
+  };
+  const int64_t page = 1ll << a.page_log2;
+  auto sequence = [&](int b) {
+    const int64_t c = a.counts[b], less = a.rejected ? a.rejected[b] : 0;
+    Sequence s{0, 0, 0, 0, a.owned[b], a.seq_lens[b], false};
+    const bool held = s.own >= 0 && s.own <= a.width;
+    if (c < 0) {
+      s.ok = held;
+      if (held) s.back = s.own;
+      return s;
+    }
+    s.end = s.len - less + c, s.tokens = c;
+    const int64_t pages = (s.end + page - 1) >> a.page_log2;
+    s.need = pages > s.own ? pages - s.own : 0;
+    s.ok = held && s.len >= 0 && less >= 0 && less <= s.len && s.end <= a.cap && (s.own << a.page_log2) >= s.len - less;
+    return s;
+  };
+  const int64_t F = a.free_count[0];
   const int run = (B + kThreads - 1) / kThreads, b0 = tid * run, b1 = min(b0 + run, B);
   bool bad = F < 0 || F > a.pages;
   int64_t sums[3] = {0, 0, 0}, total[3];
-  auto sequence = [&](int b, int64_t &tokens, int64_t &need, int64_t &back, int64_t &end, int64_t &own) {
-    const int64_t c = a.counts[b], len = a.seq_lens[b], less = a.rejected ? a.rejected[b] : 0;
-    own = a.owned[b];
-    tokens = need = back = end = 0;
-    if (own < 0 || own > a.width) return false;
-    if (c < 0) {
-      back = own;
-      return true;
-    }
-    end = len - less + c, tokens = c;
-    const int64_t pages = (end + page - 1) >> a.page_log2;
-    need = pages > own ? pages - own : 0;
-    return len >= 0 && less >= 0 && less <= len && end <= a.cap && (own << a.page_log2) >= len - less;
-  };
+  Sequence only{0, 0, 0, 0, 0, 0, true};  // of a run of one
   for (int b = b0; b < b1; ++b) {
-    int64_t tokens, need, back, end, own;
-    if (sequence(b, tokens, need, back, end, own)) sums[0] += tokens, sums[1] += need, sums[2] += back;
+    only = sequence(b);
+    if (only.ok) sums[0] += only.tokens, sums[1] += only.need, sums[2] += only.back;
     else bad = true;
   }
   scan_before<3>(sums, total, buf);
@@ -102,55 +114,86 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ 
   bad = __syncthreads_or(bad) || top > a.pages || total[0] > a.T;
   const bool fits = !bad && total[1] <= top;
   for (int b = b0; b < b1; ++b) {
-    int64_t tokens, need, back, end, own;
-    sequence(b, tokens, need, back, end, own);
-    if (!fits) end = a.seq_lens[b];  // an empty step
+    if (run > 1) only = sequence(b);
     cu[b] = fits ? (int32_t)sums[0] : 0, need_at[b] = (int32_t)sums[1], back_at[b] = (int32_t)sums[2];
-    after[b] = (int32_t)end, held[b] = a.owned[b];
-    sums[0] += tokens, sums[1] += need, sums[2] += back;
+    after[b] = (int32_t)(fits ? only.end : only.len), held[b] = (int32_t)only.own;  // or an empty step
+    sums[0] += only.tokens, sums[1] += only.need, sums[2] += only.back;
   }
+  __syncthreads();  // all is read that is written below, and the sums are in shared memory
+
   const int total_tokens = fits ? (int)total[0] : 0, total_need = fits ? (int)total[1] : 0;
   const int total_back = fits ? (int)total[2] : 0;
-  // every CTA has read what is overwritten below, and the sums are in shared memory
-  if (C > 1) cluster_sync_all(); else __syncthreads();
-
-  const int thread = rank * kThreads + tid, threads = C * kThreads;
-  for (int b = thread; b < B; b += threads) {
-    const int own = held[b], all = b + 1 < B ? need_at[b + 1] : (int)total[1];
+  for (int b = tid; b < B; b += kThreads) {
+    const int all = b + 1 < B ? need_at[b + 1] : (int)total[1];
     const bool ends = fits && (b + 1 < B ? back_at[b + 1] : total_back) > back_at[b];
     a.cu[b] = cu[b];
     a.new_lens[b] = after[b];
     // (a sequence that ended with no pages has none to need either)
-    a.new_owned[b] = !fits ? own : ends ? 0 : own + (all - need_at[b]);
+    a.new_owned[b] = !fits ? held[b] : ends ? 0 : held[b] + (all - need_at[b]);
   }
-  if (thread == 0) {
+  if (tid == 0) {
     a.cu[B] = total_tokens;
     a.new_free_count[0] = fits ? (int32_t)(top - total[1]) : (int32_t)F;
     a.missing[0] = bad ? -1 : fits ? 0 : (int32_t)(total[1] - top);
     if (bad) record_bad_value(a.status);
   }
-  // ---- pages given back go on top of the pool
-  for (int i = thread; i < total_back; i += threads) {
-    const int b = holder(back_at, B, i);
-    a.free_pages[F + i] = a.table[b * a.ld_table + (i - back_at[b])];
+  // ---- pages given back go on top of the pool, and what is needed is taken from there
+  // The sequence of the i-th of `sums`' pages, asked for i after i: found anew behind its end.
+  struct Walk {
+    int b = 0, end = 0;
+    __device__ __forceinline__ int at(const int32_t *sums, int n, int all, int i) {
+      if (i >= end) {
+        b = holder(sums, n, i);
+        end = b + 1 < n ? sums[b + 1] : all;
+      }
+      return b;
+    }
+  };
+  auto given = [&](int i, int b) { return a.table[b * a.ld_table + (i - back_at[b])]; };
+  auto taken = [&](int i) {
+    const int64_t at = top - 1 - i;
+    return at < F ? a.free_pages[at] : given((int)(at - F), holder(back_at, B, (int)(at - F)));
+  };
+  // 256 pages a warp at a time, the last warp first (the first have the tokens): a lane's
+  // eight are mostly of one sequence, which takes one bisection, and under one latency.
+  // (13000 pages given back one by one: 15 us, all of it bisections.)
+  const int warp = kThreads / 32 - 1 - tid / 32, lane = tid % 32;
+  for (int i0 = warp * 256 + lane; i0 < total_back; i0 += 8 * kThreads) {
+    Walk w;
+    int32_t v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int i = i0 + u * 32;
+      if (i < total_back) v[u] = given(i, w.at(back_at, B, total_back, i));
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (i0 + u * 32 < total_back) a.free_pages[F + i0 + u * 32] = v[u];
   }
-  if (total_back > 0 && total_need > 0) {  // the same in all CTAs
-    __threadfence();
-    if (C > 1) cluster_sync_all(); else __syncthreads();
+  for (int i0 = warp * 128 + lane; i0 < total_need; i0 += 4 * kThreads) {
+    Walk w;
+    int32_t v[4];
+    int64_t to[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = i0 + u * 32;
+      if (i >= total_need) continue;
+      const int b = w.at(need_at, B, total_need, i);
+      to[u] = b * a.ld_table + held[b] + (i - need_at[b]);
+      v[u] = taken(i);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (i0 + u * 32 < total_need) a.table[to[u]] = v[u];
   }
-  // ---- and what is needed is taken from there
-  auto taken = [&](int i) { return __ldcg(a.free_pages + (top - 1 - i)); };
-  for (int i = thread; i < total_need; i += threads) {
-    const int b = holder(need_at, B, i);
-    a.table[b * a.ld_table + held[b] + (i - need_at[b])] = taken(i);
-  }
-  // ---- the tokens: pages taken just now are read from the pool
-  for (int64_t t = thread; t < a.T; t += threads) {
+  // ---- the tokens
+  if (a.T > kOwnRows) return;
+  for (int t = tid; t < a.T; t += kThreads) {
     int32_t position = 0;
     int64_t slot = -1;
     if (t < total_tokens) {
-      const int b = holder(cu, B, (int)t), end = b + 1 < B ? cu[b + 1] : total_tokens;
-      position = after[b] - (end - (int)t);
+      const int b = holder(cu, B, t), end = b + 1 < B ? cu[b + 1] : total_tokens;
+      position = after[b] - (end - t);
       const int j = position >> a.page_log2;
       const int32_t p = j < held[b] ? a.table[b * a.ld_table + j] : taken(need_at[b] + j - held[b]);
       if (p >= 0 && p < a.pages) slot = ((int64_t)p << a.page_log2) + (position & (int)(page - 1));
@@ -161,7 +204,30 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ 
   }
 }
 
-__global__ void __launch_bounds__(kThreads) group_kernel(const __grid_constant__ GroupArgs a, int C) {
+// The rows of a large step, from what plan_kernel wrote.
+__global__ void __launch_bounds__(512) plan_rows_kernel(const __grid_constant__ PlanArgs a) {
+  extern __shared__ int32_t cu[];
+  const int B = (int)a.B, tid = threadIdx.x;
+  griddep_wait();
+  for (int b = tid; b <= B; b += 512) cu[b] = a.cu[b];
+  __syncthreads();
+  const int total = cu[B];
+  for (int64_t t = blockIdx.x * 512ll + tid; t < a.T; t += gridDim.x * 512ll) {
+    int32_t position = 0;
+    int64_t slot = -1;
+    if (t < total) {
+      const int b = holder(cu, B, (int)t);
+      position = a.new_lens[b] - (cu[b + 1] - (int)t);
+      const int32_t p = a.table[b * a.ld_table + (position >> a.page_log2)];
+      if (p >= 0 && p < a.pages) slot = ((int64_t)p << a.page_log2) + (position & ((1 << a.page_log2) - 1));
+      else record_bad_value(a.status);
+    }
+    a.positions[t] = position;
+    a.slots[t] = slot;
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) group_kernel(const __grid_constant__ GroupArgs a) {
   extern __shared__ int32_t smem[];
   __shared__ int64_t buf[64];
   const int B = (int)a.B, n = (int)a.n, tid = threadIdx.x, lane = tid % 32;
@@ -212,13 +278,14 @@ __global__ void __launch_bounds__(kThreads) group_kernel(const __grid_constant__
     for (int base = 0; base < B; base += 32) {
       const int b = base + lane, len = b < B ? cu[b + 1] - cu[b] : 0, id = b < B ? adapter(b) : n + 1 + lane;
       const uint32_t peers = __match_any_sync(0xffffffffu, id);
+      const int most = __reduce_max_sync(0xffffffffu, __popc(peers));
       int before = 0, mine = 0;
-      for (int i = 0; i < 32; ++i) {
-        const int l = __shfl_sync(0xffffffffu, len, i);
-        if (peers >> i & 1) {
-          mine += l;
-          if (i < lane) before += l;
-        }
+      uint32_t rest = peers;
+      for (int i = 0; i < most; ++i) {  // each lane its own peers, one after the other
+        const int from = rest ? __ffs(rest) - 1 : lane;
+        const int l = __shfl_sync(0xffffffffu, len, from);
+        if (rest) mine += l, before += from < lane ? l : 0;
+        rest &= rest - 1;
       }
       const int at = id <= n ? tokens[id] : 0;
       if (b < B) first[b] = at + before;
@@ -229,7 +296,7 @@ __global__ void __launch_bounds__(kThreads) group_kernel(const __grid_constant__
   }
   __syncthreads();
   int32_t *order = a.plan + 4 + 4 * a.most;
-  for (int64_t t = blockIdx.x * kThreads + tid; t < a.T; t += C * kThreads) {
+  for (int64_t t = blockIdx.x * kThreads + tid; t < a.T; t += (int64_t)gridDim.x * kThreads) {
     if (t < all) {
       const int b = holder(cu, B, (int)t);
       order[first[b] + (int)t - cu[b]] = (int)t;
@@ -239,45 +306,33 @@ __global__ void __launch_bounds__(kThreads) group_kernel(const __grid_constant__
   }
 }
 
-// One cluster: a CTA for few rows, else eight.  (A cluster's launch and barriers cost about
-// 2 us more than one CTA's; 4096 rows are four turns of a CTA's threads.)
-template <typename Args>
-int launch_cluster(void (*kern)(Args, int), const Args &a, int64_t rows, size_t smem, cudaStream_t s,
-                   const char *what) {
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
-  if (e != cudaSuccess) return cuda_error(e, what);
-  const int C = rows > 4096 ? 8 : 1;
-  cudaLaunchConfig_t cfg;
-  memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = dim3(C);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = C;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, kern, a, C);
-  if (e != cudaSuccess) return cuda_error(e, what);
+constexpr size_t kMostPlanSmem = 5 * 4 * (size_t)kMostSequences;
+constexpr size_t kMostGroupSmem = 4 * (size_t)(2 * kMostSequences + 1 + kMostAdapters + 1);
+static_assert(kMostPlanSmem <= 224 * 1024 && kMostGroupSmem <= 224 * 1024, "the sums and counts of a CTA");
+
+template <typename K, typename Args>
+int launch_one(K kern, const Args &a, int64_t grid, int block, size_t smem, size_t most, cudaStream_t s) {
+  // the limit belongs to the function, not to this call: always the largest
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+  if (e == cudaSuccess) e = launch_pdl(kern, dim3((unsigned)grid), dim3(block), smem, s, a);
+  if (e != cudaSuccess) return cuda_error(e, "plan launch");
   note_launch();
   return TP_OK;
 }
 
-static_assert(5 * 4 * kMostSequences <= 200 * 1024, "plan_kernel's sums");
-static_assert(4 * (2 * kMostSequences + 1 + kMostAdapters + 1) <= 200 * 1024, "group_kernel's counts");
-
 }  // namespace
 
 int launch_plan(const PlanArgs &a, cudaStream_t s) {
-  return launch_cluster(plan_kernel, a, a.T, 5 * 4 * (size_t)a.B, s, "plan launch");
+  if (int rc = launch_one(plan_kernel, a, 1, kThreads, 5 * 4 * (size_t)a.B, kMostPlanSmem, s)) return rc;
+  if (a.T <= kOwnRows) return TP_OK;
+  const int64_t all = (a.T + 511) / 512, most = 4 * (int64_t)sm_count();
+  return launch_one(plan_rows_kernel, a, all < most ? all : most, 512, 4 * (size_t)(a.B + 1), 4 * (kMostSequences + 1), s);
 }
 
 int launch_groups(const GroupArgs &a, cudaStream_t s) {
-  return launch_cluster(group_kernel, a, a.T, 4 * (size_t)(2 * a.B + 1 + a.n + 1), s, "adapter plan launch");
+  const int64_t all = a.T <= kOwnRows ? 1 : (a.T + kThreads - 1) / kThreads, most = sm_count();
+  return launch_one(group_kernel, a, all < most ? all : most, kThreads, 4 * (size_t)(2 * a.B + 1 + a.n + 1),
+                    kMostGroupSmem, s);
 }
 
 }  // namespace tp

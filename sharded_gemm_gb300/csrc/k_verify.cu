@@ -114,7 +114,7 @@ int launch(VerifyArgs a, cudaStream_t s) {
   cudaError_t e;
   if (a.B > 0) {
     const int C = ctas_a_row<T, true>(a);
-    a.ordered = a.B * C > sm_count();
+    a.ordered = a.B * C > 3 * sm_count() / 2;
     if (a.ordered) {
       e = launch_pdl(verify_order_kernel, dim3(1), dim3(kThreads), 0, s, a);
       if (e != cudaSuccess) return cuda_error(e, "verify launch");
