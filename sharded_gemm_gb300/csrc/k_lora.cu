@@ -10,9 +10,7 @@
 // are B's 32 rows against h, added to y.  Nothing of h goes through memory.
 //
 // Bound by bytes (each adapter is read once) and, of one token, by latency: 2 R operations
-// an element are few, so warp-level products do.  h meets B as a sum of two 16-bit numbers,
-// three of bfloat16 where the outputs are float32: 2^-16 of h is lost in outputs that are
-// rounded to 16 bits, else 2^-22.
+// an element are few, so warp-level products do.
 #include "lora.cuh"
 
 namespace tp {
@@ -125,7 +123,7 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : RP == 64 ? 2 : 3
   const int blk0 = (cluster % S * C + rank) * kWarps + warp;
   const int u0 = (int)((int64_t)units * (rank * kWarps + warp) / (C * kWarps));
   const int u1 = (int)((int64_t)units * (rank * kWarps + warp + 1) / (C * kWarps));
-  const bool three = kTerms > 2 && a.out_dt == TP_F32;
+  const int used = terms<T>(a.out_dt);
   griddep_launch_dependents();
   griddep_wait();
   const int groups = groups_of(a);
@@ -133,7 +131,7 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : RP == 64 ? 2 : 3
   int64_t before = 0;
   int4 tile;
   bool read = false;  // the others' sums: they may not change theirs before all have
-  for (int64_t at = cluster / S; find_tile(a, groups, 16, at, base, before, tile); at += gridDim.x / C / S) {
+  for (int64_t at = cluster / S; find_tile(a, groups, 16, !a.in_place, at, base, before, tile); at += gridDim.x / C / S) {
     const int id = tile.x;
     __syncthreads();  // the last tile's tokens and fragments are read
     read_tokens(a, tile, 16, sh.token);
@@ -258,7 +256,7 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : RP == 64 ? 2 : 3
         for (int s = 0; s < KS; ++s)
 #pragma unroll
           for (int i = 0; i < kTerms; ++i) {
-            if (i == 2 && !three) break;
+            if (i >= used) break;
             const uint4 f = sh.frag[i][0][s][lane];
             const uint32_t hf[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll

@@ -9,8 +9,6 @@
 // no barrier between the copy and its use.  (As one kernel, h exchanged within a cluster, the
 // barriers between the products stood in the way of the streams, and registers for both were
 // too many: 309 us for 8192 tokens, R = 64, 4096 x 11008, where 66 us of bytes move.)
-#include <type_traits>
-
 #include "lora.cuh"
 
 namespace tp {
@@ -18,42 +16,70 @@ namespace {
 
 constexpr int kTile = 64;
 
+// The tiles of a plan (in all lanes).
+__device__ __forceinline__ int count_tiles(const LoraArgs &a, int groups, bool none) {
+  int n = 0;
+#pragma unroll 4
+  for (int base = 0; base < groups; base += 32)
+    n += (int)__reduce_add_sync(0xffffffffu, tiles_of(a, group_at(a, base + threadIdx.x % 32, groups), kTile, none));
+  return n;
+}
+
+// Into how many shares of `units` to split each tile's work (1..most, at most 32) for a grid
+// of CTAs: the least turns times what a share takes, `start` units' time and its own.
+__device__ __forceinline__ int shares_of(int tiles, int grid, int units, int start, int most) {
+  const int s = threadIdx.x % 32 + 1;
+  const unsigned turns = (unsigned)((int64_t)tiles * s + grid - 1) / grid;
+  const unsigned cost = s <= most ? min(turns * (unsigned)(start + (units + s - 1) / s), 0x3ffffffu) : 0x3ffffffu;
+  return (int)(__reduce_min_sync(0xffffffffu, cost << 5 | (unsigned)(s - 1)) & 31) + 1;
+}
+// The first pass's shares of the contraction, the same in both: kG warps take a unit each.
+template <int RP>
+__device__ __forceinline__ int splits_of(const LoraArgs &a, int tiles, int grid);
+
 // ---------------------------------------------------------------- the first pass
 // Eight warps: kM groups of MW blocks of 16 tokens, kG stretches of the contraction.  A ring
-// holds units of 32 elements of the contraction: the tokens' rows, then the adapter's.
+// holds units of 32 elements of the contraction: the tokens' rows, then the adapter's.  A
+// tile's contraction may be split over several CTAs, whose sums lie side by side in the
+// workspace until the second pass adds them, in their order.
 template <int RP>
 struct ShrinkShared {
-  static constexpr int MW = RP == 128 ? 1 : 2, kM = 4 / MW, kG = kWarps / kM, kStride = RP + 4;
-  static constexpr int kAhead = RP == 16 ? 4 : 3, kRows = 2 * MW + RP / 8;  // pieces of 512 bytes a unit
-  static constexpr int kCtas = RP <= 32 ? 2 : 1;                            // of an SM
+  static constexpr int MW = RP == 128 ? 2 : RP == 64 ? 4 : 2, kM = 4 / MW, kG = kWarps / kM, kStride = RP + 4;
+  static constexpr int kAhead = RP == 128 ? 2 : RP == 16 ? 4 : 3, kRows = 2 * MW + RP / 8;  // pieces of 512 bytes a unit
+  static constexpr int kCtas = RP <= 32 ? 2 : 1;                                            // of an SM
   union {
     uint4 ring[kWarps][kAhead][kRows][32];
-    float part[kG][kTile][kStride];  // [0] in the end: this CTA's sums, read by the others
+    float part[kG][kTile][kStride];
   };
   int token[kTile];
 };
+template <int RP>
+__device__ __forceinline__ int splits_of(const LoraArgs &a, int tiles, int sms) {
+  typedef ShrinkShared<RP> Shared;
+  const int units = (int)((a.K + 31) / 32) * a.nx;
+  return shares_of(tiles, Shared::kCtas * sms, (units + Shared::kG - 1) / Shared::kG, 6, a.splits);
+}
 
 template <typename T, int RP>
 __global__ void __launch_bounds__(kLoraThreads, ShrinkShared<RP>::kCtas)
-    lora_shrink_kernel(const __grid_constant__ LoraArgs a, int C) {
+    lora_shrink_kernel(const __grid_constant__ LoraArgs a, int sms) {
   typedef ShrinkShared<RP> Shared;
   constexpr int NT = RP / 8, MW = Shared::MW, kG = Shared::kG, kAhead = Shared::kAhead, kStride = Shared::kStride;
   extern __shared__ __align__(16) uint8_t smem[];
   Shared &sh = *reinterpret_cast<Shared *>(smem);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, q = lane % 4;
-  const int rank = blockIdx.x % C, K = (int)a.K, per = (K + 31) / 32, units = per * a.nx;
-  const int m0 = warp % Shared::kM * MW, slot = rank * kG + warp / Shared::kM;
-  const int u0 = (int)((int64_t)units * slot / (C * kG)), u1 = (int)((int64_t)units * (slot + 1) / (C * kG));
+  const int K = (int)a.K, per = (K + 31) / 32, units = per * a.nx, m0 = warp % Shared::kM * MW;
   griddep_launch_dependents();
   griddep_wait();
-  const int groups = groups_of(a);
+  const int groups = groups_of(a), tiles = count_tiles(a, groups, false), S = splits_of<RP>(a, tiles, sms);
   int base = 0;
   int64_t before = 0;
   int4 tile;
-  for (int64_t at = blockIdx.x / C; find_tile(a, groups, kTile, at, base, before, tile); at += gridDim.x / C) {
-    const int id = tile.x;
-    if (id < 0) continue;  // they need no h
-    if (C > 1) cluster_sync_all(); else __syncthreads();  // the last tile's sums are read
+  for (int64_t item = blockIdx.x; item < (int64_t)tiles * S; item += gridDim.x) {
+    if (!find_tile(a, groups, kTile, false, item / S, base, before, tile)) break;
+    const int id = tile.x, split = (int)(item % S), slot = split * kG + warp / Shared::kM;
+    const int u0 = (int)((int64_t)units * slot / (S * kG)), u1 = (int)((int64_t)units * (slot + 1) / (S * kG));
+    __syncthreads();  // the last item's sums are read
     read_tokens(a, tile, kTile, sh.token);
     __syncthreads();
     int64_t row[2 * MW];  // where the lane's rows of x begin; without a token, -1
@@ -129,45 +155,26 @@ __global__ void __launch_bounds__(kLoraThreads, ShrinkShared<RP>::kCtas)
         *reinterpret_cast<float2 *>(to + 8 * kStride) = make_float2(acc[m][j][2], acc[m][j][3]);
       }
     __syncthreads();
-    // ---- the parts added over the warps, then over the CTAs, a share of the rows each
-    constexpr int kQuads = kTile * RP / 4;
-    if (C > 1) {
-      for (int i = tid; i < kQuads; i += kLoraThreads) {
-        const int r = i / (RP / 4), col = i % (RP / 4) * 4;
-        float4 sum = *reinterpret_cast<const float4 *>(&sh.part[0][r][col]);
-#pragma unroll
-        for (int j = 1; j < kG; ++j) sum = add4(sum, *reinterpret_cast<const float4 *>(&sh.part[j][r][col]));
-        *reinterpret_cast<float4 *>(&sh.part[0][r][col]) = sum;
-      }
-      cluster_sync_all();
-    }
-    const float scale = a.scales ? __ldg(a.scales + id) : 1.0f;
-    for (int i = kQuads / C * rank + tid; i < kQuads / C * (rank + 1); i += kLoraThreads) {
+    float *const to = a.workspace + ((int64_t)split * a.T + tile.y) * RP;
+    for (int i = tid; i < tile.z * (RP / 4); i += kLoraThreads) {
       const int r = i / (RP / 4), col = i % (RP / 4) * 4;
-      float4 sum = make_float4(0, 0, 0, 0);
-      if (C > 1) {
-        const uint32_t mine = smem_u32(&sh.part[0][r][col]);
-        for (int o = 0; o < C; ++o) sum = add4(sum, ld_cluster_f4(mapa_shared(mine, o)));
-      } else {
+      float4 sum = *reinterpret_cast<const float4 *>(&sh.part[0][r][col]);
 #pragma unroll
-        for (int j = 0; j < kG; ++j) sum = add4(sum, *reinterpret_cast<const float4 *>(&sh.part[j][r][col]));
-      }
-      if (r < tile.z)
-        *reinterpret_cast<float4 *>(a.workspace + (int64_t)(tile.y + r) * RP + col) =
-            make_float4(sum.x * scale, sum.y * scale, sum.z * scale, sum.w * scale);
+      for (int j = 1; j < kG; ++j) sum = add4(sum, *reinterpret_cast<const float4 *>(&sh.part[j][r][col]));
+      *reinterpret_cast<float4 *>(to + (int64_t)r * RP + col) = sum;
     }
   }
-  if (C > 1) cluster_sync_all();  // no CTA leaves while another may still read its shared memory
 }
 
 // ---------------------------------------------------------------- the second pass
 // A warp takes 32 columns of a tile at a time, its lane the rows g and g + 8 of each of the
 // four blocks of 16 tokens, 8 columns of each.  A block's old values are fetched while the
 // one before it is worked on, into the place that was just read.
-template <typename T, int RP, bool OUT32>
+template <typename T, int RP, typename O>
 struct ExpandShared {
-  static constexpr int kTerms = Half2<T>::kBf16 && OUT32 ? 3 : 2, kStride = RP + 4;
-  static constexpr int kWords = OUT32 ? 2 : 1;
+  static constexpr bool OUT32 = sizeof(O) == 4;
+  static constexpr int kTerms = terms<T>(OUT32 ? TP_F32 : std::is_same<O, __half>::value ? TP_F16 : TP_BF16);
+  static constexpr int kStride = RP + 4, kWords = OUT32 ? 2 : 1;
   union {
     uint4 ring[kWarps][4][2 * kWords][32];
     float h[kTile][kStride];
@@ -200,9 +207,9 @@ __device__ __forceinline__ void unpack8(const uint4 &v, float *d) {
 // O: the outputs' type.
 template <typename T, int RP, typename O>
 __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
-    lora_expand_kernel(const __grid_constant__ LoraArgs a, int S) {
-  constexpr bool OUT32 = sizeof(O) == 4;
-  typedef ExpandShared<T, RP, OUT32> Shared;
+    lora_expand_kernel(const __grid_constant__ LoraArgs a, int sms) {
+  typedef ExpandShared<T, RP, O> Shared;
+  constexpr bool OUT32 = Shared::OUT32;
   constexpr int KS = RP / 16, kTerms = Shared::kTerms, kStride = Shared::kStride, kWords = Shared::kWords;
   // 16-bit outputs: the products are added to the old values, whose sums lose less than the
   // rounding does; float32 ones keep the old values out of the products' sums
@@ -210,17 +217,19 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
   extern __shared__ __align__(16) uint8_t smem[];
   Shared &sh = *reinterpret_cast<Shared *>(smem);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, q = lane % 4;
-  const int cols = (int)a.O, per = (cols + 31) / 32, blocks = per * a.ny, step = S * kWarps;
-  const int blk0 = blockIdx.x % S * kWarps + warp;
+  const int cols = (int)a.O, per = (cols + 31) / 32, blocks = per * a.ny;
   uint4 *const ring = &sh.ring[warp][0][0][lane];
   griddep_launch_dependents();
   griddep_wait();
-  const int groups = groups_of(a);
+  const int groups = groups_of(a), with = count_tiles(a, groups, false), splits = splits_of<RP>(a, with, sms);
+  const int tiles = a.in_place ? with : count_tiles(a, groups, true);
+  const int S = shares_of(tiles, gridDim.x, (blocks + kWarps - 1) / kWarps, 3, 32), step = S * kWarps;
   int base = 0;
   int64_t before = 0;
   int4 tile;
-  for (int64_t at = blockIdx.x / S; find_tile(a, groups, kTile, at, base, before, tile); at += gridDim.x / S) {
-    const int id = tile.x;
+  for (int64_t item = blockIdx.x; item < (int64_t)tiles * S; item += gridDim.x) {
+    if (!find_tile(a, groups, kTile, !a.in_place, item / S, base, before, tile)) break;
+    const int id = tile.x, blk0 = (int)(item % S) * kWarps + warp;
     __syncthreads();
     read_tokens(a, tile, kTile, sh.token);
     if (tid < kTile) {  // read_tokens' own thread
@@ -229,11 +238,14 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
       sh.out_row[tid] = t < 0 ? -1 : t * a.ldo * (int64_t)sizeof(O);
     }
     if (id >= 0) {
+      const float scale = a.scales ? __ldg(a.scales + id) : 1.0f;
       for (int i = tid; i < kTile * RP / 4; i += kLoraThreads) {
         const int r = i / (RP / 4), c = i % (RP / 4) * 4;
         float4 v = make_float4(0, 0, 0, 0);
-        if (r < tile.z) v = __ldcg(reinterpret_cast<const float4 *>(a.workspace + (int64_t)(tile.y + r) * RP + c));
-        *reinterpret_cast<float4 *>(&sh.h[r][c]) = v;
+        if (r < tile.z)
+          for (int k = 0; k < splits; ++k)
+            v = add4(v, __ldcg(reinterpret_cast<const float4 *>(a.workspace + ((int64_t)k * a.T + tile.y + r) * RP + c)));
+        *reinterpret_cast<float4 *>(&sh.h[r][c]) = make_float4(v.x * scale, v.y * scale, v.z * scale, v.w * scale);
       }
       __syncthreads();
       if (!Half2<T>::kBf16) {
@@ -359,45 +371,26 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
   }
 }
 
-template <typename K, typename... Args>
-int launch_one(K kern, int64_t grid, size_t smem, int C, cudaStream_t s, const Args &...args) {
+template <typename K>
+int launch_one(K kern, int ctas, size_t smem, const LoraArgs &a, cudaStream_t s) {
+  const int sms = sm_count();
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return cuda_error(e, "adapter launch");
-  cudaLaunchConfig_t cfg;
-  memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(kLoraThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = C;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = C > 1 ? 2 : 1;
-  e = cudaLaunchKernelEx(&cfg, kern, args...);
+  if (e == cudaSuccess) e = launch_pdl(kern, dim3((unsigned)(ctas * sms)), dim3(kLoraThreads), smem, s, a, sms);
   if (e != cudaSuccess) return cuda_error(e, "adapter launch");
   note_launch();
   return TP_OK;
 }
 
+template <typename T, int RP, typename O>
+int launch_expand(const LoraArgs &a, cudaStream_t s) {
+  return launch_one(lora_expand_kernel<T, RP, O>, RP == 128 ? 1 : 2, sizeof(ExpandShared<T, RP, O>), a, s);
+}
+
 template <typename T, int RP>
 int launch(const LoraArgs &a, cudaStream_t s) {
-  int64_t tiles = a.T / kTile + a.most;  // at most
-  if (tiles > (1 << 20)) tiles = 1 << 20;
-  const int64_t room = (int64_t)ShrinkShared<RP>::kCtas * sm_count();
-  int C = 1;
-  while (C < 8 && tiles * C * 2 <= room) C *= 2;
-  if (int rc = launch_one(lora_shrink_kernel<T, RP>, tiles * C, sizeof(ShrinkShared<RP>), C, s, a, C)) return rc;
-  const int64_t blocks = (a.O + 31) / 32 * a.ny, most = (blocks + kWarps - 1) / kWarps;
-  int64_t S = (8 * (int64_t)sm_count() + tiles - 1) / tiles;
-  S = S < 1 ? 1 : S < most ? S : most;
-  const size_t smem = a.out_dt == TP_F32 ? sizeof(ExpandShared<T, RP, true>) : sizeof(ExpandShared<T, RP, false>);
-  if (a.out_dt == TP_F32) return launch_one(lora_expand_kernel<T, RP, float>, tiles * S, smem, 1, s, a, (int)S);
-  if (a.out_dt == TP_F16) return launch_one(lora_expand_kernel<T, RP, __half>, tiles * S, smem, 1, s, a, (int)S);
-  return launch_one(lora_expand_kernel<T, RP, __nv_bfloat16>, tiles * S, smem, 1, s, a, (int)S);
+  if (int rc = launch_one(lora_shrink_kernel<T, RP>, ShrinkShared<RP>::kCtas, sizeof(ShrinkShared<RP>), a, s)) return rc;
+  if (a.out_dt == TP_F32) return launch_expand<T, RP, float>(a, s);
+  return a.out_dt == TP_F16 ? launch_expand<T, RP, __half>(a, s) : launch_expand<T, RP, __nv_bfloat16>(a, s);
 }
 
 template <typename T>

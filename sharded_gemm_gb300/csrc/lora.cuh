@@ -8,6 +8,8 @@
 // neighbouring ones: column 8 (g / 2) + 2 j + g % 2 of 32 is row g of product j's B.
 #pragma once
 
+#include <type_traits>
+
 #include "mma16.cuh"
 #include "serve.cuh"
 
@@ -45,22 +47,28 @@ __device__ __forceinline__ void terms_of(float a, float b, uint32_t *to, int ste
   }
 }
 
+// The tiles of `rows` tokens of a group; none where the tokens without an adapter are
+// left alone.
+__device__ __forceinline__ int tiles_of(const LoraArgs &a, const int4 &g, int rows, bool none) {
+  if (g.x < 0 && !none) return 0;
+  if (g.x >= a.n || g.y < 0 || g.z < 0 || (int64_t)g.y + g.z > a.T) {  // not a plan of this call
+    record_bad_value(a.status);
+    return 0;
+  }
+  return (g.z + rows - 1) / rows;
+}
+__device__ __forceinline__ int4 group_at(const LoraArgs &a, int i, int groups) {
+  return i < groups ? __ldg(reinterpret_cast<const int4 *>(a.plan + 4) + i) : make_int4(-1, 0, 0, 0);
+}
+
 // Tile `tile` of the plan, counting on from group `base` (tiles `before` it): its adapter,
 // first place and tokens; false behind the last.  The same in all lanes.
-__device__ __forceinline__ bool find_tile(const LoraArgs &a, int groups, int rows, int64_t tile, int &base,
+__device__ __forceinline__ bool find_tile(const LoraArgs &a, int groups, int rows, bool none, int64_t tile, int &base,
                                           int64_t &before, int4 &found) {
   const int lane = threadIdx.x % 32;
-  const int4 *list = reinterpret_cast<const int4 *>(a.plan + 4);
   for (; base < groups; base += 32) {
-    int4 g = make_int4(-1, 0, 0, 0);
-    if (base + lane < groups) {
-      g = __ldg(list + base + lane);
-      if (g.x >= a.n || g.y < 0 || g.z < 0 || (int64_t)g.y + g.z > a.T) {  // not a plan of this call
-        g = make_int4(-1, 0, 0, 0);
-        record_bad_value(a.status);
-      }
-    }
-    const int mine = g.x < 0 && a.in_place ? 0 : (g.z + rows - 1) / rows;
+    const int4 g = group_at(a, base + lane, groups);
+    const int mine = tiles_of(a, g, rows, none);
     int run = mine;
 #pragma unroll
     for (int m = 1; m < 32; m *= 2) {
@@ -112,6 +120,16 @@ __device__ __forceinline__ void make_fragments(const float *h, uint4 (*frag)[MT]
 #pragma unroll
     for (int n = 0; n < N; ++n) frag[n][m][ks][l] = make_uint4(f[n][0], f[n][1], f[n][2], f[n][3]);
   }
+}
+
+// How many terms of T h meets B as.  Where the outputs are 16-bit too (and of no more bits
+// than T) one: h is rounded as the linears' intermediates are, and adds less to an output's
+// error than its own rounding does.  Float16 outputs of bfloat16 products take two (16 bits),
+// float32 ones two of float16 (22 bits) or three of bfloat16 (24).
+template <typename T>
+__host__ __device__ constexpr int terms(int out_dt) {
+  return out_dt == TP_F32 ? (std::is_same<T, __nv_bfloat16>::value ? 3 : 2)
+                          : std::is_same<T, __nv_bfloat16>::value && out_dt == TP_F16 ? 2 : 1;
 }
 
 // Part p of the parts of `per` units, and the unit in it.

@@ -33,8 +33,10 @@ inline int64_t plan_ints(int64_t T, int64_t n) { return 4 + 4 * most_groups(T, n
 // Steps of more tokens take two passes with h between them in memory.  (A tile of 16 reads
 // an adapter for every 16 tokens; up to here the second launch costs more.)
 constexpr int64_t kFewTokens = 1024;
+// How often a tile's contraction is split at most: few tiles leave SMs idle.
+inline int lora_splits(int64_t T) { return T <= 4096 ? 8 : T <= 8192 ? 4 : T <= 16384 ? 2 : 1; }
 inline int64_t lora_workspace(int64_t T, int R) {
-  return T <= kFewTokens ? 0 : T * (R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 ? 64 : 128);
+  return T <= kFewTokens ? 0 : T * (R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 ? 64 : 128) * lora_splits(T);
 }
 
 struct LoraArgs {
@@ -47,7 +49,8 @@ struct LoraArgs {
   int nx, ny, R;
   int dt, out_dt;
   int in_place;  // out is y: tokens without an adapter are left alone
-  float *workspace;  // many tokens: (T, R rounded up to 16, 32, 64 or 128); else null
+  float *workspace;  // many tokens: (splits, T, R rounded up to 16, 32, 64 or 128); else null
+  int splits;
   int *status;
 };
 

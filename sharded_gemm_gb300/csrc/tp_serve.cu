@@ -74,7 +74,7 @@ int lora(int nx, const void *const *x, int64_t T, int64_t K, int64_t ldx, const 
   }
   if (same && (same < ny || (T > 1 && ldy != ldo)))
     return set_error(TP_ERR_INVALID_ARG, "out must be y for all ranks, with one row stride, or for none");
-  l.plan = plan, l.scales = scales, l.workspace = lora_workspace(T, R) > 0 ? workspace : nullptr;
+  l.plan = plan, l.scales = scales, l.workspace = lora_workspace(T, R) > 0 ? workspace : nullptr, l.splits = lora_splits(T);
   l.T = T, l.n = n, l.K = K, l.O = O, l.ldx = ldx, l.ldy = ldy, l.ldo = ldo, l.most = most_groups(T, n);
   l.nx = nx, l.ny = ny, l.R = R, l.dt = dt, l.out_dt = out_dt, l.in_place = same != 0;
   if (int rc = need_status(&l.status)) return rc;

@@ -119,7 +119,9 @@ def test_sizes_of_adapter_plans(L):
 
 def test_sizes_of_adapter_workspaces(L):
     assert L.tp_lora_workspace_floats(1024, 16) == 0
-    assert [L.tp_lora_workspace_floats(1025, r) for r in (1, 16, 17, 64, 65, 128)] == [1025 * r for r in (16, 16, 32, 64, 128, 128)]
+    assert [L.tp_lora_workspace_floats(1025, r) for r in (1, 16, 17, 64, 65, 128)] == \
+        [8 * 1025 * r for r in (16, 16, 32, 64, 128, 128)]
+    assert [L.tp_lora_workspace_floats(t, 16) // (16 * t) for t in (4096, 4097, 8192, 8193, 16384, 16385)] == [8, 4, 4, 2, 2, 1]
     assert L.tp_lora_workspace_floats(2000, 129) == 0 and L.tp_lora_workspace_floats(-1, 8) == 0
 
 

@@ -2,10 +2,11 @@
 pages, the adapters beside the projections, the verification of drafted tokens, and all of them together.
 
 Whole numbers have one right answer and are compared as such.  Tolerances of the adapters: with u the unit
-roundoff of the output's type (2^-8 for bfloat16, 2^-11 for float16, 2^-24 for float32) an output is rounded
-once (u |out|); the sum over x meets B as two terms, which lose at most 2^-16 of it (bfloat16: 8 + 8 bits) or
-2^-21 (float16: 11 + 11 bits, less what falls below the smallest), and the two products are summed in float32,
-(K + R) adds of at most 2^-23 of the sum of their terms' sizes.
+roundoff of a type (2^-8 for bfloat16, 2^-11 for float16, 2^-24 for float32) an output is rounded once (u |out|).
+The sum over x meets B as terms of the operands' type: one where the outputs have no more bits than it, which
+loses at most its u of it; two of bfloat16 for float16 outputs, 2^-16 (8 + 8 bits); for float32 ones two of
+float16, 2^-21 (11 + 11 bits, less what falls below the smallest), or three of bfloat16, 2^-22 and less.  The two
+products are summed in float32, (K + R) adds of at most 2^-23 of the sum of their terms' sizes.
 """
 import numpy as np
 import pytest
@@ -264,7 +265,11 @@ def lora_ref(x, a, b, ids, scales, y):
 def check_lora(got, x, a, b, ids, scales, y, dt):
     ref, big = lora_ref(x, a, b, ids, scales, y)
     K, R = sum(t.shape[1] for t in x), a[0].shape[1]
-    lost = (2.0 ** -16 if dt == BF16 else 2.0 ** -20) + (K + R) * 2.0 ** -23
+    if got[0].dtype == F32:
+        lost = 2.0 ** -22 if dt == BF16 else 2.0 ** -20
+    else:
+        lost = 2.0 ** -16 if dt == BF16 and got[0].dtype == F16 else U[dt]
+    lost += (K + R) * 2.0 ** -23
     live = ids > -2
     for g, f, s, start in zip(got, ref, big, y):
         assert torch.equal(g[~live], start[~live])
