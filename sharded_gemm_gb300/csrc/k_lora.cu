@@ -37,46 +37,60 @@ __device__ __forceinline__ uint2 load4(const uint16_t *row, int k, int K) {
   return make_uint2(v[0] | v[1] << 16, v[2] | v[3] << 16);
 }
 
-// Eight neighbouring outputs of a row: float32 bits, or 16-bit pairs in the first four.
+// A lane's eight outputs of a row, at `col` and, float32, the second four 16 columns on:
+// float32 bits, or 16-bit pairs in the first four.  Columns of `cols` and more are not there.
 struct Out8 {
   uint32_t v[8];
 };
 template <bool VEC>
-__device__ __forceinline__ void load_out(Out8 &o, const void *base, int64_t at, int n, int dt) {
-  if (VEC) {
-    if (n <= 0) return;
-    const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const char *>(base) + at * (dt == TP_F32 ? 4 : 2));
-    const uint4 a = p[0];
-    o.v[0] = a.x, o.v[1] = a.y, o.v[2] = a.z, o.v[3] = a.w;
-    if (dt == TP_F32) {
-      const uint4 b = p[1];
-      o.v[4] = b.x, o.v[5] = b.y, o.v[6] = b.z, o.v[7] = b.w;
+__device__ __forceinline__ void load_out(Out8 &o, const void *base, int64_t row, int col, int cols, int dt) {
+  if (dt == TP_F32) {
+    const uint32_t *p = static_cast<const uint32_t *>(base) + row + col;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (VEC) {
+        if (col + i * 16 >= cols) continue;
+        const uint4 a = *reinterpret_cast<const uint4 *>(p + i * 16);
+        o.v[4 * i] = a.x, o.v[4 * i + 1] = a.y, o.v[4 * i + 2] = a.z, o.v[4 * i + 3] = a.w;
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o.v[4 * i + k] = col + i * 16 + k < cols ? p[i * 16 + k] : 0;
+      }
     }
-  } else if (dt == TP_F32) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o.v[i] = i < n ? static_cast<const uint32_t *>(base)[at + i] : 0;
+  } else if (VEC) {
+    if (col >= cols) return;
+    const uint4 a = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(base) + row + col);
+    o.v[0] = a.x, o.v[1] = a.y, o.v[2] = a.z, o.v[3] = a.w;
   } else {
-    const uint16_t *p = static_cast<const uint16_t *>(base) + at;
+    const uint16_t *p = static_cast<const uint16_t *>(base) + row + col;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o.v[i] = (2 * i < n ? p[2 * i] : 0) | (2 * i + 1 < n ? p[2 * i + 1] : 0) << 16;
+    for (int i = 0; i < 4; ++i)
+      o.v[i] = (col + 2 * i < cols ? p[2 * i] : 0) | (col + 2 * i + 1 < cols ? p[2 * i + 1] : 0) << 16;
   }
 }
 template <bool VEC>
-__device__ __forceinline__ void store_out(const Out8 &o, void *base, int64_t at, int n, int dt) {
-  if (VEC) {
-    if (n <= 0) return;
-    uint4 *p = reinterpret_cast<uint4 *>(static_cast<char *>(base) + at * (dt == TP_F32 ? 4 : 2));
-    p[0] = make_uint4(o.v[0], o.v[1], o.v[2], o.v[3]);
-    if (dt == TP_F32) p[1] = make_uint4(o.v[4], o.v[5], o.v[6], o.v[7]);
-  } else if (dt == TP_F32) {
+__device__ __forceinline__ void store_out(const Out8 &o, void *base, int64_t row, int col, int cols, int dt) {
+  if (dt == TP_F32) {
+    uint32_t *p = static_cast<uint32_t *>(base) + row + col;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) static_cast<uint32_t *>(base)[at + i] = o.v[i];
+    for (int i = 0; i < 2; ++i) {
+      if (VEC) {
+        if (col + i * 16 < cols)
+          *reinterpret_cast<uint4 *>(p + i * 16) = make_uint4(o.v[4 * i], o.v[4 * i + 1], o.v[4 * i + 2], o.v[4 * i + 3]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (col + i * 16 + k < cols) p[i * 16 + k] = o.v[4 * i + k];
+      }
+    }
+  } else if (VEC) {
+    if (col < cols)
+      *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(base) + row + col) = make_uint4(o.v[0], o.v[1], o.v[2], o.v[3]);
   } else {
-    uint16_t *p = static_cast<uint16_t *>(base) + at;
+    uint16_t *p = static_cast<uint16_t *>(base) + row + col;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (i < n) p[i] = (uint16_t)(o.v[i / 2] >> (i % 2 * 16));
+      if (col + i < cols) p[i] = (uint16_t)(o.v[i / 2] >> (i % 2 * 16));
   }
 }
 __device__ __forceinline__ void add_out(Out8 &o, const float (&d)[8], int dt) {
@@ -124,6 +138,7 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : RP == 64 ? 2 : 3
   const int u0 = (int)((int64_t)units * (rank * kWarps + warp) / (C * kWarps));
   const int u1 = (int)((int64_t)units * (rank * kWarps + warp + 1) / (C * kWarps));
   const int used = terms<T>(a.out_dt);
+  const bool out32 = a.out_dt == TP_F32;
   griddep_launch_dependents();
   griddep_wait();
   const int groups = groups_of(a);
@@ -144,12 +159,12 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : RP == 64 ? 2 : 3
       Out8 y0, y1;
     };
     auto fetch = [&](const Cursor &c, Block &o) {
-      const int col = c.i * 32 + q * 8, n = min(O - col, 8);
+      const int col = c.i * 32 + lane_col(out32, 0, q);
       if (id >= 0) {
         const uint16_t *b = static_cast<const uint16_t *>(a.b[c.p]) + ((int64_t)id * O + c.i * 32) * a.R;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int r = (g >> 1) * 8 + 2 * j + (g & 1);
+          const int r = b_row(out32, j, g);
           const uint16_t *row = b + r * a.R;
           const int R = c.i * 32 + r < O ? a.R : 0;
           if (RP == 16) {
@@ -164,8 +179,8 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : RP == 64 ? 2 : 3
           }
         }
       }
-      if (t0 >= 0) load_out<VEC>(o.y0, a.y[c.p], t0 * a.ldy + col, n, a.out_dt);
-      if (t1 >= 0) load_out<VEC>(o.y1, a.y[c.p], t1 * a.ldy + col, n, a.out_dt);
+      if (t0 >= 0) load_out<VEC>(o.y0, a.y[c.p], t0 * a.ldy, col, O, a.out_dt);
+      if (t1 >= 0) load_out<VEC>(o.y1, a.y[c.p], t1 * a.ldy, col, O, a.out_dt);
     };
     Block now;
     Cursor c(blk0, per_o);
@@ -246,7 +261,7 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : RP == 64 ? 2 : 3
     const float f0 = Half2<T>::kBf16 || id < 0 ? 1.0f : sh.unscale[g];
     const float f1 = Half2<T>::kBf16 || id < 0 ? 1.0f : sh.unscale[g + 8];
     for (int blk = blk0; blk < blocks; blk += step) {
-      const int p = c.p, col = c.i * 32 + q * 8, n = min(O - col, 8);
+      const int p = c.p, col = c.i * 32 + lane_col(out32, 0, q);
       c.next(step, per_o);
       if (id >= 0) {
         float d[4][4];
@@ -273,8 +288,8 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : RP == 64 ? 2 : 3
       }
       const Out8 y0 = now.y0, y1 = now.y1;
       if (blk + step < blocks) fetch(c, now);
-      if (t0 >= 0) store_out<VEC>(y0, a.out[p], t0 * a.ldo + col, n, a.out_dt);
-      if (t1 >= 0) store_out<VEC>(y1, a.out[p], t1 * a.ldo + col, n, a.out_dt);
+      if (t0 >= 0) store_out<VEC>(y0, a.out[p], t0 * a.ldo, col, O, a.out_dt);
+      if (t1 >= 0) store_out<VEC>(y1, a.out[p], t1 * a.ldo, col, O, a.out_dt);
     }
   }
   if (read && C > 1) cluster_wait();  // no CTA leaves while another may still read its shared memory

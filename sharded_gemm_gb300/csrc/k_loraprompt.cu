@@ -167,8 +167,8 @@ __global__ void __launch_bounds__(kLoraThreads, ShrinkShared<RP>::kCtas)
 }
 
 // ---------------------------------------------------------------- the second pass
-// A warp takes 32 columns of a tile at a time, its lane the rows g and g + 8 of each of the
-// four blocks of 16 tokens, 8 columns of each.  A block's old values are fetched while the
+// A warp takes 32 columns of a tile at a time, its lane 8 of them in the rows g and g + 8 of
+// each of the four blocks of 16 tokens.  A block's old values are fetched while the
 // one before it is worked on, into the place that was just read.
 template <typename T, int RP, typename O>
 struct ExpandShared {
@@ -265,13 +265,18 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
     // the old values of block m of the columns that cy names
     auto fetch = [&](int m, bool any) {
       if (any) {
-        const int col = cy.i * 32 + q * 8;
-        const char *y = static_cast<const char *>(a.y[cy.p]) + (col < cols ? col : 0) * (int)sizeof(O);
+        const char *y = static_cast<const char *>(a.y[cy.p]);
+        int at[kWords];
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+          const int col = cy.i * 32 + lane_col(OUT32, i, q);
+          at[i] = (col < cols ? col : 0) * (int)sizeof(O);
+        }
 #pragma unroll
         for (int r = 0; r < 2; ++r)
 #pragma unroll
           for (int i = 0; i < kWords; ++i)
-            cp_async16(smem_u32(ring + ((m * 2 + r) * kWords + i) * 32), y + sh.y_row[m * 16 + r * 8 + g] + 16 * i, true);
+            cp_async16(smem_u32(ring + ((m * 2 + r) * kWords + i) * 32), y + sh.y_row[m * 16 + r * 8 + g] + at[i], true);
       }
       cp_async_commit();
     };
@@ -284,7 +289,7 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
       const uint16_t *b = static_cast<const uint16_t *>(a.b[at.p]) + ((int64_t)id * cols + at.i * 32) * a.R;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int r = (g >> 1) * 8 + 2 * j + (g & 1);
+        const int r = b_row(OUT32, j, g);
         const bool in = at.i * 32 + r < cols;
         const uint16_t *row = b + r * a.R;
         if (RP == 16) {
@@ -299,9 +304,9 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
     };
     if (id >= 0 && blk0 < blocks) load_b(c);
     for (int blk = blk0; blk < blocks; blk += step) {
-      const int col = c.i * 32 + q * 8;
+      const int col = c.i * 32 + lane_col(OUT32, 0, q);
       char *const out = static_cast<char *>(a.out[c.p]) + col * (int)sizeof(O);
-      const bool in = col < cols, more = blk + step < blocks;
+      const bool more = blk + step < blocks;
       c.next(step, per);
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
@@ -358,10 +363,10 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
             y[r][0] = pack8<O>(add[r]);
           }
           const int64_t row = sh.out_row[m * 16 + r * 8 + g];
-          if (row >= 0 && in) {
-            uint4 *to = reinterpret_cast<uint4 *>(out + row);
+          if (row >= 0) {
 #pragma unroll
-            for (int i = 0; i < kWords; ++i) to[i] = y[r][i];
+            for (int i = 0; i < kWords; ++i)
+              if (col + i * 16 < cols) *reinterpret_cast<uint4 *>(out + row + i * 64) = y[r][i];
           }
         }
       }

@@ -4,8 +4,9 @@
 // A warp-level m16n8k16 product takes its fragments straight from memory, 16 bytes a lane,
 // because a contraction may go through its index in any order that both operands share: a
 // quad's four lanes hold 8 neighbouring elements each, which feed two products (with R of
-// 16 four, for one).  Output columns are dealt to four products so that a lane ends with 8
-// neighbouring ones: column 8 (g / 2) + 2 j + g % 2 of 32 is row g of product j's B.
+// 16 four, for one).  32 output columns are dealt to four products so that a lane ends with
+// 16 bytes of neighbouring ones (b_row): of 16-bit outputs 8, of float32 ones twice 4, so
+// that a quad's 16-byte accesses lie side by side.
 #pragma once
 
 #include <type_traits>
@@ -121,6 +122,13 @@ __device__ __forceinline__ void make_fragments(const float *h, uint4 (*frag)[MT]
     for (int n = 0; n < N; ++n) frag[n][m][ks][l] = make_uint4(f[n][0], f[n][1], f[n][2], f[n][3]);
   }
 }
+
+// Which of 32 output columns row g of product j's B is, and where a lane's i-th 16 bytes
+// of outputs begin.
+__device__ __forceinline__ int b_row(bool out32, int j, int g) {
+  return out32 ? j / 2 * 16 + g / 2 * 4 + j % 2 * 2 + g % 2 : g / 2 * 8 + 2 * j + g % 2;
+}
+__device__ __forceinline__ int lane_col(bool out32, int i, int q) { return out32 ? i * 16 + q * 4 : q * 8; }
 
 // How many terms of T h meets B as.  Where the outputs are 16-bit too (and of no more bits
 // than T) one: h is rounded as the linears' intermediates are, and adds less to an output's
