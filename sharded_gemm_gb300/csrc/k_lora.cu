@@ -135,8 +135,7 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : RP == 64 ? 2 : 3
   const int per_k = (K + 31) / 32, units = per_k * a.nx;
   const int per_o = (O + 31) / 32, blocks = per_o * a.ny, step = S * C * kWarps;
   const int blk0 = (cluster % S * C + rank) * kWarps + warp;
-  const int u0 = (int)((int64_t)units * (rank * kWarps + warp) / (C * kWarps));
-  const int u1 = (int)((int64_t)units * (rank * kWarps + warp + 1) / (C * kWarps));
+  const int u0 = rank * kWarps + warp;
   const int used = terms<T>(a.out_dt);
   const bool out32 = a.out_dt == TP_F32;
   griddep_launch_dependents();
@@ -193,7 +192,7 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : RP == 64 ? 2 : 3
       const uint4 zero = make_uint4(0, 0, 0, 0);
       Cursor cu(u0, per_k);
 #pragma unroll 2
-      for (int u = u0; u < u1; ++u) {
+      for (int u = u0; u < units; u += C * kWarps) {  // neighbours read a row's neighbouring bytes
         const int k = cu.i * 32 + q * 8;
         const uint16_t *x = static_cast<const uint16_t *>(a.x[cu.p]);
         const uint16_t *w = static_cast<const uint16_t *>(a.a[cu.p]) + ((int64_t)id * a.R + g) * K;
@@ -202,13 +201,14 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : RP == 64 ? 2 : 3
         uint4 v[NT];
 #pragma unroll
         for (int j = 0; j < NT; ++j) v[j] = j * 8 + g < a.R ? load8<VEC>(w + (int64_t)j * 8 * K, k, K) : zero;
-        const uint32_t f0[4] = {r0.x, r1.x, r0.y, r1.y}, f1[4] = {r0.z, r1.z, r0.w, r1.w};
+        uint32_t f0[4], f1[4];
+        keep4(f0, r0.x, r1.x, r0.y, r1.y);
+        keep4(f1, r0.z, r1.z, r0.w, r1.w);
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          mma16816<T>(acc[j], f0, v[j].x, v[j].y);
-          mma16816<T>(acc[j], f1, v[j].z, v[j].w);
-        }
-        cu.next(1, per_k);
+        for (int j = 0; j < NT; ++j) mma16816<T>(acc[j], f0, v[j].x, v[j].y);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) mma16816<T>(acc[j], f1, v[j].z, v[j].w);
+        cu.next(C * kWarps, per_k);
       }
       if (blk0 < blocks) fetch(c, now);  // under the sums' exchange
       if (read && C > 1) cluster_wait();

@@ -77,43 +77,43 @@ __global__ void __launch_bounds__(kLoraThreads, ShrinkShared<RP>::kCtas)
   int4 tile;
   for (int64_t item = blockIdx.x; item < (int64_t)tiles * S; item += gridDim.x) {
     if (!find_tile(a, groups, kTile, false, item / S, base, before, tile)) break;
-    const int id = tile.x, split = (int)(item % S), slot = split * kG + warp / Shared::kM;
-    const int u0 = (int)((int64_t)units * slot / (S * kG)), u1 = (int)((int64_t)units * (slot + 1) / (S * kG));
+    // the split's units in turn to the groups of warps: neighbours read a row's neighbouring bytes
+    const int id = tile.x, split = (int)(item % S), u0 = (int)((int64_t)units * split / S) + warp / Shared::kM;
+    const int u1 = (int)((int64_t)units * (split + 1) / S);
     __syncthreads();  // the last item's sums are read
     read_tokens(a, tile, kTile, sh.token);
     __syncthreads();
-    int64_t row[2 * MW];  // where the lane's rows of x begin; without a token, -1
+    int64_t row[2 * MW];  // where the lane's rows of x begin; without a token, any: its h is not kept
 #pragma unroll
-    for (int i = 0; i < 2 * MW; ++i) {
-      const int t = sh.token[(m0 + i / 2) * 16 + i % 2 * 8 + g];
-      row[i] = t < 0 ? -1 : t * a.ldx;
-    }
+    for (int i = 0; i < 2 * MW; ++i) row[i] = max(sh.token[(m0 + i / 2) * 16 + i % 2 * 8 + g], 0) * a.ldx;
     Cursor c(u0, per);
     int ahead = u0, x_slot = 0, slot_at = 0;
-    const uint16_t *x = nullptr, *w = nullptr;
+    const uint16_t *x[2 * MW], *w = nullptr;
     auto part = [&]() {
-      x = static_cast<const uint16_t *>(a.x[c.p]);
+#pragma unroll
+      for (int i = 0; i < 2 * MW; ++i) x[i] = static_cast<const uint16_t *>(a.x[c.p]) + row[i];
       w = static_cast<const uint16_t *>(a.a[c.p]) + ((int64_t)id * a.R + g) * K;
     };
     if (u0 < u1) part();
     auto fetch = [&]() {
       if (ahead < u1) {
-        const int k = c.i * 32 + q * 8;
-        const bool in = k < K;
+        // behind the rows' end zeros, and in place of the rows that the adapter lacks
+        const int at = c.i * 32 + q * 8, k = at < K ? at : 0, size = at < K ? 16 : 0;
         const uint32_t to = smem_u32(&sh.ring[warp][x_slot][0][lane]);
 #pragma unroll
-        for (int i = 0; i < 2 * MW; ++i)
-          cp_async16(to + i * 512, row[i] >= 0 && in ? x + row[i] + k : x, row[i] >= 0 && in);
+        for (int i = 0; i < 2 * MW; ++i) cp_async16(to + i * 512, x[i] + k, size);
+        const uint16_t *from = w + k;
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-          const bool valid = in && j * 8 + g < a.R;
-          cp_async16(to + (2 * MW + j) * 512, valid ? w + (int64_t)j * 8 * K + k : x, valid);
+          const bool in = j * 8 + g < a.R;
+          cp_async16(to + (2 * MW + j) * 512, in ? from : w, in ? size : 0);
+          from += 8 * (int64_t)K;
         }
         const int p = c.p;
-        c.next(1, per);
-        if (c.p != p && ahead + 1 < u1) part();
+        c.next(kG, per);
+        if (c.p != p && ahead + kG < u1) part();
       }
-      ++ahead;
+      ahead += kG;
       x_slot = x_slot + 1 == kAhead ? 0 : x_slot + 1;
       cp_async_commit();
     };
@@ -124,23 +124,31 @@ __global__ void __launch_bounds__(kLoraThreads, ShrinkShared<RP>::kCtas)
     for (int m = 0; m < MW; ++m)
 #pragma unroll
       for (int j = 0; j < NT; ++j) acc[m][j][0] = acc[m][j][1] = acc[m][j][2] = acc[m][j][3] = 0.0f;
-    for (int u = u0; u < u1; ++u) {
+    for (int u = u0; u < u1; u += kG) {
       cp_async_wait<kAhead - 2>();
       const uint4(*const ring)[32] = sh.ring[warp][slot_at];
-      uint4 r[2 * MW];
+      uint32_t f[MW][2][4];  // put together once: the products want them in neighbouring registers
 #pragma unroll
-      for (int i = 0; i < 2 * MW; ++i) r[i] = ring[i][lane];
+      for (int m = 0; m < MW; ++m) {
+        const uint4 r0 = ring[2 * m][lane], r1 = ring[2 * m + 1][lane];
+        keep4(f[m][0], r0.x, r1.x, r0.y, r1.y);
+        keep4(f[m][1], r0.z, r1.z, r0.w, r1.w);
+      }
       fetch();
+      constexpr int JW = 4 / MW;  // four products between two of one sum
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const uint4 v = ring[2 * MW + j][lane];
+      for (int j = 0; j < NT; j += JW) {
+        uint4 v[JW];
 #pragma unroll
-        for (int m = 0; m < MW; ++m) {
-          const uint32_t f0[4] = {r[2 * m].x, r[2 * m + 1].x, r[2 * m].y, r[2 * m + 1].y};
-          const uint32_t f1[4] = {r[2 * m].z, r[2 * m + 1].z, r[2 * m].w, r[2 * m + 1].w};
-          mma16816<T>(acc[m][j], f0, v.x, v.y);
-          mma16816<T>(acc[m][j], f1, v.z, v.w);
-        }
+        for (int k = 0; k < JW; ++k) v[k] = ring[2 * MW + j + k][lane];
+#pragma unroll
+        for (int k = 0; k < JW; ++k)
+#pragma unroll
+          for (int m = 0; m < MW; ++m) mma16816<T>(acc[m][j + k], f[m][0], v[k].x, v[k].y);
+#pragma unroll
+        for (int k = 0; k < JW; ++k)
+#pragma unroll
+          for (int m = 0; m < MW; ++m) mma16816<T>(acc[m][j + k], f[m][1], v[k].z, v[k].w);
       }
       slot_at = slot_at + 1 == kAhead ? 0 : slot_at + 1;
     }
@@ -179,6 +187,7 @@ struct ExpandShared {
     uint4 ring[kWarps][4][2 * kWords][32];
     float h[kTile][kStride];
   };
+  uint4 b[kWarps][RP == 16 ? 4 : RP / 8][32];  // the adapter's rows
   uint4 frag[kTerms][4][RP / 16][32];
   int64_t y_row[kTile], out_row[kTile];  // where the rows begin, in bytes; out: without a token, -1
   int token[kTile];
@@ -276,47 +285,53 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
         for (int r = 0; r < 2; ++r)
 #pragma unroll
           for (int i = 0; i < kWords; ++i)
-            cp_async16(smem_u32(ring + ((m * 2 + r) * kWords + i) * 32), y + sh.y_row[m * 16 + r * 8 + g] + at[i], true);
+            cp_async16(smem_u32(ring + ((m * 2 + r) * kWords + i) * 32), y + sh.y_row[m * 16 + r * 8 + g] + at[i], 16);
       }
       cp_async_commit();
     };
-#pragma unroll
-    for (int m = 0; m < 4; ++m) fetch(m, blk0 < blocks);
-    cy.next(step, per);
-
-    uint4 w[4][RP == 16 ? 1 : KS / 2];
-    auto load_b = [&](const Cursor &at) {
-      const uint16_t *b = static_cast<const uint16_t *>(a.b[at.p]) + ((int64_t)id * cols + at.i * 32) * a.R;
+    // the adapter's rows of the columns that cy names
+    constexpr int kB = RP == 16 ? 1 : KS / 2;
+    auto fetch_b = [&]() {
+      const uint16_t *b = static_cast<const uint16_t *>(a.b[cy.p]) + ((int64_t)id * cols + cy.i * 32) * a.R;
+      const uint32_t to = smem_u32(&sh.b[warp][0][lane]);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int r = b_row(OUT32, j, g);
-        const bool in = at.i * 32 + r < cols;
-        const uint16_t *row = b + r * a.R;
-        if (RP == 16) {
-          const uint2 v = in && q * 4 < a.R ? __ldg(reinterpret_cast<const uint2 *>(row + q * 4)) : make_uint2(0, 0);
-          w[j][0].x = v.x, w[j][0].y = v.y;
-        } else {
+        const bool in = cy.i * 32 + r < cols;
 #pragma unroll
-          for (int s = 0; s < KS / 2; ++s)
-            w[j][s] = in && s * 32 + q * 8 < a.R ? __ldg(reinterpret_cast<const uint4 *>(row + s * 32 + q * 8)) : make_uint4(0, 0, 0, 0);
+        for (int s = 0; s < kB; ++s) {
+          const int k = RP == 16 ? q * 4 : s * 32 + q * 8;
+          const bool valid = in && k < a.R;
+          if (RP == 16) cp_async8(to + j * 512, valid ? b + r * a.R + k : b, valid ? 8 : 0);
+          else cp_async16(to + (j * kB + s) * 512, valid ? b + r * a.R + k : b, valid ? 16 : 0);
         }
       }
     };
-    if (id >= 0 && blk0 < blocks) load_b(c);
+    if (id >= 0 && blk0 < blocks) fetch_b();
+#pragma unroll
+    for (int m = 0; m < 4; ++m) fetch(m, blk0 < blocks);
+    cy.next(step, per);
     for (int blk = blk0; blk < blocks; blk += step) {
       const int col = c.i * 32 + lane_col(OUT32, 0, q);
       char *const out = static_cast<char *>(a.out[c.p]) + col * (int)sizeof(O);
       const bool more = blk + step < blocks;
       c.next(step, per);
+      uint4 w[4][kB];
+      if (id >= 0) {
+        cp_async_wait<3>();
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int s = 0; s < kB; ++s) w[j][s] = sh.b[warp][j * kB + s][lane];
+      }
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
         uint4 y[2][kWords];
         float d[4][4], add[2][8];
-        auto take = [&]() {  // the old values, and the fetch of the next into their place
+        auto take = [&]() {
           cp_async_wait<3>();
 #pragma unroll
           for (int i = 0; i < 2 * kWords; ++i) y[i / kWords][i % kWords] = ring[(m * 2 * kWords + i) * 32];
-          fetch(m, more);
         };
         if (kSeed) {
           take();
@@ -343,7 +358,7 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
                 mma16816<T>(d[j], hf, s % 2 ? b.z : b.x, s % 2 ? b.w : b.y);
               }
             }
-          if (m == 3 && more) load_b(c);
+          if (m == 0 && more) fetch_b();  // the products have read the rows
         }
         if (!kSeed) take();
 #pragma unroll
@@ -369,6 +384,7 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
               if (col + i * 16 < cols) *reinterpret_cast<uint4 *>(out + row + i * 64) = y[r][i];
           }
         }
+        fetch(m, more);  // into the place of the values just used
       }
       cy.next(step, per);
     }

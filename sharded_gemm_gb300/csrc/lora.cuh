@@ -140,6 +140,13 @@ __host__ __device__ constexpr int terms(int out_dt) {
                           : std::is_same<T, __nv_bfloat16>::value && out_dt == TP_F16 ? 2 : 1;
 }
 
+// A product's fragment of A, in registers of its own.
+__device__ __forceinline__ void keep4(uint32_t (&f)[4], uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("mov.b32 %0, %4;\n mov.b32 %1, %5;\n mov.b32 %2, %6;\n mov.b32 %3, %7;"
+               : "=r"(f[0]), "=r"(f[1]), "=r"(f[2]), "=r"(f[3])
+               : "r"(a), "r"(b), "r"(c), "r"(d));
+}
+
 // Part p of the parts of `per` units, and the unit in it.
 struct Cursor {
   int p, i;

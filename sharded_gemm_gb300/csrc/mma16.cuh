@@ -13,6 +13,14 @@ namespace tp {
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
 }
+// Copies 16 bytes, or with size 0 writes 16 zero bytes.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int size) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(size) : "memory");
+}
+// The same of 8 bytes.
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void *src, int size) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(size) : "memory");
+}
 // Copies 8 or 16 bytes global -> shared.
 template <int BYTES>
 __device__ __forceinline__ void cp_async(uint32_t dst, const void *src) {
