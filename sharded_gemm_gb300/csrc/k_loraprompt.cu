@@ -14,14 +14,14 @@
 namespace tp {
 namespace {
 
-constexpr int kTile = 64;
+constexpr int kShrinkTile = 64;  // tokens of a tile of the first pass
 
 // The tiles of a plan (in all lanes).
-__device__ __forceinline__ int count_tiles(const LoraArgs &a, int groups, bool none) {
+__device__ __forceinline__ int count_tiles(const LoraArgs &a, int groups, int rows, bool none) {
   int n = 0;
 #pragma unroll 4
   for (int base = 0; base < groups; base += 32)
-    n += (int)__reduce_add_sync(0xffffffffu, tiles_of(a, group_at(a, base + threadIdx.x % 32, groups), kTile, none));
+    n += (int)__reduce_add_sync(0xffffffffu, tiles_of(a, group_at(a, base + threadIdx.x % 32, groups), rows, none));
   return n;
 }
 
@@ -49,9 +49,9 @@ struct ShrinkShared {
   static constexpr int kCtas = RP <= 32 ? 2 : 1;                                            // of an SM
   union {
     uint4 ring[kWarps][kAhead][kRows][32];
-    float part[kG][kTile][kStride];
+    float part[kG][kShrinkTile][kStride];
   };
-  int token[kTile];
+  int token[kShrinkTile];
 };
 template <int RP>
 __device__ __forceinline__ int splits_of(const LoraArgs &a, int tiles, int sms) {
@@ -69,19 +69,19 @@ __global__ void __launch_bounds__(kLoraThreads, ShrinkShared<RP>::kCtas)
   Shared &sh = *reinterpret_cast<Shared *>(smem);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, q = lane % 4;
   const int K = (int)a.K, per = (K + 31) / 32, units = per * a.nx, m0 = warp % Shared::kM * MW;
-  griddep_launch_dependents();
   griddep_wait();
-  const int groups = groups_of(a), tiles = count_tiles(a, groups, false), S = splits_of<RP>(a, tiles, sms);
+  griddep_launch_dependents();  // behind the wait: the second pass may read what came before this one
+  const int groups = groups_of(a), tiles = count_tiles(a, groups, kShrinkTile, false), S = splits_of<RP>(a, tiles, sms);
   int base = 0;
   int64_t before = 0;
   int4 tile;
   for (int64_t item = blockIdx.x; item < (int64_t)tiles * S; item += gridDim.x) {
-    if (!find_tile(a, groups, kTile, false, item / S, base, before, tile)) break;
+    if (!find_tile(a, groups, kShrinkTile, false, item / S, base, before, tile)) break;
     // the split's units in turn to the groups of warps: neighbours read a row's neighbouring bytes
     const int id = tile.x, split = (int)(item % S), u0 = (int)((int64_t)units * split / S) + warp / Shared::kM;
     const int u1 = (int)((int64_t)units * (split + 1) / S);
     __syncthreads();  // the last item's sums are read
-    read_tokens(a, tile, kTile, sh.token);
+    read_tokens(a, tile, kShrinkTile, sh.token);
     __syncthreads();
     int64_t row[2 * MW];  // where the lane's rows of x begin; without a token, any: its h is not kept
 #pragma unroll
@@ -176,19 +176,20 @@ __global__ void __launch_bounds__(kLoraThreads, ShrinkShared<RP>::kCtas)
 
 // ---------------------------------------------------------------- the second pass
 // A warp takes 32 columns of a tile at a time, its lane 8 of them in the rows g and g + 8 of
-// each of the four blocks of 16 tokens.  A block's old values are fetched while the
-// one before it is worked on, into the place that was just read.
+// each block of 16 tokens.  Old values are fetched into the place that was just read, four
+// blocks ahead.  The adapter's rows are read once a tile, from L2, whose rate bounds the pass
+// with the outputs: so its tiles are as long as its shared memory allows for two CTAs an SM.
 template <typename T, int RP, typename O>
 struct ExpandShared {
   static constexpr bool OUT32 = sizeof(O) == 4;
   static constexpr int kTerms = terms<T>(OUT32 ? TP_F32 : std::is_same<O, __half>::value ? TP_F16 : TP_BF16);
-  static constexpr int kStride = RP + 4, kWords = OUT32 ? 2 : 1;
+  static constexpr int kStride = RP + 4, kWords = OUT32 ? 2 : 1, kTile = RP == 128 ? 64 : 128;  // tokens
   union {
     uint4 ring[kWarps][4][2 * kWords][32];
     float h[kTile][kStride];
   };
   uint4 b[kWarps][RP == 16 ? 4 : RP / 8][32];  // the adapter's rows
-  uint4 frag[kTerms][4][RP / 16][32];
+  uint4 frag[kTerms][kTile / 16][RP / 16][32];
   int64_t y_row[kTile], out_row[kTile];  // where the rows begin, in bytes; out: without a token, -1
   int token[kTile];
   float unscale[kTile];
@@ -220,6 +221,7 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
   typedef ExpandShared<T, RP, O> Shared;
   constexpr bool OUT32 = Shared::OUT32;
   constexpr int KS = RP / 16, kTerms = Shared::kTerms, kStride = Shared::kStride, kWords = Shared::kWords;
+  constexpr int kTile = Shared::kTile;
   // 16-bit outputs: the products are added to the old values, whose sums lose less than the
   // rounding does; float32 ones keep the old values out of the products' sums
   constexpr bool kSeed = !OUT32 && Half2<T>::kBf16;
@@ -229,9 +231,10 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
   const int cols = (int)a.O, per = (cols + 31) / 32, blocks = per * a.ny;
   uint4 *const ring = &sh.ring[warp][0][0][lane];
   griddep_launch_dependents();
-  griddep_wait();
-  const int groups = groups_of(a), with = count_tiles(a, groups, false), splits = splits_of<RP>(a, with, sms);
-  const int tiles = a.in_place ? with : count_tiles(a, groups, true);
+  // only h comes from the kernel before: the plan and the tokens are read without a wait for it
+  bool waited = false;
+  const int groups = groups_of(a), with = count_tiles(a, groups, kShrinkTile, false), splits = splits_of<RP>(a, with, sms);
+  const int tiles = count_tiles(a, groups, kTile, !a.in_place);
   const int S = shares_of(tiles, gridDim.x, (blocks + kWarps - 1) / kWarps, 3, 32), step = S * kWarps;
   int base = 0;
   int64_t before = 0;
@@ -246,6 +249,8 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
       sh.y_row[tid] = max(t, 0) * a.ldy * (int64_t)sizeof(O);
       sh.out_row[tid] = t < 0 ? -1 : t * a.ldo * (int64_t)sizeof(O);
     }
+    if (!waited) griddep_wait();
+    waited = true;
     if (id >= 0) {
       const float scale = a.scales ? __ldg(a.scales + id) : 1.0f;
       for (int i = tid; i < kTile * RP / 4; i += kLoraThreads) {
@@ -266,14 +271,16 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
         }
         __syncthreads();
       }
-      make_fragments<T, RP, 4, kTerms, kStride>(&sh.h[0][0], sh.frag);
+      make_fragments<T, RP, kTile / 16, kTerms, kStride>(&sh.h[0][0], sh.frag);
     }
     __syncthreads();
 
+    const int mc = (tile.z + 15) / 16;  // blocks of 16 tokens
     Cursor cy(blk0, per), c(blk0, per);
-    // the old values of block m of the columns that cy names
-    auto fetch = [&](int m, bool any) {
-      if (any) {
+    int y_blk = blk0, y_m = 0, y_slot = 0;
+    // the old values that cy and y_m name, four blocks of 16 tokens ahead of their use
+    auto fetch = [&]() {
+      if (y_blk < blocks) {
         const char *y = static_cast<const char *>(a.y[cy.p]);
         int at[kWords];
 #pragma unroll
@@ -285,19 +292,24 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
         for (int r = 0; r < 2; ++r)
 #pragma unroll
           for (int i = 0; i < kWords; ++i)
-            cp_async16(smem_u32(ring + ((m * 2 + r) * kWords + i) * 32), y + sh.y_row[m * 16 + r * 8 + g] + at[i], 16);
+            cp_async16(smem_u32(ring + ((y_slot * 2 + r) * kWords + i) * 32), y + sh.y_row[y_m * 16 + r * 8 + g] + at[i], 16);
+        if (++y_m == mc) {
+          y_m = 0, y_blk += step;
+          cy.next(step, per);
+        }
       }
+      y_slot = (y_slot + 1) & 3;
       cp_async_commit();
     };
-    // the adapter's rows of the columns that cy names
+    // the adapter's rows of the columns that c names
     constexpr int kB = RP == 16 ? 1 : KS / 2;
     auto fetch_b = [&]() {
-      const uint16_t *b = static_cast<const uint16_t *>(a.b[cy.p]) + ((int64_t)id * cols + cy.i * 32) * a.R;
+      const uint16_t *b = static_cast<const uint16_t *>(a.b[c.p]) + ((int64_t)id * cols + c.i * 32) * a.R;
       const uint32_t to = smem_u32(&sh.b[warp][0][lane]);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int r = b_row(OUT32, j, g);
-        const bool in = cy.i * 32 + r < cols;
+        const bool in = c.i * 32 + r < cols;
 #pragma unroll
         for (int s = 0; s < kB; ++s) {
           const int k = RP == 16 ? q * 4 : s * 32 + q * 8;
@@ -309,29 +321,29 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
     };
     if (id >= 0 && blk0 < blocks) fetch_b();
 #pragma unroll
-    for (int m = 0; m < 4; ++m) fetch(m, blk0 < blocks);
-    cy.next(step, per);
+    for (int m = 0; m < 4; ++m) fetch();
+    int slot = 0;
     for (int blk = blk0; blk < blocks; blk += step) {
       const int col = c.i * 32 + lane_col(OUT32, 0, q);
       char *const out = static_cast<char *>(a.out[c.p]) + col * (int)sizeof(O);
-      const bool more = blk + step < blocks;
       c.next(step, per);
       uint4 w[4][kB];
       if (id >= 0) {
-        cp_async_wait<3>();
+        // they came with the old values of the first block of 16 tokens, mc copies ago
+        if (mc < 4) cp_async_wait<0>(); else cp_async_wait<3>();
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
           for (int s = 0; s < kB; ++s) w[j][s] = sh.b[warp][j * kB + s][lane];
       }
-#pragma unroll
-      for (int m = 0; m < 4; ++m) {
+#pragma unroll 2
+      for (int m = 0; m < mc; ++m) {
         uint4 y[2][kWords];
         float d[4][4], add[2][8];
         auto take = [&]() {
           cp_async_wait<3>();
 #pragma unroll
-          for (int i = 0; i < 2 * kWords; ++i) y[i / kWords][i % kWords] = ring[(m * 2 * kWords + i) * 32];
+          for (int i = 0; i < 2 * kWords; ++i) y[i / kWords][i % kWords] = ring[(slot * 2 * kWords + i) * 32];
         };
         if (kSeed) {
           take();
@@ -358,7 +370,7 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
                 mma16816<T>(d[j], hf, s % 2 ? b.z : b.x, s % 2 ? b.w : b.y);
               }
             }
-          if (m == 0 && more) fetch_b();  // the products have read the rows
+          if (m == 0 && blk + step < blocks) fetch_b();  // the products have read the rows
         }
         if (!kSeed) take();
 #pragma unroll
@@ -384,12 +396,13 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
               if (col + i * 16 < cols) *reinterpret_cast<uint4 *>(out + row + i * 64) = y[r][i];
           }
         }
-        fetch(m, more);  // into the place of the values just used
+        fetch();  // into the place of the values just used
+        slot = (slot + 1) & 3;
       }
-      cy.next(step, per);
     }
     cp_async_wait<0>();
   }
+  if (!waited) griddep_wait();  // what follows waits for this kernel, and so for the one before
 }
 
 template <typename K>

@@ -58,8 +58,11 @@ __device__ __forceinline__ int tiles_of(const LoraArgs &a, const int4 &g, int ro
   }
   return (g.z + rows - 1) / rows;
 }
+// (Read whether or not there are so many groups: the load need not wait for their number.)
 __device__ __forceinline__ int4 group_at(const LoraArgs &a, int i, int groups) {
-  return i < groups ? __ldg(reinterpret_cast<const int4 *>(a.plan + 4) + i) : make_int4(-1, 0, 0, 0);
+  int4 g = make_int4(-1, 0, 0, 0);
+  if (i < a.most) g = __ldg(reinterpret_cast<const int4 *>(a.plan + 4) + i);
+  return i < groups ? g : make_int4(-1, 0, 0, 0);
 }
 
 // Tile `tile` of the plan, counting on from group `base` (tiles `before` it): its adapter,
