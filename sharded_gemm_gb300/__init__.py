@@ -901,22 +901,19 @@ def tp_lora_plan(adapters, tokens: int, n: int, cu_seqlens=None, out=None, strea
     return _call("tp_lora_plan", (_native or _marshaller()).groups, adapters, tokens, n, cu_seqlens, out, stream)
 
 
-def _lora_workspace(x, a, stream):
-    """The memory of a call of many tokens for the sums over x, None for few.  Of the stream that the call runs on:
-    given back after the call, it is not handed out elsewhere before that stream is done with it."""
-    xs, pool = (t[0] if isinstance(t, (list, tuple)) else t for t in (x, a))
-    if xs.dim() < 2 or pool.dim() < 2 or xs.shape[-2] <= 1024:  # the call says what is wrong
-        return None
-    T, R = xs.shape[-2], pool.shape[-2]
+def _lora_workspace(T, R, device, stream):
+    """The memory of an adapter call of many tokens for the sums over x.  Of the stream that the call runs on: given
+    back after the call, it is not handed out elsewhere before that stream is done with it."""
     rec = getattr(_rec, "active", None)
     floats = (rec.real if rec is not None else _load()).tp_lora_workspace_floats(T, R)
     torch = _torch()
+    device = torch.device("cuda", device)
     if stream is None:
-        ws = torch.empty(floats, dtype=torch.float32, device=xs.device)
+        ws = torch.empty(floats, dtype=torch.float32, device=device)
     else:
-        side = torch.cuda.ExternalStream(stream, xs.device) if isinstance(stream, int) else stream
+        side = torch.cuda.ExternalStream(stream, device) if isinstance(stream, int) else stream
         with torch.cuda.stream(side):
-            ws = torch.empty(floats, dtype=torch.float32, device=xs.device)
+            ws = torch.empty(floats, dtype=torch.float32, device=device)
     if rec is not None:
         rec.keep.append(ws)
     return ws
@@ -926,16 +923,16 @@ def tp_lora_all_to_sharded(x, a, b, plan, y, scales=None, out=None, stream=None)
     """Adapters beside a column-parallel projection: out[r] = y[r] + scale (x A^T) B[r]^T
     by each token's adapter; x (T, K), a (n, R, K), b per rank (n, O / N, R), y
     per rank (T, O / N).  Written to y unless ``out`` is given; returns that."""
-    return _call("tp_lora_all_to_sharded", (_native or _marshaller()).lora, True, x, a, b, plan,
-                 _lora_workspace(x, a, stream), y, scales, out, stream)
+    return _call("tp_lora_all_to_sharded", (_native or _marshaller()).lora, True, x, a, b, plan, _lora_workspace, y,
+                 scales, out, stream)
 
 
 def tp_lora_sharded_to_all(x, a, b, plan, y, scales=None, out=None, stream=None):
     """Adapters beside a row-parallel projection: out = y + scale (sum_r x[r] A[r]^T) B^T
     by each token's adapter; x per rank (T, K / N), a per rank (n, R, K / N), b
     (n, O, R), y (T, O).  Written to y unless ``out`` is given; returns that."""
-    return _call("tp_lora_sharded_to_all", (_native or _marshaller()).lora, False, x, a, b, plan,
-                 _lora_workspace(x, a, stream), y, scales, out, stream)
+    return _call("tp_lora_sharded_to_all", (_native or _marshaller()).lora, False, x, a, b, plan, _lora_workspace, y,
+                 scales, out, stream)
 
 
 def tp_verify(logits, drafts, cu_rows, u, draft_probs=None, temperature=None, top_k=None, top_p=None, min_p=None,

@@ -38,76 +38,65 @@ __device__ __forceinline__ uint2 load4(const uint16_t *row, int k, int K) {
 }
 
 // A lane's eight outputs of a row, at `col` and, float32, the second four 16 columns on:
-// float32 bits, or 16-bit pairs in the first four.  Columns of `cols` and more are not there.
+// float32 bits, or 16-bit pairs.  Columns of `cols` and more are not there.
+template <bool OUT32>
 struct Out8 {
-  uint32_t v[8];
+  uint32_t v[OUT32 ? 8 : 4];
 };
-template <bool VEC>
-__device__ __forceinline__ void load_out(Out8 &o, const void *base, int64_t row, int col, int cols, int dt) {
-  if (dt == TP_F32) {
-    const uint32_t *p = static_cast<const uint32_t *>(base) + row + col;
+template <bool VEC, bool OUT32>
+__device__ __forceinline__ void load_out(Out8<OUT32> &o, const void *base, int64_t row, int col, int cols) {
+  constexpr int kEach = OUT32 ? 4 : 8;  // columns of 16 bytes
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if (VEC) {
-        if (col + i * 16 >= cols) continue;
-        const uint4 a = *reinterpret_cast<const uint4 *>(p + i * 16);
-        o.v[4 * i] = a.x, o.v[4 * i + 1] = a.y, o.v[4 * i + 2] = a.z, o.v[4 * i + 3] = a.w;
-      } else {
+  for (int i = 0; i < 8 / kEach; ++i) {
+    const int at = col + i * 16;
+    if (VEC) {
+      if (at >= cols) continue;
+      const uint4 a = *reinterpret_cast<const uint4 *>(static_cast<const char *>(base) + (row + at) * (16 / kEach));
+      o.v[4 * i] = a.x, o.v[4 * i + 1] = a.y, o.v[4 * i + 2] = a.z, o.v[4 * i + 3] = a.w;
+    } else if constexpr (OUT32) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) o.v[4 * i + k] = col + i * 16 + k < cols ? p[i * 16 + k] : 0;
-      }
+      for (int k = 0; k < 4; ++k) o.v[4 * i + k] = at + k < cols ? static_cast<const uint32_t *>(base)[row + at + k] : 0;
+    } else {
+      const uint16_t *p = static_cast<const uint16_t *>(base) + row + at;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        o.v[k] = (at + 2 * k < cols ? p[2 * k] : 0) | (at + 2 * k + 1 < cols ? p[2 * k + 1] : 0) << 16;
     }
-  } else if (VEC) {
-    if (col >= cols) return;
-    const uint4 a = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(base) + row + col);
-    o.v[0] = a.x, o.v[1] = a.y, o.v[2] = a.z, o.v[3] = a.w;
-  } else {
-    const uint16_t *p = static_cast<const uint16_t *>(base) + row + col;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      o.v[i] = (col + 2 * i < cols ? p[2 * i] : 0) | (col + 2 * i + 1 < cols ? p[2 * i + 1] : 0) << 16;
   }
 }
-template <bool VEC>
-__device__ __forceinline__ void store_out(const Out8 &o, void *base, int64_t row, int col, int cols, int dt) {
-  if (dt == TP_F32) {
-    uint32_t *p = static_cast<uint32_t *>(base) + row + col;
+template <bool VEC, bool OUT32>
+__device__ __forceinline__ void store_out(const Out8<OUT32> &o, void *base, int64_t row, int col, int cols) {
+  constexpr int kEach = OUT32 ? 4 : 8;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if (VEC) {
-        if (col + i * 16 < cols)
-          *reinterpret_cast<uint4 *>(p + i * 16) = make_uint4(o.v[4 * i], o.v[4 * i + 1], o.v[4 * i + 2], o.v[4 * i + 3]);
-      } else {
+  for (int i = 0; i < 8 / kEach; ++i) {
+    const int at = col + i * 16;
+    if (VEC) {
+      if (at < cols)
+        *reinterpret_cast<uint4 *>(static_cast<char *>(base) + (row + at) * (16 / kEach)) =
+            make_uint4(o.v[4 * i], o.v[4 * i + 1], o.v[4 * i + 2], o.v[4 * i + 3]);
+    } else if constexpr (OUT32) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (col + i * 16 + k < cols) p[i * 16 + k] = o.v[4 * i + k];
-      }
+      for (int k = 0; k < 4; ++k)
+        if (at + k < cols) static_cast<uint32_t *>(base)[row + at + k] = o.v[4 * i + k];
+    } else {
+      uint16_t *p = static_cast<uint16_t *>(base) + row + at;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (at + k < cols) p[k] = (uint16_t)(o.v[k / 2] >> (k % 2 * 16));
     }
-  } else if (VEC) {
-    if (col < cols)
-      *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(base) + row + col) = make_uint4(o.v[0], o.v[1], o.v[2], o.v[3]);
-  } else {
-    uint16_t *p = static_cast<uint16_t *>(base) + row + col;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (col + i < cols) p[i] = (uint16_t)(o.v[i / 2] >> (i % 2 * 16));
   }
 }
-__device__ __forceinline__ void add_out(Out8 &o, const float (&d)[8], int dt) {
-  if (dt == TP_F32) {
+template <bool OUT32>
+__device__ __forceinline__ void add_out(Out8<OUT32> &o, const float (&d)[8], bool bf16) {
+  if constexpr (OUT32) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) o.v[i] = __float_as_uint(__uint_as_float(o.v[i]) + d[i]);
-  } else if (dt == TP_BF16) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 y = Half2<__nv_bfloat16>::unpack(o.v[i]);
-      o.v[i] = Half2<__nv_bfloat16>::pack(y.x + d[2 * i], y.y + d[2 * i + 1]);
-    }
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 y = Half2<__half>::unpack(o.v[i]);
-      o.v[i] = Half2<__half>::pack(y.x + d[2 * i], y.y + d[2 * i + 1]);
+      const float2 y = bf16 ? Half2<__nv_bfloat16>::unpack(o.v[i]) : Half2<__half>::unpack(o.v[i]);
+      const float a = y.x + d[2 * i], b = y.y + d[2 * i + 1];
+      o.v[i] = bf16 ? Half2<__nv_bfloat16>::pack(a, b) : Half2<__half>::pack(a, b);
     }
   }
 }
@@ -123,9 +112,11 @@ struct LoraShared {
   float unscale[16];  // the power of two that a row's products are multiplied by
 };
 
-template <typename T, int RP, bool VEC>
-__global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : RP == 64 ? 2 : 3)
-    lora_kernel(const __grid_constant__ LoraArgs a, int C, int S) {
+constexpr int C = 8;  // CTAs of a cluster (4: 16 -> 22 us for 64 tokens of 50 adapters, R = 16, 4096 x 12288)
+
+template <typename T, int RP, bool VEC, bool OUT32>
+__global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : RP == 16 ? 3 : 2)
+    lora_kernel(const __grid_constant__ LoraArgs a, int S) {
   typedef LoraShared<T, RP> Shared;
   constexpr int NT = RP / 8, KS = RP / 16, kStride = Shared::kStride, kTerms = Shared::kTerms;
   extern __shared__ __align__(16) uint8_t smem[];
@@ -137,7 +128,7 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : RP == 64 ? 2 : 3
   const int blk0 = (cluster % S * C + rank) * kWarps + warp;
   const int u0 = rank * kWarps + warp;
   const int used = terms<T>(a.out_dt);
-  const bool out32 = a.out_dt == TP_F32;
+  const bool out_bf16 = a.out_dt == TP_BF16;
   griddep_launch_dependents();
   griddep_wait();
   const int groups = groups_of(a);
@@ -155,15 +146,15 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : RP == 64 ? 2 : 3
     // ---- a block's rows of B, and the old outputs
     struct Block {
       uint32_t w[4][KS][2];
-      Out8 y0, y1;
+      Out8<OUT32> y0, y1;
     };
     auto fetch = [&](const Cursor &c, Block &o) {
-      const int col = c.i * 32 + lane_col(out32, 0, q);
+      const int col = c.i * 32 + lane_col(OUT32, 0, q);
       if (id >= 0) {
         const uint16_t *b = static_cast<const uint16_t *>(a.b[c.p]) + ((int64_t)id * O + c.i * 32) * a.R;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int r = b_row(out32, j, g);
+          const int r = b_row(OUT32, j, g);
           const uint16_t *row = b + r * a.R;
           const int R = c.i * 32 + r < O ? a.R : 0;
           if (RP == 16) {
@@ -178,9 +169,11 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : RP == 64 ? 2 : 3
           }
         }
       }
-      if (t0 >= 0) load_out<VEC>(o.y0, a.y[c.p], t0 * a.ldy, col, O, a.out_dt);
-      if (t1 >= 0) load_out<VEC>(o.y1, a.y[c.p], t1 * a.ldy, col, O, a.out_dt);
+      if (t0 >= 0) load_out<VEC>(o.y0, a.y[c.p], t0 * a.ldy, col, O);
+      if (t1 >= 0) load_out<VEC>(o.y1, a.y[c.p], t1 * a.ldy, col, O);
     };
+    // (One block ahead: with two or three, registers for as many CTAs an SM are lacking, which
+    // costs more: 13.7 us for 64 tokens of 50 adapters against 15.4 and 21.)
     Block now;
     Cursor c(blk0, per_o);
 
@@ -211,7 +204,7 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : RP == 64 ? 2 : 3
         cu.next(C * kWarps, per_k);
       }
       if (blk0 < blocks) fetch(c, now);  // under the sums' exchange
-      if (read && C > 1) cluster_wait();
+      if (read) cluster_wait();
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         float *to = &sh.part[warp][g][j * 8 + q * 2];
@@ -227,19 +220,20 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : RP == 64 ? 2 : 3
         for (int j = 1; j < kWarps; ++j) sum = add4(sum, *reinterpret_cast<const float4 *>(&sh.part[j][row][col]));
         *reinterpret_cast<float4 *>(&sh.part[0][row][col]) = sum;
       }
-      if (C > 1) cluster_sync_all(); else __syncthreads();
+      cluster_sync_all();
       const float scale = a.scales ? __ldg(a.scales + id) : 1.0f;
       for (int i = tid; i < 4 * RP; i += kLoraThreads) {
         const int row = i / (RP / 4), col = i % (RP / 4) * 4;
         const uint32_t mine = smem_u32(&sh.part[0][row][col]);
-        float4 sum = make_float4(0, 0, 0, 0);
-        for (int r = 0; r < C; ++r)
-          sum = add4(sum, C > 1 ? ld_cluster_f4(mapa_shared(mine, r))
-                                : *reinterpret_cast<const float4 *>(&sh.part[0][row][col]));
+        float4 of[C], sum = make_float4(0, 0, 0, 0);  // all asked for before the first is added
+#pragma unroll
+        for (int r = 0; r < C; ++r) of[r] = ld_cluster_f4(mapa_shared(mine, r));
+#pragma unroll
+        for (int r = 0; r < C; ++r) sum = add4(sum, of[r]);
         *reinterpret_cast<float4 *>(&sh.h[row][col]) =
             make_float4(sum.x * scale, sum.y * scale, sum.z * scale, sum.w * scale);
       }
-      if (C > 1) cluster_arrive();
+      cluster_arrive();
       read = true;
       __syncthreads();
       if (!Half2<T>::kBf16) {
@@ -261,7 +255,7 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : RP == 64 ? 2 : 3
     const float f0 = Half2<T>::kBf16 || id < 0 ? 1.0f : sh.unscale[g];
     const float f1 = Half2<T>::kBf16 || id < 0 ? 1.0f : sh.unscale[g + 8];
     for (int blk = blk0; blk < blocks; blk += step) {
-      const int p = c.p, col = c.i * 32 + lane_col(out32, 0, q);
+      const int p = c.p, col = c.i * 32 + lane_col(OUT32, 0, q);
       c.next(step, per_o);
       if (id >= 0) {
         float d[4][4];
@@ -283,16 +277,16 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : RP == 64 ? 2 : 3
           add0[2 * j] = d[j][0] * f0, add0[2 * j + 1] = d[j][1] * f0;
           add1[2 * j] = d[j][2] * f1, add1[2 * j + 1] = d[j][3] * f1;
         }
-        add_out(now.y0, add0, a.out_dt);
-        add_out(now.y1, add1, a.out_dt);
+        add_out(now.y0, add0, out_bf16);
+        add_out(now.y1, add1, out_bf16);
       }
-      const Out8 y0 = now.y0, y1 = now.y1;
+      const Out8<OUT32> y0 = now.y0, y1 = now.y1;
       if (blk + step < blocks) fetch(c, now);
-      if (t0 >= 0) store_out<VEC>(y0, a.out[p], t0 * a.ldo, col, O, a.out_dt);
-      if (t1 >= 0) store_out<VEC>(y1, a.out[p], t1 * a.ldo, col, O, a.out_dt);
+      if (t0 >= 0) store_out<VEC>(y0, a.out[p], t0 * a.ldo, col, O);
+      if (t1 >= 0) store_out<VEC>(y1, a.out[p], t1 * a.ldo, col, O);
     }
   }
-  if (read && C > 1) cluster_wait();  // no CTA leaves while another may still read its shared memory
+  if (read) cluster_wait();  // no CTA leaves while another may still read its shared memory
 }
 
 // The same on the CUDA cores, a block a token: the cross-check.
@@ -355,13 +349,13 @@ bool all_aligned(const void *const *p, int n, int to) {
   return true;
 }
 
-template <typename T, int RP, bool VEC>
+template <typename T, int RP, bool VEC, bool OUT32>
 int launch(const LoraArgs &a, cudaStream_t s) {
-  auto kern = lora_kernel<T, RP, VEC>;
+  auto kern = lora_kernel<T, RP, VEC, OUT32>;
   const size_t smem = sizeof(LoraShared<T, RP>);
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = cudaSuccess;
+  if (smem > 48 * 1024) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return cuda_error(e, "adapter launch");
-  const int C = 8;
   int64_t tiles = a.T / 16 + a.most;  // at most
   if (tiles > (1 << 20)) tiles = 1 << 20;
   // few tiles: several clusters for one, each with h for itself and a share of the columns
@@ -381,10 +375,15 @@ int launch(const LoraArgs &a, cudaStream_t s) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, kern, a, C, S);
+  e = cudaLaunchKernelEx(&cfg, kern, a, S);
   if (e != cudaSuccess) return cuda_error(e, "adapter launch");
   note_launch();
   return TP_OK;
+}
+
+template <typename T, int RP, bool VEC>
+int launch(const LoraArgs &a, cudaStream_t s) {
+  return a.out_dt == TP_F32 ? launch<T, RP, VEC, true>(a, s) : launch<T, RP, VEC, false>(a, s);
 }
 
 template <typename T, bool VEC>

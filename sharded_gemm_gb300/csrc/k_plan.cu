@@ -313,7 +313,8 @@ static_assert(kMostPlanSmem <= 224 * 1024 && kMostGroupSmem <= 224 * 1024, "the 
 template <typename K, typename Args>
 int launch_one(K kern, const Args &a, int64_t grid, int block, size_t smem, size_t most, cudaStream_t s) {
   // the limit belongs to the function, not to this call: always the largest
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+  cudaError_t e = cudaSuccess;
+  if (smem > 48 * 1024) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
   if (e == cudaSuccess) e = launch_pdl(kern, dim3((unsigned)grid), dim3(block), smem, s, a);
   if (e != cudaSuccess) return cuda_error(e, "plan launch");
   note_launch();

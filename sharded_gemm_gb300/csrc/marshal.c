@@ -633,7 +633,8 @@ static int one_of(PyObject *t, Ranks *o, int dim, const char *name) {
   return rc;
 }
 
-/* lora(fn, column, x, a, b, plan, workspace, y, scales, out, stream) -> out */
+/* lora(fn, column, x, a, b, plan, workspace, y, scales, out, stream) -> out; workspace(T, R, device, stream) gives a
+ * step of many tokens its memory */
 static PyObject *m_lora(PyObject *self, PyObject *const *a, Py_ssize_t na) {
   if (na != 11) return PyErr_Format(PyExc_TypeError, "lora takes 11 arguments");
   void *fn = PyLong_AsVoidPtr(a[0]);
@@ -668,12 +669,19 @@ static PyObject *m_lora(PyObject *self, PyObject *const *a, Py_ssize_t na) {
     return NULL;
   }
   if (length_of(a[5], &size, &dev, "plan") || param_of(a[5], &plan, t_i32, size, x.dev, "plan") ||
-      param_of(a[8], &scales, t_f32, n, x.dev, "scales") || stream_of(a[10], x.dev, &stream) ||
-      (a[6] != Py_None &&
-       (length_of(a[6], &floats, &dev, "workspace") || param_of(a[6], &room, t_f32, floats, x.dev, "workspace"))))
+      param_of(a[8], &scales, t_f32, n, x.dev, "scales") || stream_of(a[10], x.dev, &stream))
     return NULL;
-  PyObject *keep = Py_NewRef(to);
-  if (!fn) {
+  PyObject *keep = Py_NewRef(to), *mem = NULL;
+  if (T > 1024) {
+    mem = PyObject_CallFunction(a[6], "LLlO", T, R, x.dev, a[10]);
+    if (!mem || length_of(mem, &floats, &dev, "workspace") || param_of(mem, &room, t_f32, floats, x.dev, "workspace")) {
+      Py_XDECREF(mem);
+      Py_DECREF(keep);
+      return NULL;
+    }
+  }
+  if (!fn) {  // whoever made the memory keeps it
+    Py_XDECREF(mem);
     if (column)
       return Py_BuildValue("N(iKLLLKNLiLKKLKiNLNLiK)", keep, y.n, x.ptr[0], T, K, ldx, A_.ptr[0], bytes_of(&B_), n, (int)R,
                            O * y.n, scales, plan, size, room, x.dt, bytes_of(&y), ldy, bytes_of(&out), ldo, y.dt, stream);
@@ -691,6 +699,7 @@ static PyObject *m_lora(PyObject *self, PyObject *const *a, Py_ssize_t na) {
                                                    P(scales), P(plan), size, P(room), (tp_dtype)x.dt, P(y.ptr[0]), ldy,
                                                    P(out.ptr[0]), ldo, (tp_dtype)y.dt, P(stream));
   Py_END_ALLOW_THREADS;
+  Py_XDECREF(mem);
   return answer(keep, rc);
 }
 
