@@ -12,8 +12,9 @@ import numpy as np
 import torch
 
 from . import (tp_all_to_sharded, tp_all_to_sharded_dx, tp_bias_grad, tp_gated_all_to_sharded,
-               tp_mx_all_to_sharded, tp_mx_quantize, tp_mx_sharded_to_all, tp_paged_decode, tp_paged_prefill,
-               tp_qkv_append, tp_sample,
+               tp_lora_all_to_sharded, tp_lora_plan, tp_lora_sharded_to_all,
+               tp_mx_all_to_sharded, tp_mx_quantize, tp_mx_sharded_to_all, tp_paged_decode, tp_paged_plan, tp_paged_prefill,
+               tp_qkv_append, tp_sample, tp_verify,
                tp_sharded_dw, tp_sharded_to_all_dx, tp_gathered_to_sharded, tp_q4_all_to_sharded,
                tp_q4_quantize,
                tp_q4_sharded_to_all, tp_shard_weight, tp_sharded_to_all, tp_sharded_to_sharded, tp_summa)
@@ -310,6 +311,93 @@ class PagedServing:
         tokens, self.logprobs = tp_sample(logits, u, temperature, top_k, top_p, min_p)
         self.lens, self.logits = lens, logits
         return tokens, y
+
+
+class SharedServing:
+    """The attention block and head of ``PagedServing`` for sequences that come and go over one pool of pages, with
+    low-rank adapters of their own and drafted tokens.  Lengths, pages and what was refused of the drafts stay on
+    the GPU: a step reads nothing back, and may be captured into a graph once it has run on the capturing stream.
+
+    ``cfg`` is a ``synth.qkv`` workload's (its x is not used), ``batch`` the sequences served at once, ``pages`` the
+    pool, ``capacity`` the positions of a sequence at most, ``rows`` the rows of every step.  ``adapters``: None, or a
+    dict with the adapters of both projections, each full as for one rank: qkv_a (n, R, D), qkv_b (n, 3 D, R), o_a
+    (n, R, D), o_b (n, D, R), and scales (n) or None."""
+
+    def __init__(self, cfg: dict, heads: int, batch: int, pages: int, capacity: int, rows: int, page: int = 64,
+                 rope_base: float = 10000.0, adapters=None, device="cuda"):
+        self.N = N = cfg["N"]
+        D, self.V = cfg["D"], cfg["V"]
+        self.page, self.batch, self.rows, self.head = page, batch, rows, D // heads
+        self.w_qkv = tp_shard_weight(to_device(cfg["w_qkv"], "bf16", device), 0, 3, N)
+        self.b_qkv = tp_shard_weight(to_device(cfg["b_qkv"], "f32", device), 0, 3, N)
+        self.w_o = tp_shard_weight(to_device(cfg["w_o"], "bf16", device), -1, 1, N)
+        self.b_o = to_device(cfg["b_o"], "f32", device)
+        self.w_lm = tp_shard_weight(to_device(cfg["w_lm"], "bf16", device), 0, 1, N)
+        self.k_cache = torch.empty((N, pages, heads // N, page, self.head), dtype=torch.bfloat16, device=device)
+        self.v_cache = torch.empty_like(self.k_cache)
+        angle = torch.arange(capacity, dtype=torch.float64)[:, None] * \
+            rope_base ** (-torch.arange(self.head // 2, dtype=torch.float64) * 2 / self.head)
+        self.rope = torch.cat([angle.cos(), angle.sin()], 1).float().to(device)
+
+        def ints(*shape, fill=0):
+            return torch.full(shape, fill, dtype=torch.int32, device=device)
+        self.block_table = ints(batch, -(-capacity // page), fill=-1)
+        self.free_pages = torch.arange(pages, dtype=torch.int32, device=device)
+        # a step's plan is written over the lengths, the pages held and the pool's size that it began with
+        self.plan = [ints(batch), ints(batch), ints(1, fill=pages), ints(1), ints(batch + 1), ints(rows),
+                     torch.zeros(rows, dtype=torch.int64, device=device)]
+        self.rejected = ints(batch)
+        self.adapters = None
+        if adapters is not None:
+            self.adapters = dict(adapters)
+            # the ranks' slices, as of the projections: outputs of qkv by thirds, inputs of W_o
+            third = adapters["qkv_b"].unflatten(1, (3, N, D // N))
+            self.adapters["qkv_b"] = third.permute(2, 0, 1, 3, 4).flatten(2, 3).contiguous()
+            self.adapters["o_a"] = adapters["o_a"].unflatten(2, (N, D // N)).permute(2, 0, 1, 3).contiguous()
+            self.groups = ints(4 + 4 * min(rows, len(adapters["o_b"]) + 1) + rows)
+
+    def attend(self, x, counts, adapter_ids=None):
+        """x (rows, D) bf16: counts[b] (int32 (batch), on the GPU) new tokens of each sequence in turn, then rows
+        that are not used; below 0: the sequence has ended.  Returns y (rows, D) float32."""
+        plan = tp_paged_plan(counts, self.plan[0], self.plan[1], self.block_table, self.free_pages, self.plan[2],
+                             self.page, self.rows, rejected=self.rejected, out=self.plan)
+        self.rejected.zero_()
+        qkv = tp_all_to_sharded(x, self.w_qkv, self.b_qkv)
+        lora = self.adapters if adapter_ids is not None else None
+        if lora:
+            tp_lora_plan(adapter_ids, self.rows, len(lora["o_b"]), cu_seqlens=plan.cu_seqlens, out=self.groups)
+            tp_lora_all_to_sharded(x, lora["qkv_a"], lora["qkv_b"], self.groups, qkv, scales=lora["scales"])
+        q = tp_qkv_append(qkv, self.k_cache, self.v_cache, plan.slots, positions=plan.positions, rope=self.rope)
+        o = tp_paged_prefill(q, self.k_cache, self.v_cache, self.block_table, plan.cu_seqlens, plan.seq_lens)
+        y = tp_sharded_to_all(list(o), self.w_o, self.b_o)
+        if lora:
+            tp_lora_sharded_to_all(o, lora["o_a"], lora["o_b"], self.groups, y, scales=lora["scales"])
+        return y
+
+    def head_of(self, y):
+        """Logits (T, V) float32 of rows (T, D) of the attention block's output."""
+        T, Vn = y.shape[0], self.V // self.N
+        self.logits = torch.empty((T, self.V), dtype=torch.float32, device=y.device)
+        tp_all_to_sharded(y.to(torch.bfloat16), self.w_lm, None,
+                          out=[self.logits[:, r * Vn:(r + 1) * Vn] for r in range(self.N)])
+        return self.logits
+
+    def step(self, x, counts, u, adapter_ids=None, **settings):
+        """Prompts or single tokens: a token of each sequence drawn behind its last row (of one without rows: not
+        meant).  u (batch).  Returns (tokens (batch), y)."""
+        y = self.attend(x, counts, adapter_ids)
+        tokens, self.logprobs = tp_sample(self.head_of(y[(self.plan[4][1:] - 1).clamp(min=0)]), u, **settings)
+        return tokens, y
+
+    def verify(self, x, counts, drafts, u, draft_probs=None, adapter_ids=None, **settings):
+        """Rows of drafts: each sequence's are its last token and the drafted ones behind it, drafts[i] (int64 (rows))
+        the token of row i + 1, u (rows).  The positions of refused drafts no longer count from the next step on.
+        Returns (tokens (rows), -1 behind each sequence's drawn one, accepted (batch), y)."""
+        y = self.attend(x, counts, adapter_ids)
+        tokens = torch.full((self.rows,), -1, dtype=torch.int64, device=x.device)  # rows of no sequence stay so
+        _, self.logprobs, accepted, _ = tp_verify(self.head_of(y), drafts, self.plan[4], u, draft_probs=draft_probs,
+                                                  tokens=tokens, rejected=self.rejected, **settings)
+        return tokens, accepted, y
 
 
 class Q4Pair:

@@ -14,6 +14,9 @@ import torch
 
 import sharded_gemm_gb300 as tp
 from sharded_gemm_gb300 import build as tpbuild
+from sharded_gemm_gb300 import synth
+from sharded_gemm_gb300.workloads import PagedServing, SharedServing
+from gpu_util import check_close
 
 pytestmark = pytest.mark.gpu
 
@@ -99,12 +102,14 @@ def plan_ref(counts, rejected, lens, owned, table, pool, free, page, T):
 def run_plan(counts, rejected, lens, owned, table, pool, free, page, T, in_place=False, stream=None):
     t = i32(table)
     args = [i32(counts), i32(lens), i32(owned), t, i32(pool), i32([free])]
+    less = None if rejected is None else i32(rejected)
+    torch.cuda.synchronize()
     out = None
     if in_place:
         out = [args[1], args[2], args[5], torch.empty(1, dtype=torch.int32, device="cuda"),
                torch.empty(len(counts) + 1, dtype=torch.int32, device="cuda"),
                torch.empty(T, dtype=torch.int32, device="cuda"), torch.empty(T, dtype=torch.int64, device="cuda")]
-    p = tp.tp_paged_plan(*args, page, T, rejected=None if rejected is None else i32(rejected), out=out, stream=stream)
+    p = tp.tp_paged_plan(*args, page, T, rejected=less, out=out, stream=stream)
     torch.cuda.synchronize()
     return (p.seq_lens.tolist(), p.owned.tolist(), int(p.free_count), int(p.missing), p.cu_seqlens.tolist(),
             p.positions.tolist(), p.slots.tolist(), t.tolist(), args[4].tolist())
@@ -682,3 +687,310 @@ def test_verified_tokens_follow_the_target(with_q):
     assert np.all(np.abs(seen - p) <= 5 * np.sqrt(p * (1 - p) / B))
     rate = np.minimum(p, draft.double().cpu().numpy()).sum() if with_q else p[4]
     assert abs(float(accepted.double().mean()) - rate) <= 5 * np.sqrt(rate * (1 - rate) / B)
+
+
+# ------------------------------------------------------------------ all of them together
+def embeddings(V, D, seed=11):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn((V, D), generator=g, device="cuda").to(BF16)
+
+
+def make_adapters(n, R, D, seed=5, size=0.05):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+
+    def normal(*shape):
+        return (torch.randn(shape, generator=g, device="cuda") * size).to(BF16)
+    return dict(qkv_a=normal(n, R, D), qkv_b=normal(n, 3 * D, R), o_a=normal(n, R, D), o_b=normal(n, D, R),
+                scales=torch.rand(n, generator=g, device="cuda") + 0.5)
+
+
+def padded(rows, x):
+    out = torch.full((rows, x.shape[1]), float("nan"), dtype=BF16, device="cuda")
+    out[:len(x)] = x
+    return out
+
+
+@pytest.mark.parametrize("N", [1, 2])
+def test_shared_serving_is_paged_serving(N):
+    """Without adapters and drafts the pool changes where rows lie and nothing else: the same bytes of steps whose
+    rows are all used (the linears choose their kernels by the rows), and nearly the same of padded ones."""
+    cfg = synth.qkv(seed=6, T=1, D=256, V=512, N=N)
+    table = embeddings(512, 256)
+    a, a2 = (PagedServing(cfg, heads=4, batch=3, capacity=96, page=16) for _ in range(2))
+    b = SharedServing(cfg, heads=4, batch=3, pages=18, capacity=96, rows=40, page=16)
+    c = SharedServing(cfg, heads=4, batch=3, pages=18, capacity=96, rows=40, page=16)
+    ids = torch.randint(0, 512, (40,), generator=torch.Generator().manual_seed(1)).cuda()
+    u = torch.tensor([0.2, 0.5, 0.9], device="cuda")
+    for counts in ([30, 3, 7], [1, 38, 1], [5, 5, 30]):
+        t0, y0 = a.step(table[ids], counts, u)
+        t1, y1 = b.step(table[ids], i32(counts), u)
+        assert torch.equal(y0, y1) and torch.equal(t0, t1)
+    assert b.plan[0].tolist() == a.lens and int(b.plan[3]) == 0
+    for counts in ([21, 5, 1], [2, 1, 9], [1, 1, 1]):
+        T = sum(counts)
+        _, y0 = a2.step(table[ids[:T]], counts, u)
+        _, y1 = c.step(padded(40, table[ids[:T]]), i32(counts), u)
+        check_close(y1[:T].cpu().numpy(), y0.cpu().numpy())
+    # a sequence ends, another takes its place and its pages
+    free, held = int(b.plan[2]), int(b.plan[1][0])
+    b.step(padded(40, table[ids[:2]]), i32([-1, 1, 1]), u)
+    assert int(b.plan[2]) == free + held
+    _, y = b.step(table[ids], i32([38, 1, 1]), u)
+    _, alone = PagedServing(cfg, heads=4, batch=1, capacity=96, page=16).step(table[ids[:38]], [38], u[:1])
+    check_close(y[:38].cpu().numpy(), alone.cpu().numpy())
+    assert status() == 0
+
+
+def test_shared_serving_with_adapters_against_merged_weights():
+    """An adapter beside a projection is the projection with the adapter's product added to its weight."""
+    D, V, N, R, n = 256, 512, 2, 16, 3
+    cfg = synth.qkv(seed=6, T=1, D=D, V=V, N=N)
+    table, lora = embeddings(V, D), make_adapters(n, R, D)
+    ids = torch.randint(0, V, (60,), generator=torch.Generator().manual_seed(1)).cuda()
+    serve = SharedServing(cfg, heads=4, batch=3, pages=20, capacity=96, rows=64, page=16, adapters=lora)
+    u = torch.full((3,), 0.5, device="cuda")
+    adapter_ids = i32([2, -1, 0])
+    _, y = serve.step(padded(64, table[ids[:50]]), i32([20, 13, 17]), u, adapter_ids=adapter_ids)
+    start = 0
+    for which, count in ((2, 20), (-1, 13), (0, 17)):
+        merged = dict(cfg)
+        if which >= 0:
+            for w, a, b in (("w_qkv", "qkv_a", "qkv_b"), ("w_o", "o_a", "o_b")):
+                full = torch.from_numpy(np.ascontiguousarray(cfg[w]).view(np.int16)).view(BF16).cuda().double()
+                full = full + float(lora["scales"][which]) * lora[b][which].double() @ lora[a][which].double()
+                merged[w] = full.to(BF16).cpu().view(torch.int16).numpy().view(np.uint16)
+        alone = PagedServing(merged, heads=4, batch=1, capacity=96, page=16)
+        _, ref = alone.step(table[ids[start:start + count]], [count], u[:1])
+        got = y[start:start + count]
+        # the merged weight and both sides' intermediates are rounded to bfloat16: a few of its steps
+        torch.testing.assert_close(got, ref, rtol=0, atol=2 ** -5 * float(ref.abs().max()))
+        err = float((got - ref).norm() / ref.norm())
+        assert err <= 2 ** -6, err
+        start += count
+    assert status() == 0
+
+
+def greedy_loop(serve, table, prompts, steps, guess, adapter_ids):
+    """Greedy decoding with drafts guess(b, position): the tokens of each sequence and the steps that it took."""
+    B, rows = serve.batch, serve.rows
+    done = [list(p) for p in prompts]
+    settings = dict(temperature=torch.zeros(B, device="cuda"))
+    ids = torch.tensor([t for p in prompts for t in p], device="cuda")
+    tokens, _ = serve.step(padded(rows, table[ids]), i32([len(p) for p in prompts]), torch.zeros(B, device="cuda"),
+                           adapter_ids=adapter_ids, **settings)
+    for b, t in enumerate(tokens.tolist()):
+        done[b].append(t)
+    for _ in range(steps):
+        counts, fed, drafts = [], [], []
+        for b in range(B):
+            g = guess(b, len(done[b]))
+            counts.append(1 + len(g))
+            fed += [done[b][-1], *g]
+            drafts += [*g, -1]
+        d = torch.full((rows,), -1, dtype=torch.int64, device="cuda")
+        d[:len(drafts)] = torch.tensor(drafts, device="cuda")
+        got, accepted, _ = serve.verify(padded(rows, table[torch.tensor(fed, device="cuda")]), i32(counts), d,
+                                        torch.zeros(rows, device="cuda"), adapter_ids=adapter_ids, **settings)
+        best, at = serve.logits.argmax(1).tolist(), 0
+        for b in range(B):
+            n = int(accepted[b]) + 1
+            emitted = got[at:at + n].tolist()
+            assert emitted == best[at:at + n]  # greedy: each row's largest logit
+            assert got[at + n:at + counts[b]].tolist() == [-1] * (counts[b] - n)
+            assert int(serve.rejected[b]) == counts[b] - n
+            assert drafts[at:at + n - 1] == emitted[:-1]
+            done[b] += emitted
+            at += counts[b]
+    return done
+
+
+def test_drafts_change_how_fast_tokens_come_and_not_which():
+    D, V, N = 256, 512, 2
+    cfg = synth.qkv(seed=9, T=1, D=D, V=V, N=N)
+    table, lora = embeddings(V, D), make_adapters(2, 8, D)
+    prompts = [[3, 77, 12], [500], [9, 9, 8, 7, 6]]
+    ids = i32([1, -1, 0])
+
+    def fresh():
+        return SharedServing(cfg, heads=4, batch=3, pages=30, capacity=128, rows=32, page=16, adapters=lora)
+    plain = greedy_loop(fresh(), table, prompts, 24, lambda b, n: [], ids)
+    rng = np.random.default_rng(2)
+
+    def guess(b, n):  # right for a while, then wrong
+        known = plain[b][n:n + int(rng.integers(0, 5))]
+        return [t if rng.random() < 0.7 else int(rng.integers(0, V)) for t in known]
+    serve = fresh()
+    drafted_ = greedy_loop(serve, table, prompts, 10, guess, ids)
+    for a, b, p in zip(plain, drafted_, prompts):
+        n = min(len(a), len(b))
+        assert a[:n] == b[:n]
+    assert sum(map(len, drafted_)) > sum(map(len, prompts)) + 3 + 3 * 10  # some drafts were right
+    assert status() == 0
+
+
+def test_shared_serving_step_captured_and_replayed():
+    """A step with adapters and drafts as a graph: replays on new inputs are the eager steps, byte for byte."""
+    D, V, N, B, rows = 256, 512, 2, 3, 24
+    cfg = synth.qkv(seed=9, T=1, D=D, V=V, N=N)
+    table, lora = embeddings(V, D), make_adapters(2, 8, D)
+    g = torch.Generator().manual_seed(4)
+
+    def inputs():
+        counts = torch.randint(1, 7, (B,), generator=g).to(torch.int32)
+        toks = torch.randint(0, V, (rows,), generator=g)
+        return (table[toks.cuda()], counts.cuda(), torch.randint(0, V, (rows,), generator=g).cuda(),
+                torch.rand(rows, generator=g).cuda(), i32(torch.randint(-1, 2, (B,), generator=g).numpy()))
+    steps = [inputs() for _ in range(6)]
+
+    def fresh():
+        return SharedServing(cfg, heads=4, batch=B, pages=20, capacity=96, rows=rows, page=16, adapters=lora)
+    eager = fresh()
+    want = []
+    for x, counts, d, u, ids in steps:
+        out = eager.verify(x, counts, d, u, adapter_ids=ids)
+        want.append([t.clone() for t in out] + [t.clone() for t in eager.plan] + [eager.rejected.clone()])
+    serve = fresh()
+    static = [t.clone() for t in steps[0]]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        serve.verify(*static[:4], adapter_ids=static[4])  # what the library allocates, it allocates now
+    torch.cuda.current_stream().wait_stream(side)
+    for to, t in zip([*serve.plan, serve.rejected, serve.block_table, serve.free_pages],
+                     [*fresh().plan, fresh().rejected, fresh().block_table, fresh().free_pages]):
+        to.copy_(t)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        out = serve.verify(*static[:4], adapter_ids=static[4])
+    for step, ref in zip(steps, want):
+        for to, t in zip(static, step):
+            to.copy_(t)
+        graph.replay()
+        torch.cuda.synchronize()
+        for got, r in zip([*out, *serve.plan, serve.rejected], ref):
+            assert torch.equal(got, r)
+    assert status() == 0
+
+
+def test_adapters_two_graphs_at_once():
+    """Steps of many tokens captured on one stream and replayed on two: each graph has its own memory."""
+    T, K, O, R, n = 2048, 512, 512, 16, 4
+    ids = np.random.default_rng(1).integers(0, n, T)
+    plan = tp.tp_lora_plan(i32(ids), T, n)
+    side = torch.cuda.Stream()
+    work = []
+    for seed in (1, 2):
+        x, a, b, y, s = lora_data("column", T, 1, K, O, R, n, BF16, F32, seed)
+        out = [torch.empty_like(t) for t in y]
+        want = call_lora("column", x, a, b, plan, y, scales=s, out=[torch.empty_like(t) for t in y])
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            call_lora("column", x, a, b, plan, y, scales=s, out=out)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            for _ in range(20):
+                call_lora("column", x, a, b, plan, y, scales=s, out=out)
+        work.append((graph, out, want, (x, a, b, y, s)))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        for (graph, _, _, _), st in zip(work, streams):
+            with torch.cuda.stream(st):
+                graph.replay()
+    torch.cuda.synchronize()
+    for _, out, want, _ in work:
+        assert all(torch.equal(o, w) for o, w in zip(out, want))
+
+
+def test_calls_on_a_named_stream():
+    """The operators on a stream that is not the current one, behind work that is still running there."""
+    T, K, O, R, n = 1500, 256, 256, 16, 4
+    x, a, b, y, s = lora_data("column", T, 1, K, O, R, n, BF16, F32, 1)
+    ids = i32(np.random.default_rng(1).integers(0, n, T))
+    want = call_lora("column", x, a, b, tp.tp_lora_plan(ids, T, n), y, scales=s, out=[torch.empty_like(t) for t in y])[0]
+    step = some_step(20, 16, 100, 8, 0.1, 1)
+    ref = plan_ref(*step)
+    v = drafted(5, 0, 3, 300, F32, F32, 1)
+    cu = i32(v[2])  # kept, as all inputs, until the other stream is done with it
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for st in (side, side.cuda_stream):
+        out = torch.empty_like(y[0])
+        late = torch.empty_like(x[0])
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)
+            late.copy_(x[0])
+        plan = tp.tp_lora_plan(ids, T, n, stream=st)
+        tp.tp_lora_all_to_sharded(late, a[0], b, plan, y, scales=s, out=[out], stream=st)
+        got = tp.tp_verify(v[0], v[1], cu, v[3], draft_probs=v[4], stream=st)
+        assert run_plan(*step, stream=st) == ref
+        side.synchronize()
+        assert torch.equal(out, want)
+        check_verify(got, verify_ref(v[0], v[1], v[2], v[3], v[4]))
+
+
+def test_prepared_calls_are_replayed():
+    T, K, O, R, n = 1300, 256, 256, 16, 4
+    x, a, b, y, s = lora_data("column", T, 1, K, O, R, n, BF16, F32, 1)
+    plan = tp.tp_lora_plan(i32(np.random.default_rng(1).integers(0, n, T)), T, n)
+    want = call_lora("column", x, a, b, plan, y, scales=s, out=[torch.empty_like(t) for t in y])[0].clone()
+    out = [torch.zeros_like(t) for t in y]
+    call = tp.prepare(tp.tp_lora_all_to_sharded, x[0], a[0], b, plan, y, scales=s, out=out)
+    torch.cuda.synchronize()
+    assert not out[0].any()
+    other = [torch.full((8 * T * 16,), 7.0, device="cuda") for _ in range(3)]  # in memory that the call has given back
+    call()
+    torch.cuda.synchronize()
+    assert torch.equal(out[0], want) and all(bool((t == 7).all()) for t in other)
+    xl, d, cu, u, q = drafted(4, 1, 3, 100, F32, F32, 1)
+    call = tp.prepare(tp.tp_verify, xl, d, i32(cu), u, draft_probs=q)
+    check_verify(call(), verify_ref(xl, d, cu, u, q))
+    xr, ar, br, yr, s = lora_data("row", 9, 2, 64, 64, 8, 3, F16, BF16, 2)
+    plan = tp.tp_lora_plan(i32([0, 1, 2, 0, 1, 2, -1, -1, 0]), 9, 3)
+    out = torch.zeros_like(yr[0])
+    tp.prepare(tp.tp_lora_sharded_to_all, xr, ar, br[0], plan, yr[0], out=out)()
+    assert torch.equal(out, tp.tp_lora_sharded_to_all(xr, ar, br[0], plan, yr[0], out=torch.empty_like(out)))
+    step = some_step(6, 16, 50, 3, 0.1, 2)
+    t, pool = i32(step[4]), i32(step[5])
+    call = tp.prepare(tp.tp_paged_plan, i32(step[0]), i32(step[2]), i32(step[3]), t, pool, i32([step[6]]), step[7], step[8],
+                      rejected=i32(step[1]))
+    p = call()
+    torch.cuda.synchronize()
+    ref = plan_ref(*step)
+    assert (p[0].tolist(), p[5].tolist(), p[6].tolist(), t.tolist(), pool.tolist()) == (ref[0], ref[5], ref[6], ref[7], ref[8])
+    ids = i32([1, 0, 2])
+    call = tp.prepare(tp.tp_lora_plan, ids, 3, 3)
+    assert call().tolist() == groups_ref([1, 0, 2], [0, 1, 2, 3], 3, 3)
+
+
+def test_binding_refusals():
+    x, a, b, y, s = lora_data("column", 8, 2, 64, 64, 16, 3, BF16, BF16, 1)
+    plan = tp.tp_lora_plan(i32([0] * 8), 8, 3)
+    ok = dict(x=x[0], a=a[0], b=b, plan=plan, y=y)
+    for kw in (dict(x=x[0].float()), dict(a=a[0].half()), dict(b=b[:1]), dict(y=y[:1]), dict(y=[y[0], y[1].float()]),
+               dict(plan=plan.long()), dict(plan=plan.cpu()), dict(x=x), dict(a=a[0].transpose(1, 2)), dict(out=[y[0]]),
+               dict(out=[t.float() for t in y]), dict(scales=s.double()), dict(scales=s[:2]), dict(x=x[0][:, ::2])):
+        with pytest.raises((ValueError, TypeError)):
+            tp.tp_lora_all_to_sharded(**{**ok, **kw})
+    with pytest.raises(tp.TPError):  # a plan of another step
+        tp.tp_lora_all_to_sharded(**{**ok, "plan": tp.tp_lora_plan(i32([0] * 9), 9, 3)})
+    with pytest.raises(tp.TPError):
+        tp.tp_lora_all_to_sharded(**ok, out=[y[0], torch.empty_like(y[1])])
+    with pytest.raises(ValueError):
+        tp.tp_lora_sharded_to_all(x, a, b, plan, y[0])
+    ints = i32([1, 2])
+    good = [ints, ints, ints, i32([[0, 1], [2, 3]]), i32([0] * 8), i32([4]), 16, 4]
+    for at, v in ((0, ints.long()), (1, i32([1])), (3, i32([[0, 1]])), (3, ints), (4, ints.float()), (5, ints), (7, -1)):
+        args = list(good)
+        args[at] = v
+        with pytest.raises((ValueError, TypeError)):
+            tp.tp_paged_plan(*args)
+    with pytest.raises(ValueError):
+        tp.tp_paged_plan(*good, out=[ints])
+    xl, d, cu, u, q = drafted(4, 1, 3, 100, F32, F32, 1)
+    for kw in (dict(drafts=d.int()), dict(drafts=d[:3]), dict(u=u[:3]), dict(draft_probs=q[:, :50]), dict(cu_rows=i32(cu).long()),
+               dict(temperature=u), dict(tokens=d[:2]), dict(draft_probs=q.t()), dict(logits=xl.double())):
+        with pytest.raises((ValueError, TypeError)):
+            tp.tp_verify(**{**dict(logits=xl, drafts=d, cu_rows=i32(cu), u=u, draft_probs=q), **kw})
+    with pytest.raises(tp.TPError):
+        tp.tp_lora_plan(i32([0, 1]), 3, 2)
