@@ -1023,12 +1023,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     return y;
   };
   auto z_of = [&](float v) { return exp2_of((v - top) * 1.4426950408889634f); };
+  // (of a verification without filters the logits give way to what of e is kept)
+  const bool held = VERIFY && free_draw && d >= 0;
   if (free_draw) {
 #pragma unroll 4
     for (int j = 0; j < R; ++j) {
-      const float v = row.run[j], e = row.e_of(v);
+      const float v = row.run[j], e = row.e_of(v), kept = e < min_p ? 0.0f : e;
       z += own ? e : z_of(v);
-      sum.add(e < min_p ? 0.0f : e);
+      sum.add(kept);
+      if (held) xs[tid * R + j] = kept;
     }
   } else if (guessed && !own) {
     row.sample();
@@ -1120,6 +1123,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // ---- the draw
   auto kept_e = [&](int j) {
+    if (held) return row.run[j];
     const float v = row.run[j], e = row.e_of(v);
     return cut.keeps(v, row.index0 + j) && !(e < min_p) ? e : 0.0f;
   };
@@ -1160,43 +1164,51 @@ __global__ void __launch_bounds__(kThreads, 1)
         return;
       }
       if (a.ordered && rank == 0 && tid == 0) __stcg(row_words(a, b), drawn_mark(0));  // later rows need not begin
-      // What is left, in place of the logits: four neighbours a thread, two of those at a
+      // What is left, in place of the logits: four neighbours a thread, four of those at a
       // time; what is not kept needs no exponential and nothing of the draft's.
       __syncthreads();
       const int64_t q0 = b * a.ldq + (int64_t)rank * slice;
       const uint32_t first = (uint32_t)rank * slice;
       const int es = a.q_dt == TP_F32 ? 4 : 2;
       const int quads = a.q && ((uintptr_t)a.q + q0 * es) % (4 * es) ? 0 : n / 4;
-      auto left = [&](float v, uint32_t i, float q) { return fmaxf(__fsub_rn(prob_of(v, i), q), 0.0f); };
+      auto left = [&](float v, uint32_t i, float q) {
+        return fmaxf(__fsub_rn(held ? __fmul_rn(v, share) : prob_of(v, i), q), 0.0f);
+      };
       auto left4 = [&](int i, const float4 &v, const float4 &q) {
         const uint32_t at = first + 4 * i;
         reinterpret_cast<float4 *>(xs)[i] =
             make_float4(left(v.x, at, q.x), left(v.y, at + 1, q.y), left(v.z, at + 2, q.z), left(v.w, at + 3, q.w));
       };
-      auto any4 = [&](const float4 &v) { return v.x >= cut.x || v.y >= cut.x || v.z >= cut.x || v.w >= cut.x; };
+      const float from = held ? 1e-45f : cut.x;  // what is not 0
+      auto any4 = [&](const float4 &v) { return v.x >= from || v.y >= from || v.z >= from || v.w >= from; };
       auto one_hot = [&](int i) {
         const uint32_t at = (uint32_t)d - (first + 4 * i);
         return make_float4(at == 0, at == 1, at == 2, at == 3);
       };
       const float4 none = make_float4(0, 0, 0, 0);
-      for (int i = tid; i < quads; i += 2 * kThreads) {
-        const int i2 = i + kThreads;
-        const bool in2 = i2 < quads;
-        const float4 v = reinterpret_cast<const float4 *>(xs)[i], v2 = in2 ? reinterpret_cast<const float4 *>(xs)[i2] : none;
-        const bool any = any4(v), any2 = in2 && any4(v2);
-        uint4 w = make_uint4(0, 0, 0, 0), w2 = w;
-        if (any && a.q) w = draft_words(a.q, a.q_dt, q0 + 4 * i);
-        if (any2 && a.q) w2 = draft_words(a.q, a.q_dt, q0 + 4 * i2);
-        if (any) left4(i, v, a.q ? draft_probs(w, a.q_dt) : one_hot(i));
-        else reinterpret_cast<float4 *>(xs)[i] = none;
-        if (any2) left4(i2, v2, a.q ? draft_probs(w2, a.q_dt) : one_hot(i2));
-        else if (in2) reinterpret_cast<float4 *>(xs)[i2] = none;
+      for (int i0 = tid; i0 < quads; i0 += 4 * kThreads) {
+        uint4 w[4];
+        uint32_t any = 0;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int i = i0 + u * kThreads;
+          if (i >= quads || !any4(reinterpret_cast<const float4 *>(xs)[i])) continue;
+          any |= 1u << u;
+          if (a.q) w[u] = draft_words(a.q, a.q_dt, q0 + 4 * i);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int i = i0 + u * kThreads;
+          if (i >= quads) continue;
+          if (any >> u & 1) left4(i, reinterpret_cast<const float4 *>(xs)[i], a.q ? draft_probs(w[u], a.q_dt) : one_hot(i));
+          else reinterpret_cast<float4 *>(xs)[i] = none;
+        }
       }
       for (int i = quads * 4 + tid; i < slice; i += kThreads) {
         const float v = xs[i];
         float q = 0.0f;
-        if (v >= cut.x && i < n) q = a.q ? draft_prob(a.q, a.q_dt, q0 + i) : first + i == (uint32_t)d;
-        xs[i] = v >= cut.x ? left(v, first + i, q) : 0.0f;
+        if (v >= from && i < n) q = a.q ? draft_prob(a.q, a.q_dt, q0 + i) : first + i == (uint32_t)d;
+        xs[i] = v >= from ? left(v, first + i, q) : 0.0f;
       }
       __syncthreads();
       WeightSum rest;
@@ -1213,7 +1225,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         from_rest = true;
         mine = rest_mine, before = rest_before, total = rest_total;
       } else {  // nothing: the logits again, and a draw from the target
-        for (int i = tid; i < slice; i += kThreads) xs[i] = i < n ? clean(static_cast<float>(x[i])) : -INFINITY;
+        for (int i = tid; i < slice; i += kThreads) {
+          const float v = i < n ? clean(static_cast<float>(x[i])) : -INFINITY, e = held ? row.e_of(v) : v;
+          xs[i] = held && e < min_p ? 0.0f : e;
+        }
         __syncthreads();
       }
     }
