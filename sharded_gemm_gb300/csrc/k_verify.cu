@@ -14,16 +14,16 @@
 // cluster for the rows of a sequence, one after the other, would read no row in vain, but
 // take as many times the latency as tokens were accepted.)
 //
-// More rows than the GPU holds are put in order first: the first rows of all sequences,
-// then the second ones and so on, those whose filters take several passes before the
-// others.  A row whose sequence an earlier one has ended by then is left out.
+// More rows than the GPU holds are put in order first: those whose filters take several
+// passes before the others, and of each kind the first rows of all sequences, then the
+// second ones and so on.  A row whose sequence an earlier one has ended by then is left out.
 #include "sample_row.cuh"
 
 namespace tp {
 namespace {
 
-// The order of the rows (one block): by their place in their sequences up to kLevels, then
-// the others as they lie.
+// The order of the rows (one block): of each kind by their place in their sequences up to
+// kLevels, then the others as they lie.
 constexpr int kLevels = 32;
 __global__ void __launch_bounds__(kThreads) verify_order_kernel(const __grid_constant__ VerifyArgs a) {
   __shared__ uint64_t sums[32];
@@ -37,46 +37,55 @@ __global__ void __launch_bounds__(kThreads) verify_order_kernel(const __grid_con
   auto put = [&](int64_t at, int64_t row) {  // sequences that claim each other's rows may be more than there are
     if (first + at < end) row_words(a, first + at)[1] = (int32_t)row;
   };
-  int64_t at = 0, r0 = 0, n = 0;
-  bool slow = false, known = false;
+  int64_t r0 = 0, n = 0;
+  bool slow = false;
+  auto look = [&](int64_t s) {
+    n = 0;
+    if (s >= a.seqs) return;
+    r0 = a.cu[s];
+    const int64_t r1 = a.cu[s + 1];
+    if (r0 >= 0 && r0 <= r1 && r1 <= a.B) n = r1 - r0;
+    slow = slow_row(a, s);
+  };
+  // the sums over lower threads of two values, side by side, and over all
+  auto scan = [&](uint64_t v, uint64_t &all) {
+    uint64_t run = v;
+#pragma unroll
+    for (int m = 1; m < 32; m *= 2) {
+      const uint64_t o = __shfl_up_sync(0xffffffffu, run, m);
+      if (lane >= m) run += o;
+    }
+    __syncthreads();
+    if (lane == 31) sums[warp] = run;
+    __syncthreads();
+    uint64_t lower = lane < warp ? sums[lane] : 0;
+    all = sums[lane];
+#pragma unroll
+    for (int m = 16; m > 0; m /= 2) {
+      lower += __shfl_xor_sync(0xffffffffu, lower, m);
+      all += __shfl_xor_sync(0xffffffffu, all, m);
+    }
+    return lower + run - v;
+  };
+  int64_t at[2] = {0, 0};  // where the next row of a slow sequence goes, and of another
+  uint64_t all;
+  for (int64_t base = 0; base < a.seqs; base += kThreads) {
+    look(base + tid);
+    scan(slow ? (uint64_t)n : 0, all);
+    at[1] += (int64_t)all;
+  }
   for (int level = 0; level <= kLevels; ++level) {
     bool more = false;
-    for (int64_t base = 0; base < a.seqs; base += kThreads) {  // of 1024 sequences the slow ones first
-      const int64_t s = base + tid;
-      if (!known) {
-        n = 0;
-        if (s < a.seqs) {
-          r0 = a.cu[s];
-          const int64_t r1 = a.cu[s + 1];
-          if (r0 >= 0 && r0 <= r1 && r1 <= a.B) n = r1 - r0;
-          slow = slow_row(a, s);
-        }
-        known = a.seqs <= kThreads;
-      }
+    for (int64_t base = 0; base < a.seqs; base += kThreads) {
+      if (a.seqs > kThreads) look(base + tid);
       const uint64_t left = n > level ? n - level : 0, count = level < kLevels ? left > 0 : left;
-      // how many lower threads of its kind put, and of each kind all do
-      uint64_t run = slow ? count << 32 : count;
-      const uint64_t mine = run;
-#pragma unroll
-      for (int m = 1; m < 32; m *= 2) {
-        const uint64_t o = __shfl_up_sync(0xffffffffu, run, m);
-        if (lane >= m) run += o;
-      }
-      if (lane == 31) sums[warp] = run;
-      more = __syncthreads_or(left > 1) || more;
-      uint64_t lower = lane < warp ? sums[lane] : 0, all = sums[lane];
-#pragma unroll
-      for (int m = 16; m > 0; m /= 2) {
-        lower += __shfl_xor_sync(0xffffffffu, lower, m);
-        all += __shfl_xor_sync(0xffffffffu, all, m);
-      }
-      lower += run - mine;
-      const int64_t place = at + (slow ? lower >> 32 : (all >> 32) + (lower & 0xffffffffu));
+      const uint64_t before = scan(slow ? count << 32 : count, all);
+      const int64_t place = slow ? at[0] + (int64_t)(before >> 32) : at[1] + (int64_t)(before & 0xffffffffu);
       for (uint64_t i = 0; i < count; ++i) put(place + i, r0 + level + i);
-      at += (int64_t)((all >> 32) + (all & 0xffffffffu));
-      __syncthreads();
+      at[0] += (int64_t)(all >> 32), at[1] += (int64_t)(all & 0xffffffffu);
+      more = more || left > 1;
     }
-    if (!more) break;
+    if (!__syncthreads_or(more)) break;
   }
 }
 
