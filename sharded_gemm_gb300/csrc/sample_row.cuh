@@ -850,18 +850,22 @@ __device__ __forceinline__ int32_t drawn_mark(int32_t token) { return -2 - token
 // Offsets that do not ascend within the rows are recorded, and their sequence has no rows.
 // Where the rows were put in order, one behind a row of its sequence that has ended it is
 // none either: nothing of it would be used.
+__device__ __forceinline__ int64_t ordered_row(const VerifyArgs &a, int64_t b) {
+  int64_t row = row_words(a, b)[1];  // as if the first sequence began with row 0: no load to wait for
+  const int64_t r0 = a.cu[0], r1 = a.cu[a.seqs];
+  if (r0 < 0 || r1 > a.B || b >= r1 - r0) return -1;
+  return r0 == 0 ? row : row_words(a, r0 + b)[1];
+}
 __device__ __forceinline__ bool verify_place(const VerifyArgs &a, RowShared &sh, int64_t b, int rank, int C,
                                              int64_t &row, int64_t &seq, int64_t &last) {
   const int tid = threadIdx.x;
   if (tid == 0) sh.answer = ~0ull;
-  row = b;
-  if (a.ordered) {
-    const int64_t r0 = a.cu[0], r1 = a.cu[a.seqs];
-    row = r0 >= 0 && r1 <= a.B && b < r1 - r0 ? row_words(a, r0 + b)[1] : -1;
-  }
+  int64_t r0 = 0, r1 = 0;  // of a thread's first sequence, asked for before the row is known
+  if (tid < a.seqs) r0 = a.cu[tid], r1 = a.cu[tid + 1];
+  row = a.ordered ? ordered_row(a, b) : b;
   __syncthreads();
   for (int64_t s = tid; s < a.seqs; s += kThreads) {
-    const int64_t r0 = a.cu[s], r1 = a.cu[s + 1];
+    if (s != tid) r0 = a.cu[s], r1 = a.cu[s + 1];
     if (r0 < 0 || r0 > r1 || r1 > a.B) record_bad_value(a.status);
     else if (row >= r0 && row < r1) sh.answer = s, sh.before = r0, sh.bin = r1 - 1;
   }
@@ -1147,6 +1151,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     total = block;
   }
   bool from_rest = false;  // the draw is from what the target has left over the draft
+  float rest_share = 0.0f;  // where few are kept, that is not put in place of the logits: the kept e's factor
+  // what is left of one of the run's elements
+  auto rest_of = [&](int j) {
+    if constexpr (VERIFY) {
+      if (rest_share > 0.0f) {
+        const float e = kept_e(j);
+        const uint32_t i = row.index0 + j;
+        float q = 0.0f;
+        if (e > 0.0f) q = a.q ? draft_prob(a.q, a.q_dt, b * a.ldq + i) : i == (uint32_t)d;
+        return fmaxf(__fsub_rn(__fmul_rn(e, rest_share), q), 0.0f);
+      }
+    }
+    return row.run[j];
+  };
   if constexpr (VERIFY) {
     if (d >= 0) {
       const float share = __fdiv_rn(1.0f, __ull2float_rn(total) * 9.094947017729282e-13f);
@@ -1164,55 +1182,61 @@ __global__ void __launch_bounds__(kThreads, 1)
         return;
       }
       if (a.ordered && rank == 0 && tid == 0) __stcg(row_words(a, b), drawn_mark(0));  // later rows need not begin
-      // What is left, in place of the logits: four neighbours a thread, four of those at a
-      // time; what is not kept needs no exponential and nothing of the draft's.
-      __syncthreads();
-      const int64_t q0 = b * a.ldq + (int64_t)rank * slice;
-      const uint32_t first = (uint32_t)rank * slice;
-      const int es = a.q_dt == TP_F32 ? 4 : 2;
-      const int quads = a.q && ((uintptr_t)a.q + q0 * es) % (4 * es) ? 0 : n / 4;
-      auto left = [&](float v, uint32_t i, float q) {
-        return fmaxf(__fsub_rn(held ? __fmul_rn(v, share) : prob_of(v, i), q), 0.0f);
-      };
-      auto left4 = [&](int i, const float4 &v, const float4 &q) {
-        const uint32_t at = first + 4 * i;
-        reinterpret_cast<float4 *>(xs)[i] =
-            make_float4(left(v.x, at, q.x), left(v.y, at + 1, q.y), left(v.z, at + 2, q.z), left(v.w, at + 3, q.w));
-      };
-      const float from = held ? 1e-45f : cut.x;  // what is not 0
-      auto any4 = [&](const float4 &v) { return v.x >= from || v.y >= from || v.z >= from || v.w >= from; };
-      auto one_hot = [&](int i) {
-        const uint32_t at = (uint32_t)d - (first + 4 * i);
-        return make_float4(at == 0, at == 1, at == 2, at == 3);
-      };
-      const float4 none = make_float4(0, 0, 0, 0);
-      for (int i0 = tid; i0 < quads; i0 += 4 * kThreads) {
-        uint4 w[4];
-        uint32_t any = 0;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int i = i0 + u * kThreads;
-          if (i >= quads || !any4(reinterpret_cast<const float4 *>(xs)[i])) continue;
-          any |= 1u << u;
-          if (a.q) w[u] = draft_words(a.q, a.q_dt, q0 + 4 * i);
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int i = i0 + u * kThreads;
-          if (i >= quads) continue;
-          if (any >> u & 1) left4(i, reinterpret_cast<const float4 *>(xs)[i], a.q ? draft_probs(w[u], a.q_dt) : one_hot(i));
-          else reinterpret_cast<float4 *>(xs)[i] = none;
-        }
-      }
-      for (int i = quads * 4 + tid; i < slice; i += kThreads) {
-        const float v = xs[i];
-        float q = 0.0f;
-        if (v >= from && i < n) q = a.q ? draft_prob(a.q, a.q_dt, q0 + i) : first + i == (uint32_t)d;
-        xs[i] = v >= from ? left(v, first + i, q) : 0.0f;
-      }
-      __syncthreads();
       WeightSum rest;
-      for (int j = 0; j < R; ++j) rest.add(row.run[j]);
+      if (by_k && k <= kFew) {  // a few of a thread's at most, each with its own load
+        rest_share = share;
+        for_each(mask_of(R, [&](int j) { return row.run[j] >= cut.x; }),
+                 [&](int j, bool valid) { rest.add(valid ? rest_of(j) : 0.0f); });
+      } else {
+        // What is left, in place of the logits: four neighbours a thread, four of those at a
+        // time; what is not kept needs no exponential and nothing of the draft's.
+        __syncthreads();
+        const int64_t q0 = b * a.ldq + (int64_t)rank * slice;
+        const uint32_t first = (uint32_t)rank * slice;
+        const int es = a.q_dt == TP_F32 ? 4 : 2;
+        const int quads = a.q && ((uintptr_t)a.q + q0 * es) % (4 * es) ? 0 : n / 4;
+        auto left = [&](float v, uint32_t i, float q) {
+          return fmaxf(__fsub_rn(held ? __fmul_rn(v, share) : prob_of(v, i), q), 0.0f);
+        };
+        auto left4 = [&](int i, const float4 &v, const float4 &q) {
+          const uint32_t at = first + 4 * i;
+          reinterpret_cast<float4 *>(xs)[i] =
+              make_float4(left(v.x, at, q.x), left(v.y, at + 1, q.y), left(v.z, at + 2, q.z), left(v.w, at + 3, q.w));
+        };
+        const float from = held ? 1e-45f : cut.x;  // what is not 0
+        auto any4 = [&](const float4 &v) { return v.x >= from || v.y >= from || v.z >= from || v.w >= from; };
+        auto one_hot = [&](int i) {
+          const uint32_t at = (uint32_t)d - (first + 4 * i);
+          return make_float4(at == 0, at == 1, at == 2, at == 3);
+        };
+        const float4 none = make_float4(0, 0, 0, 0);
+        for (int i0 = tid; i0 < quads; i0 += 4 * kThreads) {
+          uint4 w[4];
+          uint32_t any = 0;
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int i = i0 + u * kThreads;
+            if (i >= quads || !any4(reinterpret_cast<const float4 *>(xs)[i])) continue;
+            any |= 1u << u;
+            if (a.q) w[u] = draft_words(a.q, a.q_dt, q0 + 4 * i);
+          }
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int i = i0 + u * kThreads;
+            if (i >= quads) continue;
+            if (any >> u & 1) left4(i, reinterpret_cast<const float4 *>(xs)[i], a.q ? draft_probs(w[u], a.q_dt) : one_hot(i));
+            else reinterpret_cast<float4 *>(xs)[i] = none;
+          }
+        }
+        for (int i = quads * 4 + tid; i < slice; i += kThreads) {
+          const float v = xs[i];
+          float q = 0.0f;
+          if (v >= from && i < n) q = a.q ? draft_prob(a.q, a.q_dt, q0 + i) : first + i == (uint32_t)d;
+          xs[i] = v >= from ? left(v, first + i, q) : 0.0f;
+        }
+        __syncthreads();
+        for (int j = 0; j < R; ++j) rest.add(row.run[j]);
+      }
       const u64 rest_mine = rest.total();
       u64 rest_total, rest_before = row.scan_before(rest_mine, rest_total), rest_lower;
       if (C > 1) {
@@ -1224,7 +1248,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (rest_total) {
         from_rest = true;
         mine = rest_mine, before = rest_before, total = rest_total;
-      } else {  // nothing: the logits again, and a draw from the target
+      } else if (rest_share == 0.0f) {  // nothing: the logits again, and a draw from the target
         for (int i = tid; i < slice; i += kThreads) {
           const float v = i < n ? clean(static_cast<float>(x[i])) : -INFINITY, e = held ? row.e_of(v) : v;
           xs[i] = held && e < min_p ? 0.0f : e;
@@ -1243,7 +1267,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     u64 at = __shfl_sync(0xffffffffu, before, l);
     for (int j0 = 0; j0 < R; j0 += 32) {
       const int j = j0 + lane;
-      u64 w = j < R ? weight(from_rest ? row.run[j] : kept_e(j)) : 0;
+      u64 w = j < R ? weight(from_rest ? rest_of(j) : kept_e(j)) : 0;
 #pragma unroll
       for (int m = 1; m < 32; m *= 2) {
         const u64 o = __shfl_up_sync(0xffffffffu, w, m);
