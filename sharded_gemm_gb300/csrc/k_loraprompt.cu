@@ -29,8 +29,8 @@ __device__ __forceinline__ int count_tiles(const LoraArgs &a, int groups, int ro
 // of CTAs: the least turns times what a share takes, `start` units' time and its own.
 __device__ __forceinline__ int shares_of(int tiles, int grid, int units, int start, int most) {
   const int s = threadIdx.x % 32 + 1;
-  const unsigned turns = (unsigned)((int64_t)tiles * s + grid - 1) / grid;
-  const unsigned cost = s <= most ? min(turns * (unsigned)(start + (units + s - 1) / s), 0x3ffffffu) : 0x3ffffffu;
+  const unsigned turns = ((unsigned)(tiles * s) + grid - 1) / (unsigned)grid;  // tiles: 2^25 at most
+  const unsigned cost = s <= most ? min(turns * ((unsigned)start + (unsigned)(units + s - 1) / (unsigned)s), 0x3ffffffu) : 0x3ffffffu;
   return (int)(__reduce_min_sync(0xffffffffu, cost << 5 | (unsigned)(s - 1)) & 31) + 1;
 }
 // The first pass's shares of the contraction, the same in both: kG warps take a unit each.
@@ -71,15 +71,17 @@ __global__ void __launch_bounds__(kLoraThreads, ShrinkShared<RP>::kCtas)
   const int K = (int)a.K, per = (K + 31) / 32, units = per * a.nx, m0 = warp % Shared::kM * MW;
   griddep_wait();
   griddep_launch_dependents();  // behind the wait: the second pass may read what came before this one
-  const int groups = groups_of(a), tiles = count_tiles(a, groups, kShrinkTile, false), S = splits_of<RP>(a, tiles, sms);
+  const int groups = groups_of(a), tiles = count_tiles(a, groups, kShrinkTile, false);
+  const unsigned S = splits_of<RP>(a, tiles, sms);
   int base = 0;
   int64_t before = 0;
   int4 tile;
-  for (int64_t item = blockIdx.x; item < (int64_t)tiles * S; item += gridDim.x) {
+  for (unsigned item = blockIdx.x; item < (unsigned)(tiles * S); item += gridDim.x) {
     if (!find_tile(a, groups, kShrinkTile, false, item / S, base, before, tile)) break;
-    // the split's units in turn to the groups of warps: neighbours read a row's neighbouring bytes
-    const int id = tile.x, split = (int)(item % S), u0 = (int)((int64_t)units * split / S) + warp / Shared::kM;
-    const int u1 = (int)((int64_t)units * (split + 1) / S);
+    // the split's units (of 2^25 and a few at most) in turn to the groups of warps: neighbours
+    // read a row's neighbouring bytes
+    const int id = tile.x, split = item % S, u0 = (int)((unsigned)(units * split) / S) + warp / Shared::kM;
+    const int u1 = (int)((unsigned)(units * (split + 1)) / S);
     __syncthreads();  // the last item's sums are read
     read_tokens(a, tile, kShrinkTile, sh.token);
     __syncthreads();
@@ -235,13 +237,14 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
   bool waited = false;
   const int groups = groups_of(a), with = count_tiles(a, groups, kShrinkTile, false), splits = splits_of<RP>(a, with, sms);
   const int tiles = count_tiles(a, groups, kTile, !a.in_place);
-  const int S = shares_of(tiles, gridDim.x, (blocks + kWarps - 1) / kWarps, 3, 32), step = S * kWarps;
+  const unsigned S = shares_of(tiles, gridDim.x, (blocks + kWarps - 1) / kWarps, 3, 32);
+  const int step = S * kWarps;
   int base = 0;
   int64_t before = 0;
   int4 tile;
-  for (int64_t item = blockIdx.x; item < (int64_t)tiles * S; item += gridDim.x) {
+  for (unsigned item = blockIdx.x; item < (unsigned)(tiles * S); item += gridDim.x) {
     if (!find_tile(a, groups, kTile, !a.in_place, item / S, base, before, tile)) break;
-    const int id = tile.x, blk0 = (int)(item % S) * kWarps + warp;
+    const int id = tile.x, blk0 = item % S * kWarps + warp;
     __syncthreads();
     read_tokens(a, tile, kTile, sh.token);
     if (tid < kTile) {  // read_tokens' own thread
