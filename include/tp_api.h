@@ -736,6 +736,7 @@ int tp_sample(const void *logits, int64_t B, int64_t V, int64_t ld, tp_dtype in_
  *   above -inf accepts nothing and gives token -1 and -inf.  A draft of V or more
  *   and offsets out of range are recorded in the status word: the draft counts as
  *   none, the sequence has no rows.
+ * Outputs overlap no input, but where it is said.
  * Errors: TP_ERR_UNSUPPORTED for more sequences or adapters than these, R above
  * 128, a page or V this build does not take; TP_ERR_NOT_DIVISIBLE if K (of the
  * row-parallel) or O (of the column-parallel) does not divide by N;

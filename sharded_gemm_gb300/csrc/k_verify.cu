@@ -17,6 +17,11 @@
 // More rows than the GPU holds are put in order first: those whose filters take several
 // passes before the others, and of each kind the first rows of all sequences, then the
 // second ones and so on.  A row whose sequence an earlier one has ended by then is left out.
+// (436 mixed rows 155 us in the order given, all taken; 97 by their place; 88 so.  The
+// ordering takes 7: rows up to 1.5 an SM go as they lie, 164 of them 60 us against 66.)
+//
+// Measured, rows of 50272: one sequence of 4 drafts 26 us; 384 rows without filters 57 (two
+// turns of 152, by bytes 13); 436 with mixed settings 88 (16).
 #include "sample_row.cuh"
 
 namespace tp {

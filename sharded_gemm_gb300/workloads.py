@@ -363,6 +363,8 @@ class SharedServing:
                              self.page, self.rows, rejected=self.rejected, out=self.plan)
         self.rejected.zero_()
         qkv = tp_all_to_sharded(x, self.w_qkv, self.b_qkv)
+        if adapter_ids is not None and self.adapters is None:
+            raise ValueError("adapter_ids, but no adapters were given")
         lora = self.adapters if adapter_ids is not None else None
         if lora:
             tp_lora_plan(adapter_ids, self.rows, len(lora["o_b"]), cu_seqlens=plan.cu_seqlens, out=self.groups)

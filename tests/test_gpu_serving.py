@@ -994,3 +994,62 @@ def test_binding_refusals():
             tp.tp_verify(**{**dict(logits=xl, drafts=d, cu_rows=i32(cu), u=u, draft_probs=q), **kw})
     with pytest.raises(tp.TPError):
         tp.tp_lora_plan(i32([0, 1]), 3, 2)
+
+
+# ------------------------------------------------------------------ far addresses
+@pytest.mark.parametrize("T", [40, 1500])
+def test_adapters_beyond_32_bits(T):
+    """Rows, adapters and outputs more than 2^31 elements apart."""
+    n, R, K, O = 16384, 128, 1032, 1032  # 2.2 G elements a pool
+    g = torch.Generator(device="cuda").manual_seed(1)
+    a, b = (torch.empty((n, *shape), dtype=BF16, device="cuda") for shape in ((R, K), (O, R)))
+    used = [0, 5, n - 1]
+    for i in used:
+        a[i] = torch.randn((R, K), generator=g, device="cuda") * K ** -0.5
+        b[i] = torch.randn((O, R), generator=g, device="cuda") * R ** -0.5
+    ld = (1 << 31) // T // 8 * 8 + 2048
+    x = torch.empty((T, ld), dtype=BF16, device="cuda")[:, :K]
+    y = torch.empty((T, ld), dtype=F32, device="cuda")[:, :O]
+    x.copy_(torch.randn((T, K), generator=g, device="cuda"))
+    y.copy_(torch.randn((T, O), generator=g, device="cuda"))
+    ids = np.array(used)[np.arange(T) % 3]
+    plan = tp.tp_lora_plan(i32(ids), T, n)
+    y0 = y.clone()
+    got = tp.tp_lora_all_to_sharded(x, a, [b], plan, [y])
+    d, names = dev(np.arange(T) % 3), torch.tensor(used, device="cuda")
+    check_lora(got, [x.clone()], [a[names]], [b[names]], d, None, [y0], BF16)
+    assert status() == 0
+
+
+def test_verify_beyond_32_bits():
+    V, T = 50000, 44000  # 2.2 G logits, of which the last sequences' are used
+    x = torch.empty((T, V), dtype=F32, device="cuda")
+    q = torch.empty((T, V), dtype=F16, device="cuda")
+    xs, ds, cu, us, qs = drafted(3, 2, 2, V, F32, F16, 4)
+    x[-9:], q[-9:] = xs, qs
+    d = torch.zeros(T, dtype=torch.int64, device="cuda")
+    u = torch.zeros(T, device="cuda")
+    d[-9:], u[-9:] = ds, us
+    keep = torch.full((T,), 77, dtype=torch.int64, device="cuda")
+    got = tp.tp_verify(x, d, i32([T - 9 + c for c in cu]), u, draft_probs=q, tokens=keep)
+    check_verify((keep[-9:], got[1][-9:], got[2], got[3]), verify_ref(xs, ds, cu, us, qs))
+    assert bool((keep[:-9] == 77).all())
+    assert status() == 0
+
+
+def test_plan_beyond_32_bits():
+    B, width = 8192, 270000  # entries of the block table
+    table = torch.empty((B, width), dtype=torch.int32, device="cuda")
+    pages = 1000
+    table[B - 1, :3] = torch.tensor([4, 7, 9], dtype=torch.int32)
+    table[B - 2, :2] = torch.tensor([11, 12], dtype=torch.int32)
+    lens, owned, counts = (torch.zeros(B, dtype=torch.int32, device="cuda") for _ in range(3))
+    lens[B - 1], owned[B - 1], counts[B - 1] = 40, 3, 20
+    lens[B - 2], owned[B - 2], counts[B - 2] = 32, 2, -1
+    pool = torch.full((pages,), -1, dtype=torch.int32, device="cuda")
+    pool[:2] = torch.tensor([1, 2], dtype=torch.int32)
+    p = tp.tp_paged_plan(counts, lens, owned, table, pool, i32([2]), 16, 20)
+    assert p.positions.tolist() == list(range(40, 60)) and int(p.free_count) == 3
+    assert table[B - 1, :4].tolist() == [4, 7, 9, 12]
+    assert p.slots.tolist() == [9 * 16 + i % 16 for i in range(40, 48)] + [12 * 16 + i % 16 for i in range(48, 60)]
+    assert status() == 0
