@@ -548,10 +548,12 @@ def settings_of(B, seed):
     (1, 0, 0, 1, F32, F32), (1, 4, 4, 50, F32, F32), (5, 0, 6, 1000, F32, None), (7, 1, 3, 4097, BF16, F32),
     (3, 2, 2, 50272, F32, BF16), (40, 0, 5, 333, F16, F16), (200, 1, 1, 30, F32, F32), (2, 1, 1, 60001, BF16, None),
     (1, 40, 40, 517, F32, F32)])
-@pytest.mark.parametrize("filters", [False, True])
+@pytest.mark.parametrize("filters", [False, True, "temperature"])
 def test_verify(B, lo, hi, V, dt, q_dt, filters):
     x, d, cu, u, q = drafted(B, lo, hi, V, dt, q_dt, B + V)
     s = settings_of(B, V) if filters else {}
+    if filters == "temperature":
+        s = dict(temperature=s["temperature"])
     got = tp.tp_verify(x, d, i32(cu), u, draft_probs=q, **s)
     check_verify(got, verify_ref(x, d, cu, u, q, **s))
     assert status() == 0
@@ -562,7 +564,7 @@ def test_verify_more_rows_than_the_gpu_holds(B, lo, hi):
     """Rows are taken in another order, and those behind an ended one left out; the results keep their places."""
     V = 2000 if B == 90 else 100
     x, d, cu, u, q = drafted(B, lo, hi, V, F32, F32, B, noise=0.1 if hi > 50 else 0.7)
-    for s in ({}, settings_of(B, 3)):
+    for s in ({}, settings_of(B, 3), dict(temperature=settings_of(B, 4)["temperature"])):
         ref = verify_ref(x, d, cu, u, q, **s)
         for _ in range(3):
             check_verify(tp.tp_verify(x, d, i32(cu), u, draft_probs=q, **s), ref)
@@ -571,8 +573,21 @@ def test_verify_more_rows_than_the_gpu_holds(B, lo, hi):
 
 def test_verify_more_long_rows_than_the_gpu_holds():
     x, d, cu, u, q = drafted(40, 1, 3, 60007, BF16, BF16, 7)
-    s = settings_of(40, 5)
-    check_verify(tp.tp_verify(x, d, i32(cu), u, draft_probs=q, **s), verify_ref(x, d, cu, u, q, **s))
+    for s in (settings_of(40, 5), dict(temperature=settings_of(40, 6)["temperature"])):
+        check_verify(tp.tp_verify(x, d, i32(cu), u, draft_probs=q, **s), verify_ref(x, d, cu, u, q, **s))
+
+
+def test_verify_without_filters_reads_rows_of_any_alignment():
+    """Logits and probabilities whose rows begin at any element, and a vocabulary that ends inside a vector."""
+    for V, dt, q_dt in ((1001, F32, F16), (1003, BF16, F32), (514, F16, BF16)):
+        x, d, cu, u, q = drafted(30, 0, 3, V, dt, q_dt, V)
+        T = len(d)
+        ref = verify_ref(x, d, cu, u, q)
+        for off in (0, 1, 2, 3):
+            wide, wide_q = torch.zeros((T, V + 6), dtype=dt, device="cuda"), torch.zeros((T, V + 5), dtype=q_dt, device="cuda")
+            wide[:, off:off + V], wide_q[:, off:off + V] = x, q
+            check_verify(tp.tp_verify(wide[:, off:off + V], d, i32(cu), u, draft_probs=wide_q[:, off:off + V]), ref)
+    assert status() == 0
 
 
 def test_verify_many_rows_between_rows_of_none():
@@ -627,6 +642,8 @@ def test_verify_borders():
         check_verify(tp.tp_verify(x, d, i32(cu), u, draft_probs=probs), verify_ref(x, d, cu, u, probs))
         s = dict(temperature=dev(np.float32([0, 1, np.inf, 1, 1, 0.5, 1])), top_k=i32([0, 3, 2, 1, 0, 500, 4]),
                  top_p=dev(np.float32([1, 0.5, 1, 0, 0.9, 2, -1])), min_p=dev(np.float32([0, 1, 5, 0, 0.5, -1, 0])))
+        check_verify(tp.tp_verify(x, d, i32(cu), u, draft_probs=probs, **s), verify_ref(x, d, cu, u, probs, **s))
+        s = dict(temperature=s["temperature"])
         check_verify(tp.tp_verify(x, d, i32(cu), u, draft_probs=probs, **s), verify_ref(x, d, cu, u, probs, **s))
     assert status() == 0
 
