@@ -701,7 +701,8 @@ int tp_sample(const void *logits, int64_t B, int64_t V, int64_t ld, tp_dtype in_
  *            else they do not overlap.
  *     workspace  NULL or float32 (tp_lora_workspace_floats(T, R)), 16-byte
  *            aligned, the call's own until it has ended on the stream: with it,
- *            steps of more than 1024 tokens take two faster passes.
+ *            steps of more than 1024 tokens (R above 64: 512) take two faster
+ *            passes.
  *   The products are summed in float32.  The sum over x meets B rounded to dt where
  *   out has no more bits, else as several terms of dt that keep 16 of its bits for
  *   TP_F16 outputs, 22 or more for float32 ones; the result is rounded once.  The

@@ -3,17 +3,20 @@
 //
 // This file: steps of few tokens, operands without 16-byte alignment, and the CUDA-core
 // cross-check; prompts are k_loraprompt.cu's.  A tile is up to 16 tokens of one adapter,
-// taken from the step's plan; a cluster of C CTAs takes it in one launch.  First the C * 8
-// warps split the contraction and each multiplies its stretch of the tokens' rows with the
-// adapter's R rows; the parts are added over the warps and, through distributed shared
+// taken from the step's plan; C CTAs of a cluster of 8 take it in one launch.  First their
+// C * 8 warps split the contraction and each multiplies its stretch of the tokens' rows with
+// the adapter's R rows; the parts are added over the warps and, through distributed shared
 // memory, the CTAs, in a fixed order.  Then the warps split the output's columns: 32 of them
-// are B's 32 rows against h, added to y.  Nothing of h goes through memory.
+// are B's 32 rows against h, added to y.  Nothing of h goes through memory.  The more tiles
+// the plan holds, the fewer CTAs take one (8, 4, 2, 1), so that all run at once.
 //
 // Bound by bytes (each adapter is read once) and, of one token, by latency: 2 R operations
 // an element are few, so warp-level products do.
 //
-// Measured: one token, R = 16, 4096 x 12288 on 8 ranks 5.8 us; 64 tokens of 50 adapters 13.5
-// (28 MB, 4.2 at the copy rate); 97 tokens of 40 adapters, R = 32, 4096 x 4096, float32 10.4.
+// Measured: one token, R = 16, 4096 x 12288 on 8 ranks 5.7 us; 64 tokens of 47 adapters 13.4
+// (28 MB, 4.2 at the copy rate); 97 tokens of 33 adapters, R = 32, 4096 x 4096, float32 11.2.
+#include <atomic>
+
 #include "lora.cuh"
 
 namespace tp {
@@ -115,31 +118,37 @@ struct LoraShared {
   float unscale[16];  // the power of two that a row's products are multiplied by
 };
 
-constexpr int C = 8;  // CTAs of a cluster (4: 16 -> 22 us for 64 tokens of 50 adapters, R = 16, 4096 x 12288)
+constexpr int kCluster = 8;
+template <int RP>
+constexpr int kResident = RP == 128 ? 1 : RP == 16 ? 3 : 2;  // CTAs an SM
 
-template <typename T, int RP, bool VEC, bool OUT32>
-__global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : RP == 16 ? 3 : 2)
-    lora_kernel(const __grid_constant__ LoraArgs a, int S) {
+// The tiles of a call, C of a cluster's CTAs each.  With all eight, S clusters may share a
+// tile, each with h for itself and a share of the columns.  CTAs of one cluster go through
+// the same turns, those without a tile in the last one too.
+template <typename T, int RP, bool VEC, bool OUT32, int C>
+__device__ __forceinline__ void lora_tiles(const LoraArgs &a, int groups, int S) {
   typedef LoraShared<T, RP> Shared;
   constexpr int NT = RP / 8, KS = RP / 16, kStride = Shared::kStride, kTerms = Shared::kTerms;
   extern __shared__ __align__(16) uint8_t smem[];
   Shared &sh = *reinterpret_cast<Shared *>(smem);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, q = lane % 4;
-  const int rank = blockIdx.x % C, cluster = blockIdx.x / C, K = (int)a.K, O = (int)a.O;
+  const int K = (int)a.K, O = (int)a.O;
   const int per_k = (K + 31) / 32, units = per_k * a.nx;
-  const int per_o = (O + 31) / 32, blocks = per_o * a.ny, step = S * C * kWarps;
-  const int blk0 = (cluster % S * C + rank) * kWarps + warp;
-  const int u0 = rank * kWarps + warp;
+  const int per_o = (O + 31) / 32, blocks = per_o * a.ny;
   const int used = terms<T>(a.out_dt);
   const bool out_bf16 = a.out_dt == TP_BF16;
-  griddep_launch_dependents();
-  griddep_wait();
-  const int groups = groups_of(a);
+  constexpr int kSubs = kCluster / C;
+  const int in = blockIdx.x % kCluster, rank = in % C, sub = in / C, cluster = blockIdx.x / kCluster;
+  const int step = S * C * kWarps, blk0 = (cluster % S * C + rank) * kWarps + warp, u0 = rank * kWarps + warp;
   int base = 0;
   int64_t before = 0;
   int4 tile;
   bool read = false;  // the others' sums: they may not change theirs before all have
-  for (int64_t at = cluster / S; find_tile(a, groups, 16, !a.in_place, at, base, before, tile); at += gridDim.x / C / S) {
+  for (int64_t first = cluster / S * kSubs;; first += gridDim.x / kCluster / S * kSubs) {
+    if (!find_tile(a, groups, 16, !a.in_place, first + sub, base, before, tile)) {
+      if (kSubs == 1 || C == 1 || first >= before) break;
+      tile = make_int4(-1, 0, 0, 0);
+    }
     const int id = tile.x;
     __syncthreads();  // the last tile's tokens and fragments are read
     read_tokens(a, tile, 16, sh.token);
@@ -187,7 +196,7 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : RP == 16 ? 3 : 2
       for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
       const uint4 zero = make_uint4(0, 0, 0, 0);
       Cursor cu(u0, per_k);
-#pragma unroll 2
+#pragma unroll (RP < 64 ? 2 : 1)  // (R = 64: two spill, 22.5 us where one takes 19.5)
       for (int u = u0; u < units; u += C * kWarps) {  // neighbours read a row's neighbouring bytes
         const int k = cu.i * 32 + q * 8;
         const uint16_t *x = static_cast<const uint16_t *>(a.x[cu.p]);
@@ -223,21 +232,24 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : RP == 16 ? 3 : 2
         for (int j = 1; j < kWarps; ++j) sum = add4(sum, *reinterpret_cast<const float4 *>(&sh.part[j][row][col]));
         *reinterpret_cast<float4 *>(&sh.part[0][row][col]) = sum;
       }
-      cluster_sync_all();
+      if (C > 1)
+        cluster_sync_all();
+      else
+        __syncthreads();
       const float scale = a.scales ? __ldg(a.scales + id) : 1.0f;
       for (int i = tid; i < 4 * RP; i += kLoraThreads) {
         const int row = i / (RP / 4), col = i % (RP / 4) * 4;
         const uint32_t mine = smem_u32(&sh.part[0][row][col]);
         float4 of[C], sum = make_float4(0, 0, 0, 0);  // all asked for before the first is added
 #pragma unroll
-        for (int r = 0; r < C; ++r) of[r] = ld_cluster_f4(mapa_shared(mine, r));
+        for (int r = 0; r < C; ++r) of[r] = ld_cluster_f4(mapa_shared(mine, sub * C + r));
 #pragma unroll
         for (int r = 0; r < C; ++r) sum = add4(sum, of[r]);
         *reinterpret_cast<float4 *>(&sh.h[row][col]) =
             make_float4(sum.x * scale, sum.y * scale, sum.z * scale, sum.w * scale);
       }
-      cluster_arrive();
-      read = true;
+      if (C > 1) cluster_arrive();
+      read = C > 1;
       __syncthreads();
       if (!Half2<T>::kBf16) {
         for (int row = warp; row < 16; row += kWarps) {
@@ -250,14 +262,20 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : RP == 16 ? 3 : 2
       }
       make_fragments<T, RP, 1, kTerms, kStride>(&sh.h[0][0], sh.frag);
       __syncthreads();
-    } else if (blk0 < blocks) {
-      fetch(c, now);
+    } else {
+      if (tile.z > 0 && blk0 < blocks) fetch(c, now);
+      if (kSubs > 1 && C > 1) {
+        if (read) cluster_wait();
+        cluster_sync_all();
+        cluster_arrive();
+        read = true;
+      }
     }
 
     // ---- the outputs: 32 columns a warp at a time
     const float f0 = Half2<T>::kBf16 || id < 0 ? 1.0f : sh.unscale[g];
     const float f1 = Half2<T>::kBf16 || id < 0 ? 1.0f : sh.unscale[g + 8];
-    for (int blk = blk0; blk < blocks; blk += step) {
+    for (int blk = tile.z > 0 ? blk0 : blocks; blk < blocks; blk += step) {
       const int p = c.p, col = c.i * 32 + lane_col(OUT32, 0, q);
       c.next(step, per_o);
       if (id >= 0) {
@@ -290,6 +308,36 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : RP == 16 ? 3 : 2
     }
   }
   if (read) cluster_wait();  // no CTA leaves while another may still read its shared memory
+}
+
+template <typename T, int RP, bool VEC, bool OUT32>
+__global__ void __launch_bounds__(kLoraThreads, kResident<RP>)
+    lora_kernel(const __grid_constant__ LoraArgs a, int S) {
+  griddep_launch_dependents();
+  griddep_wait();
+  lora_tiles<T, RP, VEC, OUT32, kCluster>(a, groups_of(a), S);
+}
+
+// More tiles than clusters run at once, if the plan has as many as it may: it says how many
+// CTAs take one.  (4096 x 4096, microseconds with 8 CTAs a tile | with as many as fit:
+// R = 16, 256 tokens of 152 adapters 38 | 22, 1024 of 249 66 | 38; R = 64, 64 tokens of 40
+// adapters 30 | 19, 1024 of 249 143 | 59; R = 128 and 93 adapters 99 | 60.)
+template <typename T, int RP, bool OUT32>
+__global__ void __launch_bounds__(kLoraThreads, kResident<RP>) lora_many_kernel(const __grid_constant__ LoraArgs a, int) {
+  griddep_launch_dependents();
+  griddep_wait();
+  // About so many tiles: the groups of an adapter's few tokens are one each.
+  const int groups = groups_of(a), clusters = gridDim.x / kCluster, all = (int)a.T;
+  const int with = max(0, min(all, __ldg(a.plan + 1))), adapters = groups - (with < all);
+  const int tiles = adapters + max(0, with - 8 * adapters) / 16 + (a.in_place ? 0 : (all - with + 15) / 16);
+  if (tiles <= clusters)
+    lora_tiles<T, RP, true, OUT32, 8>(a, groups, 1);
+  else if (tiles <= 2 * clusters)
+    lora_tiles<T, RP, true, OUT32, 4>(a, groups, 1);
+  else if (RP == 128 || tiles <= 4 * clusters)
+    lora_tiles<T, RP, true, OUT32, 2>(a, groups, 1);
+  else
+    lora_tiles<T, RP, true, OUT32, 1>(a, groups, 1);
 }
 
 // The same on the CUDA cores, a block a token: the cross-check.
@@ -354,19 +402,11 @@ bool all_aligned(const void *const *p, int n, int to) {
 
 template <typename T, int RP, bool VEC, bool OUT32>
 int launch(const LoraArgs &a, cudaStream_t s) {
-  auto kern = lora_kernel<T, RP, VEC, OUT32>;
+  void (*kern)(LoraArgs, int) = lora_kernel<T, RP, VEC, OUT32>;
   const size_t smem = sizeof(LoraShared<T, RP>);
   cudaError_t e = cudaSuccess;
-  if (smem > 48 * 1024) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return cuda_error(e, "adapter launch");
-  int64_t tiles = a.T / 16 + a.most;  // at most
-  if (tiles > (1 << 20)) tiles = 1 << 20;
-  // few tiles: several clusters for one, each with h for itself and a share of the columns
-  const int64_t blocks = (a.O + 31) / 32 * a.ny, room = 2 * sm_count() / (tiles * C), most = (blocks + 8 * C - 1) / (8 * C);
-  const int S = (int)(room < 1 ? 1 : room < most ? room : most);
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = dim3((unsigned)(tiles * S * C));
   cfg.blockDim = dim3(kLoraThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -374,10 +414,31 @@ int launch(const LoraArgs &a, cudaStream_t s) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = C;
+  attr[1].val.clusterDim.x = kCluster;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
+  static std::atomic<int> resident[64];  // clusters
+  int device = 0;
+  cudaGetDevice(&device);
+  int wave = resident[device &= 63].load(std::memory_order_relaxed);
+  if (!wave) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if constexpr (VEC)
+      if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(lora_many_kernel<T, RP, OUT32>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cfg.gridDim = dim3(kCluster);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&wave, kern, &cfg);
+    if (e != cudaSuccess) return cuda_error(e, "adapter launch");
+    if (wave < 1) wave = 1;
+    resident[device].store(wave, std::memory_order_relaxed);
+  }
+  const int64_t tiles = a.T / 16 + a.most, blocks = (a.O + 31) / 32 * a.ny;  // at most
+  const int64_t most = (blocks + kCluster * kWarps - 1) / (kCluster * kWarps), room = wave / tiles;
+  const int S = (int)(room < 1 ? 1 : room < most ? room : most);
+  if constexpr (VEC)
+    if (tiles > wave) kern = lora_many_kernel<T, RP, OUT32>;
+  cfg.gridDim = dim3((unsigned)((tiles * S < wave ? tiles * S : wave) * kCluster));
   e = cudaLaunchKernelEx(&cfg, kern, a, S);
   if (e != cudaSuccess) return cuda_error(e, "adapter launch");
   note_launch();

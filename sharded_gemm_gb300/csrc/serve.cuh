@@ -30,13 +30,16 @@ struct GroupArgs {
 inline int64_t most_groups(int64_t T, int64_t n) { return T < n + 1 ? T : n + 1; }
 inline int64_t plan_ints(int64_t T, int64_t n) { return 4 + 4 * most_groups(T, n) + T; }
 
-// Steps of more tokens take two passes with h between them in memory.  (A tile of 16 reads
-// an adapter for every 16 tokens; up to here the second launch costs more.)
-constexpr int64_t kFewTokens = 1024;
+// Steps of more tokens take two passes with h between them in memory.  (One pass reads an
+// adapter for every 16 tokens, the two for every 64 or more, but they cost a launch more.
+// 4096 x 4096, tokens of 8 adapters, one pass | two: R = 16, 1024 tokens 12.6 us | 13.1, 2048
+// 22.8 | 16.7; R = 64, 1024 19.7 | 21.2, 2048 30.4 | 24.5; R = 128, 256 16.4 | 19.1, 512 25.1 |
+// 22.5, 1024 54 | 24.)
+inline int64_t few_tokens(int R) { return R <= 64 ? 1024 : 512; }
 // How often a tile's contraction is split at most: few tiles leave SMs idle.
 inline int lora_splits(int64_t T) { return T <= 4096 ? 8 : T <= 8192 ? 4 : T <= 16384 ? 2 : 1; }
 inline int64_t lora_workspace(int64_t T, int R) {
-  return T <= kFewTokens ? 0 : T * (R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 ? 64 : 128) * lora_splits(T);
+  return T <= few_tokens(R) ? 0 : T * (R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 ? 64 : 128) * lora_splits(T);
 }
 
 struct LoraArgs {

@@ -125,6 +125,11 @@ def test_sizes_of_adapter_workspaces(L):
     assert L.tp_lora_workspace_floats(2000, 129) == 0 and L.tp_lora_workspace_floats(-1, 8) == 0
 
 
+def test_high_ranks_take_two_passes_earlier(L):
+    assert [L.tp_lora_workspace_floats(512, r) for r in (64, 65, 128)] == [0, 0, 0]
+    assert [L.tp_lora_workspace_floats(513, r) for r in (64, 65, 128)] == [0] + [8 * 513 * 128] * 2
+
+
 def test_empty_calls_launch_nothing(L):
     before = L.tp_launch_count()
     assert _column(L, T=0) == tp.TP_OK

@@ -341,6 +341,30 @@ def test_adapters(policy, form, T, N, K, O, R, n, dt, out_dt):
     assert status() == 0
 
 
+@pytest.mark.parametrize("R,dt,out_dt", [(16, BF16, BF16), (16, F16, F32), (32, BF16, F32), (64, F16, F16),
+                                         (64, BF16, F32), (100, BF16, F16), (128, F16, F32)])
+@pytest.mark.parametrize("T,n,most", [(70, 60, 60), (150, 140, 140), (300, 200, 200), (512, 2000, 2000),
+                                      (1024, 900, 900), (400, 300, 3), (500, 120, 30), (200, 256, 1)])
+def test_adapters_of_many_requests(T, n, most, R, dt, out_dt):
+    """Tiles from fewer than clusters that run at once to many times as many, of `most` of n adapters."""
+    K, O, form, N = (328, 264, "column", 1) if T % 100 else (512, 320, "row", 2)
+    x, a, b, y, scales = lora_data(form, T, N, K, O, R, n, dt, out_dt, T + R)
+    rng = np.random.default_rng(T)
+    for pad, s, in_place in ((0, scales, False), (7, None, True)):
+        ids = rng.integers(-1, most, T) * (n // most)
+        ids[ids < 0] = -1
+        ids[T - pad:] = -2
+        plan = tp.tp_lora_plan(i32(ids[:T - pad]), T, n, cu_seqlens=i32(np.arange(T - pad + 1)))
+        y0 = [t.clone() for t in y]
+        got = call_lora(form, x, a, b, plan, y, scales=s, out=None if in_place else [torch.full_like(t, 7) for t in y])
+        # (rows of no sequence are left as they were)
+        check_lora(got, x, a, b, dev(ids), s, y0, dt)
+        again = [t.clone() for t in y0]
+        again = call_lora(form, x, a, b, plan, again, scales=s, out=None if in_place else [torch.full_like(t, 7) for t in y])
+        assert all(torch.equal(p, q) for p, q in zip(got, again))
+    assert status() == 0
+
+
 @pytest.mark.parametrize("T", [40, 1200])
 @pytest.mark.parametrize("form", ["column", "row"])
 def test_adapters_of_strided_and_unaligned_rows(form, T):
@@ -423,6 +447,20 @@ def test_adapters_of_plans_that_are_none():
     x, a, b, y, _ = lora_data("column", T, 1, 64, 64, 16, n, BF16, F32, 4)
     good = tp.tp_lora_plan(i32([0, 1, 0, 1, 0, 1, -1, 0]), T, n)
     for at, v in ((0, 1000), (0, -3), (4, 7), (5, -1), (5, 9), (6, 100), (6, -2), (4 + 4 * 3, 8), (4 + 4 * 3 + 2, -5)):
+        bad = good.clone()
+        bad[at] = v
+        call_lora("column", x, a, b, bad, y, out=[torch.empty_like(t) for t in y])
+        assert status() == tp.TP_ERR_INVALID_ARG, (at, v)
+
+
+def test_adapters_of_many_plans_that_are_none():
+    """The same where the plan says how many CTAs take a tile."""
+    T, n = 300, 250
+    x, a, b, y, _ = lora_data("column", T, 1, 64, 64, 16, n, BF16, F32, 4)
+    good = tp.tp_lora_plan(i32(np.arange(T) % n), T, n)
+    order = 4 + 4 * (n + 1)
+    for at, v in ((0, 1000), (0, -3), (4, 251), (4 + 4 * 200, 250), (5, -1), (5, 500), (6, 1000), (6, -2), (order + 3, 300),
+                  (order + 299, -5)):
         bad = good.clone()
         bad[at] = v
         call_lora("column", x, a, b, bad, y, out=[torch.empty_like(t) for t in y])
