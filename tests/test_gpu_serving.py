@@ -365,6 +365,21 @@ def test_adapters_of_many_requests(T, n, most, R, dt, out_dt):
     assert status() == 0
 
 
+@pytest.mark.parametrize("R,dt,out_dt", [(16, BF16, F32), (16, F16, F16), (32, BF16, BF16), (64, BF16, F16), (64, F16, F32),
+                                         (128, BF16, BF16), (128, F16, F32)])
+@pytest.mark.parametrize("lens", [[600] + [1, 2] * 200, [31, 32, 33, 15, 16, 17, 63, 64, 65, 47, 48, 49, 127, 128, 129, 500],
+                                  [1] * 1100])
+def test_adapters_of_prompts_beside_many_requests(lens, R, dt, out_dt):
+    """Tiles of one to all blocks of tokens in one step of two passes."""
+    n, T, K, O = len(lens), sum(lens), 520, 264
+    x, a, b, y, scales = lora_data("column", T, 2, K, O, R, n, dt, out_dt, T + R)
+    ids = np.random.default_rng(R).permutation(n)
+    plan = tp.tp_lora_plan(i32(ids), T, n, cu_seqlens=i32(np.concatenate([[0], np.cumsum(lens)])))
+    got = call_lora("column", x, a, b, plan, y, scales=scales, out=[torch.full_like(t, 7) for t in y])
+    check_lora(got, x, a, b, dev(np.repeat(ids, lens)), scales, y, dt)
+    assert status() == 0
+
+
 @pytest.mark.parametrize("T", [40, 1200])
 @pytest.mark.parametrize("form", ["column", "row"])
 def test_adapters_of_strided_and_unaligned_rows(form, T):
