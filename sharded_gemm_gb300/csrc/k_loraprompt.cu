@@ -11,7 +11,7 @@
 // barriers between the products stood in the way of the streams, and registers for both were
 // too many: 309 us for 8192 tokens, R = 64, 4096 x 11008, where 66 us of bytes move.)
 //
-// Measured: those 91 us, the first pass 27 (67 MB) and the second 70 (361 MB, 5.2 TB/s; its
+// Measured: those 92 us, the first pass 27 (67 MB) and the second 70 (361 MB, 5.2 TB/s; its
 // loop alone 90% of the copy rate); 5003 tokens, R = 16, 11008 x 4096, float32 outputs 60,
 // passes of 26 (110 MB) and 31 (164 MB).
 #include "lora.cuh"
