@@ -703,10 +703,10 @@ int tp_sample(const void *logits, int64_t B, int64_t V, int64_t ld, tp_dtype in_
  *            aligned, the call's own until it has ended on the stream: with it,
  *            steps of more than 1024 tokens (R above 64: 512) take two faster
  *            passes.
- *   The products are summed in float32.  The sum over x meets B rounded to dt where
- *   out has no more bits, else as several terms of dt that keep 16 of its bits for
- *   TP_F16 outputs, 22 or more for float32 ones; the result is rounded once.  The
- *   ranks' parts are added in a fixed order: the
+ *   The products are summed in float32.  The sum over x meets B as several terms of
+ *   dt that keep 16 of its bits for TP_BF16 and 22 for TP_F16, or with float32
+ *   outputs 22 or more; the result is rounded once.  (So an infinite b gives NaN:
+ *   the terms' signs differ.)  The ranks' parts are added in a fixed order: the
  *   same call gives the same bytes.  plan_size counts plan's values: a plan of another T or n is refused
  *   (TP_ERR_INVALID_ARG); one that is not a plan is recorded in the status word.
  *

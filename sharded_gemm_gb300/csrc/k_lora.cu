@@ -110,8 +110,8 @@ __device__ __forceinline__ void add_out(Out8<OUT32> &o, const float (&d)[8], boo
 // RP: R rounded up to 16, 32, 64 or 128.
 template <typename T, int RP>
 struct LoraShared {
-  static constexpr int kStride = RP + 4, kTerms = Half2<T>::kBf16 ? 3 : 2;
-  uint4 frag[kTerms][1][RP / 16][32];
+  static constexpr int kStride = RP + 4;
+  uint4 frag[terms<T>(true)][1][RP / 16][32];
   float part[kWarps][16][kStride];  // [0] in the end: this CTA's sums, read by the others
   float h[16][kStride];
   int token[16];
@@ -128,14 +128,13 @@ constexpr int kResident = RP == 128 ? 1 : RP == 16 ? 3 : 2;  // CTAs an SM
 template <typename T, int RP, bool VEC, bool OUT32, int C>
 __device__ __forceinline__ void lora_tiles(const LoraArgs &a, int groups, int S) {
   typedef LoraShared<T, RP> Shared;
-  constexpr int NT = RP / 8, KS = RP / 16, kStride = Shared::kStride, kTerms = Shared::kTerms;
+  constexpr int NT = RP / 8, KS = RP / 16, kStride = Shared::kStride, kTerms = terms<T>(OUT32);
   extern __shared__ __align__(16) uint8_t smem[];
   Shared &sh = *reinterpret_cast<Shared *>(smem);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, q = lane % 4;
   const int K = (int)a.K, O = (int)a.O;
   const int per_k = (K + 31) / 32, units = per_k * a.nx;
   const int per_o = (O + 31) / 32, blocks = per_o * a.ny;
-  const int used = terms<T>(a.out_dt);
   const bool out_bf16 = a.out_dt == TP_BF16;
   constexpr int kSubs = kCluster / C;
   const int in = blockIdx.x % kCluster, rank = in % C, sub = in / C, cluster = blockIdx.x / kCluster;
@@ -286,7 +285,6 @@ __device__ __forceinline__ void lora_tiles(const LoraArgs &a, int groups, int S)
         for (int s = 0; s < KS; ++s)
 #pragma unroll
           for (int i = 0; i < kTerms; ++i) {
-            if (i >= used) break;
             const uint4 f = sh.frag[i][0][s][lane];
             const uint32_t hf[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll

@@ -11,8 +11,8 @@
 // barriers between the products stood in the way of the streams, and registers for both were
 // too many: 309 us for 8192 tokens, R = 64, 4096 x 11008, where 66 us of bytes move.)
 //
-// Measured: those 92 us, the first pass 27 (67 MB) and the second 70 (361 MB, 5.2 TB/s; its
-// loop alone 90% of the copy rate); 5003 tokens, R = 16, 11008 x 4096, float32 outputs 60,
+// Measured: those 105 us, the first pass 27 (67 MB), the second (361 MB) bound by the products of
+// h's two terms (one alone: 70); 5003 tokens, R = 16, 11008 x 4096, float32 outputs 60,
 // passes of 26 (110 MB) and 31 (164 MB).
 #include "lora.cuh"
 
@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(kLoraThreads, ShrinkShared<RP>::kCtas)
 template <typename T, int RP, typename O>
 struct ExpandShared {
   static constexpr bool OUT32 = sizeof(O) == 4;
-  static constexpr int kTerms = terms<T>(OUT32 ? TP_F32 : std::is_same<O, __half>::value ? TP_F16 : TP_BF16);
+  static constexpr int kTerms = terms<T>(OUT32);
   static constexpr int kStride = RP + 4, kWords = OUT32 ? 2 : 1, kTile = RP == 128 ? 64 : 128;  // tokens
   union {
     uint4 ring[kWarps][4][2 * kWords][32];
