@@ -346,7 +346,8 @@ class SharedServing:
         # a step's plan is written over the lengths, the pages held and the pool's size that it began with
         self.plan = [ints(batch), ints(batch), ints(1, fill=pages), ints(1), ints(batch + 1), ints(rows),
                      torch.zeros(rows, dtype=torch.int64, device=device)]
-        self.rejected = ints(batch)
+        # what the last step refused, and what this one does
+        self.rejected, self.refused = ints(batch), ints(batch)
         self.adapters = None
         if adapters is not None:
             self.adapters = dict(adapters)
@@ -358,10 +359,11 @@ class SharedServing:
 
     def attend(self, x, counts, adapter_ids=None):
         """x (rows, D) bf16: counts[b] (int32 (batch), on the GPU) new tokens of each sequence in turn, then rows
-        that are not used; below 0: the sequence has ended.  Returns y (rows, D) float32."""
+        that are not used; below 0: the sequence has ended.  Returns y (rows, D) float32.  A step that the pool has
+        no pages for, or of a value out of range, is empty and changes nothing (plan[3], tp_paged_plan's `missing`)."""
         plan = tp_paged_plan(counts, self.plan[0], self.plan[1], self.block_table, self.free_pages, self.plan[2],
                              self.page, self.rows, rejected=self.rejected, out=self.plan)
-        self.rejected.zero_()
+        self.rejected.mul_(plan.missing != 0)  # taken off the lengths, unless the step is empty
         qkv = tp_all_to_sharded(x, self.w_qkv, self.b_qkv)
         if adapter_ids is not None and self.adapters is None:
             raise ValueError("adapter_ids, but no adapters were given")
@@ -398,7 +400,8 @@ class SharedServing:
         y = self.attend(x, counts, adapter_ids)
         tokens = torch.full((self.rows,), -1, dtype=torch.int64, device=x.device)  # rows of no sequence stay so
         _, self.logprobs, accepted, _ = tp_verify(self.head_of(y), drafts, self.plan[4], u, draft_probs=draft_probs,
-                                                  tokens=tokens, rejected=self.rejected, **settings)
+                                                  tokens=tokens, rejected=self.refused, **settings)
+        self.rejected += self.refused  # of an empty step none, behind the last one's, which still are to be taken off
         return tokens, accepted, y
 
 

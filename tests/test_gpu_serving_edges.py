@@ -46,3 +46,101 @@ def test_adapters_keep_16_bits_of_the_sum_over_x(T, R, dt, out_dt):
             worst = ((g.double() - f).abs() / tol).max()
             assert worst <= 1, float(worst)
     assert status() == 0
+
+
+# ------------------------------------------------------------------ steps that cannot be made
+def a_step(kind, counts, V, rows, seed):
+    """Tokens, drafts and random numbers of a step; `kind` is "verify" or "step"."""
+    g = torch.Generator().manual_seed(seed)
+    return (kind, counts, torch.randint(0, V, (rows,), generator=g).cuda(), torch.randint(0, V, (rows,), generator=g).cuda(),
+            torch.rand(rows, generator=g).cuda())
+
+
+def make_step(serve, table, step, ids):
+    kind, counts, toks, drafts, u = step
+    x = table[toks]
+    if kind == "step":
+        return serve.step(x, i32(counts), u[:serve.batch], adapter_ids=ids)
+    return serve.verify(x, i32(counts), drafts, u, adapter_ids=ids)
+
+
+def state_of(serve):
+    return [serve.plan[0].tolist(), serve.rejected.tolist()]
+
+
+@pytest.mark.parametrize("fails", ["step", "verify", "rows", "rows twice"])
+def test_a_step_that_cannot_be_made_changes_nothing(fails):
+    """What the last step refused stays refused over an empty step: the steps behind it are those of a server that was
+    never asked for it."""
+    D, V, N, B, rows = 256, 512, 2, 3, 48
+    cfg = synth.qkv(seed=9, T=1, D=D, V=V, N=N)
+    table, lora, ids = embeddings(V, D), make_adapters(2, 8, D), i32([1, -1, 0])
+    small, large = (SharedServing(cfg, heads=4, batch=B, pages=p, capacity=128, rows=rows, page=16, adapters=lora)
+                    for p in (6, 30))
+    script = [a_step("step", [20, 14, 9], V, rows, 1), a_step("verify", [9, 5, 7], V, rows, 2)]
+    for step in script:
+        for serve in (small, large):
+            make_step(serve, table, step, ids)
+    assert state_of(small) == state_of(large) and int(small.plan[3]) == 0
+    assert sum(small.rejected.tolist()) > 6  # random drafts are mostly refused
+    assert status() == 0
+    for _ in range(2 if fails == "rows twice" else 1):
+        before = state_of(small)
+        counts = [20, 20, 20] if "rows" in fails else [16, 16, 16]
+        make_step(small, table, a_step("verify" if "rows" in fails else fails, counts, V, rows, 3), ids)
+        assert int(small.plan[3]) == -1 if "rows" in fails else int(small.plan[3]) > 0
+        assert state_of(small) == before
+        assert status() == (tp.TP_ERR_INVALID_ARG if "rows" in fails else 0)
+    for i, (kind, counts) in enumerate([("verify", [4, -1, 5]), ("step", [1, 6, 1]), ("verify", [3, 3, 3])]):
+        step = a_step(kind, counts, V, rows, 10 + i)
+        got, want = (make_step(serve, table, step, ids) for serve in (small, large))
+        assert int(small.plan[3]) == 0
+        assert state_of(small) == state_of(large)
+        used = sum(max(c, 0) for c in counts)
+        assert torch.equal(got[-1][:used], want[-1][:used])
+        for p, q in zip(got[:-1], want[:-1]):
+            live = torch.tensor([c > 0 for c in counts], device="cuda") if kind == "step" else slice(None)
+            assert torch.equal(p[live], q[live])
+    assert status() == 0
+
+
+def test_a_captured_step_that_cannot_be_made_changes_nothing():
+    """The same as a graph that is replayed."""
+    D, V, N, B, rows = 256, 512, 2, 3, 48
+    cfg = synth.qkv(seed=9, T=1, D=D, V=V, N=N)
+    table, lora, ids = embeddings(V, D), make_adapters(2, 8, D), i32([1, -1, 0])
+
+    def fresh(pages):
+        return SharedServing(cfg, heads=4, batch=B, pages=pages, capacity=128, rows=rows, page=16, adapters=lora)
+    small, large = fresh(4), fresh(30)
+    counts, toks, drafts, u = i32([1, 1, 1]), *(t.clone() for t in a_step("verify", [], V, rows, 0)[2:])
+
+    def call():
+        return small.verify(table[toks], counts, drafts, u, adapter_ids=ids)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.current_stream().wait_stream(side)
+    new = fresh(4)
+    for to, t in zip([*small.plan, small.rejected, small.block_table, small.free_pages],
+                     [*new.plan, new.rejected, new.block_table, new.free_pages]):
+        to.copy_(t)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        out = call()
+    for i, c in enumerate([[20, 14, 9], [9, 5, 7], [16, 16, 16], [16, 16, 16], [4, -1, 5], [1, 6, 1], [3, 3, 3]]):
+        step = a_step("verify", c, V, rows, 20 + i)
+        for to, t in zip((counts, toks, drafts, u), (i32(c), *step[2:])):
+            to.copy_(t)
+        graph.replay()
+        torch.cuda.synchronize()
+        if sum(c) == 48:
+            assert int(small.plan[3]) > 0
+        else:
+            want = make_step(large, table, step, ids)
+            used = sum(max(n, 0) for n in c)
+            assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+            assert torch.equal(out[2][:used], want[2][:used])
+        assert state_of(small) == state_of(large)
+    assert status() == 0
