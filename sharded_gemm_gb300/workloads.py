@@ -317,6 +317,7 @@ class SharedServing:
     """The attention block and head of ``PagedServing`` for sequences that come and go over one pool of pages, with
     low-rank adapters of their own and drafted tokens.  Lengths, pages and what was refused of the drafts stay on
     the GPU: a step reads nothing back, and may be captured into a graph once it has run on the capturing stream.
+    A call that is refused for its arguments has changed nothing.
 
     ``cfg`` is a ``synth.qkv`` workload's (its x is not used), ``batch`` the sequences served at once, ``pages`` the
     pool, ``capacity`` the positions of a sequence at most, ``rows`` the rows of every step.  ``adapters``: None, or a
@@ -327,7 +328,7 @@ class SharedServing:
                  rope_base: float = 10000.0, adapters=None, device="cuda"):
         self.N = N = cfg["N"]
         D, self.V = cfg["D"], cfg["V"]
-        self.page, self.batch, self.rows, self.head = page, batch, rows, D // heads
+        self.page, self.batch, self.rows, self.width, self.head = page, batch, rows, D, D // heads
         self.w_qkv = tp_shard_weight(to_device(cfg["w_qkv"], "bf16", device), 0, 3, N)
         self.b_qkv = tp_shard_weight(to_device(cfg["b_qkv"], "f32", device), 0, 3, N)
         self.w_o = tp_shard_weight(to_device(cfg["w_o"], "bf16", device), -1, 1, N)
@@ -350,6 +351,17 @@ class SharedServing:
         self.rejected, self.refused = ints(batch), ints(batch)
         self.adapters = None
         if adapters is not None:
+            n = len(adapters["qkv_a"])
+            for a, b, outputs in (("qkv_a", "qkv_b", 3 * D), ("o_a", "o_b", D)):
+                R = adapters[a].shape[1]
+                if n < 1 or n > 16384 or R < 1 or R > 128:
+                    raise ValueError("1 to 16384 adapters of ranks 1 to 128")
+                for name, shape in ((a, (n, R, D)), (b, (n, outputs, R))):
+                    self._need(name, adapters[name], shape, torch.bfloat16)
+                    if not adapters[name].is_contiguous():
+                        raise ValueError("%s must be contiguous" % name)
+            if adapters["scales"] is not None:
+                self._need("scales", adapters["scales"], (n,), torch.float32)
             self.adapters = dict(adapters)
             # the ranks' slices, as of the projections: outputs of qkv by thirds, inputs of W_o
             third = adapters["qkv_b"].unflatten(1, (3, N, D // N))
@@ -357,16 +369,40 @@ class SharedServing:
             self.adapters["o_a"] = adapters["o_a"].unflatten(2, (N, D // N)).permute(2, 0, 1, 3).contiguous()
             self.groups = ints(4 + 4 * min(rows, len(adapters["o_b"]) + 1) + rows)
 
+    def _need(self, name, t, shape, *dtypes):
+        """Refuses what a call behind the plan would refuse, when lengths and pages have changed already."""
+        if tuple(t.shape) != shape or t.dtype not in dtypes or t.device != self.rejected.device or \
+                (shape[-1] > 1 and t.stride(-1) != 1) or (len(shape) == 2 and shape[0] > 1 and t.stride(0) < shape[1]):
+            raise ValueError("%s must be %s %s on %s, with contiguous rows that do not overlap" % (
+                name, " or ".join(str(d) for d in dtypes), shape, self.rejected.device))
+
+    def _check(self, x, counts, adapter_ids, settings=(), **outputs):
+        B, i32, f32 = (self.batch,), torch.int32, torch.float32
+        known = dict(temperature=(B, f32), top_k=(B, i32), top_p=(B, f32), min_p=(B, f32), **outputs)
+        self._need("x", x, (self.rows, self.width), torch.bfloat16)
+        self._need("counts", counts, B, i32)
+        if adapter_ids is not None:
+            if self.adapters is None:
+                raise ValueError("adapter_ids, but no adapters were given")
+            self._need("adapter_ids", adapter_ids, B, i32)
+        for name in settings:
+            if name not in known:
+                raise TypeError("unknown setting %s" % name)
+            if settings[name] is not None:
+                self._need(name, settings[name], *known[name])
+
     def attend(self, x, counts, adapter_ids=None):
         """x (rows, D) bf16: counts[b] (int32 (batch), on the GPU) new tokens of each sequence in turn, then rows
         that are not used; below 0: the sequence has ended.  Returns y (rows, D) float32.  A step that the pool has
         no pages for, or of a value out of range, is empty and changes nothing (plan[3], tp_paged_plan's `missing`)."""
+        self._check(x, counts, adapter_ids)
+        return self._attend(x, counts, adapter_ids)
+
+    def _attend(self, x, counts, adapter_ids):
         plan = tp_paged_plan(counts, self.plan[0], self.plan[1], self.block_table, self.free_pages, self.plan[2],
                              self.page, self.rows, rejected=self.rejected, out=self.plan)
         self.rejected.mul_(plan.missing != 0)  # taken off the lengths, unless the step is empty
         qkv = tp_all_to_sharded(x, self.w_qkv, self.b_qkv)
-        if adapter_ids is not None and self.adapters is None:
-            raise ValueError("adapter_ids, but no adapters were given")
         lora = self.adapters if adapter_ids is not None else None
         if lora:
             tp_lora_plan(adapter_ids, self.rows, len(lora["o_b"]), cu_seqlens=plan.cu_seqlens, out=self.groups)
@@ -389,7 +425,10 @@ class SharedServing:
     def step(self, x, counts, u, adapter_ids=None, **settings):
         """Prompts or single tokens: a token of each sequence drawn behind its last row (of one without rows: not
         meant).  u (batch).  Returns (tokens (batch), y)."""
-        y = self.attend(x, counts, adapter_ids)
+        self._check(x, counts, adapter_ids, settings, tokens=((self.batch,), torch.int64),
+                    logprobs=((self.batch,), torch.float32))
+        self._need("u", u, (self.batch,), torch.float32)
+        y = self._attend(x, counts, adapter_ids)
         tokens, self.logprobs = tp_sample(self.head_of(y[(self.plan[4][1:] - 1).clamp(min=0)]), u, **settings)
         return tokens, y
 
@@ -397,7 +436,13 @@ class SharedServing:
         """Rows of drafts: each sequence's are its last token and the drafted ones behind it, drafts[i] (int64 (rows))
         the token of row i + 1, u (rows).  The positions of refused drafts no longer count from the next step on.
         Returns (tokens (rows), -1 behind each sequence's drawn one, accepted (batch), y)."""
-        y = self.attend(x, counts, adapter_ids)
+        self._check(x, counts, adapter_ids, settings, logprobs=((self.rows,), torch.float32),
+                    accepted=((self.batch,), torch.int32))
+        self._need("drafts", drafts, (self.rows,), torch.int64)
+        self._need("u", u, (self.rows,), torch.float32)
+        if draft_probs is not None:
+            self._need("draft_probs", draft_probs, (self.rows, self.V), torch.float32, torch.bfloat16, torch.float16)
+        y = self._attend(x, counts, adapter_ids)
         tokens = torch.full((self.rows,), -1, dtype=torch.int64, device=x.device)  # rows of no sequence stay so
         _, self.logprobs, accepted, _ = tp_verify(self.head_of(y), drafts, self.plan[4], u, draft_probs=draft_probs,
                                                   tokens=tokens, rejected=self.refused, **settings)

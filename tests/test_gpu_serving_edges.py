@@ -144,3 +144,49 @@ def test_a_captured_step_that_cannot_be_made_changes_nothing():
             assert torch.equal(out[2][:used], want[2][:used])
         assert state_of(small) == state_of(large)
     assert status() == 0
+
+
+@pytest.mark.parametrize("kind", ["step", "verify"])
+def test_refused_steps_change_nothing(kind):
+    """A call that is refused for its arguments leaves lengths, pages and refusals as they were."""
+    D, V, N, B, rows = 256, 512, 2, 3, 48
+    cfg = synth.qkv(seed=9, T=1, D=D, V=V, N=N)
+    table, ids = embeddings(V, D), i32([1, -1, 0])
+    plain, full = (SharedServing(cfg, heads=4, batch=B, pages=30, capacity=128, rows=rows, page=16, adapters=a)
+                   for a in (None, make_adapters(2, 8, D)))
+    _, _, toks, drafts, u = a_step(kind, [], V, rows, 5)
+    ok = dict(x=table[toks], counts=i32([5, 4, 3]), u=u[:B] if kind == "step" else u, adapter_ids=ids)
+    if kind == "verify":
+        ok["drafts"] = drafts
+    for serve, bad in [(plain, {})] + [(full, b) for b in (
+            dict(adapter_ids=i32([1, 0])), dict(adapter_ids=ids.long()), dict(x=table[toks][:40]), dict(x=table[toks].float()),
+            dict(x=table[toks][:, :128]), dict(counts=i32([1, 2])), dict(counts=ids.long()), dict(u=u[:2]), dict(u=u.double()),
+            dict(temperature=u[:2]), dict(top_k=u[:3]), dict(top_q=u[:3]), dict(x=table[toks].cpu()), dict(x=table[:1].expand(rows, D)))] + [(full, b) for b in (
+                dict(drafts=drafts[:4]), dict(drafts=drafts.int()), dict(draft_probs=torch.zeros((rows, V - 1), device="cuda")),
+                dict(draft_probs=torch.zeros((rows, V), dtype=torch.float64, device="cuda"))) if kind == "verify"]:
+        make_step(serve, table, a_step("verify", [9, 5, 7], V, rows, 2), None)
+        state = [t.clone() for t in (*serve.plan[:3], serve.rejected, serve.block_table, serve.free_pages)]
+        assert sum(serve.rejected.tolist()) > 0
+        with pytest.raises((ValueError, TypeError)):
+            getattr(serve, kind)(**{**ok, **bad})
+        now = (*serve.plan[:3], serve.rejected, serve.block_table, serve.free_pages)
+        assert all(torch.equal(p, q) for p, q in zip(now, state)), bad
+        serve.step(table[toks], i32([-1, -1, -1]), u[:B])  # all end: room for the next
+    getattr(full, kind)(**ok)
+    assert full.plan[0].tolist() == [5, 4, 3]
+    assert status() == 0
+
+
+def test_adapters_that_no_step_takes_are_refused_at_once():
+    cfg, good = synth.qkv(seed=9, T=1, D=256, V=512, N=2), make_adapters(2, 8, 256)
+    wide = make_adapters(2, 129, 256)
+    for bad in (dict(qkv_a=wide["qkv_a"], qkv_b=wide["qkv_b"]), dict(o_b=good["o_b"].float()), dict(o_a=good["o_a"][:1]),
+                dict(scales=good["scales"].double()), dict(qkv_b=good["qkv_b"][:, :256]),
+                dict(qkv_a=good["qkv_a"].transpose(1, 2).contiguous().transpose(1, 2)), dict(o_b=good["o_b"].cpu())):
+        with pytest.raises(ValueError):
+            SharedServing(cfg, heads=4, batch=1, pages=8, capacity=64, rows=8, page=16, adapters={**good, **bad})
+    kept = SharedServing(cfg, heads=4, batch=1, pages=8, capacity=64, rows=8, page=16, adapters={**good, "scales": None})
+    out = torch.zeros(8, device="cuda")
+    x, u = embeddings(512, 256)[:8], torch.full((8,), 0.5, device="cuda")
+    kept.verify(x, i32([8]), torch.zeros(8, dtype=torch.int64, device="cuda"), u, adapter_ids=i32([1]), logprobs=out)
+    assert kept.logprobs is out and bool(out[0] < 0)
