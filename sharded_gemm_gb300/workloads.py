@@ -320,9 +320,9 @@ class SharedServing:
     A call that is refused for its arguments has changed nothing.
 
     ``cfg`` is a ``synth.qkv`` workload's (its x is not used), ``batch`` the sequences served at once, ``pages`` the
-    pool, ``capacity`` the positions of a sequence at most, ``rows`` the rows of every step.  ``adapters``: None, or a
-    dict with the adapters of both projections, each full as for one rank: qkv_a (n, R, D), qkv_b (n, 3 D, R), o_a
-    (n, R, D), o_b (n, D, R), and scales (n) or None."""
+    pool, ``capacity`` the positions of a sequence at most, up to the end of a page, ``rows`` the rows of every step.
+    ``adapters``: None, or a dict with the adapters of both projections, each full as for one rank: qkv_a (n, R, D),
+    qkv_b (n, 3 D, R), o_a (n, R, D), o_b (n, D, R), and scales (n) or None."""
 
     def __init__(self, cfg: dict, heads: int, batch: int, pages: int, capacity: int, rows: int, page: int = 64,
                  rope_base: float = 10000.0, adapters=None, device="cuda"):
@@ -336,13 +336,14 @@ class SharedServing:
         self.w_lm = tp_shard_weight(to_device(cfg["w_lm"], "bf16", device), 0, 1, N)
         self.k_cache = torch.empty((N, pages, heads // N, page, self.head), dtype=torch.bfloat16, device=device)
         self.v_cache = torch.empty_like(self.k_cache)
-        angle = torch.arange(capacity, dtype=torch.float64)[:, None] * \
+        width = -(-capacity // page)  # of the block table, whose positions are all rotated by their own angles
+        angle = torch.arange(width * page, dtype=torch.float64)[:, None] * \
             rope_base ** (-torch.arange(self.head // 2, dtype=torch.float64) * 2 / self.head)
         self.rope = torch.cat([angle.cos(), angle.sin()], 1).float().to(device)
 
         def ints(*shape, fill=0):
             return torch.full(shape, fill, dtype=torch.int32, device=device)
-        self.block_table = ints(batch, -(-capacity // page), fill=-1)
+        self.block_table = ints(batch, width, fill=-1)
         self.free_pages = torch.arange(pages, dtype=torch.int32, device=device)
         # a step's plan is written over the lengths, the pages held and the pool's size that it began with
         self.plan = [ints(batch), ints(batch), ints(1, fill=pages), ints(1), ints(batch + 1), ints(rows),

@@ -190,3 +190,19 @@ def test_adapters_that_no_step_takes_are_refused_at_once():
     x, u = embeddings(512, 256)[:8], torch.full((8,), 0.5, device="cuda")
     kept.verify(x, i32([8]), torch.zeros(8, dtype=torch.int64, device="cuda"), u, adapter_ids=i32([1]), logprobs=out)
     assert kept.logprobs is out and bool(out[0] < 0)
+
+
+@pytest.mark.parametrize("capacity,page", [(40, 16), (1, 16), (33, 32)])
+def test_capacities_end_with_a_page(capacity, page):
+    """Positions up to the end of a sequence's last page are rotated by their own angles."""
+    cfg = synth.qkv(seed=6, T=1, D=256, V=512, N=2)
+    table = embeddings(512, 256)
+    whole = -(-capacity // page) * page
+    a, b = (SharedServing(cfg, heads=4, batch=1, pages=8, capacity=c, rows=64, page=page) for c in (capacity, whole))
+    ids = torch.randint(0, 512, (64,), generator=torch.Generator().manual_seed(1)).cuda()
+    u = torch.tensor([0.5], device="cuda")
+    for count in (whole - 1, 1):
+        (t0, y0), (t1, y1) = (serve.step(table[ids], i32([count]), u) for serve in (a, b))
+        assert torch.equal(y0[:count], y1[:count]) and torch.equal(t0, t1)
+    assert a.plan[0].tolist() == [whole] and int(a.plan[3]) == 0
+    assert status() == 0
