@@ -201,6 +201,15 @@ def _torch():
     return torch
 
 
+def _stream_of(stream, device):
+    """The torch stream of an entry point's ``stream`` that is not None.  0 names the default stream; torch takes a
+    pointer of 0 for none given and would hand out a stream of its pool."""
+    torch = _torch()
+    if not isinstance(stream, int):
+        return stream
+    return torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
+
+
 def _dt(t) -> int:
     torch = _torch()
     m = {torch.float32: TP_F32, torch.bfloat16: TP_BF16, torch.float16: TP_F16}
@@ -911,8 +920,7 @@ def _lora_workspace(T, R, device, stream):
     if stream is None:
         ws = torch.empty(floats, dtype=torch.float32, device=device)
     else:
-        side = torch.cuda.ExternalStream(stream, device) if isinstance(stream, int) else stream
-        with torch.cuda.stream(side):
+        with torch.cuda.stream(_stream_of(stream, device)):
             ws = torch.empty(floats, dtype=torch.float32, device=device)
     if rec is not None:
         rec.keep.append(ws)

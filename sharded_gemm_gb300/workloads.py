@@ -11,7 +11,7 @@ from __future__ import annotations
 import numpy as np
 import torch
 
-from . import (tp_all_to_sharded, tp_all_to_sharded_dx, tp_bias_grad, tp_gated_all_to_sharded,
+from . import (_stream_of, tp_all_to_sharded, tp_all_to_sharded_dx, tp_bias_grad, tp_gated_all_to_sharded,
                tp_lora_all_to_sharded, tp_lora_plan, tp_lora_sharded_to_all,
                tp_mx_all_to_sharded, tp_mx_quantize, tp_mx_sharded_to_all, tp_paged_decode, tp_paged_plan, tp_paged_prefill,
                tp_qkv_append, tp_sample, tp_verify,
@@ -272,7 +272,7 @@ class PagedServing:
         if stream is None:
             return self._step(*args)
         here = torch.cuda.current_stream(x.device)
-        side = torch.cuda.ExternalStream(stream, x.device) if isinstance(stream, int) else stream
+        side = _stream_of(stream, x.device)
         side.wait_stream(here)
         try:
             with torch.cuda.stream(side):

@@ -206,3 +206,44 @@ def test_capacities_end_with_a_page(capacity, page):
         assert torch.equal(y0[:count], y1[:count]) and torch.equal(t0, t1)
     assert a.plan[0].tolist() == [whole] and int(a.plan[3]) == 0
     assert status() == 0
+
+
+# ------------------------------------------------------------------ streams
+def test_the_default_stream_by_its_handle(monkeypatch):
+    """0 names the default stream: the call's memory is of that stream, and a serving step runs there."""
+    seen = []
+
+    def empty(*args, real=torch.empty, **kwargs):
+        seen.append(torch.cuda.current_stream().cuda_stream)
+        return real(*args, **kwargs)
+    with torch.cuda.stream(torch.cuda.Stream()):
+        monkeypatch.setattr(torch, "empty", empty)
+        ws = tp._lora_workspace(2048, 16, torch.cuda.current_device(), 0)
+        monkeypatch.undo()
+    assert ws.numel() >= 2048 * 16 and seen == [0]
+    cfg = synth.qkv(seed=6, T=1, D=256, V=512, N=2)
+    table, u = embeddings(512, 256), torch.tensor([0.5], device="cuda")
+    a, b = (PagedServing(cfg, heads=4, batch=1, capacity=64, page=16) for _ in range(2))
+    real, where = b._step, []
+    b._step = lambda *args: (where.append(torch.cuda.current_stream().cuda_stream), real(*args))[1]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        want, got = a.step(table[:9], [9], u), b.step(table[:9], [9], u, stream=0)
+    torch.cuda.synchronize()
+    assert where == [0] and all(torch.equal(p, q) for p, q in zip(got, want))
+
+
+def test_adapters_on_the_default_stream_by_its_handle():
+    """Many tokens on stream 0 behind work that is still running there, called from another stream."""
+    T, K, O, R, n = 1500, 256, 256, 16, 4
+    x, a, b, y, s = lora_data("column", T, 1, K, O, R, n, BF16, F32, 1)
+    ids = i32(np.random.default_rng(1).integers(0, n, T))
+    plan = tp.tp_lora_plan(ids, T, n)
+    want = call_lora("column", x, a, b, plan, y, scales=s, out=[torch.empty_like(t) for t in y])[0]
+    out = torch.empty_like(y[0])
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)
+    with torch.cuda.stream(torch.cuda.Stream()):
+        tp.tp_lora_all_to_sharded(x[0], a[0], b, plan, y, scales=s, out=[out], stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
