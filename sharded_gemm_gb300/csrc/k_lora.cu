@@ -244,8 +244,7 @@ __device__ __forceinline__ void lora_tiles(const LoraArgs &a, int groups, int S)
         for (int r = 0; r < C; ++r) of[r] = ld_cluster_f4(mapa_shared(mine, sub * C + r));
 #pragma unroll
         for (int r = 0; r < C; ++r) sum = add4(sum, of[r]);
-        *reinterpret_cast<float4 *>(&sh.h[row][col]) =
-            make_float4(sum.x * scale, sum.y * scale, sum.z * scale, sum.w * scale);
+        *reinterpret_cast<float4 *>(&sh.h[row][col]) = scaled_h(sum, scale, col, a.R);
       }
       if (C > 1) cluster_arrive();
       read = C > 1;

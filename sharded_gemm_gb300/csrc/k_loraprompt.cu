@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
         if (r < tile.z)
           for (int k = 0; k < splits; ++k)
             v = add4(v, __ldcg(reinterpret_cast<const float4 *>(a.workspace + ((int64_t)k * a.T + tile.y + r) * RP + c)));
-        *reinterpret_cast<float4 *>(&sh.h[r][c]) = make_float4(v.x * scale, v.y * scale, v.z * scale, v.w * scale);
+        *reinterpret_cast<float4 *>(&sh.h[r][c]) = scaled_h(v, scale, c, a.R);
       }
       __syncthreads();
       if (!Half2<T>::kBf16) {

@@ -26,6 +26,13 @@ __device__ __forceinline__ float4 add4(float4 a, float4 b) {
   return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
 }
 
+// Four columns of h from `col` on.  Those behind the rank are 0 whatever the row: the zeros that
+// stand for the adapter's missing rows make NaN of an infinite x, which would go on to all outputs.
+__device__ __forceinline__ float4 scaled_h(const float4 &v, float scale, int col, int R) {
+  return make_float4(col < R ? v.x * scale : 0.0f, col + 1 < R ? v.y * scale : 0.0f, col + 2 < R ? v.z * scale : 0.0f,
+                     col + 3 < R ? v.w * scale : 0.0f);
+}
+
 // Two values as sums of N 16-bit numbers each.  A finite value stays one (bfloat16's
 // rounding may pass its largest), and behind an infinite one come zeros, not NaN.
 template <typename T, int N>

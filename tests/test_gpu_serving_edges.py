@@ -247,3 +247,32 @@ def test_adapters_on_the_default_stream_by_its_handle():
         tp.tp_lora_all_to_sharded(x[0], a[0], b, plan, y, scales=s, out=[out], stream=0)
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+# ------------------------------------------------------------------ what is not finite, and sizes from end to end
+@pytest.mark.parametrize("policy", [tp.TP_POLICY_AUTO, tp.TP_POLICY_SIMT], ids=["auto", "simt"])
+@pytest.mark.parametrize("dt,out_dt", [(BF16, F32), (BF16, BF16), (F16, F32), (F16, F16)])
+@pytest.mark.parametrize("R,O", [(1, 24), (4, 24), (5, 24), (8, 24), (16, 24), (24, 24), (24, 23), (40, 24), (100, 24), (128, 24)])
+@pytest.mark.parametrize("T", [2, 1100])
+def test_adapters_infinite_sums_of_any_rank(policy, T, R, O, dt, out_dt):
+    """An infinite sum gives infinite outputs of its sign whatever the rank is rounded up to inside."""
+    x = torch.ones((T, 32), dtype=dt, device="cuda")
+    x[1, 0] = float("inf")
+    x[T - 1, 31] = -float("inf") if T > 2 else x[T - 1, 31]
+    a = torch.ones((1, R, 32), dtype=dt, device="cuda")
+    b = torch.ones((1, O, R), dtype=dt, device="cuda")
+    b[0, 1::2] = -1
+    y = torch.zeros((T, O), dtype=out_dt, device="cuda")
+    tp.tp_set_policy(policy)
+    try:
+        got = tp.tp_lora_all_to_sharded(x, a, [b], tp.tp_lora_plan(i32([0] * T), T, 1), [y])[0].float()
+    finally:
+        tp.tp_set_policy(tp.TP_POLICY_AUTO)
+    sign = torch.ones(O, device="cuda")
+    sign[1::2] = -1
+    assert torch.equal(got[1], sign * float("inf"))
+    if T > 2:
+        assert torch.equal(got[T - 1], sign * -float("inf"))
+    rest = torch.cat([got[:1], got[2:T - 1]]) if T > 2 else got[:1]
+    assert torch.equal(rest, (sign * 32 * R).expand_as(rest))  # whole numbers that all types hold
+    assert status() == 0
