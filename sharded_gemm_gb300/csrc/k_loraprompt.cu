@@ -11,8 +11,8 @@
 // barriers between the products stood in the way of the streams, and registers for both were
 // too many: 309 us for 8192 tokens, R = 64, 4096 x 11008, where 66 us of bytes move.)
 //
-// Measured: those 105 us, the first pass 27 (67 MB), the second (361 MB) bound by the products of
-// h's two terms (one alone: 70); 5003 tokens, R = 16, 11008 x 4096, float32 outputs 60,
+// Measured: those 107 us, the first pass 27 (67 MB), the second (361 MB) bound by the products of
+// h's two terms (one alone: 70); 5003 tokens, R = 16, 11008 x 4096, float32 outputs 62,
 // passes of 26 (110 MB) and 31 (164 MB).
 #include "lora.cuh"
 
@@ -76,8 +76,8 @@ __global__ void __launch_bounds__(kLoraThreads, ShrinkShared<RP>::kCtas)
   Shared &sh = *reinterpret_cast<Shared *>(smem);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, q = lane % 4;
   const int K = (int)a.K, per = (K + 31) / 32, units = per * a.nx;
+  griddep_launch_dependents();
   griddep_wait();
-  griddep_launch_dependents();  // behind the wait: the second pass may read what came before this one
   const int groups = groups_of(a), tiles = count_tiles(a, groups, kShrinkTile, false);
   const unsigned S = splits_of<RP>(a, tiles, sms);
   int base = 0;
@@ -244,8 +244,9 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
   const int cols = (int)a.O, per = (cols + 31) / 32, blocks = per * a.ny;
   uint4 *const ring = &sh.ring[warp][0][0][lane];
   griddep_launch_dependents();
-  // only h comes from the kernel before: the plan and the tokens are read without a wait for it
-  bool waited = false;
+  // The plan too is read behind it: what kernels wrote before is promised there alone.  (Read ahead,
+  // under the first pass's end, it saved 2 us.)
+  griddep_wait();
   const int groups = groups_of(a), with = count_tiles(a, groups, kShrinkTile, false), splits = splits_of<RP>(a, with, sms);
   const int tiles = count_tiles(a, groups, kTile, !a.in_place);
   const unsigned S = shares_of(tiles, gridDim.x, (blocks + kWarps - 1) / kWarps, 3, 32);
@@ -263,8 +264,6 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
       sh.y_row[tid] = max(t, 0) * a.ldy * (int64_t)sizeof(O);
       sh.out_row[tid] = t < 0 ? -1 : t * a.ldo * (int64_t)sizeof(O);
     }
-    if (!waited) griddep_wait();
-    waited = true;
     if (id >= 0) {
       const float scale = a.scales ? __ldg(a.scales + id) : 1.0f;
       for (int i = tid; i < kTile * RP / 4; i += kLoraThreads) {
@@ -416,7 +415,6 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
     }
     cp_async_wait<0>();
   }
-  if (!waited) griddep_wait();  // what follows waits for this kernel, and so for the one before
 }
 
 template <typename K>

@@ -276,3 +276,41 @@ def test_adapters_infinite_sums_of_any_rank(policy, T, R, O, dt, out_dt):
     rest = torch.cat([got[:1], got[2:T - 1]]) if T > 2 else got[:1]
     assert torch.equal(rest, (sign * 32 * R).expand_as(rest))  # whole numbers that all types hold
     assert status() == 0
+
+
+@pytest.mark.parametrize("form,R,out_dt", [("column", 16, BF16), ("column", 64, F32), ("row", 128, F32)])
+def test_adapters_of_many_tokens_behind_a_plan_that_is_written_anew(form, R, out_dt):
+    """A step's plan and its adapters as a graph, replayed on other adapters, other offsets and other tokens."""
+    T, N, K, O, n, B = 1500, 2, 256, 320, 40, 60
+    x, a, b, y, s = lora_data(form, T, N, K, O, R, n, BF16, out_dt, 3)
+    ids, cu = i32([0] * B), i32([0] * (B + 1))
+    rng = np.random.default_rng(5)
+    steps = []
+    for i in range(8):
+        cuts = np.sort(rng.integers(0, T + 1 - 100 * (i % 2), B - 1))
+        steps.append((rng.integers(-1, n, B) if i % 3 else np.full(B, i), np.concatenate([[0], cuts, [T - 100 * (i % 2)]])))
+    out = [torch.empty_like(t) for t in y]
+    plan = tp.tp_lora_plan(ids, T, n, cu_seqlens=cu)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+
+    def step():
+        tp.tp_lora_plan(ids, T, n, cu_seqlens=cu, out=plan)
+        call_lora(form, x, a, b, plan, y, scales=s, out=out)
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        step()
+    for names, offsets in steps * 3:
+        ids.copy_(i32(names))
+        cu.copy_(i32(offsets))
+        for t in out:
+            t.fill_(7)
+        graph.replay()
+        fresh = tp.tp_lora_plan(i32(names), T, n, cu_seqlens=i32(offsets))
+        want = call_lora(form, x, a, b, fresh, y, scales=s, out=[torch.full_like(t, 7) for t in y])
+        assert torch.equal(plan, fresh)
+        assert all(torch.equal(p, q) for p, q in zip(out, want))
+    assert status() == 0
