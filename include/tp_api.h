@@ -735,8 +735,10 @@ int tp_sample(const void *logits, int64_t B, int64_t V, int64_t ld, tp_dtype in_
  *   drafts accepted, and the rows behind the drawn token (0 and 0 for a sequence
  *   of no rows).  Rows of no sequence stay as they were.  A row without a logit
  *   above -inf accepts nothing and gives token -1 and -inf.  A draft of V or more
- *   and offsets out of range are recorded in the status word: the draft counts as
- *   none, the sequence has no rows.
+ *   is recorded in the status word and counts as none.  So are offsets that do not
+ *   ascend within 0..T: a sequence between two such has no rows, nor has one into
+ *   whose rows another offset within 0..T reaches (one before its own above its first
+ *   row, or one behind them below its end).
  * Outputs overlap no input, but where it is said.
  * Errors: TP_ERR_UNSUPPORTED for more sequences or adapters than these, R above
  * 128, a page or V this build does not take; TP_ERR_NOT_DIVISIBLE if K (of the

@@ -36,20 +36,15 @@ __global__ void __launch_bounds__(kThreads) verify_order_kernel(const __grid_con
   griddep_wait();
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int64_t first = a.cu[0], end = a.cu[a.seqs];  // rows of no sequence are not touched
-  if (first < 0 || end > a.B) return;                 // recorded by the rows' kernel
-  for (int64_t i = first + tid; i < end; i += kThreads) row_words(a, i)[0] = kPending, row_words(a, i)[1] = -1;
-  __syncthreads();
-  auto put = [&](int64_t at, int64_t row) {  // sequences that claim each other's rows may be more than there are
-    if (first + at < end) row_words(a, first + at)[1] = (int32_t)row;
-  };
   int64_t r0 = 0, n = 0;
-  bool slow = false;
+  bool slow = false, bad = false;
   auto look = [&](int64_t s) {
     n = 0;
     if (s >= a.seqs) return;
     r0 = a.cu[s];
     const int64_t r1 = a.cu[s + 1];
-    if (r0 >= 0 && r0 <= r1 && r1 <= a.B) n = r1 - r0;
+    if (ascend(a, r0, r1)) n = r1 - r0;
+    else bad = true;
     slow = slow_row(a, s);
   };
   // the sums over lower threads of two values, side by side, and over all
@@ -79,6 +74,9 @@ __global__ void __launch_bounds__(kThreads) verify_order_kernel(const __grid_con
     scan(slow ? (uint64_t)n : 0, all);
     at[1] += (int64_t)all;
   }
+  if (__syncthreads_or(bad)) return;  // the rows go as they lie
+  for (int64_t i = first + tid; i < end; i += kThreads) row_words(a, i)[0] = kPending;
+  auto put = [&](int64_t at, int64_t row) { row_words(a, first + at)[1] = (int32_t)row; };
   for (int level = 0; level <= kLevels; ++level) {
     bool more = false;
     for (int64_t base = 0; base < a.seqs; base += kThreads) {
@@ -98,16 +96,23 @@ __global__ void __launch_bounds__(256) verify_end_kernel(const __grid_constant__
   griddep_wait();
   const int64_t b = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
   const int lane = threadIdx.x % 32;
+  const int64_t r0 = b < a.seqs ? a.cu[b] : 0, r1 = b < a.seqs ? a.cu[b + 1] : 0;
+  // (the first results are asked for before it is known that all offsets ascend)
+  const int32_t begin = ascend(a, r0, r1) && r0 + lane < r1 ? row_words(a, r0 + lane)[0] : 0;
+  bool bad = false;
+  for (int64_t s = threadIdx.x; s < a.seqs; s += 256) bad = bad || !ascend(a, a.cu[s], a.cu[s + 1]);
+  bad = __syncthreads_or(bad);
+  if (bad && blockIdx.x == 0 && threadIdx.x == 0) record_bad_value(a.status);
   if (b >= a.seqs) return;
-  const int64_t r0 = a.cu[b], r1 = a.cu[b + 1];
   int64_t accepted = 0, n = r1 - r0;
-  if (r0 < 0 || n <= 0 || r1 > a.B) {
+  // rows that another sequence claims are no one's
+  if (!ascend(a, r0, r1) || n == 0 || (bad && __any_sync(0xffffffffu, reached(a, b, lane, 32)))) {
     n = 1;
   } else {
     bool ended = false;
     for (int64_t i0 = r0; i0 < r1; i0 += 32) {
       const int64_t i = i0 + lane;
-      const int32_t word = i < r1 ? row_words(a, i)[0] : 0;
+      const int32_t word = i0 == r0 ? begin : i < r1 ? row_words(a, i)[0] : 0;
       const uint32_t marked = __ballot_sync(0xffffffffu, i < r1 && word < 0);
       const int end = ended ? -1 : marked ? __ffs(marked) - 1 : 32;
       if (i < r1) a.tokens[i] = lane < end ? word : lane == end ? drawn_mark(word) : -1;

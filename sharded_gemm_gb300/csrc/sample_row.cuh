@@ -846,10 +846,46 @@ __device__ __forceinline__ int32_t *row_words(const VerifyArgs &a, int64_t i) {
 // A drawn token's mark: where the accepted drafts of a sequence end.  Its own inverse.
 __device__ __forceinline__ int32_t drawn_mark(int32_t token) { return -2 - token; }
 
+// Whether a sequence's offsets ascend within the rows.
+__device__ __forceinline__ bool ascend(const VerifyArgs &a, int64_t r0, int64_t r1) {
+  return r0 >= 0 && r0 <= r1 && r1 <= a.B;
+}
+// Whether other offsets within 0..T reach into the rows of sequence s, looked for among the
+// `first`-th and every `step`-th behind it.  (Of offsets that all ascend none does.)
+__device__ __forceinline__ bool reached(const VerifyArgs &a, int64_t s, int first, int step) {
+  const int64_t r0 = a.cu[s], r1 = a.cu[s + 1];
+  bool any = false;
+  for (int64_t j = first; j <= a.seqs; j += step) {
+    const int64_t o = a.cu[j];
+    if (o >= 0 && o <= a.B) any = any || (j < s ? o > r0 : j > s + 1 && o < r1);
+  }
+  return any;
+}
+
+// Whose the row is, where offsets do not ascend: for all CTAs of a cluster the same, as it depends
+// on the offsets and the row alone.  Of the sequences that claim the row the first will do: one
+// that no other reaches is the only one.
+__device__ __forceinline__ int64_t claimed(const VerifyArgs &a, RowShared &sh, int64_t row) {
+  const int tid = threadIdx.x;
+  if (tid == 0) sh.answer = ~0ull;
+  __syncthreads();
+  for (int64_t s = tid; s < a.seqs; s += kThreads)
+    if (ascend(a, a.cu[s], a.cu[s + 1]) && row >= a.cu[s] && row < a.cu[s + 1]) atomicMin(&sh.answer, (u64)s);
+  __syncthreads();
+  const int64_t seq = (int64_t)sh.answer;
+  const bool none = __syncthreads_or(seq < 0 || reached(a, seq, tid, kThreads));
+  if (tid == 0) {
+    if (none) sh.answer = ~0ull;
+    else sh.before = row, sh.bin = a.cu[seq + 1] - 1;  // no rows before it to look at
+  }
+  __syncthreads();
+  return row;
+}
+
 // Which row of which sequence the `b`-th cluster of a verification takes; false: none.
-// Offsets that do not ascend within the rows are recorded, and their sequence has no rows.
-// Where the rows were put in order, one behind a row of its sequence that has ended it is
-// none either: nothing of it would be used.
+// Where offsets do not ascend within the rows, these go as they lie, and those that two sequences
+// claim are no one's.  Where the rows were put in order,
+// one behind a row of its sequence that has ended it is none either: nothing of it would be used.
 __device__ __forceinline__ int64_t ordered_row(const VerifyArgs &a, int64_t b) {
   int64_t row = row_words(a, b)[1];  // as if the first sequence began with row 0: no load to wait for
   const int64_t r0 = a.cu[0], r1 = a.cu[a.seqs];
@@ -864,12 +900,13 @@ __device__ __forceinline__ bool verify_place(const VerifyArgs &a, RowShared &sh,
   if (tid < a.seqs) r0 = a.cu[tid], r1 = a.cu[tid + 1];
   row = a.ordered ? ordered_row(a, b) : b;
   __syncthreads();
+  bool bad = false;
   for (int64_t s = tid; s < a.seqs; s += kThreads) {
     if (s != tid) r0 = a.cu[s], r1 = a.cu[s + 1];
-    if (r0 < 0 || r0 > r1 || r1 > a.B) record_bad_value(a.status);
+    if (!ascend(a, r0, r1)) bad = true;
     else if (row >= r0 && row < r1) sh.answer = s, sh.before = r0, sh.bin = r1 - 1;
   }
-  __syncthreads();
+  if (__syncthreads_or(bad)) row = claimed(a, sh, b);
   bool found = sh.answer != ~0ull;
   seq = (int64_t)sh.answer, last = (int64_t)sh.bin;
   if (a.ordered && found) {  // the same in all CTAs of the cluster, but for what they read next

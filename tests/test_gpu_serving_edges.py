@@ -314,3 +314,69 @@ def test_adapters_of_many_tokens_behind_a_plan_that_is_written_anew(form, R, out
         assert torch.equal(plan, fresh)
         assert all(torch.equal(p, q) for p, q in zip(out, want))
     assert status() == 0
+
+
+# ------------------------------------------------------------------ offsets that do not ascend
+def rows_of(off, T, s):
+    """The rows of sequence s: none where its offsets or others leave them unclear."""
+    r0, r1 = off[s], off[s + 1]
+    clear = 0 <= r0 <= r1 <= T and all(
+        (o <= r0 if j < s else o >= r1) for j, o in enumerate(off) if j not in (s, s + 1) and 0 <= o <= T)
+    return (r0, r1) if clear else (0, 0)
+
+
+def check_offsets(x, d, off, u, q, settings):
+    """Sequences whose rows are clear are served, the others' rows stay as they were."""
+    T, B = len(d), len(off) - 1
+    tokens = torch.full((T,), 77, dtype=torch.int64, device="cuda")
+    logprobs = torch.full((T,), 7.0, device="cuda")
+    got = tp.tp_verify(x, d, i32(off), u, draft_probs=q, tokens=tokens, logprobs=logprobs, **settings)
+    bad = any(not 0 <= off[s] <= off[s + 1] <= T for s in range(B))
+    assert status() == (tp.TP_ERR_INVALID_ARG if bad else 0)
+    used = torch.zeros(T, dtype=torch.bool, device="cuda")
+    for s in range(B):
+        r0, r1 = rows_of(off, T, s)
+        if r0 == r1:
+            assert (int(got[2][s]), int(got[3][s])) == (0, 0)
+            continue
+        used[r0:r1] = True
+        mine = {k: v[s:s + 1] for k, v in settings.items()}
+        ref = verify_ref(x[r0:r1], d[r0:r1], [0, r1 - r0], u[r0:r1], None if q is None else q[r0:r1], **mine)
+        check_verify((tokens[r0:r1], logprobs[r0:r1], got[2][s:s + 1], got[3][s:s + 1]), ref)
+    assert bool((tokens[~used] == 77).all()) and bool((logprobs[~used] == 7).all())
+
+
+@pytest.mark.parametrize("V", [40, 60001, 130003])
+@pytest.mark.parametrize("off", [[0, 5, 2, 6], [0, 3, 2, 9], [0, 3, 6, 10], [-1, 3, 6, 9], [4, 1, 6, 9], [9, 6, 3, 0],
+                                 [0, 9, 0, 9], [0, 3, 99, 4, 9], [0, 2, 5, 4, 4, 9], [3, 3, 0, 3], [0, 4, 4, 2, 8, 9], [1, 1, 4, 8]])
+def test_verify_of_offsets_that_do_not_ascend(off, V):
+    x, d, _, u, q = drafted(3, 2, 2, V, F32, F32, 2)
+    for settings in ({}, settings_of(len(off) - 1, 7)):
+        check_offsets(x, d, off, u, q, settings)
+
+
+@pytest.mark.parametrize("changes", [{0: -4}, {100: 401}, {40: 10}, {40: 390}, {1: -1}, {99: 0}, {100: 0}, {50: 203, 60: 2 ** 30},
+                                     {3: 11, 4: 11, 97: 3}, {}])
+def test_verify_of_many_rows_of_offsets_that_do_not_ascend(changes):
+    """The same where the rows are more than the GPU holds at once."""
+    x, d, cu, u, q = drafted(100, 3, 3, 20, F32, F32, 2)
+    off = list(cu)
+    for at, v in changes.items():
+        off[at] = v
+    for settings in ({}, settings_of(100, 7)):
+        check_offsets(x, d, off, u, q, settings)
+
+
+def test_verify_of_many_long_rows_of_offsets_that_do_not_ascend():
+    x, d, cu, u, q = drafted(60, 1, 3, 60007, BF16, BF16, 7)
+    for at, v in ((30, 5), (60, len(d) + 1), (0, -1)):
+        off = list(cu)
+        off[at] = v
+        check_offsets(x, d, off, u, q, settings_of(60, 5))
+
+
+def test_verify_of_no_rows_and_offsets_that_claim_some():
+    none = torch.empty((0, 40), device="cuda")
+    got = tp.tp_verify(none, torch.empty(0, dtype=torch.int64, device="cuda"), i32([0, 0, 3]), torch.empty(0, device="cuda"))
+    assert got[2].tolist() == [0, 0] and got[3].tolist() == [0, 0]
+    assert status() == tp.TP_ERR_INVALID_ARG
