@@ -101,8 +101,8 @@ __device__ __forceinline__ bool find_tile(const LoraArgs &a, int groups, int row
   return false;
 }
 
-// The exponent that takes the largest finite value of a row of h to 2^14..2^15, below
-// float16's largest; the same in all lanes.
+// The exponent that takes the largest finite value of a row of h to 2^14..2^15, below float16's
+// largest (at most 126: its power's reciprocal is a normal number); the same in all lanes.
 template <int RP>
 __device__ __forceinline__ int row_exponent(const float *row) {
   float most = 0.0f;
@@ -111,7 +111,7 @@ __device__ __forceinline__ int row_exponent(const float *row) {
     most = fmaxf(most, v <= 3.402823466e38f ? v : 0.0f);
   }
   most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));
-  return most > 0.0f ? max(-100, min(100, 14 - ilogbf(most))) : 0;
+  return most > 0.0f ? min(126, 14 - ilogbf(most)) : 0;
 }
 
 // h (rows of a stride of STRIDE floats, float16's scaled) as fragments of N terms.

@@ -380,3 +380,20 @@ def test_verify_of_no_rows_and_offsets_that_claim_some():
     got = tp.tp_verify(none, torch.empty(0, dtype=torch.int64, device="cuda"), i32([0, 0, 3]), torch.empty(0, device="cuda"))
     assert got[2].tolist() == [0, 0] and got[3].tolist() == [0, 0]
     assert status() == tp.TP_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("size", [2.0 ** 100, 2.0 ** 122, 2.0 ** -100, 2.0 ** -120])
+@pytest.mark.parametrize("T", [3, 1100])
+def test_adapters_of_float16_with_scales_from_end_to_end(T, size):
+    """Sums over x near float32's largest and smallest numbers meet B with the bits that others do."""
+    n, K, O, R = 2, 64, 40, 16
+    x, a, b, y, _ = lora_data("column", T, 1, K, O, R, n, F16, F32, 4)
+    y = [torch.zeros_like(t) for t in y]
+    b = [t * 2.0 ** (-4 if size > 1 else 4) for t in b]
+    scales = torch.tensor([size, -size / 2], device="cuda")
+    ids = np.arange(T) % n
+    got = call_lora("column", x, a, b, tp.tp_lora_plan(i32(ids), T, n), y, scales=scales)[0]
+    ref, big = lora_ref(x, a, b, dev(ids), scales, [torch.zeros_like(t) for t in y])
+    tol = U[F32] * ref[0].abs() + (2.0 ** -20 + (K + R) * 2.0 ** -23) * big[0]
+    assert ((got.double() - ref[0]).abs() <= tol).all()
+    assert status() == 0
