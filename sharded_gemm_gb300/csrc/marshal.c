@@ -543,6 +543,7 @@ static PyObject *m_plan(PyObject *self, PyObject *const *a, Py_ssize_t na) {
   const int64_t T = PyLong_AsLongLong(a[8]);
   if (PyErr_Occurred()) return NULL;
   if (T < 0 || T > 0x7fffffff) return PyErr_Format(PyExc_ValueError, "tokens must be in 0..2^31 - 1");
+  if (page != (int)page) return PyErr_Format(PyExc_ValueError, "page must be a power of two in 16..256");
   if (a[10] != Py_None && (!(PyTuple_Check(a[10]) || PyList_Check(a[10])) || PySequence_Fast_GET_SIZE(a[10]) != 7))
     return PyErr_Format(PyExc_ValueError, "out must be the seven outputs");
   static const char *const names[7] = {"out.seq_lens",   "out.owned",     "out.free_count", "out.missing",

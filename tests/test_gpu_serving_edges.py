@@ -397,3 +397,9 @@ def test_adapters_of_float16_with_scales_from_end_to_end(T, size):
     tol = U[F32] * ref[0].abs() + (2.0 ** -20 + (K + R) * 2.0 ** -23) * big[0]
     assert ((got.double() - ref[0]).abs() <= tol).all()
     assert status() == 0
+
+
+def test_plan_of_a_page_size_beyond_32_bits_is_refused():
+    ints = i32([1, 2])
+    with pytest.raises((ValueError, tp.TPError)):
+        tp.tp_paged_plan(ints, i32([0, 0]), i32([0, 0]), i32([[0, 1], [2, 3]]), i32([0] * 8), i32([4]), 2 ** 32 + 16, 4)
