@@ -13,8 +13,8 @@
 // Bound by bytes (each adapter is read once) and, of one token, by latency: 2 R operations
 // an element are few, so warp-level products do.
 //
-// Measured: one token, R = 16, 4096 x 12288 on 8 ranks 5.7 us; 64 tokens of 47 adapters 13.4
-// (28 MB, 4.2 at the copy rate); 97 tokens of 33 adapters, R = 32, 4096 x 4096, float32 11.2.
+// Measured: one token, R = 16, 4096 x 12288 on 8 ranks 5.6 us; 64 tokens of 47 adapters 12.5
+// (28 MB, 4.2 at the copy rate); 97 tokens of 33 adapters, R = 32, 4096 x 4096, float32 11.0.
 #include <atomic>
 
 #include "lora.cuh"
@@ -183,8 +183,9 @@ __device__ __forceinline__ void lora_tiles(const LoraArgs &a, int groups, int S)
       if (t0 >= 0) load_out<VEC>(o.y0, a.y[c.p], t0 * a.ldy, col, O);
       if (t1 >= 0) load_out<VEC>(o.y1, a.y[c.p], t1 * a.ldy, col, O);
     };
-    // (One block ahead: with two or three, registers for as many CTAs an SM are lacking, which
-    // costs more: 13.7 us for 64 tokens of 50 adapters against 15.4 and 21.)
+    // (One block ahead, in registers: with two or three there, as many CTAs an SM do not fit, which
+    // costs more: 13.7 us for 64 tokens of 50 adapters against 15.4 and 21.  Rings in shared memory,
+    // as k_loraprompt.cu has, would take no registers and have not been tried here.)
     Block now;
     Cursor c(blk0, per_o);
 
@@ -318,7 +319,7 @@ __global__ void __launch_bounds__(kLoraThreads, kResident<RP>)
 // More tiles than clusters run at once, if the plan has as many as it may: it says how many
 // CTAs take one.  (4096 x 4096, microseconds with 8 CTAs a tile | with as many as fit:
 // R = 16, 256 tokens of 152 adapters 38 | 22, 1024 of 249 66 | 38; R = 64, 64 tokens of 40
-// adapters 30 | 19, 1024 of 249 143 | 59; R = 128 and 93 adapters 99 | 60.)
+// adapters 30 | 19, 1024 of 249 143 | 60; R = 128 and 93 adapters 99 | 60.)
 template <typename T, int RP, bool OUT32>
 __global__ void __launch_bounds__(kLoraThreads, kResident<RP>) lora_many_kernel(const __grid_constant__ LoraArgs a, int) {
   griddep_launch_dependents();
@@ -435,7 +436,7 @@ int launch(const LoraArgs &a, cudaStream_t s) {
   const int S = (int)(room < 1 ? 1 : room < most ? room : most);
   if constexpr (VEC)
     if (tiles > wave) kern = lora_many_kernel<T, RP, OUT32>;
-  // (Operands without alignment, which come here in steps of any size: a cluster a tile, 136 us
+  // (Operands without alignment, which come here in steps of any size: a cluster a tile, 135 us
   // for 5000 tokens of R = 32, 1663 x 1511, where one wave's clusters in turns take 191.)
   const int64_t at_once = VEC ? wave : 1 << 20;
   cfg.gridDim = dim3((unsigned)((tiles * S < at_once ? tiles * S : at_once) * kCluster));

@@ -11,9 +11,9 @@
 // barriers between the products stood in the way of the streams, and registers for both were
 // too many: 309 us for 8192 tokens, R = 64, 4096 x 11008, where 66 us of bytes move.)
 //
-// Measured: those 107 us, the first pass 27 (67 MB), the second (361 MB) bound by the products of
-// h's two terms (one alone: 70); 5003 tokens, R = 16, 11008 x 4096, float32 outputs 62,
-// passes of 26 (110 MB) and 31 (164 MB).
+// Measured: those 107 us, the first pass 27 (67 MB) and the second 83 (361 MB, 4.4 TB/s: the
+// products of h's two terms; one alone took 70); 5003 tokens, R = 16, 11008 x 4096, float32
+// outputs 62, passes of 25 (110 MB) and 32 (164 MB).
 #include "lora.cuh"
 
 namespace tp {
@@ -47,8 +47,9 @@ __device__ __forceinline__ int splits_of(const LoraArgs &a, int tiles, int grid)
 // holds units of 32 elements of the contraction: the tokens' rows, then the adapter's.  Of a
 // tile of few tokens only the blocks that hold one are read and multiplied, and one group takes
 // it if that holds it all (1100 tokens of 250 adapters, R = 16, 4096 x 4096, both passes: 134 us
-// with all four blocks, 61 without, 56 so).  A tile's contraction may be split over several CTAs, whose sums lie side by side in the
-// workspace until the second pass adds them, in their order.
+// with all four blocks, 61 without, 56 so, 59 with what has come since).  A tile's contraction may
+// be split over several CTAs, whose sums lie side by side in the workspace until the second pass
+// adds them, in their order.
 template <int RP>
 struct ShrinkShared {
   static constexpr int MW = RP == 128 ? 2 : RP == 64 ? 4 : 2, kM = 4 / MW, kG = kWarps / kM, kStride = RP + 4;

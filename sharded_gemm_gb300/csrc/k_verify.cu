@@ -17,11 +17,15 @@
 // More rows than the GPU holds are put in order first: those whose filters take several
 // passes before the others, and of each kind the first rows of all sequences, then the
 // second ones and so on.  A row whose sequence an earlier one has ended by then is left out.
-// (436 mixed rows 155 us in the order given, all taken; 97 by their place; 88 so.  The
-// ordering takes 7: rows up to 1.5 an SM go as they lie, 164 of them 60 us against 66.)
+// (436 mixed rows 155 us in the order given, all taken; 97 by their place; 92 so.  The
+// ordering takes 7: rows up to 1.5 an SM go as they lie, 164 of them 60 us against 66 when that
+// was chosen, 63 now.)
 //
-// Measured, rows of 50272: one sequence of 4 drafts 26 us; 384 rows without filters 57 (two
-// turns of 152, by bytes 13); 436 with mixed settings 88 (16).
+// Offsets that do not ascend are looked for by all three kernels (0.5 to 1 us in all): CTAs of a
+// cluster that took a row for another sequence's would not meet at its barriers.
+//
+// Measured, rows of 50272: one sequence of 4 drafts 26 us; 384 rows without filters 59 (two
+// turns of 152, by bytes 13); 436 with mixed settings 92 (16).
 #include "sample_row.cuh"
 
 namespace tp {

@@ -143,7 +143,7 @@ __device__ __forceinline__ int lane_col(bool out32, int i, int q) { return out32
 // How many terms of T h meets B as.  Two hold 16 bits of it for bfloat16, 22 for float16: less
 // than the rounding of a 16-bit output, also where the products cancel.  (One of bfloat16 left
 // outputs 1.15 to 1.35 times as far off as their rounding does.  Few tokens leave the tensor pipe
-// idle and pay nothing; 8192 tokens of R = 64, 4096 x 11008, take 105 us and not 92.)  Float32
+// idle and pay nothing; 8192 tokens of R = 64, 4096 x 11008, take 13 us of 107 more.)  Float32
 // outputs take two of float16 or three of bfloat16 (24).
 template <typename T>
 __host__ __device__ constexpr int terms(bool out32) {

@@ -673,7 +673,7 @@ static PyObject *m_lora(PyObject *self, PyObject *const *a, Py_ssize_t na) {
       param_of(a[8], &scales, t_f32, n, x.dev, "scales") || stream_of(a[10], x.dev, &stream))
     return NULL;
   PyObject *keep = Py_NewRef(to), *mem = NULL;
-  if (T > (R <= 64 ? 1024 : 512)) {
+  if (T > (R <= 64 ? 1024 : 512)) {  /* few_tokens() of serve.cuh */
     mem = PyObject_CallFunction(a[6], "LLlO", T, R, x.dev, a[10]);
     if (!mem || length_of(mem, &floats, &dev, "workspace") || param_of(mem, &room, t_f32, floats, x.dev, "workspace")) {
       Py_XDECREF(mem);

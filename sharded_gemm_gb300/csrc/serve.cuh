@@ -30,11 +30,13 @@ struct GroupArgs {
 inline int64_t most_groups(int64_t T, int64_t n) { return T < n + 1 ? T : n + 1; }
 inline int64_t plan_ints(int64_t T, int64_t n) { return 4 + 4 * most_groups(T, n) + T; }
 
-// Steps of more tokens take two passes with h between them in memory.  (One pass reads an
-// adapter for every 16 tokens, the two for every 64 or more, but they cost a launch more.
-// 4096 x 4096, tokens of 8 adapters, one pass | two: R = 16, 1024 tokens 12.6 us | 13.1, 2048
-// 22.8 | 16.7; R = 64, 1024 19.7 | 21.2, 2048 30.4 | 24.5; R = 128, 256 16.4 | 19.1, 512 25.1 |
-// 22.5, 1024 54 | 24.)
+// Steps of more tokens take two passes with h between them in memory; the binding asks for their
+// workspace by the same rule (marshal.c).  One pass reads an adapter for every 16 tokens, the two
+// for every 64 or more, but they cost a launch more.  (4096 x 4096, tokens of 8 adapters, one pass
+// | two: R = 16, 1024 tokens 12.4 us | 15.0, 2048 22.7 | 18.3; R = 64, 1024 20.4 | 25.9, 2048 32.0 |
+// 28.5; R = 128, 256 14.6 | 22.0, 512 24.6 | 25.8, 1024 54 | 27.  Of 250 adapters a tile holds few
+// tokens either way, and up to R = 64 one pass stays ahead: 1100 tokens, R = 16 38 | 59, R = 64 61 |
+// 93, R = 128 153 | 131.  The call does not know how many adapters its tokens have.)
 inline int64_t few_tokens(int R) { return R <= 64 ? 1024 : 512; }
 // How often a tile's contraction is split at most: few tiles leave SMs idle.
 inline int lora_splits(int64_t T) { return T <= 4096 ? 8 : T <= 8192 ? 4 : T <= 16384 ? 2 : 1; }
